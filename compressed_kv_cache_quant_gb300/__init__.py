@@ -5,7 +5,9 @@ The hot path runs in hand-written CUDA kernels for sm_103a inside libkvq.so
 only marshals arguments to the C ABI declared in include/kvq.h.
 """
 from . import _abi  # noqa: F401
-from .kvq import (Allocator, Batch, KvqError, LayerCache, Workspace, kv_append_critical_score,  # noqa: F401
+from .kvq import (Allocator, AttnMod, Batch, RopeTable, kv_chunk_attn, kv_chunk_attn_ws, kv_decode_attn,  # noqa: F401
+                  kv_decode_attn_ws, kv_pages_copy, kv_pages_copy_ws, kv_qk_norm_rope, kv_slots_copy, kv_slots_copy_ws,
+                  kvq_table_remap, kvq_table_remap_ws, KvqError, LayerCache, Workspace, kv_append_critical_score,  # noqa: F401
                   kv_append_critical_score_ws, kv_block_select, kv_block_select_ws, kv_critical_score, kv_select_sparse_attn, kv_select_sparse_attn_ws,
                   kv_decode_attn_quant, kv_decode_attn_quant_ws, kv_dense_pref_score, kv_dense_pref_score_ws,
                   kv_h2o_accumulate, kv_h2o_accumulate_ws, kv_offload_gather, kv_offload_gather_ws, kv_page_append,

@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_char_p, c_double, c_int, c_int32, c_int64, c_size_t, c_uint32, c_uint64, c_void_p
+from ctypes import POINTER, c_char_p, c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_uint32, c_uint64, c_void_p
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libkvq.so")
@@ -57,7 +57,21 @@ class Seqs(ctypes.Structure):
                 ("max_blocks", c_int32), ("max_len", c_int32), ("reserved", c_int32)]
 
 
+class Rope(ctypes.Structure):
+    _fields_ = [("rot_dim", c_int32), ("interleaved", c_int32), ("scaling", c_int32), ("original_len", c_int32),
+                ("base", c_double), ("factor", c_double), ("low", c_double), ("high", c_double)]
+
+
+class AttnModStruct(ctypes.Structure):
+    _fields_ = [("scale", c_float), ("softcap", c_float), ("window", c_int32), ("n_sink", c_int32),
+                ("slopes", c_void_p), ("prefix_len", c_void_p), ("doc_start", c_void_p)]
+
+
+F16, BF16 = 0, 1                       # dtype of kv_qk_norm_rope
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3, "knees": 4}
+
 PL, PP, PS = POINTER(Layout), POINTER(Pool), POINTER(Seqs)
+PR, PM = POINTER(Rope), POINTER(AttnModStruct)
 VP = c_void_p
 
 # name -> (restype, argtypes); mirrors include/kvq.h
@@ -108,6 +122,19 @@ PROTOTYPES = {
     "kv_dense_pref_score_ws": (c_size_t, [PL, PS, c_int32]),
     "kv_offload_gather": (c_int, [VP, VP, c_int64, c_int64, c_int32, VP, c_int32, VP, VP, VP, VP, c_size_t, VP]),
     "kv_offload_gather_ws": (c_size_t, []),
+    "kvq_rope_steps": (c_int, [PR, POINTER(c_uint64), POINTER(c_float)]),
+    "kv_qk_norm_rope": (c_int, [PL, PR, VP, c_float, c_int32, c_int64, VP, VP, c_int64, VP, c_int64, VP, c_int64, VP, VP,
+                                c_float, VP, VP, VP, VP]),
+    "kv_decode_attn": (c_int, [PL, PP, PS, VP, PM, VP, VP, VP, c_size_t, VP]),
+    "kv_decode_attn_ws": (c_size_t, [PL, PS]),
+    "kv_chunk_attn": (c_int, [PL, PP, PS, VP, VP, c_int64, c_int32, PM, VP, VP, VP, c_size_t, VP]),
+    "kv_chunk_attn_ws": (c_size_t, [PL, PS, c_int64, c_int32]),
+    "kv_pages_copy": (c_int, [PL, PP, VP, c_int32, VP, c_size_t, VP]),
+    "kv_pages_copy_ws": (c_size_t, []),
+    "kv_slots_copy": (c_int, [PL, PP, PS, VP, c_int32, VP, c_size_t, VP]),
+    "kv_slots_copy_ws": (c_size_t, []),
+    "kvq_table_remap": (c_int, [VP, c_int64, VP, c_int64, VP, c_size_t, VP]),
+    "kvq_table_remap_ws": (c_size_t, []),
     "kvq_seq_lens_add": (c_int, [VP, c_int32, c_int32, VP]),
     "kv_page_copy": (c_int, [PL, PP, c_int32, c_int32, VP]),
     "kvq_check": (c_int, [VP, VP]),
@@ -118,6 +145,10 @@ PROTOTYPES = {
     "kvq_block_alloc": (c_int, [VP, c_int32, POINTER(c_int32)]),
     "kvq_block_ref": (c_int, [VP, c_int32]),
     "kvq_block_free": (c_int, [VP, c_int32]),
+    "kvq_block_free_n": (c_int, [VP, c_int32, POINTER(c_int32)]),
+    "kvq_block_fork": (c_int, [VP, PL, c_int64, POINTER(c_int32), POINTER(c_int32), POINTER(c_int32),
+                               POINTER(c_int32)]),
+    "kvq_block_compact": (c_int, [VP, c_int32, POINTER(c_int32), POINTER(c_int32), POINTER(c_int32)]),
     "kvq_block_refcount": (c_int, [VP, c_int32]),
     "kvq_alloc_num_free": (c_int64, [VP]),
 }

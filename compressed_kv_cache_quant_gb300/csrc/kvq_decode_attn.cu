@@ -1,0 +1,405 @@
+// kv_decode_attn: attention of one new token per sequence over an fp16 layer's pages, split over the
+// cache's length; a second, dependent launch joins the splits when there is more than one.
+//
+// Bound: bytes.  Every visible K and V row is read once for the H_q/H_kv <= 8 query heads of its kv head,
+// 8 flop per byte at most, so both products run on mma.sync m16n8k16 fragments that come straight from
+// global memory in 16-byte loads, without shared memory:
+//   S^T = K q^T   A = 16 tokens of a page, B = the group's query heads as the 8 columns.  A sum over
+//                 channels may take them in any order, so lane (g, t) holds the 16-byte chunks t, t+4,
+//                 t+8, t+12 of token g (and g + 8) and the query's fragments use the same order.
+//   O^T = V^T p   A = 16 dims x 16 tokens.  Lane (g, t) loads chunks g and g + 8 of tokens 2t, 2t+1, 2t+8,
+//                 2t+9; a byte permute pairs neighbouring tokens, and row g of product j is dim 8g + j.
+//                 p enters as two fp16 halves (22 bits), against exact fp16 V; sums are fp32.
+// p^T reaches the B operand through movmatrix.  A warp owns whole pages (8 KB of loads in flight per warp,
+// K of the next page issued as soon as the current one is consumed), keeps its own running maximum and
+// sum, and meets the others once, at the end.
+#include <algorithm>
+
+#include "kvq_attn_mod.cuh"
+
+namespace {
+
+constexpr int D = KVQ_HEAD_DIM;
+constexpr int PG = KVQ_BLOCK_TOKENS;
+constexpr int DA_NW = 4;  // warps per CTA
+constexpr int DA_NT = 32 * DA_NW;
+
+struct DecArgs {
+    const uint16_t *k16, *v16, *q;
+    int64_t num_blocks;
+    const int32_t *bt, *seq_lens;
+    int32_t max_blocks, max_len, H, GQ;
+    KvqModArgs mod;
+    float *out, *lse;
+    float* part;        // [B][H][n_splits][GQ][D] unnormalised outputs
+    float2* ml;         // [B][H][n_splits][GQ] running maximum (log2) and sum
+    KvqWsHeader* hdr;
+    int32_t n_splits, pps;
+};
+
+__device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 bits_float2(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
+__device__ __forceinline__ uint4 ldg_stream(const uint16_t* p) { return __ldcs(reinterpret_cast<const uint4*>(p)); }
+
+struct Page {
+    uint4 k[8];  // token g: chunks t + 4i; then token g + 8
+    uint4 v[8];  // tokens 2t, 2t+1, 2t+8, 2t+9: chunk g; then chunk g + 8
+};
+
+__device__ __forceinline__ void load_k(Page& P, const uint16_t* rows, int g, int t) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        P.k[i] = ldg_stream(rows + g * D + 8 * (t + 4 * i));
+        P.k[4 + i] = ldg_stream(rows + (g + 8) * D + 8 * (t + 4 * i));
+    }
+}
+__device__ __forceinline__ void load_v(Page& P, const uint16_t* rows, int g, int t) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int tok = 2 * t + (i & 1) + 8 * (i >> 1);
+        P.v[i] = ldg_stream(rows + tok * D + 8 * g);
+        P.v[4 + i] = ldg_stream(rows + tok * D + 64 + 8 * g);
+    }
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// one score in the log2 domain; `away` = |i - j|
+template <bool CAP, bool BIAS>
+__device__ __forceinline__ float score(const KvqModArgs& m, float dot, float slope2, int away) {
+    float s = CAP ? m.post * kvq_tanh(dot * m.pre) : dot * m.pre;
+    if (BIAS) s = fmaf(-slope2, (float)away, s);
+    return s;
+}
+
+// The pages the newest token of sequence b sees: n1 from p1 (sinks), then n2 from p2; the parts they
+// are cut into.  Returns false for a length out of bounds.
+struct Span {
+    KvqSee see;
+    int T, p1, n1, p2, n, used;
+    __device__ __forceinline__ int logical(int u) const { return u < n1 ? p1 + u : p2 + (u - n1); }
+};
+__device__ __forceinline__ bool span_of(const DecArgs& a, int b, Span* s) {
+    s->T = a.seq_lens[b];
+    if (s->T < 0 || s->T > a.max_len) return false;
+    s->see = KvqSee{0, 0, 0, 0};
+    if (s->T > 0)
+        s->see = kvq_see(a.mod, s->T - 1, s->T, a.mod.prefix_len ? a.mod.prefix_len[b] : 0,
+                         a.mod.doc_start ? a.mod.doc_start[b] : 0);
+    const KvqSee& e = s->see;
+    s->p1 = e.doc / PG;
+    s->n1 = e.sink > e.doc ? (e.sink + PG - 1) / PG - s->p1 : 0;
+    s->p2 = max(e.lo / PG, s->n1 > 0 ? s->p1 + s->n1 : 0);
+    s->n = s->n1 + (e.lo < e.hi ? max(0, (e.hi + PG - 1) / PG - s->p2) : 0);
+    s->used = max(1, (s->n + a.pps - 1) / a.pps);
+    return true;
+}
+
+template <bool CAP, bool BIAS>
+__global__ void __launch_bounds__(DA_NT) decode_attn_kernel(DecArgs a) {
+    __shared__ float so[DA_NW][8][D + 4];
+    __shared__ float sm[DA_NW][8], sl[DA_NW][8];
+    const int split = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int GQ = a.GQ, Hq = a.H * GQ;
+    kvq_pdl_begin();
+    Span sp;
+    if (!span_of(a, b, &sp)) {
+        if (tid == 0 && split == 0) kvq_dev_flag(a.hdr, KVQ_DEV_BAD_LENGTH, b);
+        return;
+    }
+    if (split >= sp.used) return;
+    const KvqSee see = sp.see;
+    const int T = sp.T, u0 = split * a.pps, u1 = min(sp.n, u0 + a.pps);
+
+    // query fragments: head g of the group, channels in the order of the key chunks
+    uint4 qf[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        qf[i] = g < GQ ? *reinterpret_cast<const uint4*>(a.q + ((int64_t)b * Hq + h * GQ + g) * D + 8 * (t + 4 * i))
+                       : make_uint4(0, 0, 0, 0);
+    float slope[2] = {0.0f, 0.0f};
+    if (BIAS) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (2 * t + e < GQ) slope[e] = a.mod.slopes[h * GQ + 2 * t + e] * KVQ_LOG2E;
+    }
+    float o[8][4];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+
+    const int32_t* bt = a.bt + (int64_t)b * a.max_blocks;
+    // rows of page u of this CTA's range; page 0 stands in for a bad id (flagged, the output is not valid)
+    const auto rows_of = [&](int u) -> int64_t {
+        int32_t page = bt[sp.logical(u)];
+        if (page < 0 || page >= a.num_blocks) {
+            if (lane == 0) kvq_dev_flag(a.hdr, KVQ_DEV_BAD_PAGE, page);
+            page = 0;
+        }
+        return ((int64_t)page * a.H + h) * PG * D;
+    };
+    Page P;
+    int u = u0 + warp;
+    int64_t row = 0, next = 0;
+    if (u < u1) {
+        row = rows_of(u);
+        load_k(P, a.k16 + row, g, t);
+        load_v(P, a.v16 + row, g, t);
+    }
+    if (u + DA_NW < u1) next = rows_of(u + DA_NW);
+    for (; u < u1; u += DA_NW) {
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            mma16816(s, P.k[i].x, P.k[4 + i].x, P.k[i].y, P.k[4 + i].y, qf[i].x, qf[i].y);
+            mma16816(s, P.k[i].z, P.k[4 + i].z, P.k[i].w, P.k[4 + i].w, qf[i].z, qf[i].w);
+        }
+        const bool more = u + DA_NW < u1;
+        row = next;
+        if (more) load_k(P, a.k16 + row, g, t);
+        if (u + 2 * DA_NW < u1) next = rows_of(u + 2 * DA_NW);
+
+        const int j0 = sp.logical(u) * PG;
+        const bool whole = j0 >= see.lo && j0 + PG <= see.hi;
+        const bool in0 = see(j0 + g), in1 = see(j0 + g + 8);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            s[e] = in0 ? score<CAP, BIAS>(a.mod, s[e], slope[e], abs(T - 1 - j0 - g)) : -INFINITY;
+            s[2 + e] = in1 ? score<CAP, BIAS>(a.mod, s[2 + e], slope[e], abs(T - 1 - j0 - g - 8)) : -INFINITY;
+        }
+        float mn[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float x = fmaxf(s[e], s[2 + e]);
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            mn[e] = fmaxf(m[e], x);
+        }
+        if (__any_sync(0xffffffffu, mn[0] > m[0] || mn[1] > m[1])) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float f = mn[e] > m[e] ? exp2f(m[e] - mn[e]) : 1.0f;
+                m[e] = mn[e];
+                l[e] *= f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    o[j][e] *= f;
+                    o[j][2 + e] *= f;
+                }
+            }
+        }
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            p[e] = in0 ? exp2f(s[e] - m[e]) : 0.0f;
+            p[2 + e] = in1 ? exp2f(s[2 + e] - m[e]) : 0.0f;
+            l[e] += p[e] + p[2 + e];
+        }
+        const uint32_t h0 = half2_bits(p[0], p[1]), h1 = half2_bits(p[2], p[3]);
+        const float2 f0 = bits_float2(h0), f1 = bits_float2(h1);
+        const uint32_t b0 = transpose8x8(h0), b1 = transpose8x8(h1);
+        const uint32_t c0 = transpose8x8(half2_bits(p[0] - f0.x, p[1] - f0.y));
+        const uint32_t c1 = transpose8x8(half2_bits(p[2] - f1.x, p[3] - f1.y));
+        if (!whole) {  // rows nobody sees may hold anything, also NaN: 0 * NaN must not reach the sum
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (!see(j0 + 2 * t + (i & 1) + 8 * (i >> 1))) P.v[i] = P.v[4 + i] = make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t sel = j & 1 ? 0x7632 : 0x5410;
+            const uint32_t a0 = __byte_perm(word(P.v[0], j >> 1), word(P.v[1], j >> 1), sel);
+            const uint32_t a1 = __byte_perm(word(P.v[4], j >> 1), word(P.v[5], j >> 1), sel);
+            const uint32_t a2 = __byte_perm(word(P.v[2], j >> 1), word(P.v[3], j >> 1), sel);
+            const uint32_t a3 = __byte_perm(word(P.v[6], j >> 1), word(P.v[7], j >> 1), sel);
+            mma16816(o[j], a0, a1, a2, a3, b0, b1);
+            mma16816(o[j], a0, a1, a2, a3, c0, c1);
+        }
+        if (more) load_v(P, a.v16 + row, g, t);
+    }
+
+    // the warps' states into shared memory
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 4);
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 8);
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 16);
+        if (g == 0) {
+            sm[warp][2 * t + e] = m[e];
+            sl[warp][2 * t + e] = l[e];
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            float* dst = &so[warp][2 * t + e][64 * c + 8 * g];
+#pragma unroll
+            for (int j = 0; j < 8; j += 4)
+                *reinterpret_cast<float4*>(dst + j) = make_float4(o[j][2 * c + e], o[j + 1][2 * c + e],
+                                                                  o[j + 2][2 * c + e], o[j + 3][2 * c + e]);
+        }
+    }
+    __syncthreads();
+    const int64_t bh = (int64_t)b * a.H + h;
+    for (int i = tid; i < GQ * D; i += DA_NT) {
+        const int e = i / D, d = i % D;
+        float mx = sm[0][e];
+#pragma unroll
+        for (int w = 1; w < DA_NW; ++w) mx = fmaxf(mx, sm[w][e]);
+        float x = 0.0f, y = 0.0f;
+#pragma unroll
+        for (int w = 0; w < DA_NW; ++w) {
+            const float f = sm[w][e] == -INFINITY ? 0.0f : exp2f(sm[w][e] - mx);
+            x += f * so[w][e][d];
+            y += f * sl[w][e];
+        }
+        if (sp.used == 1) {
+            const int64_t r = (int64_t)b * Hq + h * GQ + e;
+            a.out[r * D + d] = y == 0.0f ? 0.0f : x / y;
+            if (a.lse != nullptr && d == 0) a.lse[r] = y == 0.0f ? -INFINITY : (mx + log2f(y)) * KVQ_LN2;
+        } else {
+            const int64_t r = (bh * a.n_splits + split) * GQ + e;
+            a.part[r * D + d] = x;
+            if (d == 0) a.ml[r] = make_float2(mx, y);
+        }
+    }
+}
+
+// Joins the parts of one (sequence, query head) in their order and leaves the workspace zeroed.  The
+// warps take every DA_NW-th part, so the loads of a long split list overlap.
+__global__ void __launch_bounds__(DA_NT) decode_join_kernel(DecArgs a) {
+    __shared__ float4 so[DA_NW][32];
+    __shared__ float sl[DA_NW];
+    const int hq = blockIdx.x, b = blockIdx.y, h = hq / a.GQ, e = hq % a.GQ;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    kvq_pdl_begin();
+    Span sp;
+    if (!span_of(a, b, &sp) || sp.used == 1) return;
+    const int64_t first = (((int64_t)b * a.H + h) * a.n_splits) * a.GQ + e;
+    float mx = -INFINITY;
+    for (int s = lane; s < sp.used; s += 32) mx = fmaxf(mx, a.ml[first + (int64_t)s * a.GQ].x);
+    mx = kvq_warp_max(mx);
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float y = 0.0f;
+#pragma unroll 4
+    for (int s = warp; s < sp.used; s += DA_NW) {
+        const int64_t r = first + (int64_t)s * a.GQ;
+        const float2 v = a.ml[r];
+        float4* part = reinterpret_cast<float4*>(a.part + r * D) + lane;
+        const float4 w = *part;
+        const float f = v.x == -INFINITY ? 0.0f : exp2f(v.x - mx);
+        x.x += f * w.x;
+        x.y += f * w.y;
+        x.z += f * w.z;
+        x.w += f * w.w;
+        y += f * v.y;
+        *part = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    so[warp][lane] = x;
+    if (lane == 0) sl[warp] = y;
+    __syncthreads();  // also: every warp has read the maxima
+    for (int s = threadIdx.x; s < sp.used; s += DA_NT) a.ml[first + (int64_t)s * a.GQ] = make_float2(0.0f, 0.0f);
+    if (warp != 0) return;
+#pragma unroll
+    for (int w = 1; w < DA_NW; ++w) {
+        const float4 z = so[w][lane];
+        x.x += z.x;
+        x.y += z.y;
+        x.z += z.z;
+        x.w += z.w;
+        y += sl[w];
+    }
+    const int64_t r = (int64_t)b * a.H * a.GQ + hq;
+    const float inv = y == 0.0f ? 0.0f : 1.0f / y;  // nothing visible: 0
+    reinterpret_cast<float4*>(a.out + r * D)[lane] = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+    if (a.lse != nullptr && lane == 0) a.lse[r] = y == 0.0f ? -INFINITY : (mx + log2f(y)) * KVQ_LN2;
+}
+
+struct DecPlan {
+    int n_splits, pps;
+    size_t off_ml, off_part, bytes;
+};
+
+// Splits by size alone: one sequence is cut into as many equal parts as there are resident CTAs per kv
+// head (one wave); a batch, whose sequences differ in length, into parts of equal pages, small enough for
+// about eight waves, so that the long ones do not finish alone.
+DecPlan dec_plan(const kvq_layout* L, const kvq_seqs* S) {
+    DecPlan p;
+    const int H = L->n_kv_heads, GQ = L->n_q_heads / H, B = std::max(S->batch, 1);
+    const int pages = std::max(1, (S->max_len + PG - 1) / PG);
+    const int64_t slots = 3 * (int64_t)kvq_num_sms();
+    const int64_t rows = (int64_t)B * H;
+    const int64_t want = std::max<int64_t>(1, (rows <= slots ? slots : 8 * slots) / rows);
+    p.pps = (int)std::max<int64_t>((pages + want - 1) / want, 2 * DA_NW);
+    p.pps = (p.pps + DA_NW - 1) / DA_NW * DA_NW;
+    p.n_splits = (pages + p.pps - 1) / p.pps;
+    const size_t parts = p.n_splits > 1 ? (size_t)rows * p.n_splits * GQ : 0;
+    p.off_ml = sizeof(KvqWsHeader);
+    p.off_part = kvq_round_up(p.off_ml + parts * sizeof(float2), 256);
+    p.bytes = kvq_round_up(p.off_part + parts * D * sizeof(float), 256);
+    return p;
+}
+
+}  // namespace
+
+extern "C" size_t kv_decode_attn_ws(const kvq_layout* L, const kvq_seqs* S) {
+    if (kvq_check_layout(L, "kv_decode_attn_ws", true) || kvq_check_seqs_sizes(S, "kv_decode_attn_ws")) return 0;
+    return dec_plan(L, S).bytes;
+}
+
+extern "C" int kv_decode_attn(const kvq_layout* L, const kvq_pool* P, const kvq_seqs* S, const uint16_t* q,
+                              const kvq_attn_mod* mod, float* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+    static const char* fn = "kv_decode_attn";
+    kvq_clear_error();
+    int st = kvq_check_layout(L, fn, true);
+    if (st) return st;
+    KVQ_REQUIRE(L->bits == 16, KVQ_ERR_UNSUPPORTED, "%s: bits %d (an fp16 layer)", fn, L->bits);
+    st = kvq_check_seqs(S, fn);
+    if (st) return st;
+    KVQ_REQUIRE(P && P->k16 && P->v16 && P->num_blocks > 0, KVQ_ERR_INVALID_ARG, "%s: pool needs k16 and v16", fn);
+    KVQ_REQUIRE(S->batch <= 65535 && L->n_kv_heads <= 65535, KVQ_ERR_UNSUPPORTED, "%s: batch or heads", fn);
+    DecArgs a;
+    st = kvq_mod_args(mod, fn, &a.mod);
+    if (st) return st;
+    const DecPlan p = dec_plan(L, S);
+    st = kvq_check_ws(ws, ws_bytes, p.bytes, fn);
+    if (st) return st;
+    if (S->batch == 0) return KVQ_OK;
+    KVQ_REQUIRE(q && out && (S->block_table || S->max_len == 0), KVQ_ERR_INVALID_ARG, "%s: NULL buffer", fn);
+    KVQ_REQUIRE((((uintptr_t)q | (uintptr_t)out | (uintptr_t)P->k16 | (uintptr_t)P->v16) & 15u) == 0,
+                KVQ_ERR_INVALID_ARG, "%s: q, out, k16 and v16 must be 16-byte aligned", fn);
+    a.k16 = P->k16, a.v16 = P->v16, a.q = q;
+    a.num_blocks = P->num_blocks;
+    a.bt = S->block_table, a.seq_lens = S->seq_lens;
+    a.max_blocks = S->max_blocks, a.max_len = S->max_len;
+    a.H = L->n_kv_heads, a.GQ = L->n_q_heads / L->n_kv_heads;
+    a.out = out, a.lse = lse;
+    a.hdr = static_cast<KvqWsHeader*>(ws);
+    a.ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + p.off_ml);
+    a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.off_part);
+    a.n_splits = p.n_splits, a.pps = p.pps;
+    const dim3 grid(p.n_splits, L->n_kv_heads, S->batch);
+    const bool cap = a.mod.post != 0.0f, bias = a.mod.slopes != nullptr;
+    const auto go = [&](auto kernel) {
+        cudaError_t e = kvq_launch_pdl(kernel, grid, dim3(DA_NT), 0, kvq_stream(stream), a);
+        if (e == cudaSuccess && p.n_splits > 1)
+            e = kvq_launch_pdl(decode_join_kernel, dim3(L->n_q_heads, S->batch), dim3(DA_NT), 0, kvq_stream(stream), a);
+        if (e != cudaSuccess) return kvq_fail(KVQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+        return (int)KVQ_OK;
+    };
+    if (cap) return bias ? go(decode_attn_kernel<true, true>) : go(decode_attn_kernel<true, false>);
+    return bias ? go(decode_attn_kernel<false, true>) : go(decode_attn_kernel<false, false>);
+}

@@ -1,0 +1,244 @@
+// Moving a cache's pages: many page copies in one launch (forks, compaction), the per-slot state of a
+// forked sequence, renaming pages in a block table, and the host side of forking and compacting.
+//
+// Both copies are bound by bytes: each one is read and written once.  A page of a layer is two to four
+// pieces, one per array; a CTA copies 16 KB of a page's concatenated pieces, every thread four 16-byte
+// loads before the first store, so a few CTAs per SM keep enough bytes in flight.  Pairs are read on the
+// device, so one captured launch serves every list of the same length.
+#include <algorithm>
+#include <vector>
+
+#include "kvq_internal.cuh"
+
+namespace {
+
+constexpr int D = KVQ_HEAD_DIM;
+constexpr int PG = KVQ_BLOCK_TOKENS;
+constexpr int PC_NT = 256;
+constexpr int PC_UNROLL = 4;
+constexpr int PC_TILE = PC_NT * PC_UNROLL;  // 16-byte units per CTA step
+
+struct CopyArgs {
+    uint4* base[4];
+    int64_t stride[4];   // 16-byte units per page (or slot)
+    int32_t end[4];      // running ends of the pieces, in 16-byte units
+    int32_t n_arr;
+    const int32_t* pairs;
+    int32_t n_pairs;
+    int64_t n_items;     // pages (or slots) of the pool
+    KvqWsHeader* hdr;
+};
+
+// The (source, destination) of pair i, or false when the pair copies nothing.
+__device__ __forceinline__ bool pair_of(const int32_t* pairs, int i, int64_t n_items, KvqWsHeader* hdr, int32_t* src,
+                                        int32_t* dst) {
+    *src = pairs[2 * i];
+    *dst = pairs[2 * i + 1];
+    if (*src < 0 || *dst < 0 || *src >= n_items || *dst >= n_items) {
+        if (threadIdx.x == 0) kvq_dev_flag(hdr, KVQ_DEV_BAD_PAGE, i);
+        return false;
+    }
+    return *src != *dst;
+}
+
+__global__ void __launch_bounds__(PC_NT) pages_copy_kernel(CopyArgs a) {
+    const int units = a.end[a.n_arr - 1];
+    for (int i = blockIdx.y; i < a.n_pairs; i += gridDim.y) {
+        int32_t src, dst;
+        if (!pair_of(a.pairs, i, a.n_items, a.hdr, &src, &dst)) continue;
+        uint4 x[PC_UNROLL];
+        uint4* to[PC_UNROLL];
+#pragma unroll
+        for (int j = 0; j < PC_UNROLL; ++j) {
+            const int u = blockIdx.x * PC_TILE + j * PC_NT + threadIdx.x;
+            to[j] = nullptr;
+            if (u >= units) continue;
+            int arr = 0, from = 0;
+#pragma unroll
+            for (int n = 0; n < 3; ++n)
+                if (n + 1 < a.n_arr && u >= a.end[n]) arr = n + 1, from = a.end[n];
+            uint4* b = a.base[arr] + (u - from);
+            x[j] = __ldcs(b + src * a.stride[arr]);
+            to[j] = b + dst * a.stride[arr];
+        }
+#pragma unroll
+        for (int j = 0; j < PC_UNROLL; ++j)
+            if (to[j] != nullptr) __stcs(to[j], x[j]);
+    }
+}
+
+struct SlotArgs {
+    uint4 *k_tail, *k_absmax, *kT;
+    int64_t tail_units, absmax_units, kT_row_units;  // 16-byte units per slot, per slot, per channel row
+    int32_t rows;                                    // H_kv * d channel rows of kT
+    const int32_t* seq_lens;
+    int32_t max_len, batch;
+    const int32_t* pairs;
+    int32_t n_pairs;
+    int64_t max_seqs;
+    KvqWsHeader* hdr;
+};
+
+__global__ void __launch_bounds__(PC_NT) slots_copy_kernel(SlotArgs a) {
+    for (int i = blockIdx.y; i < a.n_pairs; i += gridDim.y) {
+        int32_t src, dst;
+        if (!pair_of(a.pairs, i, a.max_seqs, a.hdr, &src, &dst)) continue;
+        const int64_t first = (int64_t)blockIdx.x * PC_NT + threadIdx.x, step = (int64_t)gridDim.x * PC_NT;
+        for (int64_t u = first; u < a.tail_units; u += step)
+            a.k_tail[dst * a.tail_units + u] = a.k_tail[src * a.tail_units + u];
+        for (int64_t u = first; u < a.absmax_units; u += step)
+            a.k_absmax[dst * a.absmax_units + u] = a.k_absmax[src * a.absmax_units + u];
+        if (a.kT != nullptr) {
+            const int len = src < a.batch ? a.seq_lens[src] : -1;
+            if (len < 0 || len > a.max_len || len > 8 * a.kT_row_units) {
+                if (threadIdx.x == 0) kvq_dev_flag(a.hdr, KVQ_DEV_BAD_LENGTH, src);
+                continue;
+            }
+            const int64_t per = (len + 7) / 8;  // units of a row that hold tokens
+            for (int row = blockIdx.x; row < a.rows; row += gridDim.x) {
+                const uint4* s = a.kT + ((int64_t)src * a.rows + row) * a.kT_row_units;
+                uint4* d = a.kT + ((int64_t)dst * a.rows + row) * a.kT_row_units;
+                for (int64_t u = threadIdx.x; u < per; u += PC_NT) __stcs(d + u, __ldcs(s + u));
+            }
+        }
+    }
+}
+
+__global__ void __launch_bounds__(PC_NT) table_remap_kernel(int32_t* bt, int64_t n, const int32_t* map,
+                                                            int64_t num_blocks, KvqWsHeader* hdr) {
+    const int64_t i = (int64_t)blockIdx.x * PC_NT + threadIdx.x;
+    if (i >= n) return;
+    const int32_t p = bt[i];
+    if (p < 0) return;  // an entry without a page
+    if (p >= num_blocks) {
+        kvq_dev_flag(hdr, KVQ_DEV_BAD_PAGE, p);
+        return;
+    }
+    bt[i] = map[p];
+}
+
+// the arrays of one layer's pages: base and bytes per page
+struct Piece { void* base; size_t bytes; };
+
+int layer_pieces(const kvq_layout* L, const kvq_pool* P, const char* fn, Piece* out, int* n) {
+    const size_t H = (size_t)L->n_kv_heads;
+    const int cb = kvq_code_bits(L);
+    *n = 0;
+    if (cb == 16) {
+        out[(*n)++] = {P->k16, H * PG * D * 2};
+        out[(*n)++] = {P->v16, H * PG * D * 2};
+    } else {
+        const size_t R = cb == KVQ_BITS_E4M3 ? D : D * (size_t)cb / 8;
+        out[(*n)++] = {P->k_codes, H * PG * R};
+        out[(*n)++] = {P->v_codes, H * PG * R};
+        if (cb != KVQ_BITS_E4M3) {
+            out[(*n)++] = {P->k_sz, H * D * 4};
+            out[(*n)++] = {P->v_sz, H * PG * (D / (size_t)L->v_group_dims) * 4};
+        }
+    }
+    for (int i = 0; i < *n; ++i)
+        KVQ_REQUIRE(out[i].base && ((uintptr_t)out[i].base & 15u) == 0, KVQ_ERR_INVALID_ARG,
+                    "%s: a page array is NULL or not 16-byte aligned", fn);
+    return KVQ_OK;
+}
+
+}  // namespace
+
+extern "C" size_t kv_pages_copy_ws(void) { return sizeof(KvqWsHeader); }
+extern "C" size_t kv_slots_copy_ws(void) { return sizeof(KvqWsHeader); }
+extern "C" size_t kvq_table_remap_ws(void) { return sizeof(KvqWsHeader); }
+
+extern "C" int kv_pages_copy(const kvq_layout* L, const kvq_pool* P, const int32_t* pairs, int32_t n_pairs, void* ws,
+                             size_t ws_bytes, void* stream) {
+    static const char* fn = "kv_pages_copy";
+    kvq_clear_error();
+    int st = kvq_check_layout(L, fn, false);
+    if (st) return st;
+    KVQ_REQUIRE(P != nullptr && P->num_blocks >= 0, KVQ_ERR_INVALID_ARG, "%s: pool", fn);
+    KVQ_REQUIRE(n_pairs >= 0 && (n_pairs == 0 || pairs), KVQ_ERR_INVALID_ARG, "%s: pairs", fn);
+    st = kvq_check_ws(ws, ws_bytes, kv_pages_copy_ws(), fn);
+    if (st) return st;
+    Piece piece[4];
+    CopyArgs a = {};
+    st = layer_pieces(L, P, fn, piece, &a.n_arr);
+    if (st) return st;
+    if (n_pairs == 0) return KVQ_OK;
+    int64_t end = 0;
+    for (int i = 0; i < a.n_arr; ++i) {
+        a.base[i] = static_cast<uint4*>(piece[i].base);
+        a.stride[i] = (int64_t)(piece[i].bytes / 16);
+        end += a.stride[i];
+        KVQ_REQUIRE(end <= INT32_MAX - PC_TILE, KVQ_ERR_UNSUPPORTED, "%s: n_kv_heads %d", fn, L->n_kv_heads);
+        a.end[i] = (int32_t)end;
+    }
+    a.pairs = pairs;
+    a.n_pairs = n_pairs;
+    a.n_items = P->num_blocks;
+    a.hdr = static_cast<KvqWsHeader*>(ws);
+    const dim3 grid((unsigned)((end + PC_TILE - 1) / PC_TILE), (unsigned)std::min(n_pairs, 32768));
+    pages_copy_kernel<<<grid, PC_NT, 0, kvq_stream(stream)>>>(a);
+    return kvq_launch_status(fn);
+}
+
+extern "C" int kv_slots_copy(const kvq_layout* L, const kvq_pool* P, const kvq_seqs* S, const int32_t* pairs,
+                             int32_t n_pairs, void* ws, size_t ws_bytes, void* stream) {
+    static const char* fn = "kv_slots_copy";
+    kvq_clear_error();
+    int st = kvq_check_layout(L, fn, false);
+    if (st) return st;
+    st = kvq_check_seqs(S, fn);
+    if (st) return st;
+    KVQ_REQUIRE(P != nullptr && P->max_seqs >= 0, KVQ_ERR_INVALID_ARG, "%s: pool", fn);
+    KVQ_REQUIRE(n_pairs >= 0 && (n_pairs == 0 || pairs), KVQ_ERR_INVALID_ARG, "%s: pairs", fn);
+    KVQ_REQUIRE(S->batch <= P->max_seqs, KVQ_ERR_INVALID_ARG, "%s: batch exceeds max_seqs", fn);
+    st = kvq_check_ws(ws, ws_bytes, kv_slots_copy_ws(), fn);
+    if (st) return st;
+    const int cb = kvq_code_bits(L);
+    const size_t H = (size_t)L->n_kv_heads;
+    SlotArgs a = {};
+    if (cb == 16) {
+        KVQ_REQUIRE(!P->kT == !P->k_absmax, KVQ_ERR_INVALID_ARG, "%s: kT and k_absmax come together", fn);
+        if (P->kT) {
+            KVQ_REQUIRE(P->t_cap > 0 && P->t_cap % 8 == 0, KVQ_ERR_INVALID_ARG, "%s: t_cap", fn);
+            a.kT = reinterpret_cast<uint4*>(P->kT);
+            a.k_absmax = reinterpret_cast<uint4*>(P->k_absmax);
+            a.kT_row_units = P->t_cap / 8;
+            a.absmax_units = (int64_t)H * D / 4;
+            a.rows = (int32_t)(H * D);
+        }
+    } else if (cb != KVQ_BITS_E4M3) {
+        KVQ_REQUIRE(P->k_tail, KVQ_ERR_INVALID_ARG, "%s: k_tail NULL", fn);
+        a.k_tail = reinterpret_cast<uint4*>(P->k_tail);
+        a.tail_units = (int64_t)H * KVQ_K_GROUP_TOKENS * D / 8;
+    }
+    KVQ_REQUIRE((((uintptr_t)a.k_tail | (uintptr_t)a.kT | (uintptr_t)a.k_absmax) & 15u) == 0, KVQ_ERR_INVALID_ARG,
+                "%s: slot arrays must be 16-byte aligned", fn);
+    if (n_pairs == 0 || (!a.k_tail && !a.kT)) return KVQ_OK;  // E4M3 and unscored fp16 layers keep no slot state
+    a.seq_lens = S->seq_lens;
+    a.max_len = S->max_len;
+    a.batch = S->batch;
+    a.pairs = pairs;
+    a.n_pairs = n_pairs;
+    a.max_seqs = P->max_seqs;
+    a.hdr = static_cast<KvqWsHeader*>(ws);
+    const int ctas = std::max(1, std::min<int>(a.kT ? a.rows : (int)((a.tail_units + PC_NT - 1) / PC_NT),
+                                               4 * kvq_num_sms()));
+    slots_copy_kernel<<<dim3(ctas, std::min(n_pairs, 32768)), PC_NT, 0, kvq_stream(stream)>>>(a);
+    return kvq_launch_status(fn);
+}
+
+extern "C" int kvq_table_remap(int32_t* block_table, int64_t n_entries, const int32_t* map, int64_t num_blocks, void* ws,
+                               size_t ws_bytes, void* stream) {
+    static const char* fn = "kvq_table_remap";
+    kvq_clear_error();
+    KVQ_REQUIRE(n_entries >= 0 && num_blocks > 0 && num_blocks <= INT32_MAX && map && (n_entries == 0 || block_table),
+                KVQ_ERR_INVALID_ARG, "%s: bad arguments", fn);
+    const int st = kvq_check_ws(ws, ws_bytes, kvq_table_remap_ws(), fn);
+    if (st) return st;
+    if (n_entries == 0) return KVQ_OK;
+    const int64_t grid = (n_entries + PC_NT - 1) / PC_NT;
+    KVQ_REQUIRE(grid <= INT32_MAX, KVQ_ERR_UNSUPPORTED, "%s: n_entries", fn);
+    table_remap_kernel<<<(unsigned)grid, PC_NT, 0, kvq_stream(stream)>>>(block_table, n_entries, map, num_blocks,
+                                                                         static_cast<KvqWsHeader*>(ws));
+    return kvq_launch_status(fn);
+}

@@ -261,6 +261,99 @@ extern "C" int kvq_block_free(kvq_allocator* a, int32_t id) {
     return KVQ_OK;
 }
 
+extern "C" int kvq_block_free_n(kvq_allocator* a, int32_t n, const int32_t* ids) {
+    kvq_clear_error();
+    KVQ_REQUIRE(a && n >= 0 && (n == 0 || ids), KVQ_ERR_INVALID_ARG, "kvq_block_free_n: bad arguments");
+    // every id first (an id may be listed as often as it has references), so that a refusal changes nothing
+    int32_t i = 0;
+    for (; i < n; ++i) {
+        if (ids[i] < 0 || (size_t)ids[i] >= a->refcount.size() || a->refcount[(size_t)ids[i]] <= 0) break;
+        a->refcount[(size_t)ids[i]] -= 1;
+    }
+    if (i < n) {
+        const int32_t bad = ids[i];
+        while (i-- > 0) a->refcount[(size_t)ids[i]] += 1;
+        return kvq_fail(KVQ_ERR_INVALID_ARG, "kvq_block_free_n: page %d is no page or has no such reference", bad);
+    }
+    for (int32_t j = 0; j < n; ++j) {
+        // hand a page back once, at its last mention
+        if (a->refcount[(size_t)ids[j]] != 0) continue;
+        a->refcount[(size_t)ids[j]] = -1;
+    }
+    for (int32_t j = 0; j < n; ++j) {
+        if (a->refcount[(size_t)ids[j]] != -1) continue;
+        a->refcount[(size_t)ids[j]] = 0;
+        a->free_list.push_back(ids[j]);
+    }
+    return KVQ_OK;
+}
+
+// A fork shares every page that neither branch writes again and copies the others: the last, partly
+// filled page, and for a quantized layer all pages of an unfinished 64-token K group, whose codes are
+// written into each of them when a branch completes the group.
+extern "C" int kvq_block_fork(kvq_allocator* a, const kvq_layout* L, int64_t n_tokens, const int32_t* src_pages,
+                              int32_t* dst_pages, int32_t* pairs, int32_t* n_pairs) {
+    kvq_clear_error();
+    const int st = kvq_check_layout(L, "kvq_block_fork", false);
+    if (st) return st;
+    KVQ_REQUIRE(a && n_tokens >= 0 && n_pairs && (n_tokens == 0 || (src_pages && dst_pages && pairs)),
+                KVQ_ERR_INVALID_ARG, "kvq_block_fork: bad arguments");
+    const int cb = kvq_code_bits(L);
+    const int64_t unit = cb == 16 || cb == KVQ_BITS_E4M3 ? KVQ_BLOCK_TOKENS : KVQ_K_GROUP_TOKENS;
+    const int64_t shared = n_tokens / unit * (unit / KVQ_BLOCK_TOKENS);
+    const int64_t pages = (n_tokens + KVQ_BLOCK_TOKENS - 1) / KVQ_BLOCK_TOKENS;
+    for (int64_t j = 0; j < pages; ++j)
+        KVQ_REQUIRE(src_pages[j] >= 0 && (size_t)src_pages[j] < a->refcount.size() &&
+                        a->refcount[(size_t)src_pages[j]] > 0 && a->refcount[(size_t)src_pages[j]] < INT32_MAX,
+                    KVQ_ERR_INVALID_ARG, "kvq_block_fork: page %d (entry %lld) is not allocated", src_pages[j],
+                    (long long)j);
+    KVQ_REQUIRE((size_t)(pages - shared) <= a->free_list.size(), KVQ_ERR_NO_SPACE,
+                "kvq_block_fork: %lld pages to copy, %zu free", (long long)(pages - shared), a->free_list.size());
+    for (int64_t j = 0; j < shared; ++j) {
+        a->refcount[(size_t)src_pages[j]] += 1;
+        dst_pages[j] = src_pages[j];
+    }
+    *n_pairs = (int32_t)(pages - shared);
+    for (int64_t j = shared; j < pages; ++j) {
+        const int32_t id = a->free_list.back();
+        a->free_list.pop_back();
+        a->refcount[(size_t)id] = 1;
+        pairs[2 * (j - shared)] = src_pages[j];
+        pairs[2 * (j - shared) + 1] = id;
+        dst_pages[j] = id;
+    }
+    return KVQ_OK;
+}
+
+extern "C" int kvq_block_compact(kvq_allocator* a, int32_t max_moves, int32_t* pairs, int32_t* map, int32_t* n_moves) {
+    kvq_clear_error();
+    KVQ_REQUIRE(a && max_moves >= 0 && n_moves && map && (max_moves == 0 || pairs), KVQ_ERR_INVALID_ARG,
+                "kvq_block_compact: bad arguments");
+    const int64_t n = (int64_t)a->refcount.size();
+    for (int64_t i = 0; i < n; ++i) map[i] = (int32_t)i;
+    // the highest used page goes to the lowest free one until they meet: sources and destinations are
+    // then disjoint, so the copies may run in any order
+    int64_t lo = 0, hi = n - 1;
+    int32_t moves = 0;
+    while (moves < max_moves) {
+        while (lo < n && a->refcount[(size_t)lo] > 0) ++lo;
+        while (hi >= 0 && a->refcount[(size_t)hi] == 0) --hi;
+        if (lo >= hi) break;
+        pairs[2 * moves] = (int32_t)hi;
+        pairs[2 * moves + 1] = (int32_t)lo;
+        map[hi] = (int32_t)lo;
+        a->refcount[(size_t)lo] = a->refcount[(size_t)hi];
+        a->refcount[(size_t)hi] = 0;
+        ++moves;
+    }
+    // the free pages are handed out lowest first again, so the used ones stay together
+    a->free_list.clear();
+    for (int64_t i = n - 1; i >= 0; --i)
+        if (a->refcount[(size_t)i] == 0) a->free_list.push_back((int32_t)i);
+    *n_moves = moves;
+    return KVQ_OK;
+}
+
 extern "C" int kvq_block_refcount(const kvq_allocator* a, int32_t id) {
     kvq_clear_error();
     KVQ_REQUIRE(a && id >= 0 && (size_t)id < a->refcount.size(), KVQ_ERR_INVALID_ARG, "kvq_block_refcount: bad id");

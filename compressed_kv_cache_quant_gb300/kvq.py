@@ -9,7 +9,9 @@ Helpers:
                 the kvq_layout / kvq_pool descriptors;
   Batch      -- block table + sequence lengths (kvq_seqs);
   Workspace  -- a zero-filled, 256-byte aligned device buffer;
-  Allocator  -- the host page allocator (free list + reference counts).
+  Allocator  -- the host page allocator (free list + reference counts);
+  RopeTable  -- rotary frequencies on the device (kvq_rope);
+  AttnMod    -- score forms of the new tokens' attention (kvq_attn_mod).
 """
 from __future__ import annotations
 
@@ -115,6 +117,7 @@ class Allocator:
         self.h = lib().kvq_alloc_create(int(num_blocks), int(seed))
         if not self.h:
             raise KvqError(_abi.KVQ_ERR_INVALID_ARG, "kvq_alloc_create", _abi.last_error())
+        self.num_blocks = int(num_blocks)
 
     def alloc(self, n):
         ids = (ctypes.c_int32 * max(n, 1))()
@@ -126,6 +129,31 @@ class Allocator:
 
     def free(self, page):
         check(lib().kvq_block_free(self.h, int(page)), "kvq_block_free")
+
+    def free_n(self, pages):
+        """free() for a list of pages; nothing changes when one of them is refused."""
+        ids = _i32s(pages)
+        check(lib().kvq_block_free_n(self.h, len(pages), ids), "kvq_block_free_n")
+
+    def fork(self, cache, n_tokens, pages):
+        """(pages, pairs) of a fork of a sequence of n_tokens on `pages`: the fork's own pages and the
+        (source, destination) pairs that kv_pages_copy has to copy."""
+        n = (int(n_tokens) + BLOCK_TOKENS - 1) // BLOCK_TOKENS
+        if len(pages) < n:
+            raise KvqError(_abi.KVQ_ERR_INVALID_ARG, "kvq_block_fork", f"{len(pages)} pages for {n_tokens} tokens")
+        dst, pairs, m = (ctypes.c_int32 * max(n, 1))(), (ctypes.c_int32 * 8)(), ctypes.c_int32(0)
+        check(lib().kvq_block_fork(self.h, ctypes.byref(_layout_of(cache)), int(n_tokens), _i32s(pages), dst, pairs,
+                                   ctypes.byref(m)), "kvq_block_fork")
+        return list(dst[:n]), [(pairs[2 * i], pairs[2 * i + 1]) for i in range(m.value)]
+
+    def compact(self, max_moves=None):
+        """(pairs, map): the moves that bring the used pages to the lowest ids (at most max_moves of them),
+        for kv_pages_copy, and the new id of every page, for kvq_table_remap."""
+        n = self.num_blocks if max_moves is None else int(max_moves)
+        pairs, m = (ctypes.c_int32 * max(2 * n, 1))(), ctypes.c_int32(0)
+        new_id = (ctypes.c_int32 * self.num_blocks)()
+        check(lib().kvq_block_compact(self.h, n, pairs, new_id, ctypes.byref(m)), "kvq_block_compact")
+        return [(pairs[2 * i], pairs[2 * i + 1]) for i in range(m.value)], list(new_id)
 
     def refcount(self, page):
         r = lib().kvq_block_refcount(self.h, int(page))
@@ -141,6 +169,71 @@ class Allocator:
         if h:
             lib().kvq_alloc_destroy(h)
             self.h = None
+
+
+class RopeTable:
+    """Rotary frequencies of kv_qk_norm_rope, laid out once: kvq_rope plus its device steps and mscale.
+
+    scaling: "plain", "linear", "ntk", "yarn" (low > high: fast and slow turns, 32 and 1 by default) or
+    "knees" (low < high turns, 1 and 4 by default), as KVQ_ROPE_* in kvq.h."""
+
+    def __init__(self, rot_dim=HEAD_DIM, base=10000.0, interleaved=False, scaling="plain", factor=1.0, original_len=0,
+                 low=None, high=None, device="cuda"):
+        if scaling not in _abi.ROPE_SCALINGS:
+            raise KvqError(_abi.KVQ_ERR_UNSUPPORTED, "kvq_rope_steps", f"scaling {scaling!r}")
+        d_low, d_high = (32.0, 1.0) if scaling == "yarn" else (1.0, 4.0)
+        self.c = _abi.Rope(int(rot_dim), int(bool(interleaved)), _abi.ROPE_SCALINGS[scaling], int(original_len),
+                           float(base), float(factor), d_low if low is None else float(low),
+                           d_high if high is None else float(high))
+        steps, m = (ctypes.c_uint64 * max(1, int(rot_dim) // 2))(), ctypes.c_float(0)
+        check(lib().kvq_rope_steps(ctypes.byref(self.c), steps, ctypes.byref(m)), "kvq_rope_steps")
+        self.mscale = m.value
+        signed = [x - (1 << 64) if x >> 63 else x for x in steps]
+        self.steps = torch.tensor(signed, dtype=torch.int64, device=device)
+
+
+class AttnMod:
+    """Score forms of kv_decode_attn and kv_chunk_attn (kvq_attn_mod); keeps its tensors alive."""
+
+    def __init__(self, scale=0.0, softcap=0.0, window=0, n_sink=0, slopes=None, prefix_len=None, doc_start=None):
+        for x, dt, name in ((slopes, torch.float32, "slopes"), (prefix_len, torch.int32, "prefix_len"),
+                            (doc_start, torch.int32, "doc_start")):
+            _dev(x, dt, "kvq_attn_mod", name, optional=True)
+        self.slopes, self.prefix_len, self.doc_start = slopes, prefix_len, doc_start
+        self.c = _abi.AttnModStruct(float(scale), float(softcap), int(window), int(n_sink), _p(slopes), _p(prefix_len),
+                                    _p(doc_start))
+
+
+def _i32s(xs):
+    return (ctypes.c_int32 * max(len(xs), 1))(*[int(x) for x in xs])
+
+
+def _dev(x, dtype, fn, name, shape=None, optional=False):
+    """Refuses what would be read or written wrongly through a bare pointer: a tensor that is not on the
+    current GPU, of another type, with gaps, or smaller than `shape`."""
+    if x is None and optional:
+        return
+    why = None
+    if not isinstance(x, torch.Tensor):
+        why = "a tensor is wanted"
+    elif not x.is_cuda or x.get_device() != torch.cuda.current_device():
+        why = "not on the current GPU"
+    elif x.dtype != dtype:
+        why = f"{x.dtype} instead of {dtype}"
+    elif not x.is_contiguous():
+        why = "not contiguous"
+    elif shape is not None and tuple(x.shape) != shape:
+        why = f"shape {tuple(x.shape)} instead of {shape}"
+    if why:
+        raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, f"{name}: {why}")
+
+
+def _mod_rows(mod, fn, layout, batch, rows):
+    """The sizes of a mod's tensors against the call's."""
+    for x, n, name in ((mod.slopes, layout.n_q_heads, "slopes"), (mod.prefix_len, batch, "prefix_len"),
+                       (mod.doc_start, rows, "doc_start")):
+        if x is not None and x.numel() < n:
+            raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, f"{name}: {x.numel()} entries for {n}")
 
 
 # ------------------------------------------------------------------ the C ABI, same names
@@ -374,6 +467,125 @@ def kv_offload_gather(src_k, src_v, src_stride_h, src_rows, n_heads, sel, sel_co
     return check(lib().kv_offload_gather(_p(src_k), _p(src_v), int(src_stride_h), int(src_rows), int(n_heads),
                                          _p(sel), int(sel.shape[-1]), _p(sel_count), _p(dst_k), _p(dst_v), ws.ptr,
                                          ws.nbytes, _s(stream)), "kv_offload_gather")
+
+
+def _head_rows(x, n, heads, dtype, fn, name):
+    """Token stride of x [n][heads][d], whose heads have no gaps (a slice of a wider row is fine)."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.get_device() != torch.cuda.current_device():
+        raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, f"{name}: not a tensor on the current GPU")
+    if tuple(x.shape) != (n, heads, HEAD_DIM) or x.dtype != dtype:
+        raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, f"{name}: {x.dtype} {tuple(x.shape)} instead of "
+                       f"{dtype} {(n, heads, HEAD_DIM)}")
+    st = x.stride()
+    if st[2] != 1 or (st[1] != HEAD_DIM and heads > 1):
+        raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, f"{name}: a token's heads must lie side by side")
+    return st[0] if n > 1 else heads * HEAD_DIM
+
+
+def kv_qk_norm_rope(layout, rope, positions, q, k, q_out, k_out, q_weight=None, k_weight=None, eps=1e-6, v=None,
+                    v_out=None, stream=None):
+    """Head norms (with a weight) and rotary positions of q [n][H_q][d] and k [n][H_kv][d], fp16 or bf16,
+    into fp16 q_out and k_out; v is cast into v_out.  Each input may be None with its output.  `layout`: a
+    Layout or a cache; `rope`: a RopeTable."""
+    fn = "kv_qk_norm_rope"
+    L = _layout_of(layout)
+    given = next((x for x in (q, k, v) if x is not None), None)
+    if given is None:
+        raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, "no rows given")
+    n, dt = given.shape[0], given.dtype
+    if dt not in (torch.float16, torch.bfloat16):
+        raise KvqError(_abi.KVQ_ERR_UNSUPPORTED, fn, f"{dt}: float16 or bfloat16")
+    stride = []
+    for x, y, heads, name in ((q, q_out, L.n_q_heads, "q"), (k, k_out, L.n_kv_heads, "k"), (v, v_out, L.n_kv_heads, "v")):
+        if (x is None) != (y is None):
+            raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, f"{name} and {name}_out come together")
+        stride.append(0 if x is None else _head_rows(x, n, heads, dt, fn, name))
+        _dev(y, torch.float16, fn, name + "_out", (n, heads, HEAD_DIM), optional=True)
+    _dev(q_weight, torch.float32, fn, "q_weight", (HEAD_DIM,), optional=True)
+    _dev(k_weight, torch.float32, fn, "k_weight", (HEAD_DIM,), optional=True)
+    _dev(positions, torch.int32, fn, "positions", (n,), optional=rope.c.rot_dim == 0)
+    return check(lib().kv_qk_norm_rope(ctypes.byref(L), ctypes.byref(rope.c), _p(rope.steps), rope.mscale,
+                                       _abi.F16 if dt == torch.float16 else _abi.BF16, n, _p(positions), _p(q), stride[0],
+                                       _p(k), stride[1], _p(v), stride[2], _p(q_weight), _p(k_weight), float(eps),
+                                       _p(q_out), _p(k_out), _p(v_out), _s(stream)), fn)
+
+
+def kv_decode_attn_ws(cache, seqs):
+    return lib().kv_decode_attn_ws(_ref(cache.layout), _ref(seqs))
+
+
+def kv_decode_attn(cache, seqs, q, out, ws, mod=None, lse=None, stream=None):
+    """Attention of one new token per sequence over an fp16 layer; q [B][H_q][d] fp16, out fp32, `mod` an
+    AttnMod, lse [B][H_q] fp32 (optional)."""
+    fn, L = "kv_decode_attn", cache.layout
+    B, shape = seqs.c.batch, (seqs.c.batch, L.n_q_heads, HEAD_DIM)
+    _dev(q, torch.float16, fn, "q", shape)
+    _dev(out, torch.float32, fn, "out", shape)
+    _dev(lse, torch.float32, fn, "lse", shape[:2], optional=True)
+    if mod is not None:
+        _mod_rows(mod, fn, L, B, B)
+    return check(lib().kv_decode_attn(_ref(L), _ref(cache), _ref(seqs), _p(q), _ref(mod) if mod is not None else None,
+                                      _p(out), _p(lse), ws.ptr, ws.nbytes, _s(stream)), fn)
+
+
+def kv_chunk_attn_ws(cache, seqs, n_rows, max_new):
+    return lib().kv_chunk_attn_ws(_ref(cache.layout), _ref(seqs), int(n_rows), int(max_new))
+
+
+def kv_chunk_attn(cache, seqs, q, q_starts, max_new, out, ws, mod=None, lse=None, stream=None):
+    """Attention of the last q_starts[b+1] - q_starts[b] (at most max_new) tokens of every sequence over an
+    fp16 layer; q and out [n_rows][H_q][d] fp16, lse [n_rows][H_q] fp32 (optional)."""
+    fn, L = "kv_chunk_attn", cache.layout
+    B, n = seqs.c.batch, q.shape[0]
+    shape = (n, L.n_q_heads, HEAD_DIM)
+    _dev(q, torch.float16, fn, "q", shape)
+    _dev(out, torch.float16, fn, "out", shape)
+    _dev(lse, torch.float32, fn, "lse", shape[:2], optional=True)
+    _dev(q_starts, torch.int32, fn, "q_starts", (B + 1,))
+    if mod is not None:
+        _mod_rows(mod, fn, L, B, n)
+    return check(lib().kv_chunk_attn(_ref(L), _ref(cache), _ref(seqs), _p(q), _p(q_starts), n, int(max_new),
+                                     _ref(mod) if mod is not None else None, _p(out), _p(lse), ws.ptr, ws.nbytes,
+                                     _s(stream)), fn)
+
+
+def _pairs(pairs, fn):
+    _dev(pairs, torch.int32, fn, "pairs", (pairs.shape[0], 2))
+    return pairs.shape[0]
+
+
+def kv_pages_copy_ws():
+    return lib().kv_pages_copy_ws()
+
+
+def kv_pages_copy(cache, pairs, ws, stream=None):
+    """Copies page pairs[i][0] to page pairs[i][1] (device int32 [n][2]) in every array of the layer."""
+    n = _pairs(pairs, "kv_pages_copy")
+    return check(lib().kv_pages_copy(_ref(cache.layout), _ref(cache), _p(pairs), n, ws.ptr, ws.nbytes, _s(stream)),
+                 "kv_pages_copy")
+
+
+def kv_slots_copy_ws():
+    return lib().kv_slots_copy_ws()
+
+
+def kv_slots_copy(cache, seqs, pairs, ws, stream=None):
+    """Copies the per-sequence state (k_tail, or kT and k_absmax) of slot pairs[i][0] to slot pairs[i][1]."""
+    n = _pairs(pairs, "kv_slots_copy")
+    return check(lib().kv_slots_copy(_ref(cache.layout), _ref(cache), _ref(seqs), _p(pairs), n, ws.ptr, ws.nbytes,
+                                     _s(stream)), "kv_slots_copy")
+
+
+def kvq_table_remap_ws():
+    return lib().kvq_table_remap_ws()
+
+
+def kvq_table_remap(block_table, new_id, ws, stream=None):
+    """block_table[...] = new_id[block_table[...]], in place (device int32; negative entries stay)."""
+    _dev(block_table, torch.int32, "kvq_table_remap", "block_table")
+    _dev(new_id, torch.int32, "kvq_table_remap", "new_id", (new_id.numel(),))
+    return check(lib().kvq_table_remap(_p(block_table), block_table.numel(), _p(new_id), new_id.numel(), ws.ptr,
+                                       ws.nbytes, _s(stream)), "kvq_table_remap")
 
 
 def kvq_seq_lens_add(seq_lens, delta, stream=None):

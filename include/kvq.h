@@ -9,7 +9,11 @@
  * host-link gather of offloaded rows, block-granular and GQA-shared
  * selection, a layer whose kv heads are classified one by one (dense or
  * sparse), isolated fp16 outlier key channels beside a quantized cache, an
- * FP8 E4M3 cache and symmetric V quantization.
+ * FP8 E4M3 cache and symmetric V quantization.  Beside that path stand the
+ * operators a serving program needs around a cache: head norms with rotary
+ * positions, attention of new tokens (a prompt, a chunk, drafted tokens, one
+ * token) over an fp16 layer with capped, biased and masked scores, and copies of
+ * pages and slots for forks and compaction.
  *
  * Sources cited below (page, then section):
  *   [TailorKV]  "TailorKV" article, ijyty.com/news/1204784
@@ -624,6 +628,160 @@ int kv_offload_gather(const uint16_t* src_k, const uint16_t* src_v, int64_t src_
 size_t kv_offload_gather_ws(void);
 
 /* ------------------------------------------------------------------------
+ * kv_qk_norm_rope -- norms of the query and key heads and their rotary
+ * positions in one pass, from a projection's rows to the rows that
+ * kv_quant_pack, kv_page_append and the attention calls take.
+ * (An addition of this library, like every call down to "Device helpers": the
+ * pages take rotated q and k as given.)
+ *
+ * Per head row x of d values at position p, with fp32 weight w (or none):
+ *   y = x * w / sqrt(mean(x^2) + eps)          (no weight: y = x)
+ *   z_a = mscale (y_a cos - y_b sin), z_b = mscale (y_b cos + y_a sin)
+ * for the pairs (a, b) of the first rot_dim values at angle p * f_i, i <
+ * rot_dim/2: (i, i + rot_dim/2) in the half layout, (2i, 2i + 1) in the
+ * interleaved one; values behind rot_dim stay y.  fp32 arithmetic, one rounding
+ * to fp16 at the end (values beyond its range become infinite).  v rows are only
+ * cast.  The inverse rotation is the call with negated positions.
+ *
+ * Frequencies travel as 64-bit fractions of a turn per position: steps[i] =
+ * f_i/2pi * 2^64, device uint64 [rot_dim/2], so that an angle is exact at every
+ * position.  kvq_rope_steps (host code) fills them and mscale from the
+ * description below; an own list is as good.
+ *
+ * dtype: of q, k and v, KVQ_F16 or KVQ_BF16.  q [n_tokens][H_q][d], k and v
+ * [n_tokens][H_kv][d], device, 16-byte aligned, with `*_stride` elements between
+ * tokens (multiples of 8; so slices of one projection row work).  Each may be
+ * NULL together with its output.  positions: device int32 [n_tokens], any order,
+ * any sign.  Outputs: device fp16 without gaps, 16-byte aligned.  In place only
+ * for fp16 rows without gaps; otherwise outputs overlap no input.
+ * rot_dim: a multiple of 16, 0 .. 128 (0: norm and cast only; positions and
+ * steps may then be NULL).  Head counts are free here (any H_q, H_kv > 0).
+ * No workspace.  Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ * ---------------------------------------------------------------------- */
+#define KVQ_F16   0
+#define KVQ_BF16  1
+
+/* How frequencies f_i = base^(-2i/rot_dim) are scaled for long contexts. */
+#define KVQ_ROPE_PLAIN   0  /* not at all */
+#define KVQ_ROPE_LINEAR  1  /* f_i / factor (positions interpolated) */
+#define KVQ_ROPE_NTK     2  /* base * factor^(rot_dim/(rot_dim - 2)) */
+#define KVQ_ROPE_YARN    3  /* YaRN: pairs that turn more than `low` times within original_len
+                               stay, those that turn less than `high` times are divided by
+                               factor, a ramp over the pair index between (its ends at whole
+                               pairs); mscale = 0.1 ln(factor) + 1.  low > high, e.g. 32 and 1 */
+#define KVQ_ROPE_KNEES   4  /* pairs that turn more than `high` times within original_len stay,
+                               less than `low` times are divided by factor, a ramp over the
+                               number of turns between.  low < high, e.g. 1 and 4 */
+
+typedef struct kvq_rope {
+    int32_t rot_dim;
+    int32_t interleaved;   /* 0: half layout, 1: interleaved pairs */
+    int32_t scaling;       /* KVQ_ROPE_* */
+    int32_t original_len;  /* YARN, KNEES: the context length before scaling */
+    double  base;          /* > 1 */
+    double  factor;        /* >= 1 (unused by PLAIN) */
+    double  low, high;     /* YARN, KNEES */
+} kvq_rope;
+
+/* steps: host uint64 [rot_dim/2]; mscale: host.  fp64 arithmetic. */
+int kvq_rope_steps(const kvq_rope* rope, uint64_t* steps, float* mscale);
+
+int kv_qk_norm_rope(const kvq_layout* layout, const kvq_rope* rope, const uint64_t* steps, float mscale,
+                    int32_t dtype, int64_t n_tokens, const int32_t* positions,
+                    const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                    const void* v, int64_t v_stride,
+                    const float* q_weight, const float* k_weight, float eps,
+                    uint16_t* q_out, uint16_t* k_out, uint16_t* v_out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Score forms of kv_decode_attn and kv_chunk_attn (host struct, read during the
+ * call; NULL or all zero: softmax of q.k/sqrt(d) over the causal tokens).
+ * For the query at position i and the cached token j:
+ *   s = scale * q.k                       (scale 0: 1/sqrt(d))
+ *   s = softcap * tanh(s / softcap)       (softcap > 0)
+ *   s = s - slopes[h] * |i - j|           (slopes: device fp32 [H_q])
+ * j is visible when doc <= j < hi and, with window > 0, also (j > i - window or
+ * j < doc + n_sink); hi = min(max(i + 1, prefix_len[b]), T): the tokens before
+ * prefix_len[b] (device int32 [batch]) see one another both ways.  doc is the
+ * position where the query's document begins (doc_start: device int32, one entry
+ * per query row; NULL: 0), which may lie behind the query: it then sees nothing.
+ * A query that sees nothing gets output 0 and lse -inf.
+ * ---------------------------------------------------------------------- */
+typedef struct kvq_attn_mod {
+    float   scale;
+    float   softcap;
+    int32_t window;   /* 0: none; else the newest `window` tokens, the query's own included */
+    int32_t n_sink;   /* read with window > 0 */
+    const float*   slopes;
+    const int32_t* prefix_len;
+    const int32_t* doc_start;
+} kvq_attn_mod;
+
+/* ------------------------------------------------------------------------
+ * kv_decode_attn -- attention of one new token per sequence over every visible
+ * token of an fp16 layer (bits == 16; k16 and v16 through the block table), the
+ * context split over CTAs and joined.  The newest token (position seq_lens[b] - 1)
+ * must be in the cache already (kv_page_append).
+ * q: device fp16 [batch][H_q][d]; out: device fp32 [batch][H_q][d]; lse
+ * (optional): device fp32 [batch][H_q], the natural log of the softmax
+ * denominator.  An empty sequence gives 0 and -inf.  Exact fp16 products, fp32
+ * sums, the weights as two fp16 halves (22 bits).  Results do not depend on the
+ * run (parts are joined in their order).  Pages that hold no visible token are
+ * not read and their block table entries may be stale; rows that are not visible
+ * may hold anything, NaN included.  q, out, k16, v16 16-byte aligned.
+ * ws: kv_decode_attn_ws(layout, seqs) bytes.
+ * ---------------------------------------------------------------------- */
+int kv_decode_attn(const kvq_layout* layout, const kvq_pool* pool, const kvq_seqs* seqs,
+                   const uint16_t* q, const kvq_attn_mod* mod, float* out, float* lse,
+                   void* ws, size_t ws_bytes, void* stream);
+size_t kv_decode_attn_ws(const kvq_layout* layout, const kvq_seqs* seqs);
+
+/* ------------------------------------------------------------------------
+ * kv_chunk_attn -- attention of a run of new tokens per sequence (a whole
+ * prompt, a chunk of it, drafted tokens) over the same pages.
+ * Rows q_starts[b] .. q_starts[b+1] - 1 of q are the last tokens of sequence b,
+ * in order: their K and V are in the cache already and seq_lens[b] counts them.
+ * q_starts: device int32 [batch + 1], ascending, the last at most n_rows; a
+ * sequence may have none.  max_new: host upper bound on a sequence's rows.
+ * q: device fp16 [n_rows][H_q][d]; out: device fp16 [n_rows][H_q][d]; lse
+ * (optional): device fp32 [n_rows][H_q].  Rows behind q_starts[batch] are left as
+ * they were.  Exact fp16 products and fp32 sums; the softmax weights enter the
+ * value product in fp16.  Pages without a visible token are not read.  K and V
+ * rows that some query of the call sees must be finite (a row that a query does
+ * not see may share a tile with rows that it sees); rows at and behind
+ * seq_lens[b] may hold anything.  q, out, k16, v16 16-byte aligned.
+ * ws: kv_chunk_attn_ws(layout, seqs, n_rows, max_new) bytes.
+ * ---------------------------------------------------------------------- */
+int kv_chunk_attn(const kvq_layout* layout, const kvq_pool* pool, const kvq_seqs* seqs,
+                  const uint16_t* q, const int32_t* q_starts, int64_t n_rows, int32_t max_new,
+                  const kvq_attn_mod* mod, uint16_t* out, float* lse,
+                  void* ws, size_t ws_bytes, void* stream);
+size_t kv_chunk_attn_ws(const kvq_layout* layout, const kvq_seqs* seqs, int64_t n_rows, int32_t max_new);
+
+/* ------------------------------------------------------------------------
+ * kv_pages_copy -- kv_page_copy for a list of pages in one launch: every array
+ * of page pairs[i][0] to page pairs[i][1], i < n_pairs (device int32
+ * [n_pairs][2]).  A pair of equal ids copies nothing; an id outside the pool is
+ * skipped and flagged.  No id may be a destination twice or both a source and a
+ * destination (kvq_block_fork and kvq_block_compact give such lists).  Page
+ * arrays 16-byte aligned.  ws: kv_pages_copy_ws() bytes (status word only).
+ * ---------------------------------------------------------------------- */
+int kv_pages_copy(const kvq_layout* layout, const kvq_pool* pool, const int32_t* pairs, int32_t n_pairs,
+                  void* ws, size_t ws_bytes, void* stream);
+size_t kv_pages_copy_ws(void);
+
+/* kv_slots_copy -- the per-sequence state of a fork, which no page holds: k_tail
+ * of a quantized layer, kT (the seq_lens[src] tokens in use) and k_absmax of an
+ * fp16 layer, from slot pairs[i][0] to slot pairs[i][1] (device int32
+ * [n_pairs][2]; rules as kv_pages_copy, ids in [0, max_seqs)).  A source slot of
+ * a layer with kT must be below batch (its length is read).  Layers without
+ * slot state copy nothing.  Slot arrays 16-byte aligned.
+ * ws: kv_slots_copy_ws() bytes (status word only). */
+int kv_slots_copy(const kvq_layout* layout, const kvq_pool* pool, const kvq_seqs* seqs, const int32_t* pairs,
+                  int32_t n_pairs, void* ws, size_t ws_bytes, void* stream);
+size_t kv_slots_copy_ws(void);
+
+/* ------------------------------------------------------------------------
  * Device helpers.
  * ---------------------------------------------------------------------- */
 
@@ -634,6 +792,14 @@ int kvq_seq_lens_add(int32_t* seq_lens, int32_t batch, int32_t delta, void* stre
  * page dst (both in [0, num_blocks)) for the layer described by layout/pool. */
 int kv_page_copy(const kvq_layout* layout, const kvq_pool* pool, int32_t src, int32_t dst,
                  void* stream);
+
+/* block_table[i] = map[block_table[i]] for i < n_entries (device int32): the
+ * tables of a compacted pool, map [num_blocks] from kvq_block_compact.  Negative
+ * entries stay; entries at or above num_blocks stay and are flagged.
+ * ws: kvq_table_remap_ws() bytes (status word only). */
+int kvq_table_remap(int32_t* block_table, int64_t n_entries, const int32_t* map, int64_t num_blocks,
+                    void* ws, size_t ws_bytes, void* stream);
+size_t kvq_table_remap_ws(void);
 
 /* Synchronizes the stream, reads and clears the status word of a workspace.
  * Returns KVQ_OK, KVQ_ERR_DEVICE_CHECK (with the failing check in
@@ -675,6 +841,25 @@ int     kvq_block_alloc(kvq_allocator* a, int32_t n, int32_t* ids);
 int     kvq_block_ref(kvq_allocator* a, int32_t id);
 /* Drop a reference; the page returns to the free list at zero. */
 int     kvq_block_free(kvq_allocator* a, int32_t id);
+/* kvq_block_free for n pages at once; an id may be listed as often as it has
+ * references.  Nothing changes when one of them is refused. */
+int     kvq_block_free_n(kvq_allocator* a, int32_t n, const int32_t* ids);
+/* Forks a sequence of n_tokens on src_pages[0 .. ceil(n_tokens/16)): pages that
+ * neither branch writes again are shared (a reference each); the others get a
+ * fresh page each and a (source, destination) pair for kv_pages_copy: the last,
+ * partly filled page, and for a quantized layer every page of the unfinished
+ * 64-token K group, whose codes are written when a branch completes it.
+ * dst_pages: out, as many entries as src_pages; pairs: out int32 [4][2].
+ * NO_SPACE (nothing taken) when too few pages are free.  The slot state goes
+ * with kv_slots_copy. */
+int     kvq_block_fork(kvq_allocator* a, const kvq_layout* layout, int64_t n_tokens, const int32_t* src_pages,
+                       int32_t* dst_pages, int32_t* pairs, int32_t* n_pairs);
+/* Moves the highest used pages into the lowest free ones, at most max_moves of
+ * them, until the used pages are the lowest ids: pairs (out int32
+ * [max_moves][2]) for kv_pages_copy, map (out int32 [num_blocks], the new id of
+ * every page) for kvq_table_remap, reference counts moved along.  Free pages are
+ * handed out lowest first afterwards. */
+int     kvq_block_compact(kvq_allocator* a, int32_t max_moves, int32_t* pairs, int32_t* map, int32_t* n_moves);
 /* Reference count of a page (0 = free), or a negative error. */
 int     kvq_block_refcount(const kvq_allocator* a, int32_t id);
 int64_t kvq_alloc_num_free(const kvq_allocator* a);
