@@ -1,7 +1,22 @@
 // kv_chunk_attn: attention of a run of new tokens per sequence over an fp16 layer's pages.
 //
-// One warp per (new token, query head), four dims per lane: the plain recurrence of the running maximum
-// and sum over the visible tokens, in fp32.
+// Bound: the tensor cores from a few dozen query rows per kv head on (4 d flops per visible pair), below
+// that the bytes of the cache.  One CTA takes up to 256 query rows of one kv head as two tiles of 128:
+// row r is new token r / GQ, query head r % GQ of the group, so that the heads of a group share every
+// staged K/V tile and a short run still fills rows.  Tiles of 128 cached tokens are eight pages, each
+// fetched through the block table by its own TMA boxes (16 rows x 128 bytes, 128-byte swizzle).
+//
+//   warps 8-11 give most of their registers to the softmax warps; 10 and 11 do nothing else
+//   warp 9     loads: Q once, then K and V tiles into a ring of shared-memory stages
+//   warp 8     issues tcgen05.mma: S_i = Q_i K^T into TMEM, O_i += P_i V with P_i read from TMEM
+//   warps 0-3  softmax of tile 0: one thread per row, S from TMEM, P as fp16 back over S
+//   warps 4-7  softmax of tile 1
+//
+// While one tile's softmax runs, the tensor cores work for the other one.  O stays in TMEM over the whole
+// loop; a row is rescaled only when its maximum grew by more than 2^8 since the last time (P is at most
+// 256 then, well inside fp16, and the exponent of the kept maximum cancels at the end).
+#include <cuda.h>
+
 #include <algorithm>
 
 #include "kvq_attn_mod.cuh"
@@ -10,67 +25,661 @@ namespace {
 
 constexpr int D = KVQ_HEAD_DIM;
 constexpr int PG = KVQ_BLOCK_TOKENS;
-constexpr int CA_NT = 128;
+constexpr int CA_NT = 384;
+constexpr int CA_ROWS = 256;             // query rows per CTA
+constexpr int CA_KEYS = 128;             // cached tokens per tile
+constexpr int CA_NS = 4;                 // K or V tiles in the ring
+constexpr int CA_TILE = 128 * D * 2;     // bytes of a Q, K or V tile: two halves of 128 rows x 128 bytes
+constexpr int CA_HALF = CA_TILE / 2;
+constexpr int CA_SMEM = 2 * CA_TILE + CA_NS * CA_TILE + 1024;
+constexpr uint32_t CA_SPIN = 1u << 16;   // bound on the polls of one mbarrier wait
+constexpr float CA_SLACK = 8.0f;         // log2 growth of a row's maximum before O is rescaled
+
+// TMEM columns: S (and P over it) of the two tiles, then their O
+constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
 
 struct ChunkArgs {
-    const uint16_t *k16, *v16, *q;
-    int64_t num_blocks;
     const int32_t *bt, *seq_lens, *q_starts;
-    int32_t batch, max_blocks, max_len, max_new, H, GQ;
+    int64_t num_blocks;
+    int32_t batch, max_blocks, max_len, max_new, H, GQ, n_splits;
     int64_t n_rows;
     KvqModArgs mod;
     uint16_t* out;
     float* lse;
+    float* part;   // [item][split][CA_ROWS][D]
+    float2* ml;    // [item][split][CA_ROWS] maximum (log2) and sum
     KvqWsHeader* hdr;
 };
 
-__global__ void __launch_bounds__(CA_NT) chunk_attn_kernel(ChunkArgs a) {
-    const int b = blockIdx.y, lane = threadIdx.x & 31;
-    const int Hq = a.H * a.GQ;
-    const int64_t item = (int64_t)blockIdx.x * (CA_NT / 32) + (threadIdx.x >> 5);
-    const int i = (int)(item / Hq), hq = (int)(item % Hq);
-    const int first = a.q_starts[b], n = a.q_starts[b + 1] - first, T = a.seq_lens[b];
-    if (first < 0 || n < 0 || n > a.max_new || (int64_t)first + n > a.n_rows || T < n || T > a.max_len) {
-        if (item == 0 && lane == 0) kvq_dev_flag(a.hdr, KVQ_DEV_BAD_LENGTH, b);
-        return;
-    }
-    if (i >= n) return;
-    const int64_t row = ((int64_t)first + i) * Hq + hq;
-    const int pos = T - n + i;
-    const KvqSee see = kvq_see(a.mod, pos, T, a.mod.prefix_len ? a.mod.prefix_len[b] : 0,
-                               a.mod.doc_start ? a.mod.doc_start[first + i] : 0);
-    const float slope = a.mod.slopes ? a.mod.slopes[hq] * KVQ_LOG2E : 0.0f;
-    float q[4], o[4] = {0, 0, 0, 0}, m = -INFINITY, l = 0.0f;
-    for (int c = 0; c < 4; ++c) q[c] = kvq_h2f(a.q[row * D + 4 * lane + c]);
-    for (int j = see.sink > see.doc ? see.doc : see.lo; j < see.hi; ++j) {
-        if (!see(j)) {
-            j = max(j, see.lo - 1);
-            continue;
-        }
-        const int32_t page = a.bt[(int64_t)b * a.max_blocks + j / PG];
-        if (page < 0 || page >= a.num_blocks) {
-            if (lane == 0) kvq_dev_flag(a.hdr, KVQ_DEV_BAD_PAGE, page);
-            continue;
-        }
-        const int64_t at = (((int64_t)page * a.H + hq / a.GQ) * PG + j % PG) * D + 4 * lane;
-        float s = 0.0f;
-        for (int c = 0; c < 4; ++c) s += q[c] * kvq_h2f(a.k16[at + c]);
-        s = kvq_warp_sum(s);
-        s = a.mod.post != 0.0f ? a.mod.post * kvq_tanh(s * a.mod.pre) : s * a.mod.pre;
-        s -= slope * (float)abs(pos - j);
-        const float mn = fmaxf(m, s), f = exp2f(m - mn), p = exp2f(s - mn);
-        m = mn;
-        l = l * f + p;
-        for (int c = 0; c < 4; ++c) o[c] = o[c] * f + p * kvq_h2f(a.v16[at + c]);
-    }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    for (int c = 0; c < 4; ++c) a.out[row * D + 4 * lane + c] = kvq_f2h(o[c] * inv);
-    if (a.lse != nullptr && lane == 0) a.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * KVQ_LN2;
+// ---------------------------------------------------------------- PTX
+
+__device__ __forceinline__ uint32_t saddr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t n) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(saddr(bar)), "r"(n) : "memory");
 }
+__device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(saddr(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(bar)) : "memory");
+}
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(map), "r"(x), "r"(y), "r"(saddr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(saddr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(saddr(bar)) : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Shared-memory matrix descriptor, 128-byte swizzle: start address, byte offsets between the 64-element
+// blocks of a matrix whose rows run along K (`lead`), and between groups of eight rows (1024 bytes here).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
+    return (uint64_t)((addr & 0x3ffff) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+// f16 x f16 -> f32, M = 128, N = 128; bit 16: B's rows run along K (V), else along N (K)
+constexpr uint32_t IDESC_QK = (1u << 4) | (128u / 8 << 17) | (128u / 16 << 24);
+constexpr uint32_t IDESC_PV = IDESC_QK | (1u << 16);
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+
+#define R8(v, o) "=r"((v)[o]), "=r"((v)[o + 1]), "=r"((v)[o + 2]), "=r"((v)[o + 3]), "=r"((v)[o + 4]), "=r"((v)[o + 5]), "=r"((v)[o + 6]), "=r"((v)[o + 7])
+#define W8(v, o) "r"((v)[o]), "r"((v)[o + 1]), "r"((v)[o + 2]), "r"((v)[o + 3]), "r"((v)[o + 4]), "r"((v)[o + 5]), "r"((v)[o + 6]), "r"((v)[o + 7])
+// 32 columns of this thread's lane; the wait is part of the statement, so nothing reads v before it
+__device__ __forceinline__ void tm_ld32(uint32_t addr, uint32_t* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : R8(v, 0), R8(v, 8), R8(v, 16), R8(v, 24)
+        : "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+        W8(v, 0), W8(v, 8), W8(v, 16), W8(v, 24)
+        : "memory");
+}
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// ---------------------------------------------------------------- what a CTA works on
+
+struct Shared {
+    uint64_t q_full, kv_full[CA_NS], kv_empty[CA_NS], s_full[2], p_full[2], o_full[2], drain;
+    uint32_t tmem;
+    int32_t abort;
+    int32_t item_b, item_tok;                     // sequence and first new token of this CTA
+    int32_t doc_min, sink_max, lo_min, hi_max;    // over its rows
+    int4 see[CA_ROWS];                            // lo, hi, doc, sink of every token
+};
+
+// Waits for a phase of bar; false after CA_SPIN polls or when another thread gave up.
+__device__ __forceinline__ bool bar_wait(Shared& S, KvqWsHeader* hdr, uint64_t* bar, uint32_t parity) {
+    for (uint32_t it = 0; it < CA_SPIN; ++it) {
+        uint32_t ok;
+        asm volatile(
+            "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+            : "=r"(ok)
+            : "r"(saddr(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if ((it & 63) == 63 && *(volatile int32_t*)&S.abort) return false;
+    }
+    *(volatile int32_t*)&S.abort = 1;
+    kvq_dev_flag(hdr, KVQ_DEV_TIMEOUT, (int32_t)blockIdx.x);
+    return false;
+}
+
+// Sequence b's new tokens: *first row and count; false (flagged) when its lengths do not fit the call.
+__device__ __forceinline__ bool seq_rows(const ChunkArgs& a, int b, int* first, int* n) {
+    *first = a.q_starts[b];
+    const int64_t cnt = (int64_t)a.q_starts[b + 1] - *first;
+    const int T = a.seq_lens[b];
+    *n = 0;
+    if (*first < 0 || cnt < 0 || cnt > a.max_new || *first + cnt > a.n_rows || T < cnt || T > a.max_len) {
+        kvq_dev_flag(a.hdr, KVQ_DEV_BAD_LENGTH, b);
+        return false;
+    }
+    *n = (int)cnt;
+    return true;
+}
+
+// One warp finds item x: the x-th group of `tpc` new tokens, sequences in order, a sequence's last group
+// (the one that sees most) first.  b = -1 when there is none.
+__device__ __forceinline__ void find_item(const ChunkArgs& a, int x, int tpc, int* b_out, int* tok_out) {
+    const int lane = threadIdx.x & 31;
+    int base = 0;
+    *b_out = -1;
+    *tok_out = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+        const int b = b0 + lane;
+        int first, n = 0;
+        if (b < a.batch) seq_rows(a, b, &first, &n);
+        const int g = (n + tpc - 1) / tpc;
+        int incl = g;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        const bool mine = x >= base + incl - g && x < base + incl;
+        const unsigned who = __ballot_sync(0xffffffffu, mine);
+        if (who) {
+            const int src = __ffs(who) - 1;
+            *b_out = b0 + src;
+            *tok_out = __shfl_sync(0xffffffffu, (base + incl - 1 - x) * tpc, src);
+            return;
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+}
+
+__device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
+// bits of the columns [a, b) of a tile in its w-th word of 32
+__device__ __forceinline__ uint32_t columns(int a, int b, int w) {
+    return b > a ? below(b - 32 * w) & ~below(a - 32 * w) : 0u;
+}
+
+template <bool CAP, bool BIAS>
+__global__ void __launch_bounds__(CA_NT, 1)
+    chunk_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                      const __grid_constant__ CUtensorMap map_v, const __grid_constant__ ChunkArgs a) {
+    extern __shared__ unsigned char raw[];
+    __shared__ Shared S;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int GQ = a.GQ, tpc = CA_ROWS / GQ, h = blockIdx.y, split = blockIdx.z;
+    const uint32_t sq = (saddr(raw) + 1023) & ~1023u, skv = sq + 2 * CA_TILE;
+    kvq_pdl_begin();
+    if (warp == 0) {
+        int b, tok;
+        find_item(a, blockIdx.x, tpc, &b, &tok);
+        if (lane == 0) {
+            S.item_b = b, S.item_tok = tok;
+            S.abort = 0;
+            S.doc_min = S.lo_min = INT32_MAX;
+            S.sink_max = S.hi_max = 0;
+        }
+    }
+    __syncthreads();
+    const int b = S.item_b, tok0 = S.item_tok;
+    if (b < 0) return;
+    const int first = a.q_starts[b], n = a.q_starts[b + 1] - first, T = a.seq_lens[b];
+    const int ntok = min(tpc, n - tok0), rows = ntok * GQ;
+    const int nq = rows > 128 ? 2 : 1;
+    if (tid < ntok) {
+        const int i = tok0 + tid;
+        const KvqSee see = kvq_see(a.mod, T - n + i, T, a.mod.prefix_len ? a.mod.prefix_len[b] : 0,
+                                   a.mod.doc_start ? a.mod.doc_start[first + i] : 0);
+        S.see[tid] = make_int4(see.lo, see.hi, see.doc, see.sink);
+        if (see.lo < see.hi) {
+            atomicMin(&S.lo_min, see.lo);
+            atomicMax(&S.hi_max, see.hi);
+        }
+        if (see.doc < see.sink) {
+            atomicMin(&S.doc_min, see.doc);
+            atomicMax(&S.sink_max, see.sink);
+        }
+    }
+    if (tid == 0) {
+        bar_init(&S.q_full, 1);
+        for (int i = 0; i < CA_NS; ++i) {
+            bar_init(&S.kv_full[i], 1);
+            bar_init(&S.kv_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&S.s_full[i], 1);
+            bar_init(&S.p_full[i], 4);
+            bar_init(&S.o_full[i], 1);
+        }
+        bar_init(&S.drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&S.tmem)), "r"(TM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = S.tmem;
+    // tiles some row sees: [a1, b1) for the sinks, then [a2, b2); this split takes [it0, it1) of the list
+    int a1 = 0, b1 = 0, a2 = 0, b2 = 0;
+    if (S.doc_min < S.sink_max) a1 = S.doc_min / CA_KEYS, b1 = (S.sink_max + CA_KEYS - 1) / CA_KEYS;
+    if (S.lo_min < S.hi_max) a2 = max(S.lo_min / CA_KEYS, b1), b2 = max(a2, (S.hi_max + CA_KEYS - 1) / CA_KEYS);
+    const int total = b1 - a1 + b2 - a2;
+    const int per = (total + a.n_splits - 1) / a.n_splits;
+    const int it0 = min(total, split * per), it1 = min(total, it0 + per), nt = it1 - it0;
+    const auto tile_of = [&](int it) { return it < b1 - a1 ? a1 + it : a2 + (it - (b1 - a1)); };
+
+    // 384 threads are launched with 168 registers each: 256 * 216 + 128 * 72 is the same total
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 9 && nt > 0) {
+            // ---- loads
+            if (lane == 0) {
+                bar_expect(&S.q_full, nq * CA_TILE);
+                for (int i = 0; i < nq; ++i)
+                    for (int c = 0; c < 2; ++c)
+                        tma_3d(sq + i * CA_TILE + c * CA_HALF, &map_q, 64 * c, h * GQ, first + tok0 + i * (128 / GQ), &S.q_full);
+            }
+            __syncwarp();
+            const int pg = lane >> 1, half = lane & 1;   // lanes 0-15: one box of K and one of V each
+            const int nowhere = (int)(a.num_blocks * a.H * PG);  // a row behind the pool: zeros
+            bool ok = true;
+            for (int j = 0; j < nt && ok; ++j) {
+                const int t = tile_of(it0 + j), lp = t * (CA_KEYS / PG) + pg;
+                uint32_t need;  // bit per page of the tile that some row sees
+                if (a.mod.doc_start == nullptr) {
+                    const int p0 = lp * PG;
+                    need = __ballot_sync(0xffffffffu, lane < 16 && ((p0 < S.hi_max && p0 + PG > S.lo_min) ||
+                                                                    (p0 < S.sink_max && p0 + PG > S.doc_min)));
+                } else {
+                    uint32_t bits = 0;
+                    for (int k = lane; k < ntok; k += 32) {
+                        const int4 e = S.see[k];
+                        const int p0 = t * (CA_KEYS / PG);
+                        if (e.x < e.y) bits |= below((e.y + PG - 1) / PG - p0) & ~below(e.x / PG - p0);
+                        if (e.z < e.w) bits |= below((e.w + PG - 1) / PG - p0) & ~below(e.z / PG - p0);
+                    }
+                    bits = __reduce_or_sync(0xffffffffu, bits) & 0xff;
+                    need = 0;
+                    for (int k = 0; k < 8; ++k) need |= (bits >> k & 1) * (3u << 2 * k);
+                }
+                int y = nowhere;
+                if (lane < 16 && (need >> lane & 1)) {
+                    const int32_t page = a.bt[(int64_t)b * a.max_blocks + lp];
+                    if (page >= 0 && page < a.num_blocks)
+                        y = (page * a.H + h) * PG;
+                    else
+                        kvq_dev_flag(a.hdr, KVQ_DEV_BAD_PAGE, page);
+                }
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    const int slot = 2 * j + v, st = slot % CA_NS;
+                    if (slot >= CA_NS && !bar_wait(S, a.hdr, &S.kv_empty[st], ((slot / CA_NS) & 1) ^ 1)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) bar_expect(&S.kv_full[st], CA_TILE);
+                    __syncwarp();
+                    if (lane < 16)
+                        tma_2d(skv + st * CA_TILE + half * CA_HALF + pg * (PG * 128), v ? &map_v : &map_k, 64 * half, y,
+                               &S.kv_full[st]);
+                }
+                ok = __all_sync(0xffffffffu, ok);
+            }
+        }
+        if (warp == 8 && lane == 0 && nt > 0) {
+            // ---- tensor cores
+            bool ok = bar_wait(S, a.hdr, &S.q_full, 0) && bar_wait(S, a.hdr, &S.kv_full[0], 0);
+            const auto qk = [&](int i, int st) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = (k >> 2) * CA_HALF + (k & 3) * 32;
+                    mma_ss(tmem + TM_S + 128 * i, smem_desc(sq + i * CA_TILE + off, 16), smem_desc(skv + st * CA_TILE + off, 16),
+                           IDESC_QK, k > 0);
+                }
+            };
+            if (ok) {
+                tc_after();
+                for (int i = 0; i < nq; ++i) {
+                    qk(i, 0);
+                    tc_commit(&S.s_full[i]);
+                }
+                tc_commit(&S.kv_empty[0]);
+            }
+            for (int j = 0; j < nt && ok; ++j) {
+                const int sv = (2 * j + 1) % CA_NS, sk = (2 * j + 2) % CA_NS;
+                const bool more = j + 1 < nt;
+                for (int i = 0; i < nq && ok; ++i) {
+                    ok = bar_wait(S, a.hdr, &S.p_full[i], j & 1) &&
+                         (i > 0 || bar_wait(S, a.hdr, &S.kv_full[sv], ((2 * j + 1) / CA_NS) & 1));
+                    if (!ok) break;
+                    tc_after();
+#pragma unroll
+                    for (int k = 0; k < CA_KEYS / 16; ++k)
+                        mma_ts(tmem + TM_O + 128 * i, tmem + TM_S + 128 * i + 8 * k,
+                               smem_desc(skv + sv * CA_TILE + k * 2048, CA_HALF), IDESC_PV, j > 0 || k > 0);
+                    if (more) {
+                        ok = i > 0 || bar_wait(S, a.hdr, &S.kv_full[sk], ((2 * j + 2) / CA_NS) & 1);
+                        if (!ok) break;
+                        tc_after();
+                        qk(i, sk);
+                        tc_commit(&S.s_full[i]);
+                    } else {
+                        tc_commit(&S.o_full[i]);
+                    }
+                }
+                if (!ok) break;
+                tc_commit(&S.kv_empty[sv]);
+                if (more) tc_commit(&S.kv_empty[sk]);
+            }
+        }
+    } else {
+        // ---- softmax: thread = row
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        const int i = warp >> 2, r = tid;   // row of the CTA
+        const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21);  // TMEM lanes 32 (warp % 4) ..
+        const uint32_t ts = lane_base + TM_S + 128 * i, to = lane_base + TM_O + 128 * i;
+        const bool valid = r < rows;
+        const int tok = r / GQ;
+        int4 see = make_int4(0, 0, 0, 0);
+        int maxlo = 0, minhi = INT32_MAX;   // over the warp's rows: tiles between need no mask
+        if (valid) {
+            see = S.see[tok];
+            maxlo = see.x, minhi = see.y;
+        }
+        maxlo = __reduce_max_sync(0xffffffffu, maxlo);
+        minhi = __reduce_min_sync(0xffffffffu, minhi);
+        const int pos = T - n + tok0 + tok;
+        const float slope2 = BIAS && valid ? a.mod.slopes[h * GQ + r % GQ] * KVQ_LOG2E : 0.0f;
+        float m = -INFINITY, l = 0.0f;
+        if (i < nq) {
+            bool ok = true;
+            for (int j = 0; j < nt && ok; ++j) {
+                const int t0 = tile_of(it0 + j) * CA_KEYS;
+                // rows at and behind T may hold anything: 0 * NaN must not reach O
+                const bool tail = T < t0 + CA_KEYS && (T & (PG - 1)) != 0 && T > t0;
+                ok = bar_wait(S, a.hdr, &S.s_full[i], j & 1) &&
+                     (!tail || bar_wait(S, a.hdr, &S.kv_full[(2 * j + 1) % CA_NS], ((2 * j + 1) / CA_NS) & 1));
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (tail) {
+                    const uint32_t base = skv + (2 * j + 1) % CA_NS * CA_TILE;
+                    const int r0 = T - t0, r1 = (r0 + PG - 1) / PG * PG;
+                    for (int x = tid & 127; x < (r1 - r0) * 16; x += 128) {
+                        const uint32_t at = base + (x & 1) * CA_HALF + (r0 + (x >> 4)) * 128 + ((x >> 1) & 7) * 16;
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                tc_after();
+                float s[128];
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) tm_ld32(ts + c, reinterpret_cast<uint32_t*>(s + c));
+                float scale = a.mod.pre;
+                if (CAP) {
+                    // tanh x = 1 - 2 / (1 + e^2x): two special-function results, 1e-7 absolute
+                    const float k2 = a.mod.pre * (2.0f * KVQ_LOG2E), p2 = -2.0f * a.mod.post;
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) s[c] = fmaf(p2, rcp(1.0f + ex2(s[c] * k2)), a.mod.post);
+                    scale = 1.0f;
+                }
+                if (BIAS) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) {
+                        const float away = (float)abs(pos - t0 - c);
+                        s[c] = CAP ? fmaf(-slope2, away, s[c]) : fmaf(s[c], a.mod.pre, -slope2 * away);
+                    }
+                    scale = 1.0f;
+                }
+                if (t0 < maxlo || t0 + CA_KEYS > minhi) {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t bits = columns(see.x - t0, see.y - t0, w) | columns(see.z - t0, see.w - t0, w);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (!(bits >> c & 1)) s[32 * w + c] = -INFINITY;
+                    }
+                }
+                float mx = s[0];
+#pragma unroll
+                for (int c = 1; c < 128; ++c) mx = fmaxf(mx, s[c]);
+                mx *= scale;
+                const bool grew = mx > m + CA_SLACK || (m == -INFINITY && mx > m);
+                float f = 1.0f;
+                if (grew) {
+                    f = ex2(m - mx);
+                    m = mx;
+                    l *= f;
+                }
+                if (j > 0 && __any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tm_ld32(to + c, o);
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                        tm_st32(to + c, o);
+                    }
+                }
+                const float ms = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+                for (int c = 0; c < 128; c += 64) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) {
+                        const float p0 = ex2(fmaf(s[c + 2 * x], scale, -ms)), p1 = ex2(fmaf(s[c + 2 * x + 1], scale, -ms));
+                        l += p0 + p1;
+                        p[x] = half2_bits(p0, p1);
+                    }
+                    tm_st32(ts + c / 2, p);
+                }
+                tm_wait_st();
+                tc_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&S.p_full[i]);
+            }
+            // ---- this row's output
+            ok = ok && (nt == 0 || bar_wait(S, a.hdr, &S.o_full[i], 0));
+            if (__all_sync(0xffffffffu, ok)) {
+                tc_after();
+                const int64_t out_row = (int64_t)(first + tok0 + tok) * a.H * GQ + h * GQ + r % GQ;
+                const int64_t part_row = (((int64_t)blockIdx.x * a.H + h) * a.n_splits + split) * CA_ROWS + r;
+                const float inv = a.n_splits > 1 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    if (nt > 0) {
+                        tm_ld32(to + c, o);
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) o[x] = 0;
+                    }
+                    if (!valid) continue;
+                    if (a.n_splits > 1) {
+                        if (nt == 0) continue;
+                        uint4* dst = reinterpret_cast<uint4*>(a.part + part_row * D + c);
+#pragma unroll
+                        for (int x = 0; x < 32; x += 4) dst[x / 4] = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+                    } else {
+                        uint4* dst = reinterpret_cast<uint4*>(a.out + out_row * D + c);
+                        uint32_t w[16];
+#pragma unroll
+                        for (int x = 0; x < 16; ++x)
+                            w[x] = half2_bits(__uint_as_float(o[2 * x]) * inv, __uint_as_float(o[2 * x + 1]) * inv);
+#pragma unroll
+                        for (int x = 0; x < 16; x += 4) dst[x / 4] = make_uint4(w[x], w[x + 1], w[x + 2], w[x + 3]);
+                    }
+                }
+                if (valid && a.n_splits > 1) a.ml[part_row] = make_float2(m, l);
+                if (valid && a.n_splits == 1 && a.lse != nullptr)
+                    a.lse[out_row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * KVQ_LN2;
+            }
+        }
+    }
+    __syncwarp();
+    __syncthreads();
+    if (*(volatile int32_t*)&S.abort) {
+        // a wait gave up: let this CTA's own copies and products land (again with a limit) before it ends
+        if (warp == 8 && lane == 0) {
+            tc_commit(&S.drain);
+            bool ok = false;
+            for (uint32_t it = 0; it < CA_SPIN && !ok; ++it) {
+                uint32_t done;
+                asm volatile(
+                    "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+                    : "=r"(done)
+                    : "r"(saddr(&S.drain)), "r"(0)
+                    : "memory");
+                ok = done;
+            }
+        }
+        const long long began = clock64();
+        while (clock64() - began < 2000000) __nanosleep(1000);  // about a millisecond: far above a copy's time
+        __syncthreads();
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    if (warp == 8)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TM_COLS) : "memory");
+}
+
+// Joins the splits of 32 rows of an item in their order and leaves the workspace zeroed.
+constexpr int CJ_NT = 256;
+__global__ void __launch_bounds__(CJ_NT) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
+    __shared__ int item_b, item_tok;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int GQ = a.GQ, tpc = CA_ROWS / GQ, h = blockIdx.y;
+    kvq_pdl_begin();
+    if (warp == 0) {
+        int b, tok;
+        find_item(a, blockIdx.x, tpc, &b, &tok);
+        if (lane == 0) item_b = b, item_tok = tok;
+    }
+    __syncthreads();
+    if (item_b < 0) return;
+    const int first = a.q_starts[item_b], n = a.q_starts[item_b + 1] - first;
+    const int rows = min(tpc, n - item_tok) * GQ;
+    for (int r = blockIdx.z * 32 + warp; r < min(rows, (int)blockIdx.z * 32 + 32); r += CJ_NT / 32) {
+        const int64_t p0 = ((int64_t)blockIdx.x * a.H + h) * a.n_splits * CA_ROWS + r;
+        float mx = -INFINITY;
+        for (int s = lane; s < a.n_splits; s += 32) mx = fmaxf(mx, a.ml[p0 + (int64_t)s * CA_ROWS].x);
+        mx = kvq_warp_max(mx);
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float y = 0.0f;
+        for (int s = 0; s < a.n_splits; ++s) {
+            const int64_t row = p0 + (int64_t)s * CA_ROWS;
+            const float2 v = a.ml[row];
+            if (v.y == 0.0f) continue;
+            const float f = v.x == -INFINITY ? 0.0f : exp2f(v.x - mx);
+            float4* part = reinterpret_cast<float4*>(a.part + row * D) + lane;
+            const float4 w = *part;
+            x.x += f * w.x;
+            x.y += f * w.y;
+            x.z += f * w.z;
+            x.w += f * w.w;
+            y += f * v.y;
+        }
+        __syncwarp();
+        for (int s = 0; s < a.n_splits; ++s)
+            reinterpret_cast<float4*>(a.part + (p0 + (int64_t)s * CA_ROWS) * D)[lane] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int s = lane; s < a.n_splits; s += 32) a.ml[p0 + (int64_t)s * CA_ROWS] = make_float2(0.0f, 0.0f);
+        const float inv = y == 0.0f ? 0.0f : 1.0f / y;
+        const int64_t out_row = (int64_t)(first + item_tok + r / GQ) * a.H * GQ + h * GQ + r % GQ;
+        reinterpret_cast<uint2*>(a.out + out_row * D)[lane] =
+            make_uint2(half2_bits(x.x * inv, x.y * inv), half2_bits(x.z * inv, x.w * inv));
+        if (a.lse != nullptr && lane == 0) a.lse[out_row] = y == 0.0f ? -INFINITY : (mx + log2f(y)) * KVQ_LN2;
+    }
+}
+
+// ---------------------------------------------------------------- host
 
 int check_rows(int64_t n_rows, int32_t max_new, const char* fn) {
     KVQ_REQUIRE(n_rows >= 0 && n_rows <= INT32_MAX && max_new >= 0 && (n_rows == 0 || max_new > 0), KVQ_ERR_INVALID_ARG,
                 "%s: n_rows / max_new", fn);
+    return KVQ_OK;
+}
+
+struct ChunkPlan {
+    int64_t items;   // groups of new tokens over all sequences, at most
+    int n_splits;
+    size_t off_ml, off_part, bytes;
+};
+
+// Enough (item, kv head) CTAs fill the SMs by themselves; fewer are split along the cache, into the
+// smallest number of parts that keeps the last wave at least 90% full, four tiles per part at least.
+ChunkPlan chunk_plan(const kvq_layout* L, const kvq_seqs* S, int64_t n_rows, int32_t max_new) {
+    ChunkPlan p;
+    const int tpc = CA_ROWS / (L->n_q_heads / L->n_kv_heads);
+    const int64_t by_max = (int64_t)S->batch * ((max_new + tpc - 1) / tpc);
+    p.items = std::max<int64_t>(1, std::min(by_max, n_rows / tpc + S->batch));
+    const int64_t ctas = p.items * L->n_kv_heads, sms = kvq_num_sms();
+    const int tiles = (S->max_len + CA_KEYS - 1) / CA_KEYS;
+    p.n_splits = 1;
+    if (ctas < sms) {
+        double best = 0.0;
+        const int most = (int)std::min<int64_t>(std::max(1, tiles / 4), 4 * sms / ctas);
+        for (int s = 1; s <= most; ++s) {
+            const int64_t waves = (ctas * s + sms - 1) / sms;
+            const double fill = (double)(ctas * s) / (double)(waves * sms);
+            if (fill > best + 1e-9) best = fill, p.n_splits = s;
+            if (fill >= 0.9) break;
+        }
+    }
+    const size_t rows = p.n_splits > 1 ? (size_t)ctas * p.n_splits * CA_ROWS : 0;
+    p.off_ml = sizeof(KvqWsHeader);
+    p.off_part = kvq_round_up(p.off_ml + rows * sizeof(float2), 256);
+    p.bytes = kvq_round_up(p.off_part + rows * D * sizeof(float), 256);
+    return p;
+}
+
+// A tensor map of fp16 rows of d values, 64-value boxes of the given rows, 128-byte swizzle.
+int make_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+             const char* fn) {
+    using Encode = decltype(&cuTensorMapEncodeTiled);
+    static Encode encode = nullptr;
+    if (encode == nullptr) {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
+        if (e != cudaSuccess || found != cudaDriverEntryPointSuccess || f == nullptr) {
+            cudaGetLastError();
+            return kvq_fail(KVQ_ERR_CUDA, "%s: the driver has no cuTensorMapEncodeTiled", fn);
+        }
+        encode = reinterpret_cast<Encode>(f);
+    }
+    const cuuint32_t ones[3] = {1, 1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, const_cast<void*>(base),
+                              reinterpret_cast<const cuuint64_t*>(dims), reinterpret_cast<const cuuint64_t*>(strides),
+                              box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return kvq_fail(KVQ_ERR_CUDA, "%s: tensor map (%d)", fn, (int)r);
     return KVQ_OK;
 }
 
@@ -80,7 +689,7 @@ extern "C" size_t kv_chunk_attn_ws(const kvq_layout* L, const kvq_seqs* S, int64
     if (kvq_check_layout(L, "kv_chunk_attn_ws", true) || kvq_check_seqs_sizes(S, "kv_chunk_attn_ws") ||
         check_rows(n_rows, max_new, "kv_chunk_attn_ws"))
         return 0;
-    return sizeof(KvqWsHeader);
+    return chunk_plan(L, S, n_rows, max_new).bytes;
 }
 
 extern "C" int kv_chunk_attn(const kvq_layout* L, const kvq_pool* P, const kvq_seqs* S, const uint16_t* q,
@@ -94,28 +703,53 @@ extern "C" int kv_chunk_attn(const kvq_layout* L, const kvq_pool* P, const kvq_s
     st = kvq_check_seqs(S, fn);
     if (st) return st;
     KVQ_REQUIRE(P && P->k16 && P->v16 && P->num_blocks > 0, KVQ_ERR_INVALID_ARG, "%s: pool needs k16 and v16", fn);
-    KVQ_REQUIRE(S->batch <= 65535 && L->n_kv_heads <= 65535, KVQ_ERR_UNSUPPORTED, "%s: batch or heads", fn);
+    const int64_t pool_rows = P->num_blocks * L->n_kv_heads * PG;
+    KVQ_REQUIRE(P->num_blocks <= INT32_MAX && pool_rows <= INT32_MAX && L->n_kv_heads <= 65535, KVQ_ERR_UNSUPPORTED,
+                "%s: more than 2^31 - 1 rows in the pool", fn);
     st = check_rows(n_rows, max_new, fn);
     if (st) return st;
     ChunkArgs a;
     st = kvq_mod_args(mod, fn, &a.mod);
     if (st) return st;
-    st = kvq_check_ws(ws, ws_bytes, sizeof(KvqWsHeader), fn);
+    const ChunkPlan p = chunk_plan(L, S, n_rows, max_new);
+    st = kvq_check_ws(ws, ws_bytes, p.bytes, fn);
     if (st) return st;
     if (S->batch == 0 || n_rows == 0) return KVQ_OK;
     KVQ_REQUIRE(q && out && q_starts && (S->block_table || S->max_len == 0), KVQ_ERR_INVALID_ARG, "%s: NULL buffer", fn);
     KVQ_REQUIRE((((uintptr_t)q | (uintptr_t)out | (uintptr_t)P->k16 | (uintptr_t)P->v16) & 15u) == 0,
                 KVQ_ERR_INVALID_ARG, "%s: q, out, k16 and v16 must be 16-byte aligned", fn);
-    a.k16 = P->k16, a.v16 = P->v16, a.q = q;
+    KVQ_REQUIRE(p.items <= INT32_MAX, KVQ_ERR_UNSUPPORTED, "%s: n_rows", fn);
+    const int H = L->n_kv_heads, GQ = L->n_q_heads / H;
+    CUtensorMap map_q, map_k, map_v;
+    const uint64_t qd[3] = {D, (uint64_t)L->n_q_heads, (uint64_t)n_rows};
+    const uint64_t qs[2] = {D * 2, (uint64_t)L->n_q_heads * D * 2};
+    const uint32_t qb[3] = {64, (uint32_t)GQ, (uint32_t)(128 / GQ)};
+    const uint64_t kd[2] = {D, (uint64_t)pool_rows}, ks[1] = {D * 2};
+    const uint32_t kb[2] = {64, PG};
+    st = make_map(&map_q, q, 3, qd, qs, qb, fn);
+    if (!st) st = make_map(&map_k, P->k16, 2, kd, ks, kb, fn);
+    if (!st) st = make_map(&map_v, P->v16, 2, kd, ks, kb, fn);
+    if (st) return st;
     a.num_blocks = P->num_blocks;
     a.bt = S->block_table, a.seq_lens = S->seq_lens, a.q_starts = q_starts;
     a.batch = S->batch, a.max_blocks = S->max_blocks, a.max_len = S->max_len, a.max_new = max_new;
-    a.H = L->n_kv_heads, a.GQ = L->n_q_heads / L->n_kv_heads;
+    a.H = H, a.GQ = GQ, a.n_splits = p.n_splits;
     a.n_rows = n_rows;
     a.out = out, a.lse = lse;
     a.hdr = static_cast<KvqWsHeader*>(ws);
-    const int64_t items = (int64_t)max_new * L->n_q_heads;
-    const dim3 grid((unsigned)((items + CA_NT / 32 - 1) / (CA_NT / 32)), S->batch);
-    chunk_attn_kernel<<<grid, CA_NT, 0, kvq_stream(stream)>>>(a);
-    return kvq_launch_status(fn);
+    a.ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + p.off_ml);
+    a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.off_part);
+    const dim3 grid((unsigned)p.items, H, p.n_splits);
+    const auto go = [&](auto kernel) {
+        const int rc = kvq_prepare_kernel((const void*)kernel, CA_SMEM);
+        if (rc) return rc;
+        cudaError_t e = kvq_launch_pdl(kernel, grid, dim3(CA_NT), CA_SMEM, kvq_stream(stream), map_q, map_k, map_v, a);
+        if (e == cudaSuccess && p.n_splits > 1)
+            e = kvq_launch_pdl(chunk_join_kernel, dim3((unsigned)p.items, H, CA_ROWS / 32), dim3(CJ_NT), 0, kvq_stream(stream), a);
+        if (e != cudaSuccess) return kvq_fail(KVQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+        return (int)KVQ_OK;
+    };
+    const bool cap = a.mod.post != 0.0f, bias = a.mod.slopes != nullptr;
+    if (cap) return bias ? go(chunk_attn_kernel<true, true>) : go(chunk_attn_kernel<true, false>);
+    return bias ? go(chunk_attn_kernel<false, true>) : go(chunk_attn_kernel<false, false>);
 }
