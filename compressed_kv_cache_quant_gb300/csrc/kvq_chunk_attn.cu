@@ -80,6 +80,12 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(saddr(bar)) : "memory");
 }
+// true in one lane of a converged warp
+__device__ __forceinline__ bool elect() {
+    uint32_t one;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+    return one != 0;
+}
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
@@ -120,6 +126,24 @@ __device__ __forceinline__ void tm_ld32(uint32_t addr, uint32_t* v) {
         : "r"(addr)
         : "memory");
 }
+// all 128 columns of a score tile
+__device__ __forceinline__ void tm_ld128(uint32_t addr, uint32_t* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x128.b32 {"
+        "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+        "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+        "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63,"
+        "%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,"
+        "%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95,"
+        "%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,"
+        "%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%128];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : R8(v, 0), R8(v, 8), R8(v, 16), R8(v, 24), R8(v, 32), R8(v, 40), R8(v, 48), R8(v, 56), R8(v, 64), R8(v, 72), R8(v, 80),
+          R8(v, 88), R8(v, 96), R8(v, 104), R8(v, 112), R8(v, 120)
+        : "r"(addr)
+        : "memory");
+}
 __device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t* v) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
@@ -133,6 +157,30 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// two fp32 values per instruction
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float* lo, float* hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 __device__ __forceinline__ float rcp(float x) {
     float y;
@@ -148,7 +196,7 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 // ---------------------------------------------------------------- what a CTA works on
 
 struct Shared {
-    uint64_t q_full, kv_full[CA_NS], kv_empty[CA_NS], s_full[2], p_full[2], o_full[2], drain;
+    uint64_t q_full, kv_full[CA_NS], kv_empty[CA_NS], s_full[2], p_full[2][2], o_full[2], drain;
     uint32_t tmem;
     int32_t abort;
     int32_t item_b, item_tok;                     // sequence and first new token of this CTA
@@ -271,7 +319,8 @@ __global__ void __launch_bounds__(CA_NT, 1)
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(&S.s_full[i], 1);
-            bar_init(&S.p_full[i], 4);
+            bar_init(&S.p_full[i][0], 4);
+            bar_init(&S.p_full[i][1], 4);
             bar_init(&S.o_full[i], 1);
         }
         bar_init(&S.drain, 1);
@@ -295,9 +344,9 @@ __global__ void __launch_bounds__(CA_NT, 1)
     const int it0 = min(total, split * per), it1 = min(total, it0 + per), nt = it1 - it0;
     const auto tile_of = [&](int it) { return it < b1 - a1 ? a1 + it : a2 + (it - (b1 - a1)); };
 
-    // 384 threads are launched with 168 registers each: 256 * 216 + 128 * 72 is the same total
+    // 384 threads are launched with 168 registers each: 256 * 232 + 128 * 40 is the same total
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 9 && nt > 0) {
             // ---- loads
             if (lane == 0) {
@@ -353,55 +402,76 @@ __global__ void __launch_bounds__(CA_NT, 1)
                 ok = __all_sync(0xffffffffu, ok);
             }
         }
-        if (warp == 8 && lane == 0 && nt > 0) {
-            // ---- tensor cores
+        if (warp == 8 && nt > 0) {
+            // ---- tensor cores.  The whole warp walks the loop and one elected lane issues, so that the
+            // descriptors stay in uniform registers.  All 512 TMEM columns are this CTA's, so they start at
+            // column 0.  A descriptor is its low word plus constants: the low words are made opaque in every
+            // step, or the compiler keeps all 64 of a step's descriptors in (spilled) registers, and the
+            // reloads hold up every product (110 instead of 64 cycles each).
+            const uint32_t hi = (uint32_t)(smem_desc(0, 16) >> 32);
+            const uint32_t lq = (uint32_t)smem_desc(sq, 16), lk = (uint32_t)smem_desc(skv, 16),
+                           lv = (uint32_t)smem_desc(skv, CA_HALF);
+            const auto desc = [&](uint32_t lo) { return (uint64_t)hi << 32 | lo; };
             bool ok = bar_wait(S, a.hdr, &S.q_full, 0) && bar_wait(S, a.hdr, &S.kv_full[0], 0);
             const auto qk = [&](int i, int st) {
+                if (elect()) {
+                    uint32_t x = lq + (i * CA_TILE >> 4), y = lk + (st * CA_TILE >> 4);
+                    asm volatile("" : "+r"(x), "+r"(y));
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (k >> 2) * CA_HALF + (k & 3) * 32;
-                    mma_ss(tmem + TM_S + 128 * i, smem_desc(sq + i * CA_TILE + off, 16), smem_desc(skv + st * CA_TILE + off, 16),
-                           IDESC_QK, k > 0);
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = ((k >> 2) * CA_HALF + (k & 3) * 32) >> 4;
+                        mma_ss(TM_S + 128 * i, desc(x + off), desc(y + off), IDESC_QK, k > 0);
+                    }
+                    tc_commit(&S.s_full[i]);
                 }
+            };
+            const auto pv = [&](int i, int st, int half, bool acc) {
+                if (elect()) {
+                    uint32_t y = lv + (st * CA_TILE >> 4);
+                    asm volatile("" : "+r"(y));
+#pragma unroll
+                    for (int k = 4 * half; k < 4 * half + 4; ++k)
+                        mma_ts(TM_O + 128 * i, TM_S + 128 * i + 8 * k, desc(y + (k * 2048 >> 4)), IDESC_PV, acc || k > 0);
+                }
+            };
+            const auto commit = [&](uint64_t* bar) {
+                if (elect()) tc_commit(bar);
             };
             if (ok) {
                 tc_after();
-                for (int i = 0; i < nq; ++i) {
-                    qk(i, 0);
-                    tc_commit(&S.s_full[i]);
-                }
-                tc_commit(&S.kv_empty[0]);
+                qk(0, 0);
+                if (nq > 1) qk(1, 0);
+                commit(&S.kv_empty[0]);
             }
             for (int j = 0; j < nt && ok; ++j) {
                 const int sv = (2 * j + 1) % CA_NS, sk = (2 * j + 2) % CA_NS;
                 const bool more = j + 1 < nt;
+                ok = bar_wait(S, a.hdr, &S.kv_full[sv], ((2 * j + 1) / CA_NS) & 1);
                 for (int i = 0; i < nq && ok; ++i) {
-                    ok = bar_wait(S, a.hdr, &S.p_full[i], j & 1) &&
-                         (i > 0 || bar_wait(S, a.hdr, &S.kv_full[sv], ((2 * j + 1) / CA_NS) & 1));
+                    for (int half = 0; half < 2 && ok; ++half) {
+                        ok = bar_wait(S, a.hdr, &S.p_full[i][half], j & 1);
+                        if (!ok) break;
+                        tc_after();
+                        pv(i, sv, half, j > 0);
+                    }
                     if (!ok) break;
-                    tc_after();
-#pragma unroll
-                    for (int k = 0; k < CA_KEYS / 16; ++k)
-                        mma_ts(tmem + TM_O + 128 * i, tmem + TM_S + 128 * i + 8 * k,
-                               smem_desc(skv + sv * CA_TILE + k * 2048, CA_HALF), IDESC_PV, j > 0 || k > 0);
                     if (more) {
                         ok = i > 0 || bar_wait(S, a.hdr, &S.kv_full[sk], ((2 * j + 2) / CA_NS) & 1);
                         if (!ok) break;
                         tc_after();
                         qk(i, sk);
-                        tc_commit(&S.s_full[i]);
                     } else {
-                        tc_commit(&S.o_full[i]);
+                        commit(&S.o_full[i]);
                     }
                 }
                 if (!ok) break;
-                tc_commit(&S.kv_empty[sv]);
-                if (more) tc_commit(&S.kv_empty[sk]);
+                commit(&S.kv_empty[sv]);
+                if (more) commit(&S.kv_empty[sk]);
             }
         }
     } else {
         // ---- softmax: thread = row
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         const int i = warp >> 2, r = tid;   // row of the CTA
         const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21);  // TMEM lanes 32 (warp % 4) ..
         const uint32_t ts = lane_base + TM_S + 128 * i, to = lane_base + TM_O + 128 * i;
@@ -439,8 +509,7 @@ __global__ void __launch_bounds__(CA_NT, 1)
                 }
                 tc_after();
                 float s[128];
-#pragma unroll
-                for (int c = 0; c < 128; c += 32) tm_ld32(ts + c, reinterpret_cast<uint32_t*>(s + c));
+                tm_ld128(ts, reinterpret_cast<uint32_t*>(s));
                 float scale = a.mod.pre;
                 if (CAP) {
                     // tanh x = 1 - 2 / (1 + e^2x): two special-function results, 1e-7 absolute
@@ -466,10 +535,13 @@ __global__ void __launch_bounds__(CA_NT, 1)
                             if (!(bits >> c & 1)) s[32 * w + c] = -INFINITY;
                     }
                 }
-                float mx = s[0];
+                float mx4[4] = {s[0], s[1], s[2], s[3]};   // four chains: the maximum is not a latency chain of its own
 #pragma unroll
-                for (int c = 1; c < 128; ++c) mx = fmaxf(mx, s[c]);
-                mx *= scale;
+                for (int c = 4; c < 124; c += 8) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) mx4[x] = max3(mx4[x], s[c + x], s[c + 4 + x]);
+                }
+                const float mx = max3(max3(mx4[0], mx4[1], mx4[2]), mx4[3], max3(s[124], s[125], fmaxf(s[126], s[127]))) * scale;
                 const bool grew = mx > m + CA_SLACK || (m == -INFINITY && mx > m);
                 float f = 1.0f;
                 if (grew) {
@@ -488,21 +560,28 @@ __global__ void __launch_bounds__(CA_NT, 1)
                     }
                 }
                 const float ms = m == -INFINITY ? 0.0f : m;
+                const uint64_t scale2 = pair(scale, scale), ms2 = pair(-ms, -ms);
+                uint64_t sum2[2] = {0, 0};
 #pragma unroll
-                for (int c = 0; c < 128; c += 64) {
+                for (int c = 0; c < 128; c += 64) {   // the products start on the first half of the keys
                     uint32_t p[32];
 #pragma unroll
                     for (int x = 0; x < 32; ++x) {
-                        const float p0 = ex2(fmaf(s[c + 2 * x], scale, -ms)), p1 = ex2(fmaf(s[c + 2 * x + 1], scale, -ms));
-                        l += p0 + p1;
+                        float p0, p1;
+                        unpair(fma2(pair(s[c + 2 * x], s[c + 2 * x + 1]), scale2, ms2), &p0, &p1);
+                        p0 = ex2(p0), p1 = ex2(p1);
+                        sum2[x & 1] = add2(sum2[x & 1], pair(p0, p1));
                         p[x] = half2_bits(p0, p1);
                     }
                     tm_st32(ts + c / 2, p);
+                    tm_wait_st();
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&S.p_full[i][c / 64]);
                 }
-                tm_wait_st();
-                tc_before();
-                __syncwarp();
-                if (lane == 0) bar_arrive(&S.p_full[i]);
+                float l0, l1;
+                unpair(add2(sum2[0], sum2[1]), &l0, &l1);
+                l += l0 + l1;
             }
             // ---- this row's output
             ok = ok && (nt == 0 || bar_wait(S, a.hdr, &S.o_full[i], 0));
