@@ -4,7 +4,8 @@
 // that the bytes of the cache.  One CTA takes up to 256 query rows of one kv head as two tiles of 128:
 // row r is new token r / GQ, query head r % GQ of the group, so that the heads of a group share every
 // staged K/V tile and a short run still fills rows.  Tiles of 128 cached tokens are eight pages, each
-// fetched through the block table by its own TMA boxes (16 rows x 128 bytes, 128-byte swizzle).
+// fetched through the block table by one TMA box of 4 KB: groups of eight rows, a group's two halves of
+// 64 values behind one another, 128-byte swizzle.
 //
 //   warps 8-11 give most of their registers to the softmax warps; 10 and 11 do nothing else
 //   warp 9     loads: Q once, then K and V tiles into a ring of shared-memory stages
@@ -29,8 +30,8 @@ constexpr int CA_NT = 384;
 constexpr int CA_ROWS = 256;             // query rows per CTA
 constexpr int CA_KEYS = 128;             // cached tokens per tile
 constexpr int CA_NS = 4;                 // K or V tiles in the ring
-constexpr int CA_TILE = 128 * D * 2;     // bytes of a Q, K or V tile: two halves of 128 rows x 128 bytes
-constexpr int CA_HALF = CA_TILE / 2;
+constexpr int CA_TILE = 128 * D * 2;     // bytes of a Q, K or V tile
+constexpr int CA_HALF = CA_TILE / 2;     // a Q tile is two halves of 128 rows x 128 bytes
 constexpr int CA_SMEM = 2 * CA_TILE + CA_NS * CA_TILE + 1024;
 constexpr uint32_t CA_SPIN = 1u << 16;   // bound on the polls of one mbarrier wait
 constexpr float CA_SLACK = 8.0f;         // log2 growth of a row's maximum before O is rescaled
@@ -63,11 +64,12 @@ __device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes) {
 __device__ __forceinline__ void bar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(bar)) : "memory");
 }
-__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+// a page of one kv head: the map's dims are 64 values, 8 rows, 2 halves of a row, groups of 8 rows
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, int group, uint64_t* bar) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            dst),
-        "l"(map), "r"(x), "r"(y), "r"(saddr(bar))
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], "
+        "[%4];" ::"r"(dst),
+        "l"(map), "r"(0), "r"(group), "r"(saddr(bar))
         : "memory");
 }
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
@@ -90,9 +92,9 @@ __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::befor
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
 // Shared-memory matrix descriptor, 128-byte swizzle: start address, byte offsets between the 64-element
-// blocks of a matrix whose rows run along K (`lead`), and between groups of eight rows (1024 bytes here).
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
-    return (uint64_t)((addr & 0x3ffff) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+// blocks of a matrix whose rows run along K (`lead`), and between groups of eight rows (`group`).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t group) {
+    return (uint64_t)((addr & 0x3ffff) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(group >> 4) << 32) |
            (1ull << 46) | (2ull << 61);
 }
 // f16 x f16 -> f32, M = 128, N = 128; bit 16: B's rows run along K (V), else along N (K)
@@ -356,16 +358,17 @@ __global__ void __launch_bounds__(CA_NT, 1)
                         tma_3d(sq + i * CA_TILE + c * CA_HALF, &map_q, 64 * c, h * GQ, first + tok0 + i * (128 / GQ), &S.q_full);
             }
             __syncwarp();
-            const int pg = lane >> 1, half = lane & 1;   // lanes 0-15: one box of K and one of V each
-            const int nowhere = (int)(a.num_blocks * a.H * PG);  // a row behind the pool: zeros
-            bool ok = true;
-            for (int j = 0; j < nt && ok; ++j) {
+            const int pg = lane & 7;   // lanes 0-7 look up one page each
+            const int nowhere = (int)(a.num_blocks * a.H * (PG / 8));  // a group of rows behind the pool: zeros
+            // where this lane's page of the j-th tile begins, in groups of 8 rows: it is looked up while the
+            // stages of the tile before are still in use
+            const auto group_of = [&](int j) {
                 const int t = tile_of(it0 + j), lp = t * (CA_KEYS / PG) + pg;
-                uint32_t need;  // bit per page of the tile that some row sees
+                uint32_t need;  // bit per page: some row sees a token of it
                 if (a.mod.doc_start == nullptr) {
                     const int p0 = lp * PG;
-                    need = __ballot_sync(0xffffffffu, lane < 16 && ((p0 < S.hi_max && p0 + PG > S.lo_min) ||
-                                                                    (p0 < S.sink_max && p0 + PG > S.doc_min)));
+                    need = __ballot_sync(0xffffffffu, (p0 < S.hi_max && p0 + PG > S.lo_min) ||
+                                                          (p0 < S.sink_max && p0 + PG > S.doc_min));
                 } else {
                     uint32_t bits = 0;
                     for (int k = lane; k < ntok; k += 32) {
@@ -374,32 +377,41 @@ __global__ void __launch_bounds__(CA_NT, 1)
                         if (e.x < e.y) bits |= below((e.y + PG - 1) / PG - p0) & ~below(e.x / PG - p0);
                         if (e.z < e.w) bits |= below((e.w + PG - 1) / PG - p0) & ~below(e.z / PG - p0);
                     }
-                    bits = __reduce_or_sync(0xffffffffu, bits) & 0xff;
-                    need = 0;
-                    for (int k = 0; k < 8; ++k) need |= (bits >> k & 1) * (3u << 2 * k);
+                    need = __reduce_or_sync(0xffffffffu, bits);
                 }
                 int y = nowhere;
-                if (lane < 16 && (need >> lane & 1)) {
+                if (need >> pg & 1) {
                     const int32_t page = a.bt[(int64_t)b * a.max_blocks + lp];
                     if (page >= 0 && page < a.num_blocks)
-                        y = (page * a.H + h) * PG;
-                    else
+                        y = (page * a.H + h) * (PG / 8);
+                    else if (lane == pg)
                         kvq_dev_flag(a.hdr, KVQ_DEV_BAD_PAGE, page);
                 }
+                return y;
+            };
+            bool ok = true;
+            int y = group_of(0);
+            for (int j = 0; j < nt && ok; ++j) {
+                const int next = j + 1 < nt ? group_of(j + 1) : 0;
+                // one elected lane issues from uniform registers: a copy per lane would be issued one by one
+                // just the same, at 79 cycles each
+                int at[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) at[k] = __shfl_sync(0xffffffffu, y, k);
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
                     const int slot = 2 * j + v, st = slot % CA_NS;
-                    if (slot >= CA_NS && !bar_wait(S, a.hdr, &S.kv_empty[st], ((slot / CA_NS) & 1) ^ 1)) {
-                        ok = false;
-                        break;
+                    ok = ok && (slot < CA_NS || bar_wait(S, a.hdr, &S.kv_empty[st], ((slot / CA_NS) & 1) ^ 1));
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (elect()) {
+                        bar_expect(&S.kv_full[st], CA_TILE);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            tma_page(skv + st * CA_TILE + k * (PG * D * 2), v ? &map_v : &map_k, at[k], &S.kv_full[st]);
                     }
-                    if (lane == 0) bar_expect(&S.kv_full[st], CA_TILE);
-                    __syncwarp();
-                    if (lane < 16)
-                        tma_2d(skv + st * CA_TILE + half * CA_HALF + pg * (PG * 128), v ? &map_v : &map_k, 64 * half, y,
-                               &S.kv_full[st]);
                 }
-                ok = __all_sync(0xffffffffu, ok);
+                y = next;
             }
         }
         if (warp == 8 && nt > 0) {
@@ -408,10 +420,10 @@ __global__ void __launch_bounds__(CA_NT, 1)
             // column 0.  A descriptor is its low word plus constants: the low words are made opaque in every
             // step, or the compiler keeps all 64 of a step's descriptors in (spilled) registers, and the
             // reloads hold up every product (110 instead of 64 cycles each).
-            const uint32_t hi = (uint32_t)(smem_desc(0, 16) >> 32);
-            const uint32_t lq = (uint32_t)smem_desc(sq, 16), lk = (uint32_t)smem_desc(skv, 16),
-                           lv = (uint32_t)smem_desc(skv, CA_HALF);
-            const auto desc = [&](uint32_t lo) { return (uint64_t)hi << 32 | lo; };
+            const uint32_t hi_q = (uint32_t)(smem_desc(0, 16, 1024) >> 32), hi_kv = (uint32_t)(smem_desc(0, 16, 2048) >> 32);
+            const uint32_t lq = (uint32_t)smem_desc(sq, 16, 0), lk = (uint32_t)smem_desc(skv, 16, 0),
+                           lv = (uint32_t)smem_desc(skv, 1024, 0);
+            const auto desc = [](uint32_t hi, uint32_t lo) { return (uint64_t)hi << 32 | lo; };
             bool ok = bar_wait(S, a.hdr, &S.q_full, 0) && bar_wait(S, a.hdr, &S.kv_full[0], 0);
             const auto qk = [&](int i, int st) {
                 if (elect()) {
@@ -419,8 +431,8 @@ __global__ void __launch_bounds__(CA_NT, 1)
                     asm volatile("" : "+r"(x), "+r"(y));
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = ((k >> 2) * CA_HALF + (k & 3) * 32) >> 4;
-                        mma_ss(TM_S + 128 * i, desc(x + off), desc(y + off), IDESC_QK, k > 0);
+                        mma_ss(TM_S + 128 * i, desc(hi_q, x + (((k >> 2) * CA_HALF + (k & 3) * 32) >> 4)),
+                               desc(hi_kv, y + (((k >> 2) * 1024 + (k & 3) * 32) >> 4)), IDESC_QK, k > 0);
                     }
                     tc_commit(&S.s_full[i]);
                 }
@@ -431,7 +443,7 @@ __global__ void __launch_bounds__(CA_NT, 1)
                     asm volatile("" : "+r"(y));
 #pragma unroll
                     for (int k = 4 * half; k < 4 * half + 4; ++k)
-                        mma_ts(TM_O + 128 * i, TM_S + 128 * i + 8 * k, desc(y + (k * 2048 >> 4)), IDESC_PV, acc || k > 0);
+                        mma_ts(TM_O + 128 * i, TM_S + 128 * i + 8 * k, desc(hi_kv, y + (k * 4096 >> 4)), IDESC_PV, acc || k > 0);
                 }
             };
             const auto commit = [&](uint64_t* bar) {
@@ -502,7 +514,8 @@ __global__ void __launch_bounds__(CA_NT, 1)
                     const uint32_t base = skv + (2 * j + 1) % CA_NS * CA_TILE;
                     const int r0 = T - t0, r1 = (r0 + PG - 1) / PG * PG;
                     for (int x = tid & 127; x < (r1 - r0) * 16; x += 128) {
-                        const uint32_t at = base + (x & 1) * CA_HALF + (r0 + (x >> 4)) * 128 + ((x >> 1) & 7) * 16;
+                        const int row = r0 + (x >> 4);
+                        const uint32_t at = base + (row >> 3) * 2048 + (x & 1) * 1024 + (row & 7) * 128 + ((x >> 1) & 7) * 16;
                         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -535,36 +548,13 @@ __global__ void __launch_bounds__(CA_NT, 1)
                             if (!(bits >> c & 1)) s[32 * w + c] = -INFINITY;
                     }
                 }
-                float mx4[4] = {s[0], s[1], s[2], s[3]};   // four chains: the maximum is not a latency chain of its own
-#pragma unroll
-                for (int c = 4; c < 124; c += 8) {
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) mx4[x] = max3(mx4[x], s[c + x], s[c + 4 + x]);
-                }
-                const float mx = max3(max3(mx4[0], mx4[1], mx4[2]), mx4[3], max3(s[124], s[125], fmaxf(s[126], s[127]))) * scale;
-                const bool grew = mx > m + CA_SLACK || (m == -INFINITY && mx > m);
-                float f = 1.0f;
-                if (grew) {
-                    f = ex2(m - mx);
-                    m = mx;
-                    l *= f;
-                }
-                if (j > 0 && __any_sync(0xffffffffu, grew)) {
-#pragma unroll
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tm_ld32(to + c, o);
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                        tm_st32(to + c, o);
-                    }
-                }
-                const float ms = m == -INFINITY ? 0.0f : m;
-                const uint64_t scale2 = pair(scale, scale), ms2 = pair(-ms, -ms);
-                uint64_t sum2[2] = {0, 0};
-#pragma unroll
-                for (int c = 0; c < 128; c += 64) {   // the products start on the first half of the keys
-                    uint32_t p[32];
+                // The first half's weights are taken with the maximum so far, while the new one is still being
+                // found; only when a row's grew by more than the slack are they taken again.
+                uint32_t p[32];
+                uint64_t sum2[2];
+                const auto weights = [&](int c) {
+                    const float ms = m == -INFINITY ? 0.0f : m;
+                    const uint64_t scale2 = pair(scale, scale), ms2 = pair(-ms, -ms);
 #pragma unroll
                     for (int x = 0; x < 32; ++x) {
                         float p0, p1;
@@ -573,12 +563,44 @@ __global__ void __launch_bounds__(CA_NT, 1)
                         sum2[x & 1] = add2(sum2[x & 1], pair(p0, p1));
                         p[x] = half2_bits(p0, p1);
                     }
+                };
+                const auto hand_over = [&](int c) {   // the products start on the first half of the keys
                     tm_st32(ts + c / 2, p);
                     tm_wait_st();
                     tc_before();
                     __syncwarp();
                     if (lane == 0) bar_arrive(&S.p_full[i][c / 64]);
+                };
+                sum2[0] = sum2[1] = 0;
+                weights(0);
+                float mx4[4] = {s[0], s[1], s[2], s[3]};   // four chains: the maximum is not a latency chain of its own
+#pragma unroll
+                for (int c = 4; c < 124; c += 8) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) mx4[x] = max3(mx4[x], s[c + x], s[c + 4 + x]);
                 }
+                const float mx = max3(max3(mx4[0], mx4[1], mx4[2]), mx4[3], max3(s[124], s[125], fmaxf(s[126], s[127]))) * scale;
+                const bool grew = mx > m + CA_SLACK || (m == -INFINITY && mx > m);
+                if (__any_sync(0xffffffffu, grew)) {
+                    const float f = grew ? ex2(m - mx) : 1.0f;
+                    if (grew) m = mx;
+                    l *= f;
+                    if (j > 0) {
+#pragma unroll
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tm_ld32(to + c, o);
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                            tm_st32(to + c, o);
+                        }
+                    }
+                    sum2[0] = sum2[1] = 0;
+                    weights(0);
+                }
+                hand_over(0);
+                weights(64);
+                hand_over(64);
                 float l0, l1;
                 unpair(add2(sum2[0], sum2[1]), &l0, &l1);
                 l += l0 + l1;
@@ -738,7 +760,7 @@ ChunkPlan chunk_plan(const kvq_layout* L, const kvq_seqs* S, int64_t n_rows, int
     return p;
 }
 
-// A tensor map of fp16 rows of d values, 64-value boxes of the given rows, 128-byte swizzle.
+// A tensor map of fp16 values in boxes whose innermost extent is 64 values, 128-byte swizzle.
 int make_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
              const char* fn) {
     using Encode = decltype(&cuTensorMapEncodeTiled);
@@ -753,7 +775,7 @@ int make_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
         }
         encode = reinterpret_cast<Encode>(f);
     }
-    const cuuint32_t ones[3] = {1, 1, 1};
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
     const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, const_cast<void*>(base),
                               reinterpret_cast<const cuuint64_t*>(dims), reinterpret_cast<const cuuint64_t*>(strides),
                               box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -803,11 +825,11 @@ extern "C" int kv_chunk_attn(const kvq_layout* L, const kvq_pool* P, const kvq_s
     const uint64_t qd[3] = {D, (uint64_t)L->n_q_heads, (uint64_t)n_rows};
     const uint64_t qs[2] = {D * 2, (uint64_t)L->n_q_heads * D * 2};
     const uint32_t qb[3] = {64, (uint32_t)GQ, (uint32_t)(128 / GQ)};
-    const uint64_t kd[2] = {D, (uint64_t)pool_rows}, ks[1] = {D * 2};
-    const uint32_t kb[2] = {64, PG};
+    const uint64_t kd[4] = {64, 8, 2, (uint64_t)pool_rows / 8}, ks[3] = {D * 2, 64 * 2, 8 * D * 2};
+    const uint32_t kb[4] = {64, 8, 2, PG / 8};
     st = make_map(&map_q, q, 3, qd, qs, qb, fn);
-    if (!st) st = make_map(&map_k, P->k16, 2, kd, ks, kb, fn);
-    if (!st) st = make_map(&map_v, P->v16, 2, kd, ks, kb, fn);
+    if (!st) st = make_map(&map_k, P->k16, 4, kd, ks, kb, fn);
+    if (!st) st = make_map(&map_v, P->v16, 4, kd, ks, kb, fn);
     if (st) return st;
     a.num_blocks = P->num_blocks;
     a.bt = S->block_table, a.seq_lens = S->seq_lens, a.q_starts = q_starts;
