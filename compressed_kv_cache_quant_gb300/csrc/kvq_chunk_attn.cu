@@ -206,16 +206,22 @@ struct Shared {
     int4 see[CA_ROWS];                            // lo, hi, doc, sink of every token
 };
 
-// Waits for a phase of bar; false after CA_SPIN polls or when another thread gave up.
+__device__ __forceinline__ bool bar_done(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Waits for a phase of bar; false after CA_SPIN polls or when another thread gave up.  Most waits of the
+// issuing warps find their phase done, so that case is one poll and nothing else.
 __device__ __forceinline__ bool bar_wait(Shared& S, KvqWsHeader* hdr, uint64_t* bar, uint32_t parity) {
-    for (uint32_t it = 0; it < CA_SPIN; ++it) {
-        uint32_t ok;
-        asm volatile(
-            "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
-            : "=r"(ok)
-            : "r"(saddr(bar)), "r"(parity)
-            : "memory");
-        if (ok) return true;
+    const uint32_t at = saddr(bar);
+    if (__builtin_expect(bar_done(at, parity), 1)) return true;
+    for (uint32_t it = 1; it < CA_SPIN; ++it) {
+        if (bar_done(at, parity)) return true;
         if ((it & 63) == 63 && *(volatile int32_t*)&S.abort) return false;
     }
     *(volatile int32_t*)&S.abort = 1;
@@ -360,8 +366,8 @@ __global__ void __launch_bounds__(CA_NT, 1)
             __syncwarp();
             const int pg = lane & 7;   // lanes 0-7 look up one page each
             const int nowhere = (int)(a.num_blocks * a.H * (PG / 8));  // a group of rows behind the pool: zeros
-            // where this lane's page of the j-th tile begins, in groups of 8 rows: it is looked up while the
-            // stages of the tile before are still in use
+            // where this lane's page of the j-th tile begins, in groups of 8 rows: it is looked up a tile ahead,
+            // before the wait for V's stage
             const auto group_of = [&](int j) {
                 const int t = tile_of(it0 + j), lp = t * (CA_KEYS / PG) + pg;
                 uint32_t need;  // bit per page: some row sees a token of it
@@ -389,29 +395,28 @@ __global__ void __launch_bounds__(CA_NT, 1)
                 }
                 return y;
             };
+            // one elected lane issues from uniform registers: a copy per lane would be issued one by one just
+            // the same, at 79 cycles each
+            const auto fetch = [&](int slot, const CUtensorMap* map, const int* at) {
+                const int st = slot % CA_NS;
+                const bool ok = __all_sync(0xffffffffu, slot < CA_NS || bar_wait(S, a.hdr, &S.kv_empty[st], ((slot / CA_NS) & 1) ^ 1));
+                if (ok && elect()) {
+                    bar_expect(&S.kv_full[st], CA_TILE);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) tma_page(skv + st * CA_TILE + k * (PG * D * 2), map, at[k], &S.kv_full[st]);
+                }
+                __syncwarp();
+                return ok;
+            };
             bool ok = true;
             int y = group_of(0);
             for (int j = 0; j < nt && ok; ++j) {
-                const int next = j + 1 < nt ? group_of(j + 1) : 0;
-                // one elected lane issues from uniform registers: a copy per lane would be issued one by one
-                // just the same, at 79 cycles each
                 int at[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) at[k] = __shfl_sync(0xffffffffu, y, k);
-#pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    const int slot = 2 * j + v, st = slot % CA_NS;
-                    ok = ok && (slot < CA_NS || bar_wait(S, a.hdr, &S.kv_empty[st], ((slot / CA_NS) & 1) ^ 1));
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    if (elect()) {
-                        bar_expect(&S.kv_full[st], CA_TILE);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            tma_page(skv + st * CA_TILE + k * (PG * D * 2), v ? &map_v : &map_k, at[k], &S.kv_full[st]);
-                    }
-                }
-                y = next;
+                ok = fetch(2 * j, &map_k, at);
+                if (j + 1 < nt) y = group_of(j + 1);
+                ok = ok && fetch(2 * j + 1, &map_v, at);
             }
         }
         if (warp == 8 && nt > 0) {
@@ -459,26 +464,34 @@ __global__ void __launch_bounds__(CA_NT, 1)
                 const int sv = (2 * j + 1) % CA_NS, sk = (2 * j + 2) % CA_NS;
                 const bool more = j + 1 < nt;
                 ok = bar_wait(S, a.hdr, &S.kv_full[sv], ((2 * j + 1) / CA_NS) & 1);
-                for (int i = 0; i < nq && ok; ++i) {
-                    for (int half = 0; half < 2 && ok; ++half) {
-                        ok = bar_wait(S, a.hdr, &S.p_full[i][half], j & 1);
-                        if (!ok) break;
-                        tc_after();
-                        pv(i, sv, half, j > 0);
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (i == nq) break;
+                    if (!bar_wait(S, a.hdr, &S.p_full[i][0], j & 1)) {
+                        ok = false;
+                        break;
                     }
-                    if (!ok) break;
+                    tc_after();
+                    pv(i, sv, 0, j > 0);
+                    if (!bar_wait(S, a.hdr, &S.p_full[i][1], j & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_after();
+                    pv(i, sv, 1, true);
+                    if (i == nq - 1) commit(&S.kv_empty[sv]);
                     if (more) {
-                        ok = i > 0 || bar_wait(S, a.hdr, &S.kv_full[sk], ((2 * j + 2) / CA_NS) & 1);
-                        if (!ok) break;
-                        tc_after();
+                        if (i == 0 && !bar_wait(S, a.hdr, &S.kv_full[sk], ((2 * j + 2) / CA_NS) & 1)) {
+                            ok = false;
+                            break;
+                        }
                         qk(i, sk);
                     } else {
                         commit(&S.o_full[i]);
                     }
                 }
-                if (!ok) break;
-                commit(&S.kv_empty[sv]);
-                if (more) commit(&S.kv_empty[sk]);
+                if (ok && more) commit(&S.kv_empty[sk]);
             }
         }
     } else {
@@ -552,16 +565,33 @@ __global__ void __launch_bounds__(CA_NT, 1)
                 // found; only when a row's grew by more than the slack are they taken again.
                 uint32_t p[32];
                 uint64_t sum2[2];
-                const auto weights = [&](int c) {
+                float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                // The steps of a pair are spread over eight turns of the loop, so that no instruction waits
+                // for the one before; the maximum's comparisons fill the gaps of the first half.
+                const auto weights = [&](int c, bool with_max) {
                     const float ms = m == -INFINITY ? 0.0f : m;
                     const uint64_t scale2 = pair(scale, scale), ms2 = pair(-ms, -ms);
+                    uint64_t t[32];
+                    float e[64];
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) {
-                        float p0, p1;
-                        unpair(fma2(pair(s[c + 2 * x], s[c + 2 * x + 1]), scale2, ms2), &p0, &p1);
-                        p0 = ex2(p0), p1 = ex2(p1);
-                        sum2[x & 1] = add2(sum2[x & 1], pair(p0, p1));
-                        p[x] = half2_bits(p0, p1);
+                    for (int x = 0; x < 32 + 8; ++x) {
+                        if (x < 32) {
+                            t[x] = fma2(pair(s[c + 2 * x], s[c + 2 * x + 1]), scale2, ms2);
+                            if (with_max) {
+                                mx4[x & 1] = max3(mx4[x & 1], s[2 * x], s[2 * x + 1]);
+                                mx4[2 + (x & 1)] = max3(mx4[2 + (x & 1)], s[64 + 2 * x], s[64 + 2 * x + 1]);
+                            }
+                        }
+                        if (x >= 4 && x < 36) {
+                            unpair(t[x - 4], &e[2 * (x - 4)], &e[2 * (x - 4) + 1]);
+                            e[2 * (x - 4)] = ex2(e[2 * (x - 4)]);
+                            e[2 * (x - 4) + 1] = ex2(e[2 * (x - 4) + 1]);
+                        }
+                        if (x >= 8) {
+                            const int y = x - 8;
+                            sum2[y & 1] = add2(sum2[y & 1], pair(e[2 * y], e[2 * y + 1]));
+                            p[y] = half2_bits(e[2 * y], e[2 * y + 1]);
+                        }
                     }
                 };
                 const auto hand_over = [&](int c) {   // the products start on the first half of the keys
@@ -572,14 +602,8 @@ __global__ void __launch_bounds__(CA_NT, 1)
                     if (lane == 0) bar_arrive(&S.p_full[i][c / 64]);
                 };
                 sum2[0] = sum2[1] = 0;
-                weights(0);
-                float mx4[4] = {s[0], s[1], s[2], s[3]};   // four chains: the maximum is not a latency chain of its own
-#pragma unroll
-                for (int c = 4; c < 124; c += 8) {
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) mx4[x] = max3(mx4[x], s[c + x], s[c + 4 + x]);
-                }
-                const float mx = max3(max3(mx4[0], mx4[1], mx4[2]), mx4[3], max3(s[124], s[125], fmaxf(s[126], s[127]))) * scale;
+                weights(0, true);
+                const float mx = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]) * scale;
                 const bool grew = mx > m + CA_SLACK || (m == -INFINITY && mx > m);
                 if (__any_sync(0xffffffffu, grew)) {
                     const float f = grew ? ex2(m - mx) : 1.0f;
@@ -596,10 +620,10 @@ __global__ void __launch_bounds__(CA_NT, 1)
                         }
                     }
                     sum2[0] = sum2[1] = 0;
-                    weights(0);
+                    weights(0, false);
                 }
                 hand_over(0);
-                weights(64);
+                weights(64, false);
                 hand_over(64);
                 float l0, l1;
                 unpair(add2(sum2[0], sum2[1]), &l0, &l1);
@@ -649,16 +673,7 @@ __global__ void __launch_bounds__(CA_NT, 1)
         // a wait gave up: let this CTA's own copies and products land (again with a limit) before it ends
         if (warp == 8 && lane == 0) {
             tc_commit(&S.drain);
-            bool ok = false;
-            for (uint32_t it = 0; it < CA_SPIN && !ok; ++it) {
-                uint32_t done;
-                asm volatile(
-                    "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
-                    : "=r"(done)
-                    : "r"(saddr(&S.drain)), "r"(0)
-                    : "memory");
-                ok = done;
-            }
+            for (uint32_t it = 0; it < CA_SPIN && !bar_done(saddr(&S.drain), 0); ++it) {}
         }
         const long long began = clock64();
         while (clock64() - began < 2000000) __nanosleep(1000);  // about a millisecond: far above a copy's time
