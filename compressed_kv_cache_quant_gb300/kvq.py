@@ -196,44 +196,64 @@ class AttnMod:
     """Score forms of kv_decode_attn and kv_chunk_attn (kvq_attn_mod); keeps its tensors alive."""
 
     def __init__(self, scale=0.0, softcap=0.0, window=0, n_sink=0, slopes=None, prefix_len=None, doc_start=None):
-        for x, dt, name in ((slopes, torch.float32, "slopes"), (prefix_len, torch.int32, "prefix_len"),
-                            (doc_start, torch.int32, "doc_start")):
-            _dev(x, dt, "kvq_attn_mod", name, optional=True)
+        gpu = _gpu() if any(x is not None for x in (slopes, prefix_len, doc_start)) else -1
+        at = [_dev(x, dt, None, gpu, "kvq_attn_mod", name)
+              for x, dt, name in ((slopes, torch.float32, "slopes"), (prefix_len, torch.int32, "prefix_len"),
+                                  (doc_start, torch.int32, "doc_start"))]
         self.slopes, self.prefix_len, self.doc_start = slopes, prefix_len, doc_start
-        self.c = _abi.AttnModStruct(float(scale), float(softcap), int(window), int(n_sink), _p(slopes), _p(prefix_len),
-                                    _p(doc_start))
+        self.gpu = gpu
+        self.c = _abi.AttnModStruct(float(scale), float(softcap), int(window), int(n_sink), *at)
+
+
+_ROW = (HEAD_DIM,)
 
 
 def _i32s(xs):
     return (ctypes.c_int32 * max(len(xs), 1))(*[int(x) for x in xs])
 
 
-def _dev(x, dtype, fn, name, shape=None, optional=False):
-    """Refuses what would be read or written wrongly through a bare pointer: a tensor that is not on the
-    current GPU, of another type, with gaps, or smaller than `shape`."""
-    if x is None and optional:
-        return
-    why = None
-    if not isinstance(x, torch.Tensor):
-        why = "a tensor is wanted"
-    elif not x.is_cuda or x.get_device() != torch.cuda.current_device():
-        why = "not on the current GPU"
-    elif x.dtype != dtype:
-        why = f"{x.dtype} instead of {dtype}"
-    elif not x.is_contiguous():
-        why = "not contiguous"
-    elif shape is not None and tuple(x.shape) != shape:
-        why = f"shape {tuple(x.shape)} instead of {shape}"
-    if why:
-        raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, f"{name}: {why}")
+def _gpu():
+    return torch._C._cuda_getDevice()
 
 
-def _mod_rows(mod, fn, layout, batch, rows):
-    """The sizes of a mod's tensors against the call's."""
-    for x, n, name in ((mod.slopes, layout.n_q_heads, "slopes"), (mod.prefix_len, batch, "prefix_len"),
-                       (mod.doc_start, rows, "doc_start")):
-        if x is not None and x.numel() < n:
-            raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, f"{name}: {x.numel()} entries for {n}")
+def _raw(stream, gpu):
+    """The cudaStream_t of `stream`, or of the current stream of GPU `gpu`."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(gpu)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _dev(x, dtype, shape, gpu, fn, name):
+    """Address of x, or None for None.  Refuses what would be read or written wrongly through a bare
+    pointer: a tensor that is not on GPU `gpu`, of another type, with gaps, or not of `shape` (None: any)."""
+    if x is None:
+        return None
+    if isinstance(x, torch.Tensor):
+        if x.dtype is dtype and (shape is None or x.shape == shape) and x.is_contiguous() and x.get_device() == gpu:
+            return x.data_ptr()
+        have = f"{x.dtype} {tuple(x.shape)} on {x.device}" + ("" if x.is_contiguous() else ", not contiguous")
+    else:
+        have = f"{type(x).__name__}"
+    raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, f"{name}: {have} instead of a contiguous {dtype} tensor"
+                   f"{'' if shape is None else ' ' + str(tuple(shape))} on GPU {gpu}")
+
+
+def _need(x, fn, name):
+    if x is None:
+        raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, f"{name} is missing")
+    return x
+
+
+def _mod(mod, fn, layout, batch, rows, gpu):
+    """kvq_attn_mod by reference, its tensors' sizes checked against the call's."""
+    if mod is None:
+        return None
+    if mod.gpu >= 0:
+        for x, n, name in ((mod.slopes, layout.n_q_heads, "slopes"), (mod.prefix_len, batch, "prefix_len"),
+                           (mod.doc_start, rows, "doc_start")):
+            if x is not None and (x.numel() < n or mod.gpu != gpu):
+                raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, f"{name}: {x.numel()} entries on GPU {mod.gpu} for {n} on {gpu}")
+    return ctypes.byref(mod.c)
 
 
 # ------------------------------------------------------------------ the C ABI, same names
@@ -469,17 +489,17 @@ def kv_offload_gather(src_k, src_v, src_stride_h, src_rows, n_heads, sel, sel_co
                                          ws.nbytes, _s(stream)), "kv_offload_gather")
 
 
-def _head_rows(x, n, heads, dtype, fn, name):
-    """Token stride of x [n][heads][d], whose heads have no gaps (a slice of a wider row is fine)."""
-    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.get_device() != torch.cuda.current_device():
-        raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, f"{name}: not a tensor on the current GPU")
-    if tuple(x.shape) != (n, heads, HEAD_DIM) or x.dtype != dtype:
-        raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, f"{name}: {x.dtype} {tuple(x.shape)} instead of "
-                       f"{dtype} {(n, heads, HEAD_DIM)}")
+def _head_rows(x, shape, dtype, gpu, fn, name):
+    """(address, token stride) of x [n][heads][d], whose heads lie side by side (a slice of a wider row is fine)."""
+    if x is None:
+        return None, 0
+    if not isinstance(x, torch.Tensor) or x.dtype is not dtype or x.shape != shape or x.get_device() != gpu:
+        have = f"{x.dtype} {tuple(x.shape)} on {x.device}" if isinstance(x, torch.Tensor) else type(x).__name__
+        raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, f"{name}: {have} instead of {dtype} {shape} on GPU {gpu}")
     st = x.stride()
-    if st[2] != 1 or (st[1] != HEAD_DIM and heads > 1):
+    if st[2] != 1 or (st[1] != HEAD_DIM and shape[1] > 1):
         raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, f"{name}: a token's heads must lie side by side")
-    return st[0] if n > 1 else heads * HEAD_DIM
+    return x.data_ptr(), st[0] if shape[0] > 1 else shape[1] * HEAD_DIM
 
 
 def kv_qk_norm_rope(layout, rope, positions, q, k, q_out, k_out, q_weight=None, k_weight=None, eps=1e-6, v=None,
@@ -487,27 +507,25 @@ def kv_qk_norm_rope(layout, rope, positions, q, k, q_out, k_out, q_weight=None, 
     """Head norms (with a weight) and rotary positions of q [n][H_q][d] and k [n][H_kv][d], fp16 or bf16,
     into fp16 q_out and k_out; v is cast into v_out.  Each input may be None with its output.  `layout`: a
     Layout or a cache; `rope`: a RopeTable."""
-    fn = "kv_qk_norm_rope"
+    fn, gpu = "kv_qk_norm_rope", _gpu()
     L = _layout_of(layout)
-    given = next((x for x in (q, k, v) if x is not None), None)
-    if given is None:
-        raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, "no rows given")
+    given = q if q is not None else k if k is not None else _need(v, fn, "q, k or v")
     n, dt = given.shape[0], given.dtype
-    if dt not in (torch.float16, torch.bfloat16):
+    if dt is not torch.float16 and dt is not torch.bfloat16:
         raise KvqError(_abi.KVQ_ERR_UNSUPPORTED, fn, f"{dt}: float16 or bfloat16")
-    stride = []
-    for x, y, heads, name in ((q, q_out, L.n_q_heads, "q"), (k, k_out, L.n_kv_heads, "k"), (v, v_out, L.n_kv_heads, "v")):
-        if (x is None) != (y is None):
-            raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, f"{name} and {name}_out come together")
-        stride.append(0 if x is None else _head_rows(x, n, heads, dt, fn, name))
-        _dev(y, torch.float16, fn, name + "_out", (n, heads, HEAD_DIM), optional=True)
-    _dev(q_weight, torch.float32, fn, "q_weight", (HEAD_DIM,), optional=True)
-    _dev(k_weight, torch.float32, fn, "k_weight", (HEAD_DIM,), optional=True)
-    _dev(positions, torch.int32, fn, "positions", (n,), optional=rope.c.rot_dim == 0)
-    return check(lib().kv_qk_norm_rope(ctypes.byref(L), ctypes.byref(rope.c), _p(rope.steps), rope.mscale,
-                                       _abi.F16 if dt == torch.float16 else _abi.BF16, n, _p(positions), _p(q), stride[0],
-                                       _p(k), stride[1], _p(v), stride[2], _p(q_weight), _p(k_weight), float(eps),
-                                       _p(q_out), _p(k_out), _p(v_out), _s(stream)), fn)
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None) or (v is None) != (v_out is None):
+        raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, "an input and its output come together")
+    sq, sk = (n, L.n_q_heads, HEAD_DIM), (n, L.n_kv_heads, HEAD_DIM)
+    qa, qs = _head_rows(q, sq, dt, gpu, fn, "q")
+    ka, ks = _head_rows(k, sk, dt, gpu, fn, "k")
+    va, vs = _head_rows(v, sk, dt, gpu, fn, "v")
+    return check(lib().kv_qk_norm_rope(
+        ctypes.byref(L), ctypes.byref(rope.c), _dev(rope.steps, torch.int64, None, gpu, fn, "rope.steps"), rope.mscale,
+        _abi.F16 if dt is torch.float16 else _abi.BF16, n, _dev(positions, torch.int32, (n,), gpu, fn, "positions"), qa, qs,
+        ka, ks, va, vs, _dev(q_weight, torch.float32, _ROW, gpu, fn, "q_weight"),
+        _dev(k_weight, torch.float32, _ROW, gpu, fn, "k_weight"), eps, _dev(q_out, torch.float16, sq, gpu, fn, "q_out"),
+        _dev(k_out, torch.float16, sk, gpu, fn, "k_out"), _dev(v_out, torch.float16, sk, gpu, fn, "v_out"),
+        _raw(stream, gpu)), fn)
 
 
 def kv_decode_attn_ws(cache, seqs):
@@ -517,15 +535,13 @@ def kv_decode_attn_ws(cache, seqs):
 def kv_decode_attn(cache, seqs, q, out, ws, mod=None, lse=None, stream=None):
     """Attention of one new token per sequence over an fp16 layer; q [B][H_q][d] fp16, out fp32, `mod` an
     AttnMod, lse [B][H_q] fp32 (optional)."""
-    fn, L = "kv_decode_attn", cache.layout
-    B, shape = seqs.c.batch, (seqs.c.batch, L.n_q_heads, HEAD_DIM)
-    _dev(q, torch.float16, fn, "q", shape)
-    _dev(out, torch.float32, fn, "out", shape)
-    _dev(lse, torch.float32, fn, "lse", shape[:2], optional=True)
-    if mod is not None:
-        _mod_rows(mod, fn, L, B, B)
-    return check(lib().kv_decode_attn(_ref(L), _ref(cache), _ref(seqs), _p(q), _ref(mod) if mod is not None else None,
-                                      _p(out), _p(lse), ws.ptr, ws.nbytes, _s(stream)), fn)
+    fn, L, gpu = "kv_decode_attn", cache.layout, _gpu()
+    B, H = seqs.c.batch, L.n_q_heads
+    shape = (B, H, HEAD_DIM)
+    return check(lib().kv_decode_attn(
+        ctypes.byref(L), ctypes.byref(cache.c), ctypes.byref(seqs.c), _dev(_need(q, fn, "q"), torch.float16, shape, gpu, fn, "q"),
+        _mod(mod, fn, L, B, B, gpu), _dev(_need(out, fn, "out"), torch.float32, shape, gpu, fn, "out"),
+        _dev(lse, torch.float32, (B, H), gpu, fn, "lse"), ws.ptr, ws.nbytes, _raw(stream, gpu)), fn)
 
 
 def kv_chunk_attn_ws(cache, seqs, n_rows, max_new):
@@ -535,23 +551,20 @@ def kv_chunk_attn_ws(cache, seqs, n_rows, max_new):
 def kv_chunk_attn(cache, seqs, q, q_starts, max_new, out, ws, mod=None, lse=None, stream=None):
     """Attention of the last q_starts[b+1] - q_starts[b] (at most max_new) tokens of every sequence over an
     fp16 layer; q and out [n_rows][H_q][d] fp16, lse [n_rows][H_q] fp32 (optional)."""
-    fn, L = "kv_chunk_attn", cache.layout
-    B, n = seqs.c.batch, q.shape[0]
-    shape = (n, L.n_q_heads, HEAD_DIM)
-    _dev(q, torch.float16, fn, "q", shape)
-    _dev(out, torch.float16, fn, "out", shape)
-    _dev(lse, torch.float32, fn, "lse", shape[:2], optional=True)
-    _dev(q_starts, torch.int32, fn, "q_starts", (B + 1,))
-    if mod is not None:
-        _mod_rows(mod, fn, L, B, n)
-    return check(lib().kv_chunk_attn(_ref(L), _ref(cache), _ref(seqs), _p(q), _p(q_starts), n, int(max_new),
-                                     _ref(mod) if mod is not None else None, _p(out), _p(lse), ws.ptr, ws.nbytes,
-                                     _s(stream)), fn)
+    fn, L, gpu = "kv_chunk_attn", cache.layout, _gpu()
+    B, H, n = seqs.c.batch, L.n_q_heads, _need(q, fn, "q").shape[0]
+    shape = (n, H, HEAD_DIM)
+    return check(lib().kv_chunk_attn(
+        ctypes.byref(L), ctypes.byref(cache.c), ctypes.byref(seqs.c), _dev(q, torch.float16, shape, gpu, fn, "q"),
+        _dev(_need(q_starts, fn, "q_starts"), torch.int32, (B + 1,), gpu, fn, "q_starts"), n, max_new,
+        _mod(mod, fn, L, B, n, gpu), _dev(_need(out, fn, "out"), torch.float16, shape, gpu, fn, "out"),
+        _dev(lse, torch.float32, (n, H), gpu, fn, "lse"), ws.ptr, ws.nbytes, _raw(stream, gpu)), fn)
 
 
-def _pairs(pairs, fn):
-    _dev(pairs, torch.int32, fn, "pairs", (pairs.shape[0], 2))
-    return pairs.shape[0]
+def _pairs(pairs, gpu, fn):
+    """(address, count) of a device int32 [n][2] list."""
+    n = _need(pairs, fn, "pairs").shape[0]
+    return _dev(pairs, torch.int32, (n, 2), gpu, fn, "pairs"), n
 
 
 def kv_pages_copy_ws():
@@ -560,9 +573,10 @@ def kv_pages_copy_ws():
 
 def kv_pages_copy(cache, pairs, ws, stream=None):
     """Copies page pairs[i][0] to page pairs[i][1] (device int32 [n][2]) in every array of the layer."""
-    n = _pairs(pairs, "kv_pages_copy")
-    return check(lib().kv_pages_copy(_ref(cache.layout), _ref(cache), _p(pairs), n, ws.ptr, ws.nbytes, _s(stream)),
-                 "kv_pages_copy")
+    gpu = _gpu()
+    at, n = _pairs(pairs, gpu, "kv_pages_copy")
+    return check(lib().kv_pages_copy(ctypes.byref(cache.layout), ctypes.byref(cache.c), at, n, ws.ptr, ws.nbytes,
+                                     _raw(stream, gpu)), "kv_pages_copy")
 
 
 def kv_slots_copy_ws():
@@ -571,9 +585,10 @@ def kv_slots_copy_ws():
 
 def kv_slots_copy(cache, seqs, pairs, ws, stream=None):
     """Copies the per-sequence state (k_tail, or kT and k_absmax) of slot pairs[i][0] to slot pairs[i][1]."""
-    n = _pairs(pairs, "kv_slots_copy")
-    return check(lib().kv_slots_copy(_ref(cache.layout), _ref(cache), _ref(seqs), _p(pairs), n, ws.ptr, ws.nbytes,
-                                     _s(stream)), "kv_slots_copy")
+    gpu = _gpu()
+    at, n = _pairs(pairs, gpu, "kv_slots_copy")
+    return check(lib().kv_slots_copy(ctypes.byref(cache.layout), ctypes.byref(cache.c), ctypes.byref(seqs.c), at, n, ws.ptr,
+                                     ws.nbytes, _raw(stream, gpu)), "kv_slots_copy")
 
 
 def kvq_table_remap_ws():
@@ -582,10 +597,10 @@ def kvq_table_remap_ws():
 
 def kvq_table_remap(block_table, new_id, ws, stream=None):
     """block_table[...] = new_id[block_table[...]], in place (device int32; negative entries stay)."""
-    _dev(block_table, torch.int32, "kvq_table_remap", "block_table")
-    _dev(new_id, torch.int32, "kvq_table_remap", "new_id", (new_id.numel(),))
-    return check(lib().kvq_table_remap(_p(block_table), block_table.numel(), _p(new_id), new_id.numel(), ws.ptr,
-                                       ws.nbytes, _s(stream)), "kvq_table_remap")
+    fn, gpu = "kvq_table_remap", _gpu()
+    at = _dev(_need(block_table, fn, "block_table"), torch.int32, None, gpu, fn, "block_table")
+    ids = _dev(_need(new_id, fn, "new_id"), torch.int32, None, gpu, fn, "new_id")
+    return check(lib().kvq_table_remap(at, block_table.numel(), ids, new_id.numel(), ws.ptr, ws.nbytes, _raw(stream, gpu)), fn)
 
 
 def kvq_seq_lens_add(seq_lens, delta, stream=None):

@@ -533,3 +533,54 @@ def test_prompt_fork_and_decode_together():
     for b in range(2):
         for h in range(Hq):
             assert attn_err(sparse[b, h].cpu().numpy(), out[b, h].cpu().numpy()) <= ATTN_TOL
+
+
+# ------------------------------------------------------------------ what the binding refuses
+
+def test_binding_refuses_wrong_tensors():
+    """Wrong type, shape, gaps or place: refused before a bare pointer is taken."""
+    require_gpu()
+    c = Case(8, 2, [40], [1], "plain", 101)
+    wk = ws(kvq.kv_decode_attn_ws(c.cache, c.batch))
+    wc = ws(kvq.kv_chunk_attn_ws(c.cache, c.batch, 1, 1))
+    out, out16 = torch.zeros((1, 8, D), device="cuda"), torch.zeros((1, 8, D), device="cuda", dtype=torch.float16)
+    starts = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    gaps = torch.zeros((1, 16, D), device="cuda", dtype=torch.float16)[:, ::2]
+    few = kvq.AttnMod(slopes=torch.ones(4, device="cuda"))
+    docs = kvq.AttnMod(doc_start=torch.zeros(0, dtype=torch.int32, device="cuda"))
+    L, tab = kvq.make_layout(8, 2, 16), kvq.RopeTable(128)
+    pos, k = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros((1, 2, D), dtype=torch.float16, device="cuda")
+    pairs = torch.zeros((1, 2), dtype=torch.int32, device="cuda")
+    for call in (
+            lambda: kvq.kv_decode_attn(c.cache, c.batch, c.q.float(), out, wk),
+            lambda: kvq.kv_decode_attn(c.cache, c.batch, c.q.cpu(), out, wk),
+            lambda: kvq.kv_decode_attn(c.cache, c.batch, gaps, out, wk),
+            lambda: kvq.kv_decode_attn(c.cache, c.batch, c.q, out16, wk),
+            lambda: kvq.kv_decode_attn(c.cache, c.batch, c.q, out[:, :4], wk),
+            lambda: kvq.kv_decode_attn(c.cache, c.batch, None, out, wk),
+            lambda: kvq.kv_decode_attn(c.cache, c.batch, c.q, out, wk, mod=few),
+            lambda: kvq.kv_decode_attn(c.cache, c.batch, c.q, out, wk, mod=docs),
+            lambda: kvq.kv_decode_attn(c.cache, c.batch, c.q, out, wk, lse=out),
+            lambda: kvq.kv_chunk_attn(c.cache, c.batch, c.q, starts.long(), 1, out16, wc),
+            lambda: kvq.kv_chunk_attn(c.cache, c.batch, c.q, starts[:1], 1, out16, wc),
+            lambda: kvq.kv_chunk_attn(c.cache, c.batch, c.q, starts, 1, out, wc),
+            lambda: kvq.kv_chunk_attn(c.cache, c.batch, c.q, starts, 0, out16, wc),
+            lambda: kvq.kv_qk_norm_rope(L, tab, pos, None, k, None, k.float()),
+            lambda: kvq.kv_qk_norm_rope(L, tab, pos, None, k.float(), None, k),
+            lambda: kvq.kv_qk_norm_rope(L, tab, pos, None, k, None, None),
+            lambda: kvq.kv_qk_norm_rope(L, tab, None, None, k, None, k),
+            lambda: kvq.kv_qk_norm_rope(L, tab, pos.long(), None, k, None, k),
+            lambda: kvq.kv_qk_norm_rope(L, tab, pos, None, None, None, None),
+            lambda: kvq.kv_qk_norm_rope(L, tab, pos, k, None, k, None),
+            lambda: kvq.kv_qk_norm_rope(L, tab, pos, None, k, None, k, k_weight=torch.ones(64, device="cuda")),
+            lambda: kvq.kv_qk_norm_rope(L, tab, pos, None, k.transpose(1, 2).contiguous().transpose(1, 2), None, torch.zeros_like(k)),
+            lambda: kvq.kv_pages_copy(c.cache, pairs.long(), wk),
+            lambda: kvq.kv_pages_copy(c.cache, pairs.flatten(), wk),
+            lambda: kvq.kv_slots_copy(c.cache, c.batch, pairs.cpu(), wk),
+            lambda: kvq.kvq_table_remap(c.batch.block_table, pairs.cpu(), wk),
+            lambda: kvq.AttnMod(slopes=torch.ones(8, device="cuda", dtype=torch.float16))):
+        with pytest.raises(kvq.KvqError) as e:
+            call()
+        assert e.value.code in (_abi.KVQ_ERR_INVALID_ARG, _abi.KVQ_ERR_UNSUPPORTED)
+    with pytest.raises(kvq.KvqError):
+        kvq.RopeTable(128, scaling="other")
