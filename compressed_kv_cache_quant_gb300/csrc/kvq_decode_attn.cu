@@ -1,5 +1,5 @@
 // kv_decode_attn: attention of one new token per sequence over an fp16 layer's pages, split over the
-// cache's length; a second, dependent launch joins the splits when there is more than one.
+// cache's length and joined.
 //
 // Bound: bytes.  Every visible K and V row is read once for the H_q/H_kv <= 8 query heads of its kv head,
 // 8 flop per byte at most, so both products run on mma.sync m16n8k16 fragments that come straight from
@@ -21,8 +21,13 @@ namespace {
 
 constexpr int D = KVQ_HEAD_DIM;
 constexpr int PG = KVQ_BLOCK_TOKENS;
-constexpr int DA_NW = 4;  // warps per CTA
-constexpr int DA_NT = 32 * DA_NW;
+// Warps per CTA.  Few (sequence, kv head) rows: one CTA of DA_WIDE warps per SM, whose warps meet in shared
+// memory, so that few parts are left to join, by the part that arrives last.  Many rows: three CTAs of
+// DA_SLIM warps per SM, so that one CTA's loads fill another's beginning and end, and a second launch joins.
+constexpr int DA_WIDE = 12, DA_SLIM = 4;
+constexpr int DA_JOIN = 4;      // warps per CTA of the second launch
+constexpr int DA_TICKETS = 56;  // rows whose arrivals fit the workspace header's spare words
+constexpr int SO_ROW = D + 4;   // floats of a head's row in shared memory
 
 struct DecArgs {
     const uint16_t *k16, *v16, *q;
@@ -35,6 +40,7 @@ struct DecArgs {
     float2* ml;         // [B][H][n_splits][GQ] running maximum (log2) and sum
     KvqWsHeader* hdr;
     int32_t n_splits, pps;
+    int32_t wide;       // the last part of a row joins them (no second launch)
 };
 
 __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -108,10 +114,31 @@ __device__ __forceinline__ bool span_of(const DecArgs& a, int b, Span* s) {
     return true;
 }
 
-template <bool CAP, bool BIAS>
-__global__ void __launch_bounds__(DA_NT) decode_attn_kernel(DecArgs a) {
-    __shared__ float so[DA_NW][8][D + 4];
+// Adds part r of a row (four dims per lane), weighted against the row's maximum, and zeroes it.
+__device__ __forceinline__ void join_part(const DecArgs& a, int64_t r, int lane, float mx, float4* x, float* y) {
+    const float2 v = __ldcg(&a.ml[r]);
+    float4* part = reinterpret_cast<float4*>(a.part + r * D) + lane;
+    const float4 w = __ldcg(part);
+    const float f = v.x == -INFINITY ? 0.0f : exp2f(v.x - mx);
+    x->x += f * w.x;
+    x->y += f * w.y;
+    x->z += f * w.z;
+    x->w += f * w.w;
+    *y += f * v.y;
+    *part = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+}
+__device__ __forceinline__ void finish_row(const DecArgs& a, int64_t r, int lane, float mx, float4 x, float y) {
+    const float inv = y == 0.0f ? 0.0f : 1.0f / y;  // nothing visible: 0
+    reinterpret_cast<float4*>(a.out + r * D)[lane] = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+    if (a.lse != nullptr && lane == 0) a.lse[r] = y == 0.0f ? -INFINITY : (mx + log2f(y)) * KVQ_LN2;
+}
+
+template <bool CAP, bool BIAS, int DA_NW>
+__global__ void __launch_bounds__(32 * DA_NW) decode_attn_kernel(DecArgs a) {
+    constexpr int DA_NT = 32 * DA_NW;
+    extern __shared__ __align__(16) float so[];   // [DA_NW][GQ][SO_ROW] unnormalised outputs
     __shared__ float sm[DA_NW][8], sl[DA_NW][8];
+    __shared__ int is_last;
     const int split = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int GQ = a.GQ, Hq = a.H * GQ;
@@ -245,7 +272,8 @@ __global__ void __launch_bounds__(DA_NT) decode_attn_kernel(DecArgs a) {
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            float* dst = &so[warp][2 * t + e][64 * c + 8 * g];
+            if (2 * t + e >= GQ) break;
+            float* dst = so + (warp * GQ + 2 * t + e) * SO_ROW + 64 * c + 8 * g;
 #pragma unroll
             for (int j = 0; j < 8; j += 4)
                 *reinterpret_cast<float4*>(dst + j) = make_float4(o[j][2 * c + e], o[j + 1][2 * c + e],
@@ -263,7 +291,7 @@ __global__ void __launch_bounds__(DA_NT) decode_attn_kernel(DecArgs a) {
 #pragma unroll
         for (int w = 0; w < DA_NW; ++w) {
             const float f = sm[w][e] == -INFINITY ? 0.0f : exp2f(sm[w][e] - mx);
-            x += f * so[w][e][d];
+            x += f * so[(w * GQ + e) * SO_ROW + d];
             y += f * sl[w][e];
         }
         if (sp.used == 1) {
@@ -276,13 +304,47 @@ __global__ void __launch_bounds__(DA_NT) decode_attn_kernel(DecArgs a) {
             if (d == 0) a.ml[r] = make_float2(mx, y);
         }
     }
+    if (!a.wide || sp.used == 1) return;
+    // the part that arrives last joins the row's parts, in their order, and leaves the workspace zeroed
+    __threadfence();
+    __syncthreads();
+    int32_t* ticket = &a.hdr->pad[bh];
+    if (tid == 0) is_last = atomicAdd(ticket, 1) == sp.used - 1;
+    __syncthreads();
+    if (!is_last) return;
+    __threadfence();
+    constexpr int MOST = DA_NW;           // DA_NW / GQ warps per head, each takes every so-many-th part
+    const int per = max(1, MOST / GQ), e = warp % GQ, turn = warp / GQ;
+    const int64_t first = bh * a.n_splits * GQ + e;
+    float mx = -INFINITY, y = 0.0f;
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (turn < per) {
+        for (int s = lane; s < sp.used; s += 32) mx = fmaxf(mx, __ldcg(&a.ml[first + (int64_t)s * GQ]).x);
+        mx = kvq_warp_max(mx);
+#pragma unroll 8
+        for (int s = turn; s < sp.used; s += per) join_part(a, first + (int64_t)s * GQ, lane, mx, &x, &y);
+        float* dst = so + (turn * GQ + e) * SO_ROW;
+        reinterpret_cast<float4*>(dst)[lane] = x;
+        if (lane == 0) dst[D] = y;
+    }
+    __syncthreads();  // also: every warp has read the maxima
+    for (int64_t i = tid; i < (int64_t)sp.used * GQ; i += DA_NT) a.ml[bh * a.n_splits * GQ + i] = make_float2(0.0f, 0.0f);
+    if (tid == 0) *ticket = 0;
+    if (turn != 0) return;
+    for (int w = 1; w < per; ++w) {
+        const float* src = so + (w * GQ + e) * SO_ROW;
+        const float4 z = reinterpret_cast<const float4*>(src)[lane];
+        x.x += z.x, x.y += z.y, x.z += z.z, x.w += z.w;
+        y += src[D];
+    }
+    finish_row(a, (int64_t)b * Hq + h * GQ + e, lane, mx, x, y);
 }
 
 // Joins the parts of one (sequence, query head) in their order and leaves the workspace zeroed.  The
-// warps take every DA_NW-th part, so the loads of a long split list overlap.
-__global__ void __launch_bounds__(DA_NT) decode_join_kernel(DecArgs a) {
-    __shared__ float4 so[DA_NW][32];
-    __shared__ float sl[DA_NW];
+// warps take every DA_JOIN-th part, so the loads of a long split list overlap.
+__global__ void __launch_bounds__(32 * DA_JOIN) decode_join_kernel(DecArgs a) {
+    __shared__ float4 so[DA_JOIN][32];
+    __shared__ float sl[DA_JOIN];
     const int hq = blockIdx.x, b = blockIdx.y, h = hq / a.GQ, e = hq % a.GQ;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     kvq_pdl_begin();
@@ -295,56 +357,41 @@ __global__ void __launch_bounds__(DA_NT) decode_join_kernel(DecArgs a) {
     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float y = 0.0f;
 #pragma unroll 4
-    for (int s = warp; s < sp.used; s += DA_NW) {
-        const int64_t r = first + (int64_t)s * a.GQ;
-        const float2 v = a.ml[r];
-        float4* part = reinterpret_cast<float4*>(a.part + r * D) + lane;
-        const float4 w = *part;
-        const float f = v.x == -INFINITY ? 0.0f : exp2f(v.x - mx);
-        x.x += f * w.x;
-        x.y += f * w.y;
-        x.z += f * w.z;
-        x.w += f * w.w;
-        y += f * v.y;
-        *part = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    }
+    for (int s = warp; s < sp.used; s += DA_JOIN) join_part(a, first + (int64_t)s * a.GQ, lane, mx, &x, &y);
     so[warp][lane] = x;
     if (lane == 0) sl[warp] = y;
     __syncthreads();  // also: every warp has read the maxima
-    for (int s = threadIdx.x; s < sp.used; s += DA_NT) a.ml[first + (int64_t)s * a.GQ] = make_float2(0.0f, 0.0f);
+    for (int s = threadIdx.x; s < sp.used; s += 32 * DA_JOIN) a.ml[first + (int64_t)s * a.GQ] = make_float2(0.0f, 0.0f);
     if (warp != 0) return;
 #pragma unroll
-    for (int w = 1; w < DA_NW; ++w) {
+    for (int w = 1; w < DA_JOIN; ++w) {
         const float4 z = so[w][lane];
-        x.x += z.x;
-        x.y += z.y;
-        x.z += z.z;
-        x.w += z.w;
+        x.x += z.x, x.y += z.y, x.z += z.z, x.w += z.w;
         y += sl[w];
     }
-    const int64_t r = (int64_t)b * a.H * a.GQ + hq;
-    const float inv = y == 0.0f ? 0.0f : 1.0f / y;  // nothing visible: 0
-    reinterpret_cast<float4*>(a.out + r * D)[lane] = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-    if (a.lse != nullptr && lane == 0) a.lse[r] = y == 0.0f ? -INFINITY : (mx + log2f(y)) * KVQ_LN2;
+    finish_row(a, (int64_t)b * a.H * a.GQ + hq, lane, mx, x, y);
 }
 
 struct DecPlan {
     int n_splits, pps;
+    bool wide;
     size_t off_ml, off_part, bytes;
 };
 
-// Splits by size alone: one sequence is cut into as many equal parts as there are resident CTAs per kv
-// head (one wave); a batch, whose sequences differ in length, into parts of equal pages, small enough for
-// about eight waves, so that the long ones do not finish alone.
+// Splits by size alone.  Few rows whose work is either one sequence (equal parts) or short: as many parts
+// as there are SMs per row, one wave.  Else parts of equal pages, small enough for about eight waves, so
+// that the long sequences of a batch do not finish alone.
 DecPlan dec_plan(const kvq_layout* L, const kvq_seqs* S) {
     DecPlan p;
     const int H = L->n_kv_heads, GQ = L->n_q_heads / H, B = std::max(S->batch, 1);
     const int pages = std::max(1, (S->max_len + PG - 1) / PG);
-    const int64_t slots = 3 * (int64_t)kvq_num_sms();
-    const int64_t rows = (int64_t)B * H;
-    const int64_t want = std::max<int64_t>(1, (rows <= slots ? slots : 8 * slots) / rows);
-    p.pps = (int)std::max<int64_t>((pages + want - 1) / want, 2 * DA_NW);
-    p.pps = (p.pps + DA_NW - 1) / DA_NW * DA_NW;
+    const int64_t rows = (int64_t)B * H, sms = kvq_num_sms();
+    p.wide = rows <= DA_TICKETS && (B == 1 || rows * pages <= 16 * DA_WIDE * sms);
+    const int nw = p.wide ? DA_WIDE : DA_SLIM;
+    const int64_t slots = p.wide ? sms : 3 * sms;
+    const int64_t want = std::max<int64_t>(1, (p.wide || rows <= slots ? slots : 8 * slots) / rows);
+    p.pps = (int)std::max<int64_t>((pages + want - 1) / want, nw);
+    p.pps = (p.pps + nw - 1) / nw * nw;
     p.n_splits = (pages + p.pps - 1) / p.pps;
     const size_t parts = p.n_splits > 1 ? (size_t)rows * p.n_splits * GQ : 0;
     p.off_ml = sizeof(KvqWsHeader);
@@ -393,13 +440,24 @@ extern "C" int kv_decode_attn(const kvq_layout* L, const kvq_pool* P, const kvq_
     a.n_splits = p.n_splits, a.pps = p.pps;
     const dim3 grid(p.n_splits, L->n_kv_heads, S->batch);
     const bool cap = a.mod.post != 0.0f, bias = a.mod.slopes != nullptr;
+    a.wide = p.wide;
+    const int nw = p.wide ? DA_WIDE : DA_SLIM;
+    const size_t smem = (size_t)nw * a.GQ * SO_ROW * sizeof(float);
     const auto go = [&](auto kernel) {
-        cudaError_t e = kvq_launch_pdl(kernel, grid, dim3(DA_NT), 0, kvq_stream(stream), a);
-        if (e == cudaSuccess && p.n_splits > 1)
-            e = kvq_launch_pdl(decode_join_kernel, dim3(L->n_q_heads, S->batch), dim3(DA_NT), 0, kvq_stream(stream), a);
+        // the two halves of a 128-byte line are asked for by neighbouring loads: with the smallest L1 the
+        // second one goes out again (948 instead of 732 us for sixteen sequences of 4K-32K)
+        const int rc = kvq_prepare_kernel((const void*)kernel, nw * 8 * SO_ROW * (int)sizeof(float), true);
+        if (rc) return rc;
+        cudaError_t e = kvq_launch_pdl(kernel, grid, dim3(32 * nw), smem, kvq_stream(stream), a);
+        if (e == cudaSuccess && p.n_splits > 1 && !p.wide)
+            e = kvq_launch_pdl(decode_join_kernel, dim3(L->n_q_heads, S->batch), dim3(32 * DA_JOIN), 0, kvq_stream(stream), a);
         if (e != cudaSuccess) return kvq_fail(KVQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
         return (int)KVQ_OK;
     };
-    if (cap) return bias ? go(decode_attn_kernel<true, true>) : go(decode_attn_kernel<true, false>);
-    return bias ? go(decode_attn_kernel<false, true>) : go(decode_attn_kernel<false, false>);
+    if (p.wide) {
+        if (cap) return bias ? go(decode_attn_kernel<true, true, DA_WIDE>) : go(decode_attn_kernel<true, false, DA_WIDE>);
+        return bias ? go(decode_attn_kernel<false, true, DA_WIDE>) : go(decode_attn_kernel<false, false, DA_WIDE>);
+    }
+    if (cap) return bias ? go(decode_attn_kernel<true, true, DA_SLIM>) : go(decode_attn_kernel<true, false, DA_SLIM>);
+    return bias ? go(decode_attn_kernel<false, true, DA_SLIM>) : go(decode_attn_kernel<false, false, DA_SLIM>);
 }

@@ -167,8 +167,9 @@ __host__ __device__ static inline void kvq_v_code_pos(int tok, int d, int bits, 
 // Once per (kernel, device): prefer the largest shared-memory carveout, so that
 // the kernels of a decode step never make the SMs repartition L1 and shared
 // memory between launches, and allow `dyn_smem_max` bytes of dynamic shared
-// memory.  Returns KVQ_OK or KVQ_ERR_CUDA.
-int kvq_prepare_kernel(const void* func, int dyn_smem_max);
+// memory.  keep_l1: the carveout stays the driver's choice, for a kernel that streams through L1.
+// Returns KVQ_OK or KVQ_ERR_CUDA.
+int kvq_prepare_kernel(const void* func, int dyn_smem_max, bool keep_l1 = false);
 // kv_mixed_layer_decode's second launch (kvq_sparse.cu): the dense kv heads' attention over every token
 size_t kvq_dense_heads_attn_ws(const kvq_layout* L, const kvq_seqs* S);
 int kvq_dense_heads_attn(const kvq_layout* L, const kvq_pool* P, const kvq_seqs* S, const uint16_t* q,

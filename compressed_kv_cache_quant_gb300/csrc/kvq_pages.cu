@@ -2,9 +2,10 @@
 // forked sequence, renaming pages in a block table, and the host side of forking and compacting.
 //
 // Both copies are bound by bytes: each one is read and written once.  A page of a layer is two to four
-// pieces, one per array; a CTA copies 16 KB of a page's concatenated pieces, every thread four 16-byte
-// loads before the first store, so a few CTAs per SM keep enough bytes in flight.  Pairs are read on the
-// device, so one captured launch serves every list of the same length.
+// pieces, one per array; a step of a CTA copies 16 KB of a page's concatenated pieces, every thread four
+// 16-byte loads before the first store.  The grid is resident (8 CTAs per SM) and walks the steps, with
+// the next step's ids read ahead, so that no load waits for an id.  Pairs are read on the device, so one
+// captured launch serves every list of the same length.
 #include <algorithm>
 #include <vector>
 
@@ -29,38 +30,44 @@ struct CopyArgs {
     KvqWsHeader* hdr;
 };
 
-// The (source, destination) of pair i, or false when the pair copies nothing.
-__device__ __forceinline__ bool pair_of(const int32_t* pairs, int i, int64_t n_items, KvqWsHeader* hdr, int32_t* src,
-                                        int32_t* dst) {
-    *src = pairs[2 * i];
-    *dst = pairs[2 * i + 1];
-    if (*src < 0 || *dst < 0 || *src >= n_items || *dst >= n_items) {
+// Whether pair i = (src, dst) copies anything; flags an id outside the pool.
+__device__ __forceinline__ bool pair_ok(int2 p, int i, int64_t n_items, KvqWsHeader* hdr) {
+    if (p.x < 0 || p.y < 0 || p.x >= n_items || p.y >= n_items) {
         if (threadIdx.x == 0) kvq_dev_flag(hdr, KVQ_DEV_BAD_PAGE, i);
         return false;
     }
-    return *src != *dst;
+    return p.x != p.y;
 }
 
-__global__ void __launch_bounds__(PC_NT) pages_copy_kernel(CopyArgs a) {
+__global__ void __launch_bounds__(PC_NT, 8) pages_copy_kernel(const __grid_constant__ CopyArgs a, int tiles) {
     const int units = a.end[a.n_arr - 1];
-    for (int i = blockIdx.y; i < a.n_pairs; i += gridDim.y) {
-        int32_t src, dst;
-        if (!pair_of(a.pairs, i, a.n_items, a.hdr, &src, &dst)) continue;
+    const int64_t total = (int64_t)a.n_pairs * tiles;
+    kvq_pdl_begin();
+    int64_t it = blockIdx.x;
+    int i = (int)(it / tiles), t = (int)(it % tiles);
+    const int di = (int)(gridDim.x / tiles), dt = (int)(gridDim.x % tiles);
+    int2 p = it < total ? make_int2(a.pairs[2 * i], a.pairs[2 * i + 1]) : make_int2(0, 0);
+    while (it < total) {
         uint4 x[PC_UNROLL];
         uint4* to[PC_UNROLL];
+        const bool ok = pair_ok(p, i, a.n_items, a.hdr);
 #pragma unroll
         for (int j = 0; j < PC_UNROLL; ++j) {
-            const int u = blockIdx.x * PC_TILE + j * PC_NT + threadIdx.x;
+            const int u = t * PC_TILE + j * PC_NT + threadIdx.x;
             to[j] = nullptr;
-            if (u >= units) continue;
+            if (!ok || u >= units) continue;
             int arr = 0, from = 0;
 #pragma unroll
             for (int n = 0; n < 3; ++n)
                 if (n + 1 < a.n_arr && u >= a.end[n]) arr = n + 1, from = a.end[n];
             uint4* b = a.base[arr] + (u - from);
-            x[j] = __ldcs(b + src * a.stride[arr]);
-            to[j] = b + dst * a.stride[arr];
+            x[j] = __ldcs(b + p.x * a.stride[arr]);
+            to[j] = b + p.y * a.stride[arr];
         }
+        it += gridDim.x;
+        i += di, t += dt;
+        if (t >= tiles) t -= tiles, ++i;
+        if (it < total) p = make_int2(a.pairs[2 * i], a.pairs[2 * i + 1]);
 #pragma unroll
         for (int j = 0; j < PC_UNROLL; ++j)
             if (to[j] != nullptr) __stcs(to[j], x[j]);
@@ -81,8 +88,8 @@ struct SlotArgs {
 
 __global__ void __launch_bounds__(PC_NT) slots_copy_kernel(SlotArgs a) {
     for (int i = blockIdx.y; i < a.n_pairs; i += gridDim.y) {
-        int32_t src, dst;
-        if (!pair_of(a.pairs, i, a.max_seqs, a.hdr, &src, &dst)) continue;
+        const int32_t src = a.pairs[2 * i], dst = a.pairs[2 * i + 1];
+        if (!pair_ok(make_int2(src, dst), i, a.max_seqs, a.hdr)) continue;
         const int64_t first = (int64_t)blockIdx.x * PC_NT + threadIdx.x, step = (int64_t)gridDim.x * PC_NT;
         for (int64_t u = first; u < a.tail_units; u += step)
             a.k_tail[dst * a.tail_units + u] = a.k_tail[src * a.tail_units + u];
@@ -175,9 +182,11 @@ extern "C" int kv_pages_copy(const kvq_layout* L, const kvq_pool* P, const int32
     a.n_pairs = n_pairs;
     a.n_items = P->num_blocks;
     a.hdr = static_cast<KvqWsHeader*>(ws);
-    const dim3 grid((unsigned)((end + PC_TILE - 1) / PC_TILE), (unsigned)std::min(n_pairs, 32768));
-    pages_copy_kernel<<<grid, PC_NT, 0, kvq_stream(stream)>>>(a);
-    return kvq_launch_status(fn);
+    const int tiles = (int)((end + PC_TILE - 1) / PC_TILE);
+    const int64_t grid = std::min<int64_t>((int64_t)n_pairs * tiles, 8 * (int64_t)kvq_num_sms());
+    const cudaError_t e = kvq_launch_pdl(pages_copy_kernel, dim3((unsigned)grid), dim3(PC_NT), 0, kvq_stream(stream), a, tiles);
+    if (e != cudaSuccess) return kvq_fail(KVQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+    return KVQ_OK;
 }
 
 extern "C" int kv_slots_copy(const kvq_layout* L, const kvq_pool* P, const kvq_seqs* S, const int32_t* pairs,

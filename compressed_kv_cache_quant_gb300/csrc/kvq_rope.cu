@@ -23,7 +23,7 @@ namespace {
 constexpr int D = KVQ_HEAD_DIM;
 constexpr int RP_NT = 256;
 constexpr int RP_GROUPS = RP_NT / 8;  // head rows in flight per CTA
-constexpr int RP_TOK = 4;             // most tokens per CTA
+constexpr int RP_TOK = 8;             // most tokens per CTA
 
 struct RopeArgs {
     const void *q, *k, *v;
@@ -62,6 +62,15 @@ __device__ __forceinline__ uint4 pack_half(const float* x) {
     return w;
 }
 
+// the pairs (u, v) and (p, q) by the angles whose cosines and sines are f = (cos, sin, cos, sin)
+__device__ __forceinline__ void turn_two(float* u, float* v, float* p, float* q, float4 f) {
+    const float x = *u, y = *v, z = *p, w = *q;
+    *u = x * f.x - y * f.y;
+    *v = y * f.x + x * f.y;
+    *p = z * f.z - w * f.w;
+    *q = w * f.z + z * f.w;
+}
+
 // The two 8-value chunks of a head row that lane l (< 8) of a group holds.  Half layout: chunk c pairs
 // with chunk c + rot/16, and the chunks behind the rotated part go to the remaining lanes.
 template <bool INTER>
@@ -79,49 +88,89 @@ __device__ __forceinline__ void chunks(int l, int rot, int* a, int* b) {
     }
 }
 
+// One head row of a lane's group: where it is read and written, its weight, whether it is rotated.
+struct Row {
+    const void* src;
+    uint16_t* dst;
+    const float* w;   // its weights in shared memory, or NULL
+    bool turn;
+};
+template <typename T>
+__device__ __forceinline__ Row row_of(const RopeArgs& a, int64_t tok, int h, const float (*wt)[D]) {
+    Row r;
+    if (h < a.Hq) {
+        r.src = static_cast<const T*>(a.q) + tok * a.q_stride + h * D;
+        r.dst = a.qo + (tok * a.Hq + h) * D;
+        r.w = a.qw != nullptr ? wt[0] : nullptr;
+        r.turn = true;
+    } else if (h < a.Hq + a.Hk) {
+        r.src = static_cast<const T*>(a.k) + tok * a.k_stride + (h - a.Hq) * D;
+        r.dst = a.ko + (tok * a.Hk + h - a.Hq) * D;
+        r.w = a.kw != nullptr ? wt[1] : nullptr;
+        r.turn = true;
+    } else {
+        r.src = static_cast<const T*>(a.v) + tok * a.v_stride + (h - a.Hq - a.Hk) * D;
+        r.dst = a.vo + (tok * a.Hv + h - a.Hq - a.Hk) * D;
+        r.w = nullptr;
+        r.turn = false;
+    }
+    return r;
+}
+
 template <typename T, bool INTER>
-__global__ void __launch_bounds__(RP_NT) norm_rope_kernel(RopeArgs a, int tok_per_cta) {
-    __shared__ float2 cs[RP_TOK][D / 2];
+__global__ void __launch_bounds__(RP_NT) norm_rope_kernel(const __grid_constant__ RopeArgs a, int tok_per_cta) {
+    // cosines and sines by the lane that uses them: entry 8j + l holds the j-th two pairs of lane l, so that
+    // a group's 16-byte loads cover neighbouring words
+    __shared__ __align__(16) float2 cs[RP_TOK][D / 2];
+    __shared__ __align__(16) float wt[2][D];
     const int64_t t0 = (int64_t)blockIdx.x * tok_per_cta;
     const int nt = (int)min((int64_t)tok_per_cta, a.n - t0);
-    const int half = a.rot >> 1;
-    for (int i = threadIdx.x; i < nt * (D / 2); i += RP_NT) {
-        const int t = i / (D / 2), p = i % (D / 2);
-        if (p >= half) continue;
-        const uint64_t ph = (uint64_t)(int64_t)a.pos[t0 + t] * a.steps[p];
-        float s, c;
-        sincospif(__ll2float_rn((long long)ph) * 1.0842021724855044e-19f, &s, &c);  // * 2^-63: half turns
-        cs[t][p] = make_float2(c * a.mscale, s * a.mscale);
-    }
-    __syncthreads();
     const int l = threadIdx.x & 7;
     const int rows = a.Hq + a.Hk + a.Hv;
     int ca, cb;
     chunks<INTER>(l, a.rot, &ca, &cb);
-    for (int r = threadIdx.x >> 3; r < nt * rows; r += RP_GROUPS) {
-        const int t = r / rows, h = r % rows;
-        const int64_t tok = t0 + t;
-        const T* src;
-        uint16_t* dst;
-        const float* w = nullptr;
-        bool turn = true;
-        if (h < a.Hq) {
-            src = static_cast<const T*>(a.q) + tok * a.q_stride + h * D;
-            dst = a.qo + (tok * a.Hq + h) * D;
-            w = a.qw;
-        } else if (h < a.Hq + a.Hk) {
-            src = static_cast<const T*>(a.k) + tok * a.k_stride + (h - a.Hq) * D;
-            dst = a.ko + (tok * a.Hk + h - a.Hq) * D;
-            w = a.kw;
-        } else {
-            src = static_cast<const T*>(a.v) + tok * a.v_stride + (h - a.Hq - a.Hk) * D;
-            dst = a.vo + (tok * a.Hv + h - a.Hq - a.Hk) * D;
-            turn = false;
-        }
+    kvq_pdl_begin();
+    // the first rows are on their way while the angles are computed, every further row while the one
+    // before is
+    int t = 0, h = threadIdx.x >> 3;
+    const auto settle = [&] {
+        while (h >= rows) h -= rows, ++t;
+    };
+    settle();
+    Row r;
+    uint4 x4, y4;
+    const auto fetch = [&] {
+        if (t >= nt) return;
+        r = row_of<T>(a, t0 + t, h, wt);
+        x4 = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(r.src) + 8 * ca));
+        y4 = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(r.src) + 8 * cb));
+    };
+    fetch();
+    if (threadIdx.x < D) {
+        if (a.qw != nullptr) wt[0][threadIdx.x] = a.qw[threadIdx.x];
+        if (a.kw != nullptr) wt[1][threadIdx.x] = a.kw[threadIdx.x];
+    }
+    const int half = a.rot >> 1;
+    for (int i = threadIdx.x; i < nt * (D / 2); i += RP_NT) {
+        const int k = i / (D / 2), p = i % (D / 2);
+        if (p >= half) continue;
+        const uint64_t ph = (uint64_t)(int64_t)a.pos[t0 + k] * a.steps[p];
+        float s, c;
+        sincospif(__ll2float_rn((long long)ph) * 1.0842021724855044e-19f, &s, &c);  // * 2^-63: half turns
+        const int lane = INTER ? (p >> 2) & 7 : p >> 3, nth = INTER ? (p >> 5) * 4 + (p & 3) : p & 7;
+        cs[k][((nth >> 1) * 8 + lane) * 2 + (nth & 1)] = make_float2(c * a.mscale, s * a.mscale);
+    }
+    __syncthreads();
+    while (t < nt) {
         float x[8], y[8];
-        unpack(*reinterpret_cast<const uint4*>(src + 8 * ca), x, (T*)nullptr);
-        unpack(*reinterpret_cast<const uint4*>(src + 8 * cb), y, (T*)nullptr);
-        if (w != nullptr) {
+        unpack(x4, x, (T*)nullptr);
+        unpack(y4, y, (T*)nullptr);
+        const Row now = r;
+        const int tn = t;
+        h += RP_GROUPS;
+        settle();
+        fetch();
+        if (now.w != nullptr) {
             float ss = 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) ss += x[i] * x[i] + y[i] * y[i];
@@ -132,43 +181,25 @@ __global__ void __launch_bounds__(RP_NT) norm_rope_kernel(RopeArgs a, int tok_pe
             ss += __shfl_xor_sync(m, ss, 4);
             const float inv = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x[i] *= inv * w[8 * ca + i];
-                y[i] *= inv * w[8 * cb + i];
+            for (int i = 0; i < 8; i += 4) {
+                const float4 u = *reinterpret_cast<const float4*>(now.w + 8 * ca + i);
+                const float4 v = *reinterpret_cast<const float4*>(now.w + 8 * cb + i);
+                x[i] *= inv * u.x, x[i + 1] *= inv * u.y, x[i + 2] *= inv * u.z, x[i + 3] *= inv * u.w;
+                y[i] *= inv * v.x, y[i + 1] *= inv * v.y, y[i + 2] *= inv * v.z, y[i + 3] *= inv * v.w;
             }
         }
-        if (turn) {
+        if (now.turn) {
+            const float4* f = reinterpret_cast<const float4*>(cs[tn]) + l;
             if (INTER) {
-                if (8 * ca < a.rot) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 f = cs[t][4 * ca + i];
-                        const float u = x[2 * i], v = x[2 * i + 1];
-                        x[2 * i] = u * f.x - v * f.y;
-                        x[2 * i + 1] = v * f.x + u * f.y;
-                    }
-                }
-                if (8 * cb < a.rot) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 f = cs[t][4 * cb + i];
-                        const float u = y[2 * i], v = y[2 * i + 1];
-                        y[2 * i] = u * f.x - v * f.y;
-                        y[2 * i + 1] = v * f.x + u * f.y;
-                    }
-                }
+                if (8 * ca < a.rot) turn_two(&x[0], &x[1], &x[2], &x[3], f[0]), turn_two(&x[4], &x[5], &x[6], &x[7], f[8]);
+                if (8 * cb < a.rot) turn_two(&y[0], &y[1], &y[2], &y[3], f[16]), turn_two(&y[4], &y[5], &y[6], &y[7], f[24]);
             } else if (16 * l < a.rot) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 f = cs[t][8 * l + i];
-                    const float u = x[i], v = y[i];
-                    x[i] = u * f.x - v * f.y;
-                    y[i] = v * f.x + u * f.y;
-                }
+                for (int j = 0; j < 4; ++j) turn_two(&x[2 * j], &y[2 * j], &x[2 * j + 1], &y[2 * j + 1], f[8 * j]);
             }
         }
-        *reinterpret_cast<uint4*>(dst + 8 * ca) = pack_half(x);
-        *reinterpret_cast<uint4*>(dst + 8 * cb) = pack_half(y);
+        *reinterpret_cast<uint4*>(now.dst + 8 * ca) = pack_half(x);
+        *reinterpret_cast<uint4*>(now.dst + 8 * cb) = pack_half(y);
     }
 }
 
@@ -282,8 +313,9 @@ extern "C" int kv_qk_norm_rope(const kvq_layout* L, const kvq_rope* rope, const 
     const int64_t grid = (n_tokens + tpc - 1) / tpc;
     KVQ_REQUIRE(grid <= INT32_MAX, KVQ_ERR_UNSUPPORTED, "%s: n_tokens", fn);
     const auto go = [&](auto kernel) {
-        kernel<<<(unsigned)grid, RP_NT, 0, kvq_stream(stream)>>>(a, tpc);
-        return kvq_launch_status(fn);
+        const cudaError_t e = kvq_launch_pdl(kernel, dim3((unsigned)grid), dim3(RP_NT), 0, kvq_stream(stream), a, tpc);
+        if (e != cudaSuccess) return kvq_fail(KVQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+        return (int)KVQ_OK;
     };
     if (dtype == KVQ_F16)
         return rope->interleaved ? go(norm_rope_kernel<__half, true>) : go(norm_rope_kernel<__half, false>);

@@ -49,7 +49,7 @@ int kvq_num_sms() {
     return cache[dev];
 }
 
-int kvq_prepare_kernel(const void* func, int dyn_smem_max) {
+int kvq_prepare_kernel(const void* func, int dyn_smem_max, bool keep_l1) {
     static std::mutex mu;
     static std::map<std::pair<const void*, int>, int> done;  // (kernel, device) -> dynamic limit set
     int dev = 0;
@@ -60,8 +60,9 @@ int kvq_prepare_kernel(const void* func, int dyn_smem_max) {
     std::lock_guard<std::mutex> lk(mu);
     auto it = done.find({func, dev});
     if (it != done.end() && it->second >= dyn_smem_max) return KVQ_OK;
-    cudaError_t e = cudaFuncSetAttribute(func, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                         (int)cudaSharedmemCarveoutMaxShared);
+    cudaError_t e = cudaSuccess;
+    if (!keep_l1)
+        e = cudaFuncSetAttribute(func, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared);
     if (e == cudaSuccess && dyn_smem_max > 0)  // (static shared memory counts against the default 48 KB too)
         e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn_smem_max);
     if (e != cudaSuccess) return kvq_fail(KVQ_ERR_CUDA, "kernel attributes: %s", cudaGetErrorString(e));

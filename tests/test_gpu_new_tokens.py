@@ -183,6 +183,19 @@ def test_decode_attn(hq, hkv, mod):
     assert not bool(wk.t.any())
 
 
+@pytest.mark.parametrize("hq,hkv,mod", [(12, 3, "window_sink"), (12, 3, "cap_bias_scale"), (16, 16, "docs"), (20, 5, "plain")])
+def test_decode_attn_many_rows(hq, hkv, mod):
+    """More (sequence, kv head) rows than the one-launch form takes."""
+    require_gpu()
+    lens = [3001 - 150 * b for b in range(20)] + [0, 1]
+    c = Case(hq, hkv, lens, [1] * len(lens), mod, 88)
+    out, lse, wk = c.decode()
+    c.check(out, lse, False)
+    again, lse2, _ = c.decode(wk)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    assert not bool(wk.t.any())
+
+
 @pytest.mark.parametrize("mod", ["plain", "cap_bias_scale", "window_sink"])
 def test_decode_attn_one_long_sequence(mod):
     require_gpu()
