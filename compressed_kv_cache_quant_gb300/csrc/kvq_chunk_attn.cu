@@ -215,18 +215,24 @@ __device__ __forceinline__ bool bar_done(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-// Waits for a phase of bar; false after CA_SPIN polls or when another thread gave up.  Most waits of the
-// issuing warps find their phase done, so that case is one poll and nothing else.
-__device__ __forceinline__ bool bar_wait(Shared& S, KvqWsHeader* hdr, uint64_t* bar, uint32_t parity) {
+// Waits for a phase of bar.  After CA_SPIN polls it flags the timeout, and every wait of the CTA that is
+// not over by then returns at once: the roles run through to their ends without waiting, on data that is
+// not valid, so no step needs a branch for the failure; only the loads stop (a barrier must not be armed
+// twice).  Most waits of the issuing warps find their phase done: one poll and nothing else.
+__device__ __forceinline__ void bar_wait(Shared& S, KvqWsHeader* hdr, uint64_t* bar, uint32_t parity) {
     const uint32_t at = saddr(bar);
-    if (__builtin_expect(bar_done(at, parity), 1)) return true;
-    for (uint32_t it = 1; it < CA_SPIN; ++it) {
-        if (bar_done(at, parity)) return true;
-        if ((it & 63) == 63 && *(volatile int32_t*)&S.abort) return false;
+    for (uint32_t it = 0; !bar_done(at, parity); ++it) {
+        if ((it & 63) != 63) continue;
+        if (*(volatile int32_t*)&S.abort) return;
+        if (it > CA_SPIN) {
+            *(volatile int32_t*)&S.abort = 1;
+            kvq_dev_flag(hdr, KVQ_DEV_TIMEOUT, (int32_t)blockIdx.x);
+            return;
+        }
     }
-    *(volatile int32_t*)&S.abort = 1;
-    kvq_dev_flag(hdr, KVQ_DEV_TIMEOUT, (int32_t)blockIdx.x);
-    return false;
+}
+__device__ __forceinline__ bool aborted(Shared& S) {
+    return __any_sync(0xffffffffu, *(volatile int32_t*)&S.abort != 0);
 }
 
 // Sequence b's new tokens: *first row and count; false (flagged) when its lengths do not fit the call.
@@ -399,7 +405,8 @@ __global__ void __launch_bounds__(CA_NT, 1)
             // the same, at 79 cycles each
             const auto fetch = [&](int slot, const CUtensorMap* map, const int* at) {
                 const int st = slot % CA_NS;
-                const bool ok = __all_sync(0xffffffffu, slot < CA_NS || bar_wait(S, a.hdr, &S.kv_empty[st], ((slot / CA_NS) & 1) ^ 1));
+                if (slot >= CA_NS) bar_wait(S, a.hdr, &S.kv_empty[st], ((slot / CA_NS) & 1) ^ 1);
+                const bool ok = !aborted(S);
                 if (ok && elect()) {
                     bar_expect(&S.kv_full[st], CA_TILE);
 #pragma unroll
@@ -429,7 +436,6 @@ __global__ void __launch_bounds__(CA_NT, 1)
             const uint32_t lq = (uint32_t)smem_desc(sq, 16, 0), lk = (uint32_t)smem_desc(skv, 16, 0),
                            lv = (uint32_t)smem_desc(skv, 1024, 0);
             const auto desc = [](uint32_t hi, uint32_t lo) { return (uint64_t)hi << 32 | lo; };
-            bool ok = bar_wait(S, a.hdr, &S.q_full, 0) && bar_wait(S, a.hdr, &S.kv_full[0], 0);
             const auto qk = [&](int i, int st) {
                 if (elect()) {
                     uint32_t x = lq + (i * CA_TILE >> 4), y = lk + (st * CA_TILE >> 4);
@@ -454,44 +460,34 @@ __global__ void __launch_bounds__(CA_NT, 1)
             const auto commit = [&](uint64_t* bar) {
                 if (elect()) tc_commit(bar);
             };
-            if (ok) {
-                tc_after();
-                qk(0, 0);
-                if (nq > 1) qk(1, 0);
-                commit(&S.kv_empty[0]);
-            }
-            for (int j = 0; j < nt && ok; ++j) {
+            bar_wait(S, a.hdr, &S.q_full, 0);
+            bar_wait(S, a.hdr, &S.kv_full[0], 0);
+            tc_after();
+            qk(0, 0);
+            if (nq > 1) qk(1, 0);
+            commit(&S.kv_empty[0]);
+            for (int j = 0; j < nt; ++j) {
                 const int sv = (2 * j + 1) % CA_NS, sk = (2 * j + 2) % CA_NS;
                 const bool more = j + 1 < nt;
-                ok = bar_wait(S, a.hdr, &S.kv_full[sv], ((2 * j + 1) / CA_NS) & 1);
-                if (!ok) break;
+                bar_wait(S, a.hdr, &S.kv_full[sv], ((2 * j + 1) / CA_NS) & 1);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     if (i == nq) break;
-                    if (!bar_wait(S, a.hdr, &S.p_full[i][0], j & 1)) {
-                        ok = false;
-                        break;
-                    }
+                    bar_wait(S, a.hdr, &S.p_full[i][0], j & 1);
                     tc_after();
                     pv(i, sv, 0, j > 0);
-                    if (!bar_wait(S, a.hdr, &S.p_full[i][1], j & 1)) {
-                        ok = false;
-                        break;
-                    }
+                    bar_wait(S, a.hdr, &S.p_full[i][1], j & 1);
                     tc_after();
                     pv(i, sv, 1, true);
                     if (i == nq - 1) commit(&S.kv_empty[sv]);
                     if (more) {
-                        if (i == 0 && !bar_wait(S, a.hdr, &S.kv_full[sk], ((2 * j + 2) / CA_NS) & 1)) {
-                            ok = false;
-                            break;
-                        }
+                        if (i == 0) bar_wait(S, a.hdr, &S.kv_full[sk], ((2 * j + 2) / CA_NS) & 1);
                         qk(i, sk);
                     } else {
                         commit(&S.o_full[i]);
                     }
                 }
-                if (ok && more) commit(&S.kv_empty[sk]);
+                if (more) commit(&S.kv_empty[sk]);
             }
         }
     } else {
@@ -514,16 +510,13 @@ __global__ void __launch_bounds__(CA_NT, 1)
         const float slope2 = BIAS && valid ? a.mod.slopes[h * GQ + r % GQ] * KVQ_LOG2E : 0.0f;
         float m = -INFINITY, l = 0.0f;
         if (i < nq) {
-            bool ok = true;
-            for (int j = 0; j < nt && ok; ++j) {
+            for (int j = 0; j < nt; ++j) {
                 const int t0 = tile_of(it0 + j) * CA_KEYS;
                 // rows at and behind T may hold anything: 0 * NaN must not reach O
                 const bool tail = T < t0 + CA_KEYS && (T & (PG - 1)) != 0 && T > t0;
-                ok = bar_wait(S, a.hdr, &S.s_full[i], j & 1) &&
-                     (!tail || bar_wait(S, a.hdr, &S.kv_full[(2 * j + 1) % CA_NS], ((2 * j + 1) / CA_NS) & 1));
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
+                bar_wait(S, a.hdr, &S.s_full[i], j & 1);
                 if (tail) {
+                    bar_wait(S, a.hdr, &S.kv_full[(2 * j + 1) % CA_NS], ((2 * j + 1) / CA_NS) & 1);
                     const uint32_t base = skv + (2 * j + 1) % CA_NS * CA_TILE;
                     const int r0 = T - t0, r1 = (r0 + PG - 1) / PG * PG;
                     for (int x = tid & 127; x < (r1 - r0) * 16; x += 128) {
@@ -555,7 +548,9 @@ __global__ void __launch_bounds__(CA_NT, 1)
                 if (t0 < maxlo || t0 + CA_KEYS > minhi) {
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
+                        // an edge crosses few of a warp's words of 32 columns
                         const uint32_t bits = columns(see.x - t0, see.y - t0, w) | columns(see.z - t0, see.w - t0, w);
+                        if (__all_sync(0xffffffffu, bits == ~0u)) continue;
 #pragma unroll
                         for (int c = 0; c < 32; ++c)
                             if (!(bits >> c & 1)) s[32 * w + c] = -INFINITY;
@@ -601,11 +596,12 @@ __global__ void __launch_bounds__(CA_NT, 1)
                     __syncwarp();
                     if (lane == 0) bar_arrive(&S.p_full[i][c / 64]);
                 };
-                sum2[0] = sum2[1] = 0;
-                weights(0, true);
-                const float mx = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]) * scale;
-                const bool grew = mx > m + CA_SLACK || (m == -INFINITY && mx > m);
-                if (__any_sync(0xffffffffu, grew)) {
+                for (;;) {
+                    sum2[0] = sum2[1] = 0;
+                    weights(0, true);
+                    const float mx = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]) * scale;
+                    const bool grew = mx > m + CA_SLACK || (m == -INFINITY && mx > m);
+                    if (!__any_sync(0xffffffffu, grew)) break;
                     const float f = grew ? ex2(m - mx) : 1.0f;
                     if (grew) m = mx;
                     l *= f;
@@ -619,8 +615,6 @@ __global__ void __launch_bounds__(CA_NT, 1)
                             tm_st32(to + c, o);
                         }
                     }
-                    sum2[0] = sum2[1] = 0;
-                    weights(0, false);
                 }
                 hand_over(0);
                 weights(64, false);
@@ -630,8 +624,8 @@ __global__ void __launch_bounds__(CA_NT, 1)
                 l += l0 + l1;
             }
             // ---- this row's output
-            ok = ok && (nt == 0 || bar_wait(S, a.hdr, &S.o_full[i], 0));
-            if (__all_sync(0xffffffffu, ok)) {
+            if (nt > 0) bar_wait(S, a.hdr, &S.o_full[i], 0);
+            if (!aborted(S)) {
                 tc_after();
                 const int64_t out_row = (int64_t)(first + tok0 + tok) * a.H * GQ + h * GQ + r % GQ;
                 const int64_t part_row = (((int64_t)blockIdx.x * a.H + h) * a.n_splits + split) * CA_ROWS + r;
