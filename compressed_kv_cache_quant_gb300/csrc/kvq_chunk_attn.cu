@@ -685,52 +685,45 @@ __global__ void __launch_bounds__(CA_NT, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TM_COLS) : "memory");
 }
 
-// Joins the splits of 32 rows of an item in their order and leaves the workspace zeroed.
-constexpr int CJ_NT = 256;
-__global__ void __launch_bounds__(CJ_NT) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
-    __shared__ int item_b, item_tok;
+// Joins the splits of an item's rows, a warp per row, in their order, and leaves the workspace zeroed.
+constexpr int CJ_NW = 8;
+__global__ void __launch_bounds__(32 * CJ_NW) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int GQ = a.GQ, tpc = CA_ROWS / GQ, h = blockIdx.y;
+    const int GQ = a.GQ, tpc = CA_ROWS / GQ, h = blockIdx.y, r = blockIdx.z * CJ_NW + warp;
     kvq_pdl_begin();
-    if (warp == 0) {
-        int b, tok;
-        find_item(a, blockIdx.x, tpc, &b, &tok);
-        if (lane == 0) item_b = b, item_tok = tok;
+    int b, tok;
+    find_item(a, blockIdx.x, tpc, &b, &tok);
+    if (b < 0) return;
+    const int first = a.q_starts[b], n = a.q_starts[b + 1] - first;
+    if (r >= min(tpc, n - tok) * GQ) return;
+    const int64_t p0 = ((int64_t)blockIdx.x * a.H + h) * a.n_splits * CA_ROWS + r;
+    float mx = -INFINITY;
+    for (int s = lane; s < a.n_splits; s += 32) mx = fmaxf(mx, a.ml[p0 + (int64_t)s * CA_ROWS].x);
+    mx = kvq_warp_max(mx);
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float y = 0.0f;
+#pragma unroll 8
+    for (int s = 0; s < a.n_splits; ++s) {
+        const int64_t row = p0 + (int64_t)s * CA_ROWS;
+        const float2 v = a.ml[row];
+        float4* part = reinterpret_cast<float4*>(a.part + row * D) + lane;
+        const float4 w = *part;
+        const bool some = v.y != 0.0f;   // (a split without a visible token wrote no row)
+        const float f = some ? exp2f(v.x - mx) : 0.0f;
+        x.x += some ? f * w.x : 0.0f;
+        x.y += some ? f * w.y : 0.0f;
+        x.z += some ? f * w.z : 0.0f;
+        x.w += some ? f * w.w : 0.0f;
+        y += f * v.y;
+        *part = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
-    __syncthreads();
-    if (item_b < 0) return;
-    const int first = a.q_starts[item_b], n = a.q_starts[item_b + 1] - first;
-    const int rows = min(tpc, n - item_tok) * GQ;
-    for (int r = blockIdx.z * 32 + warp; r < min(rows, (int)blockIdx.z * 32 + 32); r += CJ_NT / 32) {
-        const int64_t p0 = ((int64_t)blockIdx.x * a.H + h) * a.n_splits * CA_ROWS + r;
-        float mx = -INFINITY;
-        for (int s = lane; s < a.n_splits; s += 32) mx = fmaxf(mx, a.ml[p0 + (int64_t)s * CA_ROWS].x);
-        mx = kvq_warp_max(mx);
-        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        float y = 0.0f;
-        for (int s = 0; s < a.n_splits; ++s) {
-            const int64_t row = p0 + (int64_t)s * CA_ROWS;
-            const float2 v = a.ml[row];
-            if (v.y == 0.0f) continue;
-            const float f = v.x == -INFINITY ? 0.0f : exp2f(v.x - mx);
-            float4* part = reinterpret_cast<float4*>(a.part + row * D) + lane;
-            const float4 w = *part;
-            x.x += f * w.x;
-            x.y += f * w.y;
-            x.z += f * w.z;
-            x.w += f * w.w;
-            y += f * v.y;
-        }
-        __syncwarp();
-        for (int s = 0; s < a.n_splits; ++s)
-            reinterpret_cast<float4*>(a.part + (p0 + (int64_t)s * CA_ROWS) * D)[lane] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int s = lane; s < a.n_splits; s += 32) a.ml[p0 + (int64_t)s * CA_ROWS] = make_float2(0.0f, 0.0f);
-        const float inv = y == 0.0f ? 0.0f : 1.0f / y;
-        const int64_t out_row = (int64_t)(first + item_tok + r / GQ) * a.H * GQ + h * GQ + r % GQ;
-        reinterpret_cast<uint2*>(a.out + out_row * D)[lane] =
-            make_uint2(half2_bits(x.x * inv, x.y * inv), half2_bits(x.z * inv, x.w * inv));
-        if (a.lse != nullptr && lane == 0) a.lse[out_row] = y == 0.0f ? -INFINITY : (mx + log2f(y)) * KVQ_LN2;
-    }
+    __syncwarp();
+    for (int s = lane; s < a.n_splits; s += 32) a.ml[p0 + (int64_t)s * CA_ROWS] = make_float2(0.0f, 0.0f);
+    const float inv = y == 0.0f ? 0.0f : 1.0f / y;
+    const int64_t out_row = (int64_t)(first + tok + r / GQ) * a.H * GQ + h * GQ + r % GQ;
+    reinterpret_cast<uint2*>(a.out + out_row * D)[lane] =
+        make_uint2(half2_bits(x.x * inv, x.y * inv), half2_bits(x.z * inv, x.w * inv));
+    if (a.lse != nullptr && lane == 0) a.lse[out_row] = y == 0.0f ? -INFINITY : (mx + log2f(y)) * KVQ_LN2;
 }
 
 // ---------------------------------------------------------------- host
@@ -747,8 +740,10 @@ struct ChunkPlan {
     size_t off_ml, off_part, bytes;
 };
 
-// Enough (item, kv head) CTAs fill the SMs by themselves; fewer are split along the cache, into the
-// smallest number of parts that keeps the last wave at least 90% full, four tiles per part at least.
+// Enough (item, kv head) CTAs fill the SMs by themselves; fewer are split along the cache, into the number
+// of parts whose waves take least: a CTA's beginning, end and share of the join cost about as much as 12 of
+// its tiles (five drafted tokens of eight 32K sequences: 64 CTAs in 2 parts, one wave, 173 us; in 7 parts,
+// three full waves, 182 us).
 ChunkPlan chunk_plan(const kvq_layout* L, const kvq_seqs* S, int64_t n_rows, int32_t max_new) {
     ChunkPlan p;
     const int tpc = CA_ROWS / (L->n_q_heads / L->n_kv_heads);
@@ -758,13 +753,11 @@ ChunkPlan chunk_plan(const kvq_layout* L, const kvq_seqs* S, int64_t n_rows, int
     const int tiles = (S->max_len + CA_KEYS - 1) / CA_KEYS;
     p.n_splits = 1;
     if (ctas < sms) {
-        double best = 0.0;
         const int most = (int)std::min<int64_t>(std::max(1, tiles / 4), 4 * sms / ctas);
+        int64_t best = INT64_MAX;
         for (int s = 1; s <= most; ++s) {
-            const int64_t waves = (ctas * s + sms - 1) / sms;
-            const double fill = (double)(ctas * s) / (double)(waves * sms);
-            if (fill > best + 1e-9) best = fill, p.n_splits = s;
-            if (fill >= 0.9) break;
+            const int64_t waves = (ctas * s + sms - 1) / sms, cost = waves * ((tiles + s - 1) / s + 12);
+            if (cost < best) best = cost, p.n_splits = s;
         }
     }
     const size_t rows = p.n_splits > 1 ? (size_t)ctas * p.n_splits * CA_ROWS : 0;
@@ -865,7 +858,7 @@ extern "C" int kv_chunk_attn(const kvq_layout* L, const kvq_pool* P, const kvq_s
         if (rc) return rc;
         cudaError_t e = kvq_launch_pdl(kernel, grid, dim3(CA_NT), CA_SMEM, kvq_stream(stream), map_q, map_k, map_v, a);
         if (e == cudaSuccess && p.n_splits > 1)
-            e = kvq_launch_pdl(chunk_join_kernel, dim3((unsigned)p.items, H, CA_ROWS / 32), dim3(CJ_NT), 0, kvq_stream(stream), a);
+            e = kvq_launch_pdl(chunk_join_kernel, dim3((unsigned)p.items, H, CA_ROWS / CJ_NW), dim3(32 * CJ_NW), 0, kvq_stream(stream), a);
         if (e != cudaSuccess) return kvq_fail(KVQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
         return (int)KVQ_OK;
     };

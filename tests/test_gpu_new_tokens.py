@@ -221,8 +221,26 @@ def test_chunk_attn(hq, hkv, lens, news, mod):
     assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("mod", sorted(MODS))
+@pytest.mark.parametrize("hq,hkv,lens,news", [
+    (8, 2, [1, 700, 16, 333, 0], [1, 6, 3, 0, 0]),
+    (8, 1, [95, 1300], [3, 2]),
+    (3, 3, [24, 257], [24, 17]),
+    (4, 2, [40, 1025, 31], [4, 1, 2]),
+])
+def test_chunk_attn_few_rows(hq, hkv, lens, news, mod):
+    """A few query rows per kv head, most of a tile empty."""
+    require_gpu()
+    c = Case(hq, hkv, lens, news, mod, 70 + hq)
+    out, lse, wk = c.chunk()
+    c.check(out, lse, True)
+    again, lse2, _ = c.chunk(wk)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    assert not bool(wk.t.any())
+
+
 @pytest.mark.parametrize("news,mod", [([3, 1], "plain"), ([40, 2], "cap_bias_scale"), ([9, 300], "window_sink"),
-                                      ([700, 700], "docs_window_sink")])
+                                      ([700, 700], "docs_window_sink"), ([6, 6], "docs_window_sink")])
 def test_chunk_attn_few_rows_over_a_long_cache(news, mod):
     require_gpu()
     c = Case(8, 2, [6011, 5000], news, mod, 92)
@@ -246,8 +264,8 @@ def test_chunk_and_decode_agree_on_one_token():
 def test_pages_out_of_sight_may_be_stale():
     """With a window, pages behind it are given back: their table entries are stale, their rows another's."""
     require_gpu()
-    for call in ("decode", "chunk"):
-        c = Case(4, 2, [1000], [1] if call == "decode" else [50], "window_sink", 94)
+    for call, new in (("decode", 1), ("chunk", 50), ("chunk", 7)):
+        c = Case(4, 2, [1000], [new], "window_sink", 94)
         gone = list(range(1, (1000 - 50 - 33) // 16))
         c.cache.k16[c.bt[0, gone].tolist()] = float("inf")
         c.cache.v16[c.bt[0, gone].tolist()] = float("nan")
