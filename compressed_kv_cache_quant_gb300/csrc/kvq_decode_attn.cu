@@ -21,10 +21,18 @@ namespace {
 
 constexpr int D = KVQ_HEAD_DIM;
 constexpr int PG = KVQ_BLOCK_TOKENS;
-// Warps per CTA.  Few (sequence, kv head) rows: one CTA of DA_WIDE warps per SM, whose warps meet in shared
-// memory, so that few parts are left to join, by the part that arrives last.  Many rows: three CTAs of
-// DA_SLIM warps per SM, so that one CTA's loads fill another's beginning and end, and a second launch joins.
+// How a (sequence, kv head) row is cut into parts and joined:
+//   DA_CLUSTER  short contexts: up to 8 CTAs of DA_WIDE warps, which join through their shared memories
+//   DA_TICKET   few rows: one CTA of DA_WIDE warps per SM, whose warps meet in shared memory, so that few
+//               parts are left for the part that arrives last to join
+//   DA_SECOND   many rows: three CTAs of DA_SLIM warps per SM, so that one CTA's loads fill another's beginning
+//               and end; a second launch joins
+enum { DA_SECOND = 0, DA_TICKET = 1, DA_CLUSTER = 2 };
 constexpr int DA_WIDE = 12, DA_SLIM = 4;
+// pages per warp up to which DA_CLUSTER is taken: where 8 CTAs leave SMs idle (4096 tokens, 2 kv heads: 9.4
+// instead of 10.5 us; 8192: 13.1 instead of 11.5), and where they do not (4 x 4000 tokens, 8 kv heads: 14.0
+// instead of 15.8 us)
+constexpr int DA_FEW_PAGES = 4, DA_MOST_PAGES = 12;
 constexpr int DA_JOIN = 4;      // warps per CTA of the second launch
 constexpr int DA_TICKETS = 56;  // rows whose arrivals fit the workspace header's spare words
 constexpr int SO_ROW = D + 4;   // floats of a head's row in shared memory
@@ -40,7 +48,7 @@ struct DecArgs {
     float2* ml;         // [B][H][n_splits][GQ] running maximum (log2) and sum
     KvqWsHeader* hdr;
     int32_t n_splits, pps;
-    int32_t wide;       // the last part of a row joins them (no second launch)
+    int32_t mode;       // DA_*
 };
 
 __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -114,6 +122,19 @@ __device__ __forceinline__ bool span_of(const DecArgs& a, int b, Span* s) {
     return true;
 }
 
+__device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the value of a shared variable in the CTA of this rank of the cluster
+__device__ __forceinline__ float peer(const float* p, int rank) {
+    uint32_t at;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
 // Adds part r of a row (four dims per lane), weighted against the row's maximum, and zeroes it.
 __device__ __forceinline__ void join_part(const DecArgs& a, int64_t r, int lane, float mx, float4* x, float* y) {
     const float2 v = __ldcg(&a.ml[r]);
@@ -138,26 +159,34 @@ __global__ void __launch_bounds__(32 * DA_NW) decode_attn_kernel(DecArgs a) {
     constexpr int DA_NT = 32 * DA_NW;
     extern __shared__ __align__(16) float so[];   // [DA_NW][GQ][SO_ROW] unnormalised outputs
     __shared__ float sm[DA_NW][8], sl[DA_NW][8];
+    __shared__ float cm[8], cl[8];   // the CTA's maximum and sum per head, for its cluster
     __shared__ int is_last;
     const int split = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int GQ = a.GQ, Hq = a.H * GQ;
     kvq_pdl_begin();
-    Span sp;
-    if (!span_of(a, b, &sp)) {
-        if (tid == 0 && split == 0) kvq_dev_flag(a.hdr, KVQ_DEV_BAD_LENGTH, b);
-        return;
-    }
-    if (split >= sp.used) return;
-    const KvqSee see = sp.see;
-    const int T = sp.T, u0 = split * a.pps, u1 = min(sp.n, u0 + a.pps);
-
-    // query fragments: head g of the group, channels in the order of the key chunks
+    // what does not depend on the length is on its way while the length is: the query's fragments (head g of
+    // the group, channels in the order of the key chunks) and, where page u of the list is page u of the
+    // table, this warp's first table entry
     uint4 qf[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         qf[i] = g < GQ ? *reinterpret_cast<const uint4*>(a.q + ((int64_t)b * Hq + h * GQ + g) * D + 8 * (t + 4 * i))
                        : make_uint4(0, 0, 0, 0);
+    const int32_t* bt = a.bt + (int64_t)b * a.max_blocks;
+    const bool straight = a.mod.window == 0 && a.mod.doc_start == nullptr;
+    const int64_t u_first = (int64_t)split * a.pps + warp;
+    const int32_t early = straight && u_first * PG < a.max_len ? bt[u_first] : -1;
+    Span sp;
+    if (!span_of(a, b, &sp)) {
+        if (tid == 0 && split == 0) kvq_dev_flag(a.hdr, KVQ_DEV_BAD_LENGTH, b);
+        return;
+    }
+    const bool cluster = DA_NW == DA_WIDE && a.mode == DA_CLUSTER;
+    if (split >= sp.used && !cluster) return;
+    const KvqSee see = sp.see;
+    const int T = sp.T, u0 = split * a.pps, u1 = min(sp.n, u0 + a.pps);
+
     float slope[2] = {0.0f, 0.0f};
     if (BIAS) {
 #pragma unroll
@@ -169,21 +198,20 @@ __global__ void __launch_bounds__(32 * DA_NW) decode_attn_kernel(DecArgs a) {
     for (int j = 0; j < 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 
-    const int32_t* bt = a.bt + (int64_t)b * a.max_blocks;
     // rows of page u of this CTA's range; page 0 stands in for a bad id (flagged, the output is not valid)
-    const auto rows_of = [&](int u) -> int64_t {
-        int32_t page = bt[sp.logical(u)];
+    const auto rows_at = [&](int32_t page) -> int64_t {
         if (page < 0 || page >= a.num_blocks) {
             if (lane == 0) kvq_dev_flag(a.hdr, KVQ_DEV_BAD_PAGE, page);
             page = 0;
         }
         return ((int64_t)page * a.H + h) * PG * D;
     };
+    const auto rows_of = [&](int u) { return rows_at(bt[sp.logical(u)]); };
     Page P;
     int u = u0 + warp;
     int64_t row = 0, next = 0;
     if (u < u1) {
-        row = rows_of(u);
+        row = straight ? rows_at(early) : rows_of(u);
         load_k(P, a.k16 + row, g, t);
         load_v(P, a.v16 + row, g, t);
     }
@@ -282,29 +310,65 @@ __global__ void __launch_bounds__(32 * DA_NW) decode_attn_kernel(DecArgs a) {
     }
     __syncthreads();
     const int64_t bh = (int64_t)b * a.H + h;
-    for (int i = tid; i < GQ * D; i += DA_NT) {
-        const int e = i / D, d = i % D;
+    for (int i = tid; i < GQ * (D / 4); i += DA_NT) {   // four dims of a head per thread
+        const int e = i / (D / 4), d = 4 * (i % (D / 4));
         float mx = sm[0][e];
 #pragma unroll
         for (int w = 1; w < DA_NW; ++w) mx = fmaxf(mx, sm[w][e]);
-        float x = 0.0f, y = 0.0f;
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float y = 0.0f;
 #pragma unroll
         for (int w = 0; w < DA_NW; ++w) {
             const float f = sm[w][e] == -INFINITY ? 0.0f : exp2f(sm[w][e] - mx);
-            x += f * so[(w * GQ + e) * SO_ROW + d];
+            const float4 z = *reinterpret_cast<const float4*>(&so[(w * GQ + e) * SO_ROW + d]);
+            x.x += f * z.x, x.y += f * z.y, x.z += f * z.z, x.w += f * z.w;
             y += f * sl[w][e];
         }
-        if (sp.used == 1) {
+        if (cluster) {
+            *reinterpret_cast<float4*>(&so[e * SO_ROW + d]) = x;   // (nobody else reads these elements)
+            if (d == 0) cm[e] = mx, cl[e] = y;
+        } else if (sp.used == 1) {
             const int64_t r = (int64_t)b * Hq + h * GQ + e;
-            a.out[r * D + d] = y == 0.0f ? 0.0f : x / y;
+            const float inv = y == 0.0f ? 0.0f : 1.0f / y;
+            *reinterpret_cast<float4*>(a.out + r * D + d) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
             if (a.lse != nullptr && d == 0) a.lse[r] = y == 0.0f ? -INFINITY : (mx + log2f(y)) * KVQ_LN2;
         } else {
             const int64_t r = (bh * a.n_splits + split) * GQ + e;
-            a.part[r * D + d] = x;
+            *reinterpret_cast<float4*>(a.part + r * D + d) = x;
             if (d == 0) a.ml[r] = make_float2(mx, y);
         }
     }
-    if (!a.wide || sp.used == 1) return;
+    if (cluster) {
+        // every CTA takes its share of the outputs and adds up all parts, in their order
+        cluster_sync();
+        const int n_parts = gridDim.x;
+        for (int i = split * DA_NT + tid; i < GQ * D; i += n_parts * DA_NT) {
+            const int e = i / D, d = i % D;
+            float mx = -INFINITY, x = 0.0f, y = 0.0f;
+            float pm[8], pl[8], px[8];
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                const int rank = min(s, n_parts - 1);
+                pm[s] = peer(&cm[e], rank);
+                pl[s] = peer(&cl[e], rank);
+                px[s] = peer(&so[e * SO_ROW + d], rank);
+                if (s < n_parts) mx = fmaxf(mx, pm[s]);
+            }
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                if (s >= n_parts || pm[s] == -INFINITY) continue;
+                const float f = exp2f(pm[s] - mx);
+                x += f * px[s];
+                y += f * pl[s];
+            }
+            const int64_t r = (int64_t)b * Hq + h * GQ + e;
+            a.out[r * D + d] = y == 0.0f ? 0.0f : x / y;
+            if (a.lse != nullptr && d == 0) a.lse[r] = y == 0.0f ? -INFINITY : (mx + log2f(y)) * KVQ_LN2;
+        }
+        cluster_sync();   // no CTA ends while another reads its shared memory
+        return;
+    }
+    if (DA_NW != DA_WIDE || a.mode != DA_TICKET || sp.used == 1) return;
     // the part that arrives last joins the row's parts, in their order, and leaves the workspace zeroed
     __threadfence();
     __syncthreads();
@@ -373,27 +437,35 @@ __global__ void __launch_bounds__(32 * DA_JOIN) decode_join_kernel(DecArgs a) {
 }
 
 struct DecPlan {
-    int n_splits, pps;
-    bool wide;
+    int n_splits, pps, mode;
     size_t off_ml, off_part, bytes;
 };
 
-// Splits by size alone.  Few rows whose work is either one sequence (equal parts) or short: as many parts
-// as there are SMs per row, one wave.  Else parts of equal pages, small enough for about eight waves, so
-// that the long sequences of a batch do not finish alone.
+// Splits by size alone.  Short contexts: a cluster per row, as many CTAs as there are SMs per row, 8 at most.
+// Few rows whose work is either one sequence (equal parts) or not long: as many parts as there are SMs per
+// row, one wave.  Else parts of equal pages, small enough for about eight waves, so that the long sequences
+// of a batch do not finish alone, with 8 pages per warp at least.
 DecPlan dec_plan(const kvq_layout* L, const kvq_seqs* S) {
     DecPlan p;
     const int H = L->n_kv_heads, GQ = L->n_q_heads / H, B = std::max(S->batch, 1);
     const int pages = std::max(1, (S->max_len + PG - 1) / PG);
     const int64_t rows = (int64_t)B * H, sms = kvq_num_sms();
-    p.wide = rows <= DA_TICKETS && (B == 1 || rows * pages <= 16 * DA_WIDE * sms);
-    const int nw = p.wide ? DA_WIDE : DA_SLIM;
-    const int64_t slots = p.wide ? sms : 3 * sms;
-    const int64_t want = std::max<int64_t>(1, (p.wide || rows <= slots ? slots : 8 * slots) / rows);
-    p.pps = (int)std::max<int64_t>((pages + want - 1) / want, nw);
-    p.pps = (p.pps + nw - 1) / nw * nw;
+    const int ctas = (int)std::min<int64_t>({8, std::max<int64_t>(1, sms / rows), (pages + DA_WIDE - 1) / DA_WIDE});
+    const auto up = [](int64_t x, int64_t m) { return (x + m - 1) / m * m; };
+    if (rows <= sms && pages <= ctas * DA_WIDE * (sms / rows > 8 ? DA_FEW_PAGES : DA_MOST_PAGES)) {
+        p.mode = DA_CLUSTER;
+        p.pps = (int)up((pages + ctas - 1) / ctas, DA_WIDE);
+    } else if (rows <= DA_TICKETS && (B == 1 || rows * pages <= 16 * DA_WIDE * sms)) {
+        const int64_t want = std::max<int64_t>(1, sms / rows);
+        p.mode = DA_TICKET;
+        p.pps = (int)up((pages + want - 1) / want, DA_WIDE);
+    } else {
+        const int64_t slots = 3 * sms, want = std::max<int64_t>(1, (rows <= slots ? slots : 8 * slots) / rows);
+        p.mode = DA_SECOND;
+        p.pps = (int)up(std::max<int64_t>((pages + want - 1) / want, 8 * DA_SLIM), DA_SLIM);
+    }
     p.n_splits = (pages + p.pps - 1) / p.pps;
-    const size_t parts = p.n_splits > 1 ? (size_t)rows * p.n_splits * GQ : 0;
+    const size_t parts = p.n_splits > 1 && p.mode != DA_CLUSTER ? (size_t)rows * p.n_splits * GQ : 0;
     p.off_ml = sizeof(KvqWsHeader);
     p.off_part = kvq_round_up(p.off_ml + parts * sizeof(float2), 256);
     p.bytes = kvq_round_up(p.off_part + parts * D * sizeof(float), 256);
@@ -440,21 +512,32 @@ extern "C" int kv_decode_attn(const kvq_layout* L, const kvq_pool* P, const kvq_
     a.n_splits = p.n_splits, a.pps = p.pps;
     const dim3 grid(p.n_splits, L->n_kv_heads, S->batch);
     const bool cap = a.mod.post != 0.0f, bias = a.mod.slopes != nullptr;
-    a.wide = p.wide;
-    const int nw = p.wide ? DA_WIDE : DA_SLIM;
-    const size_t smem = (size_t)nw * a.GQ * SO_ROW * sizeof(float);
+    a.mode = p.mode;
+    const int nw = p.mode == DA_SECOND ? DA_SLIM : DA_WIDE;
     const auto go = [&](auto kernel) {
         // the two halves of a 128-byte line are asked for by neighbouring loads: with the smallest L1 the
         // second one goes out again (948 instead of 732 us for sixteen sequences of 4K-32K)
         const int rc = kvq_prepare_kernel((const void*)kernel, nw * 8 * SO_ROW * (int)sizeof(float), true);
         if (rc) return rc;
-        cudaError_t e = kvq_launch_pdl(kernel, grid, dim3(32 * nw), smem, kvq_stream(stream), a);
-        if (e == cudaSuccess && p.n_splits > 1 && !p.wide)
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3(32 * nw);
+        cfg.dynamicSmemBytes = (size_t)nw * a.GQ * SO_ROW * sizeof(float);
+        cfg.stream = kvq_stream(stream);
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim = {(unsigned)p.n_splits, 1, 1};
+        cfg.attrs = attr;
+        cfg.numAttrs = p.mode == DA_CLUSTER ? 2 : 1;
+        cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+        if (e == cudaSuccess && p.n_splits > 1 && p.mode == DA_SECOND)
             e = kvq_launch_pdl(decode_join_kernel, dim3(L->n_q_heads, S->batch), dim3(32 * DA_JOIN), 0, kvq_stream(stream), a);
         if (e != cudaSuccess) return kvq_fail(KVQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
         return (int)KVQ_OK;
     };
-    if (p.wide) {
+    if (nw == DA_WIDE) {
         if (cap) return bias ? go(decode_attn_kernel<true, true, DA_WIDE>) : go(decode_attn_kernel<true, false, DA_WIDE>);
         return bias ? go(decode_attn_kernel<false, true, DA_WIDE>) : go(decode_attn_kernel<false, false, DA_WIDE>);
     }

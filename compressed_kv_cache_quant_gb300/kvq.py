@@ -523,7 +523,7 @@ def kv_qk_norm_rope(layout, rope, positions, q, k, q_out, k_out, q_weight=None, 
         ctypes.byref(L), ctypes.byref(rope.c), _dev(rope.steps, torch.int64, None, gpu, fn, "rope.steps"), rope.mscale,
         _abi.F16 if dt is torch.float16 else _abi.BF16, n, _dev(positions, torch.int32, (n,), gpu, fn, "positions"), qa, qs,
         ka, ks, va, vs, _dev(q_weight, torch.float32, _ROW, gpu, fn, "q_weight"),
-        _dev(k_weight, torch.float32, _ROW, gpu, fn, "k_weight"), eps, _dev(q_out, torch.float16, sq, gpu, fn, "q_out"),
+        _dev(k_weight, torch.float32, _ROW, gpu, fn, "k_weight"), float(eps), _dev(q_out, torch.float16, sq, gpu, fn, "q_out"),
         _dev(k_out, torch.float16, sk, gpu, fn, "k_out"), _dev(v_out, torch.float16, sk, gpu, fn, "v_out"),
         _raw(stream, gpu)), fn)
 
@@ -556,7 +556,7 @@ def kv_chunk_attn(cache, seqs, q, q_starts, max_new, out, ws, mod=None, lse=None
     shape = (n, H, HEAD_DIM)
     return check(lib().kv_chunk_attn(
         ctypes.byref(L), ctypes.byref(cache.c), ctypes.byref(seqs.c), _dev(q, torch.float16, shape, gpu, fn, "q"),
-        _dev(_need(q_starts, fn, "q_starts"), torch.int32, (B + 1,), gpu, fn, "q_starts"), n, max_new,
+        _dev(_need(q_starts, fn, "q_starts"), torch.int32, (B + 1,), gpu, fn, "q_starts"), n, int(max_new),
         _mod(mod, fn, L, B, n, gpu), _dev(_need(out, fn, "out"), torch.float16, shape, gpu, fn, "out"),
         _dev(lse, torch.float32, (n, H), gpu, fn, "lse"), ws.ptr, ws.nbytes, _raw(stream, gpu)), fn)
 

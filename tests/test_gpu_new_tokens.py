@@ -261,6 +261,47 @@ def test_chunk_and_decode_agree_on_one_token():
     assert float((a - b.float()).abs().max()) <= 2 ** -10 * float(a.abs().max()) * 2
 
 
+def test_batches_without_a_token():
+    """Empty sequences only, with and without a block table; a batch of none; chunks without rows."""
+    require_gpu()
+    cache = kvq.LayerCache(8, 2, 16, 4, 3)
+    for bt in (torch.zeros((3, 4), dtype=torch.int32, device="cuda"), torch.zeros((3, 0), dtype=torch.int32, device="cuda")):
+        batch = kvq.Batch(bt, torch.zeros(3, dtype=torch.int32, device="cuda"), 0)
+        batch.c.block_table = None
+        q, out = rnd((3, 8, D), 40).cuda(), torch.full((3, 8, D), float("nan"), device="cuda")
+        lse = torch.zeros((3, 8), device="cuda")
+        wk = ws(kvq.kv_decode_attn_ws(cache, batch))
+        kvq.kv_decode_attn(cache, batch, q, out, wk, lse=lse)
+        kvq.kvq_check(wk)
+        assert not bool(out.any()) and bool((lse == -math.inf).all())
+        starts, o16 = torch.zeros(4, dtype=torch.int32, device="cuda"), torch.full((3, 8, D), 7.0, device="cuda").half()
+        wc = ws(kvq.kv_chunk_attn_ws(cache, batch, 3, 2))
+        kvq.kv_chunk_attn(cache, batch, q, starts, 2, o16, wc)
+        kvq.kvq_check(wc)
+        assert bool((o16 == 7).all())
+        kvq.kv_chunk_attn(cache, batch, q[:0], starts, 0, o16[:0], wc)
+    none = kvq.Batch(torch.zeros((0, 4), dtype=torch.int32, device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda"), 64)
+    kvq.kv_decode_attn(cache, none, q[:0], out[:0], wk)
+    kvq.kv_chunk_attn(cache, none, q[:0], starts[:1], 1, o16[:0], wc)
+    torch.cuda.synchronize()
+
+
+def test_one_workspace_for_every_call():
+    """Calls of all kinds and sizes in turn on one workspace: each finds it as it needs it."""
+    require_gpu()
+    cases = [Case(8, 2, [5000, 3], [40, 3], "cap", 110), Case(3, 3, [300] * 20, [1] * 20, "plain", 111),
+             Case(8, 2, [9000], [1], "window_sink", 112), Case(4, 2, [50, 60], [1, 1], "docs", 113)]
+    need = [max(kvq.kv_decode_attn_ws(c.cache, c.batch), kvq.kv_chunk_attn_ws(c.cache, c.batch, sum(c.news) + 2, max(c.news)))
+            for c in cases]
+    wk = ws(max(need))
+    want = [(c.decode() if max(c.news) == 1 else c.chunk())[0] for c in cases]
+    for _ in range(2):
+        for c, w in zip(cases, want):
+            got = (c.decode(wk) if max(c.news) == 1 else c.chunk(wk))[0]
+            assert torch.equal(got, w)
+    assert not bool(wk.t.any())
+
+
 def test_pages_out_of_sight_may_be_stale():
     """With a window, pages behind it are given back: their table entries are stale, their rows another's."""
     require_gpu()
