@@ -10,7 +10,9 @@
 // Bound: bytes (every head row is read and written once, about 3 flops per byte).  One CTA takes a few
 // tokens: 256 threads compute the tokens' cosines and sines once into shared memory (64 pairs per token,
 // reused by every head), then every group of 8 lanes takes whole head rows, 16 values per lane as two
-// 16-byte loads, so a row's norm is three shuffles and both members of every pair are in one lane.
+// 16-byte loads, so a row's norm is three shuffles and both members of every pair are in one lane.  A row's
+// loads are issued while the one before is worked on.  Measured: 32768 tokens of 32 + 8 + 8 bf16 heads with
+// norms 128 us (6.3 TB/s, 93% of the measured copy rate); eight tokens 1.8 us in a graph.
 #include <cuda_bf16.h>
 
 #include <algorithm>
