@@ -265,8 +265,9 @@ __global__ void __launch_bounds__(32 * DA_NW) decode_attn_kernel(DecArgs a) {
         float p[4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            p[e] = in0 ? exp2f(s[e] - m[e]) : 0.0f;
-            p[2 + e] = in1 ? exp2f(s[2 + e] - m[e]) : 0.0f;
+            const float ms = m[e] == -INFINITY ? 0.0f : m[e];   // (nothing but scores of -inf so far: weights 0)
+            p[e] = in0 ? exp2f(s[e] - ms) : 0.0f;
+            p[2 + e] = in1 ? exp2f(s[2 + e] - ms) : 0.0f;
             l[e] += p[e] + p[2 + e];
         }
         const uint32_t h0 = half2_bits(p[0], p[1]), h1 = half2_bits(p[2], p[3]);

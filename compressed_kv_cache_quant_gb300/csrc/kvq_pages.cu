@@ -2,8 +2,8 @@
 // forked sequence, renaming pages in a block table, and the host side of forking and compacting.
 //
 // Both copies are bound by bytes: each one is read and written once.  A page of a layer is two to four
-// pieces, one per array; a step of a CTA copies 16 KB of a page's concatenated pieces, every thread four
-// 16-byte loads before the first store.  The grid is resident (8 CTAs per SM) and walks the steps, with
+// pieces, one per array; a step of a CTA copies 8 KB of a page's concatenated pieces, every thread two 16-byte
+// loads before the first store (four: 2% slower).  The grid is resident (8 CTAs per SM) and walks the steps, with
 // the next step's ids read ahead, so that no load waits for an id.  Pairs are read on the device, so one
 // captured launch serves every list of the same length.  Measured: 20001 INT4 pages of 32 heads (3.6 GB moved)
 // 577 us, 6.2 TB/s, 92% of the measured copy rate; sixteen fp16 pages 2.0 us in a graph.
@@ -17,7 +17,7 @@ namespace {
 constexpr int D = KVQ_HEAD_DIM;
 constexpr int PG = KVQ_BLOCK_TOKENS;
 constexpr int PC_NT = 256;
-constexpr int PC_UNROLL = 4;
+constexpr int PC_UNROLL = 2;
 constexpr int PC_TILE = PC_NT * PC_UNROLL;  // 16-byte units per CTA step
 
 struct CopyArgs {

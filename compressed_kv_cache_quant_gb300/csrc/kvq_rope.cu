@@ -12,7 +12,7 @@
 // reused by every head), then every group of 8 lanes takes whole head rows, 16 values per lane as two
 // 16-byte loads, so a row's norm is three shuffles and both members of every pair are in one lane.  A row's
 // loads are issued while the one before is worked on.  Measured: 32768 tokens of 32 + 8 + 8 bf16 heads with
-// norms 128 us (6.3 TB/s, 93% of the measured copy rate); eight tokens 1.8 us in a graph.
+// norms 125 us (6.45 TB/s, 95% of the measured copy rate); eight tokens 1.8 us in a graph.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -144,8 +144,8 @@ __global__ void __launch_bounds__(RP_NT) norm_rope_kernel(const __grid_constant_
     const auto fetch = [&] {
         if (t >= nt) return;
         r = row_of<T>(a, t0 + t, h, wt);
-        x4 = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(r.src) + 8 * ca));
-        y4 = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(r.src) + 8 * cb));
+        x4 = *reinterpret_cast<const uint4*>(static_cast<const T*>(r.src) + 8 * ca);
+        y4 = *reinterpret_cast<const uint4*>(static_cast<const T*>(r.src) + 8 * cb);
     };
     fetch();
     if (threadIdx.x < D) {
@@ -309,9 +309,11 @@ extern "C" int kv_qk_norm_rope(const kvq_layout* L, const kvq_rope* rope, const 
     a.Hq = q ? L->n_q_heads : 0, a.Hk = k ? L->n_kv_heads : 0, a.Hv = v ? L->n_kv_heads : 0;
     a.n = n_tokens;
     a.qo = q_out, a.ko = k_out, a.vo = v_out;
-    // one token per CTA until every SM has CTAs enough to hide the loads' latency, then RP_TOK, which
-    // shares the launch and the angles' latency
-    const int tpc = n_tokens <= 8 * (int64_t)kvq_num_sms() ? 1 : RP_TOK;
+    // one token per CTA until every SM has CTAs enough to hide the loads' latency, then more, which share the
+    // CTA's start: 4 (2000 tokens 9.3 us, with 8 10.8 us), and RP_TOK when there are many waves of them
+    // (32768 tokens 125 us, with 4 127 us, with 2 133 us)
+    const int64_t sms = kvq_num_sms();
+    const int tpc = n_tokens <= 8 * sms ? 1 : n_tokens <= 32 * sms ? 4 : RP_TOK;
     const int64_t grid = (n_tokens + tpc - 1) / tpc;
     KVQ_REQUIRE(grid <= INT32_MAX, KVQ_ERR_UNSUPPORTED, "%s: n_tokens", fn);
     const auto go = [&](auto kernel) {

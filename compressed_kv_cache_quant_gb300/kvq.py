@@ -190,6 +190,7 @@ class RopeTable:
         self.mscale = m.value
         signed = [x - (1 << 64) if x >> 63 else x for x in steps]
         self.steps = torch.tensor(signed, dtype=torch.int64, device=device)
+        self.at, self.gpu = self.steps.data_ptr(), self.steps.get_device()
 
 
 class AttnMod:
@@ -515,16 +516,27 @@ def kv_qk_norm_rope(layout, rope, positions, q, k, q_out, k_out, q_weight=None, 
         raise KvqError(_abi.KVQ_ERR_UNSUPPORTED, fn, f"{dt}: float16 or bfloat16")
     if (q is None) != (q_out is None) or (k is None) != (k_out is None) or (v is None) != (v_out is None):
         raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, "an input and its output come together")
+    if rope.gpu != gpu:
+        raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, f"the RopeTable is on GPU {rope.gpu}, not on {gpu}")
     sq, sk = (n, L.n_q_heads, HEAD_DIM), (n, L.n_kv_heads, HEAD_DIM)
-    qa, qs = _head_rows(q, sq, dt, gpu, fn, "q")
-    ka, ks = _head_rows(k, sk, dt, gpu, fn, "k")
-    va, vs = _head_rows(v, sk, dt, gpu, fn, "v")
+    qa = ka = va = wq = wk = qo = ko = vo = None
+    qs = ks = vs = 0
+    if q is not None:
+        qa, qs = _head_rows(q, sq, dt, gpu, fn, "q")
+        qo = _dev(q_out, torch.float16, sq, gpu, fn, "q_out")
+    if k is not None:
+        ka, ks = _head_rows(k, sk, dt, gpu, fn, "k")
+        ko = _dev(k_out, torch.float16, sk, gpu, fn, "k_out")
+    if v is not None:
+        va, vs = _head_rows(v, sk, dt, gpu, fn, "v")
+        vo = _dev(v_out, torch.float16, sk, gpu, fn, "v_out")
+    if q_weight is not None:
+        wq = _dev(q_weight, torch.float32, _ROW, gpu, fn, "q_weight")
+    if k_weight is not None:
+        wk = _dev(k_weight, torch.float32, _ROW, gpu, fn, "k_weight")
     return check(lib().kv_qk_norm_rope(
-        ctypes.byref(L), ctypes.byref(rope.c), _dev(rope.steps, torch.int64, None, gpu, fn, "rope.steps"), rope.mscale,
-        _abi.F16 if dt is torch.float16 else _abi.BF16, n, _dev(positions, torch.int32, (n,), gpu, fn, "positions"), qa, qs,
-        ka, ks, va, vs, _dev(q_weight, torch.float32, _ROW, gpu, fn, "q_weight"),
-        _dev(k_weight, torch.float32, _ROW, gpu, fn, "k_weight"), float(eps), _dev(q_out, torch.float16, sq, gpu, fn, "q_out"),
-        _dev(k_out, torch.float16, sk, gpu, fn, "k_out"), _dev(v_out, torch.float16, sk, gpu, fn, "v_out"),
+        ctypes.byref(L), ctypes.byref(rope.c), rope.at, rope.mscale, _abi.F16 if dt is torch.float16 else _abi.BF16, n,
+        _dev(positions, torch.int32, (n,), gpu, fn, "positions"), qa, qs, ka, ks, va, vs, wq, wk, float(eps), qo, ko, vo,
         _raw(stream, gpu)), fn)
 
 
