@@ -12,6 +12,7 @@
 struct KvqModArgs {
     // a score q.k in the log2 domain: without a cap dot * pre; with one post * tanh(dot * pre)
     float pre, post;
+    float lin;               // the score without its cap: dot * lin
     int32_t window, n_sink;  // window 0: none
     const float* slopes;
     const int32_t* prefix_len;
@@ -21,12 +22,13 @@ struct KvqModArgs {
 // Fills m from the caller's descriptor (NULL: the plain softmax of q.k/sqrt(d)).
 static inline int kvq_mod_args(const kvq_attn_mod* mod, const char* fn, KvqModArgs* m) {
     const float dflt = 0.08838834764831845f;  // 1/sqrt(128)
-    *m = KvqModArgs{dflt * KVQ_LOG2E, 0.0f, 0, 0, nullptr, nullptr, nullptr};
+    *m = KvqModArgs{dflt * KVQ_LOG2E, 0.0f, dflt * KVQ_LOG2E, 0, 0, nullptr, nullptr, nullptr};
     if (mod == nullptr) return KVQ_OK;
     KVQ_REQUIRE(std::isfinite(mod->scale) && mod->scale >= 0.0f, KVQ_ERR_INVALID_ARG, "%s: scale", fn);
     KVQ_REQUIRE(std::isfinite(mod->softcap) && mod->softcap >= 0.0f, KVQ_ERR_INVALID_ARG, "%s: softcap", fn);
     KVQ_REQUIRE(mod->window >= 0 && mod->n_sink >= 0, KVQ_ERR_INVALID_ARG, "%s: window / n_sink", fn);
     const float scale = mod->scale > 0.0f ? mod->scale : dflt;
+    m->lin = scale * KVQ_LOG2E;
     if (mod->softcap > 0.0f) {
         m->pre = scale / mod->softcap;
         m->post = mod->softcap * KVQ_LOG2E;
@@ -62,6 +64,18 @@ __device__ __forceinline__ KvqSee kvq_see(const KvqModArgs& m, int i, int T, int
     return s;
 }
 
-// tanh to about 1 ulp of the larger of |x| and its use: 1 - 2/(1 + e^2x) away from zero (absolute error
-// 1e-7), the odd series near zero, where the former cancels.
-__device__ __forceinline__ float kvq_tanh(float x) { return tanhf(x); }
+// cap * tanh(scale * dot / cap) in the log2 domain.  A cap many times the scores leaves s(1 + x^2 Q(x^2)), s
+// the plain score and x = s/cap: on |x| <= 3/4 (Q the polynomial through the Chebyshev points, 3e-8 of the
+// score) s is rounded twice in all, where a rounded tanh near 1/5 times the cap is off by 2e-6 in the weight.
+__device__ __forceinline__ float kvq_capped(const KvqModArgs& m, float dot) {
+    const float x = dot * m.pre, u = x * x;
+    if (!(u <= 0.5625f)) return m.post * tanhf(x);
+    float q = 0.001914540189318359f;
+    q = fmaf(q, u, -0.0079409284517169f);
+    q = fmaf(q, u, 0.02161884680390358f);
+    q = fmaf(q, u, -0.05393656715750694f);
+    q = fmaf(q, u, 0.13333185017108917f);
+    q = fmaf(q, u, -0.3333333134651184f);
+    const float s = dot * m.lin;
+    return fmaf(s, u * q, s);
+}

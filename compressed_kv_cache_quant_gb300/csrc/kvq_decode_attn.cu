@@ -98,7 +98,7 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 
 // one score in the log2 domain; `away` = |i - j|
 template <bool CAP, bool BIAS>
 __device__ __forceinline__ float score(const KvqModArgs& m, float dot, float slope2, int away) {
-    float s = CAP ? m.post * kvq_tanh(dot * m.pre) : dot * m.pre;
+    float s = CAP ? kvq_capped(m, dot) : dot * m.pre;
     if (BIAS) s = fmaf(-slope2, (float)away, s);
     return s;
 }
