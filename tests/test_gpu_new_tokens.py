@@ -656,3 +656,120 @@ def test_binding_refuses_wrong_tensors():
         assert e.value.code in (_abi.KVQ_ERR_INVALID_ARG, _abi.KVQ_ERR_UNSUPPORTED)
     with pytest.raises(kvq.KvqError):
         kvq.RopeTable(128, scaling="other")
+
+
+# ------------------------------------------------------------------ at the edges of what the calls allow
+
+def test_two_streams_at_once():
+    """Calls that overlap on the GPU, each with its own workspace, give what they give alone."""
+    require_gpu()
+    cases = [Case(8, 2, [3000, 2000], [700, 300], "plain", 120), Case(8, 2, [2500, 900], [600, 900], "cap", 121)]
+    dec = [Case(8, 2, [20000], [1], "plain", 122), Case(3, 3, [900] * 20, [1] * 20, "bias", 123)]
+    want = [c.chunk(extra=0)[0] for c in cases] + [c.decode()[0] for c in dec]
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    outs, keep = [], []
+    for c in cases:
+        outs.append(torch.empty((c.q.shape[0], c.hq, D), dtype=torch.float16, device="cuda"))
+        keep.append((torch.tensor(c.starts).cuda(), ws(kvq.kv_chunk_attn_ws(c.cache, c.batch, c.q.shape[0], max(c.news)))))
+    for c in dec:
+        outs.append(torch.empty((len(c.lens), c.hq, D), device="cuda"))
+        keep.append((None, ws(kvq.kv_decode_attn_ws(c.cache, c.batch))))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for c, o, (st, wk), s in zip(cases, outs, keep, streams):
+            kvq.kv_chunk_attn(c.cache, c.batch, c.q, st, max(c.news), o, wk, mod=c.mod, stream=s)
+        for c, o, (_, wk), s in zip(dec, outs[2:], keep[2:], streams[2:]):
+            kvq.kv_decode_attn(c.cache, c.batch, c.q, o, wk, mod=c.mod, stream=s)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+
+
+def test_pages_beyond_32_bit_offsets():
+    """A pool whose last pages lie more than 2^31 values from its first."""
+    require_gpu()
+    H, n, T = 8, 140000, 300
+    low = kvq.LayerCache(H, H, 16, 40, 1)
+    cache = kvq.LayerCache(H, H, 16, n, 1)
+    assert (n - 40) * H * 16 * D > 2 ** 31
+    K, V = synth.kv_rows(T, H, 77)
+    pages = math.ceil(T / 16)
+    far = torch.arange(n - pages, n, dtype=torch.int32, device="cuda")[None]
+    near = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    lens = torch.tensor([T], dtype=torch.int32, device="cuda")
+    batches = [kvq.Batch(far, lens, T), kvq.Batch(near, lens, T)]
+    for c, b in zip((cache, low), batches):
+        kvq.kv_quant_pack(c, b, 0, 0, T, K.cuda(), V.cuda())
+    q = rnd((40, H, D), 50).cuda()
+    starts = torch.tensor([0, 40], dtype=torch.int32, device="cuda")
+    got = []
+    for c, b in zip((cache, low), batches):
+        o, o16 = torch.empty((1, H, D), device="cuda"), torch.empty((40, H, D), dtype=torch.float16, device="cuda")
+        kvq.kv_decode_attn(c, b, q[:1], o, ws(kvq.kv_decode_attn_ws(c, b)))
+        kvq.kv_chunk_attn(c, b, q, starts, 40, o16, ws(kvq.kv_chunk_attn_ws(c, b, 40, 40)))
+        got.append((o, o16))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    wk = ws(256)
+    kvq.kv_pages_copy(cache, torch.stack([far[0], near[0]], dim=1).contiguous(), wk)
+    kvq.kvq_check(wk)
+    assert torch.equal(cache.k16[:pages], low.k16[:pages]) and torch.equal(cache.v16[:pages], low.v16[:pages])
+
+
+@pytest.mark.parametrize("window,sink", [(2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31 - 1, 0), (1, 2 ** 31 - 1)])
+def test_largest_window_and_sinks_see_everything(window, sink):
+    require_gpu()
+    for news in ([1], [33]):
+        c = Case(4, 2, [700], news, "plain", 130)
+        run = c.decode if news == [1] else c.chunk
+        want = run()
+        c.mod = kvq.AttnMod(window=window, n_sink=sink)
+        got = run()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_document_starts_outside_the_sequence():
+    """Before its beginning: all of it; behind its end: nothing."""
+    require_gpu()
+    for news in ([1], [5]):
+        c = Case(4, 2, [90], news, "plain", 131)
+        run = c.decode if news == [1] else (lambda: c.chunk(extra=0))
+        want = run()
+        for start, same in ((-2 ** 31, True), (-1, True), (90, False), (2 ** 31 - 1, False)):
+            c.mod = kvq.AttnMod(doc_start=torch.full((news[0],), start, dtype=torch.int32, device="cuda"))
+            out, lse, _ = run()
+            if same:
+                assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+            else:
+                assert not bool(out.any()) and bool((lse == -math.inf).all())
+
+
+def test_more_new_tokens_than_announced():
+    """max_new bounds every sequence's rows: a longer run is flagged and left out, the others are attended."""
+    require_gpu()
+    c = Case(4, 2, [90, 200], [5, 80], "plain", 132)
+    want = c.chunk(extra=0)[0]
+    out = torch.full((85, 4, D), -7.0, dtype=torch.float16, device="cuda")
+    wk = ws(kvq.kv_chunk_attn_ws(c.cache, c.batch, 85, 80))
+    kvq.kv_chunk_attn(c.cache, c.batch, c.q, torch.tensor(c.starts).cuda(), 79, out, wk)
+    with pytest.raises(kvq.KvqError) as e:
+        kvq.kvq_check(wk)
+    assert e.value.code == _abi.KVQ_ERR_DEVICE_CHECK
+    assert torch.equal(out[:5], want[:5]) and bool((out[5:] == -7).all())
+
+
+def test_scores_of_minus_infinity():
+    """A visible key of -inf against a positive query: weight 0; nothing else visible: output 0."""
+    require_gpu()
+    c = Case(2, 2, [40], [1], "plain", 133)
+    c.q[:] = 1.0
+    for t in range(20, 40):
+        c.cache.k16[int(c.bt[0, t // 16]), :, t % 16] = -math.inf
+    out, lse, _ = c.decode()
+    c.lens, keep = [40], [(K.clone(), V) for K, V in c.KV]
+    K, V = R.as64(keep[0][0]), R.as64(keep[0][1])
+    for h in range(2):
+        o, z, bo, bz = R.attend(np.ones(D), K[:, h], V[:, h], np.arange(40) < 20, 39)
+        assert np.all(np.abs(R.as64(out[0, h]) - o) <= bo) and abs(float(lse[0, h]) - z) <= bz
+    c.mod = kvq.AttnMod(window=20)
+    out, lse, _ = c.decode()
+    assert not bool(out.any()) and bool((lse == -math.inf).all())
