@@ -736,14 +736,24 @@ __global__ void __launch_bounds__(CA_NT, 1)
 // Joins the splits of an item's rows, a warp per row, in their order, and leaves the workspace zeroed.
 constexpr int CJ_NW = 8;
 __global__ void __launch_bounds__(32 * CJ_NW) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
+    __shared__ int item[4];   // its sequence, first new token, the sequence's first row, rows of the item
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int GQ = a.GQ, tpc = CA_ROWS / GQ, h = blockIdx.y, r = blockIdx.z * CJ_NW + warp;
     kvq_pdl_begin();
-    int b, tok;
-    find_item(a, blockIdx.x, tpc, &b, &tok);
-    if (b < 0) return;
-    const int first = a.q_starts[b], n = a.q_starts[b + 1] - first;
-    if (r >= min(tpc, n - tok) * GQ) return;
+    if (warp == 0) {
+        int b, tok;
+        find_item(a, blockIdx.x, tpc, &b, &tok);
+        if (lane == 0) {
+            item[0] = b, item[1] = tok;
+            if (b >= 0) {
+                item[2] = a.q_starts[b];
+                item[3] = min(tpc, a.q_starts[b + 1] - item[2] - tok) * GQ;
+            }
+        }
+    }
+    __syncthreads();
+    if (item[0] < 0 || r >= item[3]) return;
+    const int tok = item[1], first = item[2];
     const int64_t p0 = ((int64_t)blockIdx.x * a.H + h) * a.n_splits * CA_ROWS + r;
     float mx = -INFINITY;
     for (int s = lane; s < a.n_splits; s += 32) mx = fmaxf(mx, a.ml[p0 + (int64_t)s * CA_ROWS].x);
@@ -754,8 +764,7 @@ __global__ void __launch_bounds__(32 * CJ_NW) chunk_join_kernel(const __grid_con
     for (int s = 0; s < a.n_splits; ++s) {
         const int64_t row = p0 + (int64_t)s * CA_ROWS;
         const float2 v = a.ml[row];
-        float4* part = reinterpret_cast<float4*>(a.part + row * D) + lane;
-        const float4 w = *part;
+        const float4 w = reinterpret_cast<const float4*>(a.part + row * D)[lane];
         const bool some = v.y != 0.0f;   // (a split without a visible token wrote no row)
         const float f = some ? exp2f(v.x - mx) : 0.0f;
         x.x += some ? f * w.x : 0.0f;
@@ -763,8 +772,10 @@ __global__ void __launch_bounds__(32 * CJ_NW) chunk_join_kernel(const __grid_con
         x.z += some ? f * w.z : 0.0f;
         x.w += some ? f * w.w : 0.0f;
         y += f * v.y;
-        *part = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
+    // (behind the loads: a store between them would hold up the next one)
+    for (int s = 0; s < a.n_splits; ++s)
+        reinterpret_cast<float4*>(a.part + (p0 + (int64_t)s * CA_ROWS) * D)[lane] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     __syncwarp();
     for (int s = lane; s < a.n_splits; s += 32) a.ml[p0 + (int64_t)s * CA_ROWS] = make_float2(0.0f, 0.0f);
     const float inv = y == 0.0f ? 0.0f : 1.0f / y;
@@ -789,12 +800,14 @@ struct ChunkPlan {
 };
 
 // Enough (item, kv head) CTAs fill the SMs by themselves; fewer are split along the cache, into the number
-// of parts whose waves take least: a CTA's beginning, end and share of the join cost about as much as 12 of
-// its tiles (five drafted tokens of eight 32K sequences: 64 CTAs in 2 parts, one wave, 173 us; in 7 parts,
-// three full waves, 182 us).
+// of parts whose waves take least: a CTA's beginning and end cost about as much as 12 of its tiles (five
+// drafted tokens of eight 32K sequences: 64 CTAs in 2 parts, one wave, 173 us; in 7 parts, three full waves,
+// 182 us), the join's launch as 3, and the parts' rows are written, read and zeroed, 0.036 tiles' time per CTA
+// of 256 rows (200 new tokens of 1000: 32 CTAs whole 19.9 us, in 2 parts 22.6 us; 500 of 8000: 91 us, in 2
+// parts 62 us).
 ChunkPlan chunk_plan(const kvq_layout* L, const kvq_seqs* S, int64_t n_rows, int32_t max_new) {
     ChunkPlan p;
-    const int tpc = CA_ROWS / (L->n_q_heads / L->n_kv_heads);
+    const int GQ = L->n_q_heads / L->n_kv_heads, tpc = CA_ROWS / GQ;
     const int64_t by_max = (int64_t)S->batch * ((max_new + tpc - 1) / tpc);
     p.items = std::max<int64_t>(1, std::min(by_max, n_rows / tpc + S->batch));
     const int64_t ctas = p.items * L->n_kv_heads, sms = kvq_num_sms();
@@ -802,10 +815,13 @@ ChunkPlan chunk_plan(const kvq_layout* L, const kvq_seqs* S, int64_t n_rows, int
     p.n_splits = 1;
     if (ctas < sms) {
         const int most = (int)std::min<int64_t>(std::max(1, tiles / 4), 4 * sms / ctas);
-        int64_t best = INT64_MAX;
+        const double full = std::min(1.0, (double)max_new * GQ / CA_ROWS);   // how much of a CTA's rows is used
+        double best = 0.0;
         for (int s = 1; s <= most; ++s) {
-            const int64_t waves = (ctas * s + sms - 1) / sms, cost = waves * ((tiles + s - 1) / s + 12);
-            if (cost < best) best = cost, p.n_splits = s;
+            const int64_t waves = (ctas * s + sms - 1) / sms;
+            double cost = (double)waves * ((tiles + s - 1) / s + 12);
+            if (s > 1) cost += 3.0 + 0.036 * full * (double)(ctas * s);
+            if (s == 1 || cost < best) best = cost, p.n_splits = s;
         }
     }
     const size_t rows = p.n_splits > 1 ? (size_t)ctas * p.n_splits * CA_ROWS : 0;

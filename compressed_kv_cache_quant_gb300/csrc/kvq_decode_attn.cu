@@ -139,18 +139,20 @@ __device__ __forceinline__ float peer(const float* p, int rank) {
     return v;
 }
 
-// Adds part r of a row (four dims per lane), weighted against the row's maximum, and zeroes it.
+// Adds part r of a row (four dims per lane), weighted against the row's maximum.  The part is zeroed behind
+// all loads (drop_part): a store between them would hold up the next one.
 __device__ __forceinline__ void join_part(const DecArgs& a, int64_t r, int lane, float mx, float4* x, float* y) {
     const float2 v = __ldcg(&a.ml[r]);
-    float4* part = reinterpret_cast<float4*>(a.part + r * D) + lane;
-    const float4 w = __ldcg(part);
+    const float4 w = __ldcg(reinterpret_cast<const float4*>(a.part + r * D) + lane);
     const float f = v.x == -INFINITY ? 0.0f : exp2f(v.x - mx);
     x->x += f * w.x;
     x->y += f * w.y;
     x->z += f * w.z;
     x->w += f * w.w;
     *y += f * v.y;
-    *part = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+}
+__device__ __forceinline__ void drop_part(const DecArgs& a, int64_t r, int lane) {
+    reinterpret_cast<float4*>(a.part + r * D)[lane] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 }
 __device__ __forceinline__ void finish_row(const DecArgs& a, int64_t r, int lane, float mx, float4 x, float y) {
     const float inv = y == 0.0f ? 0.0f : 1.0f / y;  // nothing visible: 0
@@ -392,6 +394,7 @@ __global__ void __launch_bounds__(32 * DA_NW) decode_attn_kernel(DecArgs a) {
         mx = kvq_warp_max(mx);
 #pragma unroll 8
         for (int s = turn; s < sp.used; s += per) join_part(a, first + (int64_t)s * GQ, lane, mx, &x, &y);
+        for (int s = turn; s < sp.used; s += per) drop_part(a, first + (int64_t)s * GQ, lane);
         float* dst = so + (turn * GQ + e) * SO_ROW;
         reinterpret_cast<float4*>(dst)[lane] = x;
         if (lane == 0) dst[D] = y;
@@ -427,6 +430,7 @@ __global__ void __launch_bounds__(32 * DA_JOIN) decode_join_kernel(DecArgs a) {
     float y = 0.0f;
 #pragma unroll 4
     for (int s = warp; s < sp.used; s += DA_JOIN) join_part(a, first + (int64_t)s * a.GQ, lane, mx, &x, &y);
+    for (int s = warp; s < sp.used; s += DA_JOIN) drop_part(a, first + (int64_t)s * a.GQ, lane);
     so[warp][lane] = x;
     if (lane == 0) sl[warp] = y;
     __syncthreads();  // also: every warp has read the maxima
