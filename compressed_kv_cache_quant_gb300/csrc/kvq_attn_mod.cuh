@@ -21,20 +21,22 @@ struct KvqModArgs {
 
 // Fills m from the caller's descriptor (NULL: the plain softmax of q.k/sqrt(d)).
 static inline int kvq_mod_args(const kvq_attn_mod* mod, const char* fn, KvqModArgs* m) {
-    const float dflt = 0.08838834764831845f;  // 1/sqrt(128)
-    *m = KvqModArgs{dflt * KVQ_LOG2E, 0.0f, dflt * KVQ_LOG2E, 0, 0, nullptr, nullptr, nullptr};
+    // constants are combined in fp64 and rounded once
+    const double dflt = 0.08838834764831844055, log2e = 1.44269504088896340736;  // 1/sqrt(128)
+    const float plain = (float)(dflt * log2e);
+    *m = KvqModArgs{plain, 0.0f, plain, 0, 0, nullptr, nullptr, nullptr};
     if (mod == nullptr) return KVQ_OK;
     KVQ_REQUIRE(std::isfinite(mod->scale) && mod->scale >= 0.0f, KVQ_ERR_INVALID_ARG, "%s: scale", fn);
     KVQ_REQUIRE(std::isfinite(mod->softcap) && mod->softcap >= 0.0f, KVQ_ERR_INVALID_ARG, "%s: softcap", fn);
     KVQ_REQUIRE(mod->window >= 0 && mod->n_sink >= 0, KVQ_ERR_INVALID_ARG, "%s: window / n_sink", fn);
-    const float scale = mod->scale > 0.0f ? mod->scale : dflt;
-    m->lin = scale * KVQ_LOG2E;
+    const double scale = mod->scale > 0.0f ? (double)mod->scale : dflt;
+    m->lin = (float)(scale * log2e);
     if (mod->softcap > 0.0f) {
-        m->pre = scale / mod->softcap;
-        m->post = mod->softcap * KVQ_LOG2E;
+        m->pre = (float)(scale / mod->softcap);
+        m->post = (float)(mod->softcap * log2e);
         KVQ_REQUIRE(std::isfinite(m->pre) && std::isfinite(m->post), KVQ_ERR_INVALID_ARG, "%s: scale / softcap", fn);
     } else {
-        m->pre = scale * KVQ_LOG2E;
+        m->pre = m->lin;
     }
     m->window = mod->window;
     m->n_sink = mod->n_sink;
