@@ -44,6 +44,7 @@ constexpr int CA_HALF = CA_TILE / 2;     // a Q tile is two halves of 128 rows x
 constexpr int CA_SMEM = 2 * CA_TILE + CA_NS * CA_TILE + 1024;
 constexpr uint32_t CA_SPIN = 1u << 16;   // bound on the polls of one mbarrier wait
 constexpr float CA_SLACK = 14.0f;        // log2 growth of a row's maximum before O is rescaled
+constexpr float CA_FAR = 1048576.0f;     // scores (log2) beyond which they are rounded before the maximum is taken off
 
 // TMEM columns: S (and P over it) of the two tiles, then their O
 constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
@@ -524,7 +525,8 @@ __global__ void __launch_bounds__(CA_NT, 1)
         minhi = __reduce_min_sync(0xffffffffu, minhi);
         const int pos = T - n + tok0 + tok;
         const float slope2 = BIAS && valid ? a.mod.slopes[h * GQ + r % GQ] * KVQ_LOG2E : 0.0f;
-        float m = -INFINITY, l = 0.0f;
+        float m = valid ? -INFINITY : INFINITY, l = 0.0f;   // (no row: weights 0, never a new maximum)
+        bool far = false;   // some row of the warp has its maximum beyond CA_FAR
         if (i < nq) {
             for (int j = 0; j < nt; ++j) {
                 const int t0 = tile_of(it0 + j) * CA_KEYS;
@@ -649,12 +651,29 @@ __global__ void __launch_bounds__(CA_NT, 1)
                     __syncwarp();
                     if (lane == 0) bar_arrive(&S.p_full[i][c / 64]);
                 };
+                // A weight's exponent s * scale - m is rounded once, behind the difference.  That is exact enough
+                // until an fp32 step of m is no longer far below 1: then the product is rounded like m itself, or a
+                // row's largest weight would be 2^(m's rounding error), 0 or infinite.  At most three turns: one for
+                // `far`, one that moves m; behind that the largest exponent is at most half a step of m.
                 for (;;) {
+                    if (!CAP && !BIAS && far && scale != 1.0f) {   // (a cap or a bias left rounded scores, scale 1)
+                        const uint64_t by = pair(scale, scale);
+#pragma unroll
+                        for (int c = 0; c < 128; c += 2) unpair(mul2(pair(s[c], s[c + 1]), by), &s[c], &s[c + 1]);
+                        scale = 1.0f;
+                        mx4[0] = mx4[1] = mx4[2] = mx4[3] = -INFINITY;
+                    }
                     sum2[0] = sum2[1] = 0;
                     weights(0, true);
-                    const float mx = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]) * scale;
-                    const bool grew = mx > m + CA_SLACK || (m == -INFINITY && mx > m);
+                    const float top = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]);
+                    // the exponent of the row's largest weight, rounded as the weights' are
+                    const bool grew = fmaf(top, scale, -m) > CA_SLACK || (m == -INFINITY && top > m);
                     if (!__any_sync(0xffffffffu, grew)) break;
+                    const float mx = top * scale;
+                    if (!CAP && !BIAS && scale != 1.0f && __any_sync(0xffffffffu, grew && fabsf(mx) > CA_FAR)) {
+                        far = true;
+                        continue;
+                    }
                     const float f = grew ? ex2(m - mx) : 1.0f;
                     if (grew) m = mx;
                     l *= f;

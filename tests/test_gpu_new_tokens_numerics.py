@@ -1,0 +1,99 @@
+"""GPU tests of the new tokens' attention where its arithmetic is tight: weights far below a dominant token's,
+scores beyond 2^24, NaN in a query or a key, and rows that no query sees."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import new_token_ref as R
+from compressed_kv_cache_quant_gb300 import kvq
+from gpu_helpers import require_gpu, ws
+from test_gpu_new_tokens import Case
+
+pytestmark = pytest.mark.gpu
+D = 128
+
+
+def store(c, K, V):
+    """Puts K, V [T][H_kv][d] (fp16) into sequence 0 .. of Case c, the same rows for every sequence (cut to its length)."""
+    for b, T in enumerate(c.lens):
+        c.KV[b] = (K[:T].clone(), V[:T].clone())
+        if T:
+            kvq.kv_quant_pack(c.cache, c.batch, b, 0, T, c.KV[b][0].cuda(), c.KV[b][1].cuda())
+
+
+def dominated(c, every, low):
+    """Scores of 8 at every `every`-th token, whose V is 0, and of 8 - low at the others, whose V is of one sign: the
+    output is what the small weights add up to.  Products and sums of the scores are exact."""
+    T, H = max(c.lens), c.hkv
+    K = torch.zeros((T, H, D), dtype=torch.float16)
+    K[..., 0] = 8.0 - low
+    K[::every, :, 0] = 8.0
+    V = torch.from_numpy(np.random.default_rng(5).uniform(500.0, 1000.0, (T, H, D))).half()
+    V[::every] = 0
+    store(c, K, V)
+    c.q[..., 0] = 1.0
+    c.spec["scale"] = 1.0
+    c.mod = kvq.AttnMod(scale=1.0, softcap=c.spec.get("softcap", 0.0))
+
+
+def check_dominated(c, out, lse, rows, half, floor, fp16):
+    """A weight is kept to `half` of itself or, in units of the row's largest, to `floor` (2^-25, half the smallest fp16 step,
+    over the scale of the weights); the rest of the bound is the 64-bit form's for the scores and sums."""
+    row = 0
+    for b, (T, n) in enumerate(zip(c.lens, c.news)):
+        K, V = R.as64(c.KV[b][0]), R.as64(c.KV[b][1])
+        for i in range(n):
+            if row in rows:
+                pos = T - n + i
+                for h in range(c.hq):
+                    k, v = K[:pos + 1, h // (c.hq // c.hkv)], V[:pos + 1, h // (c.hq // c.hkv)]
+                    o, z, bo, bz = R.attend(R.as64(c.q[row, h]), k, v, np.ones(pos + 1, bool), pos, 1.0, c.spec.get("softcap", 0.0))
+                    top = 8.0 if "softcap" not in c.spec else c.spec["softcap"] * math.tanh(8.0 / c.spec["softcap"])
+                    bo = bo + half * o + floor * v.sum(0) / math.exp(z - top)
+                    if fp16:
+                        bo = bo + 2.0 ** -11 * (o + bo) + 2.0 ** -25
+                    assert np.all(np.abs(R.as64(out[row, h]) - o) <= bo), (b, i, h, R.as64(out[row, h])[:2], o[:2], bo[:2])
+                    assert abs(float(lse[row, h]) - z) <= bz
+            row += 1
+
+
+@pytest.mark.parametrize("sign", ["both", "negative"])
+@pytest.mark.parametrize("hq,hkv,lens,news", [(8, 2, [700], [1]), (8, 2, [700, 333], [70, 333]), (2, 2, [5000], [3])])
+def test_scores_beyond_fp32_whole_numbers(hq, hkv, lens, news, sign):
+    """Finite keys and queries whose scores lie far beyond 2^24, where neighbouring fp32 values are more than a step of the
+    exponent apart: the largest score takes all the weight."""
+    require_gpu()
+    c = Case(hq, hkv, lens, news, "plain", 142, poison=False)
+    T = max(lens)
+    if sign == "both":
+        K = c_rnd((T, hkv, D), 1) * 20000
+        c.q.copy_((c_rnd(c.q.shape, 2) * 20000).clamp(-60000, 60000))
+    else:
+        K = (c_rnd((T, hkv, D), 1) * 0.3 + 1) * 20000
+        c.q.fill_(-20000.0)
+    K = K.clamp(-60000, 60000).half()
+    store(c, K, c_rnd((T, hkv, D), 3).half())
+    runs = [(c.chunk(extra=0), True)] + ([(c.decode(), False)] if news == [1] else [])
+    row = 0
+    for b, (T, n) in enumerate(zip(lens, news)):
+        K, V = R.as64(c.KV[b][0]), R.as64(c.KV[b][1])
+        for i in range(n):
+            for h in range(hq):
+                q, g = R.as64(c.q[row, h]), h // (hq // hkv)
+                k = K[:T - n + i + 1, g]
+                s = k @ q / math.sqrt(D)
+                eps = 130 * 2 * R.U / math.sqrt(D) * np.max(np.abs(k) @ np.abs(q))
+                at = int(np.argmax(s))
+                others = np.delete(s, at)
+                if len(others) and s[at] - others.max() < 4 * eps:
+                    continue   # too close to tell
+                for (out, lse, _), half in runs:
+                    assert bool((R.as64(out[row, h]) == V[at, g]).all()), (b, i, h)
+                    assert abs(float(lse[row, h]) - s[at]) <= 2 * eps
+            row += 1
+
+
+def c_rnd(shape, seed):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed))
