@@ -14,10 +14,17 @@
 //   warps 4-7  softmax of tile 1
 //
 // While one tile's softmax runs, the tensor cores work for the other one.  O stays in TMEM over the whole
-// loop; a row is rescaled only when its maximum grew by more than 2^14 since the last time (P is at most
-// 16384 then, inside fp16's range with its relative precision, and the kept maximum cancels at the end).  A
-// rescale holds up its tile for about 900 cycles: with 2^8, 2048 tokens under a 4096-token window took 132
-// us, with 2^12 125 us.
+// loop.  A row's weights are taken against an anchor, which cancels at the end: 2^7 below the row's maximum when
+// it is set, and set anew (O rescaled) when a weight would pass 2^15.99.  A rescale holds up its tile for about 900
+// cycles, so one row's turn is the turn of every row of its warp whose maximum has grown: 2048 tokens under a
+// 4096-token window take 119 us, with anchors that move one by one 138 us, without the room below (an anchor at
+// the maximum, moved for a growth beyond 2^14) 123 us.
+//
+// P is one fp16 rounding of a weight, since the tensor cores take P and V in one type: off by 2^-11 of itself, or
+// by 2^-25 where it is subnormal.  Against a largest weight of 2^7 or more that is 2^-32, so what many small weights
+// add up to beside a dominant token is kept: 131072 of them lose under 2^-15 of the whole.  The rounding shows beside
+// the fp16 output's own: 2.5e-4 to 2.9e-4 of the output (normwise) where the output's rounding alone is 2.1e-4.  A
+// second half of P would bring that down for half as many products again.
 //
 // Measured (32 q / 8 kv heads): a causal prompt of 16384 tokens 1.36 ms, 1.62 PFLOP/s of the needed products,
 // in a short run, 1.45 ms under the power limit of a long one; five drafted tokens of eight 32K sequences
@@ -43,8 +50,9 @@ constexpr int CA_TILE = 128 * D * 2;     // bytes of a Q, K or V tile
 constexpr int CA_HALF = CA_TILE / 2;     // a Q tile is two halves of 128 rows x 128 bytes
 constexpr int CA_SMEM = 2 * CA_TILE + CA_NS * CA_TILE + 1024;
 constexpr uint32_t CA_SPIN = 1u << 16;   // bound on the polls of one mbarrier wait
-constexpr float CA_SLACK = 14.0f;        // log2 growth of a row's maximum before O is rescaled
-constexpr float CA_FAR = 1048576.0f;     // scores (log2) beyond which they are rounded before the maximum is taken off
+constexpr float CA_HEAD = 7.0f;          // log2 of a row's largest weight when its anchor is set
+constexpr float CA_TOP = 15.99f;         // log2 of the largest weight before the anchor is set anew (fp16 ends at 2^16)
+constexpr float CA_FAR = 1048576.0f;     // scores (log2) beyond which they are rounded before the anchor is taken off
 
 // TMEM columns: S (and P over it) of the two tiles, then their O
 constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
@@ -59,7 +67,7 @@ struct ChunkArgs {
     uint16_t* out;
     float* lse;
     float* part;   // [item][split][CA_ROWS][D]
-    float2* ml;    // [item][split][CA_ROWS] maximum (log2) and sum
+    float2* ml;    // [item][split][CA_ROWS] anchor (log2) and sum
     KvqWsHeader* hdr;
 };
 
@@ -525,7 +533,7 @@ __global__ void __launch_bounds__(CA_NT, 1)
         minhi = __reduce_min_sync(0xffffffffu, minhi);
         const int pos = T - n + tok0 + tok;
         const float slope2 = BIAS && valid ? a.mod.slopes[h * GQ + r % GQ] * KVQ_LOG2E : 0.0f;
-        float m = valid ? -INFINITY : INFINITY, l = 0.0f;   // (no row: weights 0, never a new maximum)
+        float m = valid ? -INFINITY : INFINITY, l = 0.0f;   // (no row: weights 0, never a new anchor)
         bool far = false;   // some row of the warp has its maximum beyond CA_FAR
         if (i < nq) {
             for (int j = 0; j < nt; ++j) {
@@ -611,8 +619,8 @@ __global__ void __launch_bounds__(CA_NT, 1)
                             if (!(bits >> c & 1)) s[32 * w + c] = -INFINITY;
                     }
                 }
-                // The first half's weights are taken with the maximum so far, while the new one is still being
-                // found; only when a row's grew by more than the slack are they taken again.
+                // The first half's weights are taken with the anchor so far, while the tile's maximum is still being
+                // found; only when that is too far above a row's anchor are they taken again.
                 uint32_t p[32];
                 uint64_t sum2[2];
                 float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -654,7 +662,7 @@ __global__ void __launch_bounds__(CA_NT, 1)
                 // A weight's exponent s * scale - m is rounded once, behind the difference.  That is exact enough
                 // until an fp32 step of m is no longer far below 1: then the product is rounded like m itself, or a
                 // row's largest weight would be 2^(m's rounding error), 0 or infinite.  At most three turns: one for
-                // `far`, one that moves m; behind that the largest exponent is at most half a step of m.
+                // `far`, one that moves m; behind that the largest exponent is CA_HEAD and at most half a step of m.
                 for (;;) {
                     if (!CAP && !BIAS && far && scale != 1.0f) {   // (a cap or a bias left rounded scores, scale 1)
                         const uint64_t by = pair(scale, scale);
@@ -667,15 +675,18 @@ __global__ void __launch_bounds__(CA_NT, 1)
                     weights(0, true);
                     const float top = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]);
                     // the exponent of the row's largest weight, rounded as the weights' are
-                    const bool grew = fmaf(top, scale, -m) > CA_SLACK || (m == -INFINITY && top > m);
-                    if (!__any_sync(0xffffffffu, grew)) break;
+                    const float most = fmaf(top, scale, -m);
+                    if (!__any_sync(0xffffffffu, most > CA_TOP || (m == -INFINITY && top > m))) break;
+                    // one row's turn is every row's: an anchor that would have to follow later is set now
+                    const bool grew = most > CA_HEAD;
                     const float mx = top * scale;
                     if (!CAP && !BIAS && scale != 1.0f && __any_sync(0xffffffffu, grew && fabsf(mx) > CA_FAR)) {
                         far = true;
                         continue;
                     }
-                    const float f = grew ? ex2(m - mx) : 1.0f;
-                    if (grew) m = mx;
+                    const float anchor = mx - CA_HEAD;
+                    const float f = grew ? ex2(m - anchor) : 1.0f;
+                    if (grew) m = anchor;
                     l *= f;
                     if (j > 0) {
 #pragma unroll

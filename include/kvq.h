@@ -746,11 +746,13 @@ size_t kv_decode_attn_ws(const kvq_layout* layout, const kvq_seqs* seqs);
  * q: device fp16 [n_rows][H_q][d]; out: device fp16 [n_rows][H_q][d]; lse
  * (optional): device fp32 [n_rows][H_q].  Rows behind q_starts[batch] are left as
  * they were.  Exact fp16 products and fp32 sums; the softmax weights enter the
- * value product in fp16.  Results do not depend on the run.  Pages without a
- * token that some query of the call sees are not read, and their block table
- * entries may be stale.  In the pages that are read, the sequence's own rows must
- * be finite (a query's weight 0 times an infinite V row of its tile is NaN); rows
- * at and behind seq_lens[b] may hold anything.  num_blocks * H_kv * 16 < 2^31.
+ * value product in fp16, off by 2^-11 of themselves or by 2^-32 of the largest
+ * weight of the row (of one part, where the cache is split).  Results do not
+ * depend on the run.  Pages without a token that some query of the call sees are
+ * not read, and their block table entries may be stale.  In the pages that are
+ * read, the sequence's own rows must be finite (a query's weight 0 times an
+ * infinite V row of its tile is NaN); rows at and behind seq_lens[b] may hold
+ * anything.  num_blocks * H_kv * 16 < 2^31.
  * q, out, k16, v16 16-byte aligned.
  * ws: kv_chunk_attn_ws(layout, seqs, n_rows, max_new) bytes.
  * ---------------------------------------------------------------------- */

@@ -59,6 +59,20 @@ def check_dominated(c, out, lse, rows, half, floor, fp16):
             row += 1
 
 
+@pytest.mark.parametrize("mod", ["plain", "cap"])
+@pytest.mark.parametrize("every,low", [(64, 16.25), (64, 17.0), (100000, 17.0), (100000, 17.5)])
+@pytest.mark.parametrize("hq,hkv,lens,news", [(8, 2, [4096], [300]), (2, 2, [6011, 900], [5, 130]), (8, 1, [1500], [1500])])
+def test_chunk_weights_far_below_the_largest(hq, hkv, lens, news, every, low, mod):
+    """One fp16 rounding of a weight: 2^-11 of itself, and 2^-25 where the largest is 2^7."""
+    require_gpu()
+    c = Case(hq, hkv, lens, news, mod, 140, poison=False)
+    dominated(c, every, low)
+    out, lse, _ = c.chunk(extra=0)
+    total = sum(news)
+    rows = set(np.random.default_rng(6).integers(0, total, 10).tolist()) | {0, total - 1}
+    check_dominated(c, out, lse, rows, 2.0 ** -11, 2.0 ** -32, True)
+
+
 @pytest.mark.parametrize("sign", ["both", "negative"])
 @pytest.mark.parametrize("hq,hkv,lens,news", [(8, 2, [700], [1]), (8, 2, [700, 333], [70, 333]), (2, 2, [5000], [3])])
 def test_scores_beyond_fp32_whole_numbers(hq, hkv, lens, news, sign):
