@@ -560,13 +560,20 @@ __global__ void __launch_bounds__(CA_NT, 1)
                 tm_ld128(ts, reinterpret_cast<uint32_t*>(s));
                 float scale = a.mod.pre;
                 if (CAP) {
+                    // the choice below is the warp's: neither rows behind T nor queries that are not the sequence's
+                    // have a part in it, or what they hold would change the others' last bits
+                    if (tail) {
+#pragma unroll
+                        for (int c = 0; c < 128; ++c)
+                            if (t0 + c >= T) s[c] = 0.0f;
+                    }
                     float big[2] = {0.0f, 0.0f};
 #pragma unroll
                     for (int c = 0; c < 128; c += 4) {
                         big[0] = max3(big[0], fabsf(s[c]), fabsf(s[c + 1]));
                         big[1] = max3(big[1], fabsf(s[c + 2]), fabsf(s[c + 3]));
                     }
-                    if (__all_sync(0xffffffffu, fmaxf(big[0], big[1]) * a.mod.pre <= 0.75f)) {
+                    if (__all_sync(0xffffffffu, !valid || fmaxf(big[0], big[1]) * a.mod.pre <= 0.75f)) {
                         // the usual case: tanh x = x P(x^2) on |x| <= 3/4, P the polynomial through the Chebyshev
                         // points, 6e-7 relative; 3.5 instructions per score (below they are 2 special-function
                         // results on top of the weight's one: packed documents 87 us instead of 73)

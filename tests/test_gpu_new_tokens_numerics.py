@@ -111,3 +111,26 @@ def test_scores_beyond_fp32_whole_numbers(hq, hkv, lens, news, sign):
 
 def c_rnd(shape, seed):
     return torch.randn(shape, generator=torch.Generator().manual_seed(seed))
+
+
+@pytest.mark.parametrize("mod", ["cap", "cap_bias_scale"])
+def test_rows_that_no_query_sees_leave_no_trace(mod):
+    """Queries behind the last sequence and keys behind a sequence's last token may hold anything: not one bit of what the
+    others give depends on them."""
+    require_gpu()
+    got = []
+    for fill in (0.0, 60000.0):
+        c = Case(8, 2, [777, 390], [9, 3], mod, 144, poison=False)
+        for b, T in enumerate(c.lens):
+            page = int(c.bt[b, T // 16])
+            c.cache.k16[page, :, T % 16:] = fill
+            c.cache.v16[page, :, T % 16:] = fill
+        q = torch.cat([c.q, torch.full((30, 8, D), fill, dtype=torch.float16, device="cuda")])
+        out = torch.zeros((42, 8, D), dtype=torch.float16, device="cuda")
+        lse = torch.zeros((42, 8), device="cuda")
+        wk = ws(kvq.kv_chunk_attn_ws(c.cache, c.batch, 42, 9))
+        kvq.kv_chunk_attn(c.cache, c.batch, q, torch.tensor(c.starts).cuda(), 9, out, wk, mod=c.mod, lse=lse)
+        kvq.kvq_check(wk)
+        c.check(out, lse, True)
+        got.append((out, lse))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
