@@ -9,7 +9,9 @@
 //                 t+8, t+12 of token g (and g + 8) and the query's fragments use the same order.
 //   O^T = V^T p   A = 16 dims x 16 tokens.  Lane (g, t) loads chunks g and g + 8 of tokens 2t, 2t+1, 2t+8,
 //                 2t+9; a byte permute pairs neighbouring tokens, and row g of product j is dim 8g + j.
-//                 p enters as two fp16 halves (22 bits), against exact fp16 V; sums are fp32.
+//                 p enters as two fp16 halves, against exact fp16 V; sums are fp32.  The halves are taken of
+//                 2^15 p, so that both use fp16's whole range: p is off by 2^-22 of itself down to 2^-18 of the
+//                 warp's largest weight, and by 2^-40 of that below.
 // p^T reaches the B operand through movmatrix.  A warp owns whole pages (8 KB of loads in flight per warp,
 // K of the next page issued as soon as the current one is consumed), keeps its own running maximum and
 // sum, and meets the others once, at the end.
@@ -37,6 +39,7 @@ constexpr int DA_WIDE = 12, DA_SLIM = 4;
 // instead of 10.5 us; 8192: 13.1 instead of 11.5), and where they do not (4 x 4000 tokens, 8 kv heads: 14.0
 // instead of 15.8 us)
 constexpr int DA_FEW_PAGES = 4, DA_MOST_PAGES = 12;
+constexpr float DA_LIFT = 32768.0f;   // the scale of the weights in the value product: the largest is 2^15
 constexpr int DA_JOIN = 4;      // warps per CTA of the second launch
 constexpr int DA_TICKETS = 56;  // rows whose arrivals fit the workspace header's spare words
 constexpr int SO_ROW = D + 4;   // floats of a head's row in shared memory
@@ -271,8 +274,8 @@ __global__ void __launch_bounds__(32 * DA_NW) decode_attn_kernel(DecArgs a) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const float ms = m[e] == -INFINITY ? 0.0f : m[e];   // (nothing but scores of -inf so far: weights 0)
-            p[e] = in0 ? exp2f(s[e] - ms) : 0.0f;
-            p[2 + e] = in1 ? exp2f(s[2 + e] - ms) : 0.0f;
+            p[e] = in0 ? exp2f(s[e] - ms) * DA_LIFT : 0.0f;
+            p[2 + e] = in1 ? exp2f(s[2 + e] - ms) * DA_LIFT : 0.0f;
             l[e] += p[e] + p[2 + e];
         }
         const uint32_t h0 = half2_bits(p[0], p[1]), h1 = half2_bits(p[2], p[3]);
@@ -298,9 +301,14 @@ __global__ void __launch_bounds__(32 * DA_NW) decode_attn_kernel(DecArgs a) {
         if (more) load_v(P, a.v16 + row, g, t);
     }
 
-    // the warps' states into shared memory
+    // the warps' states into shared memory, their scale taken off (a power of two: exact)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][e] *= 1.0f / DA_LIFT;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
+        l[e] *= 1.0f / DA_LIFT;
         l[e] += __shfl_xor_sync(0xffffffffu, l[e], 4);
         l[e] += __shfl_xor_sync(0xffffffffu, l[e], 8);
         l[e] += __shfl_xor_sync(0xffffffffu, l[e], 16);

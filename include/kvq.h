@@ -725,8 +725,9 @@ typedef struct kvq_attn_mod {
  * q: device fp16 [batch][H_q][d]; out: device fp32 [batch][H_q][d]; lse
  * (optional): device fp32 [batch][H_q], the natural log of the softmax
  * denominator.  An empty sequence gives 0 and -inf.  Exact fp16 products, fp32
- * sums, the weights as two fp16 halves (22 bits).  Results do not depend on the
- * run (parts are joined in their order).  Pages that hold no visible token are
+ * sums, the weights as two fp16 halves: off by 2^-22 of themselves or by 2^-40 of
+ * the largest weight that their warp meets.  Results do not depend on the run
+ * (parts are joined in their order).  Pages that hold no visible token are
  * not read and their block table entries may be stale; rows that are not visible
  * may hold anything, NaN included.  q, out, k16, v16 16-byte aligned.
  * ws: kv_decode_attn_ws(layout, seqs) bytes.

@@ -134,3 +134,16 @@ def test_rows_that_no_query_sees_leave_no_trace(mod):
         c.check(out, lse, True)
         got.append((out, lse))
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("mod", ["plain", "cap"])
+@pytest.mark.parametrize("every,low", [(16, 8.0), (16, 16.25), (16, 17.0), (64, 17.5), (100000, 17.0)])
+@pytest.mark.parametrize("hq,hkv,lens", [(8, 2, [2049]), (8, 2, [20011]), (16, 16, [3001, 700, 17] * 8)])
+def test_decode_weights_far_below_the_largest(hq, hkv, lens, every, low, mod):
+    """Two fp16 halves of a weight: 2^-22 of itself (each half rounds by 2^-11 of what it takes), and 2^-25 where the largest
+    of its warp is 2^15."""
+    require_gpu()
+    c = Case(hq, hkv, lens, [1] * len(lens), mod, 141, poison=False)
+    dominated(c, every, low)
+    out, lse, _ = c.decode()
+    check_dominated(c, out, lse, range(3), 2.0 ** -22, 2.0 ** -40, False)
