@@ -374,8 +374,9 @@ __global__ void __launch_bounds__(32 * DA_NW) decode_attn_kernel(DecArgs a) {
             }
 #pragma unroll
             for (int s = 0; s < 8; ++s) {
-                if (s >= n_parts || pm[s] == -INFINITY) continue;
-                const float f = exp2f(pm[s] - mx);
+                if (s >= n_parts) continue;
+                // (a part without a maximum holds zeros, or NaN where all that it sees is NaN: that has to show)
+                const float f = pm[s] == -INFINITY ? 0.0f : exp2f(pm[s] - mx);
                 x += f * px[s];
                 y += f * pl[s];
             }

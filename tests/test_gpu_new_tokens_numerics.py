@@ -147,3 +147,24 @@ def test_decode_weights_far_below_the_largest(hq, hkv, lens, every, low, mod):
     dominated(c, every, low)
     out, lse, _ = c.decode()
     check_dominated(c, out, lse, range(3), 2.0 ** -22, 2.0 ** -40, False)
+
+
+@pytest.mark.parametrize("hq,hkv,lens", [(8, 2, [40, 700]), (8, 2, [20011]), (16, 16, [3001, 700, 17] * 8)])
+@pytest.mark.parametrize("where", ["query", "key"])
+def test_nan_in_what_a_query_sees(hq, hkv, lens, where):
+    """A NaN in a query, or in every key that it sees, gives NaN in its rows and in no other's."""
+    require_gpu()
+    c = Case(hq, hkv, lens, [1] * len(lens), "plain", 143, poison=False)
+    clean = [c.decode()[:2], c.chunk(extra=0)[:2]]
+    GQ, last = hq // hkv, len(lens) - 1
+    hit = torch.zeros((len(lens), hq), dtype=torch.bool, device="cuda")
+    if where == "query":
+        c.q[last, 1, 5] = math.nan
+        hit[last, 1] = True
+    else:
+        for t in range(lens[last]):
+            c.cache.k16[int(c.bt[last, t // 16]), 1, t % 16, 3] = math.nan
+        hit[last, GQ:2 * GQ] = True
+    for (out, lse), (want, wlse) in zip([c.decode()[:2], c.chunk(extra=0)[:2]], clean):
+        assert bool(out[hit].isnan().all()) and bool(lse[hit].isnan().all())
+        assert torch.equal(out[~hit], want[~hit]) and torch.equal(lse[~hit], wlse[~hit])
