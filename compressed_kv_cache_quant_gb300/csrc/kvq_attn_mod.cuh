@@ -31,6 +31,7 @@ static inline int kvq_mod_args(const kvq_attn_mod* mod, const char* fn, KvqModAr
     KVQ_REQUIRE(mod->window >= 0 && mod->n_sink >= 0, KVQ_ERR_INVALID_ARG, "%s: window / n_sink", fn);
     const double scale = mod->scale > 0.0f ? (double)mod->scale : dflt;
     m->lin = (float)(scale * log2e);
+    KVQ_REQUIRE(std::isfinite(m->lin), KVQ_ERR_INVALID_ARG, "%s: scale", fn);
     if (mod->softcap > 0.0f) {
         m->pre = (float)(scale / mod->softcap);
         m->post = (float)(mod->softcap * log2e);

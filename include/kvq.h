@@ -697,7 +697,7 @@ int kv_qk_norm_rope(const kvq_layout* layout, const kvq_rope* rope, const uint64
  * Score forms of kv_decode_attn and kv_chunk_attn (host struct, read during the
  * call; NULL or all zero: softmax of q.k/sqrt(d) over the causal tokens).
  * For the query at position i and the cached token j:
- *   s = scale * q.k                       (scale 0: 1/sqrt(d))
+ *   s = scale * q.k                       (scale 0: 1/sqrt(d); at most 2.3e38)
  *   s = softcap * tanh(s / softcap)       (softcap > 0)
  *   s = s - slopes[h] * |i - j|           (slopes: device fp32 [H_q])
  * j is visible when doc <= j < hi and, with window > 0, also (j > i - window or
