@@ -884,10 +884,18 @@ int make_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
         encode = reinterpret_cast<Encode>(f);
     }
     const cuuint32_t ones[4] = {1, 1, 1, 1};
-    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, const_cast<void*>(base),
-                              reinterpret_cast<const cuuint64_t*>(dims), reinterpret_cast<const cuuint64_t*>(strides),
-                              box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const auto fill = [&] {
+        return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, const_cast<void*>(base),
+                      reinterpret_cast<const cuuint64_t*>(dims), reinterpret_cast<const cuuint64_t*>(strides), box, ones,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = fill();
+    if (r == CUDA_ERROR_INVALID_CONTEXT) {
+        // the thread has made no runtime call yet that makes its device's context current, as a launch would
+        int dev = 0;
+        if (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = fill();
+    }
     if (r != CUDA_SUCCESS) return kvq_fail(KVQ_ERR_CUDA, "%s: tensor map (%d)", fn, (int)r);
     return KVQ_OK;
 }

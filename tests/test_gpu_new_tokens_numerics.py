@@ -1,6 +1,9 @@
 """GPU tests of the new tokens' attention where its arithmetic is tight: weights far below a dominant token's,
 scores beyond 2^24, NaN in a query or a key, and rows that no query sees."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -168,3 +171,39 @@ def test_nan_in_what_a_query_sees(hq, hkv, lens, where):
     for (out, lse), (want, wlse) in zip([c.decode()[:2], c.chunk(extra=0)[:2]], clean):
         assert bool(out[hit].isnan().all()) and bool(lse[hit].isnan().all())
         assert torch.equal(out[~hit], want[~hit]) and torch.equal(lse[~hit], wlse[~hit])
+
+
+def test_first_calls_from_many_threads():
+    """Threads whose first CUDA call is the library's, and whose calls come together, each on a stream and a workspace of its
+    own, give what one thread gives."""
+    require_gpu()
+    prog = '''
+import threading, torch
+import new_token_ref
+from compressed_kv_cache_quant_gb300 import kvq
+from gpu_helpers import ws
+from test_gpu_new_tokens import Case, D
+c = Case(8, 2, [300, 90], [20, 7], "cap", 145)
+starts = torch.tensor(c.starts).cuda()
+need = kvq.kv_chunk_attn_ws(c.cache, c.batch, 27, 20)
+own = [(torch.cuda.Stream(), ws(need), torch.empty((27, 8, D), dtype=torch.float16, device="cuda")) for _ in range(8)]
+torch.cuda.synchronize()
+ready, errors = threading.Barrier(8), []
+def call(s, w, o):
+    try:
+        ready.wait()
+        kvq.kv_chunk_attn(c.cache, c.batch, c.q, starts, 20, o, w, mod=c.mod, stream=s)
+    except Exception as e:
+        errors.append(e)
+threads = [threading.Thread(target=call, args=x) for x in own]
+for t in threads: t.start()
+for t in threads: t.join()
+torch.cuda.synchronize()
+want = c.chunk(extra=0)[0]
+assert not errors and all(torch.equal(o, want) for _, _, o in own), errors
+print("as one")
+'''
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([here, os.path.dirname(here)]))
+    got = subprocess.run([sys.executable, "-c", prog], env=env, capture_output=True, text=True, timeout=300)
+    assert got.returncode == 0 and "as one" in got.stdout, got.stdout + got.stderr
