@@ -35,6 +35,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "kvq_attn_mod.cuh"
 
@@ -872,7 +873,8 @@ ChunkPlan chunk_plan(const kvq_layout* L, const kvq_seqs* S, int64_t n_rows, int
 int make_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
              const char* fn) {
     using Encode = decltype(&cuTensorMapEncodeTiled);
-    static Encode encode = nullptr;
+    static std::atomic<Encode> found_encode{nullptr};   // (threads that make the first call together each look it up)
+    Encode encode = found_encode.load(std::memory_order_relaxed);
     if (encode == nullptr) {
         void* f = nullptr;
         cudaDriverEntryPointQueryResult found;
@@ -882,6 +884,7 @@ int make_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
             return kvq_fail(KVQ_ERR_CUDA, "%s: the driver has no cuTensorMapEncodeTiled", fn);
         }
         encode = reinterpret_cast<Encode>(f);
+        found_encode.store(encode, std::memory_order_relaxed);
     }
     const cuuint32_t ones[4] = {1, 1, 1, 1};
     const auto fill = [&] {
