@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(CA_NT, 1)
                             unpair(mul2(x, fma2(fma2(fma2(fma2(c4, u, c3), u, c2), u, c1), u, c0)), &s[c], &s[c + 1]);
                         }
                     } else {
-                        // tanh x = 1 - 2 / (1 + e^2x), 1e-7 absolute
+                        // tanh x = 1 - 2 / (1 + e^2x), 5e-7 absolute: ex2's and rcp's 2^-22, and three fp32 roundings
                         const float k2 = a.mod.pre * (2.0f * KVQ_LOG2E), p2 = -2.0f * a.mod.post;
 #pragma unroll
                         for (int c = 0; c < 128; ++c) s[c] = fmaf(p2, rcp(1.0f + ex2(s[c] * k2)), a.mod.post);

@@ -3,9 +3,11 @@
 //
 // Positions.  A pair that turns f radians per position is at angle p * f.  At long positions an fp32
 // product loses it (p * f near 1e5 rad has 8e-3 rad steps) and fp64 arithmetic is slow on this GPU, so
-// frequencies are kept in turns as 64-bit fractions, step = round(f / 2pi * 2^64): the wrapping integer
-// product p * step IS the angle modulo one turn, off by at most |p| * 2^-65 turns.  Its top bits as a
-// signed fp32 fraction go to sincospif.
+// frequencies are kept in turns as 64-bit fractions, step = f / 2pi * 2^64: the wrapping integer product
+// p * step is p times the step modulo one turn, without any rounding, so positions add nothing to the step's own
+// error.  That is fp64's (kvq_rope_steps: a power, a logarithm for some scalings, a few roundings): at most 2^-48 of
+// the step and one unit of 2^-63, 2^-33 turns at position 131072.  The angle's top bits as a signed fp32 fraction go
+// to sincospif.
 //
 // Bound: bytes (every head row is read and written once, about 3 flops per byte).  One CTA takes a few
 // tokens: 256 threads compute the tokens' cosines and sines once into shared memory (64 pairs per token,

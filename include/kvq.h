@@ -644,9 +644,10 @@ size_t kv_offload_gather_ws(void);
  * cast.  The inverse rotation is the call with negated positions.
  *
  * Frequencies travel as 64-bit fractions of a turn per position: steps[i] =
- * f_i/2pi * 2^64, device uint64 [rot_dim/2], so that an angle is exact at every
- * position.  kvq_rope_steps (host code) fills them and mscale from the
- * description below; an own list is as good.
+ * f_i/2pi * 2^64, device uint64 [rot_dim/2].  Their product with a position wraps
+ * at whole turns and is not rounded.  kvq_rope_steps (host code) fills them and
+ * mscale from the description below, in fp64: a step is off by at most 2^-48 of
+ * itself and 2^-63 turns.  An own list is as good.
  *
  * dtype: of q, k and v, KVQ_F16 or KVQ_BF16.  q [n_tokens][H_q][d], k and v
  * [n_tokens][H_kv][d], device, 16-byte aligned, with `*_stride` elements between

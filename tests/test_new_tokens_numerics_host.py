@@ -1,5 +1,7 @@
 """Host side of the new-token operators where numbers are at the end of their range: score scales and rotary steps."""
 import ctypes
+import math
+from decimal import Decimal, getcontext
 
 import pytest
 
@@ -28,3 +30,46 @@ def test_scale_beyond_fp32_in_log2_units_is_refused(lib, scale, softcap):
         got = (lib.kv_decode_attn(by(L), by(pool), by(seqs), 256, by(mod), 256, None, 256, 1 << 30, None),
                lib.kv_chunk_attn(by(L), by(pool), by(seqs), 256, 256, 4, 2, by(mod), 256, None, 256, 1 << 30, None))
         assert got == ((_abi.KVQ_ERR_INVALID_ARG,) * 2 if bad else (0, 0)), kvq._abi.last_error()
+
+
+def turns_of(rot, kind, original, base, factor, low, high):
+    """Turns per position of every pair, to 60 digits."""
+    getcontext().prec = 60
+    # pi = 16 atan(1/5) - 4 atan(1/239)
+    atan = lambda n: sum((-1) ** k / (Decimal(2 * k + 1) * Decimal(n) ** (2 * k + 1)) for k in range(45))  # noqa: E731
+    pi = 16 * atan(5) - 4 * atan(239)
+    b, x = Decimal(base), Decimal(factor)
+    if kind == "ntk":
+        b = b * (Decimal(rot) / (rot - 2) * x.ln()).exp()
+    out = []
+    for i in range(rot // 2):
+        f = (-Decimal(2 * i) / rot * b.ln()).exp()
+        keep = Decimal(0 if kind == "linear" else 1)
+        if kind == "yarn":
+            at = [rot * (Decimal(original) / (Decimal(n) * 2 * pi)).ln() / (2 * b.ln()) for n in (low, high)]
+            lo, hi = max(math.floor(at[0]), 0), min(math.ceil(at[1]), rot - 1)
+            keep = 1 - min(max(Decimal(i - lo) / max(Decimal(hi - lo), Decimal("0.001")), Decimal(0)), Decimal(1))
+        if kind == "knees":
+            keep = min(max((original * f / (2 * pi) - Decimal(low)) / (Decimal(high) - Decimal(low)), Decimal(0)), Decimal(1))
+        out.append((f * keep + f / x * (1 - keep)) / (2 * pi) if kind in ("linear", "yarn", "knees") else f / (2 * pi))
+    return out
+
+
+@pytest.mark.parametrize("rot", [16, 96, 128])
+@pytest.mark.parametrize("base", [10000.0, 500000.0, 1000000.0])
+@pytest.mark.parametrize("kind,factor,original,low,high", [("plain", 1.0, 0, 0.0, 0.0), ("linear", 4.0, 0, 0.0, 0.0),
+                                                           ("ntk", 8.0, 0, 0.0, 0.0), ("yarn", 4.0, 32768, 32.0, 1.0),
+                                                           ("knees", 8.0, 8192, 1.0, 4.0)])
+def test_rope_angles_at_far_positions(lib, rot, base, kind, factor, original, low, high):
+    """The wrapped product of a position and a step against the angle itself, both in turns.  A step is within 2^-48 of itself
+    (the power's exponent is rounded, 2^-53 of it times ln(base) < 14; the power, the division and the ramp add a few
+    2^-53) and 2^-63 turns (the fraction's last two units)."""
+    r = _abi.Rope(rot, 0, _abi.ROPE_SCALINGS[kind], original, base, factor, low, high)
+    steps, m = (ctypes.c_uint64 * 64)(), ctypes.c_float(0)
+    assert lib.kvq_rope_steps(by(r), steps, by(m)) == 0
+    for i, f in enumerate(turns_of(rot, kind, original, base, factor, low, high)):
+        off = f * Decimal(2) ** -48 + Decimal(2) ** -63
+        for p in (1, 4097, 131071, 10 ** 6 + 3, 2 ** 31 - 1, -77777, -2 ** 31):
+            got = Decimal(p * steps[i] % 2 ** 64) / Decimal(2) ** 64
+            gap = abs(got - p * f % 1) % 1
+            assert min(gap, 1 - gap) <= abs(p) * off, (i, p)
