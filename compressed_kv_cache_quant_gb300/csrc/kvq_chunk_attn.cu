@@ -17,8 +17,8 @@
 // loop.  A row's weights are taken against an anchor, which cancels at the end: 2^7 below the row's maximum when
 // it is set, and set anew (O rescaled) when a weight would pass 2^15.99.  A rescale holds up its tile for about 900
 // cycles, so one row's turn is the turn of every row of its warp whose maximum has grown: 2048 tokens under a
-// 4096-token window take 119 us, with anchors that move one by one 138 us, without the room below (an anchor at
-// the maximum, moved for a growth beyond 2^14) 123 us.
+// 4096-token window take 115 us in a graph, 117 us with anchors at the maximum that move for a growth beyond 2^14;
+// anchors 2^7 below it that move one by one cost 16% more.
 //
 // P is one fp16 rounding of a weight, since the tensor cores take P and V in one type: off by 2^-11 of itself, or
 // by 2^-25 where it is subnormal.  Against a largest weight of 2^7 or more that is 2^-32, so what many small weights
@@ -172,6 +172,9 @@ __device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t* v) {
         "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
         W8(v, 0), W8(v, 8), W8(v, 16), W8(v, 24)
         : "memory");
+}
+__device__ __forceinline__ void tm_st1(uint32_t addr, uint32_t v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -535,7 +538,6 @@ __global__ void __launch_bounds__(CA_NT, 1)
         const int pos = T - n + tok0 + tok;
         const float slope2 = BIAS && valid ? a.mod.slopes[h * GQ + r % GQ] * KVQ_LOG2E : 0.0f;
         float m = valid ? -INFINITY : INFINITY, l = 0.0f;   // (no row: weights 0, never a new anchor)
-        bool far = false;   // some row of the warp has its maximum beyond CA_FAR
         if (i < nq) {
             for (int j = 0; j < nt; ++j) {
                 const int t0 = tile_of(it0 + j) * CA_KEYS;
@@ -555,19 +557,21 @@ __global__ void __launch_bounds__(CA_NT, 1)
                         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    if (CAP) {
+                        // The form of the cap below is the warp's choice, by the size of its scores: neither these rows
+                        // nor queries that are not the sequence's have a part in it, or what they hold would change
+                        // the others' last bits.
+                        tc_after();
+#pragma unroll 1
+                        for (int c = r0; c < r1; ++c) tm_st1(ts + c, 0);
+                        tm_wait_st();
+                    }
                 }
                 tc_after();
                 float s[128];
                 tm_ld128(ts, reinterpret_cast<uint32_t*>(s));
                 float scale = a.mod.pre;
                 if (CAP) {
-                    // the choice below is the warp's: neither rows behind T nor queries that are not the sequence's
-                    // have a part in it, or what they hold would change the others' last bits
-                    if (tail) {
-#pragma unroll
-                        for (int c = 0; c < 128; ++c)
-                            if (t0 + c >= T) s[c] = 0.0f;
-                    }
                     float big[2] = {0.0f, 0.0f};
 #pragma unroll
                     for (int c = 0; c < 128; c += 4) {
@@ -660,6 +664,16 @@ __global__ void __launch_bounds__(CA_NT, 1)
                         }
                     }
                 };
+                const auto rescale = [&](float f) {
+#pragma unroll
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tm_ld32(to + c, o);
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                        tm_st32(to + c, o);
+                    }
+                };
                 const auto hand_over = [&](int c) {   // the products start on the first half of the keys
                     tm_st32(ts + c / 2, p);
                     tm_wait_st();
@@ -667,18 +681,47 @@ __global__ void __launch_bounds__(CA_NT, 1)
                     __syncwarp();
                     if (lane == 0) bar_arrive(&S.p_full[i][c / 64]);
                 };
-                // A weight's exponent s * scale - m is rounded once, behind the difference.  That is exact enough
-                // until an fp32 step of m is no longer far below 1: then the product is rounded like m itself, or a
-                // row's largest weight would be 2^(m's rounding error), 0 or infinite.  At most three turns: one for
-                // `far`, one that moves m; behind that the largest exponent is CA_HEAD and at most half a step of m.
-                for (;;) {
-                    if (!CAP && !BIAS && far && scale != 1.0f) {   // (a cap or a bias left rounded scores, scale 1)
-                        const uint64_t by = pair(scale, scale);
+                // A weight's exponent s * scale - m is rounded once, behind the difference.  That is exact enough until an
+                // fp32 step of m is no longer far below 1: a row's largest weight would be 2^(m's rounding error), 0 or
+                // infinite.  Then the products are rounded like m itself, from S as it still lies in TMEM (an own path,
+                // since a change of s in the loop below costs every prompt 3%).
+                const auto far_tile = [&] {
+                    const auto seen = [&](int c) {
+                        return (columns(see.x - t0, see.y - t0, c >> 5) | columns(see.z - t0, see.w - t0, c >> 5)) >> (c & 31) & 1;
+                    };
+                    uint32_t v[32];
+                    float top = -INFINITY;
+                    for (int c = 0; c < 128; c += 32) {
+                        tm_ld32(ts + c, v);
 #pragma unroll
-                        for (int c = 0; c < 128; c += 2) unpair(mul2(pair(s[c], s[c + 1]), by), &s[c], &s[c + 1]);
-                        scale = 1.0f;
-                        mx4[0] = mx4[1] = mx4[2] = mx4[3] = -INFINITY;
+                        for (int x = 0; x < 32; ++x)
+                            if (seen(c + x)) top = fmaxf(top, __fmul_rn(__uint_as_float(v[x]), scale));
                     }
+                    const float anchor = fmaxf(m, top - CA_HEAD);
+                    const float f = m == anchor ? 1.0f : ex2(m - anchor);
+                    m = anchor;
+                    l *= f;
+                    if (j > 0) rescale(f);
+                    const float ms = m == -INFINITY ? 0.0f : m;
+                    for (int c = 0; c < 128; c += 64) {
+#pragma unroll
+                        for (int k = 0; k < 64; k += 32) {
+                            tm_ld32(ts + c + k, v);
+#pragma unroll
+                            for (int x = 0; x < 32; x += 2) {
+                                const float e0 = seen(c + k + x) ? ex2(__fmul_rn(__uint_as_float(v[x]), scale) - ms) : 0.0f;
+                                const float e1 = seen(c + k + x + 1) ? ex2(__fmul_rn(__uint_as_float(v[x + 1]), scale) - ms) : 0.0f;
+                                l += e0 + e1;
+                                p[(k + x) / 2] = half2_bits(e0, e1);
+                            }
+                        }
+                        hand_over(c);
+                    }
+                };
+                // At most two turns (with far_tile in place of a third): behind a move of m the largest exponent is
+                // CA_HEAD and the roundings of m, under 1/8 up to CA_FAR.
+                bool done = false;
+                for (;;) {
                     sum2[0] = sum2[1] = 0;
                     weights(0, true);
                     const float top = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]);
@@ -688,25 +731,18 @@ __global__ void __launch_bounds__(CA_NT, 1)
                     // one row's turn is every row's: an anchor that would have to follow later is set now
                     const bool grew = most > CA_HEAD;
                     const float mx = top * scale;
-                    if (!CAP && !BIAS && scale != 1.0f && __any_sync(0xffffffffu, grew && fabsf(mx) > CA_FAR)) {
-                        far = true;
-                        continue;
+                    if (!CAP && !BIAS && __any_sync(0xffffffffu, grew && fabsf(mx) > CA_FAR)) {
+                        far_tile();
+                        done = true;
+                        break;
                     }
                     const float anchor = mx - CA_HEAD;
                     const float f = grew ? ex2(m - anchor) : 1.0f;
                     if (grew) m = anchor;
                     l *= f;
-                    if (j > 0) {
-#pragma unroll
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t o[32];
-                            tm_ld32(to + c, o);
-#pragma unroll
-                            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                            tm_st32(to + c, o);
-                        }
-                    }
+                    if (j > 0) rescale(f);
                 }
+                if (done) continue;
                 hand_over(0);
                 weights(64, false);
                 hand_over(64);
