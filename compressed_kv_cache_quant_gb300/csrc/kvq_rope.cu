@@ -307,7 +307,7 @@ extern "C" int kv_qk_norm_rope(const kvq_layout* L, const kvq_rope* rope, const 
     a.qw = q_weight, a.kw = k_weight;
     a.eps = eps, a.mscale = mscale;
     a.pos = positions, a.steps = steps;
-    a.rot = rope->rot_dim;
+    a.rot = q || k ? rope->rot_dim : 0;   // (v alone is cast: positions and steps may then be NULL)
     a.Hq = q ? L->n_q_heads : 0, a.Hk = k ? L->n_kv_heads : 0, a.Hv = v ? L->n_kv_heads : 0;
     a.n = n_tokens;
     a.qo = q_out, a.ko = k_out, a.vo = v_out;

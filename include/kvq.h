@@ -655,8 +655,8 @@ size_t kv_offload_gather_ws(void);
  * NULL together with its output.  positions: device int32 [n_tokens], any order,
  * any sign.  Outputs: device fp16 without gaps, 16-byte aligned.  In place only
  * for fp16 rows without gaps; otherwise outputs overlap no input.
- * rot_dim: a multiple of 16, 0 .. 128 (0: norm and cast only; positions and
- * steps may then be NULL).  Head counts are free here (any H_q, H_kv > 0).
+ * rot_dim: a multiple of 16, 0 .. 128 (0: norm and cast only; then, and where v is
+ * given alone, positions and steps may be NULL).  Head counts are free here (any H_q, H_kv > 0).
  * No workspace.  Errors: INVALID_ARG, UNSUPPORTED, CUDA.
  * ---------------------------------------------------------------------- */
 #define KVQ_F16   0

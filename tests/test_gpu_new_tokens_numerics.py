@@ -207,3 +207,16 @@ print("as one")
     env = dict(os.environ, PYTHONPATH=os.pathsep.join([here, os.path.dirname(here)]))
     got = subprocess.run([sys.executable, "-c", prog], env=env, capture_output=True, text=True, timeout=300)
     assert got.returncode == 0 and "as one" in got.stdout, got.stdout + got.stderr
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("n", [1, 37, 5000])
+def test_v_alone_needs_no_positions(n, dt):
+    """v is only cast: with a table that rotates, a call for v alone takes no positions."""
+    require_gpu()
+    v = (c_rnd((n, 3, D), 7) * 3).to(dt).cuda()
+    out = torch.full((n + 1, 3, D), -7.0, dtype=torch.float16, device="cuda")
+    for tab in (kvq.RopeTable(128), kvq.RopeTable(64, interleaved=True), kvq.RopeTable(0)):
+        out[:n] = 0
+        kvq.kv_qk_norm_rope(kvq.make_layout(6, 3, 16), tab, None, None, None, None, None, v=v, v_out=out[:n])
+        assert torch.equal(out[:n], v.half()) and bool((out[n] == -7).all())
