@@ -882,7 +882,7 @@ struct ChunkPlan {
 ChunkPlan chunk_plan(const kvq_layout* L, const kvq_seqs* S, int64_t n_rows, int32_t max_new) {
     ChunkPlan p;
     const int GQ = L->n_q_heads / L->n_kv_heads, tpc = CA_ROWS / GQ;
-    const int64_t by_max = (int64_t)S->batch * ((max_new + tpc - 1) / tpc);
+    const int64_t by_max = S->batch * (((int64_t)max_new + tpc - 1) / tpc);
     p.items = std::max<int64_t>(1, std::min(by_max, n_rows / tpc + S->batch));
     const int64_t ctas = p.items * L->n_kv_heads, sms = kvq_num_sms();
     const int tiles = (S->max_len + CA_KEYS - 1) / CA_KEYS;

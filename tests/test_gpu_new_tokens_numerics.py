@@ -220,3 +220,17 @@ def test_v_alone_needs_no_positions(n, dt):
         out[:n] = 0
         kvq.kv_qk_norm_rope(kvq.make_layout(6, 3, 16), tab, None, None, None, None, None, v=v, v_out=out[:n])
         assert torch.equal(out[:n], v.half()) and bool((out[n] == -7).all())
+
+
+@pytest.mark.parametrize("most", [2 ** 31 - 1, 2 ** 31 - 100])
+def test_largest_bound_on_the_new_tokens(most):
+    """max_new is an upper bound: the largest there is gives what the exact one gives."""
+    require_gpu()
+    c = Case(8, 2, [300, 700, 90], [300, 150, 9], "plain", 146)
+    want = c.chunk(extra=0)[0]
+    out = torch.full_like(want, -7.0)
+    wk = ws(kvq.kv_chunk_attn_ws(c.cache, c.batch, 459, most))
+    kvq.kv_chunk_attn(c.cache, c.batch, c.q, torch.tensor(c.starts).cuda(), most, out, wk, mod=c.mod)
+    kvq.kvq_check(wk)
+    assert not bool((out == -7).all(-1).any())
+    c.check(out, c.chunk(extra=0)[1], True)
