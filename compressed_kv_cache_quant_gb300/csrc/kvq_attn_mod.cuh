@@ -47,6 +47,12 @@ static inline int kvq_mod_args(const kvq_attn_mod* mod, const char* fn, KvqModAr
     return KVQ_OK;
 }
 
+// Positions and counts of pages and tiles are 32-bit numbers, and sums of two of them have to be, too.
+static inline int kvq_check_max_len(const kvq_seqs* S, const char* fn) {
+    KVQ_REQUIRE(S->max_len <= 1 << 30, KVQ_ERR_UNSUPPORTED, "%s: max_len %d (at most 2^30)", fn, S->max_len);
+    return KVQ_OK;
+}
+
 // The cached tokens a query sees: [lo, hi) and, under a window, its document's first tokens [doc, sink).
 struct KvqSee {
     int32_t lo, hi, doc, sink;

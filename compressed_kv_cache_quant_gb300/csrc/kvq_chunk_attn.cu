@@ -943,7 +943,7 @@ int make_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
 
 extern "C" size_t kv_chunk_attn_ws(const kvq_layout* L, const kvq_seqs* S, int64_t n_rows, int32_t max_new) {
     if (kvq_check_layout(L, "kv_chunk_attn_ws", true) || kvq_check_seqs_sizes(S, "kv_chunk_attn_ws") ||
-        check_rows(n_rows, max_new, "kv_chunk_attn_ws"))
+        kvq_check_max_len(S, "kv_chunk_attn_ws") || check_rows(n_rows, max_new, "kv_chunk_attn_ws"))
         return 0;
     return chunk_plan(L, S, n_rows, max_new).bytes;
 }
@@ -957,6 +957,7 @@ extern "C" int kv_chunk_attn(const kvq_layout* L, const kvq_pool* P, const kvq_s
     if (st) return st;
     KVQ_REQUIRE(L->bits == 16, KVQ_ERR_UNSUPPORTED, "%s: bits %d (an fp16 layer)", fn, L->bits);
     st = kvq_check_seqs(S, fn);
+    if (!st) st = kvq_check_max_len(S, fn);
     if (st) return st;
     KVQ_REQUIRE(P && P->k16 && P->v16 && P->num_blocks > 0, KVQ_ERR_INVALID_ARG, "%s: pool needs k16 and v16", fn);
     const int64_t pool_rows = P->num_blocks * L->n_kv_heads * PG;

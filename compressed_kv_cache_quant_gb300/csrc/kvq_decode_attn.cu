@@ -496,7 +496,9 @@ DecPlan dec_plan(const kvq_layout* L, const kvq_seqs* S) {
 }  // namespace
 
 extern "C" size_t kv_decode_attn_ws(const kvq_layout* L, const kvq_seqs* S) {
-    if (kvq_check_layout(L, "kv_decode_attn_ws", true) || kvq_check_seqs_sizes(S, "kv_decode_attn_ws")) return 0;
+    if (kvq_check_layout(L, "kv_decode_attn_ws", true) || kvq_check_seqs_sizes(S, "kv_decode_attn_ws") ||
+        kvq_check_max_len(S, "kv_decode_attn_ws"))
+        return 0;
     return dec_plan(L, S).bytes;
 }
 
@@ -508,6 +510,7 @@ extern "C" int kv_decode_attn(const kvq_layout* L, const kvq_pool* P, const kvq_
     if (st) return st;
     KVQ_REQUIRE(L->bits == 16, KVQ_ERR_UNSUPPORTED, "%s: bits %d (an fp16 layer)", fn, L->bits);
     st = kvq_check_seqs(S, fn);
+    if (!st) st = kvq_check_max_len(S, fn);
     if (st) return st;
     KVQ_REQUIRE(P && P->k16 && P->v16 && P->num_blocks > 0, KVQ_ERR_INVALID_ARG, "%s: pool needs k16 and v16", fn);
     KVQ_REQUIRE(S->batch <= 65535 && L->n_kv_heads <= 65535, KVQ_ERR_UNSUPPORTED, "%s: batch or heads", fn);

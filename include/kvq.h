@@ -707,6 +707,7 @@ int kv_qk_norm_rope(const kvq_layout* layout, const kvq_rope* rope, const uint64
  * position where the query's document begins (doc_start: device int32, one entry
  * per query row; NULL: 0), which may lie behind the query: it then sees nothing.
  * A query that sees nothing gets output 0 and lse -inf.
+ * Both calls take max_len up to 2^30.
  * ---------------------------------------------------------------------- */
 typedef struct kvq_attn_mod {
     float   scale;

@@ -73,3 +73,17 @@ def test_rope_angles_at_far_positions(lib, rot, base, kind, factor, original, lo
             got = Decimal(p * steps[i] % 2 ** 64) / Decimal(2) ** 64
             gap = abs(got - p * f % 1) % 1
             assert min(gap, 1 - gap) <= abs(p) * off, (i, p)
+
+
+def test_max_len_beyond_2_30_is_refused(lib):
+    """Positions, pages and tiles are counted in 32 bits with sums of two of them: the attention of new tokens takes up to 2^30
+    tokens a sequence (512 GB of an fp16 layer with one kv head)."""
+    L = kvq.make_layout(8, 2, 16)
+    pool = _abi.Pool(num_blocks=16, max_seqs=4, t_cap=0, k16=256, v16=256)
+    for max_len, want in ((2 ** 30, 0), (2 ** 30 + 1, _abi.KVQ_ERR_UNSUPPORTED), (2 ** 31 - 1, _abi.KVQ_ERR_UNSUPPORTED)):
+        seqs = _abi.Seqs(256, 256, 0, 2 ** 27, max_len, 0)   # a batch of none
+        assert lib.kv_decode_attn(by(L), by(pool), by(seqs), 256, None, 256, None, 256, 1 << 40, None) == want
+        assert lib.kv_chunk_attn(by(L), by(pool), by(seqs), 256, 256, 4, 2, None, 256, None, 256, 1 << 40, None) == want
+        seqs.batch = 1
+        assert (lib.kv_decode_attn_ws(by(L), by(seqs)) == 0) == (want != 0)
+        assert (lib.kv_chunk_attn_ws(by(L), by(seqs), 4, 2) == 0) == (want != 0)
