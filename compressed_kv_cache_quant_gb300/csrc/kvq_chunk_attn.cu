@@ -26,8 +26,8 @@
 // the fp16 output's own: 2.5e-4 to 2.9e-4 of the output (normwise) where the output's rounding alone is 2.1e-4.  A
 // second half of P would bring that down for half as many products again.
 //
-// Measured (32 q / 8 kv heads): a causal prompt of 16384 tokens 1.36 ms, 1.62 PFLOP/s of the needed products,
-// in a short run, 1.45 ms under the power limit of a long one; five drafted tokens of eight 32K sequences
+// Measured (32 q / 8 kv heads): a causal prompt of 16384 tokens 1.35 ms, 1.63 PFLOP/s of the needed products,
+// in a short run, 1.44 ms under the power limit of a long one; five drafted tokens of eight 32K sequences
 // 171 us, 6.0 TB/s.  A turn (two tiles, 128 cached tokens) takes about 2700 cycles against 2048 of products:
 // a tile's softmax takes 1250 (128 exponentials per row, 4-5 cycles each per warp), then its 768 last cycles
 // of products and some 300 of signals close its chain, and the issuing warp spends 100 cycles on every wait,

@@ -731,7 +731,12 @@ typedef struct kvq_attn_mod {
  * the largest weight that their warp meets.  Results do not depend on the run
  * (parts are joined in their order).  Pages that hold no visible token are
  * not read and their block table entries may be stale; rows that are not visible
- * may hold anything, NaN included.  q, out, k16, v16 16-byte aligned.
+ * may hold anything, NaN included.  A visible infinite V value gives NaN (it meets
+ * both halves of a weight).  The parts are cut for max_len, not for what is visible:
+ * under a window or a late document far shorter than max_len most parts are empty,
+ * and the call costs several times what the visible rows would (131072 tokens, 8 kv
+ * heads, a window of 4096: 34 us, where a cache of 4096 tokens takes 9).  q, out, k16,
+ * v16 16-byte aligned.
  * ws: kv_decode_attn_ws(layout, seqs) bytes.
  * ---------------------------------------------------------------------- */
 int kv_decode_attn(const kvq_layout* layout, const kvq_pool* pool, const kvq_seqs* seqs,
@@ -771,7 +776,9 @@ size_t kv_chunk_attn_ws(const kvq_layout* layout, const kvq_seqs* seqs, int64_t 
  * [n_pairs][2]).  A pair of equal ids copies nothing; an id outside the pool is
  * skipped and flagged.  No id may be a destination twice or both a source and a
  * destination (kvq_block_fork and kvq_block_compact give such lists).  Page
- * arrays 16-byte aligned.  ws: kv_pages_copy_ws() bytes (status word only).
+ * arrays 16-byte aligned.  What a caller keeps by page beside the pool (k_out of an
+ * isolated layer) moves with a copy of its own.  ws: kv_pages_copy_ws() bytes
+ * (status word only).
  * ---------------------------------------------------------------------- */
 int kv_pages_copy(const kvq_layout* layout, const kvq_pool* pool, const int32_t* pairs, int32_t n_pairs,
                   void* ws, size_t ws_bytes, void* stream);
@@ -782,7 +789,8 @@ size_t kv_pages_copy_ws(void);
  * fp16 layer, from slot pairs[i][0] to slot pairs[i][1] (device int32
  * [n_pairs][2]; rules as kv_pages_copy, ids in [0, max_seqs)).  A source slot of
  * a layer with kT must be below batch (its length is read).  Layers without
- * slot state copy nothing.  Slot arrays 16-byte aligned.
+ * slot state copy nothing.  What a caller keeps by sequence beside the pool (out_ch
+ * of an isolated layer, H2O scores) is copied by the caller.  Slot arrays 16-byte aligned.
  * ws: kv_slots_copy_ws() bytes (status word only). */
 int kv_slots_copy(const kvq_layout* layout, const kvq_pool* pool, const kvq_seqs* seqs, const int32_t* pairs,
                   int32_t n_pairs, void* ws, size_t ws_bytes, void* stream);
@@ -858,14 +866,16 @@ int     kvq_block_free_n(kvq_allocator* a, int32_t n, const int32_t* ids);
  * 64-token K group, whose codes are written when a branch completes it.
  * dst_pages: out, as many entries as src_pages; pairs: out int32 [4][2].
  * NO_SPACE (nothing taken) when too few pages are free.  The slot state goes
- * with kv_slots_copy. */
+ * with kv_slots_copy.  Where layers share their page ids, fork with the layout of a
+ * quantized one, if there is one, and copy the pairs in every layer. */
 int     kvq_block_fork(kvq_allocator* a, const kvq_layout* layout, int64_t n_tokens, const int32_t* src_pages,
                        int32_t* dst_pages, int32_t* pairs, int32_t* n_pairs);
 /* Moves the highest used pages into the lowest free ones, at most max_moves of
  * them, until the used pages are the lowest ids: pairs (out int32
  * [max_moves][2]) for kv_pages_copy, map (out int32 [num_blocks], the new id of
  * every page) for kvq_table_remap, reference counts moved along.  Free pages are
- * handed out lowest first afterwards. */
+ * handed out lowest first afterwards.  The pairs are copied in every layer that uses
+ * these page ids, k_out of isolated layers included. */
 int     kvq_block_compact(kvq_allocator* a, int32_t max_moves, int32_t* pairs, int32_t* map, int32_t* n_moves);
 /* Reference count of a page (0 = free), or a negative error. */
 int     kvq_block_refcount(const kvq_allocator* a, int32_t id);
