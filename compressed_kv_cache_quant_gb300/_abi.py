@@ -67,11 +67,17 @@ class AttnModStruct(ctypes.Structure):
                 ("slopes", c_void_p), ("prefix_len", c_void_p), ("doc_start", c_void_p)]
 
 
+class Latent(ctypes.Structure):
+    _fields_ = [("latent_dim", c_int32), ("rope_dim", c_int32), ("num_blocks", c_int64), ("rows", c_void_p)]
+
+
+LATENT_DIM, LATENT_ROPE = 512, 64      # a latent layer's row
+TREE_MAX = 256                         # nodes of a sequence's drafted trees
 F16, BF16 = 0, 1                       # dtype of kv_qk_norm_rope
 ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3, "knees": 4}
 
 PL, PP, PS = POINTER(Layout), POINTER(Pool), POINTER(Seqs)
-PR, PM = POINTER(Rope), POINTER(AttnModStruct)
+PR, PM, PC = POINTER(Rope), POINTER(AttnModStruct), POINTER(Latent)
 VP = c_void_p
 
 # name -> (restype, argtypes); mirrors include/kvq.h
@@ -129,6 +135,18 @@ PROTOTYPES = {
     "kv_decode_attn_ws": (c_size_t, [PL, PS]),
     "kv_chunk_attn": (c_int, [PL, PP, PS, VP, VP, c_int64, c_int32, PM, VP, VP, VP, c_size_t, VP]),
     "kv_chunk_attn_ws": (c_size_t, [PL, PS, c_int64, c_int32]),
+    "kv_rope_append": (c_int, [PL, PP, PS, PR, VP, c_float, c_int32, c_int64, VP, VP, VP, c_int64, VP, c_int64, VP, c_int64,
+                               VP, VP, c_float, VP, VP, c_size_t, VP]),
+    "kv_rope_append_ws": (c_size_t, []),
+    "kv_tree_attn": (c_int, [PL, PP, PS, VP, VP, VP, c_int64, c_int32, PM, VP, VP, VP, c_size_t, VP]),
+    "kv_tree_attn_ws": (c_size_t, [PL, PS, c_int64, c_int32]),
+    "kv_latent_append": (c_int, [PC, PS, PR, VP, c_float, c_int32, c_int64, VP, VP, VP, c_int64, VP, c_int64, VP, c_float,
+                                 c_int32, VP, c_int64, c_int64, VP, c_int64, c_int64, VP, c_size_t, VP]),
+    "kv_latent_attn": (c_int, [PC, PS, c_int32, VP, VP, VP, c_int64, c_int32, c_float, VP, VP, VP, c_size_t, VP]),
+    "kv_latent_attn_ws": (c_size_t, [PS, c_int32, c_int64, c_int32]),
+    "kv_latent_expanded_attn": (c_int, [c_int32, c_int32, VP, VP, c_int64, c_int64, VP, c_int64, VP, c_int64, c_int64, c_int64,
+                                        VP, VP, c_int64, c_int32, c_int32, c_float, VP, VP, VP, c_size_t, VP]),
+    "kv_latent_expanded_attn_ws": (c_size_t, [c_int32, c_int32, c_int64, c_int32, c_int32]),
     "kv_pages_copy": (c_int, [PL, PP, VP, c_int32, VP, c_size_t, VP]),
     "kv_pages_copy_ws": (c_size_t, []),
     "kv_slots_copy": (c_int, [PL, PP, PS, VP, c_int32, VP, c_size_t, VP]),

@@ -36,8 +36,10 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "kvq_attn_mod.cuh"
+#include "kvq_tree.cuh"
 
 namespace {
 
@@ -60,6 +62,7 @@ constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
 
 struct ChunkArgs {
     const int32_t *bt, *seq_lens, *q_starts;
+    const int32_t* parents;       // kv_tree_attn: of every row
     int64_t num_blocks;
     int32_t batch, max_blocks, max_len, max_new, H, GQ, n_splits;
     int32_t items, heads_first;   // groups of new tokens, at most; which of heads and groups runs faster in the grid
@@ -313,12 +316,15 @@ __device__ __forceinline__ uint32_t columns(int a, int b, int w) {
     return b > a ? below(b - 32 * w) & ~below(a - 32 * w) : 0u;
 }
 
-template <bool CAP, bool BIAS>
+// TREE: the new tokens are nodes of trees.  A node's interval ends with the cached tokens before them, and its path
+// adds a few bits among the last columns; positions go by depth.
+template <bool CAP, bool BIAS, bool TREE>
 __global__ void __launch_bounds__(CA_NT, 1)
     chunk_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_v, const __grid_constant__ ChunkArgs a) {
     extern __shared__ unsigned char raw[];
     __shared__ Shared S;
+    __shared__ std::conditional_t<TREE, KvqTree, int> tree;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int GQ = a.GQ, tpc = CA_ROWS / GQ, split = blockIdx.y;
     const int h = a.heads_first ? blockIdx.x % a.H : blockIdx.x / a.items;
@@ -341,10 +347,37 @@ __global__ void __launch_bounds__(CA_NT, 1)
     const int first = a.q_starts[b], n = a.q_starts[b + 1] - first, T = a.seq_lens[b];
     const int ntok = min(tpc, n - tok0), rows = ntok * GQ;
     const int nq = rows > 128 ? 2 : 1;
+    const int ctx = T - n;   // cached tokens before the new ones
+    if constexpr (TREE) {
+        if (tid < n) kvq_tree_fetch(tree, a.parents + first, tid, a.hdr);
+        __syncthreads();
+        if (tid < n) kvq_tree_walk(tree, tid);
+        __syncthreads();   // (of the nodes' paths a row reads its own, of their depths all)
+    }
     if (tid < ntok) {
         const int i = tok0 + tid;
-        const KvqSee see = kvq_see(a.mod, T - n + i, T, a.mod.prefix_len ? a.mod.prefix_len[b] : 0,
-                                   a.mod.doc_start ? a.mod.doc_start[first + i] : 0);
+        const int doc = a.mod.doc_start ? a.mod.doc_start[first + i] : 0;
+        KvqSee see;
+        if constexpr (TREE) {
+            const int pos = ctx + tree.depth[i];
+            see = kvq_see(a.mod, pos, ctx, 0, doc);
+            // ancestors the document or the window leaves out, by the rules of the cached tokens
+            if (doc > ctx || a.mod.window > 0) {
+                for (int k = i, at = pos; k >= 0; k = tree.parent[k], --at) {
+                    if (at < doc || (a.mod.window > 0 && at <= pos - a.mod.window && at - max(doc, 0) >= a.mod.n_sink))
+                        tree.path[i][k >> 5] &= ~(1u << (k & 31));
+                }
+            }
+            uint32_t any = 0;
+#pragma unroll
+            for (int w = 0; w < KVQ_TREE_WORDS; ++w) any |= tree.path[i][w];
+            if (any) {
+                atomicMin(&S.lo_min, ctx);
+                atomicMax(&S.hi_max, T);
+            }
+        } else {
+            see = kvq_see(a.mod, ctx + i, T, a.mod.prefix_len ? a.mod.prefix_len[b] : 0, doc);
+        }
         S.see[tid] = make_int4(see.lo, see.hi, see.doc, see.sink);
         if (see.lo < see.hi) {
             atomicMin(&S.lo_min, see.lo);
@@ -418,6 +451,7 @@ __global__ void __launch_bounds__(CA_NT, 1)
                         const int p0 = t * (CA_KEYS / PG);
                         if (e.x < e.y) bits |= below((e.y + PG - 1) / PG - p0) & ~below(e.x / PG - p0);
                         if (e.z < e.w) bits |= below((e.w + PG - 1) / PG - p0) & ~below(e.z / PG - p0);
+                        if (TREE) bits |= below((T + PG - 1) / PG - p0) & ~below(ctx / PG - p0);
                     }
                     need = __reduce_or_sync(0xffffffffu, bits);
                 }
@@ -535,7 +569,16 @@ __global__ void __launch_bounds__(CA_NT, 1)
         }
         maxlo = __reduce_max_sync(0xffffffffu, maxlo);
         minhi = __reduce_min_sync(0xffffffffu, minhi);
-        const int pos = T - n + tok0 + tok;
+        int pos = ctx + tok0 + tok;
+        if constexpr (TREE) pos = ctx + (valid ? tree.depth[tok0 + tok] : 0);
+        // what the row sees of the w-th 32 columns of the tile at t0
+        const auto seen_bits = [&](int t0, int w) {
+            uint32_t bits = columns(see.x - t0, see.y - t0, w) | columns(see.z - t0, see.w - t0, w);
+            if constexpr (TREE) {
+                if (valid) bits |= kvq_tree_bits(tree, tok0 + tok, t0 + 32 * w - ctx);
+            }
+            return bits;
+        };
         const float slope2 = BIAS && valid ? a.mod.slopes[h * GQ + r % GQ] * KVQ_LOG2E : 0.0f;
         float m = valid ? -INFINITY : INFINITY, l = 0.0f;   // (no row: weights 0, never a new anchor)
         if (i < nq) {
@@ -605,7 +648,20 @@ __global__ void __launch_bounds__(CA_NT, 1)
                 if (BIAS) {
                     const float from = (float)(pos - t0);   // (whole numbers: exact below 2^24)
                     const float mul = CAP ? 1.0f : a.mod.pre;
-                    if (a.mod.prefix_len == nullptr) {
+                    bool nodes = false;
+                    if constexpr (TREE) {
+                        nodes = t0 + CA_KEYS > ctx;
+                        if (nodes) {
+#pragma unroll
+                            for (int c = 0; c < 128; ++c) {
+                                const int k = t0 + c - ctx;
+                                const int at = k < 0 ? t0 + c : k < n ? ctx + tree.depth[k] : pos;
+                                s[c] = fmaf(s[c], mul, -slope2 * fabsf((float)(pos - at)));
+                            }
+                        }
+                    }
+                    if (nodes) {
+                    } else if (TREE || a.mod.prefix_len == nullptr) {
                         // what is seen is not ahead: -slope (from - c), linear in the column
                         const float at0 = -slope2 * from;
                         const uint64_t mul_2 = pair(mul, mul);
@@ -624,7 +680,7 @@ __global__ void __launch_bounds__(CA_NT, 1)
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
                         // an edge crosses few of a warp's words of 32 columns
-                        const uint32_t bits = columns(see.x - t0, see.y - t0, w) | columns(see.z - t0, see.w - t0, w);
+                        const uint32_t bits = seen_bits(t0, w);
                         if (__all_sync(0xffffffffu, bits == ~0u)) continue;
 #pragma unroll
                         for (int c = 0; c < 32; ++c)
@@ -687,7 +743,7 @@ __global__ void __launch_bounds__(CA_NT, 1)
                 // since a change of s in the loop below costs every prompt 3%).
                 const auto far_tile = [&] {
                     const auto seen = [&](int c) {
-                        return (columns(see.x - t0, see.y - t0, c >> 5) | columns(see.z - t0, see.w - t0, c >> 5)) >> (c & 31) & 1;
+                        return seen_bits(t0, c >> 5) >> (c & 31) & 1;
                     };
                     uint32_t v[32];
                     float top = -INFINITY;
@@ -867,6 +923,13 @@ int check_rows(int64_t n_rows, int32_t max_new, const char* fn) {
     return KVQ_OK;
 }
 
+int check_tree_rows(int64_t n_rows, int32_t max_new, const char* fn) {
+    const int st = check_rows(n_rows, max_new, fn);
+    if (st) return st;
+    KVQ_REQUIRE(max_new <= KVQ_TREE_MAX, KVQ_ERR_UNSUPPORTED, "%s: max_new %d (at most %d)", fn, max_new, KVQ_TREE_MAX);
+    return KVQ_OK;
+}
+
 struct ChunkPlan {
     int64_t items;   // groups of new tokens over all sequences, at most
     int n_splits;
@@ -948,10 +1011,10 @@ extern "C" size_t kv_chunk_attn_ws(const kvq_layout* L, const kvq_seqs* S, int64
     return chunk_plan(L, S, n_rows, max_new).bytes;
 }
 
-extern "C" int kv_chunk_attn(const kvq_layout* L, const kvq_pool* P, const kvq_seqs* S, const uint16_t* q,
-                             const int32_t* q_starts, int64_t n_rows, int32_t max_new, const kvq_attn_mod* mod,
-                             uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
-    static const char* fn = "kv_chunk_attn";
+// kv_chunk_attn, or with `tree` kv_tree_attn.
+static int chunk_attn(const char* fn, bool tree, const kvq_layout* L, const kvq_pool* P, const kvq_seqs* S, const uint16_t* q,
+                      const int32_t* parents, const int32_t* q_starts, int64_t n_rows, int32_t max_new,
+                      const kvq_attn_mod* mod, uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
     kvq_clear_error();
     int st = kvq_check_layout(L, fn, true);
     if (st) return st;
@@ -963,16 +1026,17 @@ extern "C" int kv_chunk_attn(const kvq_layout* L, const kvq_pool* P, const kvq_s
     const int64_t pool_rows = P->num_blocks * L->n_kv_heads * PG;
     KVQ_REQUIRE(P->num_blocks <= INT32_MAX && pool_rows <= INT32_MAX && L->n_kv_heads <= 65535, KVQ_ERR_UNSUPPORTED,
                 "%s: more than 2^31 - 1 rows in the pool", fn);
-    st = check_rows(n_rows, max_new, fn);
+    st = tree ? check_tree_rows(n_rows, max_new, fn) : check_rows(n_rows, max_new, fn);
     if (st) return st;
     ChunkArgs a;
     st = kvq_mod_args(mod, fn, &a.mod);
     if (st) return st;
+    KVQ_REQUIRE(!tree || a.mod.prefix_len == nullptr, KVQ_ERR_UNSUPPORTED, "%s: prefix_len (trees have no prefix)", fn);
     const ChunkPlan p = chunk_plan(L, S, n_rows, max_new);
     st = kvq_check_ws(ws, ws_bytes, p.bytes, fn);
     if (st) return st;
     if (S->batch == 0 || n_rows == 0) return KVQ_OK;
-    KVQ_REQUIRE(q && out && q_starts && (S->block_table || S->max_len == 0), KVQ_ERR_INVALID_ARG, "%s: NULL buffer", fn);
+    KVQ_REQUIRE(q && out && q_starts && (!tree || parents) && (S->block_table || S->max_len == 0), KVQ_ERR_INVALID_ARG, "%s: NULL buffer", fn);
     KVQ_REQUIRE((((uintptr_t)q | (uintptr_t)out | (uintptr_t)P->k16 | (uintptr_t)P->v16) & 15u) == 0,
                 KVQ_ERR_INVALID_ARG, "%s: q, out, k16 and v16 must be 16-byte aligned", fn);
     KVQ_REQUIRE(p.items * L->n_kv_heads <= INT32_MAX, KVQ_ERR_UNSUPPORTED, "%s: n_rows", fn);
@@ -988,7 +1052,7 @@ extern "C" int kv_chunk_attn(const kvq_layout* L, const kvq_pool* P, const kvq_s
     if (!st) st = make_map(&map_v, P->v16, 4, kd, ks, kb, fn);
     if (st) return st;
     a.num_blocks = P->num_blocks;
-    a.bt = S->block_table, a.seq_lens = S->seq_lens, a.q_starts = q_starts;
+    a.bt = S->block_table, a.seq_lens = S->seq_lens, a.q_starts = q_starts, a.parents = parents;
     a.batch = S->batch, a.max_blocks = S->max_blocks, a.max_len = S->max_len, a.max_new = max_new;
     a.H = H, a.GQ = GQ, a.n_splits = p.n_splits;
     a.n_rows = n_rows;
@@ -1012,6 +1076,31 @@ extern "C" int kv_chunk_attn(const kvq_layout* L, const kvq_pool* P, const kvq_s
         return (int)KVQ_OK;
     };
     const bool cap = a.mod.post != 0.0f, bias = a.mod.slopes != nullptr;
-    if (cap) return bias ? go(chunk_attn_kernel<true, true>) : go(chunk_attn_kernel<true, false>);
-    return bias ? go(chunk_attn_kernel<false, true>) : go(chunk_attn_kernel<false, false>);
+    if (tree) {
+        if (cap) return bias ? go(chunk_attn_kernel<true, true, true>) : go(chunk_attn_kernel<true, false, true>);
+        return bias ? go(chunk_attn_kernel<false, true, true>) : go(chunk_attn_kernel<false, false, true>);
+    }
+    if (cap) return bias ? go(chunk_attn_kernel<true, true, false>) : go(chunk_attn_kernel<true, false, false>);
+    return bias ? go(chunk_attn_kernel<false, true, false>) : go(chunk_attn_kernel<false, false, false>);
+}
+
+extern "C" int kv_chunk_attn(const kvq_layout* L, const kvq_pool* P, const kvq_seqs* S, const uint16_t* q,
+                             const int32_t* q_starts, int64_t n_rows, int32_t max_new, const kvq_attn_mod* mod,
+                             uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+    return chunk_attn("kv_chunk_attn", false, L, P, S, q, nullptr, q_starts, n_rows, max_new, mod, out, lse, ws, ws_bytes,
+                      stream);
+}
+
+extern "C" size_t kv_tree_attn_ws(const kvq_layout* L, const kvq_seqs* S, int64_t n_rows, int32_t max_new) {
+    if (kvq_check_layout(L, "kv_tree_attn_ws", true) || kvq_check_seqs_sizes(S, "kv_tree_attn_ws") ||
+        kvq_check_max_len(S, "kv_tree_attn_ws") || check_tree_rows(n_rows, max_new, "kv_tree_attn_ws"))
+        return 0;
+    return chunk_plan(L, S, n_rows, max_new).bytes;
+}
+
+extern "C" int kv_tree_attn(const kvq_layout* L, const kvq_pool* P, const kvq_seqs* S, const uint16_t* q,
+                            const int32_t* parents, const int32_t* q_starts, int64_t n_rows, int32_t max_new,
+                            const kvq_attn_mod* mod, uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+    return chunk_attn("kv_tree_attn", true, L, P, S, q, parents, q_starts, n_rows, max_new, mod, out, lse, ws, ws_bytes,
+                      stream);
 }

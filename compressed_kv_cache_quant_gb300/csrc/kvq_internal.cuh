@@ -182,6 +182,8 @@ static inline bool kvq_v_sym(const kvq_layout* L) { return (L->bits & KVQ_V_SYMM
 // Validates the fields of a layout shared by all calls.  need_q: the call
 // reads query heads (H_q / H_kv must be 1, 2, 4 or 8).
 int kvq_check_layout(const kvq_layout* L, const char* fn, bool need_q);
+// Validates a latent layer's descriptor.
+int kvq_check_latent(const kvq_latent* C, const char* fn);
 // Validates the batch descriptor (pointers, sizes).
 int kvq_check_seqs(const kvq_seqs* S, const char* fn);
 // Validates only the sizes of a batch descriptor (for workspace queries).

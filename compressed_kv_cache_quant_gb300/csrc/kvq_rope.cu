@@ -15,12 +15,10 @@
 // 16-byte loads, so a row's norm is three shuffles and both members of every pair are in one lane.  A row's
 // loads are issued while the one before is worked on.  Measured: 32768 tokens of 32 + 8 + 8 bf16 heads with
 // norms 125 us (6.45 TB/s, 95% of the measured copy rate); eight tokens 1.9 us in a graph.
-#include <cuda_bf16.h>
-
 #include <algorithm>
 #include <cmath>
 
-#include "kvq_internal.cuh"
+#include "kvq_rope.cuh"
 
 namespace {
 
@@ -40,57 +38,6 @@ struct RopeArgs {
     int64_t n;
     uint16_t *qo, *ko, *vo;
 };
-
-__device__ __forceinline__ void unpack(const uint4& w, float* x, __half*) {
-    const __half2* h = reinterpret_cast<const __half2*>(&w);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(h[i]);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-    }
-}
-__device__ __forceinline__ void unpack(const uint4& w, float* x, __nv_bfloat16*) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(u[i] << 16);
-        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ uint4 pack_half(const float* x) {
-    uint4 w;
-    __half2* h = reinterpret_cast<__half2*>(&w);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-    return w;
-}
-
-// the pairs (u, v) and (p, q) by the angles whose cosines and sines are f = (cos, sin, cos, sin)
-__device__ __forceinline__ void turn_two(float* u, float* v, float* p, float* q, float4 f) {
-    const float x = *u, y = *v, z = *p, w = *q;
-    *u = x * f.x - y * f.y;
-    *v = y * f.x + x * f.y;
-    *p = z * f.z - w * f.w;
-    *q = w * f.z + z * f.w;
-}
-
-// The two 8-value chunks of a head row that lane l (< 8) of a group holds.  Half layout: chunk c pairs
-// with chunk c + rot/16, and the chunks behind the rotated part go to the remaining lanes.
-template <bool INTER>
-__device__ __forceinline__ void chunks(int l, int rot, int* a, int* b) {
-    const int half = rot >> 4;
-    if (INTER) {
-        *a = l;
-        *b = l + 8;
-    } else if (l < half) {
-        *a = l;
-        *b = l + half;
-    } else {
-        *a = 2 * l;
-        *b = 2 * l + 1;
-    }
-}
 
 // One head row of a lane's group: where it is read and written, its weight, whether it is rotated.
 struct Row {
@@ -123,8 +70,6 @@ __device__ __forceinline__ Row row_of(const RopeArgs& a, int64_t tok, int h, con
 
 template <typename T, bool INTER>
 __global__ void __launch_bounds__(RP_NT) norm_rope_kernel(const __grid_constant__ RopeArgs a, int tok_per_cta) {
-    // cosines and sines by the lane that uses them: entry 8j + l holds the j-th two pairs of lane l, so that
-    // a group's 16-byte loads cover neighbouring words
     __shared__ __align__(16) float2 cs[RP_TOK][D / 2];
     __shared__ __align__(16) float wt[2][D];
     const int64_t t0 = (int64_t)blockIdx.x * tok_per_cta;
@@ -158,11 +103,7 @@ __global__ void __launch_bounds__(RP_NT) norm_rope_kernel(const __grid_constant_
     for (int i = threadIdx.x; i < nt * (D / 2); i += RP_NT) {
         const int k = i / (D / 2), p = i % (D / 2);
         if (p >= half) continue;
-        const uint64_t ph = (uint64_t)(int64_t)a.pos[t0 + k] * a.steps[p];
-        float s, c;
-        sincospif(__ll2float_rn((long long)ph) * 1.0842021724855044e-19f, &s, &c);  // * 2^-63: half turns
-        const int lane = INTER ? (p >> 2) & 7 : p >> 3, nth = INTER ? (p >> 5) * 4 + (p & 3) : p & 7;
-        cs[k][((nth >> 1) * 8 + lane) * 2 + (nth & 1)] = make_float2(c * a.mscale, s * a.mscale);
+        cs[k][pair_entry<INTER>(p)] = kvq_cos_sin(a.pos[t0 + k], a.steps[p], a.mscale);
     }
     __syncthreads();
     while (t < nt) {
@@ -174,54 +115,18 @@ __global__ void __launch_bounds__(RP_NT) norm_rope_kernel(const __grid_constant_
         h += RP_GROUPS;
         settle();
         fetch();
-        if (now.w != nullptr) {
-            float ss = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss += x[i] * x[i] + y[i] * y[i];
-            // the 8 lanes of a group run the same trip count, so the mask is the group's own lanes
-            const unsigned m = 0xffu << (threadIdx.x & 24);
-            ss += __shfl_xor_sync(m, ss, 1);
-            ss += __shfl_xor_sync(m, ss, 2);
-            ss += __shfl_xor_sync(m, ss, 4);
-            const float inv = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
-#pragma unroll
-            for (int i = 0; i < 8; i += 4) {
-                const float4 u = *reinterpret_cast<const float4*>(now.w + 8 * ca + i);
-                const float4 v = *reinterpret_cast<const float4*>(now.w + 8 * cb + i);
-                x[i] *= inv * u.x, x[i + 1] *= inv * u.y, x[i + 2] *= inv * u.z, x[i + 3] *= inv * u.w;
-                y[i] *= inv * v.x, y[i + 1] *= inv * v.y, y[i + 2] *= inv * v.z, y[i + 3] *= inv * v.w;
-            }
-        }
-        if (now.turn) {
-            const float4* f = reinterpret_cast<const float4*>(cs[tn]) + l;
-            if (INTER) {
-                if (8 * ca < a.rot) turn_two(&x[0], &x[1], &x[2], &x[3], f[0]), turn_two(&x[4], &x[5], &x[6], &x[7], f[8]);
-                if (8 * cb < a.rot) turn_two(&y[0], &y[1], &y[2], &y[3], f[16]), turn_two(&y[4], &y[5], &y[6], &y[7], f[24]);
-            } else if (16 * l < a.rot) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) turn_two(&x[2 * j], &y[2 * j], &x[2 * j + 1], &y[2 * j + 1], f[8 * j]);
-            }
-        }
+        if (now.w != nullptr) norm_row(x, y, now.w, ca, cb, a.eps);
+        if (now.turn) turn_row<INTER>(x, y, cs[tn], l, ca, cb, a.rot);
         *reinterpret_cast<uint4*>(now.dst + 8 * ca) = pack_half(x);
         *reinterpret_cast<uint4*>(now.dst + 8 * cb) = pack_half(y);
     }
 }
 
-int rope_spec_ok(const kvq_rope* r, const char* fn) {
-    KVQ_REQUIRE(r != nullptr, KVQ_ERR_INVALID_ARG, "%s: NULL rope", fn);
-    KVQ_REQUIRE(r->rot_dim >= 0 && r->rot_dim <= D && r->rot_dim % 16 == 0, KVQ_ERR_UNSUPPORTED,
-                "%s: rot_dim %d (a multiple of 16 up to 128)", fn, r->rot_dim);
-    KVQ_REQUIRE(r->interleaved == 0 || r->interleaved == 1, KVQ_ERR_INVALID_ARG, "%s: interleaved", fn);
-    return KVQ_OK;
-}
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
 }  // namespace
 
 extern "C" int kvq_rope_steps(const kvq_rope* r, uint64_t* steps, float* mscale) {
     kvq_clear_error();
-    const int st = rope_spec_ok(r, "kvq_rope_steps");
+    const int st = kvq_check_rope(r, "kvq_rope_steps");
     if (st) return st;
     KVQ_REQUIRE(mscale != nullptr && (steps != nullptr || r->rot_dim == 0), KVQ_ERR_INVALID_ARG,
                 "kvq_rope_steps: NULL output");
@@ -277,7 +182,7 @@ extern "C" int kv_qk_norm_rope(const kvq_layout* L, const kvq_rope* rope, const 
     kvq_clear_error();
     int st = kvq_check_layout(L, fn, false);
     if (st) return st;
-    st = rope_spec_ok(rope, fn);
+    st = kvq_check_rope(rope, fn);
     if (st) return st;
     KVQ_REQUIRE(dtype == KVQ_F16 || dtype == KVQ_BF16, KVQ_ERR_UNSUPPORTED, "%s: dtype %d", fn, dtype);
     KVQ_REQUIRE(n_tokens >= 0, KVQ_ERR_INVALID_ARG, "%s: n_tokens", fn);
@@ -294,7 +199,7 @@ extern "C" int kv_qk_norm_rope(const kvq_layout* L, const kvq_rope* rope, const 
                 "%s: a token stride below the row's width", fn);
     KVQ_REQUIRE((q_stride | k_stride | v_stride) % 8 == 0, KVQ_ERR_INVALID_ARG, "%s: strides must be multiples of 8",
                 fn);
-    KVQ_REQUIRE(aligned16(q) && aligned16(k) && aligned16(v) && aligned16(q_out) && aligned16(k_out) && aligned16(v_out),
+    KVQ_REQUIRE(kvq_aligned16(q) && kvq_aligned16(k) && kvq_aligned16(v) && kvq_aligned16(q_out) && kvq_aligned16(k_out) && kvq_aligned16(v_out),
                 KVQ_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned", fn);
     // in place only where every row is written where it was read (v in place would be no work at all)
     KVQ_REQUIRE((!q || q != q_out || (dtype == KVQ_F16 && q_stride == wq)) &&

@@ -395,6 +395,16 @@ int kvq_check_layout(const kvq_layout* L, const char* fn, bool need_q) {
     return KVQ_OK;
 }
 
+int kvq_check_latent(const kvq_latent* C, const char* fn) {
+    KVQ_REQUIRE(C != nullptr, KVQ_ERR_INVALID_ARG, "%s: NULL latent layer", fn);
+    KVQ_REQUIRE(C->latent_dim == KVQ_LATENT_DIM && C->rope_dim == KVQ_LATENT_ROPE, KVQ_ERR_UNSUPPORTED,
+                "%s: rows of %d + %d values (512 + 64)", fn, C->latent_dim, C->rope_dim);
+    KVQ_REQUIRE(C->num_blocks > 0 && C->num_blocks <= INT32_MAX, KVQ_ERR_INVALID_ARG, "%s: num_blocks", fn);
+    KVQ_REQUIRE(C->rows != nullptr && ((uintptr_t)C->rows & 15u) == 0, KVQ_ERR_INVALID_ARG,
+                "%s: rows must be 16-byte aligned", fn);
+    return KVQ_OK;
+}
+
 int kvq_check_seqs(const kvq_seqs* S, const char* fn) {
     KVQ_REQUIRE(S != nullptr, KVQ_ERR_INVALID_ARG, "%s: NULL seqs", fn);
     KVQ_REQUIRE(S->batch >= 0 && S->max_blocks >= 0 && S->max_len >= 0, KVQ_ERR_INVALID_ARG, "%s: negative sizes",

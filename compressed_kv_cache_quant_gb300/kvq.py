@@ -11,7 +11,8 @@ Helpers:
   Workspace  -- a zero-filled, 256-byte aligned device buffer;
   Allocator  -- the host page allocator (free list + reference counts);
   RopeTable  -- rotary frequencies on the device (kvq_rope);
-  AttnMod    -- score forms of the new tokens' attention (kvq_attn_mod).
+  AttnMod    -- score forms of the new tokens' attention (kvq_attn_mod);
+  LatentCache -- a latent layer's pages (kvq_latent).
 """
 from __future__ import annotations
 
@@ -20,8 +21,8 @@ import ctypes
 import torch
 
 from . import _abi
-from ._abi import (BITS_E4M3, BLOCK_TOKENS, HEAD_DIM, K_GROUP_TOKENS, V_SYMMETRIC, KvqError, Layout, Pool,  # noqa: F401
-                   Seqs, check, lib)
+from ._abi import (BITS_E4M3, BLOCK_TOKENS, HEAD_DIM, K_GROUP_TOKENS, LATENT_DIM, LATENT_ROPE, TREE_MAX,  # noqa: F401
+                   V_SYMMETRIC, KvqError, Layout, Pool, Seqs, check, lib)
 
 
 def _p(x):
@@ -81,6 +82,16 @@ class LayerCache:
         self.c = Pool(num_blocks, max_seqs, t_cap, _p(self.k_codes), _p(self.v_codes), _p(self.k_sz),
                       _p(self.v_sz), _p(self.k_tail), _p(self.k16), _p(self.v16), _p(self.kT),
                       _p(self.k_absmax))
+
+
+class LatentCache:
+    """Device storage of one latent layer: rows [num_blocks][16][576] fp16 (512 latent values and the 64 of the rotated
+    key part of every token) plus its kvq_latent."""
+
+    def __init__(self, num_blocks, device="cuda"):
+        self.num_blocks = int(num_blocks)
+        self.rows = torch.zeros((self.num_blocks, BLOCK_TOKENS, LATENT_DIM + LATENT_ROPE), dtype=torch.float16, device=device)
+        self.c = _abi.Latent(LATENT_DIM, LATENT_ROPE, self.num_blocks, self.rows.data_ptr())
 
 
 class Batch:
@@ -570,6 +581,150 @@ def kv_chunk_attn(cache, seqs, q, q_starts, max_new, out, ws, mod=None, lse=None
         ctypes.byref(L), ctypes.byref(cache.c), ctypes.byref(seqs.c), _dev(q, torch.float16, shape, gpu, fn, "q"),
         _dev(_need(q_starts, fn, "q_starts"), torch.int32, (B + 1,), gpu, fn, "q_starts"), n, int(max_new),
         _mod(mod, fn, L, B, n, gpu), _dev(_need(out, fn, "out"), torch.float16, shape, gpu, fn, "out"),
+        _dev(lse, torch.float32, (n, H), gpu, fn, "lse"), ws.ptr, ws.nbytes, _raw(stream, gpu)), fn)
+
+
+def kv_rope_append_ws():
+    """Workspace bytes of kv_rope_append and kv_latent_append."""
+    return lib().kv_rope_append_ws()
+
+
+def _dtype_of(x, fn):
+    if x.dtype is torch.float16:
+        return _abi.F16
+    if x.dtype is torch.bfloat16:
+        return _abi.BF16
+    raise KvqError(_abi.KVQ_ERR_UNSUPPORTED, fn, f"{x.dtype}: float16 or bfloat16")
+
+
+def _on(gpu, fn, **parts):
+    """Every part (a RopeTable, a cache, a Batch, a Workspace) has to live on GPU `gpu`."""
+    for name, t in parts.items():
+        if t is not None and t.get_device() != gpu:
+            raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, f"{name} is on {t.device}, not on GPU {gpu}")
+
+
+def kv_rope_append(cache, seqs, rope, row_starts, q, k, v, q_out, ws, positions=None, q_weight=None, k_weight=None,
+                   eps=1e-6, stream=None):
+    """Norms (with a weight) and rotary positions of the new tokens' q [n][H_q][d] and k [n][H_kv][d], fp16 or bf16; k and
+    v go to the pages of an fp16 or E4M3 layer at the last row_starts[b+1] - row_starts[b] places of every sequence,
+    q to q_out (fp16).  q may be None with q_out; `positions` (int32 [n]): other than the places."""
+    fn, L, gpu = "kv_rope_append", cache.layout, _gpu()
+    n, dt = _need(k, fn, "k").shape[0], k.dtype
+    code = _dtype_of(k, fn)
+    if (q is None) != (q_out is None):
+        raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, "q and q_out come together")
+    _on(gpu, fn, rope=rope.steps, cache=cache.v16 if cache.v16 is not None else cache.v_codes, seqs=seqs.seq_lens, ws=ws.t)
+    sq, sk = (n, L.n_q_heads, HEAD_DIM), (n, L.n_kv_heads, HEAD_DIM)
+    qa, qs = _head_rows(q, sq, dt, gpu, fn, "q")
+    ka, ks = _head_rows(k, sk, dt, gpu, fn, "k")
+    va, vs = _head_rows(_need(v, fn, "v"), sk, dt, gpu, fn, "v")
+    return check(lib().kv_rope_append(
+        ctypes.byref(L), ctypes.byref(cache.c), ctypes.byref(seqs.c), ctypes.byref(rope.c), rope.at, rope.mscale, code, n,
+        _dev(_need(row_starts, fn, "row_starts"), torch.int32, (seqs.c.batch + 1,), gpu, fn, "row_starts"),
+        _dev(positions, torch.int32, (n,), gpu, fn, "positions"), qa, qs, ka, ks, va, vs,
+        _dev(q_weight, torch.float32, _ROW, gpu, fn, "q_weight"), _dev(k_weight, torch.float32, _ROW, gpu, fn, "k_weight"),
+        float(eps), _dev(q_out, torch.float16, sq, gpu, fn, "q_out"), ws.ptr, ws.nbytes, _raw(stream, gpu)), fn)
+
+
+def kv_tree_attn_ws(cache, seqs, n_rows, max_new):
+    return lib().kv_tree_attn_ws(_ref(cache.layout), _ref(seqs), int(n_rows), int(max_new))
+
+
+def kv_tree_attn(cache, seqs, q, parents, q_starts, max_new, out, ws, mod=None, lse=None, stream=None):
+    """kv_chunk_attn for trees of drafted tokens: parents (int32 [n_rows]) is every row's parent among its sequence's new
+    tokens, -1 for a root; a node sees the cached tokens, itself and its ancestors."""
+    fn, L, gpu = "kv_tree_attn", cache.layout, _gpu()
+    B, H, n = seqs.c.batch, L.n_q_heads, _need(q, fn, "q").shape[0]
+    shape = (n, H, HEAD_DIM)
+    return check(lib().kv_tree_attn(
+        ctypes.byref(L), ctypes.byref(cache.c), ctypes.byref(seqs.c), _dev(q, torch.float16, shape, gpu, fn, "q"),
+        _dev(_need(parents, fn, "parents"), torch.int32, (n,), gpu, fn, "parents"),
+        _dev(_need(q_starts, fn, "q_starts"), torch.int32, (B + 1,), gpu, fn, "q_starts"), n, int(max_new),
+        _mod(mod, fn, L, B, n, gpu), _dev(_need(out, fn, "out"), torch.float16, shape, gpu, fn, "out"),
+        _dev(lse, torch.float32, (n, H), gpu, fn, "lse"), ws.ptr, ws.nbytes, _raw(stream, gpu)), fn)
+
+
+def _strided(x, shape, dtype, gpu, fn, name):
+    """(address, stride of every dimension but the last) of x, whose last dimension has no gaps."""
+    if not isinstance(x, torch.Tensor) or x.dtype is not dtype or x.shape != shape or x.get_device() != gpu:
+        have = f"{x.dtype} {tuple(x.shape)} on {x.device}" if isinstance(x, torch.Tensor) else type(x).__name__
+        raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, f"{name}: {have} instead of {dtype} {shape} on GPU {gpu}")
+    st = x.stride()
+    if st[-1] != 1:
+        raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, f"{name}: a row's values must lie side by side")
+    # (the stride of a dimension of one entry is never used, and may be anything)
+    return (x.data_ptr(), *(s if n > 1 else 1 << 30 for s, n in zip(st[:-1], shape[:-1])))
+
+
+def kv_latent_append(cache, seqs, rope, row_starts, c, k_rope, ws, c_weight=None, eps=1e-6, positions=None, q=None,
+                     q_out=None, stream=None):
+    """The latent rows of new tokens into a LatentCache: c [n][512] (normed with a weight) and k_rope [n][64] (rotated),
+    fp16 or bf16, at the last row_starts[b+1] - row_starts[b] places of every sequence; q [n][heads][64], the rotated
+    part of the queries, goes to q_out (fp16; slices of wider heads are fine)."""
+    fn, gpu = "kv_latent_append", _gpu()
+    n, dt = _need(c, fn, "c").shape[0], c.dtype
+    code = _dtype_of(c, fn)
+    if (q is None) != (q_out is None):
+        raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, "q and q_out come together")
+    _on(gpu, fn, rope=rope.steps, cache=cache.rows, seqs=seqs.seq_lens, ws=ws.t)
+    ca, cs = _strided(c, (n, LATENT_DIM), dt, gpu, fn, "c")
+    ka, ks = _strided(_need(k_rope, fn, "k_rope"), (n, LATENT_ROPE), dt, gpu, fn, "k_rope")
+    heads, qa, qs, qh, oa, os, oh = 0, None, 0, 0, None, 0, 0
+    if q is not None and n:
+        heads = q.shape[1]
+        qa, qs, qh = _strided(q, (n, heads, LATENT_ROPE), dt, gpu, fn, "q")
+        oa, os, oh = _strided(q_out, (n, heads, LATENT_ROPE), torch.float16, gpu, fn, "q_out")
+    return check(lib().kv_latent_append(
+        ctypes.byref(cache.c), ctypes.byref(seqs.c), ctypes.byref(rope.c), rope.at, rope.mscale, code, n,
+        _dev(_need(row_starts, fn, "row_starts"), torch.int32, (seqs.c.batch + 1,), gpu, fn, "row_starts"),
+        _dev(positions, torch.int32, (n,), gpu, fn, "positions"), ca, cs, ka, ks,
+        _dev(c_weight, torch.float32, (LATENT_DIM,), gpu, fn, "c_weight"), float(eps), heads, qa, qs, qh, oa, os, oh,
+        ws.ptr, ws.nbytes, _raw(stream, gpu)), fn)
+
+
+def kv_latent_attn_ws(seqs, n_heads, n_rows, max_new):
+    return lib().kv_latent_attn_ws(_ref(seqs), int(n_heads), int(n_rows), int(max_new))
+
+
+def kv_latent_attn(cache, seqs, q, q_starts, max_new, out, ws, scale=0.0, parents=None, lse=None, stream=None):
+    """Absorbed attention of the last q_starts[b+1] - q_starts[b] (at most max_new) tokens of every sequence over a
+    LatentCache; q [n_rows][heads][576] and out [n_rows][heads][512] fp16, lse [n_rows][heads] fp32 (optional).
+    scale 0: 1/sqrt(192).  parents: the new tokens are trees, as kv_tree_attn."""
+    fn, gpu = "kv_latent_attn", _gpu()
+    n, H = _need(q, fn, "q").shape[:2]
+    _on(gpu, fn, cache=cache.rows, seqs=seqs.seq_lens, ws=ws.t)
+    return check(lib().kv_latent_attn(
+        ctypes.byref(cache.c), ctypes.byref(seqs.c), H,
+        _dev(q, torch.float16, (n, H, LATENT_DIM + LATENT_ROPE), gpu, fn, "q"),
+        _dev(parents, torch.int32, (n,), gpu, fn, "parents"),
+        _dev(_need(q_starts, fn, "q_starts"), torch.int32, (seqs.c.batch + 1,), gpu, fn, "q_starts"), n, int(max_new),
+        float(scale), _dev(_need(out, fn, "out"), torch.float16, (n, H, LATENT_DIM), gpu, fn, "out"),
+        _dev(lse, torch.float32, (n, H), gpu, fn, "lse"), ws.ptr, ws.nbytes, _raw(stream, gpu)), fn)
+
+
+def kv_latent_expanded_attn_ws(batch, n_heads, n_rows, max_new, max_len):
+    return lib().kv_latent_expanded_attn_ws(int(batch), int(n_heads), int(n_rows), int(max_new), int(max_len))
+
+
+def kv_latent_expanded_attn(q, k_nope, k_rope, v, q_starts, k_starts, max_new, max_len, out, ws, scale=0.0, lse=None,
+                            stream=None):
+    """Causal attention over keys and values expanded from latent rows: q [n_rows][heads][192], k_nope and v
+    [n_keys][heads][128], k_rope [n_keys][64] (shared by the heads), out [n_rows][heads][128], all fp16; k_nope, v and
+    k_rope may be slices of wider rows.  Sequence b has the queries q_starts[b] .. q_starts[b+1] - 1, the last of its
+    tokens k_starts[b] .. k_starts[b+1] - 1.  scale 0: 1/sqrt(192)."""
+    fn, gpu = "kv_latent_expanded_attn", _gpu()
+    n, H = _need(q, fn, "q").shape[:2]
+    m, B = _need(k_nope, fn, "k_nope").shape[0], _need(q_starts, fn, "q_starts").shape[0] - 1
+    _on(gpu, fn, ws=ws.t)
+    na, ns, nh = _strided(k_nope, (m, H, HEAD_DIM), torch.float16, gpu, fn, "k_nope")
+    ra, rs = _strided(_need(k_rope, fn, "k_rope"), (m, LATENT_ROPE), torch.float16, gpu, fn, "k_rope")
+    va, vs, vh = _strided(_need(v, fn, "v"), (m, H, HEAD_DIM), torch.float16, gpu, fn, "v")
+    return check(lib().kv_latent_expanded_attn(
+        B, H, _dev(q, torch.float16, (n, H, HEAD_DIM + LATENT_ROPE), gpu, fn, "q"), na, ns, nh, ra, rs, va, vs, vh, m,
+        _dev(q_starts, torch.int32, (B + 1,), gpu, fn, "q_starts"),
+        _dev(_need(k_starts, fn, "k_starts"), torch.int32, (B + 1,), gpu, fn, "k_starts"), n, int(max_new), int(max_len),
+        float(scale), _dev(_need(out, fn, "out"), torch.float16, (n, H, HEAD_DIM), gpu, fn, "out"),
         _dev(lse, torch.float32, (n, H), gpu, fn, "lse"), ws.ptr, ws.nbytes, _raw(stream, gpu)), fn)
 
 

@@ -12,8 +12,10 @@
  * FP8 E4M3 cache and symmetric V quantization.  Beside that path stand the
  * operators a serving program needs around a cache: head norms with rotary
  * positions, attention of new tokens (a prompt, a chunk, drafted tokens, one
- * token) over an fp16 layer with capped, biased and masked scores, and copies of
- * pages and slots for forks and compaction.
+ * token, a tree of drafts) over an fp16 layer with capped, biased and masked scores,
+ * new tokens written into a cache with the rotation applied on the way, layers
+ * whose heads share one latent row per token, and copies of pages and slots for
+ * forks and compaction.
  *
  * Sources cited below (page, then section):
  *   [TailorKV]  "TailorKV" article, ijyty.com/news/1204784
@@ -769,6 +771,142 @@ int kv_chunk_attn(const kvq_layout* layout, const kvq_pool* pool, const kvq_seqs
                   const kvq_attn_mod* mod, uint16_t* out, float* lse,
                   void* ws, size_t ws_bytes, void* stream);
 size_t kv_chunk_attn_ws(const kvq_layout* layout, const kvq_seqs* seqs, int64_t n_rows, int32_t max_new);
+
+/* ------------------------------------------------------------------------
+ * kv_rope_append -- a run of new tokens per sequence (a prompt, a chunk, drafted
+ * tokens, one token) into an fp16 or E4M3 layer, the head norms and rotary
+ * positions of kv_qk_norm_rope applied on the way; q goes to q_out.
+ * Rows row_starts[b] .. row_starts[b+1] - 1 of q, k and v are the last tokens of
+ * sequence b, in order: seq_lens[b] counts them already, and row r goes to place
+ * seq_lens[b] - n_b + (r - row_starts[b]) of the sequence.  row_starts: device
+ * int32 [batch + 1], ascending, the last at most n_rows; a sequence may have none.
+ * positions: device int32 [n_rows], the rotation's positions, any order and sign
+ * (drafted trees: by depth); NULL: the places.  dtype, q, k, v, strides, weights,
+ * steps, mscale and eps as kv_qk_norm_rope (q with q_out may be NULL; fp32
+ * arithmetic, one rounding from fp32 to the cache's type, E4M3 saturating at
+ * +-448).  q_out: device fp16 [n_rows][H_q][d]; in place only for fp16 q without
+ * gaps.  An fp16 layer with kT and k_absmax has them follow (a second launch over
+ * the rows just written; k_absmax is raised, never lowered).  Pages of the new
+ * tokens must be allocated and not shared.  Rows behind row_starts[batch] and rows
+ * of a sequence whose lengths do not fit (flagged) are left as they were, q_out
+ * included; where a page id is none (flagged) the row's K and V are skipped.
+ * No two sequences may write the same page's rows.  Quantized layers
+ * are written by kv_quant_pack and kv_page_append.
+ * ws: kv_rope_append_ws() bytes (status word only).
+ * Errors: INVALID_ARG, UNSUPPORTED (bits, dtype, rot_dim), CUDA.
+ * ---------------------------------------------------------------------- */
+int kv_rope_append(const kvq_layout* layout, const kvq_pool* pool, const kvq_seqs* seqs, const kvq_rope* rope,
+                   const uint64_t* steps, float mscale, int32_t dtype, int64_t n_rows,
+                   const int32_t* row_starts, const int32_t* positions,
+                   const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                   const void* v, int64_t v_stride, const float* q_weight, const float* k_weight, float eps,
+                   uint16_t* q_out, void* ws, size_t ws_bytes, void* stream);
+size_t kv_rope_append_ws(void);
+
+/* ------------------------------------------------------------------------
+ * kv_tree_attn -- kv_chunk_attn for trees of drafted tokens: the new tokens of
+ * sequence b (at most KVQ_TREE_MAX, in any order that has parents before their
+ * children) are the nodes of one or more trees that hang from its last cached
+ * token.  parents: device int32 [n_rows], for row r the index of its parent among
+ * its sequence's new tokens, or -1 for a root; an entry that is no earlier node is
+ * flagged and taken for -1.
+ * A node sees the cached tokens before the new ones, itself and its ancestors.
+ * Its position is seq_lens[b] - n_b + depth (a root's depth is 0), and window,
+ * sinks, documents and slopes go by positions, a node's as a key included.
+ * mod->prefix_len must be NULL.  Everything else as kv_chunk_attn; max_new is at
+ * most KVQ_TREE_MAX.  The accepted path is appended again in its order
+ * (kv_rope_append of those rows) before the next call, or its rows are moved.
+ * ws: kv_tree_attn_ws(layout, seqs, n_rows, max_new) bytes.
+ * ---------------------------------------------------------------------- */
+#define KVQ_TREE_MAX  256
+
+int kv_tree_attn(const kvq_layout* layout, const kvq_pool* pool, const kvq_seqs* seqs,
+                 const uint16_t* q, const int32_t* parents, const int32_t* q_starts, int64_t n_rows, int32_t max_new,
+                 const kvq_attn_mod* mod, uint16_t* out, float* lse,
+                 void* ws, size_t ws_bytes, void* stream);
+size_t kv_tree_attn_ws(const kvq_layout* layout, const kvq_seqs* seqs, int64_t n_rows, int32_t max_new);
+
+/* ------------------------------------------------------------------------
+ * Latent layers: every token has one row that all heads share, 512 latent values
+ * (the shared low-rank form of its keys and values) and 64 values of a rotated
+ * key part, 1152 bytes of fp16 in 16-token pages.  Attention runs in two forms:
+ *   absorbed  the up-projections are multiplied into the queries and the outputs
+ *             (the caller's products): a row is the key, its first 512 values the
+ *             value of every head.  For few new tokens: bytes of the rows only.
+ *   expanded  the rows are multiplied by the up-projections (the caller's product)
+ *             into 128 key and 128 value dimensions per head.  For prompts: 3.4 times
+ *             fewer operations per pair.
+ * ---------------------------------------------------------------------- */
+#define KVQ_LATENT_DIM   512
+#define KVQ_LATENT_ROPE  64
+
+typedef struct kvq_latent {
+    int32_t   latent_dim;   /* must be 512 */
+    int32_t   rope_dim;     /* must be 64 */
+    int64_t   num_blocks;
+    uint16_t* rows;         /* device fp16 [num_blocks][16][576], 16-byte aligned */
+} kvq_latent;
+
+/* kv_latent_append -- the rows of new tokens into a latent layer's pages, and the
+ * rotated part of their queries.  c: [n_rows][512] (`c_stride` elements between
+ * tokens), RMS-normed with c_weight (device fp32 [512], 16-byte aligned; NULL: no norm) and eps; k_rope: [n_rows][64],
+ * rotated at the row's position; both dtype, rounded once to fp16.  rope: rot_dim
+ * must be 64.  q (optional): [n_rows][n_heads][64] with strides between tokens and
+ * heads (a slice of wider query heads), rotated into q_out, fp16, with strides of
+ * its own (the last 64 values of absorbed query heads of 576, or of heads of 192);
+ * in place only for fp16 with one set of strides; otherwise outputs overlap no
+ * input.  Rows, row_starts, positions and what is skipped as kv_rope_append.
+ * Strides are multiples of 8, rows 16-byte aligned.
+ * ws: kv_rope_append_ws() bytes.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int kv_latent_append(const kvq_latent* cache, const kvq_seqs* seqs, const kvq_rope* rope, const uint64_t* steps,
+                     float mscale, int32_t dtype, int64_t n_rows, const int32_t* row_starts, const int32_t* positions,
+                     const void* c, int64_t c_stride, const void* k_rope, int64_t k_stride,
+                     const float* c_weight, float eps,
+                     int32_t n_heads, const void* q, int64_t q_stride, int64_t q_head_stride,
+                     uint16_t* q_out, int64_t q_out_stride, int64_t q_out_head_stride,
+                     void* ws, size_t ws_bytes, void* stream);
+
+/* kv_latent_attn -- absorbed attention of a run of new tokens per sequence (one
+ * token, drafted tokens; with parents a tree of them, as kv_tree_attn) over a
+ * latent layer.  q: device fp16 [n_rows][n_heads][576], out: device fp16
+ * [n_rows][n_heads][512] (the weighted sum of the rows' latent values), lse
+ * (optional): device fp32 [n_rows][n_heads].  Score: scale * q.row (scale 0:
+ * 1/sqrt(192)); causal, q_starts, n_rows and max_new as kv_chunk_attn, parents
+ * (NULL: a chain) and then max_new <= KVQ_TREE_MAX as kv_tree_attn.  Any n_heads
+ * from 1 to 65536.  Exact fp16 products and fp32 sums; weights enter the value
+ * product in fp16, off by 2^-11 of themselves or by 2^-32 of the largest weight of
+ * the row (of one part, where the cache is split).  Results do not depend on the
+ * run.  A sequence's own rows must be finite; rows behind seq_lens[b] may hold
+ * anything; pages behind it are not read.  num_blocks * 16 < 2^31.  q, out 16-byte aligned.
+ * ws: kv_latent_attn_ws(seqs, n_heads, n_rows, max_new) bytes. */
+int kv_latent_attn(const kvq_latent* cache, const kvq_seqs* seqs, int32_t n_heads, const uint16_t* q,
+                   const int32_t* parents, const int32_t* q_starts, int64_t n_rows, int32_t max_new, float scale,
+                   uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+size_t kv_latent_attn_ws(const kvq_seqs* seqs, int32_t n_heads, int64_t n_rows, int32_t max_new);
+
+/* kv_latent_expanded_attn -- causal attention of a run of new tokens per sequence
+ * over keys and values that the caller expanded from latent rows.  The last
+ * q_starts[b+1] - q_starts[b] (at most max_new) of the k_starts[b+1] - k_starts[b]
+ * (at most max_len) tokens of sequence b are its queries.  q: device fp16
+ * [n_rows][n_heads][192], 128 values against k_nope, then 64 against k_rope.
+ * k_nope, v: device fp16 [n_keys][n_heads][128], k_rope: device fp16 [n_keys][64],
+ * which all heads share; kn_stride, v_stride, kr_stride elements between tokens and
+ * kn_head_stride, v_head_stride between heads (multiples of 8; so k_nope and v are
+ * slices of one product's rows, k_rope of gathered latent rows).  out: device
+ * fp16 [n_rows][n_heads][128]; lse (optional): device fp32 [n_rows][n_heads].
+ * scale 0: 1/sqrt(192).  q_starts, k_starts: device int32 [batch + 1], ascending.
+ * Rows behind q_starts[batch] are left as they were.  Precision as kv_latent_attn.
+ * All K and V rows of a sequence must be finite; what lies outside the sequences may
+ * hold anything.  16-byte aligned.  n_keys < 2^31.
+ * ws: kv_latent_expanded_attn_ws(batch, n_heads, n_rows, max_new, max_len) bytes. */
+int kv_latent_expanded_attn(int32_t batch, int32_t n_heads, const uint16_t* q,
+                            const uint16_t* k_nope, int64_t kn_stride, int64_t kn_head_stride,
+                            const uint16_t* k_rope, int64_t kr_stride,
+                            const uint16_t* v, int64_t v_stride, int64_t v_head_stride, int64_t n_keys,
+                            const int32_t* q_starts, const int32_t* k_starts, int64_t n_rows, int32_t max_new,
+                            int32_t max_len, float scale, uint16_t* out, float* lse,
+                            void* ws, size_t ws_bytes, void* stream);
+size_t kv_latent_expanded_attn_ws(int32_t batch, int32_t n_heads, int64_t n_rows, int32_t max_new, int32_t max_len);
 
 /* ------------------------------------------------------------------------
  * kv_pages_copy -- kv_page_copy for a list of pages in one launch: every array
