@@ -32,13 +32,11 @@
 // a tile's softmax takes 1250 (128 exponentials per row, 4-5 cycles each per warp), then its 768 last cycles
 // of products and some 300 of signals close its chain, and the issuing warp spends 100 cycles on every wait,
 // ready or not.
-#include <cuda.h>
-
 #include <algorithm>
-#include <atomic>
 #include <type_traits>
 
 #include "kvq_attn_mod.cuh"
+#include "kvq_tc.cuh"
 #include "kvq_tree.cuh"
 
 namespace {
@@ -52,13 +50,13 @@ constexpr int CA_NS = 4;                 // K or V tiles in the ring
 constexpr int CA_TILE = 128 * D * 2;     // bytes of a Q, K or V tile
 constexpr int CA_HALF = CA_TILE / 2;     // a Q tile is two halves of 128 rows x 128 bytes
 constexpr int CA_SMEM = 2 * CA_TILE + CA_NS * CA_TILE + 1024;
-constexpr uint32_t CA_SPIN = 1u << 16;   // bound on the polls of one mbarrier wait
 constexpr float CA_HEAD = 7.0f;          // log2 of a row's largest weight when its anchor is set
 constexpr float CA_TOP = 15.99f;         // log2 of the largest weight before the anchor is set anew (fp16 ends at 2^16)
 constexpr float CA_FAR = 1048576.0f;     // scores (log2) beyond which they are rounded before the anchor is taken off
 
 // TMEM columns: S (and P over it) of the two tiles, then their O
 constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
+constexpr uint32_t IDESC_QK = idesc_f16(128, 128), IDESC_PV = IDESC_QK | KVQ_B_MN;   // (V's rows run along K)
 
 struct ChunkArgs {
     const int32_t *bt, *seq_lens, *q_starts;
@@ -75,157 +73,6 @@ struct ChunkArgs {
     KvqWsHeader* hdr;
 };
 
-// ---------------------------------------------------------------- PTX
-
-__device__ __forceinline__ uint32_t saddr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t n) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(saddr(bar)), "r"(n) : "memory");
-}
-__device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(saddr(bar)), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void bar_arrive(uint64_t* bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(bar)) : "memory");
-}
-// a page of one kv head: the map's dims are 64 values, 8 rows, 2 halves of a row, groups of 8 rows
-__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, int group, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], "
-        "[%4];" ::"r"(dst),
-        "l"(map), "r"(0), "r"(group), "r"(saddr(bar))
-        : "memory");
-}
-__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-        "[%5];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(saddr(bar))
-        : "memory");
-}
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(saddr(bar)) : "memory");
-}
-// true in one lane of a converged warp
-__device__ __forceinline__ bool elect() {
-    uint32_t one;
-    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(one));
-    return one != 0;
-}
-__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// Shared-memory matrix descriptor, 128-byte swizzle: start address, byte offsets between the 64-element
-// blocks of a matrix whose rows run along K (`lead`), and between groups of eight rows (`group`).
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t group) {
-    return (uint64_t)((addr & 0x3ffff) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(group >> 4) << 32) |
-           (1ull << 46) | (2ull << 61);
-}
-// f16 x f16 -> f32, M = 128, N = 128; bit 16: B's rows run along K (V), else along N (K)
-constexpr uint32_t IDESC_QK = (1u << 4) | (128u / 8 << 17) | (128u / 16 << 24);
-constexpr uint32_t IDESC_PV = IDESC_QK | (1u << 16);
-
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
-    asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
-        : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
-    asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
-        : "memory");
-}
-
-#define R8(v, o) "=r"((v)[o]), "=r"((v)[o + 1]), "=r"((v)[o + 2]), "=r"((v)[o + 3]), "=r"((v)[o + 4]), "=r"((v)[o + 5]), "=r"((v)[o + 6]), "=r"((v)[o + 7])
-#define W8(v, o) "r"((v)[o]), "r"((v)[o + 1]), "r"((v)[o + 2]), "r"((v)[o + 3]), "r"((v)[o + 4]), "r"((v)[o + 5]), "r"((v)[o + 6]), "r"((v)[o + 7])
-// 32 columns of this thread's lane; the wait is part of the statement, so nothing reads v before it
-__device__ __forceinline__ void tm_ld32(uint32_t addr, uint32_t* v) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-        "tcgen05.wait::ld.sync.aligned;"
-        : R8(v, 0), R8(v, 8), R8(v, 16), R8(v, 24)
-        : "r"(addr)
-        : "memory");
-}
-// all 128 columns of a score tile
-__device__ __forceinline__ void tm_ld128(uint32_t addr, uint32_t* v) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x128.b32 {"
-        "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
-        "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
-        "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63,"
-        "%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,"
-        "%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95,"
-        "%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,"
-        "%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%128];\n"
-        "tcgen05.wait::ld.sync.aligned;"
-        : R8(v, 0), R8(v, 8), R8(v, 16), R8(v, 24), R8(v, 32), R8(v, 40), R8(v, 48), R8(v, 56), R8(v, 64), R8(v, 72), R8(v, 80),
-          R8(v, 88), R8(v, 96), R8(v, 104), R8(v, 112), R8(v, 120)
-        : "r"(addr)
-        : "memory");
-}
-__device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t* v) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-        W8(v, 0), W8(v, 8), W8(v, 16), W8(v, 24)
-        : "memory");
-}
-__device__ __forceinline__ void tm_st1(uint32_t addr, uint32_t v) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(addr), "r"(v) : "memory");
-}
-__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-// two fp32 values per instruction
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpair(uint64_t x, float* lo, float* hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(x));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ float rcp(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // ---------------------------------------------------------------- what a CTA works on
 
 struct Shared {
@@ -236,35 +83,6 @@ struct Shared {
     int32_t doc_min, sink_max, lo_min, hi_max;    // over its rows
     int4 see[CA_ROWS];                            // lo, hi, doc, sink of every token
 };
-
-__device__ __forceinline__ bool bar_done(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-// Waits for a phase of bar.  After CA_SPIN polls it flags the timeout, and every wait of the CTA that is
-// not over by then returns at once: the roles run through to their ends without waiting, on data that is
-// not valid, so no step needs a branch for the failure; only the loads stop (a barrier must not be armed
-// twice).  Most waits of the issuing warps find their phase done: one poll and nothing else.
-__device__ __forceinline__ void bar_wait(Shared& S, KvqWsHeader* hdr, uint64_t* bar, uint32_t parity) {
-    const uint32_t at = saddr(bar);
-    for (uint32_t it = 0; !bar_done(at, parity); ++it) {
-        if ((it & 63) != 63) continue;
-        if (*(volatile int32_t*)&S.abort) return;
-        if (it > CA_SPIN) {
-            *(volatile int32_t*)&S.abort = 1;
-            kvq_dev_flag(hdr, KVQ_DEV_TIMEOUT, (int32_t)blockIdx.x);
-            return;
-        }
-    }
-}
-__device__ __forceinline__ bool aborted(Shared& S) {
-    return __any_sync(0xffffffffu, *(volatile int32_t*)&S.abort != 0);
-}
 
 // Sequence b's new tokens: *first row and count; false (flagged) when its lengths do not fit the call.
 __device__ __forceinline__ bool seq_rows(const ChunkArgs& a, int b, int* first, int* n) {
@@ -469,8 +287,8 @@ __global__ void __launch_bounds__(CA_NT, 1)
             // the same, at 79 cycles each
             const auto fetch = [&](int slot, const CUtensorMap* map, const int* at) {
                 const int st = slot % CA_NS;
-                if (slot >= CA_NS) bar_wait(S, a.hdr, &S.kv_empty[st], ((slot / CA_NS) & 1) ^ 1);
-                const bool ok = !aborted(S);
+                if (slot >= CA_NS) bar_wait(&S.abort, a.hdr, &S.kv_empty[st], ((slot / CA_NS) & 1) ^ 1);
+                const bool ok = !aborted(&S.abort);
                 if (ok && elect()) {
                     bar_expect(&S.kv_full[st], CA_TILE);
 #pragma unroll
@@ -524,8 +342,8 @@ __global__ void __launch_bounds__(CA_NT, 1)
             const auto commit = [&](uint64_t* bar) {
                 if (elect()) tc_commit(bar);
             };
-            bar_wait(S, a.hdr, &S.q_full, 0);
-            bar_wait(S, a.hdr, &S.kv_full[0], 0);
+            bar_wait(&S.abort, a.hdr, &S.q_full, 0);
+            bar_wait(&S.abort, a.hdr, &S.kv_full[0], 0);
             tc_after();
             qk(0, 0);
             if (nq > 1) qk(1, 0);
@@ -536,15 +354,15 @@ __global__ void __launch_bounds__(CA_NT, 1)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     if (i == nq) break;
-                    bar_wait(S, a.hdr, &S.p_full[i][0], j & 1);
+                    bar_wait(&S.abort, a.hdr, &S.p_full[i][0], j & 1);
                     tc_after();
                     pv(i, sv, 0, j > 0);
-                    bar_wait(S, a.hdr, &S.p_full[i][1], j & 1);
+                    bar_wait(&S.abort, a.hdr, &S.p_full[i][1], j & 1);
                     tc_after();
                     pv(i, sv, 1, true);
                     if (i == nq - 1) commit(&S.kv_empty[sv]);
                     if (more) {
-                        if (i == 0) bar_wait(S, a.hdr, &S.kv_full[sk], ((2 * j + 2) / CA_NS) & 1);
+                        if (i == 0) bar_wait(&S.abort, a.hdr, &S.kv_full[sk], ((2 * j + 2) / CA_NS) & 1);
                         qk(i, sk);
                     } else {
                         commit(&S.o_full[i]);
@@ -586,12 +404,12 @@ __global__ void __launch_bounds__(CA_NT, 1)
                 const int t0 = tile_of(it0 + j) * CA_KEYS;
                 // rows at and behind T may hold anything: 0 * NaN must not reach O
                 const bool tail = T < t0 + CA_KEYS && (T & (PG - 1)) != 0 && T > t0;
-                bar_wait(S, a.hdr, &S.s_full[i], j & 1);
+                bar_wait(&S.abort, a.hdr, &S.s_full[i], j & 1);
                 // tile 0's weights stand for V's arrival too (its products are issued after these waits, and tile
                 // 1's after tile 0's): the issuing warp is the busier one.  1.38 -> 1.36 ms for the prompt
-                if (i == 0) bar_wait(S, a.hdr, &S.kv_full[(2 * j + 1) % CA_NS], ((2 * j + 1) / CA_NS) & 1);
+                if (i == 0) bar_wait(&S.abort, a.hdr, &S.kv_full[(2 * j + 1) % CA_NS], ((2 * j + 1) / CA_NS) & 1);
                 if (tail) {
-                    bar_wait(S, a.hdr, &S.kv_full[(2 * j + 1) % CA_NS], ((2 * j + 1) / CA_NS) & 1);
+                    bar_wait(&S.abort, a.hdr, &S.kv_full[(2 * j + 1) % CA_NS], ((2 * j + 1) / CA_NS) & 1);
                     const uint32_t base = skv + (2 * j + 1) % CA_NS * CA_TILE;
                     const int r0 = T - t0, r1 = (r0 + PG - 1) / PG * PG;
                     for (int x = tid & 127; x < (r1 - r0) * 16; x += 128) {
@@ -807,8 +625,8 @@ __global__ void __launch_bounds__(CA_NT, 1)
                 l += l0 + l1;
             }
             // ---- this row's output
-            if (nt > 0) bar_wait(S, a.hdr, &S.o_full[i], 0);
-            if (!aborted(S)) {
+            if (nt > 0) bar_wait(&S.abort, a.hdr, &S.o_full[i], 0);
+            if (!aborted(&S.abort)) {
                 tc_after();
                 const int64_t out_row = (int64_t)(first + tok0 + tok) * a.H * GQ + h * GQ + r % GQ;
                 const int64_t part_row = (((int64_t)item * a.H + h) * a.n_splits + split) * CA_ROWS + r;
@@ -847,14 +665,7 @@ __global__ void __launch_bounds__(CA_NT, 1)
     __syncwarp();
     __syncthreads();
     if (*(volatile int32_t*)&S.abort) {
-        // a wait gave up: let this CTA's own copies and products land (again with a limit) before it ends
-        if (warp == 8 && lane == 0) {
-            tc_commit(&S.drain);
-            for (uint32_t it = 0; it < CA_SPIN && !bar_done(saddr(&S.drain), 0); ++it) {}
-        }
-        const long long began = clock64();
-        while (clock64() - began < 2000000) __nanosleep(1000);  // about a millisecond: far above a copy's time
-        __syncthreads();
+        drain_after_abort(warp == 8 && lane == 0, &S.drain);
     }
     tc_before();
     __syncthreads();
@@ -966,40 +777,6 @@ ChunkPlan chunk_plan(const kvq_layout* L, const kvq_seqs* S, int64_t n_rows, int
     p.off_part = kvq_round_up(p.off_ml + rows * sizeof(float2), 256);
     p.bytes = kvq_round_up(p.off_part + rows * D * sizeof(float), 256);
     return p;
-}
-
-// A tensor map of fp16 values in boxes whose innermost extent is 64 values, 128-byte swizzle.
-int make_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
-             const char* fn) {
-    using Encode = decltype(&cuTensorMapEncodeTiled);
-    static std::atomic<Encode> found_encode{nullptr};   // (threads that make the first call together each look it up)
-    Encode encode = found_encode.load(std::memory_order_relaxed);
-    if (encode == nullptr) {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
-        if (e != cudaSuccess || found != cudaDriverEntryPointSuccess || f == nullptr) {
-            cudaGetLastError();
-            return kvq_fail(KVQ_ERR_CUDA, "%s: the driver has no cuTensorMapEncodeTiled", fn);
-        }
-        encode = reinterpret_cast<Encode>(f);
-        found_encode.store(encode, std::memory_order_relaxed);
-    }
-    const cuuint32_t ones[4] = {1, 1, 1, 1};
-    const auto fill = [&] {
-        return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, const_cast<void*>(base),
-                      reinterpret_cast<const cuuint64_t*>(dims), reinterpret_cast<const cuuint64_t*>(strides), box, ones,
-                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    };
-    CUresult r = fill();
-    if (r == CUDA_ERROR_INVALID_CONTEXT) {
-        // the thread has made no runtime call yet that makes its device's context current, as a launch would
-        int dev = 0;
-        if (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = fill();
-    }
-    if (r != CUDA_SUCCESS) return kvq_fail(KVQ_ERR_CUDA, "%s: tensor map (%d)", fn, (int)r);
-    return KVQ_OK;
 }
 
 }  // namespace

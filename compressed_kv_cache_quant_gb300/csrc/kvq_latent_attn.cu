@@ -1,0 +1,646 @@
+// kv_latent_attn: absorbed attention over a latent layer, whose rows (576 values of fp16 per token) are the keys, and
+// their first 512 values the values, of every head.
+//
+// Bound: the bytes of the rows for few query rows (1152 bytes and 2176 flops per query row and token), the tensor
+// cores from some 100 query rows per sequence on.  Query rows are (new token, head) pairs, side by side in memory; a
+// CTA takes up to 64 of one sequence and a range of its tokens in steps of 64, four pages, each fetched through the
+// block table by one TMA box: groups of eight rows, a group's nine chunks of 64 values behind one another, 128-byte
+// swizzle.  The same staged rows serve both products:
+//
+//   S   = Q K^T      64 rows x 64 tokens    A = Q, B = the rows along their 576 values
+//   O^T = V^T P^T    512 values x rows      A = the rows' first 512 values in four blocks of 128, B = P
+//
+// O transposed, because 64 rows of 512 values would fill all of TMEM (M = 64 uses half of its lanes) and leave no
+// place for S; as O^T they take 256 columns, and for few rows the second product shrinks with them.
+//
+//   warps 0-3  softmax: warp w has rows 16w .. 16w + 15, a lane per row (M = 64 puts them there); then the output
+//   warp 4     issues tcgen05.mma: S of the next step before O^T of this one
+//   warp 5     loads
+//
+// The steps of all sequences and row groups are one list, cut into equal ranges, one per SM: a CTA works through its
+// range segment by segment, and a second launch joins the row groups that a cut runs through.  Weights are taken
+// against an anchor per row as in kv_chunk_attn: 2^7 below the row's maximum when it is set, set anew (O^T's column
+// rescaled) when a weight would pass 2^15.99.
+#include <algorithm>
+#include <cmath>
+
+#include "kvq_attn_mod.cuh"
+#include "kvq_latent.cuh"
+#include "kvq_tc.cuh"
+#include "kvq_tree.cuh"
+
+namespace {
+
+constexpr int PG = KVQ_BLOCK_TOKENS;
+constexpr int LAT = KVQ_LATENT_DIM, ROT = KVQ_LATENT_ROPE, ROW = LAT + ROT;
+constexpr int LA_NT = 192;
+constexpr int LA_ROWS = 64;               // query rows per CTA
+constexpr int LA_KEYS = 64;               // tokens per step
+constexpr int LA_NS = 2;                  // stages
+constexpr int LA_CHUNKS = ROW / 64;
+constexpr int LA_GROUP = LA_CHUNKS * 1024;              // bytes of eight staged rows
+constexpr int LA_STAGE = LA_KEYS / 8 * LA_GROUP;
+constexpr float LA_HEAD = 7.0f;           // log2 of a row's largest weight when its anchor is set
+constexpr float LA_TOP = 15.99f;          // log2 of the largest weight before the anchor is set anew
+constexpr uint32_t TM_O = 0, TM_S = 256, TM_COLS = 512;   // TMEM columns: four blocks of O^T, two S
+
+struct LatArgs {
+    const int32_t *bt, *seq_lens, *q_starts, *parents;
+    int64_t n_rows, num_blocks;
+    int32_t batch, max_blocks, max_len, max_new, H, nr;   // nr: rows per CTA as the products see them, a multiple of 16
+    float scale2;                                         // of a score, in log2 units
+    uint16_t* out;
+    float* lse;
+    float* part;   // [slot][nr][LAT]
+    float2* ml;    // [slot][nr] anchor (log2) and sum
+    KvqWsHeader* hdr;
+};
+
+// ---------------------------------------------------------------- the list of steps
+
+struct Seq {
+    int32_t first, n, T;   // first row of the call, new tokens, tokens
+    int32_t groups, steps; // of 64 query rows; of tokens, per group
+};
+
+__device__ __forceinline__ Seq seq_at(const LatArgs& a, int b) {
+    Seq s = {0, 0, 0, 0, 0};
+    const int first = a.q_starts[b], T = a.seq_lens[b];
+    const int64_t cnt = (int64_t)a.q_starts[b + 1] - first;
+    if (first < 0 || cnt < 0 || cnt > a.max_new || first + cnt > a.n_rows || T < cnt || T > a.max_len) {
+        kvq_dev_flag(a.hdr, KVQ_DEV_BAD_LENGTH, b);
+        return s;
+    }
+    s.first = first, s.n = (int)cnt, s.T = T;
+    s.groups = (int)((cnt * a.H + a.nr - 1) / a.nr);
+    s.steps = s.groups > 0 ? (T + LA_KEYS - 1) / LA_KEYS : 0;
+    return s;
+}
+
+// One warp: steps of the whole call.
+__device__ __forceinline__ int64_t all_steps(const LatArgs& a) {
+    int64_t sum = 0;
+    for (int b = threadIdx.x & 31; b < a.batch; b += 32) {
+        const Seq s = seq_at(a, b);
+        sum += (int64_t)s.groups * s.steps;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+}
+
+// One warp: the sequence of the x-th entry of a list of `per(sequence)` entries each, the entries before it, and
+// the steps before it; -1 behind the end.
+template <typename Per>
+__device__ __forceinline__ int find_seq(const LatArgs& a, int64_t x, Per per, int64_t* before, int64_t* steps_before) {
+    const int lane = threadIdx.x & 31;
+    int64_t base = 0, base_steps = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+        const Seq s = b0 + lane < a.batch ? seq_at(a, b0 + lane) : Seq{0, 0, 0, 0, 0};
+        const int64_t mine = per(s), steps = (int64_t)s.groups * s.steps;
+        int64_t incl = mine, incl_steps = steps;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t u = __shfl_up_sync(0xffffffffu, incl, o), v = __shfl_up_sync(0xffffffffu, incl_steps, o);
+            if (lane >= o) incl += u, incl_steps += v;
+        }
+        const unsigned who = __ballot_sync(0xffffffffu, x >= base + incl - mine && x < base + incl);
+        if (who) {
+            const int src = __ffs(who) - 1;
+            *before = __shfl_sync(0xffffffffu, base + incl - mine, src);
+            *steps_before = __shfl_sync(0xffffffffu, base_steps + incl_steps - steps, src);
+            return b0 + src;
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+        base_steps += __shfl_sync(0xffffffffu, incl_steps, 31);
+    }
+    return -1;
+}
+
+// A CTA's range, segment by segment: `cnt` steps of one row group from `step` on.
+struct Segment {
+    int64_t left;      // steps of the range from this segment on
+    int32_t b, group, step, cnt;
+    Seq s;
+    __device__ __forceinline__ void clip() { cnt = (int)min(left, (int64_t)(s.steps - step)); }
+    __device__ __forceinline__ bool next(const LatArgs& a) {
+        left -= cnt;
+        if (left <= 0) return false;
+        step = 0;
+        if (++group == s.groups) {
+            group = 0;
+            do {
+                if (++b >= a.batch) return false;
+                s = seq_at(a, b);
+            } while (s.steps == 0);
+        }
+        clip();
+        return true;
+    }
+    // tokens that some row of the group sees, and steps of the segment that hold any
+    __device__ __forceinline__ int end(const LatArgs& a) const {
+        if (a.parents != nullptr) return s.T;
+        const int64_t last = min((int64_t)s.n * a.H, (int64_t)(group + 1) * a.nr) - 1;
+        return s.T - s.n + (int)(last / a.H) + 1;
+    }
+    __device__ __forceinline__ int steps(const LatArgs& a) const {
+        return max(0, min(cnt, (end(a) + LA_KEYS - 1) / LA_KEYS - step));
+    }
+};
+
+struct Shared {
+    uint64_t q_full, q_free, kv_full[LA_NS], kv_empty[LA_NS], s_full[2], p_full, pv_done[2], drain;
+    uint32_t tmem;
+    int32_t abort;
+    Segment seg;
+    float factor[LA_ROWS];
+};
+
+__device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
+
+// one barrier of the softmax warps; true when some thread's x is
+__device__ __forceinline__ bool sm_any(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.or.pred q, 1, 128, p;\nselp.u32 %0, 1, 0, q;\n}"
+        : "=r"(r)
+        : "r"((uint32_t)x)
+        : "memory");
+    return r != 0;
+}
+
+__global__ void __launch_bounds__(LA_NT, 1)
+    latent_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_rows,
+                       const __grid_constant__ LatArgs a) {
+    extern __shared__ unsigned char raw[];
+    __shared__ Shared S;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // queries, stages, weights: with nr below 64 the first product reads behind the queries, into the stages, for
+    // rows of S that nothing looks at
+    const uint32_t sq = (saddr(raw) + 1023) & ~1023u, skv = sq + a.nr * ROW * 2, sp = skv + LA_NS * LA_STAGE;
+    kvq_pdl_begin();
+    if (warp == 0) {
+        const int64_t total = all_steps(a);
+        const int64_t per = latent_range(total, gridDim.x), x = per * blockIdx.x;
+        int64_t before, steps_before;
+        Segment g = {0, -1, 0, 0, 0, {0, 0, 0, 0, 0}};
+        if (x < total) {
+            g.b = find_seq(a, x, [](const Seq& s) { return (int64_t)s.groups * s.steps; }, &before, &steps_before);
+            g.s = seq_at(a, g.b);
+            g.group = (int)((x - before) / g.s.steps);
+            g.step = (int)((x - before) % g.s.steps);
+            g.left = min(per, total - x);
+            g.clip();
+        }
+        if (lane == 0) S.seg = g, S.abort = 0;
+    }
+    if (tid == 32) {
+        bar_init(&S.q_full, 1);
+        bar_init(&S.q_free, 1);
+        for (int i = 0; i < LA_NS; ++i) {
+            bar_init(&S.kv_full[i], 1);
+            bar_init(&S.kv_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&S.s_full[i], 1);
+            bar_init(&S.pv_done[i], 1);
+        }
+        bar_init(&S.p_full, 4);
+        bar_init(&S.drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    Segment g = S.seg;
+    if (g.b < 0) return;   // no work
+    if (warp == 4) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&S.tmem)), "r"(TM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = S.tmem;
+
+    if (warp == 5) {
+        // ---- loads
+        const int nowhere = (int)(a.num_blocks * (PG / 8));   // a group of rows behind the pool: zeros
+        int at = 0;        // steps so far
+        bool ok = true;
+        for (int seg = 0; ok; ++seg) {
+            const int nt = g.steps(a), end = g.end(a);
+            if (nt > 0) {
+                if (seg > 0) bar_wait(&S.abort, a.hdr, &S.q_free, (seg - 1) & 1);
+                ok = !aborted(&S.abort);
+                if (ok && elect()) {
+                    bar_expect(&S.q_full, a.nr * ROW * 2);
+                    tma_3d(sq, &map_q, 0, (int)((int64_t)g.s.first * a.H + (int64_t)g.group * a.nr), 0, &S.q_full);
+                }
+                __syncwarp();
+            } else {
+                --seg;     // (no queries are loaded for it)
+            }
+            for (int j = 0; j < nt && ok; ++j, ++at) {
+                const int st = at % LA_NS, t0 = (g.step + j) * LA_KEYS;
+                const int pages = min(LA_KEYS / PG, (end - t0 + PG - 1) / PG);
+                int y = nowhere;
+                if (lane < pages) {
+                    const int32_t page = a.bt[(int64_t)g.b * a.max_blocks + t0 / PG + lane];
+                    if (page >= 0 && page < a.num_blocks)
+                        y = page * (PG / 8);
+                    else
+                        kvq_dev_flag(a.hdr, KVQ_DEV_BAD_PAGE, page);
+                }
+                if (at >= LA_NS) bar_wait(&S.abort, a.hdr, &S.kv_empty[st], ((at / LA_NS) & 1) ^ 1);
+                ok = !aborted(&S.abort);
+                int to[LA_KEYS / PG];
+#pragma unroll
+                for (int k = 0; k < LA_KEYS / PG; ++k) to[k] = __shfl_sync(0xffffffffu, y, k);
+                if (ok && elect()) {
+                    bar_expect(&S.kv_full[st], pages * PG * ROW * 2);
+#pragma unroll
+                    for (int k = 0; k < LA_KEYS / PG; ++k)
+                        if (k < pages) tma_page(skv + st * LA_STAGE + k * (PG * ROW * 2), &map_rows, to[k], &S.kv_full[st]);
+                }
+                __syncwarp();
+            }
+            if (!g.next(a)) break;
+        }
+    } else if (warp == 4) {
+        // ---- tensor cores: the whole warp walks the loop and one elected lane issues
+        const uint32_t hi_q = (uint32_t)(smem_desc(0, 16, 1024) >> 32), hi_kv = (uint32_t)(smem_desc(0, 16, LA_GROUP) >> 32);
+        const uint32_t lq = (uint32_t)smem_desc(sq, 16, 0), lk = (uint32_t)smem_desc(skv, 16, 0),
+                       lv = (uint32_t)smem_desc(skv, 1024, 0), lp = (uint32_t)smem_desc(sp, 16, 0);
+        const uint32_t idesc_s = idesc_f16(64, LA_KEYS), idesc_o = idesc_f16(128, a.nr) | KVQ_A_MN;
+        const auto desc = [](uint32_t hi, uint32_t lo) { return (uint64_t)hi << 32 | lo; };
+        const uint32_t q_chunk = (uint32_t)a.nr * 128 >> 4;
+        const auto qk = [&](int at) {
+            if (elect()) {
+                uint32_t x = lq, y = lk + (at % LA_NS * LA_STAGE >> 4);
+                asm volatile("" : "+r"(x), "+r"(y));
+#pragma unroll
+                for (int c = 0; c < LA_CHUNKS; ++c) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_ss(TM_S + (at & 1) * LA_KEYS, desc(hi_q, x + 2 * k), desc(hi_kv, y + (c * 1024 >> 4) + 2 * k), idesc_s,
+                               c + k > 0);
+                    x += q_chunk;
+                }
+                tc_commit(&S.s_full[at & 1]);
+            }
+        };
+        int at = 0;
+        for (int seg = 0;; ++seg) {
+            const int nt = g.steps(a);
+            if (nt > 0) {
+                bar_wait(&S.abort, a.hdr, &S.q_full, seg & 1);
+                bar_wait(&S.abort, a.hdr, &S.kv_full[at % LA_NS], (at / LA_NS) & 1);
+                tc_after();
+                qk(at);
+            } else {
+                --seg;
+            }
+            for (int j = 0; j < nt; ++j, ++at) {
+                if (j + 1 < nt) {
+                    bar_wait(&S.abort, a.hdr, &S.kv_full[(at + 1) % LA_NS], ((at + 1) / LA_NS) & 1);
+                    qk(at + 1);
+                } else if (elect()) {
+                    tc_commit(&S.q_free);
+                }
+                bar_wait(&S.abort, a.hdr, &S.p_full, at & 1);
+                tc_after();
+                if (elect()) {
+                    uint32_t y = lv + (at % LA_NS * LA_STAGE >> 4);
+                    asm volatile("" : "+r"(y));
+#pragma unroll
+                    for (int d = 0; d < LAT / 128; ++d)
+#pragma unroll
+                        for (int k = 0; k < LA_KEYS / 16; ++k)
+                            mma_ss(TM_O + 64 * d, desc(hi_kv, y + ((k * 2 * LA_GROUP + d * 2048) >> 4)), desc(hi_q, lp + 2 * k), idesc_o,
+                                   j > 0 || k > 0);
+                    tc_commit(&S.kv_empty[at % LA_NS]);
+                    tc_commit(&S.pv_done[at & 1]);
+                }
+            }
+            if (!g.next(a)) break;
+        }
+    } else {
+        // ---- softmax: a lane per row
+        const uint32_t lane_base = tmem + ((uint32_t)warp << 21);   // TMEM lanes 32 warp ..
+        const int r = 16 * warp + (lane & 15);
+        int at = 0;
+        do {
+            const int nt = g.steps(a), end = g.end(a), ctx = g.s.T - g.s.n;
+            const int64_t row0 = (int64_t)g.group * a.nr, n_rows = (int64_t)g.s.n * a.H;   // of the sequence
+            const int rows = (int)min((int64_t)a.nr, n_rows - row0);
+            const bool active = 16 * warp < rows, valid = lane < 16 && r < rows;
+            const int tok = valid ? (int)((row0 + r) / a.H) : 0;
+            const bool tree = a.parents != nullptr;
+            uint32_t path[KVQ_TREE_WORDS] = {};
+            if (tree && valid) {
+                for (int k = tok; k >= 0;) {
+#pragma unroll
+                    for (int w = 0; w < KVQ_TREE_WORDS; ++w)
+                        if (k >> 5 == w) path[w] |= 1u << (k & 31);
+                    const int p = a.parents[g.s.first + k];
+                    if (p < -1 || p >= k) kvq_dev_flag(a.hdr, KVQ_DEV_BAD_INDEX, p);
+                    k = p < -1 || p >= k ? -1 : p;
+                }
+            }
+            const int cut = tree ? ctx : ctx + tok + 1;     // every token before it is seen
+            const int full = __reduce_min_sync(0xffffffffu, valid ? cut : INT32_MAX);
+            float m = -INFINITY, l = 0.0f;
+            for (int j = 0; j < nt; ++j, ++at) {
+                const int t0 = (g.step + j) * LA_KEYS;
+                bar_wait(&S.abort, a.hdr, &S.s_full[at & 1], (at >> 1) & 1);
+                tc_after();
+                if (end < t0 + LA_KEYS) {
+                    // rows at and behind the end may hold anything: 0 * NaN must not reach O^T
+                    const uint32_t base = skv + at % LA_NS * LA_STAGE;
+                    const int r0 = end - t0;
+                    for (int x = tid; x < (LA_KEYS - r0) * (LAT / 8); x += 128) {
+                        const int row = r0 + x / (LAT / 8), c = x % (LAT / 8);
+                        const uint32_t to = base + (row >> 3) * LA_GROUP + (c >> 3) * 1024 + (row & 7) * 128 + (c & 7) * 16;
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
+                    }
+                }
+                float s[LA_KEYS];
+                float top = -INFINITY;
+                if (active) {
+                    const uint32_t ts = lane_base + TM_S + (at & 1) * LA_KEYS;
+                    tm_ld32(ts, reinterpret_cast<uint32_t*>(s));
+                    tm_ld32(ts + 32, reinterpret_cast<uint32_t*>(s) + 32);
+                    const bool edge = t0 + LA_KEYS > full || t0 + LA_KEYS > end;
+#pragma unroll
+                    for (int w = 0; w < LA_KEYS / 32; ++w) {
+                        uint32_t bits = valid ? below(cut - t0 - 32 * w) : 0u;
+                        if (tree && edge && valid) {
+                            const int from = t0 + 32 * w - ctx, at_w = from >> 5;
+                            uint32_t lo = 0, hi = 0;
+#pragma unroll
+                            for (int i = 0; i < KVQ_TREE_WORDS; ++i) {
+                                if (i == at_w) lo = path[i];
+                                if (i == at_w + 1) hi = path[i];
+                            }
+                            bits |= __funnelshift_r(lo, hi, from & 31);
+                        }
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            const float x = __fmul_rn(s[32 * w + c], a.scale2);
+                            s[32 * w + c] = bits >> c & 1 ? x : -INFINITY;
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < LA_KEYS; ++c) top = fmaxf(top, s[c]);
+                }
+                // (a first anchor, or a weight that would leave fp16's range)
+                const bool far = valid && (m == -INFINITY ? top > m : top - m > LA_TOP);
+                if (sm_any(far)) {
+                    // one row's turn is every row's: an anchor that would have to follow later is set now
+                    float f = 1.0f;
+                    if (valid && (m == -INFINITY ? top > m : top - m > LA_HEAD)) {
+                        const float anchor = top - LA_HEAD;
+                        f = ex2(m - anchor);
+                        m = anchor;
+                        l *= f;
+                    }
+                    if (j > 0) {
+                        if (lane < 16) S.factor[r] = f;
+                        bar_wait(&S.abort, a.hdr, &S.pv_done[(at - 1) & 1], ((at - 1) >> 1) & 1);
+                        tc_after();
+                        sm_any(false);
+                        for (int d = 0; d < LAT / 128; ++d)
+                            for (int c = 0; c < a.nr; c += 16) {
+                                uint32_t o[16];
+                                tm_ld16(lane_base + TM_O + 64 * d + c, o);
+#pragma unroll
+                                for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * S.factor[c + x]);
+                                tm_st16(lane_base + TM_O + 64 * d + c, o);
+                            }
+                        tm_wait_st();
+                    }
+                }
+                // P's place is free when the products before are done
+                if (at > 0) bar_wait(&S.abort, a.hdr, &S.pv_done[(at - 1) & 1], ((at - 1) >> 1) & 1);
+                if (active) {
+                    const float ms = m == -INFINITY ? 0.0f : m;
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < LA_KEYS; c += 8) {
+                        uint32_t p[4];
+#pragma unroll
+                        for (int x = 0; x < 8; x += 2) {
+                            const float e0 = ex2(s[c + x] - ms), e1 = ex2(s[c + x + 1] - ms);
+                            sum += e0 + e1;
+                            p[x / 2] = half2_bits(e0, e1);
+                        }
+                        const uint32_t to = sp + (r >> 3) * 1024 + (r & 7) * 128 + (((c >> 3) ^ (r & 7)) << 4);
+                        if (lane < 16)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3])
+                                         : "memory");
+                    }
+                    l += sum;
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                tc_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&S.p_full);
+            }
+            // ---- the segment's rows: to the output, or as a part of them
+            const bool whole = g.step == 0 && g.cnt == g.s.steps;
+            if (nt > 0) {
+                bar_wait(&S.abort, a.hdr, &S.pv_done[(at - 1) & 1], ((at - 1) >> 1) & 1);
+                tc_after();
+                const int64_t out_row = (int64_t)g.s.first * a.H + row0;
+                const int64_t slot = 2 * (int64_t)blockIdx.x + (g.step == 0 ? 1 : 0);
+                if (valid) {
+                    S.factor[r] = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+                    if (!whole) a.ml[slot * a.nr + r] = make_float2(m, l);
+                    if (whole && a.lse != nullptr) a.lse[out_row + r] = l == 0.0f ? -INFINITY : (m + log2f(l)) * KVQ_LN2;
+                }
+                sm_any(false);
+                if (!aborted(&S.abort)) {
+                    for (int d = 0; d < LAT / 128; ++d)
+                        for (int c = 0; c < rows; c += 16) {
+                            uint32_t o[16];
+                            tm_ld16(lane_base + TM_O + 64 * d + c, o);
+                            const int dim = 128 * d + 32 * warp + lane;
+#pragma unroll
+                            for (int x = 0; x < 16; ++x) {
+                                if (c + x >= rows) break;
+                                const float v = __uint_as_float(o[x]) * S.factor[c + x];
+                                if (whole)
+                                    a.out[(out_row + c + x) * LAT + dim] = kvq_f2h(v);
+                                else
+                                    a.part[(slot * a.nr + c + x) * LAT + dim] = v;
+                            }
+                        }
+                }
+            }
+        } while (g.next(a));
+    }
+    __syncwarp();
+    __syncthreads();
+    if (*(volatile int32_t*)&S.abort) drain_after_abort(warp == 4 && lane == 0, &S.drain);
+    tc_before();
+    __syncthreads();
+    tc_after();
+    if (warp == 4)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TM_COLS) : "memory");
+}
+
+// Joins the parts of a row group's rows in the order of the CTAs and leaves the workspace zeroed.  A CTA per (row
+// group, row): GR groups of 128 threads take every GR-th part, four values per thread.
+template <int GR>
+__global__ void __launch_bounds__(128 * GR) latent_join_kernel(const __grid_constant__ LatArgs a, int ctas) {
+    __shared__ int64_t item[4];              // first part's CTA, parts, whether the first part is a last segment, the output row
+    __shared__ float weight[KVQ_LATENT_MAX_CTAS];
+    __shared__ float4 sums[GR][128];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = blockIdx.y;
+    kvq_pdl_begin();
+    if (warp == 0) {
+        const int64_t per = latent_range(all_steps(a), ctas);
+        int64_t before = 0, base = 0;
+        const int b = find_seq(a, blockIdx.x, [](const Seq& s) { return (int64_t)s.groups; }, &before, &base);
+        if (lane == 0) item[1] = 0;
+        if (b >= 0) {
+            const Seq s = seq_at(a, b);
+            const int group = (int)(blockIdx.x - before);
+            base += (int64_t)group * s.steps;
+            const int64_t c0 = base / per, c1 = (base + s.steps - 1) / per;
+            const bool mine = c1 > c0 && (int64_t)group * a.nr + r < (int64_t)s.n * a.H;
+            if (mine) {
+                // weights of the parts: 2^(anchor - largest anchor); a part without a visible token wrote no row
+                const auto slot_of = [&](int64_t c) { return 2 * c + (base >= c * per ? 1 : 0); };
+                float mx = -INFINITY, y = 0.0f;
+                for (int64_t c = c0 + lane; c <= c1; c += 32) {
+                    const float2 v = a.ml[slot_of(c) * a.nr + r];
+                    if (v.y != 0.0f) mx = fmaxf(mx, v.x);
+                }
+                mx = kvq_warp_max(mx);
+                for (int64_t c = c0 + lane; c <= c1; c += 32) {
+                    float2* at = a.ml + slot_of(c) * a.nr + r;
+                    const float2 v = *at;
+                    const float f = v.y != 0.0f ? exp2f(v.x - mx) : 0.0f;
+                    weight[c - c0] = f;
+                    y += f * v.y;
+                    *at = make_float2(0.0f, 0.0f);
+                }
+                // (every lane's sum is over its own parts, joined in one order)
+                y = kvq_warp_sum(y);
+                const int64_t row = (int64_t)s.first * a.H + (int64_t)group * a.nr + r;
+                const float inv = y == 0.0f ? 0.0f : 1.0f / y;
+                for (int c = lane; c <= c1 - c0; c += 32) weight[c] *= inv;
+                if (lane == 0) {
+                    item[0] = c0, item[1] = c1 - c0 + 1, item[2] = base >= c0 * per, item[3] = row;
+                    if (a.lse != nullptr) a.lse[row] = y == 0.0f ? -INFINITY : (mx + log2f(y)) * KVQ_LN2;
+                }
+            }
+        }
+    }
+    __syncthreads();
+    const int n = (int)item[1], grp = tid >> 7, x = tid & 127;
+    if (n == 0) return;
+    // the first part is its CTA's last segment (or its only one, which may begin inside the row group: its first)
+    const auto part_of = [&](int i) {
+        const int64_t slot = 2 * (item[0] + i) + (i == 0 ? item[2] : 0);
+        return reinterpret_cast<float4*>(a.part + (slot * a.nr + r) * LAT) + x;
+    };
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int i = grp; i < n; i += GR) {
+        const float4 v = *part_of(i);
+        const float f = weight[i];
+        o.x += f * v.x, o.y += f * v.y, o.z += f * v.z, o.w += f * v.w;
+    }
+    // (behind the loads: a store between them would hold up the next one)
+    for (int i = grp; i < n; i += GR) *part_of(i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (GR > 1) {
+        sums[grp][x] = o;
+        __syncthreads();
+        if (grp > 0) return;
+        for (int k = 1; k < GR; ++k) {
+            const float4 v = sums[k][x];
+            o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+        }
+    }
+    reinterpret_cast<uint2*>(a.out + item[3] * LAT)[x] = make_uint2(half2_bits(o.x, o.y), half2_bits(o.z, o.w));
+}
+
+struct LatPlan {
+    int nr, ctas;
+    int64_t items;
+    size_t smem, off_ml, off_part, bytes;
+};
+
+LatPlan latent_plan(const kvq_seqs* S, int32_t n_heads, int64_t n_rows, int32_t max_new) {
+    LatPlan p;
+    p.nr = (int)std::min<int64_t>(LA_ROWS, ((int64_t)max_new * n_heads + 15) / 16 * 16);
+    p.nr = std::max(p.nr, 16);
+    const int64_t by_max = S->batch * (((int64_t)max_new * n_heads + p.nr - 1) / p.nr);
+    p.items = std::max<int64_t>(1, std::min(by_max, n_rows * n_heads / p.nr + S->batch));
+    const int64_t steps = p.items * ((S->max_len + LA_KEYS - 1) / LA_KEYS);
+    p.ctas = (int)std::max<int64_t>(1, std::min<int64_t>({steps, kvq_num_sms(), KVQ_LATENT_MAX_CTAS}));
+    p.smem = 1024 + LA_NS * LA_STAGE + LA_ROWS * 128 + (size_t)p.nr * ROW * 2;
+    const size_t rows = (size_t)2 * p.ctas * p.nr;
+    p.off_ml = sizeof(KvqWsHeader);
+    p.off_part = kvq_round_up(p.off_ml + rows * sizeof(float2), 256);
+    p.bytes = kvq_round_up(p.off_part + rows * LAT * sizeof(float), 256);
+    return p;
+}
+
+}  // namespace
+
+extern "C" size_t kv_latent_attn_ws(const kvq_seqs* S, int32_t n_heads, int64_t n_rows, int32_t max_new) {
+    static const char* fn = "kv_latent_attn_ws";
+    if (kvq_check_seqs_sizes(S, fn) || kvq_check_max_len(S, fn) || check_latent_rows(n_heads, n_rows, max_new, false, fn)) return 0;
+    return latent_plan(S, n_heads, n_rows, max_new).bytes;
+}
+
+extern "C" int kv_latent_attn(const kvq_latent* C, const kvq_seqs* S, int32_t n_heads, const uint16_t* q,
+                              const int32_t* parents, const int32_t* q_starts, int64_t n_rows, int32_t max_new, float scale,
+                              uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+    static const char* fn = "kv_latent_attn";
+    kvq_clear_error();
+    int st = kvq_check_latent(C, fn);
+    if (!st) st = kvq_check_seqs(S, fn);
+    if (!st) st = kvq_check_max_len(S, fn);
+    if (!st) st = check_latent_rows(n_heads, n_rows, max_new, parents != nullptr, fn);
+    LatArgs a;
+    if (!st) st = latent_scale(scale, fn, &a.scale2);
+    if (st) return st;
+    const LatPlan p = latent_plan(S, n_heads, n_rows, max_new);
+    st = kvq_check_ws(ws, ws_bytes, p.bytes, fn);
+    if (st) return st;
+    KVQ_REQUIRE(C->num_blocks * PG <= INT32_MAX && n_rows * n_heads <= INT32_MAX - LA_ROWS, KVQ_ERR_UNSUPPORTED,
+                "%s: more than 2^31 - 1 rows in the pool or queries", fn);
+    if (S->batch == 0 || n_rows == 0) return KVQ_OK;
+    KVQ_REQUIRE(q && out && q_starts && (S->block_table || S->max_len == 0), KVQ_ERR_INVALID_ARG, "%s: NULL buffer", fn);
+    KVQ_REQUIRE((((uintptr_t)q | (uintptr_t)out) & 15u) == 0, KVQ_ERR_INVALID_ARG, "%s: q and out must be 16-byte aligned", fn);
+    CUtensorMap map_q, map_rows;
+    const uint64_t qd[3] = {64, (uint64_t)n_rows * n_heads, LA_CHUNKS}, qs[2] = {ROW * 2, 128};
+    const uint32_t qb[3] = {64, (uint32_t)p.nr, LA_CHUNKS};
+    const uint64_t rd[4] = {64, 8, LA_CHUNKS, (uint64_t)C->num_blocks * (PG / 8)}, rs[3] = {ROW * 2, 128, 8 * ROW * 2};
+    const uint32_t rb[4] = {64, 8, LA_CHUNKS, PG / 8};
+    st = make_map(&map_q, q, 3, qd, qs, qb, fn);
+    if (!st) st = make_map(&map_rows, C->rows, 4, rd, rs, rb, fn);
+    if (!st) st = kvq_prepare_kernel((const void*)latent_attn_kernel, (int)p.smem);
+    if (st) return st;
+    a.bt = S->block_table, a.seq_lens = S->seq_lens, a.q_starts = q_starts, a.parents = parents;
+    a.n_rows = n_rows, a.num_blocks = C->num_blocks;
+    a.batch = S->batch, a.max_blocks = S->max_blocks, a.max_len = S->max_len, a.max_new = max_new, a.H = n_heads, a.nr = p.nr;
+    a.out = out, a.lse = lse, a.hdr = static_cast<KvqWsHeader*>(ws);
+    a.ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + p.off_ml);
+    a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.off_part);
+    cudaError_t e = kvq_launch_pdl(latent_attn_kernel, dim3(p.ctas), dim3(LA_NT), p.smem, kvq_stream(stream), map_q, map_rows, a);
+    if (e == cudaSuccess && p.ctas > 1) {
+        // few row groups have many parts each
+        const dim3 grid((unsigned)p.items, p.nr);
+        if (p.items * 8 <= p.ctas)
+            e = kvq_launch_pdl(latent_join_kernel<8>, grid, dim3(1024), 0, kvq_stream(stream), a, p.ctas);
+        else
+            e = kvq_launch_pdl(latent_join_kernel<1>, grid, dim3(128), 0, kvq_stream(stream), a, p.ctas);
+    }
+    if (e != cudaSuccess) return kvq_fail(KVQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+    return KVQ_OK;
+}
