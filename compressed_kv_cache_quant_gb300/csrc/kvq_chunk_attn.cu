@@ -1,4 +1,5 @@
-// kv_chunk_attn: attention of a run of new tokens per sequence over an fp16 layer's pages.
+// kv_chunk_attn: attention of a run of new tokens per sequence over an fp16 layer's pages; kv_tree_attn, where the new
+// tokens are trees of drafts; kv_latent_expanded_attn, a run over keys and values expanded from latent rows.
 //
 // Bound: the tensor cores from a few dozen query rows per kv head on (4 d flops per visible pair), below
 // that the bytes of the cache.  One CTA takes up to 256 query rows of one kv head as two tiles of 128:
@@ -36,6 +37,7 @@
 #include <type_traits>
 
 #include "kvq_attn_mod.cuh"
+#include "kvq_latent.cuh"
 #include "kvq_tc.cuh"
 #include "kvq_tree.cuh"
 
@@ -50,6 +52,9 @@ constexpr int CA_NS = 4;                 // K or V tiles in the ring
 constexpr int CA_TILE = 128 * D * 2;     // bytes of a Q, K or V tile
 constexpr int CA_HALF = CA_TILE / 2;     // a Q tile is two halves of 128 rows x 128 bytes
 constexpr int CA_SMEM = 2 * CA_TILE + CA_NS * CA_TILE + 1024;
+constexpr int EX_QC = (D + KVQ_LATENT_ROPE) / 64;   // expanded form: halves of a query or key row of 192 values
+constexpr int EX_NS = 8;                 // its ring, in pieces of CA_HALF: five per tile
+constexpr int EX_SMEM = 2 * EX_QC * CA_HALF + EX_NS * CA_HALF + 1024;
 constexpr float CA_HEAD = 7.0f;          // log2 of a row's largest weight when its anchor is set
 constexpr float CA_TOP = 15.99f;         // log2 of the largest weight before the anchor is set anew (fp16 ends at 2^16)
 constexpr float CA_FAR = 1048576.0f;     // scores (log2) beyond which they are rounded before the anchor is taken off
@@ -61,6 +66,8 @@ constexpr uint32_t IDESC_QK = idesc_f16(128, 128), IDESC_PV = IDESC_QK | KVQ_B_M
 struct ChunkArgs {
     const int32_t *bt, *seq_lens, *q_starts;
     const int32_t* parents;       // kv_tree_attn: of every row
+    const int32_t* k_starts;      // kv_latent_expanded_attn: first key of every sequence, in place of seq_lens
+    int64_t n_keys;
     int64_t num_blocks;
     int32_t batch, max_blocks, max_len, max_new, H, GQ, n_splits;
     int32_t items, heads_first;   // groups of new tokens, at most; which of heads and groups runs faster in the grid
@@ -81,14 +88,24 @@ struct Shared {
     int32_t abort;
     int32_t item_b, item_tok;                     // sequence and first new token of this CTA
     int32_t doc_min, sink_max, lo_min, hi_max;    // over its rows
-    int4 see[CA_ROWS];                            // lo, hi, doc, sink of every token
 };
+
+// What the new tokens are: a run; nodes of trees (kv_tree_attn); a run over expanded latent rows
+// (kv_latent_expanded_attn).
+enum Kind { RUN, TREES, EXPANDED };
+
+// Tokens of sequence b; -1 where its keys lie outside the call's.
+__device__ __forceinline__ int seq_len(const ChunkArgs& a, int b) {
+    if (a.k_starts == nullptr) return a.seq_lens[b];
+    const int64_t k0 = a.k_starts[b], k1 = a.k_starts[b + 1];
+    return k0 < 0 || k1 < k0 || k1 > a.n_keys ? -1 : (int)(k1 - k0);
+}
 
 // Sequence b's new tokens: *first row and count; false (flagged) when its lengths do not fit the call.
 __device__ __forceinline__ bool seq_rows(const ChunkArgs& a, int b, int* first, int* n) {
     *first = a.q_starts[b];
     const int64_t cnt = (int64_t)a.q_starts[b + 1] - *first;
-    const int T = a.seq_lens[b];
+    const int T = seq_len(a, b);
     *n = 0;
     if (*first < 0 || cnt < 0 || cnt > a.max_new || *first + cnt > a.n_rows || T < cnt || T > a.max_len) {
         kvq_dev_flag(a.hdr, KVQ_DEV_BAD_LENGTH, b);
@@ -136,18 +153,26 @@ __device__ __forceinline__ uint32_t columns(int a, int b, int w) {
 
 // TREE: the new tokens are nodes of trees.  A node's interval ends with the cached tokens before them, and its path
 // adds a few bits among the last columns; positions go by depth.
-template <bool CAP, bool BIAS, bool TREE>
+//
+// EXPANDED: a key has 128 values of its head and 64 that all heads share, so a query row has three halves; keys and
+// values lie in one piece per sequence.  The ring then holds 16 KB pieces, three of a K tile and two of a V tile (of 64
+// tokens each): 1.6 tiles, since two query tiles take 96 KB.
+template <bool CAP, bool BIAS, Kind KIND>
 __global__ void __launch_bounds__(CA_NT, 1)
     chunk_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                      const __grid_constant__ CUtensorMap map_v, const __grid_constant__ ChunkArgs a) {
+                      const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_r,
+                      const __grid_constant__ ChunkArgs a) {
+    constexpr bool TREE = KIND == TREES, EXP = KIND == EXPANDED;
+    constexpr int Q_TILE = EXP ? EX_QC * CA_HALF : CA_TILE;
     extern __shared__ unsigned char raw[];
     __shared__ Shared S;
+    __shared__ int4 seen_of[EXP ? 1 : CA_ROWS];   // lo, hi, doc, sink of every token
     __shared__ std::conditional_t<TREE, KvqTree, int> tree;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int GQ = a.GQ, tpc = CA_ROWS / GQ, split = blockIdx.y;
     const int h = a.heads_first ? blockIdx.x % a.H : blockIdx.x / a.items;
     const int item = a.heads_first ? blockIdx.x / a.H : blockIdx.x % a.items;
-    const uint32_t sq = (saddr(raw) + 1023) & ~1023u, skv = sq + 2 * CA_TILE;
+    const uint32_t sq = (saddr(raw) + 1023) & ~1023u, skv = sq + 2 * Q_TILE;
     kvq_pdl_begin();
     if (warp == 0) {
         int b, tok;
@@ -162,7 +187,7 @@ __global__ void __launch_bounds__(CA_NT, 1)
     __syncthreads();
     const int b = S.item_b, tok0 = S.item_tok;
     if (b < 0) return;
-    const int first = a.q_starts[b], n = a.q_starts[b + 1] - first, T = a.seq_lens[b];
+    const int first = a.q_starts[b], n = a.q_starts[b + 1] - first, T = seq_len(a, b);
     const int ntok = min(tpc, n - tok0), rows = ntok * GQ;
     const int nq = rows > 128 ? 2 : 1;
     const int ctx = T - n;   // cached tokens before the new ones
@@ -196,7 +221,7 @@ __global__ void __launch_bounds__(CA_NT, 1)
         } else {
             see = kvq_see(a.mod, ctx + i, T, a.mod.prefix_len ? a.mod.prefix_len[b] : 0, doc);
         }
-        S.see[tid] = make_int4(see.lo, see.hi, see.doc, see.sink);
+        if (!EXP) seen_of[tid] = make_int4(see.lo, see.hi, see.doc, see.sink);
         if (see.lo < see.hi) {
             atomicMin(&S.lo_min, see.lo);
             atomicMax(&S.hi_max, see.hi);
@@ -245,12 +270,42 @@ __global__ void __launch_bounds__(CA_NT, 1)
         if (warp == 9 && nt > 0) {
             // ---- loads
             if (lane == 0) {
-                bar_expect(&S.q_full, nq * CA_TILE);
+                bar_expect(&S.q_full, nq * Q_TILE);
                 for (int i = 0; i < nq; ++i)
-                    for (int c = 0; c < 2; ++c)
-                        tma_3d(sq + i * CA_TILE + c * CA_HALF, &map_q, 64 * c, h * GQ, first + tok0 + i * (128 / GQ), &S.q_full);
+                    for (int c = 0; c < Q_TILE / CA_HALF; ++c)
+                        tma_3d(sq + i * Q_TILE + c * CA_HALF, &map_q, 64 * c, h * GQ, first + tok0 + i * (128 / GQ), &S.q_full);
             }
             __syncwarp();
+            if constexpr (EXP) {
+                // tile j is the pieces 5j .. 5j + 4 of a list that goes round the ring: K's three, V's two.  A piece's
+                // place was that of the piece eight before: of K(j - 2), V(j - 2) for K, of K(j - 1) for V.
+                const int key0 = a.k_starts[b];
+                const auto to = [&](int j, int piece) { return skv + (5 * j + piece) % EX_NS * CA_HALF; };
+                for (int j = 0; j < nt; ++j) {
+                    const int key = key0 + tile_of(it0 + j) * CA_KEYS;
+                    if (j >= 2) {
+                        bar_wait(&S.abort, a.hdr, &S.kv_empty[j & 1], ((j - 2) >> 1) & 1);
+                        bar_wait(&S.abort, a.hdr, &S.kv_empty[2 + (j & 1)], ((j - 2) >> 1) & 1);
+                    }
+                    if (aborted(&S.abort)) break;
+                    if (elect()) {
+                        bar_expect(&S.kv_full[j & 1], 3 * CA_HALF);
+                        tma_3d(to(j, 0), &map_k, 0, h, key, &S.kv_full[j & 1]);
+                        tma_3d(to(j, 1), &map_k, 64, h, key, &S.kv_full[j & 1]);
+                        tma_3d(to(j, 2), &map_r, 0, key, 0, &S.kv_full[j & 1]);
+                    }
+                    __syncwarp();
+                    if (j >= 1) bar_wait(&S.abort, a.hdr, &S.kv_empty[(j - 1) & 1], ((j - 1) >> 1) & 1);
+                    if (aborted(&S.abort)) break;
+                    if (elect()) {
+                        bar_expect(&S.kv_full[2 + (j & 1)], CA_TILE);
+                        for (int x = 0; x < 4; ++x)
+                            tma_3d(to(j, 3 + x / 2) + x % 2 * (CA_HALF / 2), &map_v, 64 * (x % 2), h, key + 64 * (x / 2),
+                                   &S.kv_full[2 + (j & 1)]);
+                    }
+                    __syncwarp();
+                }
+            } else {
             const int pg = lane & 7;   // lanes 0-7 look up one page each
             const int nowhere = (int)(a.num_blocks * a.H * (PG / 8));  // a group of rows behind the pool: zeros
             // where this lane's page of the j-th tile begins, in groups of 8 rows: it is looked up a tile ahead,
@@ -265,7 +320,7 @@ __global__ void __launch_bounds__(CA_NT, 1)
                 } else {
                     uint32_t bits = 0;
                     for (int k = lane; k < ntok; k += 32) {
-                        const int4 e = S.see[k];
+                        const int4 e = seen_of[k];
                         const int p0 = t * (CA_KEYS / PG);
                         if (e.x < e.y) bits |= below((e.y + PG - 1) / PG - p0) & ~below(e.x / PG - p0);
                         if (e.z < e.w) bits |= below((e.w + PG - 1) / PG - p0) & ~below(e.z / PG - p0);
@@ -307,6 +362,7 @@ __global__ void __launch_bounds__(CA_NT, 1)
                 if (j + 1 < nt) y = group_of(j + 1);
                 ok = ok && fetch(2 * j + 1, &map_v, at);
             }
+            }
         }
         if (warp == 8 && nt > 0) {
             // ---- tensor cores.  The whole warp walks the loop and one elected lane issues, so that the
@@ -314,29 +370,36 @@ __global__ void __launch_bounds__(CA_NT, 1)
             // column 0.  A descriptor is its low word plus constants: the low words are made opaque in every
             // step, or the compiler keeps all 64 of a step's descriptors in (spilled) registers, and the
             // reloads hold up every product (110 instead of 64 cycles each).
-            const uint32_t hi_q = (uint32_t)(smem_desc(0, 16, 1024) >> 32), hi_kv = (uint32_t)(smem_desc(0, 16, 2048) >> 32);
+            const uint32_t hi_q = (uint32_t)(smem_desc(0, 16, 1024) >> 32),
+                           hi_kv = (uint32_t)(smem_desc(0, 16, EXP ? 1024 : 2048) >> 32);
             const uint32_t lq = (uint32_t)smem_desc(sq, 16, 0), lk = (uint32_t)smem_desc(skv, 16, 0),
-                           lv = (uint32_t)smem_desc(skv, 1024, 0);
+                           lv = (uint32_t)smem_desc(skv, EXP ? CA_HALF / 2 : 1024, 0);
             const auto desc = [](uint32_t hi, uint32_t lo) { return (uint64_t)hi << 32 | lo; };
+            // (st: the tile's stage in the ring; the expanded form's tile)
             const auto qk = [&](int i, int st) {
                 if (elect()) {
-                    uint32_t x = lq + (i * CA_TILE >> 4), y = lk + (st * CA_TILE >> 4);
+                    uint32_t x = lq + (i * Q_TILE >> 4), y = lk + (EXP ? 0 : st * CA_TILE >> 4);
                     asm volatile("" : "+r"(x), "+r"(y));
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
+                    for (int k = 0; k < Q_TILE / CA_HALF * 4; ++k) {
+                        if (EXP && (k & 3) == 0) {
+                            y = lk + ((5 * st + (k >> 2)) % EX_NS * CA_HALF >> 4);
+                            asm volatile("" : "+r"(y));
+                        }
                         mma_ss(TM_S + 128 * i, desc(hi_q, x + (((k >> 2) * CA_HALF + (k & 3) * 32) >> 4)),
-                               desc(hi_kv, y + (((k >> 2) * 1024 + (k & 3) * 32) >> 4)), IDESC_QK, k > 0);
+                               desc(hi_kv, y + (((EXP ? 0 : k >> 2) * 1024 + (k & 3) * 32) >> 4)), IDESC_QK, k > 0);
                     }
                     tc_commit(&S.s_full[i]);
                 }
             };
             const auto pv = [&](int i, int st, int half, bool acc) {
                 if (elect()) {
-                    uint32_t y = lv + (st * CA_TILE >> 4);
+                    uint32_t y = lv + ((EXP ? (5 * st + 3 + half) % EX_NS * CA_HALF : st * CA_TILE) >> 4);
                     asm volatile("" : "+r"(y));
 #pragma unroll
                     for (int k = 4 * half; k < 4 * half + 4; ++k)
-                        mma_ts(TM_O + 128 * i, TM_S + 128 * i + 8 * k, desc(hi_kv, y + (k * 4096 >> 4)), IDESC_PV, acc || k > 0);
+                        mma_ts(TM_O + 128 * i, TM_S + 128 * i + 8 * k, desc(hi_kv, y + ((EXP ? (k & 3) * 2048 : k * 4096) >> 4)),
+                               IDESC_PV, acc || k > 0);
                 }
             };
             const auto commit = [&](uint64_t* bar) {
@@ -349,8 +412,10 @@ __global__ void __launch_bounds__(CA_NT, 1)
             if (nq > 1) qk(1, 0);
             commit(&S.kv_empty[0]);
             for (int j = 0; j < nt; ++j) {
-                const int sv = (2 * j + 1) % CA_NS, sk = (2 * j + 2) % CA_NS;
+                const int sv = EXP ? j : (2 * j + 1) % CA_NS, sk = EXP ? j + 1 : (2 * j + 2) % CA_NS;
                 const bool more = j + 1 < nt;
+                uint64_t* const next_full = EXP ? &S.kv_full[(j + 1) & 1] : &S.kv_full[sk];
+                const uint32_t next_phase = EXP ? ((j + 1) >> 1) & 1 : ((2 * j + 2) / CA_NS) & 1;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     if (i == nq) break;
@@ -360,15 +425,15 @@ __global__ void __launch_bounds__(CA_NT, 1)
                     bar_wait(&S.abort, a.hdr, &S.p_full[i][1], j & 1);
                     tc_after();
                     pv(i, sv, 1, true);
-                    if (i == nq - 1) commit(&S.kv_empty[sv]);
+                    if (i == nq - 1) commit(EXP ? &S.kv_empty[2 + (j & 1)] : &S.kv_empty[sv]);
                     if (more) {
-                        if (i == 0) bar_wait(&S.abort, a.hdr, &S.kv_full[sk], ((2 * j + 2) / CA_NS) & 1);
+                        if (i == 0) bar_wait(&S.abort, a.hdr, next_full, next_phase);
                         qk(i, sk);
                     } else {
                         commit(&S.o_full[i]);
                     }
                 }
-                if (more) commit(&S.kv_empty[sk]);
+                if (more) commit(EXP ? &S.kv_empty[(j + 1) & 1] : &S.kv_empty[sk]);
             }
         }
     } else {
@@ -382,7 +447,7 @@ __global__ void __launch_bounds__(CA_NT, 1)
         int4 see = make_int4(0, 0, 0, 0);
         int maxlo = 0, minhi = INT32_MAX;   // over the warp's rows: tiles between need no mask
         if (valid) {
-            see = S.see[tok];
+            see = EXP ? make_int4(0, ctx + tok0 + tok + 1, 0, 0) : seen_of[tok];
             maxlo = see.x, minhi = see.y;
         }
         maxlo = __reduce_max_sync(0xffffffffu, maxlo);
@@ -403,18 +468,22 @@ __global__ void __launch_bounds__(CA_NT, 1)
             for (int j = 0; j < nt; ++j) {
                 const int t0 = tile_of(it0 + j) * CA_KEYS;
                 // rows at and behind T may hold anything: 0 * NaN must not reach O
-                const bool tail = T < t0 + CA_KEYS && (T & (PG - 1)) != 0 && T > t0;
+                const bool tail = T < t0 + CA_KEYS && (EXP || (T & (PG - 1)) != 0) && T > t0;
+                uint64_t* const v_full = EXP ? &S.kv_full[2 + (j & 1)] : &S.kv_full[(2 * j + 1) % CA_NS];
+                const uint32_t v_phase = EXP ? (j >> 1) & 1 : ((2 * j + 1) / CA_NS) & 1;
                 bar_wait(&S.abort, a.hdr, &S.s_full[i], j & 1);
                 // tile 0's weights stand for V's arrival too (its products are issued after these waits, and tile
                 // 1's after tile 0's): the issuing warp is the busier one.  1.38 -> 1.36 ms for the prompt
-                if (i == 0) bar_wait(&S.abort, a.hdr, &S.kv_full[(2 * j + 1) % CA_NS], ((2 * j + 1) / CA_NS) & 1);
+                if (i == 0) bar_wait(&S.abort, a.hdr, v_full, v_phase);
                 if (tail) {
-                    bar_wait(&S.abort, a.hdr, &S.kv_full[(2 * j + 1) % CA_NS], ((2 * j + 1) / CA_NS) & 1);
+                    bar_wait(&S.abort, a.hdr, v_full, v_phase);
                     const uint32_t base = skv + (2 * j + 1) % CA_NS * CA_TILE;
-                    const int r0 = T - t0, r1 = (r0 + PG - 1) / PG * PG;
+                    const int r0 = T - t0, r1 = EXP ? CA_KEYS : (r0 + PG - 1) / PG * PG;
                     for (int x = tid & 127; x < (r1 - r0) * 16; x += 128) {
                         const int row = r0 + (x >> 4);
-                        const uint32_t at = base + (row >> 3) * 2048 + (x & 1) * 1024 + (row & 7) * 128 + ((x >> 1) & 7) * 16;
+                        const uint32_t at = EXP ? skv + (5 * j + 3 + (row >> 6)) % EX_NS * CA_HALF + (x & 1) * (CA_HALF / 2) +
+                                                      (row & 63) * 128 + ((x >> 1) & 7) * 16
+                                                : base + (row >> 3) * 2048 + (x & 1) * 1024 + (row & 7) * 128 + ((x >> 1) & 7) * 16;
                         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -753,13 +822,13 @@ struct ChunkPlan {
 // 182 us), the join's launch as 3, and the parts' rows are written, read and zeroed, 0.036 tiles' time per CTA
 // of 256 rows (200 new tokens of 1000: 32 CTAs whole 19.9 us, in 2 parts 22.6 us; 500 of 8000: 91 us, in 2
 // parts 62 us).
-ChunkPlan chunk_plan(const kvq_layout* L, const kvq_seqs* S, int64_t n_rows, int32_t max_new) {
+ChunkPlan chunk_plan(int H, int GQ, int32_t batch, int32_t max_len, int64_t n_rows, int32_t max_new) {
     ChunkPlan p;
-    const int GQ = L->n_q_heads / L->n_kv_heads, tpc = CA_ROWS / GQ;
-    const int64_t by_max = S->batch * (((int64_t)max_new + tpc - 1) / tpc);
-    p.items = std::max<int64_t>(1, std::min(by_max, n_rows / tpc + S->batch));
-    const int64_t ctas = p.items * L->n_kv_heads, sms = kvq_num_sms();
-    const int tiles = (S->max_len + CA_KEYS - 1) / CA_KEYS;
+    const int tpc = CA_ROWS / GQ;
+    const int64_t by_max = batch * (((int64_t)max_new + tpc - 1) / tpc);
+    p.items = std::max<int64_t>(1, std::min(by_max, n_rows / tpc + batch));
+    const int64_t ctas = p.items * H, sms = kvq_num_sms();
+    const int tiles = (max_len + CA_KEYS - 1) / CA_KEYS;
     p.n_splits = 1;
     if (ctas < sms) {
         const int most = (int)std::min<int64_t>(std::max(1, tiles / 4), 4 * sms / ctas);
@@ -777,6 +846,33 @@ ChunkPlan chunk_plan(const kvq_layout* L, const kvq_seqs* S, int64_t n_rows, int
     p.off_part = kvq_round_up(p.off_ml + rows * sizeof(float2), 256);
     p.bytes = kvq_round_up(p.off_part + rows * D * sizeof(float), 256);
     return p;
+}
+
+ChunkPlan chunk_plan(const kvq_layout* L, const kvq_seqs* S, int64_t n_rows, int32_t max_new) {
+    return chunk_plan(L->n_kv_heads, L->n_q_heads / L->n_kv_heads, S->batch, S->max_len, n_rows, max_new);
+}
+
+// Fills in what follows from the plan and launches the kernel and, over parts of the cache, their join.
+template <typename Kernel>
+int launch_chunk(Kernel kernel, int smem, const ChunkPlan& p, ChunkArgs& a, const CUtensorMap& map_q, const CUtensorMap& map_k,
+                 const CUtensorMap& map_v, const CUtensorMap& map_r, void* ws, cudaStream_t stream, const char* fn) {
+    a.n_splits = p.n_splits;
+    a.items = (int32_t)p.items;
+    a.hdr = static_cast<KvqWsHeader*>(ws);
+    a.ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + p.off_ml);
+    a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.off_part);
+    // The longest groups come first.  In a few waves, the heads' long groups run side by side, or the last
+    // head's would start late (packed documents: 92 -> 82 us); in many waves one head after the other, so
+    // that all CTAs read the same K and V (a 16384-token prompt: 1.38 instead of 1.42 ms).
+    a.heads_first = p.items * a.H <= 6 * (int64_t)kvq_num_sms();
+    const int rc = kvq_prepare_kernel((const void*)kernel, smem);
+    if (rc) return rc;
+    cudaError_t e = kvq_launch_pdl(kernel, dim3((unsigned)(p.items * a.H), p.n_splits), dim3(CA_NT), smem, stream, map_q, map_k,
+                                   map_v, map_r, a);
+    if (e == cudaSuccess && p.n_splits > 1)
+        e = kvq_launch_pdl(chunk_join_kernel, dim3((unsigned)p.items, a.H, CA_ROWS / CJ_NW), dim3(32 * CJ_NW), 0, stream, a);
+    if (e != cudaSuccess) return kvq_fail(KVQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+    return KVQ_OK;
 }
 
 }  // namespace
@@ -830,35 +926,21 @@ static int chunk_attn(const char* fn, bool tree, const kvq_layout* L, const kvq_
     if (st) return st;
     a.num_blocks = P->num_blocks;
     a.bt = S->block_table, a.seq_lens = S->seq_lens, a.q_starts = q_starts, a.parents = parents;
+    a.k_starts = nullptr, a.n_keys = 0;
     a.batch = S->batch, a.max_blocks = S->max_blocks, a.max_len = S->max_len, a.max_new = max_new;
-    a.H = H, a.GQ = GQ, a.n_splits = p.n_splits;
+    a.H = H, a.GQ = GQ;
     a.n_rows = n_rows;
     a.out = out, a.lse = lse;
-    a.hdr = static_cast<KvqWsHeader*>(ws);
-    a.ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + p.off_ml);
-    a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.off_part);
-    a.items = (int32_t)p.items;
-    // The longest groups come first.  In a few waves, the heads' long groups run side by side, or the last
-    // head's would start late (packed documents: 92 -> 82 us); in many waves one head after the other, so
-    // that all CTAs read the same K and V (a 16384-token prompt: 1.38 instead of 1.42 ms).
-    a.heads_first = p.items * H <= 6 * (int64_t)kvq_num_sms();
-    const dim3 grid((unsigned)(p.items * H), p.n_splits);
     const auto go = [&](auto kernel) {
-        const int rc = kvq_prepare_kernel((const void*)kernel, CA_SMEM);
-        if (rc) return rc;
-        cudaError_t e = kvq_launch_pdl(kernel, grid, dim3(CA_NT), CA_SMEM, kvq_stream(stream), map_q, map_k, map_v, a);
-        if (e == cudaSuccess && p.n_splits > 1)
-            e = kvq_launch_pdl(chunk_join_kernel, dim3((unsigned)p.items, H, CA_ROWS / CJ_NW), dim3(32 * CJ_NW), 0, kvq_stream(stream), a);
-        if (e != cudaSuccess) return kvq_fail(KVQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
-        return (int)KVQ_OK;
+        return launch_chunk(kernel, CA_SMEM, p, a, map_q, map_k, map_v, map_q, ws, kvq_stream(stream), fn);
     };
     const bool cap = a.mod.post != 0.0f, bias = a.mod.slopes != nullptr;
     if (tree) {
-        if (cap) return bias ? go(chunk_attn_kernel<true, true, true>) : go(chunk_attn_kernel<true, false, true>);
-        return bias ? go(chunk_attn_kernel<false, true, true>) : go(chunk_attn_kernel<false, false, true>);
+        if (cap) return bias ? go(chunk_attn_kernel<true, true, TREES>) : go(chunk_attn_kernel<true, false, TREES>);
+        return bias ? go(chunk_attn_kernel<false, true, TREES>) : go(chunk_attn_kernel<false, false, TREES>);
     }
-    if (cap) return bias ? go(chunk_attn_kernel<true, true, false>) : go(chunk_attn_kernel<true, false, false>);
-    return bias ? go(chunk_attn_kernel<false, true, false>) : go(chunk_attn_kernel<false, false, false>);
+    if (cap) return bias ? go(chunk_attn_kernel<true, true, RUN>) : go(chunk_attn_kernel<true, false, RUN>);
+    return bias ? go(chunk_attn_kernel<false, true, RUN>) : go(chunk_attn_kernel<false, false, RUN>);
 }
 
 extern "C" int kv_chunk_attn(const kvq_layout* L, const kvq_pool* P, const kvq_seqs* S, const uint16_t* q,
@@ -880,4 +962,69 @@ extern "C" int kv_tree_attn(const kvq_layout* L, const kvq_pool* P, const kvq_se
                             const kvq_attn_mod* mod, uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
     return chunk_attn("kv_tree_attn", true, L, P, S, q, parents, q_starts, n_rows, max_new, mod, out, lse, ws, ws_bytes,
                       stream);
+}
+
+static int check_expanded(int32_t batch, int32_t n_heads, int64_t n_rows, int32_t max_new, int32_t max_len, const char* fn) {
+    KVQ_REQUIRE(batch >= 0 && max_len >= 0, KVQ_ERR_INVALID_ARG, "%s: negative sizes", fn);
+    KVQ_REQUIRE(max_len <= 1 << 30, KVQ_ERR_UNSUPPORTED, "%s: max_len %d (at most 2^30)", fn, max_len);
+    return check_latent_rows(n_heads, n_rows, max_new, false, fn);
+}
+
+extern "C" size_t kv_latent_expanded_attn_ws(int32_t batch, int32_t n_heads, int64_t n_rows, int32_t max_new, int32_t max_len) {
+    kvq_clear_error();
+    if (check_expanded(batch, n_heads, n_rows, max_new, max_len, "kv_latent_expanded_attn_ws")) return 0;
+    return chunk_plan(n_heads, 1, batch, max_len, n_rows, max_new).bytes;
+}
+
+extern "C" int kv_latent_expanded_attn(int32_t batch, int32_t n_heads, const uint16_t* q, const uint16_t* k_nope,
+                                       int64_t kn_stride, int64_t kn_head_stride, const uint16_t* k_rope, int64_t kr_stride,
+                                       const uint16_t* v, int64_t v_stride, int64_t v_head_stride, int64_t n_keys,
+                                       const int32_t* q_starts, const int32_t* k_starts, int64_t n_rows, int32_t max_new,
+                                       int32_t max_len, float scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                                       void* stream) {
+    static const char* fn = "kv_latent_expanded_attn";
+    kvq_clear_error();
+    int st = check_expanded(batch, n_heads, n_rows, max_new, max_len, fn);
+    ChunkArgs a;
+    if (!st) st = kvq_mod_args(nullptr, fn, &a.mod);
+    if (!st) st = latent_scale(scale, fn, &a.mod.pre);
+    if (st) return st;
+    a.mod.lin = a.mod.pre;
+    const ChunkPlan p = chunk_plan(n_heads, 1, batch, max_len, n_rows, max_new);
+    st = kvq_check_ws(ws, ws_bytes, p.bytes, fn);
+    if (st) return st;
+    KVQ_REQUIRE(n_keys >= 0 && n_keys <= INT32_MAX - CA_KEYS, KVQ_ERR_INVALID_ARG, "%s: n_keys", fn);
+    if (batch == 0 || n_rows == 0) return KVQ_OK;
+    KVQ_REQUIRE(n_keys > 0, KVQ_ERR_INVALID_ARG, "%s: queries without keys", fn);
+    KVQ_REQUIRE(q && out && q_starts && k_starts && k_nope && k_rope && v, KVQ_ERR_INVALID_ARG, "%s: NULL buffer", fn);
+    KVQ_REQUIRE((((uintptr_t)q | (uintptr_t)out | (uintptr_t)k_nope | (uintptr_t)k_rope | (uintptr_t)v) & 15u) == 0,
+                KVQ_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned", fn);
+    KVQ_REQUIRE((kn_stride | kn_head_stride | kr_stride | v_stride | v_head_stride) % 8 == 0, KVQ_ERR_INVALID_ARG,
+                "%s: strides must be multiples of 8", fn);
+    // (a tensor map's strides are below 2^40 bytes)
+    KVQ_REQUIRE(kn_stride >= D && kn_head_stride >= D && v_stride >= D && v_head_stride >= D && kr_stride >= KVQ_LATENT_ROPE &&
+                    std::max({kn_stride, kn_head_stride, kr_stride, v_stride, v_head_stride}) < (int64_t)1 << 39,
+                KVQ_ERR_INVALID_ARG, "%s: a stride below the row's width, or above 2^39", fn);
+    KVQ_REQUIRE(p.items * n_heads <= INT32_MAX, KVQ_ERR_UNSUPPORTED, "%s: n_rows", fn);
+    const uint64_t H = n_heads;
+    CUtensorMap map_q, map_k, map_v, map_r;
+    const uint64_t qd[3] = {D + KVQ_LATENT_ROPE, H, (uint64_t)n_rows}, qs[2] = {(D + KVQ_LATENT_ROPE) * 2, H * (D + KVQ_LATENT_ROPE) * 2};
+    const uint64_t kd[3] = {D, H, (uint64_t)n_keys}, ks[2] = {(uint64_t)kn_head_stride * 2, (uint64_t)kn_stride * 2},
+                   vs[2] = {(uint64_t)v_head_stride * 2, (uint64_t)v_stride * 2};
+    const uint64_t rd[3] = {KVQ_LATENT_ROPE, (uint64_t)n_keys, 1}, rs[2] = {(uint64_t)kr_stride * 2, 16};
+    const uint32_t rows128[3] = {64, 1, 128}, rows64[3] = {64, 1, 64}, shared128[3] = {64, 128, 1};
+    st = make_map(&map_q, q, 3, qd, qs, rows128, fn);
+    if (!st) st = make_map(&map_k, k_nope, 3, kd, ks, rows128, fn);
+    if (!st) st = make_map(&map_v, v, 3, kd, vs, rows64, fn);
+    if (!st) st = make_map(&map_r, k_rope, 3, rd, rs, shared128, fn);
+    if (st) return st;
+    a.num_blocks = 0;
+    a.bt = a.seq_lens = a.parents = nullptr;
+    a.q_starts = q_starts, a.k_starts = k_starts, a.n_keys = n_keys;
+    a.batch = batch, a.max_blocks = 0, a.max_len = max_len, a.max_new = max_new;
+    a.H = n_heads, a.GQ = 1;
+    a.n_rows = n_rows;
+    a.out = out, a.lse = lse;
+    return launch_chunk(chunk_attn_kernel<false, false, EXPANDED>, EX_SMEM, p, a, map_q, map_k, map_v, map_r, ws,
+                        kvq_stream(stream), fn);
 }
