@@ -35,11 +35,10 @@ constexpr int PG = KVQ_BLOCK_TOKENS;
 constexpr int LAT = KVQ_LATENT_DIM, ROT = KVQ_LATENT_ROPE, ROW = LAT + ROT;
 constexpr int LA_NT = 192;
 constexpr int LA_ROWS = 64;               // query rows per CTA
-constexpr int LA_KEYS = 64;               // tokens per step
-constexpr int LA_NS = 2;                  // stages
+constexpr int LA_MAX_NS = 8;              // most stages
 constexpr int LA_CHUNKS = ROW / 64;
 constexpr int LA_GROUP = LA_CHUNKS * 1024;              // bytes of eight staged rows
-constexpr int LA_STAGE = LA_KEYS / 8 * LA_GROUP;
+constexpr int LA_SMEM = 232448 - 1024;    // dynamic shared memory of a CTA, at most (static: under 1 KB)
 constexpr float LA_HEAD = 7.0f;           // log2 of a row's largest weight when its anchor is set
 constexpr float LA_TOP = 15.99f;          // log2 of the largest weight before the anchor is set anew
 constexpr uint32_t TM_O = 0, TM_S = 256, TM_COLS = 512;   // TMEM columns: four blocks of O^T, two S
@@ -47,12 +46,13 @@ constexpr uint32_t TM_O = 0, TM_S = 256, TM_COLS = 512;   // TMEM columns: four 
 struct LatArgs {
     const int32_t *bt, *seq_lens, *q_starts, *parents;
     int64_t n_rows, num_blocks;
-    int32_t batch, max_blocks, max_len, max_new, H, nr;   // nr: rows per CTA as the products see them, a multiple of 16
+    int32_t batch, max_blocks, max_len, max_new, H;
+    int32_t nr, ns;                                       // rows per CTA as the products see them, a multiple of 16; stages
     float scale2;                                         // of a score, in log2 units
     uint16_t* out;
     float* lse;
     float* part;   // [slot][nr][LAT]
-    float2* ml;    // [slot][nr] anchor (log2) and sum
+    int4* ml;      // [slot][nr] anchor (log2) and sum; in an item's last part its first part's CTA + 1, and the output row
     KvqWsHeader* hdr;
 };
 
@@ -63,6 +63,7 @@ struct Seq {
     int32_t groups, steps; // of 64 query rows; of tokens, per group
 };
 
+template <int KEYS>
 __device__ __forceinline__ Seq seq_at(const LatArgs& a, int b) {
     Seq s = {0, 0, 0, 0, 0};
     const int first = a.q_starts[b], T = a.seq_lens[b];
@@ -73,15 +74,16 @@ __device__ __forceinline__ Seq seq_at(const LatArgs& a, int b) {
     }
     s.first = first, s.n = (int)cnt, s.T = T;
     s.groups = (int)((cnt * a.H + a.nr - 1) / a.nr);
-    s.steps = s.groups > 0 ? (T + LA_KEYS - 1) / LA_KEYS : 0;
+    s.steps = s.groups > 0 ? (T + KEYS - 1) / KEYS : 0;
     return s;
 }
 
 // One warp: steps of the whole call.
+template <int KEYS>
 __device__ __forceinline__ int64_t all_steps(const LatArgs& a) {
     int64_t sum = 0;
     for (int b = threadIdx.x & 31; b < a.batch; b += 32) {
-        const Seq s = seq_at(a, b);
+        const Seq s = seq_at<KEYS>(a, b);
         sum += (int64_t)s.groups * s.steps;
     }
 #pragma unroll
@@ -91,12 +93,12 @@ __device__ __forceinline__ int64_t all_steps(const LatArgs& a) {
 
 // One warp: the sequence of the x-th entry of a list of `per(sequence)` entries each, the entries before it, and
 // the steps before it; -1 behind the end.
-template <typename Per>
+template <int KEYS, typename Per>
 __device__ __forceinline__ int find_seq(const LatArgs& a, int64_t x, Per per, int64_t* before, int64_t* steps_before) {
     const int lane = threadIdx.x & 31;
     int64_t base = 0, base_steps = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 32) {
-        const Seq s = b0 + lane < a.batch ? seq_at(a, b0 + lane) : Seq{0, 0, 0, 0, 0};
+        const Seq s = b0 + lane < a.batch ? seq_at<KEYS>(a, b0 + lane) : Seq{0, 0, 0, 0, 0};
         const int64_t mine = per(s), steps = (int64_t)s.groups * s.steps;
         int64_t incl = mine, incl_steps = steps;
 #pragma unroll
@@ -118,20 +120,21 @@ __device__ __forceinline__ int find_seq(const LatArgs& a, int64_t x, Per per, in
 }
 
 // A CTA's range, segment by segment: `cnt` steps of one row group from `step` on.
+template <int KEYS>
 struct Segment {
-    int64_t left;      // steps of the range from this segment on
+    int64_t at, end_at;   // where it begins in the list, and where the CTA's range ends
     int32_t b, group, step, cnt;
     Seq s;
-    __device__ __forceinline__ void clip() { cnt = (int)min(left, (int64_t)(s.steps - step)); }
+    __device__ __forceinline__ void clip() { cnt = (int)min(end_at - at, (int64_t)(s.steps - step)); }
     __device__ __forceinline__ bool next(const LatArgs& a) {
-        left -= cnt;
-        if (left <= 0) return false;
+        at += cnt;
+        if (at >= end_at) return false;
         step = 0;
         if (++group == s.groups) {
             group = 0;
             do {
                 if (++b >= a.batch) return false;
-                s = seq_at(a, b);
+                s = seq_at<KEYS>(a, b);
             } while (s.steps == 0);
         }
         clip();
@@ -144,15 +147,26 @@ struct Segment {
         return s.T - s.n + (int)(last / a.H) + 1;
     }
     __device__ __forceinline__ int steps(const LatArgs& a) const {
-        return max(0, min(cnt, (end(a) + LA_KEYS - 1) / LA_KEYS - step));
+        return max(0, min(cnt, (end(a) + KEYS - 1) / KEYS - step));
     }
 };
 
+// A place in a ring of n: the index, and the parity of the rounds before it.
+struct Place {
+    int i = 0;
+    uint32_t round = 0;
+    __device__ __forceinline__ void next(int n) {
+        if (++i == n) i = 0, round ^= 1;
+    }
+};
+
+template <int KEYS, int AHEAD>
 struct Shared {
-    uint64_t q_full, q_free, kv_full[LA_NS], kv_empty[LA_NS], s_full[2], p_full, pv_done[2], drain;
+    uint64_t q_full, q_free, kv_full[LA_MAX_NS], kv_empty[LA_MAX_NS], s_full[AHEAD + 1], p_full[AHEAD + 1], pv_done[AHEAD + 1], drain;
     uint32_t tmem;
     int32_t abort;
-    Segment seg;
+    Segment<KEYS> seg;
+    int64_t per;       // steps per CTA
     float factor[LA_ROWS];
 };
 
@@ -169,49 +183,84 @@ __device__ __forceinline__ bool sm_any(bool x) {
     return r != 0;
 }
 
+// 16 lanes by 32 columns: of column group k (8 columns), v[4k] and v[4k + 1] are row lane / 4, columns 2 (lane % 4) and
+// the one behind it, v[4k + 2] and v[4k + 3] the same of row lane / 4 + 8
+__device__ __forceinline__ void tm_ld_frag(uint32_t addr, float* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(addr)
+        : "memory");
+}
+
+// A row's path to its root, 32 nodes per word, walked through the parents.
+__device__ __forceinline__ void walk_path(const LatArgs& a, int first, int tok, uint32_t* path) {
+    for (int k = tok; k >= 0;) {
+#pragma unroll
+        for (int w = 0; w < KVQ_TREE_WORDS; ++w)
+            if (k >> 5 == w) path[w] |= 1u << (k & 31);
+        const int p = a.parents[first + k];
+        if (p < -1 || p >= k) kvq_dev_flag(a.hdr, KVQ_DEV_BAD_INDEX, p);
+        k = p < -1 || p >= k ? -1 : p;
+    }
+}
+// 32 bits of it from node `from` on
+__device__ __forceinline__ uint32_t path_bits(const uint32_t* path, int from) {
+    const int at = from >> 5;
+    uint32_t lo = 0, hi = 0;
+#pragma unroll
+    for (int i = 0; i < KVQ_TREE_WORDS; ++i) {
+        if (i == at) lo = path[i];
+        if (i == at + 1) hi = path[i];
+    }
+    return __funnelshift_r(lo, hi, from & 31);
+}
+
+template <int KEYS, int AHEAD>
 __global__ void __launch_bounds__(LA_NT, 1)
     latent_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_rows,
                        const __grid_constant__ LatArgs a) {
+    static_assert(KEYS == 32, "a fragment load covers 32 columns");
+    constexpr int STAGE = KEYS / 8 * LA_GROUP, NP = AHEAD + 1;
     extern __shared__ unsigned char raw[];
-    __shared__ Shared S;
+    __shared__ Shared<KEYS, AHEAD> S;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // queries, stages, weights: with nr below 64 the first product reads behind the queries, into the stages, for
     // rows of S that nothing looks at
-    const uint32_t sq = (saddr(raw) + 1023) & ~1023u, skv = sq + a.nr * ROW * 2, sp = skv + LA_NS * LA_STAGE;
+    const uint32_t sq = (saddr(raw) + 1023) & ~1023u, skv = sq + a.nr * ROW * 2, sp = skv + a.ns * STAGE,
+                   p_bytes = a.nr * 128;   // (a row of weights takes 128 bytes, as the swizzle wants it)
     kvq_pdl_begin();
     if (warp == 0) {
-        const int64_t total = all_steps(a);
+        const int64_t total = all_steps<KEYS>(a);
         const int64_t per = latent_range(total, gridDim.x), x = per * blockIdx.x;
         int64_t before, steps_before;
-        Segment g = {0, -1, 0, 0, 0, {0, 0, 0, 0, 0}};
+        Segment<KEYS> g = {x, min(x + per, total), -1, 0, 0, 0, {0, 0, 0, 0, 0}};
         if (x < total) {
-            g.b = find_seq(a, x, [](const Seq& s) { return (int64_t)s.groups * s.steps; }, &before, &steps_before);
-            g.s = seq_at(a, g.b);
+            g.b = find_seq<KEYS>(a, x, [](const Seq& s) { return (int64_t)s.groups * s.steps; }, &before, &steps_before);
+            g.s = seq_at<KEYS>(a, g.b);
             g.group = (int)((x - before) / g.s.steps);
             g.step = (int)((x - before) % g.s.steps);
-            g.left = min(per, total - x);
             g.clip();
         }
-        if (lane == 0) S.seg = g, S.abort = 0;
+        if (lane == 0) S.seg = g, S.per = per, S.abort = 0;
     }
     if (tid == 32) {
         bar_init(&S.q_full, 1);
         bar_init(&S.q_free, 1);
-        for (int i = 0; i < LA_NS; ++i) {
+        for (int i = 0; i < a.ns; ++i) {
             bar_init(&S.kv_full[i], 1);
             bar_init(&S.kv_empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < NP; ++i) {
             bar_init(&S.s_full[i], 1);
+            bar_init(&S.p_full[i], 4);
             bar_init(&S.pv_done[i], 1);
         }
-        bar_init(&S.p_full, 4);
         bar_init(&S.drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    __syncthreads();
-    Segment g = S.seg;
-    if (g.b < 0) return;   // no work
     if (warp == 4) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&S.tmem)), "r"(TM_COLS)
                      : "memory");
@@ -221,13 +270,18 @@ __global__ void __launch_bounds__(LA_NT, 1)
     __syncthreads();
     tc_after();
     const uint32_t tmem = S.tmem;
+    Segment<KEYS> g = S.seg;
+    const int64_t per = S.per;
 
-    if (warp == 5) {
+    if (g.b < 0) {
+        // no work
+    } else if (warp == 5) {
         // ---- loads
         const int nowhere = (int)(a.num_blocks * (PG / 8));   // a group of rows behind the pool: zeros
-        int at = 0;        // steps so far
+        Place st;
+        int loaded = 0;    // steps so far
         bool ok = true;
-        for (int seg = 0; ok; ++seg) {
+        for (int seg = 0; ok;) {
             const int nt = g.steps(a), end = g.end(a);
             if (nt > 0) {
                 if (seg > 0) bar_wait(&S.abort, a.hdr, &S.q_free, (seg - 1) & 1);
@@ -237,12 +291,11 @@ __global__ void __launch_bounds__(LA_NT, 1)
                     tma_3d(sq, &map_q, 0, (int)((int64_t)g.s.first * a.H + (int64_t)g.group * a.nr), 0, &S.q_full);
                 }
                 __syncwarp();
-            } else {
-                --seg;     // (no queries are loaded for it)
+                ++seg;
             }
-            for (int j = 0; j < nt && ok; ++j, ++at) {
-                const int st = at % LA_NS, t0 = (g.step + j) * LA_KEYS;
-                const int pages = min(LA_KEYS / PG, (end - t0 + PG - 1) / PG);
+            for (int j = 0; j < nt && ok; ++j, ++loaded) {
+                const int t0 = (g.step + j) * KEYS;
+                const int pages = min(KEYS / PG, (end - t0 + PG - 1) / PG);
                 int y = nowhere;
                 if (lane < pages) {
                     const int32_t page = a.bt[(int64_t)g.b * a.max_blocks + t0 / PG + lane];
@@ -251,18 +304,19 @@ __global__ void __launch_bounds__(LA_NT, 1)
                     else
                         kvq_dev_flag(a.hdr, KVQ_DEV_BAD_PAGE, page);
                 }
-                if (at >= LA_NS) bar_wait(&S.abort, a.hdr, &S.kv_empty[st], ((at / LA_NS) & 1) ^ 1);
+                if (loaded >= a.ns) bar_wait(&S.abort, a.hdr, &S.kv_empty[st.i], st.round ^ 1);
                 ok = !aborted(&S.abort);
-                int to[LA_KEYS / PG];
+                int to[KEYS / PG];
 #pragma unroll
-                for (int k = 0; k < LA_KEYS / PG; ++k) to[k] = __shfl_sync(0xffffffffu, y, k);
+                for (int k = 0; k < KEYS / PG; ++k) to[k] = __shfl_sync(0xffffffffu, y, k);
                 if (ok && elect()) {
-                    bar_expect(&S.kv_full[st], pages * PG * ROW * 2);
+                    bar_expect(&S.kv_full[st.i], pages * PG * ROW * 2);
 #pragma unroll
-                    for (int k = 0; k < LA_KEYS / PG; ++k)
-                        if (k < pages) tma_page(skv + st * LA_STAGE + k * (PG * ROW * 2), &map_rows, to[k], &S.kv_full[st]);
+                    for (int k = 0; k < KEYS / PG; ++k)
+                        if (k < pages) tma_page(skv + st.i * STAGE + k * (PG * ROW * 2), &map_rows, to[k], &S.kv_full[st.i]);
                 }
                 __syncwarp();
+                st.next(a.ns);
             }
             if (!g.next(a)) break;
         }
@@ -271,142 +325,145 @@ __global__ void __launch_bounds__(LA_NT, 1)
         const uint32_t hi_q = (uint32_t)(smem_desc(0, 16, 1024) >> 32), hi_kv = (uint32_t)(smem_desc(0, 16, LA_GROUP) >> 32);
         const uint32_t lq = (uint32_t)smem_desc(sq, 16, 0), lk = (uint32_t)smem_desc(skv, 16, 0),
                        lv = (uint32_t)smem_desc(skv, 1024, 0), lp = (uint32_t)smem_desc(sp, 16, 0);
-        const uint32_t idesc_s = idesc_f16(64, LA_KEYS), idesc_o = idesc_f16(128, a.nr) | KVQ_A_MN;
+        const uint32_t idesc_s = idesc_f16(64, KEYS), idesc_o = idesc_f16(128, a.nr) | KVQ_A_MN;
         const auto desc = [](uint32_t hi, uint32_t lo) { return (uint64_t)hi << 32 | lo; };
         const uint32_t q_chunk = (uint32_t)a.nr * 128 >> 4;
-        const auto qk = [&](int at) {
+        Place in, s, out, p;   // stage and S of the next first product, stage and P of the next second one
+        const auto qk = [&] {
+            bar_wait(&S.abort, a.hdr, &S.kv_full[in.i], in.round);
+            tc_after();
             if (elect()) {
-                uint32_t x = lq, y = lk + (at % LA_NS * LA_STAGE >> 4);
+                uint32_t x = lq, y = lk + (in.i * STAGE >> 4);
                 asm volatile("" : "+r"(x), "+r"(y));
 #pragma unroll
                 for (int c = 0; c < LA_CHUNKS; ++c) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_ss(TM_S + (at & 1) * LA_KEYS, desc(hi_q, x + 2 * k), desc(hi_kv, y + (c * 1024 >> 4) + 2 * k), idesc_s,
-                               c + k > 0);
+                        mma_ss(TM_S + s.i * KEYS, desc(hi_q, x + 2 * k), desc(hi_kv, y + (c * 1024 >> 4) + 2 * k), idesc_s, c + k > 0);
                     x += q_chunk;
                 }
-                tc_commit(&S.s_full[at & 1]);
+                // (all products so far: where S is there, so is O^T of AHEAD + 1 steps before, and P's place is free)
+                tc_commit(&S.s_full[s.i]);
             }
+            in.next(a.ns);
+            s.next(NP);
         };
-        int at = 0;
-        for (int seg = 0;; ++seg) {
+        for (int seg = 0;;) {
             const int nt = g.steps(a);
             if (nt > 0) {
                 bar_wait(&S.abort, a.hdr, &S.q_full, seg & 1);
-                bar_wait(&S.abort, a.hdr, &S.kv_full[at % LA_NS], (at / LA_NS) & 1);
-                tc_after();
-                qk(at);
-            } else {
-                --seg;
+                ++seg;
+                for (int j = 0; j < min(AHEAD, nt); ++j) qk();
+                if (nt <= AHEAD && elect()) tc_commit(&S.q_free);
             }
-            for (int j = 0; j < nt; ++j, ++at) {
-                if (j + 1 < nt) {
-                    bar_wait(&S.abort, a.hdr, &S.kv_full[(at + 1) % LA_NS], ((at + 1) / LA_NS) & 1);
-                    qk(at + 1);
-                } else if (elect()) {
-                    tc_commit(&S.q_free);
+            for (int j = 0; j < nt; ++j) {
+                if (j + AHEAD < nt) {
+                    qk();
+                    if (j + AHEAD == nt - 1 && elect()) tc_commit(&S.q_free);
                 }
-                bar_wait(&S.abort, a.hdr, &S.p_full, at & 1);
+                bar_wait(&S.abort, a.hdr, &S.p_full[p.i], p.round);
                 tc_after();
                 if (elect()) {
-                    uint32_t y = lv + (at % LA_NS * LA_STAGE >> 4);
-                    asm volatile("" : "+r"(y));
+                    uint32_t y = lv + (out.i * STAGE >> 4), z = lp + (p.i * p_bytes >> 4);
+                    asm volatile("" : "+r"(y), "+r"(z));
 #pragma unroll
                     for (int d = 0; d < LAT / 128; ++d)
 #pragma unroll
-                        for (int k = 0; k < LA_KEYS / 16; ++k)
-                            mma_ss(TM_O + 64 * d, desc(hi_kv, y + ((k * 2 * LA_GROUP + d * 2048) >> 4)), desc(hi_q, lp + 2 * k), idesc_o,
+                        for (int k = 0; k < KEYS / 16; ++k)
+                            mma_ss(TM_O + 64 * d, desc(hi_kv, y + ((k * 2 * LA_GROUP + d * 2048) >> 4)), desc(hi_q, z + 2 * k), idesc_o,
                                    j > 0 || k > 0);
-                    tc_commit(&S.kv_empty[at % LA_NS]);
-                    tc_commit(&S.pv_done[at & 1]);
+                    tc_commit(&S.kv_empty[out.i]);
+                    tc_commit(&S.pv_done[p.i]);
                 }
+                out.next(a.ns);
+                p.next(NP);
             }
             if (!g.next(a)) break;
         }
     } else {
-        // ---- softmax: a lane per row
+        // ---- softmax: a thread has columns 8k + 2 (lane % 4) and the one behind of rows ra and ra + 8
         const uint32_t lane_base = tmem + ((uint32_t)warp << 21);   // TMEM lanes 32 warp ..
-        const int r = 16 * warp + (lane & 15);
-        int at = 0;
+        const int ra = 16 * warp + (lane >> 2), c0 = 2 * (lane & 3);
+        const bool tree = a.parents != nullptr;
+        // `done`: the step before.  Where S of a step is there, O^T of AHEAD + 1 steps before is, so that of the step before
+        // is at most one phase of its barrier away
+        Place st, s_at, done;
         do {
             const int nt = g.steps(a), end = g.end(a), ctx = g.s.T - g.s.n;
-            const int64_t row0 = (int64_t)g.group * a.nr, n_rows = (int64_t)g.s.n * a.H;   // of the sequence
-            const int rows = (int)min((int64_t)a.nr, n_rows - row0);
-            const bool active = 16 * warp < rows, valid = lane < 16 && r < rows;
-            const int tok = valid ? (int)((row0 + r) / a.H) : 0;
-            const bool tree = a.parents != nullptr;
-            uint32_t path[KVQ_TREE_WORDS] = {};
-            if (tree && valid) {
-                for (int k = tok; k >= 0;) {
+            const int64_t row0 = (int64_t)g.group * a.nr;   // of the sequence
+            const int rows = (int)min((int64_t)a.nr, (int64_t)g.s.n * a.H - row0);
+            const bool active = 16 * warp < rows;
+            bool valid[2];
+            int cut[2];                                     // every token before it is seen
+            uint32_t path[2][KVQ_TREE_WORDS] = {};
+            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll
-                    for (int w = 0; w < KVQ_TREE_WORDS; ++w)
-                        if (k >> 5 == w) path[w] |= 1u << (k & 31);
-                    const int p = a.parents[g.s.first + k];
-                    if (p < -1 || p >= k) kvq_dev_flag(a.hdr, KVQ_DEV_BAD_INDEX, p);
-                    k = p < -1 || p >= k ? -1 : p;
-                }
+            for (int i = 0; i < 2; ++i) {
+                valid[i] = ra + 8 * i < rows;
+                const int tok = valid[i] ? (int)((row0 + ra + 8 * i) / a.H) : 0;
+                cut[i] = valid[i] ? (tree ? ctx : ctx + tok + 1) : 0;
+                if (tree && valid[i]) walk_path(a, g.s.first, tok, path[i]);
             }
-            const int cut = tree ? ctx : ctx + tok + 1;     // every token before it is seen
-            const int full = __reduce_min_sync(0xffffffffu, valid ? cut : INT32_MAX);
-            float m = -INFINITY, l = 0.0f;
-            for (int j = 0; j < nt; ++j, ++at) {
-                const int t0 = (g.step + j) * LA_KEYS;
-                bar_wait(&S.abort, a.hdr, &S.s_full[at & 1], (at >> 1) & 1);
+            const int full = __reduce_min_sync(0xffffffffu, min(cut[0], cut[1]));
+            for (int j = 0; j < nt; ++j, done = s_at, st.next(a.ns), s_at.next(NP)) {
+                const int t0 = (g.step + j) * KEYS;
+                bar_wait(&S.abort, a.hdr, &S.s_full[s_at.i], s_at.round);
                 tc_after();
-                if (end < t0 + LA_KEYS) {
+                if (end < t0 + KEYS) {
                     // rows at and behind the end may hold anything: 0 * NaN must not reach O^T
-                    const uint32_t base = skv + at % LA_NS * LA_STAGE;
+                    const uint32_t base = skv + st.i * STAGE;
                     const int r0 = end - t0;
-                    for (int x = tid; x < (LA_KEYS - r0) * (LAT / 8); x += 128) {
+                    for (int x = tid; x < (KEYS - r0) * (LAT / 8); x += 128) {
                         const int row = r0 + x / (LAT / 8), c = x % (LAT / 8);
                         const uint32_t to = base + (row >> 3) * LA_GROUP + (c >> 3) * 1024 + (row & 7) * 128 + (c & 7) * 16;
                         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
                     }
                 }
-                float s[LA_KEYS];
-                float top = -INFINITY;
+                float s[16];
+                float top[2] = {-INFINITY, -INFINITY};
+                bool far = false;
                 if (active) {
-                    const uint32_t ts = lane_base + TM_S + (at & 1) * LA_KEYS;
-                    tm_ld32(ts, reinterpret_cast<uint32_t*>(s));
-                    tm_ld32(ts + 32, reinterpret_cast<uint32_t*>(s) + 32);
-                    const bool edge = t0 + LA_KEYS > full || t0 + LA_KEYS > end;
+                    tm_ld_frag(lane_base + TM_S + s_at.i * KEYS, s);
 #pragma unroll
-                    for (int w = 0; w < LA_KEYS / 32; ++w) {
-                        uint32_t bits = valid ? below(cut - t0 - 32 * w) : 0u;
-                        if (tree && edge && valid) {
-                            const int from = t0 + 32 * w - ctx, at_w = from >> 5;
-                            uint32_t lo = 0, hi = 0;
+                    for (int c = 0; c < 16; ++c) s[c] = __fmul_rn(s[c], a.scale2);
+                    if (t0 + KEYS > full) {   // (full: what every row of the warp sees all of)
 #pragma unroll
-                            for (int i = 0; i < KVQ_TREE_WORDS; ++i) {
-                                if (i == at_w) lo = path[i];
-                                if (i == at_w + 1) hi = path[i];
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t bits = below(cut[i] - t0);
+                            if (tree && valid[i]) bits |= path_bits(path[i], t0 - ctx);
+                            bits >>= c0;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                if (!(bits >> (8 * k) & 1)) s[4 * k + 2 * i] = -INFINITY;
+                                if (!(bits >> (8 * k) & 2)) s[4 * k + 2 * i + 1] = -INFINITY;
                             }
-                            bits |= __funnelshift_r(lo, hi, from & 31);
-                        }
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            const float x = __fmul_rn(s[32 * w + c], a.scale2);
-                            s[32 * w + c] = bits >> c & 1 ? x : -INFINITY;
                         }
                     }
 #pragma unroll
-                    for (int c = 0; c < LA_KEYS; ++c) top = fmaxf(top, s[c]);
+                    for (int i = 0; i < 2; ++i) {
+                        const float x = max3(s[2 * i], s[2 * i + 1], fmaxf(s[4 + 2 * i], s[5 + 2 * i]));
+                        top[i] = max3(x, fmaxf(s[8 + 2 * i], s[9 + 2 * i]), fmaxf(s[12 + 2 * i], s[13 + 2 * i]));
+                        // a first anchor, or a weight that would leave fp16's range (any lane of the row's four tells)
+                        far |= m[i] == -INFINITY ? top[i] > m[i] : top[i] - m[i] > LA_TOP;
+                    }
                 }
-                // (a first anchor, or a weight that would leave fp16's range)
-                const bool far = valid && (m == -INFINITY ? top > m : top - m > LA_TOP);
                 if (sm_any(far)) {
                     // one row's turn is every row's: an anchor that would have to follow later is set now
-                    float f = 1.0f;
-                    if (valid && (m == -INFINITY ? top > m : top - m > LA_HEAD)) {
-                        const float anchor = top - LA_HEAD;
-                        f = ex2(m - anchor);
-                        m = anchor;
-                        l *= f;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float x = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                        float f = 1.0f;
+                        if (m[i] == -INFINITY ? x > m[i] : x - m[i] > LA_HEAD) {
+                            const float anchor = x - LA_HEAD;
+                            f = ex2(m[i] - anchor);
+                            m[i] = anchor;
+                            l[i] *= f;
+                        }
+                        if ((lane & 3) == 0) S.factor[ra + 8 * i] = f;
                     }
                     if (j > 0) {
-                        if (lane < 16) S.factor[r] = f;
-                        bar_wait(&S.abort, a.hdr, &S.pv_done[(at - 1) & 1], ((at - 1) >> 1) & 1);
+                        bar_wait(&S.abort, a.hdr, &S.pv_done[done.i], done.round);
                         tc_after();
                         sm_any(false);
                         for (int d = 0; d < LAT / 128; ++d)
@@ -420,63 +477,65 @@ __global__ void __launch_bounds__(LA_NT, 1)
                         tm_wait_st();
                     }
                 }
-                // P's place is free when the products before are done
-                if (at > 0) bar_wait(&S.abort, a.hdr, &S.pv_done[(at - 1) & 1], ((at - 1) >> 1) & 1);
                 if (active) {
-                    const float ms = m == -INFINITY ? 0.0f : m;
-                    float sum = 0.0f;
+                    const uint32_t to = sp + s_at.i * p_bytes + (ra >> 3) * 1024 + (ra & 7) * 128 + 4 * (lane & 3);
 #pragma unroll
-                    for (int c = 0; c < LA_KEYS; c += 8) {
-                        uint32_t p[4];
+                    for (int i = 0; i < 2; ++i) {
+                        const float ms = m[i] == -INFINITY ? 0.0f : m[i];
+                        float e[8];
 #pragma unroll
-                        for (int x = 0; x < 8; x += 2) {
-                            const float e0 = ex2(s[c + x] - ms), e1 = ex2(s[c + x + 1] - ms);
-                            sum += e0 + e1;
-                            p[x / 2] = half2_bits(e0, e1);
-                        }
-                        const uint32_t to = sp + (r >> 3) * 1024 + (r & 7) * 128 + (((c >> 3) ^ (r & 7)) << 4);
-                        if (lane < 16)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3])
+                        for (int k = 0; k < 4; ++k) e[2 * k] = ex2(s[4 * k + 2 * i] - ms), e[2 * k + 1] = ex2(s[4 * k + 2 * i + 1] - ms);
+                        l[i] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + 1024 * i + ((k ^ (ra & 7)) << 4)),
+                                         "r"(half2_bits(e[2 * k], e[2 * k + 1]))
                                          : "memory");
                     }
-                    l += sum;
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 tc_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(&S.p_full);
+                if (lane == 0) bar_arrive(&S.p_full[s_at.i]);
             }
             // ---- the segment's rows: to the output, or as a part of them
-            const bool whole = g.step == 0 && g.cnt == g.s.steps;
-            if (nt > 0) {
-                bar_wait(&S.abort, a.hdr, &S.pv_done[(at - 1) & 1], ((at - 1) >> 1) & 1);
-                tc_after();
-                const int64_t out_row = (int64_t)g.s.first * a.H + row0;
-                const int64_t slot = 2 * (int64_t)blockIdx.x + (g.step == 0 ? 1 : 0);
-                if (valid) {
-                    S.factor[r] = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
-                    if (!whole) a.ml[slot * a.nr + r] = make_float2(m, l);
-                    if (whole && a.lse != nullptr) a.lse[out_row + r] = l == 0.0f ? -INFINITY : (m + log2f(l)) * KVQ_LN2;
-                }
-                sm_any(false);
-                if (!aborted(&S.abort)) {
-                    for (int d = 0; d < LAT / 128; ++d)
-                        for (int c = 0; c < rows; c += 16) {
-                            uint32_t o[16];
-                            tm_ld16(lane_base + TM_O + 64 * d + c, o);
-                            const int dim = 128 * d + 32 * warp + lane;
+            const bool whole = g.step == 0 && g.cnt == g.s.steps, last = g.step + g.cnt == g.s.steps;
+            const int64_t out_row = (int64_t)g.s.first * a.H + row0;
+            const int64_t slot = 2 * (int64_t)blockIdx.x + (g.step == 0 ? 1 : 0);
+            if (nt > 0) bar_wait(&S.abort, a.hdr, &S.pv_done[done.i], done.round);
+            tc_after();
 #pragma unroll
-                            for (int x = 0; x < 16; ++x) {
-                                if (c + x >= rows) break;
-                                const float v = __uint_as_float(o[x]) * S.factor[c + x];
-                                if (whole)
-                                    a.out[(out_row + c + x) * LAT + dim] = kvq_f2h(v);
-                                else
-                                    a.part[(slot * a.nr + c + x) * LAT + dim] = v;
-                            }
-                        }
-                }
+            for (int i = 0; i < 2; ++i) {
+                float sum = l[i] + __shfl_xor_sync(0xffffffffu, l[i], 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                const int r = ra + 8 * i;
+                if (!valid[i] || (lane & 3) != 0) continue;
+                S.factor[r] = whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
+                // (an item's last part is its CTA's first segment: the launch behind this one looks there)
+                if (!whole)
+                    a.ml[slot * a.nr + r] = make_int4(__float_as_int(m[i]), __float_as_int(sum),
+                                                      last ? (int)((g.at - g.step) / per) + 1 : 0, (int)(out_row + r));
+                if (whole && a.lse != nullptr) a.lse[out_row + r] = sum == 0.0f ? -INFINITY : (m[i] + log2f(sum)) * KVQ_LN2;
             }
+            sm_any(false);
+            if (nt > 0 && !aborted(&S.abort)) {
+                for (int d = 0; d < LAT / 128; ++d)
+                    for (int c = 0; c < rows; c += 16) {
+                        uint32_t o[16];
+                        tm_ld16(lane_base + TM_O + 64 * d + c, o);
+                        const int dim = 128 * d + 32 * warp + lane;
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) {
+                            if (c + x >= rows) break;
+                            const float v = __uint_as_float(o[x]) * S.factor[c + x];
+                            if (whole)
+                                a.out[(out_row + c + x) * LAT + dim] = kvq_f2h(v);
+                            else
+                                a.part[(slot * a.nr + c + x) * LAT + dim] = v;
+                        }
+                    }
+            }
+            tc_before();   // (O^T is read before the next segment's first weights are handed over)
         } while (g.next(a));
     }
     __syncwarp();
@@ -489,64 +548,45 @@ __global__ void __launch_bounds__(LA_NT, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TM_COLS) : "memory");
 }
 
-// Joins the parts of a row group's rows in the order of the CTAs and leaves the workspace zeroed.  A CTA per (row
-// group, row): GR groups of 128 threads take every GR-th part, four values per thread.
+// Joins the parts of a row in the order of their CTAs and leaves the workspace zeroed.  A CTA per (CTA of the launch
+// before, row): where that one's first segment ended a row group, it left the first part's CTA behind.  GR groups of
+// 128 threads take every GR-th part, four values per thread.
 template <int GR>
-__global__ void __launch_bounds__(128 * GR) latent_join_kernel(const __grid_constant__ LatArgs a, int ctas) {
-    __shared__ int64_t item[4];              // first part's CTA, parts, whether the first part is a last segment, the output row
+__global__ void __launch_bounds__(128 * GR) latent_join_kernel(const __grid_constant__ LatArgs a) {
     __shared__ float weight[KVQ_LATENT_MAX_CTAS];
     __shared__ float4 sums[GR][128];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = blockIdx.y;
+    const int tid = threadIdx.x, lane = tid & 31, c1 = blockIdx.x, r = blockIdx.y;
     kvq_pdl_begin();
-    if (warp == 0) {
-        const int64_t per = latent_range(all_steps(a), ctas);
-        int64_t before = 0, base = 0;
-        const int b = find_seq(a, blockIdx.x, [](const Seq& s) { return (int64_t)s.groups; }, &before, &base);
-        if (lane == 0) item[1] = 0;
-        if (b >= 0) {
-            const Seq s = seq_at(a, b);
-            const int group = (int)(blockIdx.x - before);
-            base += (int64_t)group * s.steps;
-            const int64_t c0 = base / per, c1 = (base + s.steps - 1) / per;
-            const bool mine = c1 > c0 && (int64_t)group * a.nr + r < (int64_t)s.n * a.H;
-            if (mine) {
-                // weights of the parts: 2^(anchor - largest anchor); a part without a visible token wrote no row
-                const auto slot_of = [&](int64_t c) { return 2 * c + (base >= c * per ? 1 : 0); };
-                float mx = -INFINITY, y = 0.0f;
-                for (int64_t c = c0 + lane; c <= c1; c += 32) {
-                    const float2 v = a.ml[slot_of(c) * a.nr + r];
-                    if (v.y != 0.0f) mx = fmaxf(mx, v.x);
-                }
-                mx = kvq_warp_max(mx);
-                for (int64_t c = c0 + lane; c <= c1; c += 32) {
-                    float2* at = a.ml + slot_of(c) * a.nr + r;
-                    const float2 v = *at;
-                    const float f = v.y != 0.0f ? exp2f(v.x - mx) : 0.0f;
-                    weight[c - c0] = f;
-                    y += f * v.y;
-                    *at = make_float2(0.0f, 0.0f);
-                }
-                // (every lane's sum is over its own parts, joined in one order)
-                y = kvq_warp_sum(y);
-                const int64_t row = (int64_t)s.first * a.H + (int64_t)group * a.nr + r;
-                const float inv = y == 0.0f ? 0.0f : 1.0f / y;
-                for (int c = lane; c <= c1 - c0; c += 32) weight[c] *= inv;
-                if (lane == 0) {
-                    item[0] = c0, item[1] = c1 - c0 + 1, item[2] = base >= c0 * per, item[3] = row;
-                    if (a.lse != nullptr) a.lse[row] = y == 0.0f ? -INFINITY : (mx + log2f(y)) * KVQ_LN2;
-                }
-            }
+    const int4 end = a.ml[(int64_t)2 * c1 * a.nr + r];
+    if (end.z == 0) return;
+    const int c0 = end.z - 1, n = c1 - c0 + 1;
+    // the first part is its CTA's last segment, the others are their CTAs' first ones
+    const auto slot_of = [&](int i) { return ((int64_t)2 * (c0 + i) + (i == 0 ? 1 : 0)) * a.nr + r; };
+    const auto part_of = [&](int i) { return reinterpret_cast<float4*>(a.part + slot_of(i) * LAT) + (tid & 127); };
+    if (tid < 32) {
+        // weights of the parts: 2^(anchor - largest anchor); a part without a visible token wrote no row
+        float mx = -INFINITY, y = 0.0f;
+        for (int i = lane; i < n; i += 32) {
+            const int4 v = a.ml[slot_of(i)];
+            if (__int_as_float(v.y) != 0.0f) mx = fmaxf(mx, __int_as_float(v.x));
         }
+        mx = kvq_warp_max(mx);
+        for (int i = lane; i < n; i += 32) {
+            const int4 v = a.ml[slot_of(i)];
+            const float sum = __int_as_float(v.y), f = sum != 0.0f ? exp2f(__int_as_float(v.x) - mx) : 0.0f;
+            weight[i] = f;
+            y += f * sum;
+        }
+        // (every lane's sum is over its own parts, joined in one order)
+        y = kvq_warp_sum(y);
+        const float inv = y == 0.0f ? 0.0f : 1.0f / y;
+        for (int i = lane; i < n; i += 32) weight[i] *= inv;
+        if (lane == 0 && a.lse != nullptr) a.lse[end.w] = y == 0.0f ? -INFINITY : (mx + log2f(y)) * KVQ_LN2;
     }
     __syncthreads();
-    const int n = (int)item[1], grp = tid >> 7, x = tid & 127;
-    if (n == 0) return;
-    // the first part is its CTA's last segment (or its only one, which may begin inside the row group: its first)
-    const auto part_of = [&](int i) {
-        const int64_t slot = 2 * (item[0] + i) + (i == 0 ? item[2] : 0);
-        return reinterpret_cast<float4*>(a.part + (slot * a.nr + r) * LAT) + x;
-    };
+    for (int i = tid; i < n; i += 128 * GR) a.ml[slot_of(i)] = make_int4(0, 0, 0, 0);
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const int grp = tid >> 7;
 #pragma unroll 8
     for (int i = grp; i < n; i += GR) {
         const float4 v = *part_of(i);
@@ -556,22 +596,24 @@ __global__ void __launch_bounds__(128 * GR) latent_join_kernel(const __grid_cons
     // (behind the loads: a store between them would hold up the next one)
     for (int i = grp; i < n; i += GR) *part_of(i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (GR > 1) {
-        sums[grp][x] = o;
+        sums[grp][tid & 127] = o;
         __syncthreads();
         if (grp > 0) return;
         for (int k = 1; k < GR; ++k) {
-            const float4 v = sums[k][x];
+            const float4 v = sums[k][tid];
             o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
         }
     }
-    reinterpret_cast<uint2*>(a.out + item[3] * LAT)[x] = make_uint2(half2_bits(o.x, o.y), half2_bits(o.z, o.w));
+    reinterpret_cast<uint2*>(a.out + (int64_t)end.w * LAT)[tid & 127] = make_uint2(half2_bits(o.x, o.y), half2_bits(o.z, o.w));
 }
 
 struct LatPlan {
-    int nr, ctas;
+    int nr, ns, ahead, ctas;
     int64_t items;
     size_t smem, off_ml, off_part, bytes;
 };
+
+constexpr int LP_KEYS = 32;
 
 LatPlan latent_plan(const kvq_seqs* S, int32_t n_heads, int64_t n_rows, int32_t max_new) {
     LatPlan p;
@@ -579,12 +621,16 @@ LatPlan latent_plan(const kvq_seqs* S, int32_t n_heads, int64_t n_rows, int32_t 
     p.nr = std::max(p.nr, 16);
     const int64_t by_max = S->batch * (((int64_t)max_new * n_heads + p.nr - 1) / p.nr);
     p.items = std::max<int64_t>(1, std::min(by_max, n_rows * n_heads / p.nr + S->batch));
-    const int64_t steps = p.items * ((S->max_len + LA_KEYS - 1) / LA_KEYS);
+    const int64_t steps = p.items * ((S->max_len + LP_KEYS - 1) / LP_KEYS);
     p.ctas = (int)std::max<int64_t>(1, std::min<int64_t>({steps, kvq_num_sms(), KVQ_LATENT_MAX_CTAS}));
-    p.smem = 1024 + LA_NS * LA_STAGE + LA_ROWS * 128 + (size_t)p.nr * ROW * 2;
+    // two steps of S ahead where the stages are there for it
+    p.ahead = p.nr <= 32 ? 2 : 1;
+    const size_t stage = LP_KEYS / 8 * LA_GROUP, fixed = 1024 + (size_t)p.nr * (ROW * 2 + (p.ahead + 1) * 128);
+    p.ns = (int)std::min<size_t>((LA_SMEM - fixed) / stage, LA_MAX_NS);
+    p.smem = fixed + p.ns * stage;
     const size_t rows = (size_t)2 * p.ctas * p.nr;
     p.off_ml = sizeof(KvqWsHeader);
-    p.off_part = kvq_round_up(p.off_ml + rows * sizeof(float2), 256);
+    p.off_part = kvq_round_up(p.off_ml + rows * sizeof(int4), 256);
     p.bytes = kvq_round_up(p.off_part + rows * LAT * sizeof(float), 256);
     return p;
 }
@@ -624,23 +670,27 @@ extern "C" int kv_latent_attn(const kvq_latent* C, const kvq_seqs* S, int32_t n_
     const uint32_t rb[4] = {64, 8, LA_CHUNKS, PG / 8};
     st = make_map(&map_q, q, 3, qd, qs, qb, fn);
     if (!st) st = make_map(&map_rows, C->rows, 4, rd, rs, rb, fn);
-    if (!st) st = kvq_prepare_kernel((const void*)latent_attn_kernel, (int)p.smem);
     if (st) return st;
     a.bt = S->block_table, a.seq_lens = S->seq_lens, a.q_starts = q_starts, a.parents = parents;
     a.n_rows = n_rows, a.num_blocks = C->num_blocks;
-    a.batch = S->batch, a.max_blocks = S->max_blocks, a.max_len = S->max_len, a.max_new = max_new, a.H = n_heads, a.nr = p.nr;
+    a.batch = S->batch, a.max_blocks = S->max_blocks, a.max_len = S->max_len, a.max_new = max_new, a.H = n_heads, a.nr = p.nr, a.ns = p.ns;
     a.out = out, a.lse = lse, a.hdr = static_cast<KvqWsHeader*>(ws);
-    a.ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + p.off_ml);
+    a.ml = reinterpret_cast<int4*>(static_cast<char*>(ws) + p.off_ml);
     a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.off_part);
-    cudaError_t e = kvq_launch_pdl(latent_attn_kernel, dim3(p.ctas), dim3(LA_NT), p.smem, kvq_stream(stream), map_q, map_rows, a);
-    if (e == cudaSuccess && p.ctas > 1) {
-        // few row groups have many parts each
-        const dim3 grid((unsigned)p.items, p.nr);
-        if (p.items * 8 <= p.ctas)
-            e = kvq_launch_pdl(latent_join_kernel<8>, grid, dim3(1024), 0, kvq_stream(stream), a, p.ctas);
-        else
-            e = kvq_launch_pdl(latent_join_kernel<1>, grid, dim3(128), 0, kvq_stream(stream), a, p.ctas);
-    }
+    const auto go = [&](auto kernel) {
+        const int rc = kvq_prepare_kernel((const void*)kernel, (int)p.smem);
+        if (rc) return rc;
+        const cudaError_t e = kvq_launch_pdl(kernel, dim3(p.ctas), dim3(LA_NT), p.smem, kvq_stream(stream), map_q, map_rows, a);
+        return e == cudaSuccess ? (int)KVQ_OK : kvq_fail(KVQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+    };
+    st = p.ahead == 2 ? go(latent_attn_kernel<LP_KEYS, 2>) : go(latent_attn_kernel<LP_KEYS, 1>);
+    if (st || p.ctas == 1) return st;
+    const dim3 grid(p.ctas, p.nr);
+    // few row groups have many parts each
+    const int64_t parts = p.ctas / p.items;
+    const cudaError_t e = parts > 32  ? kvq_launch_pdl(latent_join_kernel<8>, grid, dim3(1024), 0, kvq_stream(stream), a)
+                          : parts > 6 ? kvq_launch_pdl(latent_join_kernel<2>, grid, dim3(256), 0, kvq_stream(stream), a)
+                                      : kvq_launch_pdl(latent_join_kernel<1>, grid, dim3(128), 0, kvq_stream(stream), a);
     if (e != cudaSuccess) return kvq_fail(KVQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
     return KVQ_OK;
 }
