@@ -183,16 +183,30 @@ __device__ __forceinline__ bool sm_any(bool x) {
     return r != 0;
 }
 
-// 16 lanes by 32 columns: of column group k (8 columns), v[4k] and v[4k + 1] are row lane / 4, columns 2 (lane % 4) and
+// 16 lanes by KEYS columns: of column group k (8 columns), v[4k] and v[4k + 1] are row lane / 4, columns 2 (lane % 4) and
 // the one behind it, v[4k + 2] and v[4k + 3] the same of row lane / 4 + 8
+template <int KEYS>
 __device__ __forceinline__ void tm_ld_frag(uint32_t addr, float* v) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-        "tcgen05.wait::ld.sync.aligned;"
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
           "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
         : "r"(addr)
         : "memory");
+    if (KEYS == 48)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+            : "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23])
+            : "r"(addr + 32)
+            : "memory");
+    // (the wait names the registers, so that nothing reads them before it)
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
+                   "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+                 :
+                 : "memory");
+    if (KEYS == 48)
+        asm volatile("" : "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23])::"memory");
 }
 
 // A row's path to its root, 32 nodes per word, walked through the parents.
@@ -222,8 +236,8 @@ template <int KEYS, int AHEAD>
 __global__ void __launch_bounds__(LA_NT, 1)
     latent_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_rows,
                        const __grid_constant__ LatArgs a) {
-    static_assert(KEYS == 32, "a fragment load covers 32 columns");
-    constexpr int STAGE = KEYS / 8 * LA_GROUP, NP = AHEAD + 1;
+    static_assert(KEYS == 32 || KEYS == 48, "columns of the fragment loads");
+    constexpr int STAGE = KEYS / 8 * LA_GROUP, NP = AHEAD + 1, NG = KEYS / 8;
     extern __shared__ unsigned char raw[];
     __shared__ Shared<KEYS, AHEAD> S;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -321,7 +335,8 @@ __global__ void __launch_bounds__(LA_NT, 1)
             if (!g.next(a)) break;
         }
     } else if (warp == 4) {
-        // ---- tensor cores: the whole warp walks the loop and one elected lane issues
+        // ---- tensor cores: one lane walks the loop (elected anew for every batch, it starts some 100 cycles later)
+        if (elect()) {
         const uint32_t hi_q = (uint32_t)(smem_desc(0, 16, 1024) >> 32), hi_kv = (uint32_t)(smem_desc(0, 16, LA_GROUP) >> 32);
         const uint32_t lq = (uint32_t)smem_desc(sq, 16, 0), lk = (uint32_t)smem_desc(skv, 16, 0),
                        lv = (uint32_t)smem_desc(skv, 1024, 0), lp = (uint32_t)smem_desc(sp, 16, 0);
@@ -332,7 +347,7 @@ __global__ void __launch_bounds__(LA_NT, 1)
         const auto qk = [&] {
             bar_wait(&S.abort, a.hdr, &S.kv_full[in.i], in.round);
             tc_after();
-            if (elect()) {
+            {
                 uint32_t x = lq, y = lk + (in.i * STAGE >> 4);
                 asm volatile("" : "+r"(x), "+r"(y));
 #pragma unroll
@@ -354,16 +369,16 @@ __global__ void __launch_bounds__(LA_NT, 1)
                 bar_wait(&S.abort, a.hdr, &S.q_full, seg & 1);
                 ++seg;
                 for (int j = 0; j < min(AHEAD, nt); ++j) qk();
-                if (nt <= AHEAD && elect()) tc_commit(&S.q_free);
+                if (nt <= AHEAD) tc_commit(&S.q_free);
             }
             for (int j = 0; j < nt; ++j) {
                 if (j + AHEAD < nt) {
                     qk();
-                    if (j + AHEAD == nt - 1 && elect()) tc_commit(&S.q_free);
+                    if (j + AHEAD == nt - 1) tc_commit(&S.q_free);
                 }
                 bar_wait(&S.abort, a.hdr, &S.p_full[p.i], p.round);
                 tc_after();
-                if (elect()) {
+                {
                     uint32_t y = lv + (out.i * STAGE >> 4), z = lp + (p.i * p_bytes >> 4);
                     asm volatile("" : "+r"(y), "+r"(z));
 #pragma unroll
@@ -379,6 +394,7 @@ __global__ void __launch_bounds__(LA_NT, 1)
                 p.next(NP);
             }
             if (!g.next(a)) break;
+        }
         }
     } else {
         // ---- softmax: a thread has columns 8k + 2 (lane % 4) and the one behind of rows ra and ra + 8
@@ -419,21 +435,22 @@ __global__ void __launch_bounds__(LA_NT, 1)
                         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
                     }
                 }
-                float s[16];
+                float s[4 * NG];
                 float top[2] = {-INFINITY, -INFINITY};
                 bool far = false;
                 if (active) {
-                    tm_ld_frag(lane_base + TM_S + s_at.i * KEYS, s);
+                    tm_ld_frag<KEYS>(lane_base + TM_S + s_at.i * KEYS, s);
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) s[c] = __fmul_rn(s[c], a.scale2);
+                    for (int c = 0; c < 4 * NG; ++c) s[c] = __fmul_rn(s[c], a.scale2);
                     if (t0 + KEYS > full) {   // (full: what every row of the warp sees all of)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            uint32_t bits = below(cut[i] - t0);
-                            if (tree && valid[i]) bits |= path_bits(path[i], t0 - ctx);
+                            uint64_t bits = (uint64_t)below(cut[i] - t0 - 32) << 32 | below(cut[i] - t0);
+                            if (tree && valid[i])
+                                bits |= (uint64_t)path_bits(path[i], t0 + 32 - ctx) << 32 | path_bits(path[i], t0 - ctx);
                             bits >>= c0;
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
+                            for (int k = 0; k < NG; ++k) {
                                 if (!(bits >> (8 * k) & 1)) s[4 * k + 2 * i] = -INFINITY;
                                 if (!(bits >> (8 * k) & 2)) s[4 * k + 2 * i + 1] = -INFINITY;
                             }
@@ -441,8 +458,8 @@ __global__ void __launch_bounds__(LA_NT, 1)
                     }
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float x = max3(s[2 * i], s[2 * i + 1], fmaxf(s[4 + 2 * i], s[5 + 2 * i]));
-                        top[i] = max3(x, fmaxf(s[8 + 2 * i], s[9 + 2 * i]), fmaxf(s[12 + 2 * i], s[13 + 2 * i]));
+#pragma unroll
+                        for (int k = 0; k < NG; ++k) top[i] = max3(top[i], s[4 * k + 2 * i], s[4 * k + 2 * i + 1]);
                         // a first anchor, or a weight that would leave fp16's range (any lane of the row's four tells)
                         far |= m[i] == -INFINITY ? top[i] > m[i] : top[i] - m[i] > LA_TOP;
                     }
@@ -482,15 +499,15 @@ __global__ void __launch_bounds__(LA_NT, 1)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const float ms = m[i] == -INFINITY ? 0.0f : m[i];
-                        float e[8];
+                        float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) e[2 * k] = ex2(s[4 * k + 2 * i] - ms), e[2 * k + 1] = ex2(s[4 * k + 2 * i + 1] - ms);
-                        l[i] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + 1024 * i + ((k ^ (ra & 7)) << 4)),
-                                         "r"(half2_bits(e[2 * k], e[2 * k + 1]))
+                        for (int k = 0; k < NG; ++k) {
+                            const float e0 = ex2(s[4 * k + 2 * i] - ms), e1 = ex2(s[4 * k + 2 * i + 1] - ms);
+                            sum[k & 1] += e0 + e1;
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + 1024 * i + ((k ^ (ra & 7)) << 4)), "r"(half2_bits(e0, e1))
                                          : "memory");
+                        }
+                        l[i] += sum[0] + sum[1];
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -608,12 +625,10 @@ __global__ void __launch_bounds__(128 * GR) latent_join_kernel(const __grid_cons
 }
 
 struct LatPlan {
-    int nr, ns, ahead, ctas;
+    int nr, ns, keys, ahead, ctas;
     int64_t items;
     size_t smem, off_ml, off_part, bytes;
 };
-
-constexpr int LP_KEYS = 32;
 
 LatPlan latent_plan(const kvq_seqs* S, int32_t n_heads, int64_t n_rows, int32_t max_new) {
     LatPlan p;
@@ -621,11 +636,11 @@ LatPlan latent_plan(const kvq_seqs* S, int32_t n_heads, int64_t n_rows, int32_t 
     p.nr = std::max(p.nr, 16);
     const int64_t by_max = S->batch * (((int64_t)max_new * n_heads + p.nr - 1) / p.nr);
     p.items = std::max<int64_t>(1, std::min(by_max, n_rows * n_heads / p.nr + S->batch));
-    const int64_t steps = p.items * ((S->max_len + LP_KEYS - 1) / LP_KEYS);
+    p.keys = p.nr <= 32 ? 48 : 32;
+    p.ahead = 1;
+    const int64_t steps = p.items * ((S->max_len + p.keys - 1) / p.keys);
     p.ctas = (int)std::max<int64_t>(1, std::min<int64_t>({steps, kvq_num_sms(), KVQ_LATENT_MAX_CTAS}));
-    // two steps of S ahead where the stages are there for it
-    p.ahead = p.nr <= 32 ? 2 : 1;
-    const size_t stage = LP_KEYS / 8 * LA_GROUP, fixed = 1024 + (size_t)p.nr * (ROW * 2 + (p.ahead + 1) * 128);
+    const size_t stage = p.keys / 8 * LA_GROUP, fixed = 1024 + (size_t)p.nr * (ROW * 2 + (p.ahead + 1) * 128);
     p.ns = (int)std::min<size_t>((LA_SMEM - fixed) / stage, LA_MAX_NS);
     p.smem = fixed + p.ns * stage;
     const size_t rows = (size_t)2 * p.ctas * p.nr;
@@ -683,7 +698,7 @@ extern "C" int kv_latent_attn(const kvq_latent* C, const kvq_seqs* S, int32_t n_
         const cudaError_t e = kvq_launch_pdl(kernel, dim3(p.ctas), dim3(LA_NT), p.smem, kvq_stream(stream), map_q, map_rows, a);
         return e == cudaSuccess ? (int)KVQ_OK : kvq_fail(KVQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
     };
-    st = p.ahead == 2 ? go(latent_attn_kernel<LP_KEYS, 2>) : go(latent_attn_kernel<LP_KEYS, 1>);
+    st = p.keys == 48 ? go(latent_attn_kernel<48, 1>) : go(latent_attn_kernel<32, 1>);
     if (st || p.ctas == 1) return st;
     const dim3 grid(p.ctas, p.nr);
     // few row groups have many parts each
