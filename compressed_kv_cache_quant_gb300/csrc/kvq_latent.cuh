@@ -23,6 +23,3 @@ static inline int latent_scale(float scale, const char* fn, float* scale2) {
     KVQ_REQUIRE(std::isfinite(*scale2), KVQ_ERR_INVALID_ARG, "%s: scale", fn);
     return KVQ_OK;
 }
-
-// Steps per CTA of a list of `total`.
-__device__ __forceinline__ int64_t latent_range(int64_t total, int ctas) { return max((total + ctas - 1) / ctas, (int64_t)1); }

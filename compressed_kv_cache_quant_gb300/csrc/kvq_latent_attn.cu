@@ -52,7 +52,8 @@ struct LatArgs {
     uint16_t* out;
     float* lse;
     float* part;   // [slot][nr][LAT]
-    int4* ml;      // [slot][nr] anchor (log2) and sum; in an item's last part its first part's CTA + 1, and the output row
+    float2* ml;    // [slot][nr] anchor (log2) and sum
+    int4* cuts;    // [row group][nr] of a row in parts: its first part's CTA + 1, its parts, its row of the output
     KvqWsHeader* hdr;
 };
 
@@ -73,63 +74,33 @@ __device__ __forceinline__ Seq seq_at(const LatArgs& a, int b) {
         return s;
     }
     s.first = first, s.n = (int)cnt, s.T = T;
-    s.groups = (int)((cnt * a.H + a.nr - 1) / a.nr);
+    s.groups = (int)(((uint32_t)s.n * a.H + a.nr - 1) / (uint32_t)a.nr);   // (rows of all heads are below 2^31)
     s.steps = s.groups > 0 ? (T + KEYS - 1) / KEYS : 0;
     return s;
 }
 
-// One warp: steps of the whole call.
-template <int KEYS>
-__device__ __forceinline__ int64_t all_steps(const LatArgs& a) {
-    int64_t sum = 0;
-    for (int b = threadIdx.x & 31; b < a.batch; b += 32) {
-        const Seq s = seq_at<KEYS>(a, b);
-        sum += (int64_t)s.groups * s.steps;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    return sum;
-}
-
-// One warp: the sequence of the x-th entry of a list of `per(sequence)` entries each, the entries before it, and
-// the steps before it; -1 behind the end.
-template <int KEYS, typename Per>
-__device__ __forceinline__ int find_seq(const LatArgs& a, int64_t x, Per per, int64_t* before, int64_t* steps_before) {
-    const int lane = threadIdx.x & 31;
-    int64_t base = 0, base_steps = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += 32) {
-        const Seq s = b0 + lane < a.batch ? seq_at<KEYS>(a, b0 + lane) : Seq{0, 0, 0, 0, 0};
-        const int64_t mine = per(s), steps = (int64_t)s.groups * s.steps;
-        int64_t incl = mine, incl_steps = steps;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t u = __shfl_up_sync(0xffffffffu, incl, o), v = __shfl_up_sync(0xffffffffu, incl_steps, o);
-            if (lane >= o) incl += u, incl_steps += v;
-        }
-        const unsigned who = __ballot_sync(0xffffffffu, x >= base + incl - mine && x < base + incl);
-        if (who) {
-            const int src = __ffs(who) - 1;
-            *before = __shfl_sync(0xffffffffu, base + incl - mine, src);
-            *steps_before = __shfl_sync(0xffffffffu, base_steps + incl_steps - steps, src);
-            return b0 + src;
-        }
-        base += __shfl_sync(0xffffffffu, incl, 31);
-        base_steps += __shfl_sync(0xffffffffu, incl_steps, 31);
-    }
-    return -1;
-}
-
-// A CTA's range, segment by segment: `cnt` steps of one row group from `step` on.
+// A CTA's range, segment by segment: `cnt` steps of one row group from `step` on, of which the first nt hold a token
+// that some row of the group sees; those end before token `end`.
 template <int KEYS>
 struct Segment {
-    int64_t at, end_at;   // where it begins in the list, and where the CTA's range ends
-    int32_t b, group, step, cnt;
+    int32_t at, end_at;   // where it begins in the list, and where the CTA's range ends
+    int32_t item;         // row groups before it, over all sequences
+    int32_t b, group, step, cnt, nt, end;
     Seq s;
-    __device__ __forceinline__ void clip() { cnt = (int)min(end_at - at, (int64_t)(s.steps - step)); }
+    __device__ __forceinline__ void clip(const LatArgs& a) {
+        cnt = min(end_at - at, s.steps - step);
+        end = s.T;
+        if (a.parents == nullptr) {
+            const uint32_t last = min((uint32_t)s.n * a.H, (uint32_t)(group + 1) * a.nr) - 1;
+            end = s.T - s.n + (int)(last / (uint32_t)a.H) + 1;
+        }
+        nt = max(0, min(cnt, (end + KEYS - 1) / KEYS - step));
+    }
     __device__ __forceinline__ bool next(const LatArgs& a) {
         at += cnt;
         if (at >= end_at) return false;
         step = 0;
+        ++item;
         if (++group == s.groups) {
             group = 0;
             do {
@@ -137,19 +108,58 @@ struct Segment {
                 s = seq_at<KEYS>(a, b);
             } while (s.steps == 0);
         }
-        clip();
+        clip(a);
         return true;
     }
-    // tokens that some row of the group sees, and steps of the segment that hold any
-    __device__ __forceinline__ int end(const LatArgs& a) const {
-        if (a.parents != nullptr) return s.T;
-        const int64_t last = min((int64_t)s.n * a.H, (int64_t)(group + 1) * a.nr) - 1;
-        return s.T - s.n + (int)(last / a.H) + 1;
-    }
-    __device__ __forceinline__ int steps(const LatArgs& a) const {
-        return max(0, min(cnt, (end(a) + KEYS - 1) / KEYS - step));
-    }
 };
+
+// One warp: this CTA's first segment (b = -1: none), and the steps per CTA.  Steps of all sequences are below 2^31.
+template <int KEYS>
+__device__ __forceinline__ Segment<KEYS> first_segment(const LatArgs& a, int* per_out) {
+    const int lane = threadIdx.x & 31;
+    const Seq none = {0, 0, 0, 0, 0};
+    const Seq mine = lane < a.batch ? seq_at<KEYS>(a, lane) : none;   // (of the first 32 sequences, kept)
+    int sum = mine.groups * mine.steps;
+    for (int b = lane + 32; b < a.batch; b += 32) {
+        const Seq s = seq_at<KEYS>(a, b);
+        sum += s.groups * s.steps;
+    }
+    const int total = (int)__reduce_add_sync(0xffffffffu, (unsigned)sum);
+    const int per = max(1, (int)((uint32_t)(total + gridDim.x - 1) / gridDim.x));
+    *per_out = per;
+    Segment<KEYS> g = {0, 0, 0, -1, 0, 0, 0, 0, 0, none};
+    const int64_t x64 = (int64_t)per * blockIdx.x;
+    if (x64 >= total) return g;
+    const int x = (int)x64;
+    int base = 0, items = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+        const Seq s = b0 == 0 ? mine : b0 + lane < a.batch ? seq_at<KEYS>(a, b0 + lane) : none;
+        const int steps = s.groups * s.steps;
+        int incl = steps, incl_items = s.groups;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, incl, o), v = __shfl_up_sync(0xffffffffu, incl_items, o);
+            if (lane >= o) incl += u, incl_items += v;
+        }
+        const unsigned who = __ballot_sync(0xffffffffu, x >= base + incl - steps && x < base + incl);
+        if (who) {
+            const int src = __ffs(who) - 1;
+            const auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, src); };
+            g.s = Seq{of(s.first), of(s.n), of(s.T), of(s.groups), of(s.steps)};
+            const uint32_t in = (uint32_t)(x - of(base + incl - steps));
+            g.at = x, g.end_at = min(x + per, total);
+            g.b = b0 + src;
+            g.group = (int)(in / (uint32_t)g.s.steps);
+            g.step = (int)in - g.group * g.s.steps;
+            g.item = of(items + incl_items - s.groups) + g.group;
+            g.clip(a);
+            return g;
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+        items += __shfl_sync(0xffffffffu, incl_items, 31);
+    }
+    return g;
+}
 
 // A place in a ring of n: the index, and the parity of the rounds before it.
 struct Place {
@@ -166,7 +176,7 @@ struct Shared {
     uint32_t tmem;
     int32_t abort;
     Segment<KEYS> seg;
-    int64_t per;       // steps per CTA
+    int32_t per;       // steps per CTA
     float factor[LA_ROWS];
 };
 
@@ -247,17 +257,8 @@ __global__ void __launch_bounds__(LA_NT, 1)
                    p_bytes = a.nr * 128;   // (a row of weights takes 128 bytes, as the swizzle wants it)
     kvq_pdl_begin();
     if (warp == 0) {
-        const int64_t total = all_steps<KEYS>(a);
-        const int64_t per = latent_range(total, gridDim.x), x = per * blockIdx.x;
-        int64_t before, steps_before;
-        Segment<KEYS> g = {x, min(x + per, total), -1, 0, 0, 0, {0, 0, 0, 0, 0}};
-        if (x < total) {
-            g.b = find_seq<KEYS>(a, x, [](const Seq& s) { return (int64_t)s.groups * s.steps; }, &before, &steps_before);
-            g.s = seq_at<KEYS>(a, g.b);
-            g.group = (int)((x - before) / g.s.steps);
-            g.step = (int)((x - before) % g.s.steps);
-            g.clip();
-        }
+        int per;
+        const Segment<KEYS> g = first_segment<KEYS>(a, &per);
         if (lane == 0) S.seg = g, S.per = per, S.abort = 0;
     }
     if (tid == 32) {
@@ -285,7 +286,6 @@ __global__ void __launch_bounds__(LA_NT, 1)
     tc_after();
     const uint32_t tmem = S.tmem;
     Segment<KEYS> g = S.seg;
-    const int64_t per = S.per;
 
     if (g.b < 0) {
         // no work
@@ -296,33 +296,33 @@ __global__ void __launch_bounds__(LA_NT, 1)
         int loaded = 0;    // steps so far
         bool ok = true;
         for (int seg = 0; ok;) {
-            const int nt = g.steps(a), end = g.end(a);
-            if (nt > 0) {
+            // lanes 0 .. KEYS / 16 - 1 look up one page each, a step ahead
+            const auto group_of = [&](int j) {
+                const int lp = (g.step + j) * (KEYS / PG) + lane;
+                if (j >= g.nt || lane >= KEYS / PG || lp * PG >= g.end) return nowhere;
+                const int32_t page = a.bt[(int64_t)g.b * a.max_blocks + lp];
+                if (page >= 0 && page < a.num_blocks) return page * (PG / 8);
+                kvq_dev_flag(a.hdr, KVQ_DEV_BAD_PAGE, page);
+                return nowhere;
+            };
+            int y = group_of(0);
+            if (g.nt > 0) {
                 if (seg > 0) bar_wait(&S.abort, a.hdr, &S.q_free, (seg - 1) & 1);
                 ok = !aborted(&S.abort);
                 if (ok && elect()) {
                     bar_expect(&S.q_full, a.nr * ROW * 2);
-                    tma_3d(sq, &map_q, 0, (int)((int64_t)g.s.first * a.H + (int64_t)g.group * a.nr), 0, &S.q_full);
+                    tma_3d(sq, &map_q, 0, g.s.first * a.H + g.group * a.nr, 0, &S.q_full);
                 }
                 __syncwarp();
                 ++seg;
             }
-            for (int j = 0; j < nt && ok; ++j, ++loaded) {
-                const int t0 = (g.step + j) * KEYS;
-                const int pages = min(KEYS / PG, (end - t0 + PG - 1) / PG);
-                int y = nowhere;
-                if (lane < pages) {
-                    const int32_t page = a.bt[(int64_t)g.b * a.max_blocks + t0 / PG + lane];
-                    if (page >= 0 && page < a.num_blocks)
-                        y = page * (PG / 8);
-                    else
-                        kvq_dev_flag(a.hdr, KVQ_DEV_BAD_PAGE, page);
-                }
-                if (loaded >= a.ns) bar_wait(&S.abort, a.hdr, &S.kv_empty[st.i], st.round ^ 1);
-                ok = !aborted(&S.abort);
+            for (int j = 0; j < g.nt && ok; ++j, ++loaded) {
+                const int pages = min(KEYS / PG, (g.end - (g.step + j) * KEYS + PG - 1) / PG);
                 int to[KEYS / PG];
 #pragma unroll
                 for (int k = 0; k < KEYS / PG; ++k) to[k] = __shfl_sync(0xffffffffu, y, k);
+                if (loaded >= a.ns) bar_wait(&S.abort, a.hdr, &S.kv_empty[st.i], st.round ^ 1);
+                ok = !aborted(&S.abort);
                 if (ok && elect()) {
                     bar_expect(&S.kv_full[st.i], pages * PG * ROW * 2);
 #pragma unroll
@@ -330,6 +330,7 @@ __global__ void __launch_bounds__(LA_NT, 1)
                         if (k < pages) tma_page(skv + st.i * STAGE + k * (PG * ROW * 2), &map_rows, to[k], &S.kv_full[st.i]);
                 }
                 __syncwarp();
+                y = group_of(j + 1);
                 st.next(a.ns);
             }
             if (!g.next(a)) break;
@@ -364,7 +365,7 @@ __global__ void __launch_bounds__(LA_NT, 1)
             s.next(NP);
         };
         for (int seg = 0;;) {
-            const int nt = g.steps(a);
+            const int nt = g.nt;
             if (nt > 0) {
                 bar_wait(&S.abort, a.hdr, &S.q_full, seg & 1);
                 ++seg;
@@ -405,9 +406,9 @@ __global__ void __launch_bounds__(LA_NT, 1)
         // is at most one phase of its barrier away
         Place st, s_at, done;
         do {
-            const int nt = g.steps(a), end = g.end(a), ctx = g.s.T - g.s.n;
-            const int64_t row0 = (int64_t)g.group * a.nr;   // of the sequence
-            const int rows = (int)min((int64_t)a.nr, (int64_t)g.s.n * a.H - row0);
+            const int nt = g.nt, end = g.end, ctx = g.s.T - g.s.n;
+            const int row0 = g.group * a.nr;   // of the sequence
+            const int rows = min(a.nr, g.s.n * a.H - row0);
             const bool active = 16 * warp < rows;
             bool valid[2];
             int cut[2];                                     // every token before it is seen
@@ -416,7 +417,7 @@ __global__ void __launch_bounds__(LA_NT, 1)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 valid[i] = ra + 8 * i < rows;
-                const int tok = valid[i] ? (int)((row0 + ra + 8 * i) / a.H) : 0;
+                const int tok = valid[i] ? (int)((uint32_t)(row0 + ra + 8 * i) / (uint32_t)a.H) : 0;
                 cut[i] = valid[i] ? (tree ? ctx : ctx + tok + 1) : 0;
                 if (tree && valid[i]) walk_path(a, g.s.first, tok, path[i]);
             }
@@ -517,7 +518,7 @@ __global__ void __launch_bounds__(LA_NT, 1)
             }
             // ---- the segment's rows: to the output, or as a part of them
             const bool whole = g.step == 0 && g.cnt == g.s.steps, last = g.step + g.cnt == g.s.steps;
-            const int64_t out_row = (int64_t)g.s.first * a.H + row0;
+            const int out_row = g.s.first * a.H + row0;
             const int64_t slot = 2 * (int64_t)blockIdx.x + (g.step == 0 ? 1 : 0);
             if (nt > 0) bar_wait(&S.abort, a.hdr, &S.pv_done[done.i], done.round);
             tc_after();
@@ -527,30 +528,38 @@ __global__ void __launch_bounds__(LA_NT, 1)
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                 const int r = ra + 8 * i;
                 if (!valid[i] || (lane & 3) != 0) continue;
-                S.factor[r] = whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
-                // (an item's last part is its CTA's first segment: the launch behind this one looks there)
-                if (!whole)
-                    a.ml[slot * a.nr + r] = make_int4(__float_as_int(m[i]), __float_as_int(sum),
-                                                      last ? (int)((g.at - g.step) / per) + 1 : 0, (int)(out_row + r));
-                if (whole && a.lse != nullptr) a.lse[out_row + r] = sum == 0.0f ? -INFINITY : (m[i] + log2f(sum)) * KVQ_LN2;
+                if (whole) {
+                    S.factor[r] = sum == 0.0f ? 0.0f : 1.0f / sum;
+                    if (a.lse != nullptr) a.lse[out_row + r] = sum == 0.0f ? -INFINITY : (m[i] + log2f(sum)) * KVQ_LN2;
+                } else {
+                    a.ml[slot * a.nr + r] = make_float2(m[i], sum);
+                    if (last) {
+                        const int c0 = (g.at - g.step) / S.per;
+                        a.cuts[(int64_t)g.item * a.nr + r] = make_int4(c0 + 1, (int)blockIdx.x - c0 + 1, out_row + r, 0);
+                    }
+                }
             }
             sm_any(false);
             if (nt > 0 && !aborted(&S.abort)) {
-                for (int d = 0; d < LAT / 128; ++d)
-                    for (int c = 0; c < rows; c += 16) {
+                const int dim = 32 * warp + lane;
+                for (int c = 0; c < rows; c += 16) {
+                    float* part = a.part + (slot * a.nr + c) * LAT + dim;
+                    uint16_t* out = a.out + (int64_t)(out_row + c) * LAT + dim;
+                    const int n = min(16, rows - c);
+#pragma unroll
+                    for (int d = 0; d < LAT / 128; ++d) {
                         uint32_t o[16];
                         tm_ld16(lane_base + TM_O + 64 * d + c, o);
-                        const int dim = 128 * d + 32 * warp + lane;
 #pragma unroll
                         for (int x = 0; x < 16; ++x) {
-                            if (c + x >= rows) break;
-                            const float v = __uint_as_float(o[x]) * S.factor[c + x];
+                            if (x >= n) break;
                             if (whole)
-                                a.out[(out_row + c + x) * LAT + dim] = kvq_f2h(v);
+                                out[x * LAT + 128 * d] = kvq_f2h(__uint_as_float(o[x]) * S.factor[c + x]);
                             else
-                                a.part[(slot * a.nr + c + x) * LAT + dim] = v;
+                                part[x * LAT + 128 * d] = __uint_as_float(o[x]);
                         }
                     }
+                }
             }
             tc_before();   // (O^T is read before the next segment's first weights are handed over)
         } while (g.next(a));
@@ -565,45 +574,53 @@ __global__ void __launch_bounds__(LA_NT, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TM_COLS) : "memory");
 }
 
-// Joins the parts of a row in the order of their CTAs and leaves the workspace zeroed.  A CTA per (CTA of the launch
-// before, row): where that one's first segment ended a row group, it left the first part's CTA behind.  GR groups of
-// 128 threads take every GR-th part, four values per thread.
-template <int GR>
-__global__ void __launch_bounds__(128 * GR) latent_join_kernel(const __grid_constant__ LatArgs a) {
+// Joins the parts of a row in the order of their CTAs and leaves the workspace zeroed: 128 / Q threads per part take
+// four values each, GR parts at a time.  Q > 1, for rows of many parts: a cluster of Q CTAs per row.
+template <int Q, int GR>
+__global__ void __launch_bounds__(128 / Q * GR) latent_join_kernel(const __grid_constant__ LatArgs a) {
+    constexpr int W = 128 / Q;
     __shared__ float weight[KVQ_LATENT_MAX_CTAS];
-    __shared__ float4 sums[GR][128];
-    const int tid = threadIdx.x, lane = tid & 31, c1 = blockIdx.x, r = blockIdx.y;
+    __shared__ float4 sums[GR][W];
+    const int tid = threadIdx.x, lane = tid & 31, quarter = blockIdx.x % Q;
+    int4* const cut_at = a.cuts + (int64_t)(blockIdx.x / Q) * a.nr + blockIdx.y;
     kvq_pdl_begin();
-    const int4 end = a.ml[(int64_t)2 * c1 * a.nr + r];
-    if (end.z == 0) return;
-    const int c0 = end.z - 1, n = c1 - c0 + 1;
+    const int4 cut = *cut_at;
+    if (cut.x == 0) return;   // (a cluster's CTAs read the same)
+    const int c0 = cut.x - 1, n = cut.y;
     // the first part is its CTA's last segment, the others are their CTAs' first ones
-    const auto slot_of = [&](int i) { return ((int64_t)2 * (c0 + i) + (i == 0 ? 1 : 0)) * a.nr + r; };
-    const auto part_of = [&](int i) { return reinterpret_cast<float4*>(a.part + slot_of(i) * LAT) + (tid & 127); };
+    const auto slot_of = [&](int i) { return ((int64_t)2 * (c0 + i) + (i == 0 ? 1 : 0)) * a.nr + blockIdx.y; };
+    const auto part_of = [&](int i) { return reinterpret_cast<float4*>(a.part + slot_of(i) * LAT) + quarter * W + tid % W; };
     if (tid < 32) {
         // weights of the parts: 2^(anchor - largest anchor); a part without a visible token wrote no row
         float mx = -INFINITY, y = 0.0f;
         for (int i = lane; i < n; i += 32) {
-            const int4 v = a.ml[slot_of(i)];
-            if (__int_as_float(v.y) != 0.0f) mx = fmaxf(mx, __int_as_float(v.x));
+            const float2 v = a.ml[slot_of(i)];
+            if (v.y != 0.0f) mx = fmaxf(mx, v.x);
         }
         mx = kvq_warp_max(mx);
         for (int i = lane; i < n; i += 32) {
-            const int4 v = a.ml[slot_of(i)];
-            const float sum = __int_as_float(v.y), f = sum != 0.0f ? exp2f(__int_as_float(v.x) - mx) : 0.0f;
+            const float2 v = a.ml[slot_of(i)];
+            const float f = v.y != 0.0f ? exp2f(v.x - mx) : 0.0f;
             weight[i] = f;
-            y += f * sum;
+            y += f * v.y;
         }
         // (every lane's sum is over its own parts, joined in one order)
         y = kvq_warp_sum(y);
         const float inv = y == 0.0f ? 0.0f : 1.0f / y;
         for (int i = lane; i < n; i += 32) weight[i] *= inv;
-        if (lane == 0 && a.lse != nullptr) a.lse[end.w] = y == 0.0f ? -INFINITY : (mx + log2f(y)) * KVQ_LN2;
+        if (lane == 0 && quarter == 0 && a.lse != nullptr) a.lse[cut.z] = y == 0.0f ? -INFINITY : (mx + log2f(y)) * KVQ_LN2;
     }
-    __syncthreads();
-    for (int i = tid; i < n; i += 128 * GR) a.ml[slot_of(i)] = make_int4(0, 0, 0, 0);
+    if (Q > 1) {
+        asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+    } else {
+        __syncthreads();
+    }
+    if (quarter == 0) {
+        for (int i = tid; i < n; i += W * GR) a.ml[slot_of(i)] = make_float2(0.0f, 0.0f);
+        if (tid == 0) *cut_at = make_int4(0, 0, 0, 0);
+    }
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const int grp = tid >> 7;
+    const int grp = tid / W;
 #pragma unroll 8
     for (int i = grp; i < n; i += GR) {
         const float4 v = *part_of(i);
@@ -613,7 +630,7 @@ __global__ void __launch_bounds__(128 * GR) latent_join_kernel(const __grid_cons
     // (behind the loads: a store between them would hold up the next one)
     for (int i = grp; i < n; i += GR) *part_of(i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (GR > 1) {
-        sums[grp][tid & 127] = o;
+        sums[grp][tid % W] = o;
         __syncthreads();
         if (grp > 0) return;
         for (int k = 1; k < GR; ++k) {
@@ -621,13 +638,14 @@ __global__ void __launch_bounds__(128 * GR) latent_join_kernel(const __grid_cons
             o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
         }
     }
-    reinterpret_cast<uint2*>(a.out + (int64_t)end.w * LAT)[tid & 127] = make_uint2(half2_bits(o.x, o.y), half2_bits(o.z, o.w));
+    reinterpret_cast<uint2*>(a.out + (int64_t)cut.z * LAT)[quarter * W + tid % W] =
+        make_uint2(half2_bits(o.x, o.y), half2_bits(o.z, o.w));
 }
 
 struct LatPlan {
     int nr, ns, keys, ahead, ctas;
-    int64_t items;
-    size_t smem, off_ml, off_part, bytes;
+    int64_t items, steps;   // row groups and steps of the list, at most
+    size_t smem, off_ml, off_cuts, off_part, bytes;
 };
 
 LatPlan latent_plan(const kvq_seqs* S, int32_t n_heads, int64_t n_rows, int32_t max_new) {
@@ -639,13 +657,15 @@ LatPlan latent_plan(const kvq_seqs* S, int32_t n_heads, int64_t n_rows, int32_t 
     p.keys = p.nr <= 32 ? 48 : 32;
     p.ahead = 1;
     const int64_t steps = p.items * ((S->max_len + p.keys - 1) / p.keys);
+    p.steps = steps;
     p.ctas = (int)std::max<int64_t>(1, std::min<int64_t>({steps, kvq_num_sms(), KVQ_LATENT_MAX_CTAS}));
     const size_t stage = p.keys / 8 * LA_GROUP, fixed = 1024 + (size_t)p.nr * (ROW * 2 + (p.ahead + 1) * 128);
     p.ns = (int)std::min<size_t>((LA_SMEM - fixed) / stage, LA_MAX_NS);
     p.smem = fixed + p.ns * stage;
     const size_t rows = (size_t)2 * p.ctas * p.nr;
     p.off_ml = sizeof(KvqWsHeader);
-    p.off_part = kvq_round_up(p.off_ml + rows * sizeof(int4), 256);
+    p.off_cuts = kvq_round_up(p.off_ml + rows * sizeof(float2), 256);
+    p.off_part = kvq_round_up(p.off_cuts + (size_t)p.items * p.nr * sizeof(int4), 256);
     p.bytes = kvq_round_up(p.off_part + rows * LAT * sizeof(float), 256);
     return p;
 }
@@ -675,6 +695,7 @@ extern "C" int kv_latent_attn(const kvq_latent* C, const kvq_seqs* S, int32_t n_
     if (st) return st;
     KVQ_REQUIRE(C->num_blocks * PG <= INT32_MAX && n_rows * n_heads <= INT32_MAX - LA_ROWS, KVQ_ERR_UNSUPPORTED,
                 "%s: more than 2^31 - 1 rows in the pool or queries", fn);
+    KVQ_REQUIRE(p.steps <= INT32_MAX - KVQ_LATENT_MAX_CTAS, KVQ_ERR_UNSUPPORTED, "%s: more than 2^31 steps (queries times max_len)", fn);
     if (S->batch == 0 || n_rows == 0) return KVQ_OK;
     KVQ_REQUIRE(q && out && q_starts && (S->block_table || S->max_len == 0), KVQ_ERR_INVALID_ARG, "%s: NULL buffer", fn);
     KVQ_REQUIRE((((uintptr_t)q | (uintptr_t)out) & 15u) == 0, KVQ_ERR_INVALID_ARG, "%s: q and out must be 16-byte aligned", fn);
@@ -690,7 +711,8 @@ extern "C" int kv_latent_attn(const kvq_latent* C, const kvq_seqs* S, int32_t n_
     a.n_rows = n_rows, a.num_blocks = C->num_blocks;
     a.batch = S->batch, a.max_blocks = S->max_blocks, a.max_len = S->max_len, a.max_new = max_new, a.H = n_heads, a.nr = p.nr, a.ns = p.ns;
     a.out = out, a.lse = lse, a.hdr = static_cast<KvqWsHeader*>(ws);
-    a.ml = reinterpret_cast<int4*>(static_cast<char*>(ws) + p.off_ml);
+    a.ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + p.off_ml);
+    a.cuts = reinterpret_cast<int4*>(static_cast<char*>(ws) + p.off_cuts);
     a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.off_part);
     const auto go = [&](auto kernel) {
         const int rc = kvq_prepare_kernel((const void*)kernel, (int)p.smem);
@@ -700,12 +722,24 @@ extern "C" int kv_latent_attn(const kvq_latent* C, const kvq_seqs* S, int32_t n_
     };
     st = p.keys == 48 ? go(latent_attn_kernel<48, 1>) : go(latent_attn_kernel<32, 1>);
     if (st || p.ctas == 1) return st;
-    const dim3 grid(p.ctas, p.nr);
-    // few row groups have many parts each
-    const int64_t parts = p.ctas / p.items;
-    const cudaError_t e = parts > 32  ? kvq_launch_pdl(latent_join_kernel<8>, grid, dim3(1024), 0, kvq_stream(stream), a)
-                          : parts > 6 ? kvq_launch_pdl(latent_join_kernel<2>, grid, dim3(256), 0, kvq_stream(stream), a)
-                                      : kvq_launch_pdl(latent_join_kernel<1>, grid, dim3(128), 0, kvq_stream(stream), a);
+    cudaError_t e;
+    if (p.ctas > 6 * p.items) {
+        // few row groups, of many parts each
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)p.items * 4, p.nr);
+        cfg.blockDim = dim3(512);
+        cfg.stream = kvq_stream(stream);
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = 4, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        e = cudaLaunchKernelEx(&cfg, latent_join_kernel<4, 16>, a);
+    } else {
+        e = kvq_launch_pdl(latent_join_kernel<1, 1>, dim3((unsigned)p.items, p.nr), dim3(128), 0, kvq_stream(stream), a);
+    }
     if (e != cudaSuccess) return kvq_fail(KVQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
     return KVQ_OK;
 }
