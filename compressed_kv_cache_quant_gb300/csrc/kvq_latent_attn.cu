@@ -23,6 +23,8 @@
 // rescaled) when a weight would pass 2^15.99.
 #include <algorithm>
 #include <cmath>
+#include <mutex>
+#include <vector>
 
 #include "kvq_attn_mod.cuh"
 #include "kvq_latent.cuh"
@@ -113,9 +115,10 @@ struct Segment {
     }
 };
 
-// One warp: this CTA's first segment (b = -1: none), and the steps per CTA.  Steps of all sequences are below 2^31.
+// One warp: the first segment (b = -1: none) of the index-th of `count` CTAs, or pairs of them, and the steps of each.
+// Steps of all sequences are below 2^31.
 template <int KEYS>
-__device__ __forceinline__ Segment<KEYS> first_segment(const LatArgs& a, int* per_out) {
+__device__ __forceinline__ Segment<KEYS> first_segment(const LatArgs& a, int index, int count, int* per_out) {
     const int lane = threadIdx.x & 31;
     const Seq none = {0, 0, 0, 0, 0};
     const Seq mine = lane < a.batch ? seq_at<KEYS>(a, lane) : none;   // (of the first 32 sequences, kept)
@@ -125,10 +128,10 @@ __device__ __forceinline__ Segment<KEYS> first_segment(const LatArgs& a, int* pe
         sum += s.groups * s.steps;
     }
     const int total = (int)__reduce_add_sync(0xffffffffu, (unsigned)sum);
-    const int per = max(1, (int)((uint32_t)(total + gridDim.x - 1) / gridDim.x));
+    const int per = max(1, (int)((uint32_t)(total + count - 1) / (uint32_t)count));
     *per_out = per;
     Segment<KEYS> g = {0, 0, 0, -1, 0, 0, 0, 0, 0, none};
-    const int64_t x64 = (int64_t)per * blockIdx.x;
+    const int64_t x64 = (int64_t)per * index;
     if (x64 >= total) return g;
     const int x = (int)x64;
     int base = 0, items = 0;
@@ -258,7 +261,7 @@ __global__ void __launch_bounds__(LA_NT, 1)
     kvq_pdl_begin();
     if (warp == 0) {
         int per;
-        const Segment<KEYS> g = first_segment<KEYS>(a, &per);
+        const Segment<KEYS> g = first_segment<KEYS>(a, blockIdx.x, gridDim.x, &per);
         if (lane == 0) S.seg = g, S.per = per, S.abort = 0;
     }
     if (tid == 32) {
@@ -574,6 +577,347 @@ __global__ void __launch_bounds__(LA_NT, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TM_COLS) : "memory");
 }
 
+// ---------------------------------------------------------------- many query rows: pairs of CTAs
+//
+// 128 query rows, 64 per CTA, and 64 tokens per step.  S = Q K^T is one product of both (M = 128, N = 64): a CTA stages
+// its rows' queries and the keys of half of the tokens.  O = P V keeps its rows as they are (M = 128, N = 256, twice): a
+// CTA stages half of the 512 values of all tokens, so that O takes 256 of its TMEM columns (a CTA of a pair keeps 64 rows
+// of M = 128 in 128 lanes: lanes 64 and up have the second half of the columns).  Half a token's values is thus staged
+// twice, but no row's key is staged for only 64 query rows, as above.
+constexpr int LB_KEYS = 64;
+constexpr int LB_K = LB_KEYS / 2 * ROW * 2;      // bytes of a CTA's keys of a step
+constexpr int LB_V = LB_KEYS * LAT;              // and of its values (two bytes each, half of them)
+constexpr int LB_V_GROUP = 4 * 1024;             // eight rows of its four chunks
+constexpr int LB_NS = 2;
+constexpr int LB_Q = 64 * ROW * 2, LB_P = 64 * 128;
+constexpr int LB_SMEM = 1024 + LB_Q + LB_NS * (LB_K + LB_V) + 2 * LB_P;
+
+struct SharedPair {
+    uint64_t q_full, q_free, k_full[LB_NS], k_empty[LB_NS], v_full[LB_NS], v_empty[LB_NS], s_full[2], p_full[2], pv_done[2], drain;
+    uint32_t tmem;
+    int32_t abort, per;
+    Segment<LB_KEYS> seg;
+    float half[128];      // what the two threads of a row have to tell one another
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LA_NT, 1)
+    latent_pair_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                       const __grid_constant__ CUtensorMap map_v, const __grid_constant__ LatArgs a) {
+    extern __shared__ unsigned char raw[];
+    __shared__ SharedPair S;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1;
+    const uint32_t sq = (saddr(raw) + 1023) & ~1023u, sk = sq + LB_Q, sv = sk + LB_NS * LB_K, sp = sv + LB_NS * LB_V;
+    kvq_pdl_begin();
+    if (warp == 0) {
+        int per;
+        const Segment<LB_KEYS> g = first_segment<LB_KEYS>(a, pair, gridDim.x >> 1, &per);
+        if (lane == 0) S.seg = g, S.per = per, S.abort = 0;
+    }
+    if (tid == 32) {
+        bar_init(&S.q_full, 1);
+        bar_init(&S.q_free, 1);
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&S.k_full[i], 1);
+            bar_init(&S.k_empty[i], 1);
+            bar_init(&S.v_full[i], 1);
+            bar_init(&S.v_empty[i], 1);
+            bar_init(&S.s_full[i], 1);
+            bar_init(&S.p_full[i], 8);
+            bar_init(&S.pv_done[i], 1);
+        }
+        bar_init(&S.drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 4) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&S.tmem)), "r"(TM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_before();
+    __syncthreads();
+    cluster_sync();   // (both CTAs' barriers and TMEM are there)
+    tc_after();
+    const uint32_t tmem = S.tmem;
+    Segment<LB_KEYS> g = S.seg;
+
+    if (g.b < 0) {
+        // no work for this pair
+    } else if (warp == 5) {
+        // ---- loads: keys and queries signal rank 0, which issues the products; values stay within the CTA
+        const int nowhere = (int)(a.num_blocks * (PG / 8));   // a group of rows behind the pool: zeros
+        Place st;
+        int loaded = 0;
+        bool ok = true;
+        for (int seg = 0; ok;) {
+            const auto group_of = [&](int j) {
+                const int lp = (g.step + j) * (LB_KEYS / PG) + lane;
+                if (j >= g.nt || lane >= LB_KEYS / PG || lp * PG >= g.end) return nowhere;
+                const int32_t page = a.bt[(int64_t)g.b * a.max_blocks + lp];
+                if (page >= 0 && page < a.num_blocks) return page * (PG / 8);
+                kvq_dev_flag(a.hdr, KVQ_DEV_BAD_PAGE, page);
+                return nowhere;
+            };
+            int y = group_of(0);
+            if (g.nt > 0) {
+                if (seg > 0) bar_wait(&S.abort, a.hdr, &S.q_free, (seg - 1) & 1);
+                ok = !aborted(&S.abort);
+                if (ok && elect()) {
+                    if (rank == 0) bar_expect(&S.q_full, 2 * LB_Q);
+                    tma_3d_pair(sq, &map_q, 0, g.s.first * a.H + g.group * a.nr + 64 * (int)rank, 0, saddr_in(&S.q_full, 0));
+                }
+                __syncwarp();
+                ++seg;
+            }
+            for (int j = 0; j < g.nt && ok; ++j, ++loaded) {
+                const int pages = min(LB_KEYS / PG, (g.end - (g.step + j) * LB_KEYS + PG - 1) / PG);
+                int to[LB_KEYS / PG];
+#pragma unroll
+                for (int k = 0; k < LB_KEYS / PG; ++k) to[k] = __shfl_sync(0xffffffffu, y, k);
+                if (loaded >= LB_NS) bar_wait(&S.abort, a.hdr, &S.k_empty[st.i], st.round ^ 1);
+                ok = !aborted(&S.abort);
+                if (ok && elect()) {
+                    if (rank == 0) bar_expect(&S.k_full[st.i], pages * PG * ROW * 2);
+                    const uint32_t bar = saddr_in(&S.k_full[st.i], 0);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (2 * (int)rank + k < pages)
+                            tma_page_pair(sk + st.i * LB_K + k * (PG * ROW * 2), &map_k, rank == 0 ? to[k] : to[2 + k], bar);
+                }
+                __syncwarp();
+                if (loaded >= LB_NS) bar_wait(&S.abort, a.hdr, &S.v_empty[st.i], st.round ^ 1);
+                ok = !aborted(&S.abort);
+                if (ok && elect()) {
+                    bar_expect(&S.v_full[st.i], pages * PG * LAT);
+#pragma unroll
+                    for (int k = 0; k < LB_KEYS / PG; ++k)
+                        if (k < pages) tma_4d(sv + st.i * LB_V + k * (PG * LAT), &map_v, 0, 0, 4 * (int)rank, to[k], &S.v_full[st.i]);
+                }
+                __syncwarp();
+                y = group_of(j + 1);
+                st.next(LB_NS);
+            }
+            if (!g.next(a)) break;
+        }
+    } else if (warp == 4) {
+        // ---- tensor cores: one lane of rank 0
+        if (rank == 0 && elect()) {
+            const uint32_t hi_q = (uint32_t)(smem_desc(0, 16, 1024) >> 32), hi_k = (uint32_t)(smem_desc(0, 16, LA_GROUP) >> 32),
+                           hi_v = (uint32_t)(smem_desc(0, 16, LB_V_GROUP) >> 32);
+            const uint32_t lq = (uint32_t)smem_desc(sq, 16, 0), lk = (uint32_t)smem_desc(sk, 16, 0),
+                           lv = (uint32_t)smem_desc(sv, 1024, 0), lp = (uint32_t)smem_desc(sp, 16, 0);
+            constexpr uint32_t idesc_s = idesc_f16(128, LB_KEYS), idesc_o = idesc_f16(128, 256) | KVQ_B_MN;
+            const auto desc = [](uint32_t hi, uint32_t lo) { return (uint64_t)hi << 32 | lo; };
+            Place in, out;   // of the next S and the next O (stages and buffers alike: two of each)
+            const auto qk = [&] {
+                bar_wait_pair(&S.abort, a.hdr, &S.k_full[in.i], in.round);
+                tc_after();
+                uint32_t x = lq, y = lk + (in.i * LB_K >> 4);
+                asm volatile("" : "+r"(x), "+r"(y));
+#pragma unroll
+                for (int c = 0; c < LA_CHUNKS; ++c)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_ss_pair(TM_S + in.i * (LB_KEYS / 2), desc(hi_q, x + (c * 8192 >> 4) + 2 * k),
+                                    desc(hi_k, y + (c * 1024 >> 4) + 2 * k), idesc_s, c + k > 0);
+                // (all products so far: where S is there, so is O of two steps before, and P's place is free)
+                tc_commit_pair(&S.s_full[in.i]);
+                tc_commit_pair(&S.k_empty[in.i]);
+                in.next(2);
+            };
+            for (int seg = 0;;) {
+                if (g.nt > 0) {
+                    bar_wait_pair(&S.abort, a.hdr, &S.q_full, seg & 1);
+                    ++seg;
+                    qk();
+                    if (g.nt == 1) tc_commit_pair(&S.q_free);
+                }
+                for (int j = 0; j < g.nt; ++j) {
+                    if (j + 1 < g.nt) {
+                        qk();
+                        if (j + 2 == g.nt) tc_commit_pair(&S.q_free);
+                    }
+                    bar_wait_pair(&S.abort, a.hdr, &S.p_full[out.i], out.round);
+                    tc_after();
+                    uint32_t y = lv + (out.i * LB_V >> 4), z = lp + (out.i * LB_P >> 4);
+                    asm volatile("" : "+r"(y), "+r"(z));
+#pragma unroll
+                    for (int k = 0; k < LB_KEYS / 16; ++k)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            mma_ss_pair(TM_O + 128 * h, desc(hi_q, z + 2 * k), desc(hi_v, y + ((k * 2 * LB_V_GROUP + h * 2048) >> 4)),
+                                        idesc_o, j > 0 || k > 0);
+                    tc_commit_pair(&S.v_empty[out.i]);
+                    tc_commit_pair(&S.pv_done[out.i]);
+                    out.next(2);
+                }
+                if (!g.next(a)) break;
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---- softmax: thread t has half of the step's columns of row t % 64, and the same half of O's
+        const uint32_t lane_base = tmem + ((uint32_t)warp << 21);   // TMEM lanes 32 warp ..
+        const int r = tid & 63, half = tid >> 6;
+        const bool tree = a.parents != nullptr;
+        const uint32_t p_full[2] = {saddr_in(&S.p_full[0], 0), saddr_in(&S.p_full[1], 0)};
+        Place at, done;   // `done`: the step before
+        do {
+            const int nt = g.nt, end = g.end, ctx = g.s.T - g.s.n;
+            const int row0 = g.group * a.nr + 64 * (int)rank;   // of the sequence
+            const int rows = min(64, g.s.n * a.H - row0);       // (below 1: none in this CTA)
+            const bool valid = r < rows;
+            uint32_t path[KVQ_TREE_WORDS] = {};
+            const int tok = valid ? (int)((uint32_t)(row0 + r) / (uint32_t)a.H) : 0;
+            const int cut = valid ? (tree ? ctx : ctx + tok + 1) : 0;    // every token before it is seen
+            if (tree && valid) walk_path(a, g.s.first, tok, path);
+            const int full = __reduce_min_sync(0xffffffffu, cut);
+            float m = -INFINITY, l = 0.0f;
+            for (int j = 0; j < nt; ++j, done = at, at.next(2)) {
+                const int t0 = (g.step + j) * LB_KEYS, c0 = t0 + 32 * half;
+                bar_wait(&S.abort, a.hdr, &S.s_full[at.i], at.round);
+                tc_after();
+                float s[32];
+                tm_ld32(lane_base + TM_S + at.i * (LB_KEYS / 2), reinterpret_cast<uint32_t*>(s));
+#pragma unroll
+                for (int c = 0; c < 32; ++c) s[c] = __fmul_rn(s[c], a.scale2);
+                if (c0 + 32 > full) {   // (full: what every row of the warp sees all of)
+                    uint32_t bits = below(cut - c0);
+                    if (tree && valid) bits |= path_bits(path, c0 - ctx);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        if (!(bits >> c & 1)) s[c] = -INFINITY;
+                }
+                float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < 32; c += 8)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) t4[x] = max3(t4[x], s[c + 2 * x], s[c + 2 * x + 1]);
+                float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+                // a first anchor, or a weight that would leave fp16's range (either thread of a row tells)
+                if (sm_any(m == -INFINITY ? top > m : top - m > LA_TOP)) {
+                    // one row's turn is every row's: an anchor that would have to follow later is set now
+                    S.half[tid] = top;
+                    sm_any(false);
+                    top = fmaxf(top, S.half[tid ^ 64]);
+                    float f = 1.0f;
+                    if (m == -INFINITY ? top > m : top - m > LA_HEAD) {
+                        const float anchor = top - LA_HEAD;
+                        f = ex2(m - anchor);
+                        m = anchor;
+                        l *= f;
+                    }
+                    if (j > 0) {
+                        bar_wait(&S.abort, a.hdr, &S.pv_done[done.i], done.round);
+                        tc_after();
+#pragma unroll 1
+                        for (int c = 0; c < 256; c += 32) {
+                            uint32_t o[32];
+                            tm_ld32(lane_base + TM_O + c, o);
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                            tm_st32(lane_base + TM_O + c, o);
+                        }
+                        tm_wait_st();
+                    }
+                }
+                const float ms = m == -INFINITY ? 0.0f : m;
+                float sum[2] = {0.0f, 0.0f};
+                const uint32_t to = sp + at.i * LB_P + (r >> 3) * 1024 + (r & 7) * 128;
+#pragma unroll
+                for (int c = 0; c < 32; c += 8) {
+                    uint32_t p[4];
+#pragma unroll
+                    for (int x = 0; x < 8; x += 2) {
+                        const float e0 = ex2(s[c + x] - ms), e1 = ex2(s[c + x + 1] - ms);
+                        sum[(x >> 1) & 1] += e0 + e1;
+                        p[x / 2] = half2_bits(e0, e1);
+                    }
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (((4 * half + (c >> 3)) ^ (r & 7)) << 4)), "r"(p[0]),
+                                 "r"(p[1]), "r"(p[2]), "r"(p[3])
+                                 : "memory");
+                }
+                l += sum[0] + sum[1];
+                // the weights stand for the values' arrival, too
+                bar_wait(&S.abort, a.hdr, &S.v_full[at.i], at.round);
+                if (end < t0 + LB_KEYS) {
+                    // rows at and behind the end may hold anything: 0 * NaN must not reach O
+                    const uint32_t base = sv + at.i * LB_V;
+                    const int r0 = end - t0;
+                    for (int x = tid; x < (LB_KEYS - r0) * 32; x += 128) {
+                        const int row = r0 + (x >> 5), c = x & 31;
+                        const uint32_t z = base + (row >> 3) * LB_V_GROUP + (c >> 3) * 1024 + (row & 7) * 128 + (c & 7) * 16;
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(z), "r"(0) : "memory");
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                tc_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive_in(p_full[at.i]);
+            }
+            // ---- the segment's rows: to the output, or as a part of them
+            const bool whole = g.step == 0 && g.cnt == g.s.steps, last = g.step + g.cnt == g.s.steps;
+            const int out_row = g.s.first * a.H + row0;
+            const int64_t slot = 2 * (int64_t)pair + (g.step == 0 ? 1 : 0);
+            const int in_group = 64 * (int)rank + r;
+            if (nt > 0) bar_wait(&S.abort, a.hdr, &S.pv_done[done.i], done.round);
+            tc_after();
+            S.half[tid] = l;
+            sm_any(false);
+            l += S.half[tid ^ 64];   // (one sum of two, whichever thread takes it)
+            sm_any(false);
+            const float f = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+            if (valid && half == 0) {
+                if (whole) {
+                    if (a.lse != nullptr) a.lse[out_row + r] = l == 0.0f ? -INFINITY : (m + log2f(l)) * KVQ_LN2;
+                } else {
+                    a.ml[slot * a.nr + in_group] = make_float2(m, l);
+                    if (last) {
+                        const int p0 = (g.at - g.step) / S.per;
+                        a.cuts[(int64_t)g.item * a.nr + in_group] = make_int4(p0 + 1, pair - p0 + 1, out_row + r, 0);
+                    }
+                }
+            }
+            if (nt > 0 && !aborted(&S.abort)) {
+#pragma unroll 2
+                for (int c = 0; c < 256; c += 32) {
+                    uint32_t o[32];
+                    tm_ld32(lane_base + TM_O + c, o);
+                    if (!valid) continue;
+                    if (whole) {
+                        uint4* dst = reinterpret_cast<uint4*>(a.out + (int64_t)(out_row + r) * LAT + 256 * half + c);
+                        uint32_t w[16];
+#pragma unroll
+                        for (int x = 0; x < 16; ++x)
+                            w[x] = half2_bits(__uint_as_float(o[2 * x]) * f, __uint_as_float(o[2 * x + 1]) * f);
+#pragma unroll
+                        for (int x = 0; x < 16; x += 4) dst[x / 4] = make_uint4(w[x], w[x + 1], w[x + 2], w[x + 3]);
+                    } else {
+                        uint4* dst = reinterpret_cast<uint4*>(a.part + (slot * a.nr + in_group) * LAT + 256 * half + c);
+#pragma unroll
+                        for (int x = 0; x < 32; x += 4) dst[x / 4] = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+                    }
+                }
+            }
+            tc_before();   // (O is read before the next segment's first weights are handed over)
+        } while (g.next(a));
+    }
+    __syncwarp();
+    __syncthreads();
+    if (*(volatile int32_t*)&S.abort) {
+        // a wait gave up: this pair's own copies and products land before it ends (far above a copy's time)
+        const long long began = clock64();
+        while (clock64() - began < 4000000) __nanosleep(1000);
+    }
+    tc_before();
+    __syncthreads();
+    cluster_sync();   // (neither ends while the other may still signal it or read its shared memory)
+    tc_after();
+    if (warp == 4)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TM_COLS) : "memory");
+}
+
 // Joins the parts of a row in the order of their CTAs and leaves the workspace zeroed: 128 / Q threads per part take
 // four values each, GR parts at a time.  Q > 1, for rows of many parts: a cluster of Q CTAs per row.
 template <int Q, int GR>
@@ -643,25 +987,52 @@ __global__ void __launch_bounds__(128 / Q * GR) latent_join_kernel(const __grid_
 }
 
 struct LatPlan {
-    int nr, ns, keys, ahead, ctas;
+    bool pairs;
+    int nr, ns, keys, ctas;   // ctas: CTAs, or pairs of them
     int64_t items, steps;   // row groups and steps of the list, at most
     size_t smem, off_ml, off_cuts, off_part, bytes;
 };
 
+// Pairs of CTAs that run at the same time on the current device (asked once per device).
+int latent_pairs() {
+    static std::mutex mu;
+    static std::vector<int> found;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return kvq_num_sms() / 2;
+    }
+    std::lock_guard<std::mutex> lk(mu);
+    if ((int)found.size() <= dev) found.resize(dev + 1, 0);
+    if (found[dev] == 0) {
+        int n = 0;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * (kvq_num_sms() / 2));
+        cfg.blockDim = dim3(LA_NT);
+        cfg.dynamicSmemBytes = LB_SMEM;
+        if (kvq_prepare_kernel((const void*)latent_pair_kernel, LB_SMEM) != KVQ_OK ||
+            cudaOccupancyMaxActiveClusters(&n, latent_pair_kernel, &cfg) != cudaSuccess || n <= 0) {
+            cudaGetLastError();
+            return kvq_num_sms() / 2;
+        }
+        found[dev] = n;
+    }
+    return found[dev];
+}
+
 LatPlan latent_plan(const kvq_seqs* S, int32_t n_heads, int64_t n_rows, int32_t max_new) {
     LatPlan p;
-    p.nr = (int)std::min<int64_t>(LA_ROWS, ((int64_t)max_new * n_heads + 15) / 16 * 16);
-    p.nr = std::max(p.nr, 16);
-    const int64_t by_max = S->batch * (((int64_t)max_new * n_heads + p.nr - 1) / p.nr);
+    const int64_t most = (int64_t)max_new * n_heads;   // query rows of a sequence
+    p.pairs = most > 32;
+    p.nr = p.pairs ? 128 : std::max(16, (int)((most + 15) / 16 * 16));
+    const int64_t by_max = S->batch * ((most + p.nr - 1) / p.nr);
     p.items = std::max<int64_t>(1, std::min(by_max, n_rows * n_heads / p.nr + S->batch));
-    p.keys = p.nr <= 32 ? 48 : 32;
-    p.ahead = 1;
-    const int64_t steps = p.items * ((S->max_len + p.keys - 1) / p.keys);
-    p.steps = steps;
-    p.ctas = (int)std::max<int64_t>(1, std::min<int64_t>({steps, kvq_num_sms(), KVQ_LATENT_MAX_CTAS}));
-    const size_t stage = p.keys / 8 * LA_GROUP, fixed = 1024 + (size_t)p.nr * (ROW * 2 + (p.ahead + 1) * 128);
-    p.ns = (int)std::min<size_t>((LA_SMEM - fixed) / stage, LA_MAX_NS);
-    p.smem = fixed + p.ns * stage;
+    p.keys = p.pairs ? LB_KEYS : 48;
+    p.steps = p.items * ((S->max_len + p.keys - 1) / p.keys);
+    p.ctas = (int)std::max<int64_t>(1, std::min<int64_t>({p.steps, p.pairs ? latent_pairs() : kvq_num_sms(), KVQ_LATENT_MAX_CTAS}));
+    const size_t stage = p.keys / 8 * LA_GROUP, fixed = 1024 + (size_t)p.nr * (ROW * 2 + 2 * 128);
+    p.ns = p.pairs ? LB_NS : (int)std::min<size_t>((LA_SMEM - fixed) / stage, LA_MAX_NS);
+    p.smem = p.pairs ? LB_SMEM : fixed + p.ns * stage;
     const size_t rows = (size_t)2 * p.ctas * p.nr;
     p.off_ml = sizeof(KvqWsHeader);
     p.off_cuts = kvq_round_up(p.off_ml + rows * sizeof(float2), 256);
@@ -699,13 +1070,14 @@ extern "C" int kv_latent_attn(const kvq_latent* C, const kvq_seqs* S, int32_t n_
     if (S->batch == 0 || n_rows == 0) return KVQ_OK;
     KVQ_REQUIRE(q && out && q_starts && (S->block_table || S->max_len == 0), KVQ_ERR_INVALID_ARG, "%s: NULL buffer", fn);
     KVQ_REQUIRE((((uintptr_t)q | (uintptr_t)out) & 15u) == 0, KVQ_ERR_INVALID_ARG, "%s: q and out must be 16-byte aligned", fn);
-    CUtensorMap map_q, map_rows;
+    CUtensorMap map_q, map_rows, map_v;
     const uint64_t qd[3] = {64, (uint64_t)n_rows * n_heads, LA_CHUNKS}, qs[2] = {ROW * 2, 128};
-    const uint32_t qb[3] = {64, (uint32_t)p.nr, LA_CHUNKS};
+    const uint32_t qb[3] = {64, (uint32_t)std::min(p.nr, LA_ROWS), LA_CHUNKS};
     const uint64_t rd[4] = {64, 8, LA_CHUNKS, (uint64_t)C->num_blocks * (PG / 8)}, rs[3] = {ROW * 2, 128, 8 * ROW * 2};
-    const uint32_t rb[4] = {64, 8, LA_CHUNKS, PG / 8};
+    const uint32_t rb[4] = {64, 8, LA_CHUNKS, PG / 8}, vb[4] = {64, 8, LAT / 128, PG / 8};
     st = make_map(&map_q, q, 3, qd, qs, qb, fn);
     if (!st) st = make_map(&map_rows, C->rows, 4, rd, rs, rb, fn);
+    if (!st && p.pairs) st = make_map(&map_v, C->rows, 4, rd, rs, vb, fn);
     if (st) return st;
     a.bt = S->block_table, a.seq_lens = S->seq_lens, a.q_starts = q_starts, a.parents = parents;
     a.n_rows = n_rows, a.num_blocks = C->num_blocks;
@@ -720,10 +1092,18 @@ extern "C" int kv_latent_attn(const kvq_latent* C, const kvq_seqs* S, int32_t n_
         const cudaError_t e = kvq_launch_pdl(kernel, dim3(p.ctas), dim3(LA_NT), p.smem, kvq_stream(stream), map_q, map_rows, a);
         return e == cudaSuccess ? (int)KVQ_OK : kvq_fail(KVQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
     };
-    st = p.keys == 48 ? go(latent_attn_kernel<48, 1>) : go(latent_attn_kernel<32, 1>);
+    if (p.pairs) {
+        st = kvq_prepare_kernel((const void*)latent_pair_kernel, LB_SMEM);
+        if (st) return st;
+        const cudaError_t e = kvq_launch_pdl(latent_pair_kernel, dim3(2 * p.ctas), dim3(LA_NT), LB_SMEM, kvq_stream(stream), map_q,
+                                             map_rows, map_v, a);
+        st = e == cudaSuccess ? (int)KVQ_OK : kvq_fail(KVQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+    } else {
+        st = go(latent_attn_kernel<48, 1>);
+    }
     if (st || p.ctas == 1) return st;
     cudaError_t e;
-    if (p.ctas > 6 * p.items) {
+    if (p.items * p.nr <= 128 && p.ctas > 6) {
         // few row groups, of many parts each
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)p.items * 4, p.nr);
