@@ -711,7 +711,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LA_NT, 1)
             const auto desc = [](uint32_t hi, uint32_t lo) { return (uint64_t)hi << 32 | lo; };
             Place in, out;   // of the next S and the next O (stages and buffers alike: two of each)
             const auto qk = [&] {
-                bar_wait_pair(&S.abort, a.hdr, &S.k_full[in.i], in.round);
+                bar_wait(&S.abort, a.hdr, &S.k_full[in.i], in.round);
                 tc_after();
                 uint32_t x = lq, y = lk + (in.i * LB_K >> 4);
                 asm volatile("" : "+r"(x), "+r"(y));
@@ -728,7 +728,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LA_NT, 1)
             };
             for (int seg = 0;;) {
                 if (g.nt > 0) {
-                    bar_wait_pair(&S.abort, a.hdr, &S.q_full, seg & 1);
+                    bar_wait(&S.abort, a.hdr, &S.q_full, seg & 1);
                     ++seg;
                     qk();
                     if (g.nt == 1) tc_commit_pair(&S.q_free);
@@ -738,7 +738,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LA_NT, 1)
                         qk();
                         if (j + 2 == g.nt) tc_commit_pair(&S.q_free);
                     }
-                    bar_wait_pair(&S.abort, a.hdr, &S.p_full[out.i], out.round);
+                    bar_wait(&S.abort, a.hdr, &S.p_full[out.i], out.round);
                     tc_after();
                     uint32_t y = lv + (out.i * LB_V >> 4), z = lp + (out.i * LB_P >> 4);
                     asm volatile("" : "+r"(y), "+r"(z));

@@ -230,27 +230,10 @@ __device__ __forceinline__ uint32_t saddr_in(const void* p, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr(p)), "r"(rank));
     return r;
 }
+// (what an arrival stands for lies in the arriving CTA's own shared memory, where products of the pair read it: the
+// order within that CTA is enough, and a release to the cluster costs 1000 to 2500 cycles)
 __device__ __forceinline__ void bar_arrive_in(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// bar_wait for a barrier that the other CTA of the pair arrives at, too
-__device__ __forceinline__ void bar_wait_pair(int32_t* abort, KvqWsHeader* hdr, uint64_t* bar, uint32_t parity) {
-    for (uint32_t it = 0;; ++it) {
-        uint32_t ok;
-        asm volatile(
-            "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
-            : "=r"(ok)
-            : "r"(saddr(bar)), "r"(parity)
-            : "memory");
-        if (ok) return;
-        if ((it & 63) != 63) continue;
-        if (*(volatile int32_t*)abort) return;
-        if (it > KVQ_SPIN) {
-            *(volatile int32_t*)abort = 1;
-            kvq_dev_flag(hdr, KVQ_DEV_TIMEOUT, (int32_t)blockIdx.x);
-            return;
-        }
-    }
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // a copy into this CTA that signals a barrier of the pair (an address of saddr_in)
 __device__ __forceinline__ void tma_page_pair(uint32_t dst, const CUtensorMap* map, int group, uint32_t bar) {
