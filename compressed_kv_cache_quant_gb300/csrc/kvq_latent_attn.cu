@@ -589,6 +589,8 @@ constexpr int LB_K = LB_KEYS / 2 * ROW * 2;      // bytes of a CTA's keys of a s
 constexpr int LB_V = LB_KEYS * LAT;              // and of its values (two bytes each, half of them)
 constexpr int LB_V_GROUP = 4 * 1024;             // eight rows of its four chunks
 constexpr int LB_NS = 2;
+constexpr int LB_NT = 224;                       // softmax 0-3, products 4, keys 5, values 6
+constexpr int LB_FAR = 3;                        // steps that keys are brought into L2 ahead of their load
 constexpr int LB_Q = 64 * ROW * 2, LB_P = 64 * 128;
 constexpr int LB_SMEM = 1024 + LB_Q + LB_NS * (LB_K + LB_V) + 2 * LB_P;
 
@@ -600,7 +602,7 @@ struct SharedPair {
     float half[128];      // what the two threads of a row have to tell one another
 };
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LA_NT, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LB_NT, 1)
     latent_pair_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v, const __grid_constant__ LatArgs a) {
     extern __shared__ unsigned char raw[];
@@ -645,21 +647,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LA_NT, 1)
     if (g.b < 0) {
         // no work for this pair
     } else if (warp == 5) {
-        // ---- loads: keys and queries signal rank 0, which issues the products; values stay within the CTA
+        // ---- queries and keys: they signal rank 0, which issues the products.  Two stages are too few for the latency of
+        // HBM, so a step's pages are brought into L2 LB_FAR steps before
         const int nowhere = (int)(a.num_blocks * (PG / 8));   // a group of rows behind the pool: zeros
         Place st;
         int loaded = 0;
         bool ok = true;
         for (int seg = 0; ok;) {
+            // lanes 0 and 1 look up one of this CTA's two pages of a step each
             const auto group_of = [&](int j) {
-                const int lp = (g.step + j) * (LB_KEYS / PG) + lane;
-                if (j >= g.nt || lane >= LB_KEYS / PG || lp * PG >= g.end) return nowhere;
+                const int lp = (g.step + j) * (LB_KEYS / PG) + 2 * (int)rank + lane;
+                if (j >= g.nt || lane >= 2 || lp * PG >= g.end) return nowhere;
                 const int32_t page = a.bt[(int64_t)g.b * a.max_blocks + lp];
                 if (page >= 0 && page < a.num_blocks) return page * (PG / 8);
                 kvq_dev_flag(a.hdr, KVQ_DEV_BAD_PAGE, page);
                 return nowhere;
             };
-            int y = group_of(0);
+            int y[LB_FAR + 1];   // of the steps j .. j + LB_FAR
+#pragma unroll
+            for (int k = 0; k <= LB_FAR; ++k) y[k] = group_of(k);
             if (g.nt > 0) {
                 if (seg > 0) bar_wait(&S.abort, a.hdr, &S.q_free, (seg - 1) & 1);
                 ok = !aborted(&S.abort);
@@ -672,9 +678,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LA_NT, 1)
             }
             for (int j = 0; j < g.nt && ok; ++j, ++loaded) {
                 const int pages = min(LB_KEYS / PG, (g.end - (g.step + j) * LB_KEYS + PG - 1) / PG);
-                int to[LB_KEYS / PG];
+                int to[2];
 #pragma unroll
-                for (int k = 0; k < LB_KEYS / PG; ++k) to[k] = __shfl_sync(0xffffffffu, y, k);
+                for (int k = 0; k < 2; ++k) to[k] = __shfl_sync(0xffffffffu, y[0], k);
                 if (loaded >= LB_NS) bar_wait(&S.abort, a.hdr, &S.k_empty[st.i], st.round ^ 1);
                 ok = !aborted(&S.abort);
                 if (ok && elect()) {
@@ -682,10 +688,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LA_NT, 1)
                     const uint32_t bar = saddr_in(&S.k_full[st.i], 0);
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
-                        if (2 * (int)rank + k < pages)
-                            tma_page_pair(sk + st.i * LB_K + k * (PG * ROW * 2), &map_k, rank == 0 ? to[k] : to[2 + k], bar);
+                        if (2 * (int)rank + k < pages) tma_page_pair(sk + st.i * LB_K + k * (PG * ROW * 2), &map_k, to[k], bar);
                 }
                 __syncwarp();
+                if (y[LB_FAR] != nowhere && lane < 2) tma_page_prefetch(&map_k, y[LB_FAR]);
+#pragma unroll
+                for (int k = 0; k < LB_FAR; ++k) y[k] = y[k + 1];
+                y[LB_FAR] = group_of(j + 1 + LB_FAR);
+                st.next(LB_NS);
+            }
+            if (!g.next(a)) break;
+        }
+    } else if (warp == 6) {
+        // ---- values: they stay within the CTA
+        const int nowhere = (int)(a.num_blocks * (PG / 8));
+        Place st;
+        int loaded = 0;
+        for (bool ok = true; ok;) {
+            const auto group_of = [&](int j) {   // (what is no page the keys' warp flags)
+                const int lp = (g.step + j) * (LB_KEYS / PG) + lane;
+                if (j >= g.nt || lane >= LB_KEYS / PG || lp * PG >= g.end) return nowhere;
+                const int32_t page = a.bt[(int64_t)g.b * a.max_blocks + lp];
+                return page >= 0 && page < a.num_blocks ? page * (PG / 8) : nowhere;
+            };
+            int y = group_of(0);
+            for (int j = 0; j < g.nt && ok; ++j, ++loaded) {
+                const int pages = min(LB_KEYS / PG, (g.end - (g.step + j) * LB_KEYS + PG - 1) / PG);
+                int to[LB_KEYS / PG];
+#pragma unroll
+                for (int k = 0; k < LB_KEYS / PG; ++k) to[k] = __shfl_sync(0xffffffffu, y, k);
                 if (loaded >= LB_NS) bar_wait(&S.abort, a.hdr, &S.v_empty[st.i], st.round ^ 1);
                 ok = !aborted(&S.abort);
                 if (ok && elect()) {
@@ -879,25 +910,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LA_NT, 1)
                     }
                 }
             }
-            if (nt > 0 && !aborted(&S.abort)) {
-#pragma unroll 2
+            if (nt > 0) {
+                // Through the weights' place (16 KB, free until the next segment's first ones), 32 values of every thread at a
+                // time, so that a warp writes whole lines: written by the rows' threads they take 10000 cycles.
+                // Thread t's 16-byte pieces lie at t * 128, piece k at k ^ (t % 8).
+                const bool ok = !aborted(&S.abort);
+#pragma unroll 1
                 for (int c = 0; c < 256; c += 32) {
                     uint32_t o[32];
                     tm_ld32(lane_base + TM_O + c, o);
-                    if (!valid) continue;
                     if (whole) {
-                        uint4* dst = reinterpret_cast<uint4*>(a.out + (int64_t)(out_row + r) * LAT + 256 * half + c);
-                        uint32_t w[16];
 #pragma unroll
                         for (int x = 0; x < 16; ++x)
-                            w[x] = half2_bits(__uint_as_float(o[2 * x]) * f, __uint_as_float(o[2 * x + 1]) * f);
-#pragma unroll
-                        for (int x = 0; x < 16; x += 4) dst[x / 4] = make_uint4(w[x], w[x + 1], w[x + 2], w[x + 3]);
-                    } else {
-                        uint4* dst = reinterpret_cast<uint4*>(a.part + (slot * a.nr + in_group) * LAT + 256 * half + c);
-#pragma unroll
-                        for (int x = 0; x < 32; x += 4) dst[x / 4] = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+                            o[x] = half2_bits(__uint_as_float(o[2 * x]) * f, __uint_as_float(o[2 * x + 1]) * f);
                     }
+                    const int pieces = whole ? 4 : 8;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (k < pieces)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sp + tid * 128 + ((k ^ (tid & 7)) << 4)), "r"(o[4 * k]),
+                                         "r"(o[4 * k + 1]), "r"(o[4 * k + 2]), "r"(o[4 * k + 3])
+                                         : "memory");
+                    sm_any(false);
+                    for (int x = tid; x < 128 * pieces; x += 128) {
+                        const int t = whole ? x >> 2 : x >> 3, k = x & (pieces - 1), row = t & 63, at_dim = 256 * (t >> 6) + c;
+                        if (!ok || row >= rows) continue;
+                        uint4 w;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                                     : "r"(sp + t * 128 + ((k ^ (t & 7)) << 4))
+                                     : "memory");
+                        if (whole)
+                            *reinterpret_cast<uint4*>(a.out + (int64_t)(out_row + row) * LAT + at_dim + 8 * k) = w;
+                        else
+                            *reinterpret_cast<uint4*>(a.part + (slot * a.nr + 64 * (int)rank + row) * LAT + at_dim + 4 * k) = w;
+                    }
+                    sm_any(false);
                 }
             }
             tc_before();   // (O is read before the next segment's first weights are handed over)
@@ -1008,7 +1056,7 @@ int latent_pairs() {
         int n = 0;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2 * (kvq_num_sms() / 2));
-        cfg.blockDim = dim3(LA_NT);
+        cfg.blockDim = dim3(LB_NT);
         cfg.dynamicSmemBytes = LB_SMEM;
         if (kvq_prepare_kernel((const void*)latent_pair_kernel, LB_SMEM) != KVQ_OK ||
             cudaOccupancyMaxActiveClusters(&n, latent_pair_kernel, &cfg) != cudaSuccess || n <= 0) {
@@ -1095,7 +1143,7 @@ extern "C" int kv_latent_attn(const kvq_latent* C, const kvq_seqs* S, int32_t n_
     if (p.pairs) {
         st = kvq_prepare_kernel((const void*)latent_pair_kernel, LB_SMEM);
         if (st) return st;
-        const cudaError_t e = kvq_launch_pdl(latent_pair_kernel, dim3(2 * p.ctas), dim3(LA_NT), LB_SMEM, kvq_stream(stream), map_q,
+        const cudaError_t e = kvq_launch_pdl(latent_pair_kernel, dim3(2 * p.ctas), dim3(LB_NT), LB_SMEM, kvq_stream(stream), map_q,
                                              map_rows, map_v, a);
         st = e == cudaSuccess ? (int)KVQ_OK : kvq_fail(KVQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
     } else {

@@ -257,6 +257,10 @@ __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(saddr(bar))
         : "memory");
 }
+// brings a page into L2
+__device__ __forceinline__ void tma_page_prefetch(const CUtensorMap* map, int group) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %1, %1, %2}];" ::"l"(map), "r"(0), "r"(group) : "memory");
+}
 // arrives at the barrier in both CTAs when all products so far are done
 __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(saddr(bar)),
