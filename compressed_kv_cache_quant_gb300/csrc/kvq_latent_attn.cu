@@ -37,6 +37,7 @@ constexpr int PG = KVQ_BLOCK_TOKENS;
 constexpr int LAT = KVQ_LATENT_DIM, ROT = KVQ_LATENT_ROPE, ROW = LAT + ROT;
 constexpr int LA_NT = 192;
 constexpr int LA_ROWS = 64;               // query rows per CTA
+constexpr int LA_FAR = 2;                 // steps that pages are brought into L2 ahead of their load
 constexpr int LA_MAX_NS = 8;              // most stages
 constexpr int LA_CHUNKS = ROW / 64;
 constexpr int LA_GROUP = LA_CHUNKS * 1024;              // bytes of eight staged rows
@@ -308,7 +309,9 @@ __global__ void __launch_bounds__(LA_NT, 1)
                 kvq_dev_flag(a.hdr, KVQ_DEV_BAD_PAGE, page);
                 return nowhere;
             };
-            int y = group_of(0);
+            int y = group_of(0), ahead[LA_FAR];
+#pragma unroll
+            for (int k = 0; k < LA_FAR; ++k) ahead[k] = group_of(1 + k);
             if (g.nt > 0) {
                 if (seg > 0) bar_wait(&S.abort, a.hdr, &S.q_free, (seg - 1) & 1);
                 ok = !aborted(&S.abort);
@@ -333,7 +336,11 @@ __global__ void __launch_bounds__(LA_NT, 1)
                         if (k < pages) tma_page(skv + st.i * STAGE + k * (PG * ROW * 2), &map_rows, to[k], &S.kv_full[st.i]);
                 }
                 __syncwarp();
-                y = group_of(j + 1);
+                if (ahead[LA_FAR - 1] != nowhere) tma_page_prefetch(&map_rows, ahead[LA_FAR - 1]);
+                y = ahead[0];
+#pragma unroll
+                for (int k = 0; k + 1 < LA_FAR; ++k) ahead[k] = ahead[k + 1];
+                ahead[LA_FAR - 1] = group_of(j + 1 + LA_FAR);
                 st.next(a.ns);
             }
             if (!g.next(a)) break;
