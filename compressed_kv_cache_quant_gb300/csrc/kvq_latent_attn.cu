@@ -257,6 +257,7 @@ __global__ void __launch_bounds__(LA_NT, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // queries, stages, weights: with nr below 64 the first product reads behind the queries, into the stages, for
     // rows of S that nothing looks at
+    if (tid == 64) map_prefetch(&map_q), map_prefetch(&map_rows);
     const uint32_t sq = (saddr(raw) + 1023) & ~1023u, skv = sq + a.nr * ROW * 2, sp = skv + a.ns * STAGE,
                    p_bytes = a.nr * 128;   // (a row of weights takes 128 bytes, as the swizzle wants it)
     kvq_pdl_begin();
@@ -616,6 +617,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LB_NT, 1)
     __shared__ SharedPair S;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_rank();
+    if (tid == 64) map_prefetch(&map_q), map_prefetch(&map_k), map_prefetch(&map_v);
     const int pair = blockIdx.x >> 1;
     const uint32_t sq = (saddr(raw) + 1023) & ~1023u, sk = sq + LB_Q, sv = sk + LB_NS * LB_K, sp = sv + LB_NS * LB_V;
     kvq_pdl_begin();
@@ -973,72 +975,128 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LB_NT, 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TM_COLS) : "memory");
 }
 
-// Joins the parts of a row in the order of their CTAs and leaves the workspace zeroed: 128 / Q threads per part take
-// four values each, GR parts at a time.  Q > 1, for rows of many parts: a cluster of Q CTAs per row.
-template <int Q, int GR>
-__global__ void __launch_bounds__(128 / Q * GR) latent_join_kernel(const __grid_constant__ LatArgs a) {
-    constexpr int W = 128 / Q;
+// ---------------------------------------------------------------- the join of a row's parts
+//
+// In the order of their CTAs, so that results do not depend on the run, and the workspace is left zeroed.  A row's first
+// part is its CTA's last segment, the others are their CTAs' first ones.  Weights of the parts: 2^(anchor - largest
+// anchor); a part without a visible token wrote no row.  (Joined by the CTA whose part came last, the work is spread over
+// too few threads: 57 us more for 40 row groups of 128 rows in three parts each.)
+
+__device__ __forceinline__ int64_t part_slot(const LatArgs& a, int c0, int i, int r) {
+    return ((int64_t)2 * (c0 + i) + (i == 0 ? 1 : 0)) * a.nr + r;
+}
+
+// A warp per row: 16 values per lane.
+constexpr int LJ_NW = 8;
+__global__ void __launch_bounds__(32 * LJ_NW) latent_join_kernel(const __grid_constant__ LatArgs a, int n_rows) {
+    const int lane = threadIdx.x & 31, row = blockIdx.x * LJ_NW + (threadIdx.x >> 5);
+    if (row >= n_rows) return;
+    kvq_pdl_begin();
+    const int4 cut = a.cuts[row];
+    if (cut.x == 0) return;
+    const int c0 = cut.x - 1, n = cut.y, r = row % a.nr;
+    float mx = -INFINITY, y = 0.0f;
+    float2 v = make_float2(0.0f, 0.0f);
+    for (int i = lane; i < n; i += 32) {
+        v = a.ml[part_slot(a, c0, i, r)];
+        if (v.y != 0.0f) mx = fmaxf(mx, v.x);
+    }
+    mx = kvq_warp_max(mx);
+    float4 o[4] = {};
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        float f = 0.0f;
+        if (i0 + lane < n) {
+            float2* const at = a.ml + part_slot(a, c0, i0 + lane, r);
+            if (n > 32) v = *at;
+            f = v.y != 0.0f ? exp2f(v.x - mx) : 0.0f;
+            y += f * v.y;
+            *at = make_float2(0.0f, 0.0f);
+        }
+        const int m = min(32, n - i0);
+#pragma unroll 4
+        for (int i = 0; i < m; ++i) {
+            const float4* part = reinterpret_cast<const float4*>(a.part + part_slot(a, c0, i0 + i, r) * LAT) + lane;
+            const float w = __shfl_sync(0xffffffffu, f, i);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float4 p = part[32 * x];
+                o[x].x += w * p.x, o[x].y += w * p.y, o[x].z += w * p.z, o[x].w += w * p.w;
+            }
+        }
+    }
+    // (behind the loads: a store between them would hold up the next one)
+    for (int i = 0; i < n; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            reinterpret_cast<float4*>(a.part + part_slot(a, c0, i, r) * LAT)[lane + 32 * x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    // (every lane's sum is over its own parts, joined in one order)
+    y = kvq_warp_sum(y);
+    const float inv = y == 0.0f ? 0.0f : 1.0f / y;
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+        reinterpret_cast<uint2*>(a.out + (int64_t)cut.z * LAT)[lane + 32 * x] =
+            make_uint2(half2_bits(o[x].x * inv, o[x].y * inv), half2_bits(o[x].z * inv, o[x].w * inv));
+    if (lane == 0) {
+        a.cuts[row] = make_int4(0, 0, 0, 0);
+        if (a.lse != nullptr) a.lse[cut.z] = y == 0.0f ? -INFINITY : (mx + log2f(y)) * KVQ_LN2;
+    }
+}
+
+// Few rows of many parts: a cluster of LQ CTAs per row, 128 / LQ threads per part with four values each, LQ_GR parts at a
+// time.
+constexpr int LQ = 4, LQ_W = 128 / LQ, LQ_GR = 16;
+__global__ void __cluster_dims__(LQ, 1, 1) __launch_bounds__(LQ_W * LQ_GR) latent_join_wide_kernel(const __grid_constant__ LatArgs a) {
     __shared__ float weight[KVQ_LATENT_MAX_CTAS];
-    __shared__ float4 sums[GR][W];
-    const int tid = threadIdx.x, lane = tid & 31, quarter = blockIdx.x % Q;
-    int4* const cut_at = a.cuts + (int64_t)(blockIdx.x / Q) * a.nr + blockIdx.y;
+    __shared__ float4 sums[LQ_GR][LQ_W];
+    const int tid = threadIdx.x, lane = tid & 31, quarter = blockIdx.x % LQ;
+    int4* const cut_at = a.cuts + blockIdx.x / LQ;
+    const int r = blockIdx.x / LQ % a.nr;
     kvq_pdl_begin();
     const int4 cut = *cut_at;
     if (cut.x == 0) return;   // (a cluster's CTAs read the same)
     const int c0 = cut.x - 1, n = cut.y;
-    // the first part is its CTA's last segment, the others are their CTAs' first ones
-    const auto slot_of = [&](int i) { return ((int64_t)2 * (c0 + i) + (i == 0 ? 1 : 0)) * a.nr + blockIdx.y; };
-    const auto part_of = [&](int i) { return reinterpret_cast<float4*>(a.part + slot_of(i) * LAT) + quarter * W + tid % W; };
+    const auto part_of = [&](int i) { return reinterpret_cast<float4*>(a.part + part_slot(a, c0, i, r) * LAT) + quarter * LQ_W + tid % LQ_W; };
     if (tid < 32) {
-        // weights of the parts: 2^(anchor - largest anchor); a part without a visible token wrote no row
         float mx = -INFINITY, y = 0.0f;
         for (int i = lane; i < n; i += 32) {
-            const float2 v = a.ml[slot_of(i)];
+            const float2 v = a.ml[part_slot(a, c0, i, r)];
             if (v.y != 0.0f) mx = fmaxf(mx, v.x);
         }
         mx = kvq_warp_max(mx);
         for (int i = lane; i < n; i += 32) {
-            const float2 v = a.ml[slot_of(i)];
+            const float2 v = a.ml[part_slot(a, c0, i, r)];
             const float f = v.y != 0.0f ? exp2f(v.x - mx) : 0.0f;
             weight[i] = f;
             y += f * v.y;
         }
-        // (every lane's sum is over its own parts, joined in one order)
         y = kvq_warp_sum(y);
         const float inv = y == 0.0f ? 0.0f : 1.0f / y;
         for (int i = lane; i < n; i += 32) weight[i] *= inv;
         if (lane == 0 && quarter == 0 && a.lse != nullptr) a.lse[cut.z] = y == 0.0f ? -INFINITY : (mx + log2f(y)) * KVQ_LN2;
     }
-    if (Q > 1) {
-        asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
-    } else {
-        __syncthreads();
-    }
+    __syncthreads();
+    cluster_sync();   // (the others have read what is zeroed below)
     if (quarter == 0) {
-        for (int i = tid; i < n; i += W * GR) a.ml[slot_of(i)] = make_float2(0.0f, 0.0f);
+        for (int i = tid; i < n; i += LQ_W * LQ_GR) a.ml[part_slot(a, c0, i, r)] = make_float2(0.0f, 0.0f);
         if (tid == 0) *cut_at = make_int4(0, 0, 0, 0);
     }
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const int grp = tid / W;
+    const int grp = tid / LQ_W;
 #pragma unroll 8
-    for (int i = grp; i < n; i += GR) {
+    for (int i = grp; i < n; i += LQ_GR) {
         const float4 v = *part_of(i);
         const float f = weight[i];
         o.x += f * v.x, o.y += f * v.y, o.z += f * v.z, o.w += f * v.w;
     }
-    // (behind the loads: a store between them would hold up the next one)
-    for (int i = grp; i < n; i += GR) *part_of(i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (GR > 1) {
-        sums[grp][tid % W] = o;
-        __syncthreads();
-        if (grp > 0) return;
-        for (int k = 1; k < GR; ++k) {
-            const float4 v = sums[k][tid];
-            o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
-        }
+    for (int i = grp; i < n; i += LQ_GR) *part_of(i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    sums[grp][tid % LQ_W] = o;
+    __syncthreads();
+    if (grp > 0) return;
+    for (int k = 1; k < LQ_GR; ++k) {
+        const float4 v = sums[k][tid];
+        o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
     }
-    reinterpret_cast<uint2*>(a.out + (int64_t)cut.z * LAT)[quarter * W + tid % W] =
-        make_uint2(half2_bits(o.x, o.y), half2_bits(o.z, o.w));
+    reinterpret_cast<uint2*>(a.out + (int64_t)cut.z * LAT)[quarter * LQ_W + tid] = make_uint2(half2_bits(o.x, o.y), half2_bits(o.z, o.w));
 }
 
 struct LatPlan {
@@ -1121,7 +1179,7 @@ extern "C" int kv_latent_attn(const kvq_latent* C, const kvq_seqs* S, int32_t n_
     if (st) return st;
     KVQ_REQUIRE(C->num_blocks * PG <= INT32_MAX && n_rows * n_heads <= INT32_MAX - LA_ROWS, KVQ_ERR_UNSUPPORTED,
                 "%s: more than 2^31 - 1 rows in the pool or queries", fn);
-    KVQ_REQUIRE(p.steps <= INT32_MAX - KVQ_LATENT_MAX_CTAS, KVQ_ERR_UNSUPPORTED, "%s: more than 2^31 steps (queries times max_len)", fn);
+    KVQ_REQUIRE(p.items * p.nr <= INT32_MAX / 8 && p.steps <= INT32_MAX - KVQ_LATENT_MAX_CTAS, KVQ_ERR_UNSUPPORTED, "%s: more than 2^31 steps (queries times max_len)", fn);
     if (S->batch == 0 || n_rows == 0) return KVQ_OK;
     KVQ_REQUIRE(q && out && q_starts && (S->block_table || S->max_len == 0), KVQ_ERR_INVALID_ARG, "%s: NULL buffer", fn);
     KVQ_REQUIRE((((uintptr_t)q | (uintptr_t)out) & 15u) == 0, KVQ_ERR_INVALID_ARG, "%s: q and out must be 16-byte aligned", fn);
@@ -1157,24 +1215,12 @@ extern "C" int kv_latent_attn(const kvq_latent* C, const kvq_seqs* S, int32_t n_
         st = go(latent_attn_kernel<48, 1>);
     }
     if (st || p.ctas == 1) return st;
-    cudaError_t e;
-    if (p.items * p.nr <= 128 && p.ctas > 6) {
-        // few row groups, of many parts each
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)p.items * 4, p.nr);
-        cfg.blockDim = dim3(512);
-        cfg.stream = kvq_stream(stream);
-        cudaLaunchAttribute attr[2];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = 4, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 2;
-        e = cudaLaunchKernelEx(&cfg, latent_join_kernel<4, 16>, a);
-    } else {
-        e = kvq_launch_pdl(latent_join_kernel<1, 1>, dim3((unsigned)p.items, p.nr), dim3(128), 0, kvq_stream(stream), a);
-    }
+    const int64_t group_rows = p.items * p.nr;
+    const cudaError_t e =
+        group_rows <= 128 && p.ctas > 6
+            ? kvq_launch_pdl(latent_join_wide_kernel, dim3((unsigned)group_rows * LQ), dim3(LQ_W * LQ_GR), 0, kvq_stream(stream), a)
+            : kvq_launch_pdl(latent_join_kernel, dim3((unsigned)((group_rows + LJ_NW - 1) / LJ_NW)), dim3(32 * LJ_NW), 0,
+                             kvq_stream(stream), a, (int)group_rows);
     if (e != cudaSuccess) return kvq_fail(KVQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
     return KVQ_OK;
 }

@@ -257,6 +257,9 @@ __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(saddr(bar))
         : "memory");
 }
+__device__ __forceinline__ void map_prefetch(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 // brings a page into L2
 __device__ __forceinline__ void tma_page_prefetch(const CUtensorMap* map, int group) {
     asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %1, %1, %2}];" ::"l"(map), "r"(0), "r"(group) : "memory");
