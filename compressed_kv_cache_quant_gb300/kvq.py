@@ -82,6 +82,7 @@ class LayerCache:
         self.c = Pool(num_blocks, max_seqs, t_cap, _p(self.k_codes), _p(self.v_codes), _p(self.k_sz),
                       _p(self.v_sz), _p(self.k_tail), _p(self.k16), _p(self.v16), _p(self.kT),
                       _p(self.k_absmax))
+        self.gpu = (self.v_codes if self.v16 is None else self.v16).get_device()
 
 
 class LatentCache:
@@ -92,6 +93,7 @@ class LatentCache:
         self.num_blocks = int(num_blocks)
         self.rows = torch.zeros((self.num_blocks, BLOCK_TOKENS, LATENT_DIM + LATENT_ROPE), dtype=torch.float16, device=device)
         self.c = _abi.Latent(LATENT_DIM, LATENT_ROPE, self.num_blocks, self.rows.data_ptr())
+        self.gpu = self.rows.get_device()
 
 
 class Batch:
@@ -104,6 +106,7 @@ class Batch:
         self.max_len = int(max_len)
         B, mb = self.block_table.shape
         self.c = Seqs(_p(self.block_table), _p(self.seq_lens), B, mb, self.max_len, 0)
+        self.gpu = self.seq_lens.get_device()
 
     @property
     def batch(self):
@@ -119,6 +122,7 @@ class Workspace:
         off = (-self.t.data_ptr()) % 256
         self.ptr = self.t.data_ptr() + off
         self.nbytes = n
+        self.gpu = self.t.get_device()
 
 
 class Allocator:
@@ -597,11 +601,10 @@ def _dtype_of(x, fn):
     raise KvqError(_abi.KVQ_ERR_UNSUPPORTED, fn, f"{x.dtype}: float16 or bfloat16")
 
 
-def _on(gpu, fn, **parts):
-    """Every part (a RopeTable, a cache, a Batch, a Workspace) has to live on GPU `gpu`."""
-    for name, t in parts.items():
-        if t is not None and t.get_device() != gpu:
-            raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, f"{name} is on {t.device}, not on GPU {gpu}")
+def _elsewhere(gpu, fn, *parts):
+    """The refusal of a call whose caches, tables or workspaces are not all on GPU `gpu`."""
+    where = ", ".join(f"{type(x).__name__} on {x.gpu}" for x in parts)
+    raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, f"{where}: not all on GPU {gpu}")
 
 
 def kv_rope_append(cache, seqs, rope, row_starts, q, k, v, q_out, ws, positions=None, q_weight=None, k_weight=None,
@@ -614,7 +617,8 @@ def kv_rope_append(cache, seqs, rope, row_starts, q, k, v, q_out, ws, positions=
     code = _dtype_of(k, fn)
     if (q is None) != (q_out is None):
         raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, "q and q_out come together")
-    _on(gpu, fn, rope=rope.steps, cache=cache.v16 if cache.v16 is not None else cache.v_codes, seqs=seqs.seq_lens, ws=ws.t)
+    if not rope.gpu == cache.gpu == seqs.gpu == ws.gpu == gpu:
+        _elsewhere(gpu, fn, rope, cache, seqs, ws)
     sq, sk = (n, L.n_q_heads, HEAD_DIM), (n, L.n_kv_heads, HEAD_DIM)
     qa, qs = _head_rows(q, sq, dt, gpu, fn, "q")
     ka, ks = _head_rows(k, sk, dt, gpu, fn, "k")
@@ -635,6 +639,8 @@ def kv_tree_attn(cache, seqs, q, parents, q_starts, max_new, out, ws, mod=None, 
     """kv_chunk_attn for trees of drafted tokens: parents (int32 [n_rows]) is every row's parent among its sequence's new
     tokens, -1 for a root; a node sees the cached tokens, itself and its ancestors."""
     fn, L, gpu = "kv_tree_attn", cache.layout, _gpu()
+    if not cache.gpu == seqs.gpu == ws.gpu == gpu:
+        _elsewhere(gpu, fn, cache, seqs, ws)
     B, H, n = seqs.c.batch, L.n_q_heads, _need(q, fn, "q").shape[0]
     shape = (n, H, HEAD_DIM)
     return check(lib().kv_tree_attn(
@@ -646,15 +652,17 @@ def kv_tree_attn(cache, seqs, q, parents, q_starts, max_new, out, ws, mod=None, 
 
 
 def _strided(x, shape, dtype, gpu, fn, name):
-    """(address, stride of every dimension but the last) of x, whose last dimension has no gaps."""
+    """(address, strides but the last) of x, whose last dimension has no gaps."""
     if not isinstance(x, torch.Tensor) or x.dtype is not dtype or x.shape != shape or x.get_device() != gpu:
         have = f"{x.dtype} {tuple(x.shape)} on {x.device}" if isinstance(x, torch.Tensor) else type(x).__name__
         raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, f"{name}: {have} instead of {dtype} {shape} on GPU {gpu}")
     st = x.stride()
     if st[-1] != 1:
         raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, f"{name}: a row's values must lie side by side")
-    # (the stride of a dimension of one entry is never used, and may be anything)
-    return (x.data_ptr(), *(s if n > 1 else 1 << 30 for s, n in zip(st[:-1], shape[:-1])))
+    # (the stride of a dimension of one entry is never used, and may be anything: a wide one stands for it)
+    if len(shape) == 2:
+        return x.data_ptr(), st[0] if shape[0] > 1 else 1 << 30
+    return x.data_ptr(), st[0] if shape[0] > 1 else 1 << 30, st[1] if shape[1] > 1 else 1 << 30
 
 
 def kv_latent_append(cache, seqs, rope, row_starts, c, k_rope, ws, c_weight=None, eps=1e-6, positions=None, q=None,
@@ -667,7 +675,8 @@ def kv_latent_append(cache, seqs, rope, row_starts, c, k_rope, ws, c_weight=None
     code = _dtype_of(c, fn)
     if (q is None) != (q_out is None):
         raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, "q and q_out come together")
-    _on(gpu, fn, rope=rope.steps, cache=cache.rows, seqs=seqs.seq_lens, ws=ws.t)
+    if not rope.gpu == cache.gpu == seqs.gpu == ws.gpu == gpu:
+        _elsewhere(gpu, fn, rope, cache, seqs, ws)
     ca, cs = _strided(c, (n, LATENT_DIM), dt, gpu, fn, "c")
     ka, ks = _strided(_need(k_rope, fn, "k_rope"), (n, LATENT_ROPE), dt, gpu, fn, "k_rope")
     heads, qa, qs, qh, oa, os, oh = 0, None, 0, 0, None, 0, 0
@@ -693,7 +702,8 @@ def kv_latent_attn(cache, seqs, q, q_starts, max_new, out, ws, scale=0.0, parent
     scale 0: 1/sqrt(192).  parents: the new tokens are trees, as kv_tree_attn."""
     fn, gpu = "kv_latent_attn", _gpu()
     n, H = _need(q, fn, "q").shape[:2]
-    _on(gpu, fn, cache=cache.rows, seqs=seqs.seq_lens, ws=ws.t)
+    if not cache.gpu == seqs.gpu == ws.gpu == gpu:
+        _elsewhere(gpu, fn, cache, seqs, ws)
     return check(lib().kv_latent_attn(
         ctypes.byref(cache.c), ctypes.byref(seqs.c), H,
         _dev(q, torch.float16, (n, H, LATENT_DIM + LATENT_ROPE), gpu, fn, "q"),
@@ -716,7 +726,8 @@ def kv_latent_expanded_attn(q, k_nope, k_rope, v, q_starts, k_starts, max_new, m
     fn, gpu = "kv_latent_expanded_attn", _gpu()
     n, H = _need(q, fn, "q").shape[:2]
     m, B = _need(k_nope, fn, "k_nope").shape[0], _need(q_starts, fn, "q_starts").shape[0] - 1
-    _on(gpu, fn, ws=ws.t)
+    if ws.gpu != gpu:
+        _elsewhere(gpu, fn, ws)
     na, ns, nh = _strided(k_nope, (m, H, HEAD_DIM), torch.float16, gpu, fn, "k_nope")
     ra, rs = _strided(_need(k_rope, fn, "k_rope"), (m, LATENT_ROPE), torch.float16, gpu, fn, "k_rope")
     va, vs, vh = _strided(_need(v, fn, "v"), (m, H, HEAD_DIM), torch.float16, gpu, fn, "v")
