@@ -83,7 +83,7 @@ struct ChunkArgs {
 // ---------------------------------------------------------------- what a CTA works on
 
 struct Shared {
-    uint64_t q_full, kv_full[CA_NS], kv_empty[CA_NS], s_full[2], p_full[2][2], o_full[2], drain;
+    uint64_t q_full, kv_full[EX_NS], kv_empty[EX_NS], s_full[2], p_full[2][2], o_full[2], drain;
     uint32_t tmem;
     int32_t abort;
     int32_t item_b, item_tok;                     // sequence and first new token of this CTA
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(CA_NT, 1)
     }
     if (tid == 0) {
         bar_init(&S.q_full, 1);
-        for (int i = 0; i < CA_NS; ++i) {
+        for (int i = 0; i < (EXP ? EX_NS : CA_NS); ++i) {
             bar_init(&S.kv_full[i], 1);
             bar_init(&S.kv_empty[i], 1);
         }
@@ -277,34 +277,26 @@ __global__ void __launch_bounds__(CA_NT, 1)
             }
             __syncwarp();
             if constexpr (EXP) {
-                // tile j is the pieces 5j .. 5j + 4 of a list that goes round the ring: K's three, V's two.  A piece's
-                // place was that of the piece eight before: of K(j - 2), V(j - 2) for K, of K(j - 1) for V.
+                // tile j is the pieces 5j .. 5j + 4 of a list that goes round the ring: K's three, V's two.  A piece's place was
+                // that of the piece eight before, and every place has its own barriers.
                 const int key0 = a.k_starts[b];
-                const auto to = [&](int j, int piece) { return skv + (5 * j + piece) % EX_NS * CA_HALF; };
-                for (int j = 0; j < nt; ++j) {
-                    const int key = key0 + tile_of(it0 + j) * CA_KEYS;
-                    if (j >= 2) {
-                        bar_wait(&S.abort, a.hdr, &S.kv_empty[j & 1], ((j - 2) >> 1) & 1);
-                        bar_wait(&S.abort, a.hdr, &S.kv_empty[2 + (j & 1)], ((j - 2) >> 1) & 1);
+                if (elect()) {
+                    for (int p = 0; p < 5 * nt; ++p) {
+                        const int j = p / 5, x = p - 5 * j, at = p % EX_NS, key = key0 + tile_of(it0 + j) * CA_KEYS;
+                        if (p >= EX_NS) bar_wait(&S.abort, a.hdr, &S.kv_empty[at], ((p / EX_NS) & 1) ^ 1);
+                        if (*(volatile int32_t*)&S.abort) break;
+                        const uint32_t to = skv + at * CA_HALF;
+                        bar_expect(&S.kv_full[at], CA_HALF);
+                        if (x < 2)
+                            tma_3d(to, &map_k, 64 * x, h, key, &S.kv_full[at]);
+                        else if (x == 2)
+                            tma_3d(to, &map_r, 0, key, 0, &S.kv_full[at]);
+                        else
+                            for (int y = 0; y < 2; ++y)
+                                tma_3d(to + y * (CA_HALF / 2), &map_v, 64 * y, h, key + 64 * (x - 3), &S.kv_full[at]);
                     }
-                    if (aborted(&S.abort)) break;
-                    if (elect()) {
-                        bar_expect(&S.kv_full[j & 1], 3 * CA_HALF);
-                        tma_3d(to(j, 0), &map_k, 0, h, key, &S.kv_full[j & 1]);
-                        tma_3d(to(j, 1), &map_k, 64, h, key, &S.kv_full[j & 1]);
-                        tma_3d(to(j, 2), &map_r, 0, key, 0, &S.kv_full[j & 1]);
-                    }
-                    __syncwarp();
-                    if (j >= 1) bar_wait(&S.abort, a.hdr, &S.kv_empty[(j - 1) & 1], ((j - 1) >> 1) & 1);
-                    if (aborted(&S.abort)) break;
-                    if (elect()) {
-                        bar_expect(&S.kv_full[2 + (j & 1)], CA_TILE);
-                        for (int x = 0; x < 4; ++x)
-                            tma_3d(to(j, 3 + x / 2) + x % 2 * (CA_HALF / 2), &map_v, 64 * (x % 2), h, key + 64 * (x / 2),
-                                   &S.kv_full[2 + (j & 1)]);
-                    }
-                    __syncwarp();
                 }
+                __syncwarp();
             } else {
             const int pg = lane & 7;   // lanes 0-7 look up one page each
             const int nowhere = (int)(a.num_blocks * a.H * (PG / 8));  // a group of rows behind the pool: zeros
@@ -375,36 +367,77 @@ __global__ void __launch_bounds__(CA_NT, 1)
             const uint32_t lq = (uint32_t)smem_desc(sq, 16, 0), lk = (uint32_t)smem_desc(skv, 16, 0),
                            lv = (uint32_t)smem_desc(skv, EXP ? CA_HALF / 2 : 1024, 0);
             const auto desc = [](uint32_t hi, uint32_t lo) { return (uint64_t)hi << 32 | lo; };
-            // (st: the tile's stage in the ring; the expanded form's tile)
             const auto qk = [&](int i, int st) {
                 if (elect()) {
-                    uint32_t x = lq + (i * Q_TILE >> 4), y = lk + (EXP ? 0 : st * CA_TILE >> 4);
+                    uint32_t x = lq + (i * CA_TILE >> 4), y = lk + (st * CA_TILE >> 4);
                     asm volatile("" : "+r"(x), "+r"(y));
 #pragma unroll
-                    for (int k = 0; k < Q_TILE / CA_HALF * 4; ++k) {
-                        if (EXP && (k & 3) == 0) {
-                            y = lk + ((5 * st + (k >> 2)) % EX_NS * CA_HALF >> 4);
-                            asm volatile("" : "+r"(y));
-                        }
+                    for (int k = 0; k < D / 16; ++k) {
                         mma_ss(TM_S + 128 * i, desc(hi_q, x + (((k >> 2) * CA_HALF + (k & 3) * 32) >> 4)),
-                               desc(hi_kv, y + (((EXP ? 0 : k >> 2) * 1024 + (k & 3) * 32) >> 4)), IDESC_QK, k > 0);
+                               desc(hi_kv, y + (((k >> 2) * 1024 + (k & 3) * 32) >> 4)), IDESC_QK, k > 0);
                     }
                     tc_commit(&S.s_full[i]);
                 }
             };
             const auto pv = [&](int i, int st, int half, bool acc) {
                 if (elect()) {
-                    uint32_t y = lv + ((EXP ? (5 * st + 3 + half) % EX_NS * CA_HALF : st * CA_TILE) >> 4);
+                    uint32_t y = lv + (st * CA_TILE >> 4);
                     asm volatile("" : "+r"(y));
 #pragma unroll
                     for (int k = 4 * half; k < 4 * half + 4; ++k)
-                        mma_ts(TM_O + 128 * i, TM_S + 128 * i + 8 * k, desc(hi_kv, y + ((EXP ? (k & 3) * 2048 : k * 4096) >> 4)),
-                               IDESC_PV, acc || k > 0);
+                        mma_ts(TM_O + 128 * i, TM_S + 128 * i + 8 * k, desc(hi_kv, y + (k * 4096 >> 4)), IDESC_PV, acc || k > 0);
                 }
             };
             const auto commit = [&](uint64_t* bar) {
                 if (elect()) tc_commit(bar);
             };
+            if constexpr (EXP) {
+                // one lane walks the loop
+                if (elect()) {
+                    const auto scores = [&](int i, int j) {
+#pragma unroll
+                        for (int c = 0; c < EX_QC; ++c) {
+                            const int p = 5 * j + c;
+                            if (i == 0) bar_wait(&S.abort, a.hdr, &S.kv_full[p % EX_NS], (p / EX_NS) & 1);
+                            uint32_t x = lq + (i * Q_TILE + c * CA_HALF >> 4), y = lk + (p % EX_NS * CA_HALF >> 4);
+                            asm volatile("" : "+r"(x), "+r"(y));
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_ss(TM_S + 128 * i, desc(hi_q, x + 2 * k), desc(hi_kv, y + 2 * k), IDESC_QK, c + k > 0);
+                            if (i == nq - 1) tc_commit(&S.kv_empty[p % EX_NS]);
+                        }
+                        tc_commit(&S.s_full[i]);
+                    };
+                    bar_wait(&S.abort, a.hdr, &S.q_full, 0);
+                    for (int i = 0; i < nq; ++i) scores(i, 0);
+                    for (int j = 0; j < nt; ++j) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if (i == nq) break;
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                const int p = 5 * j + 3 + half;
+                                // (V first: this lane waits for P some 700 cycles, so here it costs nothing)
+                                if (i == 0) bar_wait(&S.abort, a.hdr, &S.kv_full[p % EX_NS], (p / EX_NS) & 1);
+                                bar_wait(&S.abort, a.hdr, &S.p_full[i][half], j & 1);
+                                tc_after();
+                                uint32_t y = lv + (p % EX_NS * CA_HALF >> 4);
+                                asm volatile("" : "+r"(y));
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    mma_ts(TM_O + 128 * i, TM_S + 128 * i + 8 * (4 * half + k), desc(hi_kv, y + (k * 2048 >> 4)), IDESC_PV,
+                                           j > 0 || half + k > 0);
+                                if (i == nq - 1) tc_commit(&S.kv_empty[p % EX_NS]);
+                            }
+                            if (j + 1 < nt)
+                                scores(i, j + 1);
+                            else
+                                tc_commit(&S.o_full[i]);
+                        }
+                    }
+                }
+                __syncwarp();
+            } else {
             bar_wait(&S.abort, a.hdr, &S.q_full, 0);
             bar_wait(&S.abort, a.hdr, &S.kv_full[0], 0);
             tc_after();
@@ -412,10 +445,8 @@ __global__ void __launch_bounds__(CA_NT, 1)
             if (nq > 1) qk(1, 0);
             commit(&S.kv_empty[0]);
             for (int j = 0; j < nt; ++j) {
-                const int sv = EXP ? j : (2 * j + 1) % CA_NS, sk = EXP ? j + 1 : (2 * j + 2) % CA_NS;
+                const int sv = (2 * j + 1) % CA_NS, sk = (2 * j + 2) % CA_NS;
                 const bool more = j + 1 < nt;
-                uint64_t* const next_full = EXP ? &S.kv_full[(j + 1) & 1] : &S.kv_full[sk];
-                const uint32_t next_phase = EXP ? ((j + 1) >> 1) & 1 : ((2 * j + 2) / CA_NS) & 1;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     if (i == nq) break;
@@ -425,15 +456,16 @@ __global__ void __launch_bounds__(CA_NT, 1)
                     bar_wait(&S.abort, a.hdr, &S.p_full[i][1], j & 1);
                     tc_after();
                     pv(i, sv, 1, true);
-                    if (i == nq - 1) commit(EXP ? &S.kv_empty[2 + (j & 1)] : &S.kv_empty[sv]);
+                    if (i == nq - 1) commit(&S.kv_empty[sv]);
                     if (more) {
-                        if (i == 0) bar_wait(&S.abort, a.hdr, next_full, next_phase);
+                        if (i == 0) bar_wait(&S.abort, a.hdr, &S.kv_full[sk], ((2 * j + 2) / CA_NS) & 1);
                         qk(i, sk);
                     } else {
                         commit(&S.o_full[i]);
                     }
                 }
-                if (more) commit(EXP ? &S.kv_empty[(j + 1) & 1] : &S.kv_empty[sk]);
+                if (more) commit(&S.kv_empty[sk]);
+            }
             }
         }
     } else {
@@ -456,11 +488,12 @@ __global__ void __launch_bounds__(CA_NT, 1)
         if constexpr (TREE) pos = ctx + (valid ? tree.depth[tok0 + tok] : 0);
         // what the row sees of the w-th 32 columns of the tile at t0
         const auto seen_bits = [&](int t0, int w) {
-            uint32_t bits = columns(see.x - t0, see.y - t0, w) | columns(see.z - t0, see.w - t0, w);
-            if constexpr (TREE) {
-                if (valid) bits |= kvq_tree_bits(tree, tok0 + tok, t0 + 32 * w - ctx);
+            if constexpr (TREE) {   // (from shared memory: kept in registers over the loop, some of them spill)
+                if (!valid) return 0u;
+                const int4 e = seen_of[tok];
+                return columns(e.x - t0, e.y - t0, w) | columns(e.z - t0, e.w - t0, w) | kvq_tree_bits(tree, tok0 + tok, t0 + 32 * w - ctx);
             }
-            return bits;
+            return columns(see.x - t0, see.y - t0, w) | columns(see.z - t0, see.w - t0, w);
         };
         const float slope2 = BIAS && valid ? a.mod.slopes[h * GQ + r % GQ] * KVQ_LOG2E : 0.0f;
         float m = valid ? -INFINITY : INFINITY, l = 0.0f;   // (no row: weights 0, never a new anchor)
@@ -469,14 +502,20 @@ __global__ void __launch_bounds__(CA_NT, 1)
                 const int t0 = tile_of(it0 + j) * CA_KEYS;
                 // rows at and behind T may hold anything: 0 * NaN must not reach O
                 const bool tail = T < t0 + CA_KEYS && (EXP || (T & (PG - 1)) != 0) && T > t0;
-                uint64_t* const v_full = EXP ? &S.kv_full[2 + (j & 1)] : &S.kv_full[(2 * j + 1) % CA_NS];
-                const uint32_t v_phase = EXP ? (j >> 1) & 1 : ((2 * j + 1) / CA_NS) & 1;
+                const auto v_wait = [&] {
+                    if (EXP) {
+                        bar_wait(&S.abort, a.hdr, &S.kv_full[(5 * j + 3) % EX_NS], ((5 * j + 3) / EX_NS) & 1);
+                        bar_wait(&S.abort, a.hdr, &S.kv_full[(5 * j + 4) % EX_NS], ((5 * j + 4) / EX_NS) & 1);
+                    } else {
+                        bar_wait(&S.abort, a.hdr, &S.kv_full[(2 * j + 1) % CA_NS], ((2 * j + 1) / CA_NS) & 1);
+                    }
+                };
                 bar_wait(&S.abort, a.hdr, &S.s_full[i], j & 1);
                 // tile 0's weights stand for V's arrival too (its products are issued after these waits, and tile
                 // 1's after tile 0's): the issuing warp is the busier one.  1.38 -> 1.36 ms for the prompt
-                if (i == 0) bar_wait(&S.abort, a.hdr, v_full, v_phase);
+                if (!EXP && i == 0) v_wait();
                 if (tail) {
-                    bar_wait(&S.abort, a.hdr, v_full, v_phase);
+                    v_wait();
                     const uint32_t base = skv + (2 * j + 1) % CA_NS * CA_TILE;
                     const int r0 = T - t0, r1 = EXP ? CA_KEYS : (r0 + PG - 1) / PG * PG;
                     for (int x = tid & 127; x < (r1 - r0) * 16; x += 128) {
