@@ -121,23 +121,36 @@ __global__ void __launch_bounds__(AP_NT) rope_append_kernel(const __grid_constan
     }
 }
 
-// The scored state of an fp16 layer: the rows just written, from their pages into the channel-major copy, and the
-// channels' maxima.  One CTA per (64 positions of a sequence, kv head), one thread per channel.
-constexpr int SC_TOK = 64;
-__global__ void __launch_bounds__(D) append_scored_kernel(const __grid_constant__ AppendArgs a) {
-    __shared__ __align__(16) uint16_t tile[SC_TOK][D];
-    __shared__ int32_t who[4];   // sequence, first position of the tile, the new tokens' first and last + 1 in it
-    __shared__ int64_t at[SC_TOK / PG];
-    const int h = blockIdx.y, c = threadIdx.x, lane = c & 31;
+// The same into an fp16 layer with a channel-major copy of its keys and their channels' maxima.  A CTA takes the new
+// tokens of eight places of a sequence (0 .. 7 modulo 8), so that a channel's values are one 16-byte piece of the copy:
+// queries and values as above, then the keys, SC_HEADS heads at a time, which are written to their pages and, through
+// shared memory, to the copy.  (As a second launch over the rows just written: 32 us for 4097 tokens of 32 + 8 + 8 heads.)
+constexpr int SC_TOK = 8, SC_HEADS = 16;
+template <typename T, bool INTER>
+__global__ void __launch_bounds__(AP_NT) rope_append_scored_kernel(const __grid_constant__ AppendArgs a) {
+    __shared__ __align__(16) float2 cs[SC_TOK][D / 2];
+    __shared__ __align__(16) float wt[2][D];
+    __shared__ __align__(16) uint16_t keys[SC_HEADS][SC_TOK][D];
+    __shared__ int32_t who[4];          // sequence, its first new row here, that row's place, rows here
+    __shared__ int32_t pos[SC_TOK];
+    __shared__ int32_t page;
+    const int tid = threadIdx.x, l = tid & 7, grp = tid >> 3, lane = tid & 31;
+    int ca, cb;
+    chunks<INTER>(l, a.rot, &ca, &cb);
     kvq_pdl_begin();
-    if (c < 32) {
-        int base = 0;
+    if (tid < D) {
+        if (a.qw != nullptr) wt[0][tid] = a.qw[tid];
+        if (a.kw != nullptr) wt[1][tid] = a.kw[tid];
+    }
+    if (tid >= AP_NT - 32) {
         if (lane == 0) who[0] = -1;
+        __syncwarp();
+        int base = 0;
         for (int b0 = 0; b0 < a.rows.batch; b0 += 32) {
             const int b = b0 + lane;
-            int first, n = 0, T = 0;
-            if (b < a.rows.batch) kvq_new_rows_of(a.rows, b, &first, &n, &T);
-            const int lo = (T - n) / SC_TOK, tiles = n > 0 ? (T - 1) / SC_TOK + 1 - lo : 0;
+            int first = 0, n = 0, len = 0;
+            if (b < a.rows.batch) kvq_new_rows_of(a.rows, b, &first, &n, &len);
+            const int lo = (len - n) / SC_TOK, tiles = n > 0 ? (len - 1) / SC_TOK + 1 - lo : 0;
             int incl = tiles;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -146,54 +159,91 @@ __global__ void __launch_bounds__(D) append_scored_kernel(const __grid_constant_
             }
             const int mine = (int)blockIdx.x - (base + incl - tiles);
             if (mine >= 0 && mine < tiles) {
-                who[0] = b;
-                who[1] = (lo + mine) * SC_TOK;
-                who[2] = max(T - n, who[1]) - who[1];
-                who[3] = min(T, who[1] + SC_TOK) - who[1];
+                const int at = max(len - n, (lo + mine) * SC_TOK);
+                who[0] = b, who[1] = first + at - (len - n), who[2] = at, who[3] = min(len, (lo + mine + 1) * SC_TOK) - at;
+                page = kvq_page_at(a.rows, b, at / PG);
             }
             base += __shfl_sync(0xffffffffu, incl, 31);
         }
         __syncwarp();
-        if (who[0] >= 0 && lane < SC_TOK / PG) {
-            const int p0 = lane * PG;   // (pages without a new token are not looked up)
-            at[lane] = p0 < who[3] && p0 + PG > who[2] ? kvq_page_at(a.rows, who[0], who[1] / PG + lane) : -1;
-        }
+        if (who[0] >= 0 && lane < who[3]) pos[lane] = a.rows.pos != nullptr ? a.rows.pos[who[1] + lane] : who[2] + lane;
     }
     __syncthreads();
-    const int b = who[0], t0 = who[1], lo = who[2], hi = who[3];
+    const int b = who[0], r0 = who[1], place = who[2], nt = who[3];
     if (b < 0) return;
-    const uint16_t* k16 = static_cast<const uint16_t*>(a.k_pages);
-    for (int i = c; i < SC_TOK * (D / 8); i += D) {
-        const int t = i / (D / 8), x = i % (D / 8);
-        const int64_t page = at[t / PG];
-        if (t < lo || t >= hi || page < 0) continue;
-        *reinterpret_cast<uint4*>(&tile[t][8 * x]) =
-            *reinterpret_cast<const uint4*>(k16 + ((page * a.H + h) * PG + t % PG) * D + 8 * x);
+    for (int i = tid; i < nt * (D / 2); i += AP_NT) {
+        const int k = i / (D / 2), p = i % (D / 2);
+        if (p < a.rot >> 1) cs[k][pair_entry<INTER>(p)] = kvq_cos_sin(pos[k], a.steps[p], a.mscale);
     }
     __syncthreads();
-    uint16_t* dst = a.kT + (((int64_t)b * a.H + h) * D + c) * a.t_cap + t0;
-    float top = 0.0f;
-#pragma unroll
-    for (int t = 0; t < SC_TOK; t += 8) {
-        if (at[t / PG] < 0 || t + 8 <= lo || t >= hi) continue;
-        __align__(16) uint16_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = tile[t + i][c];
-        if (t >= lo && t + 8 <= hi) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(kvq_h2f(w[i])));
-            *reinterpret_cast<uint4*>(dst + t) = *reinterpret_cast<const uint4*>(w);
+    // (the rows here share a page)
+    const auto row_at = [&](int g, int k) { return (((int64_t)page * a.H + g) * PG + place % PG + k) * D; };
+    // queries and values
+    for (int i = grp; i < nt * (a.Hq + a.H); i += AP_NT / 8) {
+        const int k = i / (a.Hq + a.H), h = i - k * (a.Hq + a.H);
+        const bool is_q = h < a.Hq;
+        const T* src = is_q ? static_cast<const T*>(a.q) + (r0 + k) * a.q_stride + (int64_t)h * D
+                            : static_cast<const T*>(a.v) + (r0 + k) * a.v_stride + (int64_t)(h - a.Hq) * D;
+        float x[8], y[8];
+        unpack(*reinterpret_cast<const uint4*>(src + 8 * ca), x, (T*)nullptr);
+        unpack(*reinterpret_cast<const uint4*>(src + 8 * cb), y, (T*)nullptr);
+        uint16_t* dst;
+        if (is_q) {
+            if (a.qw != nullptr) norm_row(x, y, wt[0], ca, cb, a.eps);
+            turn_row<INTER>(x, y, cs[k], l, ca, cb, a.rot);
+            dst = a.qo + ((int64_t)(r0 + k) * a.Hq + h) * D;
         } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (t + i < lo || t + i >= hi) continue;
-                top = fmaxf(top, fabsf(kvq_h2f(w[i])));
-                dst[t + i] = w[i];
-            }
+            if (page < 0) continue;
+            dst = static_cast<uint16_t*>(a.v_pages) + row_at(h - a.Hq, k);
         }
+        *reinterpret_cast<uint4*>(dst + 8 * ca) = pack_half(x);
+        *reinterpret_cast<uint4*>(dst + 8 * cb) = pack_half(y);
     }
-    // (maxima are not negative, so their bits are ordered as integers; the order of arrival does not matter)
-    atomicMax(reinterpret_cast<int*>(a.k_absmax + ((int64_t)b * a.H + h) * D + c), __float_as_int(top));
+    if (page < 0) return;
+    // keys
+    for (int g0 = 0; g0 < a.H; g0 += SC_HEADS) {
+        const int ng = min(SC_HEADS, a.H - g0);
+        for (int i = grp; i < nt * ng; i += AP_NT / 8) {
+            const int k = i / ng, g = i - k * ng;
+            const T* src = static_cast<const T*>(a.k) + (r0 + k) * a.k_stride + (int64_t)(g0 + g) * D;
+            float x[8], y[8];
+            unpack(*reinterpret_cast<const uint4*>(src + 8 * ca), x, (T*)nullptr);
+            unpack(*reinterpret_cast<const uint4*>(src + 8 * cb), y, (T*)nullptr);
+            if (a.kw != nullptr) norm_row(x, y, wt[1], ca, cb, a.eps);
+            turn_row<INTER>(x, y, cs[k], l, ca, cb, a.rot);
+            const uint4 u = pack_half(x), v = pack_half(y);
+            uint16_t* dst = static_cast<uint16_t*>(a.k_pages) + row_at(g0 + g, k);
+            *reinterpret_cast<uint4*>(dst + 8 * ca) = u;
+            *reinterpret_cast<uint4*>(dst + 8 * cb) = v;
+            *reinterpret_cast<uint4*>(&keys[g][k][8 * ca]) = u;
+            *reinterpret_cast<uint4*>(&keys[g][k][8 * cb]) = v;
+        }
+        __syncthreads();
+        for (int i = tid; i < ng * D; i += AP_NT) {
+            const int g = i / D, c = i % D;
+            const int64_t ch = ((int64_t)b * a.H + g0 + g) * D + c;
+            const float so_far = a.k_absmax[ch];
+            __align__(16) uint16_t w[SC_TOK];
+            float top = 0.0f;
+#pragma unroll
+            for (int k = 0; k < SC_TOK; ++k) {
+                w[k] = k < nt ? keys[g][k][c] : (uint16_t)0;
+                top = fmaxf(top, fabsf(kvq_h2f(w[k])));
+            }
+            uint16_t* dst = a.kT + ch * a.t_cap + place;
+            if (nt == SC_TOK) {
+                *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(w);
+            } else {
+#pragma unroll
+                for (int k = 0; k < SC_TOK; ++k)
+                    if (k < nt) dst[k] = w[k];
+            }
+            // (maxima are not negative, so their bits are ordered as integers; the order of arrival does not matter, and a
+            // maximum only grows: most CTAs find theirs passed already)
+            if (top > so_far) atomicMax(reinterpret_cast<int*>(a.k_absmax + ch), __float_as_int(top));
+        }
+        __syncthreads();
+    }
 }
 
 // ---------------------------------------------------------------- latent rows
@@ -214,7 +264,7 @@ struct LatentArgs {
 // A token's work comes in warps: its latent row (16 values per lane), then its rotated rows of 64 values, the key's
 // and the query heads', eight rows per warp (four lanes per row, 16 values per lane).
 template <typename T, bool INTER>
-__global__ void __launch_bounds__(AP_NT) latent_append_kernel(const __grid_constant__ LatentArgs a, int tok_per_cta) {
+__global__ void __launch_bounds__(AP_NT, 5) latent_append_kernel(const __grid_constant__ LatentArgs a, int tok_per_cta) {
     __shared__ __align__(16) float2 cs[AP_TOK][ROT / 2];
     __shared__ int64_t at[AP_TOK];
     __shared__ int32_t pos[AP_TOK];
@@ -369,18 +419,25 @@ extern "C" int kv_rope_append(const kvq_layout* L, const kvq_pool* P, const kvq_
     a.eps = eps, a.mscale = mscale, a.steps = steps, a.rot = rope->rot_dim;
     a.Hq = q ? L->n_q_heads : 0, a.H = L->n_kv_heads;
     a.qo = q_out;
+    const auto launched = [&](cudaError_t e) {
+        return e == cudaSuccess ? (int)KVQ_OK : kvq_fail(KVQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+    };
+    if (a.kT != nullptr) {
+        // n new tokens of a sequence touch at most n / 8 + 2 groups of eight places
+        const int64_t tiles = n_rows / SC_TOK + 2 * (int64_t)S->batch;
+        KVQ_REQUIRE(tiles <= INT32_MAX, KVQ_ERR_UNSUPPORTED, "%s: batch", fn);
+        const auto go = [&](auto kernel) {
+            return launched(kvq_launch_pdl(kernel, dim3((unsigned)tiles), dim3(AP_NT), 0, kvq_stream(stream), a));
+        };
+        if (dtype == KVQ_F16)
+            return rope->interleaved ? go(rope_append_scored_kernel<__half, true>) : go(rope_append_scored_kernel<__half, false>);
+        return rope->interleaved ? go(rope_append_scored_kernel<__nv_bfloat16, true>)
+                                 : go(rope_append_scored_kernel<__nv_bfloat16, false>);
+    }
     const int tpc = rows_per_cta(n_rows);
     const unsigned grid = (unsigned)((n_rows + tpc - 1) / tpc);
     const auto go = [&](auto kernel) {
-        cudaError_t e = kvq_launch_pdl(kernel, dim3(grid), dim3(AP_NT), 0, kvq_stream(stream), a, tpc);
-        if (e == cudaSuccess && a.kT != nullptr) {
-            // n new tokens of a sequence touch at most n / 64 + 2 of its tiles
-            const int64_t tiles = n_rows / SC_TOK + 2 * (int64_t)S->batch;
-            KVQ_REQUIRE(tiles <= INT32_MAX && a.H <= 65535, KVQ_ERR_UNSUPPORTED, "%s: batch / heads", fn);
-            e = kvq_launch_pdl(append_scored_kernel, dim3((unsigned)tiles, a.H), dim3(D), 0, kvq_stream(stream), a);
-        }
-        if (e != cudaSuccess) return kvq_fail(KVQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
-        return (int)KVQ_OK;
+        return launched(kvq_launch_pdl(kernel, dim3(grid), dim3(AP_NT), 0, kvq_stream(stream), a, tpc));
     };
     const auto by_layout = [&](auto type) {
         using T = decltype(type);

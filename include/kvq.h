@@ -785,8 +785,8 @@ size_t kv_chunk_attn_ws(const kvq_layout* layout, const kvq_seqs* seqs, int64_t 
  * steps, mscale and eps as kv_qk_norm_rope (q with q_out may be NULL; fp32
  * arithmetic, one rounding from fp32 to the cache's type, E4M3 saturating at
  * +-448).  q_out: device fp16 [n_rows][H_q][d]; in place only for fp16 q without
- * gaps.  An fp16 layer with kT and k_absmax has them follow (a second launch over
- * the rows just written; k_absmax is raised, never lowered).  Pages of the new
+ * gaps.  An fp16 layer with kT and k_absmax has them follow (k_absmax is raised,
+ * never lowered).  Pages of the new
  * tokens must be allocated and not shared.  Rows behind row_starts[batch] and rows
  * of a sequence whose lengths do not fit (flagged) are left as they were, q_out
  * included; where a page id is none (flagged) the row's K and V are skipped.
