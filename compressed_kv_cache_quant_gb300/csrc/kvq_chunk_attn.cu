@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(CA_NT, 1)
     if constexpr (TREE) {
         if (tid < n) kvq_tree_fetch(tree, a.parents + first, tid, a.hdr);
         __syncthreads();
-        if (tid < n) kvq_tree_walk(tree, tid);
+        if (tid < n) kvq_tree_walk(tree, tid, ctx & 31);
         __syncthreads();   // (of the nodes' paths a row reads its own, of their depths all)
     }
     if (tid < ntok) {
@@ -208,12 +208,12 @@ __global__ void __launch_bounds__(CA_NT, 1)
             if (doc > ctx || a.mod.window > 0) {
                 for (int k = i, at = pos; k >= 0; k = tree.parent[k], --at) {
                     if (at < doc || (a.mod.window > 0 && at <= pos - a.mod.window && at - max(doc, 0) >= a.mod.n_sink))
-                        tree.path[i][k >> 5] &= ~(1u << (k & 31));
+                        tree.path[i][(k + (ctx & 31)) >> 5] &= ~(1u << ((k + ctx) & 31));
                 }
             }
             uint32_t any = 0;
 #pragma unroll
-            for (int w = 0; w < KVQ_TREE_WORDS; ++w) any |= tree.path[i][w];
+            for (int w = 0; w <= KVQ_TREE_WORDS; ++w) any |= tree.path[i][w];
             if (any) {
                 atomicMin(&S.lo_min, ctx);
                 atomicMax(&S.hi_max, T);
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(CA_NT, 1)
             if constexpr (TREE) {   // (from shared memory: kept in registers over the loop, some of them spill)
                 if (!valid) return 0u;
                 const int4 e = seen_of[tok];
-                return columns(e.x - t0, e.y - t0, w) | columns(e.z - t0, e.w - t0, w) | kvq_tree_bits(tree, tok0 + tok, t0 + 32 * w - ctx);
+                return columns(e.x - t0, e.y - t0, w) | columns(e.z - t0, e.w - t0, w) | kvq_tree_bits(tree, tok0 + tok, t0 + 32 * w, ctx);
             }
             return columns(see.x - t0, see.y - t0, w) | columns(see.z - t0, see.w - t0, w);
         };
@@ -860,8 +860,9 @@ struct ChunkPlan {
 // drafted tokens of eight 32K sequences: 64 CTAs in 2 parts, one wave, 173 us; in 7 parts, three full waves,
 // 182 us), the join's launch as 3, and the parts' rows are written, read and zeroed, 0.036 tiles' time per CTA
 // of 256 rows (200 new tokens of 1000: 32 CTAs whole 19.9 us, in 2 parts 22.6 us; 500 of 8000: 91 us, in 2
-// parts 62 us).
-ChunkPlan chunk_plan(int H, int GQ, int32_t batch, int32_t max_len, int64_t n_rows, int32_t max_new) {
+// parts 62 us).  `least`: tiles of a part; two for trees, which are few rows (25 nodes behind 4096 tokens, two kv heads:
+// in 7 parts of five tiles 24.7 us, in 16 20.4 us).
+ChunkPlan chunk_plan(int H, int GQ, int32_t batch, int32_t max_len, int64_t n_rows, int32_t max_new, int least = 4) {
     ChunkPlan p;
     const int tpc = CA_ROWS / GQ;
     const int64_t by_max = batch * (((int64_t)max_new + tpc - 1) / tpc);
@@ -870,7 +871,7 @@ ChunkPlan chunk_plan(int H, int GQ, int32_t batch, int32_t max_len, int64_t n_ro
     const int tiles = (max_len + CA_KEYS - 1) / CA_KEYS;
     p.n_splits = 1;
     if (ctas < sms) {
-        const int most = (int)std::min<int64_t>(std::max(1, tiles / 4), 4 * sms / ctas);
+        const int most = (int)std::min<int64_t>(std::max(1, tiles / least), 4 * sms / ctas);
         const double full = std::min(1.0, (double)max_new * GQ / CA_ROWS);   // how much of a CTA's rows is used
         double best = 0.0;
         for (int s = 1; s <= most; ++s) {
@@ -887,8 +888,8 @@ ChunkPlan chunk_plan(int H, int GQ, int32_t batch, int32_t max_len, int64_t n_ro
     return p;
 }
 
-ChunkPlan chunk_plan(const kvq_layout* L, const kvq_seqs* S, int64_t n_rows, int32_t max_new) {
-    return chunk_plan(L->n_kv_heads, L->n_q_heads / L->n_kv_heads, S->batch, S->max_len, n_rows, max_new);
+ChunkPlan chunk_plan(const kvq_layout* L, const kvq_seqs* S, int64_t n_rows, int32_t max_new, bool tree) {
+    return chunk_plan(L->n_kv_heads, L->n_q_heads / L->n_kv_heads, S->batch, S->max_len, n_rows, max_new, tree ? 2 : 4);
 }
 
 // Fills in what follows from the plan and launches the kernel and, over parts of the cache, their join.
@@ -920,7 +921,7 @@ extern "C" size_t kv_chunk_attn_ws(const kvq_layout* L, const kvq_seqs* S, int64
     if (kvq_check_layout(L, "kv_chunk_attn_ws", true) || kvq_check_seqs_sizes(S, "kv_chunk_attn_ws") ||
         kvq_check_max_len(S, "kv_chunk_attn_ws") || check_rows(n_rows, max_new, "kv_chunk_attn_ws"))
         return 0;
-    return chunk_plan(L, S, n_rows, max_new).bytes;
+    return chunk_plan(L, S, n_rows, max_new, false).bytes;
 }
 
 // kv_chunk_attn, or with `tree` kv_tree_attn.
@@ -944,7 +945,7 @@ static int chunk_attn(const char* fn, bool tree, const kvq_layout* L, const kvq_
     st = kvq_mod_args(mod, fn, &a.mod);
     if (st) return st;
     KVQ_REQUIRE(!tree || a.mod.prefix_len == nullptr, KVQ_ERR_UNSUPPORTED, "%s: prefix_len (trees have no prefix)", fn);
-    const ChunkPlan p = chunk_plan(L, S, n_rows, max_new);
+    const ChunkPlan p = chunk_plan(L, S, n_rows, max_new, tree);
     st = kvq_check_ws(ws, ws_bytes, p.bytes, fn);
     if (st) return st;
     if (S->batch == 0 || n_rows == 0) return KVQ_OK;
@@ -993,7 +994,7 @@ extern "C" size_t kv_tree_attn_ws(const kvq_layout* L, const kvq_seqs* S, int64_
     if (kvq_check_layout(L, "kv_tree_attn_ws", true) || kvq_check_seqs_sizes(S, "kv_tree_attn_ws") ||
         kvq_check_max_len(S, "kv_tree_attn_ws") || check_tree_rows(n_rows, max_new, "kv_tree_attn_ws"))
         return 0;
-    return chunk_plan(L, S, n_rows, max_new).bytes;
+    return chunk_plan(L, S, n_rows, max_new, true).bytes;
 }
 
 extern "C" int kv_tree_attn(const kvq_layout* L, const kvq_pool* P, const kvq_seqs* S, const uint16_t* q,

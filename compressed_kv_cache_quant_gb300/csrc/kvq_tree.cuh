@@ -8,8 +8,10 @@ constexpr int KVQ_TREE_WORDS = KVQ_TREE_MAX / 32;
 
 struct KvqTree {
     int16_t parent[KVQ_TREE_MAX];
-    int16_t depth[KVQ_TREE_MAX];                    // nodes above it
-    uint32_t path[KVQ_TREE_MAX][KVQ_TREE_WORDS];    // bit k: it is node k or hangs below it (and sees it)
+    int16_t depth[KVQ_TREE_MAX];                        // nodes above it
+    // bit `shift` + k: it is node k or hangs below it (and sees it); shift: the nodes' first place modulo 32, so that a
+    // word is 32 columns of the cache
+    uint32_t path[KVQ_TREE_MAX][KVQ_TREE_WORDS + 1];
 };
 
 // One thread per node: fetches its parent (a flagged -1 where the entry is no earlier node).  A barrier follows.
@@ -20,21 +22,19 @@ __device__ __forceinline__ void kvq_tree_fetch(KvqTree& t, const int32_t* parent
 }
 
 // One thread per node: its depth and path.  A path goes down in the nodes' order, so the walk ends.
-__device__ __forceinline__ void kvq_tree_walk(KvqTree& t, int i) {
+__device__ __forceinline__ void kvq_tree_walk(KvqTree& t, int i, int shift) {
 #pragma unroll
-    for (int w = 0; w < KVQ_TREE_WORDS; ++w) t.path[i][w] = 0;
+    for (int w = 0; w <= KVQ_TREE_WORDS; ++w) t.path[i][w] = 0;
     int above = -1;
     for (int k = i; k >= 0; k = t.parent[k]) {
-        t.path[i][k >> 5] |= 1u << (k & 31);
+        t.path[i][(k + shift) >> 5] |= 1u << ((k + shift) & 31);
         ++above;
     }
     t.depth[i] = (int16_t)above;
 }
 
-// 32 bits of node i's path from node `from` on (which may lie outside the tree).
-__device__ __forceinline__ uint32_t kvq_tree_bits(const KvqTree& t, int i, int from) {
-    const int w = from >> 5;   // (floor)
-    const uint32_t lo = w >= 0 && w < KVQ_TREE_WORDS ? t.path[i][w] : 0u;
-    const uint32_t hi = w + 1 >= 0 && w + 1 < KVQ_TREE_WORDS ? t.path[i][w + 1] : 0u;
-    return __funnelshift_r(lo, hi, from & 31);
+// What node i sees of the 32 columns from `column` on, a multiple of 32; ctx: the nodes' first place.
+__device__ __forceinline__ uint32_t kvq_tree_bits(const KvqTree& t, int i, int column, int ctx) {
+    const uint32_t w = (uint32_t)((column >> 5) - (ctx >> 5));
+    return w <= (uint32_t)KVQ_TREE_WORDS ? t.path[i][w] : 0u;
 }

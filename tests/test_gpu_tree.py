@@ -120,12 +120,12 @@ def test_long_split_contexts(mod):
 
 
 def test_chain_is_kv_chunk_attn():
-    """A chain is the causal run: the same bits."""
+    """A chain is the causal run: the same bits, where both take the cache whole."""
     require_gpu()
-    batch, _ = paged_batch([1000], kvq.Allocator(70, seed=2))
+    batch, _ = paged_batch([250], kvq.Allocator(70, seed=2))
     cache = kvq.LayerCache(8, 2, 16, 70, 1)
-    kv = synth.kv_rows(1000, 2, 77)
-    kvq.kv_quant_pack(cache, batch, 0, 0, 1000, kv[0].cuda(), kv[1].cuda())
+    kv = synth.kv_rows(250, 2, 77)
+    kvq.kv_quant_pack(cache, batch, 0, 0, 250, kv[0].cuda(), kv[1].cuda())
     q = rnd((50, 8, D), 8).cuda()
     starts = torch.tensor([0, 50], dtype=torch.int32, device="cuda")
     a, b = torch.empty_like(q), torch.empty_like(q)
