@@ -260,12 +260,7 @@ __global__ void __launch_bounds__(LA_NT, 1)
     if (tid == 64) map_prefetch(&map_q), map_prefetch(&map_rows);
     const uint32_t sq = (saddr(raw) + 1023) & ~1023u, skv = sq + a.nr * ROW * 2, sp = skv + a.ns * STAGE,
                    p_bytes = a.nr * 128;   // (a row of weights takes 128 bytes, as the swizzle wants it)
-    kvq_pdl_begin();
-    if (warp == 0) {
-        int per;
-        const Segment<KEYS> g = first_segment<KEYS>(a, blockIdx.x, gridDim.x, &per);
-        if (lane == 0) S.seg = g, S.per = per, S.abort = 0;
-    }
+    // (what does not read global memory goes before the wait for the launch before)
     if (tid == 32) {
         bar_init(&S.q_full, 1);
         bar_init(&S.q_free, 1);
@@ -285,6 +280,12 @@ __global__ void __launch_bounds__(LA_NT, 1)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&S.tmem)), "r"(TM_COLS)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    kvq_pdl_begin();
+    if (warp == 0) {
+        int per;
+        const Segment<KEYS> g = first_segment<KEYS>(a, blockIdx.x, gridDim.x, &per);
+        if (lane == 0) S.seg = g, S.per = per, S.abort = 0;
     }
     tc_before();
     __syncthreads();
@@ -620,12 +621,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LB_NT, 1)
     if (tid == 64) map_prefetch(&map_q), map_prefetch(&map_k), map_prefetch(&map_v);
     const int pair = blockIdx.x >> 1;
     const uint32_t sq = (saddr(raw) + 1023) & ~1023u, sk = sq + LB_Q, sv = sk + LB_NS * LB_K, sp = sv + LB_NS * LB_V;
-    kvq_pdl_begin();
-    if (warp == 0) {
-        int per;
-        const Segment<LB_KEYS> g = first_segment<LB_KEYS>(a, pair, gridDim.x >> 1, &per);
-        if (lane == 0) S.seg = g, S.per = per, S.abort = 0;
-    }
+    // (what does not read global memory goes before the wait for the launch before)
     if (tid == 32) {
         bar_init(&S.q_full, 1);
         bar_init(&S.q_free, 1);
@@ -650,6 +646,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LB_NT, 1)
     __syncthreads();
     cluster_sync();   // (both CTAs' barriers and TMEM are there)
     tc_after();
+    kvq_pdl_begin();
+    if (warp == 0) {
+        int per;
+        const Segment<LB_KEYS> g = first_segment<LB_KEYS>(a, pair, gridDim.x >> 1, &per);
+        if (lane == 0) S.seg = g, S.per = per, S.abort = 0;
+    }
+    __syncthreads();
     const uint32_t tmem = S.tmem;
     Segment<LB_KEYS> g = S.seg;
 
