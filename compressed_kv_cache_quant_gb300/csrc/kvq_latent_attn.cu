@@ -36,11 +36,13 @@ namespace {
 constexpr int PG = KVQ_BLOCK_TOKENS;
 constexpr int LAT = KVQ_LATENT_DIM, ROT = KVQ_LATENT_ROPE, ROW = LAT + ROT;
 constexpr int LA_NT = 192;
-constexpr int LA_ROWS = 64;               // query rows per CTA
+constexpr int LA_ROWS = 32;               // query rows per CTA, at most
+constexpr int LA_KEYS = 48;               // tokens per step
 constexpr int LA_FAR = 2;                 // steps that pages are brought into L2 ahead of their load
 constexpr int LA_MAX_NS = 8;              // most stages
 constexpr int LA_CHUNKS = ROW / 64;
 constexpr int LA_GROUP = LA_CHUNKS * 1024;              // bytes of eight staged rows
+constexpr int LA_STAGE = LA_KEYS / 8 * LA_GROUP;
 constexpr int LA_SMEM = 232448 - 1024;    // dynamic shared memory of a CTA, at most (static: under 1 KB)
 constexpr float LA_HEAD = 7.0f;           // log2 of a row's largest weight when its anchor is set
 constexpr float LA_TOP = 15.99f;          // log2 of the largest weight before the anchor is set anew
@@ -49,7 +51,7 @@ constexpr uint32_t TM_O = 0, TM_S = 256, TM_COLS = 512;   // TMEM columns: four 
 struct LatArgs {
     const int32_t *bt, *seq_lens, *q_starts, *parents;
     int64_t n_rows, num_blocks;
-    int32_t batch, max_blocks, max_len, max_new, H;
+    int32_t batch, max_blocks, max_len, max_new, H, items;   // items: row groups, at most
     int32_t nr, ns;                                       // rows per CTA as the products see them, a multiple of 16; stages
     float scale2;                                         // of a score, in log2 units
     uint16_t* out;
@@ -174,14 +176,13 @@ struct Place {
     }
 };
 
-template <int KEYS, int AHEAD>
 struct Shared {
-    uint64_t q_full, q_free, kv_full[LA_MAX_NS], kv_empty[LA_MAX_NS], s_full[AHEAD + 1], p_full[AHEAD + 1], pv_done[AHEAD + 1], drain;
+    uint64_t q_full, q_free, kv_full[LA_MAX_NS], kv_empty[LA_MAX_NS], s_full[2], p_full[2], pv_done[2], drain;
     uint32_t tmem;
     int32_t abort;
-    Segment<KEYS> seg;
+    Segment<LA_KEYS> seg;
     int32_t per;       // steps per CTA
-    float factor[LA_ROWS];
+    float factor[64];  // (of 64 rows: M of the first product)
 };
 
 __device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
@@ -197,30 +198,18 @@ __device__ __forceinline__ bool sm_any(bool x) {
     return r != 0;
 }
 
-// 16 lanes by KEYS columns: of column group k (8 columns), v[4k] and v[4k + 1] are row lane / 4, columns 2 (lane % 4) and
+// 16 lanes by 48 columns: of column group k (8 columns), v[4k] and v[4k + 1] are row lane / 4, columns 2 (lane % 4) and
 // the one behind it, v[4k + 2] and v[4k + 3] the same of row lane / 4 + 8
-template <int KEYS>
 __device__ __forceinline__ void tm_ld_frag(uint32_t addr, float* v) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%24];\n"
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%16,%17,%18,%19,%20,%21,%22,%23}, [%25];\n"
+        "tcgen05.wait::ld.sync.aligned;"
         : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
-        : "r"(addr)
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]),
+          "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23])
+        : "r"(addr), "r"(addr + 32)
         : "memory");
-    if (KEYS == 48)
-        asm volatile(
-            "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-            : "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23])
-            : "r"(addr + 32)
-            : "memory");
-    // (the wait names the registers, so that nothing reads them before it)
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
-                   "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
-                 :
-                 : "memory");
-    if (KEYS == 48)
-        asm volatile("" : "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23])::"memory");
 }
 
 // A row's path to its root, 32 nodes per word, walked through the parents.
@@ -246,19 +235,17 @@ __device__ __forceinline__ uint32_t path_bits(const uint32_t* path, int from) {
     return __funnelshift_r(lo, hi, from & 31);
 }
 
-template <int KEYS, int AHEAD>
 __global__ void __launch_bounds__(LA_NT, 1)
     latent_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_rows,
                        const __grid_constant__ LatArgs a) {
-    static_assert(KEYS == 32 || KEYS == 48, "columns of the fragment loads");
-    constexpr int STAGE = KEYS / 8 * LA_GROUP, NP = AHEAD + 1, NG = KEYS / 8;
+    constexpr int NG = LA_KEYS / 8;
     extern __shared__ unsigned char raw[];
-    __shared__ Shared<KEYS, AHEAD> S;
+    __shared__ Shared S;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // queries, stages, weights: with nr below 64 the first product reads behind the queries, into the stages, for
     // rows of S that nothing looks at
     if (tid == 64) map_prefetch(&map_q), map_prefetch(&map_rows);
-    const uint32_t sq = (saddr(raw) + 1023) & ~1023u, skv = sq + a.nr * ROW * 2, sp = skv + a.ns * STAGE,
+    const uint32_t sq = (saddr(raw) + 1023) & ~1023u, skv = sq + a.nr * ROW * 2, sp = skv + a.ns * LA_STAGE,
                    p_bytes = a.nr * 128;   // (a row of weights takes 128 bytes, as the swizzle wants it)
     // (what does not read global memory goes before the wait for the launch before)
     if (tid == 32) {
@@ -268,7 +255,7 @@ __global__ void __launch_bounds__(LA_NT, 1)
             bar_init(&S.kv_full[i], 1);
             bar_init(&S.kv_empty[i], 1);
         }
-        for (int i = 0; i < NP; ++i) {
+        for (int i = 0; i < 2; ++i) {
             bar_init(&S.s_full[i], 1);
             bar_init(&S.p_full[i], 4);
             bar_init(&S.pv_done[i], 1);
@@ -284,14 +271,14 @@ __global__ void __launch_bounds__(LA_NT, 1)
     kvq_pdl_begin();
     if (warp == 0) {
         int per;
-        const Segment<KEYS> g = first_segment<KEYS>(a, blockIdx.x, gridDim.x, &per);
+        const Segment<LA_KEYS> g = first_segment<LA_KEYS>(a, blockIdx.x, gridDim.x, &per);
         if (lane == 0) S.seg = g, S.per = per, S.abort = 0;
     }
     tc_before();
     __syncthreads();
     tc_after();
     const uint32_t tmem = S.tmem;
-    Segment<KEYS> g = S.seg;
+    Segment<LA_KEYS> g = S.seg;
 
     if (g.b < 0) {
         // no work
@@ -302,10 +289,10 @@ __global__ void __launch_bounds__(LA_NT, 1)
         int loaded = 0;    // steps so far
         bool ok = true;
         for (int seg = 0; ok;) {
-            // lanes 0 .. KEYS / 16 - 1 look up one page each, a step ahead
+            // lanes 0 .. LA_KEYS / 16 - 1 look up one page each, a step ahead
             const auto group_of = [&](int j) {
-                const int lp = (g.step + j) * (KEYS / PG) + lane;
-                if (j >= g.nt || lane >= KEYS / PG || lp * PG >= g.end) return nowhere;
+                const int lp = (g.step + j) * (LA_KEYS / PG) + lane;
+                if (j >= g.nt || lane >= LA_KEYS / PG || lp * PG >= g.end) return nowhere;
                 const int32_t page = a.bt[(int64_t)g.b * a.max_blocks + lp];
                 if (page >= 0 && page < a.num_blocks) return page * (PG / 8);
                 kvq_dev_flag(a.hdr, KVQ_DEV_BAD_PAGE, page);
@@ -325,17 +312,17 @@ __global__ void __launch_bounds__(LA_NT, 1)
                 ++seg;
             }
             for (int j = 0; j < g.nt && ok; ++j, ++loaded) {
-                const int pages = min(KEYS / PG, (g.end - (g.step + j) * KEYS + PG - 1) / PG);
-                int to[KEYS / PG];
+                const int pages = min(LA_KEYS / PG, (g.end - (g.step + j) * LA_KEYS + PG - 1) / PG);
+                int to[LA_KEYS / PG];
 #pragma unroll
-                for (int k = 0; k < KEYS / PG; ++k) to[k] = __shfl_sync(0xffffffffu, y, k);
+                for (int k = 0; k < LA_KEYS / PG; ++k) to[k] = __shfl_sync(0xffffffffu, y, k);
                 if (loaded >= a.ns) bar_wait(&S.abort, a.hdr, &S.kv_empty[st.i], st.round ^ 1);
                 ok = !aborted(&S.abort);
                 if (ok && elect()) {
                     bar_expect(&S.kv_full[st.i], pages * PG * ROW * 2);
 #pragma unroll
-                    for (int k = 0; k < KEYS / PG; ++k)
-                        if (k < pages) tma_page(skv + st.i * STAGE + k * (PG * ROW * 2), &map_rows, to[k], &S.kv_full[st.i]);
+                    for (int k = 0; k < LA_KEYS / PG; ++k)
+                        if (k < pages) tma_page(skv + st.i * LA_STAGE + k * (PG * ROW * 2), &map_rows, to[k], &S.kv_full[st.i]);
                 }
                 __syncwarp();
                 if (ahead[LA_FAR - 1] != nowhere) tma_page_prefetch(&map_rows, ahead[LA_FAR - 1]);
@@ -353,7 +340,7 @@ __global__ void __launch_bounds__(LA_NT, 1)
         const uint32_t hi_q = (uint32_t)(smem_desc(0, 16, 1024) >> 32), hi_kv = (uint32_t)(smem_desc(0, 16, LA_GROUP) >> 32);
         const uint32_t lq = (uint32_t)smem_desc(sq, 16, 0), lk = (uint32_t)smem_desc(skv, 16, 0),
                        lv = (uint32_t)smem_desc(skv, 1024, 0), lp = (uint32_t)smem_desc(sp, 16, 0);
-        const uint32_t idesc_s = idesc_f16(64, KEYS), idesc_o = idesc_f16(128, a.nr) | KVQ_A_MN;
+        const uint32_t idesc_s = idesc_f16(64, LA_KEYS), idesc_o = idesc_f16(128, a.nr) | KVQ_A_MN;
         const auto desc = [](uint32_t hi, uint32_t lo) { return (uint64_t)hi << 32 | lo; };
         const uint32_t q_chunk = (uint32_t)a.nr * 128 >> 4;
         Place in, s, out, p;   // stage and S of the next first product, stage and P of the next second one
@@ -361,50 +348,50 @@ __global__ void __launch_bounds__(LA_NT, 1)
             bar_wait(&S.abort, a.hdr, &S.kv_full[in.i], in.round);
             tc_after();
             {
-                uint32_t x = lq, y = lk + (in.i * STAGE >> 4);
+                uint32_t x = lq, y = lk + (in.i * LA_STAGE >> 4);
                 asm volatile("" : "+r"(x), "+r"(y));
 #pragma unroll
                 for (int c = 0; c < LA_CHUNKS; ++c) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_ss(TM_S + s.i * KEYS, desc(hi_q, x + 2 * k), desc(hi_kv, y + (c * 1024 >> 4) + 2 * k), idesc_s, c + k > 0);
+                        mma_ss(TM_S + s.i * LA_KEYS, desc(hi_q, x + 2 * k), desc(hi_kv, y + (c * 1024 >> 4) + 2 * k), idesc_s, c + k > 0);
                     x += q_chunk;
                 }
-                // (all products so far: where S is there, so is O^T of AHEAD + 1 steps before, and P's place is free)
+                // (all products so far: where S is there, so is O^T of two steps before, and P's place is free)
                 tc_commit(&S.s_full[s.i]);
             }
             in.next(a.ns);
-            s.next(NP);
+            s.next(2);
         };
         for (int seg = 0;;) {
             const int nt = g.nt;
             if (nt > 0) {
                 bar_wait(&S.abort, a.hdr, &S.q_full, seg & 1);
                 ++seg;
-                for (int j = 0; j < min(AHEAD, nt); ++j) qk();
-                if (nt <= AHEAD) tc_commit(&S.q_free);
+                qk();
+                if (nt == 1) tc_commit(&S.q_free);
             }
             for (int j = 0; j < nt; ++j) {
-                if (j + AHEAD < nt) {
+                if (j + 1 < nt) {
                     qk();
-                    if (j + AHEAD == nt - 1) tc_commit(&S.q_free);
+                    if (j + 2 == nt) tc_commit(&S.q_free);
                 }
                 bar_wait(&S.abort, a.hdr, &S.p_full[p.i], p.round);
                 tc_after();
                 {
-                    uint32_t y = lv + (out.i * STAGE >> 4), z = lp + (p.i * p_bytes >> 4);
+                    uint32_t y = lv + (out.i * LA_STAGE >> 4), z = lp + (p.i * p_bytes >> 4);
                     asm volatile("" : "+r"(y), "+r"(z));
 #pragma unroll
                     for (int d = 0; d < LAT / 128; ++d)
 #pragma unroll
-                        for (int k = 0; k < KEYS / 16; ++k)
+                        for (int k = 0; k < LA_KEYS / 16; ++k)
                             mma_ss(TM_O + 64 * d, desc(hi_kv, y + ((k * 2 * LA_GROUP + d * 2048) >> 4)), desc(hi_q, z + 2 * k), idesc_o,
                                    j > 0 || k > 0);
                     tc_commit(&S.kv_empty[out.i]);
                     tc_commit(&S.pv_done[p.i]);
                 }
                 out.next(a.ns);
-                p.next(NP);
+                p.next(2);
             }
             if (!g.next(a)) break;
         }
@@ -414,8 +401,8 @@ __global__ void __launch_bounds__(LA_NT, 1)
         const uint32_t lane_base = tmem + ((uint32_t)warp << 21);   // TMEM lanes 32 warp ..
         const int ra = 16 * warp + (lane >> 2), c0 = 2 * (lane & 3);
         const bool tree = a.parents != nullptr;
-        // `done`: the step before.  Where S of a step is there, O^T of AHEAD + 1 steps before is, so that of the step before
-        // is at most one phase of its barrier away
+        // `done`: the step before.  Where S of a step is there, O^T of two steps before is, so that of the step before is
+        // at most one phase of its barrier away
         Place st, s_at, done;
         do {
             const int nt = g.nt, end = g.end, ctx = g.s.T - g.s.n;
@@ -434,15 +421,15 @@ __global__ void __launch_bounds__(LA_NT, 1)
                 if (tree && valid[i]) walk_path(a, g.s.first, tok, path[i]);
             }
             const int full = __reduce_min_sync(0xffffffffu, min(cut[0], cut[1]));
-            for (int j = 0; j < nt; ++j, done = s_at, st.next(a.ns), s_at.next(NP)) {
-                const int t0 = (g.step + j) * KEYS;
+            for (int j = 0; j < nt; ++j, done = s_at, st.next(a.ns), s_at.next(2)) {
+                const int t0 = (g.step + j) * LA_KEYS;
                 bar_wait(&S.abort, a.hdr, &S.s_full[s_at.i], s_at.round);
                 tc_after();
-                if (end < t0 + KEYS) {
+                if (end < t0 + LA_KEYS) {
                     // rows at and behind the end may hold anything: 0 * NaN must not reach O^T
-                    const uint32_t base = skv + st.i * STAGE;
+                    const uint32_t base = skv + st.i * LA_STAGE;
                     const int r0 = end - t0;
-                    for (int x = tid; x < (KEYS - r0) * (LAT / 8); x += 128) {
+                    for (int x = tid; x < (LA_KEYS - r0) * (LAT / 8); x += 128) {
                         const int row = r0 + x / (LAT / 8), c = x % (LAT / 8);
                         const uint32_t to = base + (row >> 3) * LA_GROUP + (c >> 3) * 1024 + (row & 7) * 128 + (c & 7) * 16;
                         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
@@ -452,10 +439,10 @@ __global__ void __launch_bounds__(LA_NT, 1)
                 float top[2] = {-INFINITY, -INFINITY};
                 bool far = false;
                 if (active) {
-                    tm_ld_frag<KEYS>(lane_base + TM_S + s_at.i * KEYS, s);
+                    tm_ld_frag(lane_base + TM_S + s_at.i * LA_KEYS, s);
 #pragma unroll
                     for (int c = 0; c < 4 * NG; ++c) s[c] = __fmul_rn(s[c], a.scale2);
-                    if (t0 + KEYS > full) {   // (full: what every row of the warp sees all of)
+                    if (t0 + LA_KEYS > full) {   // (full: what every row of the warp sees all of)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             uint64_t bits = (uint64_t)below(cut[i] - t0 - 32) << 32 | below(cut[i] - t0);
@@ -545,7 +532,7 @@ __global__ void __launch_bounds__(LA_NT, 1)
                     if (a.lse != nullptr) a.lse[out_row + r] = sum == 0.0f ? -INFINITY : (m[i] + log2f(sum)) * KVQ_LN2;
                 } else {
                     a.ml[slot * a.nr + r] = make_float2(m[i], sum);
-                    if (last) {
+                    if (last && g.item < a.items) {   // (more only where q_starts is not ascending)
                         const int c0 = (g.at - g.step) / S.per;
                         a.cuts[(int64_t)g.item * a.nr + r] = make_int4(c0 + 1, (int)blockIdx.x - c0 + 1, out_row + r, 0);
                     }
@@ -604,7 +591,7 @@ constexpr int LB_Q = 64 * ROW * 2, LB_P = 64 * 128;
 constexpr int LB_SMEM = 1024 + LB_Q + LB_NS * (LB_K + LB_V) + 2 * LB_P;
 
 struct SharedPair {
-    uint64_t q_full, q_free, k_full[LB_NS], k_empty[LB_NS], v_full[LB_NS], v_empty[LB_NS], s_full[2], p_full[2], pv_done[2], drain;
+    uint64_t q_full, q_free, k_full[LB_NS], k_empty[LB_NS], v_full[LB_NS], v_empty[LB_NS], s_full[2], p_full[2], pv_done[2];
     uint32_t tmem;
     int32_t abort, per;
     Segment<LB_KEYS> seg;
@@ -634,7 +621,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LB_NT, 1)
             bar_init(&S.p_full[i], 8);
             bar_init(&S.pv_done[i], 1);
         }
-        bar_init(&S.drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 4) {
@@ -916,7 +902,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LB_NT, 1)
                     if (a.lse != nullptr) a.lse[out_row + r] = l == 0.0f ? -INFINITY : (m + log2f(l)) * KVQ_LN2;
                 } else {
                     a.ml[slot * a.nr + in_group] = make_float2(m, l);
-                    if (last) {
+                    if (last && g.item < a.items) {
                         const int p0 = (g.at - g.step) / S.per;
                         a.cuts[(int64_t)g.item * a.nr + in_group] = make_int4(p0 + 1, pair - p0 + 1, out_row + r, 0);
                     }
@@ -1139,16 +1125,16 @@ int latent_pairs() {
 LatPlan latent_plan(const kvq_seqs* S, int32_t n_heads, int64_t n_rows, int32_t max_new) {
     LatPlan p;
     const int64_t most = (int64_t)max_new * n_heads;   // query rows of a sequence
-    p.pairs = most > 32;
+    p.pairs = most > LA_ROWS;
     p.nr = p.pairs ? 128 : std::max(16, (int)((most + 15) / 16 * 16));
     const int64_t by_max = S->batch * ((most + p.nr - 1) / p.nr);
     p.items = std::max<int64_t>(1, std::min(by_max, n_rows * n_heads / p.nr + S->batch));
-    p.keys = p.pairs ? LB_KEYS : 48;
+    p.keys = p.pairs ? LB_KEYS : LA_KEYS;
     p.steps = p.items * ((S->max_len + p.keys - 1) / p.keys);
     p.ctas = (int)std::max<int64_t>(1, std::min<int64_t>({p.steps, p.pairs ? latent_pairs() : kvq_num_sms(), KVQ_LATENT_MAX_CTAS}));
-    const size_t stage = p.keys / 8 * LA_GROUP, fixed = 1024 + (size_t)p.nr * (ROW * 2 + 2 * 128);
-    p.ns = p.pairs ? LB_NS : (int)std::min<size_t>((LA_SMEM - fixed) / stage, LA_MAX_NS);
-    p.smem = p.pairs ? LB_SMEM : fixed + p.ns * stage;
+    const size_t fixed = 1024 + (size_t)p.nr * (ROW * 2 + 2 * 128);
+    p.ns = p.pairs ? LB_NS : (int)std::min<size_t>((LA_SMEM - fixed) / LA_STAGE, LA_MAX_NS);
+    p.smem = p.pairs ? LB_SMEM : fixed + p.ns * LA_STAGE;
     const size_t rows = (size_t)2 * p.ctas * p.nr;
     p.off_ml = sizeof(KvqWsHeader);
     p.off_cuts = kvq_round_up(p.off_ml + rows * sizeof(float2), 256);
@@ -1180,7 +1166,7 @@ extern "C" int kv_latent_attn(const kvq_latent* C, const kvq_seqs* S, int32_t n_
     const LatPlan p = latent_plan(S, n_heads, n_rows, max_new);
     st = kvq_check_ws(ws, ws_bytes, p.bytes, fn);
     if (st) return st;
-    KVQ_REQUIRE(C->num_blocks * PG <= INT32_MAX && n_rows * n_heads <= INT32_MAX - LA_ROWS, KVQ_ERR_UNSUPPORTED,
+    KVQ_REQUIRE(C->num_blocks * PG <= INT32_MAX && n_rows * n_heads <= INT32_MAX - 128, KVQ_ERR_UNSUPPORTED,
                 "%s: more than 2^31 - 1 rows in the pool or queries", fn);
     KVQ_REQUIRE(p.items * p.nr <= INT32_MAX / 8 && p.steps <= INT32_MAX - KVQ_LATENT_MAX_CTAS, KVQ_ERR_UNSUPPORTED, "%s: more than 2^31 steps (queries times max_len)", fn);
     if (S->batch == 0 || n_rows == 0) return KVQ_OK;
@@ -1188,7 +1174,7 @@ extern "C" int kv_latent_attn(const kvq_latent* C, const kvq_seqs* S, int32_t n_
     KVQ_REQUIRE((((uintptr_t)q | (uintptr_t)out) & 15u) == 0, KVQ_ERR_INVALID_ARG, "%s: q and out must be 16-byte aligned", fn);
     CUtensorMap map_q, map_rows, map_v;
     const uint64_t qd[3] = {64, (uint64_t)n_rows * n_heads, LA_CHUNKS}, qs[2] = {ROW * 2, 128};
-    const uint32_t qb[3] = {64, (uint32_t)std::min(p.nr, LA_ROWS), LA_CHUNKS};
+    const uint32_t qb[3] = {64, (uint32_t)(p.pairs ? 64 : p.nr), LA_CHUNKS};
     const uint64_t rd[4] = {64, 8, LA_CHUNKS, (uint64_t)C->num_blocks * (PG / 8)}, rs[3] = {ROW * 2, 128, 8 * ROW * 2};
     const uint32_t rb[4] = {64, 8, LA_CHUNKS, PG / 8}, vb[4] = {64, 8, LAT / 128, PG / 8};
     st = make_map(&map_q, q, 3, qd, qs, qb, fn);
@@ -1197,30 +1183,22 @@ extern "C" int kv_latent_attn(const kvq_latent* C, const kvq_seqs* S, int32_t n_
     if (st) return st;
     a.bt = S->block_table, a.seq_lens = S->seq_lens, a.q_starts = q_starts, a.parents = parents;
     a.n_rows = n_rows, a.num_blocks = C->num_blocks;
-    a.batch = S->batch, a.max_blocks = S->max_blocks, a.max_len = S->max_len, a.max_new = max_new, a.H = n_heads, a.nr = p.nr, a.ns = p.ns;
+    a.batch = S->batch, a.max_blocks = S->max_blocks, a.max_len = S->max_len, a.max_new = max_new, a.H = n_heads, a.nr = p.nr, a.ns = p.ns, a.items = (int)p.items;
     a.out = out, a.lse = lse, a.hdr = static_cast<KvqWsHeader*>(ws);
     a.ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + p.off_ml);
     a.cuts = reinterpret_cast<int4*>(static_cast<char*>(ws) + p.off_cuts);
     a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.off_part);
-    const auto go = [&](auto kernel) {
-        const int rc = kvq_prepare_kernel((const void*)kernel, (int)p.smem);
-        if (rc) return rc;
-        const cudaError_t e = kvq_launch_pdl(kernel, dim3(p.ctas), dim3(LA_NT), p.smem, kvq_stream(stream), map_q, map_rows, a);
-        return e == cudaSuccess ? (int)KVQ_OK : kvq_fail(KVQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
-    };
-    if (p.pairs) {
-        st = kvq_prepare_kernel((const void*)latent_pair_kernel, LB_SMEM);
-        if (st) return st;
-        const cudaError_t e = kvq_launch_pdl(latent_pair_kernel, dim3(2 * p.ctas), dim3(LB_NT), LB_SMEM, kvq_stream(stream), map_q,
-                                             map_rows, map_v, a);
-        st = e == cudaSuccess ? (int)KVQ_OK : kvq_fail(KVQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
-    } else {
-        st = go(latent_attn_kernel<48, 1>);
-    }
-    if (st || p.ctas == 1) return st;
+    const void* const kernel = p.pairs ? (const void*)latent_pair_kernel : (const void*)latent_attn_kernel;
+    st = kvq_prepare_kernel(kernel, (int)p.smem);
+    if (st) return st;
+    cudaError_t e = p.pairs ? kvq_launch_pdl(latent_pair_kernel, dim3(2 * p.ctas), dim3(LB_NT), p.smem, kvq_stream(stream), map_q,
+                                             map_rows, map_v, a)
+                            : kvq_launch_pdl(latent_attn_kernel, dim3(p.ctas), dim3(LA_NT), p.smem, kvq_stream(stream), map_q,
+                                             map_rows, a);
+    if (e != cudaSuccess) return kvq_fail(KVQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+    if (p.ctas == 1) return KVQ_OK;
     const int64_t group_rows = p.items * p.nr;
-    const cudaError_t e =
-        group_rows <= 128 && p.ctas > 6
+    e = group_rows <= 128 && p.ctas > 6
             ? kvq_launch_pdl(latent_join_wide_kernel, dim3((unsigned)group_rows * LQ), dim3(LQ_W * LQ_GR), 0, kvq_stream(stream), a)
             : kvq_launch_pdl(latent_join_kernel, dim3((unsigned)((group_rows + LJ_NW - 1) / LJ_NW)), dim3(32 * LJ_NW), 0,
                              kvq_stream(stream), a, (int)group_rows);
