@@ -6,6 +6,11 @@
 // threads then compute the rows' cosines and sines once into shared memory, and every group of lanes takes whole
 // head rows in two 16-byte loads per lane, as kv_qk_norm_rope does.  Angles are 64-bit turns.  Every value is
 // rounded once, from fp32 to the cache's type.
+//
+// Measured (in a graph): two prompts of 16001 and 16384 tokens, bf16, normed, 32 + 8 + 8 heads into E4M3 pages 121 us,
+// 6.0 TB/s (89% of the copy rate); 16385 latent rows with the rotated part of 16 heads 24 us, 4.3 TB/s, where 3.4 waves of
+// CTAs each begin with the chain of lookups; one token of 16 sequences 3 us.  More loads per lane cost CTAs per SM and
+// more time (24 -> 34 us with four head rows on their way).
 #include <algorithm>
 #include <cmath>
 

@@ -1,4 +1,4 @@
-// The score forms shared by kv_decode_attn and kv_chunk_attn: host checks, kernel arguments and which
+// The score forms shared by kv_decode_attn, kv_chunk_attn and kv_tree_attn: host checks, kernel arguments and which
 // cached tokens a query row sees.
 #pragma once
 

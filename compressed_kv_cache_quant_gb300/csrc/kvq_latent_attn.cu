@@ -2,25 +2,36 @@
 // their first 512 values the values, of every head.
 //
 // Bound: the bytes of the rows for few query rows (1152 bytes and 2176 flops per query row and token), the tensor
-// cores from some 100 query rows per sequence on.  Query rows are (new token, head) pairs, side by side in memory; a
-// CTA takes up to 64 of one sequence and a range of its tokens in steps of 64, four pages, each fetched through the
-// block table by one TMA box: groups of eight rows, a group's nine chunks of 64 values behind one another, 128-byte
-// swizzle.  The same staged rows serve both products:
+// cores from some 100 query rows per sequence on.  Query rows are (new token, head) pairs, side by side in memory.  A
+// token's row is read from its page by a TMA box of 16 tokens: groups of eight rows, a group's nine chunks of 64 values
+// behind one another, 128-byte swizzle.
 //
-//   S   = Q K^T      64 rows x 64 tokens    A = Q, B = the rows along their 576 values
+// Up to 32 query rows per sequence (latent_attn_kernel), steps of 48 tokens; the same staged rows serve both products:
+//
+//   S   = Q K^T      64 rows (32 at most in use) x 48 tokens    A = Q, B = the rows along their 576 values
 //   O^T = V^T P^T    512 values x rows      A = the rows' first 512 values in four blocks of 128, B = P
 //
-// O transposed, because 64 rows of 512 values would fill all of TMEM (M = 64 uses half of its lanes) and leave no
-// place for S; as O^T they take 256 columns, and for few rows the second product shrinks with them.
+// O transposed, because rows of 512 values would fill TMEM (M = 64 uses half of its lanes) and leave no place for S; as
+// O^T they take a block's columns each, and the second product shrinks with the rows.  48 tokens, because three stages of
+// them fit, and a step's products (1730 cycles) take less than its bytes at the rate of HBM (2350); with 64 tokens in two
+// stages the loads' latency shows (32 sequences of 4096 to 32767 tokens, 16 heads: 169 us), with 32 in five the issuing
+// lane is the bound (124 us).
 //
-//   warps 0-3  softmax: warp w has rows 16w .. 16w + 15, a lane per row (M = 64 puts them there); then the output
+//   warps 0-3  softmax: warp w has rows 16w .. 16w + 15 (M = 64 puts them into 16 lanes per warp), read as fragments
+//              of 16 rows by 8 columns, two rows per thread; then the output
 //   warp 4     issues tcgen05.mma: S of the next step before O^T of this one
-//   warp 5     loads
+//   warp 5     loads, and brings the pages of two steps later into L2
 //
-// The steps of all sequences and row groups are one list, cut into equal ranges, one per SM: a CTA works through its
-// range segment by segment, and a second launch joins the row groups that a cut runs through.  Weights are taken
-// against an anchor per row as in kv_chunk_attn: 2^7 below the row's maximum when it is set, set anew (O^T's column
-// rescaled) when a weight would pass 2^15.99.
+// More query rows: pairs of CTAs, further below.
+//
+// The steps of all sequences and row groups are one list, cut into equal ranges, one per SM (or pair): a CTA works
+// through its range segment by segment, and a second launch joins the row groups that a cut runs through.  Weights are
+// taken against an anchor per row as in kv_chunk_attn: 2^7 below the row's maximum when it is set, set anew (O rescaled)
+// when a weight would pass 2^15.99; their exponents are differences of rounded products, so that far scores stay exact
+// enough.
+//
+// Measured (in a graph): that batch 118 us, 5.8 TB/s (6.2 in this launch, 7 us of join); 131072 tokens of one sequence
+// 43 us; one of 1025 tokens 11 us.
 #include <algorithm>
 #include <cmath>
 #include <mutex>
@@ -46,7 +57,7 @@ constexpr int LA_STAGE = LA_KEYS / 8 * LA_GROUP;
 constexpr int LA_SMEM = 232448 - 1024;    // dynamic shared memory of a CTA, at most (static: under 1 KB)
 constexpr float LA_HEAD = 7.0f;           // log2 of a row's largest weight when its anchor is set
 constexpr float LA_TOP = 15.99f;          // log2 of the largest weight before the anchor is set anew
-constexpr uint32_t TM_O = 0, TM_S = 256, TM_COLS = 512;   // TMEM columns: four blocks of O^T, two S
+constexpr uint32_t TM_O = 0, TM_S = 256, TM_COLS = 512;   // TMEM columns: O (O^T in four blocks of 64), two S
 
 struct LatArgs {
     const int32_t *bt, *seq_lens, *q_starts, *parents;
@@ -579,7 +590,13 @@ __global__ void __launch_bounds__(LA_NT, 1)
 // its rows' queries and the keys of half of the tokens.  O = P V keeps its rows as they are (M = 128, N = 256, twice): a
 // CTA stages half of the 512 values of all tokens, so that O takes 256 of its TMEM columns (a CTA of a pair keeps 64 rows
 // of M = 128 in 128 lanes: lanes 64 and up have the second half of the columns).  Half a token's values is thus staged
-// twice, but no row's key is staged for only 64 query rows, as above.
+// twice, since one descriptor serves both CTAs, and at different places they cannot read it.
+//
+// Bound: the shared-memory reads of the products, 128 bytes per cycle: 24 cycles for each of the 36 products of S, 64 for
+// each of the eight of O, 1376 per step; measured 1420.  Two stages of keys and of values fit beside 64 rows of queries,
+// too few for the latency of HBM, which L2 takes up (three steps ahead; 186 -> 141 us together with loads of keys and
+// values by warps of their own).  Five drafted tokens of eight sequences of 12001 to 16384 tokens, 128 heads: 142 us,
+// 1.11 PFLOP/s, of which the steps 100 us, the join 12 us, the rest starts and outputs of the segments.
 constexpr int LB_KEYS = 64;
 constexpr int LB_K = LB_KEYS / 2 * ROW * 2;      // bytes of a CTA's keys of a step
 constexpr int LB_V = LB_KEYS * LAT;              // and of its values (two bytes each, half of them)

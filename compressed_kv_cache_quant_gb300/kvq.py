@@ -209,7 +209,7 @@ class RopeTable:
 
 
 class AttnMod:
-    """Score forms of kv_decode_attn and kv_chunk_attn (kvq_attn_mod); keeps its tensors alive."""
+    """Score forms of kv_decode_attn, kv_chunk_attn and kv_tree_attn (kvq_attn_mod); keeps its tensors alive."""
 
     def __init__(self, scale=0.0, softcap=0.0, window=0, n_sink=0, slopes=None, prefix_len=None, doc_start=None):
         gpu = _gpu() if any(x is not None for x in (slopes, prefix_len, doc_start)) else -1

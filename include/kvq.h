@@ -697,8 +697,8 @@ int kv_qk_norm_rope(const kvq_layout* layout, const kvq_rope* rope, const uint64
                     uint16_t* q_out, uint16_t* k_out, uint16_t* v_out, void* stream);
 
 /* ------------------------------------------------------------------------
- * Score forms of kv_decode_attn and kv_chunk_attn (host struct, read during the
- * call; NULL or all zero: softmax of q.k/sqrt(d) over the causal tokens).
+ * Score forms of kv_decode_attn, kv_chunk_attn and kv_tree_attn (host struct, read
+ * during the call; NULL or all zero: softmax of q.k/sqrt(d) over the causal tokens).
  * For the query at position i and the cached token j:
  *   s = scale * q.k                       (scale 0: 1/sqrt(d); at most 2.3e38)
  *   s = softcap * tanh(s / softcap)       (softcap > 0)
@@ -709,7 +709,7 @@ int kv_qk_norm_rope(const kvq_layout* layout, const kvq_rope* rope, const uint64
  * position where the query's document begins (doc_start: device int32, one entry
  * per query row; NULL: 0), which may lie behind the query: it then sees nothing.
  * A query that sees nothing gets output 0 and lse -inf.
- * Both calls take max_len up to 2^30.
+ * These calls take max_len up to 2^30.
  * ---------------------------------------------------------------------- */
 typedef struct kvq_attn_mod {
     float   scale;
