@@ -82,8 +82,16 @@ struct ChunkArgs {
 
 // ---------------------------------------------------------------- what a CTA works on
 
+// A CTA's next group of the expanded form, from the warp that loads to the others.
+struct Job {
+    int32_t h, item, split, row0, rows, pos0, T, it0, nt;   // row0, pos0: its first query's row and place; rows 0: the end
+};
+
 struct Shared {
     uint64_t q_full, kv_full[EX_NS], kv_empty[EX_NS], s_full[2], p_full[2][2], o_full[2], drain;
+    uint64_t q_empty, job_full[2], job_empty[2], cta_full;
+    __align__(16) uint32_t cta[4];                // answer of a request for a CTA that was not launched yet
+    Job job[2];
     uint32_t tmem;
     int32_t abort;
     int32_t item_b, item_tok;                     // sequence and first new token of this CTA
@@ -151,12 +159,38 @@ __device__ __forceinline__ uint32_t columns(int a, int b, int w) {
     return b > a ? below(b - 32 * w) & ~below(a - 32 * w) : 0u;
 }
 
+// Asks for a CTA of this grid that was not launched yet; it will not be, and the caller does its work.
+__device__ __forceinline__ void next_cta_request(uint32_t to, uint64_t* bar) {
+    bar_expect(bar, 16);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(to),
+                 "r"(saddr(bar))
+                 : "memory");
+}
+// The answer: its place in the grid, or false when all have been launched (then no further request is allowed).
+__device__ __forceinline__ bool next_cta_answer(uint32_t at, int* x, int* y) {
+    uint32_t some, px, py;
+    asm volatile(
+        "{\n.reg .b128 r;\n.reg .pred p;\nld.shared.b128 r, [%3];\n"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\nselp.u32 %0, 1, 0, p;\nmov.u32 %1, 0;\nmov.u32 %2, 0;\n"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::y.b32.b128 %2, r;\n}"
+        : "=r"(some), "=r"(px), "=r"(py)
+        : "r"(at)
+        : "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // (the next answer is written by the asynchronous proxy)
+    *x = (int)px, *y = (int)py;
+    return some != 0;
+}
+
 // TREE: the new tokens are nodes of trees.  A node's interval ends with the cached tokens before them, and its path
 // adds a few bits among the last columns; positions go by depth.
 //
 // EXPANDED: a key has 128 values of its head and 64 that all heads share, so a query row has three halves; keys and
 // values lie in one piece per sequence.  The ring then holds 16 KB pieces, three of a K tile and two of a V tile (of 64
-// tokens each): 1.6 tiles, since two query tiles take 96 KB.
+// tokens each): 1.6 tiles, since two query tiles take 96 KB.  A CTA works through several groups: while the softmax warps
+// end one, the loading warp asks for another that no CTA has begun and fetches its queries and first keys; all barriers and
+// the ring go on counting.  With a CTA per group 7 us passed between the last turn of one and the first of the next
+// (five prompts of 333-4001 tokens, 16 heads: 116 instead of 109 us).
 template <bool CAP, bool BIAS, Kind KIND>
 __global__ void __launch_bounds__(CA_NT, 1)
     chunk_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -169,27 +203,36 @@ __global__ void __launch_bounds__(CA_NT, 1)
     __shared__ int4 seen_of[EXP ? 1 : CA_ROWS];   // lo, hi, doc, sink of every token
     __shared__ std::conditional_t<TREE, KvqTree, int> tree;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int GQ = a.GQ, tpc = CA_ROWS / GQ, split = blockIdx.y;
-    const int h = a.heads_first ? blockIdx.x % a.H : blockIdx.x / a.items;
-    const int item = a.heads_first ? blockIdx.x / a.H : blockIdx.x % a.items;
+    const int GQ = a.GQ, tpc = CA_ROWS / GQ;
+    const auto place = [&](int x, int* h, int* item) {
+        *h = a.heads_first ? x % a.H : x / a.items;
+        *item = a.heads_first ? x / a.H : x % a.items;
+    };
+    int split = blockIdx.y, h, item;
+    place(blockIdx.x, &h, &item);
     const uint32_t sq = (saddr(raw) + 1023) & ~1023u, skv = sq + 2 * Q_TILE;
     kvq_pdl_begin();
-    if (warp == 0) {
-        int b, tok;
-        find_item(a, item, tpc, &b, &tok);
-        if (lane == 0) {
-            S.item_b = b, S.item_tok = tok;
-            S.abort = 0;
-            S.doc_min = S.lo_min = INT32_MAX;
-            S.sink_max = S.hi_max = 0;
+    int b = 0, tok0 = 0, first = 0, n = 0, T = 0, ntok = 0;
+    if constexpr (EXP) {
+        if (tid == 0) S.abort = 0;
+    } else {
+        if (warp == 0) {
+            int of, tok;
+            find_item(a, item, tpc, &of, &tok);
+            if (lane == 0) {
+                S.item_b = of, S.item_tok = tok;
+                S.abort = 0;
+                S.doc_min = S.lo_min = INT32_MAX;
+                S.sink_max = S.hi_max = 0;
+            }
         }
+        __syncthreads();
+        b = S.item_b, tok0 = S.item_tok;
+        if (b < 0) return;
+        first = a.q_starts[b], n = a.q_starts[b + 1] - first, T = seq_len(a, b);
+        ntok = min(tpc, n - tok0);
     }
-    __syncthreads();
-    const int b = S.item_b, tok0 = S.item_tok;
-    if (b < 0) return;
-    const int first = a.q_starts[b], n = a.q_starts[b + 1] - first, T = seq_len(a, b);
-    const int ntok = min(tpc, n - tok0), rows = ntok * GQ;
-    const int nq = rows > 128 ? 2 : 1;
+    int rows = ntok * GQ, nq = rows > 128 ? 2 : 1;
     const int ctx = T - n;   // cached tokens before the new ones
     if constexpr (TREE) {
         if (tid < n) kvq_tree_fetch(tree, a.parents + first, tid, a.hdr);
@@ -197,7 +240,7 @@ __global__ void __launch_bounds__(CA_NT, 1)
         if (tid < n) kvq_tree_walk(tree, tid, ctx & 31);
         __syncthreads();   // (of the nodes' paths a row reads its own, of their depths all)
     }
-    if (tid < ntok) {
+    if (!EXP && tid < ntok) {
         const int i = tok0 + tid;
         const int doc = a.mod.doc_start ? a.mod.doc_start[first + i] : 0;
         KvqSee see;
@@ -221,7 +264,7 @@ __global__ void __launch_bounds__(CA_NT, 1)
         } else {
             see = kvq_see(a.mod, ctx + i, T, a.mod.prefix_len ? a.mod.prefix_len[b] : 0, doc);
         }
-        if (!EXP) seen_of[tid] = make_int4(see.lo, see.hi, see.doc, see.sink);
+        seen_of[tid] = make_int4(see.lo, see.hi, see.doc, see.sink);
         if (see.lo < see.hi) {
             atomicMin(&S.lo_min, see.lo);
             atomicMax(&S.hi_max, see.hi);
@@ -244,6 +287,14 @@ __global__ void __launch_bounds__(CA_NT, 1)
             bar_init(&S.o_full[i], 1);
         }
         bar_init(&S.drain, 1);
+        if (EXP) {
+            bar_init(&S.q_empty, 1);
+            bar_init(&S.cta_full, 1);
+            for (int i = 0; i < 2; ++i) {
+                bar_init(&S.job_full[i], 1);
+                bar_init(&S.job_empty[i], 1 + 8);   // the issuing lane and the softmax warps
+            }
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 8) {
@@ -257,106 +308,148 @@ __global__ void __launch_bounds__(CA_NT, 1)
     const uint32_t tmem = S.tmem;
     // tiles some row sees: [a1, b1) for the sinks, then [a2, b2); this split takes [it0, it1) of the list
     int a1 = 0, b1 = 0, a2 = 0, b2 = 0;
-    if (S.doc_min < S.sink_max) a1 = S.doc_min / CA_KEYS, b1 = (S.sink_max + CA_KEYS - 1) / CA_KEYS;
-    if (S.lo_min < S.hi_max) a2 = max(S.lo_min / CA_KEYS, b1), b2 = max(a2, (S.hi_max + CA_KEYS - 1) / CA_KEYS);
+    if (!EXP && S.doc_min < S.sink_max) a1 = S.doc_min / CA_KEYS, b1 = (S.sink_max + CA_KEYS - 1) / CA_KEYS;
+    if (!EXP && S.lo_min < S.hi_max) a2 = max(S.lo_min / CA_KEYS, b1), b2 = max(a2, (S.hi_max + CA_KEYS - 1) / CA_KEYS);
     const int total = b1 - a1 + b2 - a2;
     const int per = (total + a.n_splits - 1) / a.n_splits;
-    const int it0 = min(total, split * per), it1 = min(total, it0 + per), nt = it1 - it0;
+    int it0 = min(total, split * per), nt = min(total, it0 + per) - it0;
+    int row0 = first + tok0, pos0 = ctx + tok0;   // the first query's row and place
     const auto tile_of = [&](int it) { return it < b1 - a1 ? a1 + it : a2 + (it - (b1 - a1)); };
 
     // 384 threads are launched with 168 registers each: 256 * 232 + 128 * 40 is the same total
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        if (warp == 9 && nt > 0) {
+        if (warp == 9 && (EXP || nt > 0)) {
             // ---- loads
-            if (lane == 0) {
+            const auto queries = [&] {
                 bar_expect(&S.q_full, nq * Q_TILE);
                 for (int i = 0; i < nq; ++i)
                     for (int c = 0; c < Q_TILE / CA_HALF; ++c)
-                        tma_3d(sq + i * Q_TILE + c * CA_HALF, &map_q, 64 * c, h * GQ, first + tok0 + i * (128 / GQ), &S.q_full);
-            }
-            __syncwarp();
+                        tma_3d(sq + i * Q_TILE + c * CA_HALF, &map_q, 64 * c, h * GQ, row0 + i * (128 / GQ), &S.q_full);
+            };
             if constexpr (EXP) {
-                // tile j is the pieces 5j .. 5j + 4 of a list that goes round the ring: K's three, V's two.  A piece's place was
-                // that of the piece eight before, and every place has its own barriers.
-                const int key0 = a.k_starts[b];
-                if (elect()) {
-                    for (int p = 0; p < 5 * nt; ++p) {
-                        const int j = p / 5, x = p - 5 * j, at = p % EX_NS, key = key0 + tile_of(it0 + j) * CA_KEYS;
-                        if (p >= EX_NS) bar_wait(&S.abort, a.hdr, &S.kv_empty[at], ((p / EX_NS) & 1) ^ 1);
-                        if (*(volatile int32_t*)&S.abort) break;
-                        const uint32_t to = skv + at * CA_HALF;
-                        bar_expect(&S.kv_full[at], CA_HALF);
-                        if (x < 2)
-                            tma_3d(to, &map_k, 64 * x, h, key, &S.kv_full[at]);
-                        else if (x == 2)
-                            tma_3d(to, &map_r, 0, key, 0, &S.kv_full[at]);
-                        else
-                            for (int y = 0; y < 2; ++y)
-                                tma_3d(to + y * (CA_HALF / 2), &map_v, 64 * y, h, key + 64 * (x - 3), &S.kv_full[at]);
+                // A tile is five pieces of a list that goes round the ring: K's three, V's two.  A piece's place was that of the
+                // piece eight before, and every place has its own barriers.
+                int p = 0, k = 0, loads = 0;   // pieces, groups and groups with keys so far
+                int x = blockIdx.x, asked = 0;
+                bool more = true;
+                while (more && !aborted(&S.abort)) {
+                    place(x, &h, &item);
+                    find_item(a, item, tpc, &b, &tok0);
+                    if (b >= 0) {
+                        first = a.q_starts[b], n = a.q_starts[b + 1] - first, T = seq_len(a, b);
+                        rows = min(tpc, n - tok0), nq = rows > 128 ? 2 : 1;
+                        row0 = first + tok0, pos0 = T - n + tok0;
+                        const int tiles = (pos0 + rows + CA_KEYS - 1) / CA_KEYS, each = (tiles + a.n_splits - 1) / a.n_splits;
+                        it0 = min(tiles, split * each), nt = min(tiles, it0 + each) - it0;
+                        if (k >= 2) bar_wait(&S.abort, a.hdr, &S.job_empty[k & 1], ((k >> 1) & 1) ^ 1);
+                        if (lane == 0) {
+                            S.job[k & 1] = Job{h, item, split, row0, rows, pos0, T, it0, nt};
+                            bar_arrive(&S.job_full[k & 1]);
+                        }
+                        __syncwarp();
+                        ++k;
+                        if (nt > 0 && elect()) {
+                            if (loads > 0) bar_wait(&S.abort, a.hdr, &S.q_empty, (loads & 1) ^ 1);
+                            if (!*(volatile int32_t*)&S.abort) queries();
+                            int key = a.k_starts[b] + it0 * CA_KEYS;
+                            for (int j = 0, at = p; j < nt; ++j, key += CA_KEYS) {
+#pragma unroll
+                                for (int c = 0; c < 5; ++c, ++at) {
+                                    uint64_t* full = &S.kv_full[at % EX_NS];
+                                    if (at >= EX_NS) bar_wait(&S.abort, a.hdr, &S.kv_empty[at % EX_NS], ((at / EX_NS) & 1) ^ 1);
+                                    if (*(volatile int32_t*)&S.abort) break;
+                                    const uint32_t to = skv + at % EX_NS * CA_HALF;
+                                    bar_expect(full, CA_HALF);
+                                    if (c < 2)
+                                        tma_3d(to, &map_k, 64 * c, h, key, full);
+                                    else if (c == 2)
+                                        tma_3d(to, &map_r, 0, key, 0, full);
+                                    else
+                                        for (int y = 0; y < 2; ++y)
+                                            tma_3d(to + y * (CA_HALF / 2), &map_v, 64 * y, h, key + 64 * (c - 3), full);
+                                }
+                                if (*(volatile int32_t*)&S.abort) break;
+                            }
+                        }
+                        __syncwarp();
+                        p += 5 * nt, loads += nt > 0;
                     }
+                    if (aborted(&S.abort)) break;
+                    if (lane == 0) next_cta_request(saddr(S.cta), &S.cta_full);
+                    __syncwarp();
+                    bar_wait(&S.abort, a.hdr, &S.cta_full, asked++ & 1);
+                    more = next_cta_answer(saddr(S.cta), &x, &split);
+                    __syncwarp();
+                }
+                if (k >= 2) bar_wait(&S.abort, a.hdr, &S.job_empty[k & 1], ((k >> 1) & 1) ^ 1);
+                if (lane == 0) {
+                    S.job[k & 1].rows = 0;
+                    bar_arrive(&S.job_full[k & 1]);
                 }
                 __syncwarp();
             } else {
-            const int pg = lane & 7;   // lanes 0-7 look up one page each
-            const int nowhere = (int)(a.num_blocks * a.H * (PG / 8));  // a group of rows behind the pool: zeros
-            // where this lane's page of the j-th tile begins, in groups of 8 rows: it is looked up a tile ahead,
-            // before the wait for V's stage
-            const auto group_of = [&](int j) {
-                const int t = tile_of(it0 + j), lp = t * (CA_KEYS / PG) + pg;
-                uint32_t need;  // bit per page: some row sees a token of it
-                if (a.mod.doc_start == nullptr) {
-                    const int p0 = lp * PG;
-                    need = __ballot_sync(0xffffffffu, (p0 < S.hi_max && p0 + PG > S.lo_min) ||
-                                                          (p0 < S.sink_max && p0 + PG > S.doc_min));
-                } else {
-                    uint32_t bits = 0;
-                    for (int k = lane; k < ntok; k += 32) {
-                        const int4 e = seen_of[k];
-                        const int p0 = t * (CA_KEYS / PG);
-                        if (e.x < e.y) bits |= below((e.y + PG - 1) / PG - p0) & ~below(e.x / PG - p0);
-                        if (e.z < e.w) bits |= below((e.w + PG - 1) / PG - p0) & ~below(e.z / PG - p0);
-                        if (TREE) bits |= below((T + PG - 1) / PG - p0) & ~below(ctx / PG - p0);
-                    }
-                    need = __reduce_or_sync(0xffffffffu, bits);
-                }
-                int y = nowhere;
-                if (need >> pg & 1) {
-                    const int32_t page = a.bt[(int64_t)b * a.max_blocks + lp];
-                    if (page >= 0 && page < a.num_blocks)
-                        y = (page * a.H + h) * (PG / 8);
-                    else if (lane == pg)
-                        kvq_dev_flag(a.hdr, KVQ_DEV_BAD_PAGE, page);
-                }
-                return y;
-            };
-            // one elected lane issues from uniform registers: a copy per lane would be issued one by one just
-            // the same, at 79 cycles each
-            const auto fetch = [&](int slot, const CUtensorMap* map, const int* at) {
-                const int st = slot % CA_NS;
-                if (slot >= CA_NS) bar_wait(&S.abort, a.hdr, &S.kv_empty[st], ((slot / CA_NS) & 1) ^ 1);
-                const bool ok = !aborted(&S.abort);
-                if (ok && elect()) {
-                    bar_expect(&S.kv_full[st], CA_TILE);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) tma_page(skv + st * CA_TILE + k * (PG * D * 2), map, at[k], &S.kv_full[st]);
-                }
+                if (lane == 0) queries();
                 __syncwarp();
-                return ok;
-            };
-            bool ok = true;
-            int y = group_of(0);
-            for (int j = 0; j < nt && ok; ++j) {
-                int at[8];
+                const int pg = lane & 7;   // lanes 0-7 look up one page each
+                const int nowhere = (int)(a.num_blocks * a.H * (PG / 8));  // a group of rows behind the pool: zeros
+                // where this lane's page of the j-th tile begins, in groups of 8 rows: it is looked up a tile ahead,
+                // before the wait for V's stage
+                const auto group_of = [&](int j) {
+                    const int t = tile_of(it0 + j), lp = t * (CA_KEYS / PG) + pg;
+                    uint32_t need;  // bit per page: some row sees a token of it
+                    if (a.mod.doc_start == nullptr) {
+                        const int p0 = lp * PG;
+                        need = __ballot_sync(0xffffffffu, (p0 < S.hi_max && p0 + PG > S.lo_min) ||
+                                                              (p0 < S.sink_max && p0 + PG > S.doc_min));
+                    } else {
+                        uint32_t bits = 0;
+                        for (int k = lane; k < ntok; k += 32) {
+                            const int4 e = seen_of[k];
+                            const int p0 = t * (CA_KEYS / PG);
+                            if (e.x < e.y) bits |= below((e.y + PG - 1) / PG - p0) & ~below(e.x / PG - p0);
+                            if (e.z < e.w) bits |= below((e.w + PG - 1) / PG - p0) & ~below(e.z / PG - p0);
+                            if (TREE) bits |= below((T + PG - 1) / PG - p0) & ~below(ctx / PG - p0);
+                        }
+                        need = __reduce_or_sync(0xffffffffu, bits);
+                    }
+                    int y = nowhere;
+                    if (need >> pg & 1) {
+                        const int32_t page = a.bt[(int64_t)b * a.max_blocks + lp];
+                        if (page >= 0 && page < a.num_blocks)
+                            y = (page * a.H + h) * (PG / 8);
+                        else if (lane == pg)
+                            kvq_dev_flag(a.hdr, KVQ_DEV_BAD_PAGE, page);
+                    }
+                    return y;
+                };
+                // one elected lane issues from uniform registers: a copy per lane would be issued one by one just
+                // the same, at 79 cycles each
+                const auto fetch = [&](int slot, const CUtensorMap* map, const int* at) {
+                    const int st = slot % CA_NS;
+                    if (slot >= CA_NS) bar_wait(&S.abort, a.hdr, &S.kv_empty[st], ((slot / CA_NS) & 1) ^ 1);
+                    const bool ok = !aborted(&S.abort);
+                    if (ok && elect()) {
+                        bar_expect(&S.kv_full[st], CA_TILE);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) at[k] = __shfl_sync(0xffffffffu, y, k);
-                ok = fetch(2 * j, &map_k, at);
-                if (j + 1 < nt) y = group_of(j + 1);
-                ok = ok && fetch(2 * j + 1, &map_v, at);
-            }
+                        for (int k = 0; k < 8; ++k) tma_page(skv + st * CA_TILE + k * (PG * D * 2), map, at[k], &S.kv_full[st]);
+                    }
+                    __syncwarp();
+                    return ok;
+                };
+                bool ok = true;
+                int y = group_of(0);
+                for (int j = 0; j < nt && ok; ++j) {
+                    int at[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) at[k] = __shfl_sync(0xffffffffu, y, k);
+                    ok = fetch(2 * j, &map_k, at);
+                    if (j + 1 < nt) y = group_of(j + 1);
+                    ok = ok && fetch(2 * j + 1, &map_v, at);
+                }
             }
         }
-        if (warp == 8 && nt > 0) {
+        if (warp == 8 && (EXP || nt > 0)) {
             // ---- tensor cores.  The whole warp walks the loop and one elected lane issues, so that the
             // descriptors stay in uniform registers.  All 512 TMEM columns are this CTA's, so they start at
             // column 0.  A descriptor is its low word plus constants: the low words are made opaque in every
@@ -394,10 +487,11 @@ __global__ void __launch_bounds__(CA_NT, 1)
             if constexpr (EXP) {
                 // one lane walks the loop
                 if (elect()) {
+                    int p0 = 0, loads = 0, turns[2] = {0, 0};   // pieces, groups with keys and tiles so far
                     const auto scores = [&](int i, int j) {
 #pragma unroll
                         for (int c = 0; c < EX_QC; ++c) {
-                            const int p = 5 * j + c;
+                            const int p = p0 + 5 * j + c;
                             if (i == 0) bar_wait(&S.abort, a.hdr, &S.kv_full[p % EX_NS], (p / EX_NS) & 1);
                             uint32_t x = lq + (i * Q_TILE + c * CA_HALF >> 4), y = lk + (p % EX_NS * CA_HALF >> 4);
                             asm volatile("" : "+r"(x), "+r"(y));
@@ -407,65 +501,77 @@ __global__ void __launch_bounds__(CA_NT, 1)
                             if (i == nq - 1) tc_commit(&S.kv_empty[p % EX_NS]);
                         }
                         tc_commit(&S.s_full[i]);
+                        if (i == nq - 1 && j == nt - 1) tc_commit(&S.q_empty);
                     };
-                    bar_wait(&S.abort, a.hdr, &S.q_full, 0);
-                    for (int i = 0; i < nq; ++i) scores(i, 0);
-                    for (int j = 0; j < nt; ++j) {
+                    for (int g = 0;; ++g) {
+                        bar_wait(&S.abort, a.hdr, &S.job_full[g & 1], (g >> 1) & 1);
+                        if (*(volatile int32_t*)&S.abort) break;
+                        rows = S.job[g & 1].rows, nt = S.job[g & 1].nt;
+                        bar_arrive(&S.job_empty[g & 1]);
+                        if (rows == 0) break;
+                        if (nt == 0) continue;
+                        nq = rows > 128 ? 2 : 1;
+                        bar_wait(&S.abort, a.hdr, &S.q_full, loads++ & 1);
+                        for (int i = 0; i < nq; ++i) scores(i, 0);
+                        for (int j = 0; j < nt; ++j) {
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            if (i == nq) break;
+                            for (int i = 0; i < 2; ++i) {
+                                if (i == nq) break;
 #pragma unroll
-                            for (int half = 0; half < 2; ++half) {
-                                const int p = 5 * j + 3 + half;
-                                // (V first: this lane waits for P some 700 cycles, so here it costs nothing)
-                                if (i == 0) bar_wait(&S.abort, a.hdr, &S.kv_full[p % EX_NS], (p / EX_NS) & 1);
-                                bar_wait(&S.abort, a.hdr, &S.p_full[i][half], j & 1);
-                                tc_after();
-                                uint32_t y = lv + (p % EX_NS * CA_HALF >> 4);
-                                asm volatile("" : "+r"(y));
+                                for (int half = 0; half < 2; ++half) {
+                                    const int p = p0 + 5 * j + 3 + half;
+                                    // (V first: this lane waits for P some 700 cycles, so here it costs nothing)
+                                    if (i == 0) bar_wait(&S.abort, a.hdr, &S.kv_full[p % EX_NS], (p / EX_NS) & 1);
+                                    bar_wait(&S.abort, a.hdr, &S.p_full[i][half], (turns[i] + j) & 1);
+                                    tc_after();
+                                    uint32_t y = lv + (p % EX_NS * CA_HALF >> 4);
+                                    asm volatile("" : "+r"(y));
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    mma_ts(TM_O + 128 * i, TM_S + 128 * i + 8 * (4 * half + k), desc(hi_kv, y + (k * 2048 >> 4)), IDESC_PV,
-                                           j > 0 || half + k > 0);
-                                if (i == nq - 1) tc_commit(&S.kv_empty[p % EX_NS]);
+                                    for (int k = 0; k < 4; ++k)
+                                        mma_ts(TM_O + 128 * i, TM_S + 128 * i + 8 * (4 * half + k), desc(hi_kv, y + (k * 2048 >> 4)), IDESC_PV,
+                                               j > 0 || half + k > 0);
+                                    if (i == nq - 1) tc_commit(&S.kv_empty[p % EX_NS]);
+                                }
+                                if (j + 1 < nt)
+                                    scores(i, j + 1);
+                                else
+                                    tc_commit(&S.o_full[i]);
                             }
-                            if (j + 1 < nt)
-                                scores(i, j + 1);
-                            else
-                                tc_commit(&S.o_full[i]);
                         }
+                        p0 += 5 * nt, turns[0] += nt;
+                        if (nq == 2) turns[1] += nt;
                     }
                 }
                 __syncwarp();
             } else {
-            bar_wait(&S.abort, a.hdr, &S.q_full, 0);
-            bar_wait(&S.abort, a.hdr, &S.kv_full[0], 0);
-            tc_after();
-            qk(0, 0);
-            if (nq > 1) qk(1, 0);
-            commit(&S.kv_empty[0]);
-            for (int j = 0; j < nt; ++j) {
-                const int sv = (2 * j + 1) % CA_NS, sk = (2 * j + 2) % CA_NS;
-                const bool more = j + 1 < nt;
+                bar_wait(&S.abort, a.hdr, &S.q_full, 0);
+                bar_wait(&S.abort, a.hdr, &S.kv_full[0], 0);
+                tc_after();
+                qk(0, 0);
+                if (nq > 1) qk(1, 0);
+                commit(&S.kv_empty[0]);
+                for (int j = 0; j < nt; ++j) {
+                    const int sv = (2 * j + 1) % CA_NS, sk = (2 * j + 2) % CA_NS;
+                    const bool more = j + 1 < nt;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (i == nq) break;
-                    bar_wait(&S.abort, a.hdr, &S.p_full[i][0], j & 1);
-                    tc_after();
-                    pv(i, sv, 0, j > 0);
-                    bar_wait(&S.abort, a.hdr, &S.p_full[i][1], j & 1);
-                    tc_after();
-                    pv(i, sv, 1, true);
-                    if (i == nq - 1) commit(&S.kv_empty[sv]);
-                    if (more) {
-                        if (i == 0) bar_wait(&S.abort, a.hdr, &S.kv_full[sk], ((2 * j + 2) / CA_NS) & 1);
-                        qk(i, sk);
-                    } else {
-                        commit(&S.o_full[i]);
+                    for (int i = 0; i < 2; ++i) {
+                        if (i == nq) break;
+                        bar_wait(&S.abort, a.hdr, &S.p_full[i][0], j & 1);
+                        tc_after();
+                        pv(i, sv, 0, j > 0);
+                        bar_wait(&S.abort, a.hdr, &S.p_full[i][1], j & 1);
+                        tc_after();
+                        pv(i, sv, 1, true);
+                        if (i == nq - 1) commit(&S.kv_empty[sv]);
+                        if (more) {
+                            if (i == 0) bar_wait(&S.abort, a.hdr, &S.kv_full[sk], ((2 * j + 2) / CA_NS) & 1);
+                            qk(i, sk);
+                        } else {
+                            commit(&S.o_full[i]);
+                        }
                     }
+                    if (more) commit(&S.kv_empty[sk]);
                 }
-                if (more) commit(&S.kv_empty[sk]);
-            }
             }
         }
     } else {
@@ -474,300 +580,317 @@ __global__ void __launch_bounds__(CA_NT, 1)
         const int i = warp >> 2, r = tid;   // row of the CTA
         const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21);  // TMEM lanes 32 (warp % 4) ..
         const uint32_t ts = lane_base + TM_S + 128 * i, to = lane_base + TM_O + 128 * i;
-        const bool valid = r < rows;
-        const int tok = r / GQ;
-        int4 see = make_int4(0, 0, 0, 0);
-        int maxlo = 0, minhi = INT32_MAX;   // over the warp's rows: tiles between need no mask
-        if (valid) {
-            see = EXP ? make_int4(0, ctx + tok0 + tok + 1, 0, 0) : seen_of[tok];
-            maxlo = see.x, minhi = see.y;
-        }
-        maxlo = __reduce_max_sync(0xffffffffu, maxlo);
-        minhi = __reduce_min_sync(0xffffffffu, minhi);
-        int pos = ctx + tok0 + tok;
-        if constexpr (TREE) pos = ctx + (valid ? tree.depth[tok0 + tok] : 0);
-        // what the row sees of the w-th 32 columns of the tile at t0
-        const auto seen_bits = [&](int t0, int w) {
-            if constexpr (TREE) {   // (from shared memory: kept in registers over the loop, some of them spill)
-                if (!valid) return 0u;
-                const int4 e = seen_of[tok];
-                return columns(e.x - t0, e.y - t0, w) | columns(e.z - t0, e.w - t0, w) | kvq_tree_bits(tree, tok0 + tok, t0 + 32 * w, ctx);
+        int p0 = 0, turns = 0, outs = 0;   // expanded form: pieces of the ring, this tile's turns and outputs so far
+        for (int g = 0;; ++g) {
+            if constexpr (EXP) {
+                // (a group of at most 128 rows is tile 0's alone: these warps may wait for as long as it has tiles)
+                bar_wait(&S.abort, a.hdr, &S.job_full[g & 1], (g >> 1) & 1, KVQ_SPIN * (1 + min(nt >> 6, 4095)));
+                if (aborted(&S.abort)) break;
+                const Job w = S.job[g & 1];
+                __syncwarp();
+                if (lane == 0) bar_arrive(&S.job_empty[g & 1]);
+                if (w.rows == 0) break;
+                h = w.h, item = w.item, split = w.split, row0 = w.row0, rows = w.rows, pos0 = w.pos0, T = w.T, it0 = w.it0, nt = w.nt;
+                nq = rows > 128 ? 2 : 1;
             }
-            return columns(see.x - t0, see.y - t0, w) | columns(see.z - t0, see.w - t0, w);
-        };
-        const float slope2 = BIAS && valid ? a.mod.slopes[h * GQ + r % GQ] * KVQ_LOG2E : 0.0f;
-        float m = valid ? -INFINITY : INFINITY, l = 0.0f;   // (no row: weights 0, never a new anchor)
-        if (i < nq) {
-            for (int j = 0; j < nt; ++j) {
-                const int t0 = tile_of(it0 + j) * CA_KEYS;
-                // rows at and behind T may hold anything: 0 * NaN must not reach O
-                const bool tail = T < t0 + CA_KEYS && (EXP || (T & (PG - 1)) != 0) && T > t0;
-                const auto v_wait = [&] {
-                    if (EXP) {
-                        bar_wait(&S.abort, a.hdr, &S.kv_full[(5 * j + 3) % EX_NS], ((5 * j + 3) / EX_NS) & 1);
-                        bar_wait(&S.abort, a.hdr, &S.kv_full[(5 * j + 4) % EX_NS], ((5 * j + 4) / EX_NS) & 1);
-                    } else {
-                        bar_wait(&S.abort, a.hdr, &S.kv_full[(2 * j + 1) % CA_NS], ((2 * j + 1) / CA_NS) & 1);
-                    }
-                };
-                bar_wait(&S.abort, a.hdr, &S.s_full[i], j & 1);
-                // tile 0's weights stand for V's arrival too (its products are issued after these waits, and tile
-                // 1's after tile 0's): the issuing warp is the busier one.  1.38 -> 1.36 ms for the prompt
-                if (!EXP && i == 0) v_wait();
-                if (tail) {
-                    v_wait();
-                    const uint32_t base = skv + (2 * j + 1) % CA_NS * CA_TILE;
-                    const int r0 = T - t0, r1 = EXP ? CA_KEYS : (r0 + PG - 1) / PG * PG;
-                    for (int x = tid & 127; x < (r1 - r0) * 16; x += 128) {
-                        const int row = r0 + (x >> 4);
-                        const uint32_t at = EXP ? skv + (5 * j + 3 + (row >> 6)) % EX_NS * CA_HALF + (x & 1) * (CA_HALF / 2) +
-                                                      (row & 63) * 128 + ((x >> 1) & 7) * 16
-                                                : base + (row >> 3) * 2048 + (x & 1) * 1024 + (row & 7) * 128 + ((x >> 1) & 7) * 16;
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    if (CAP) {
-                        // The form of the cap below is the warp's choice, by the size of its scores: neither these rows
-                        // nor queries that are not the sequence's have a part in it, or what they hold would change
-                        // the others' last bits.
-                        tc_after();
+            const bool valid = r < rows;
+            const int tok = r / GQ;
+            int4 see = make_int4(0, 0, 0, 0);
+            int maxlo = 0, minhi = INT32_MAX;   // over the warp's rows: tiles between need no mask
+            if (valid) {
+                see = EXP ? make_int4(0, pos0 + tok + 1, 0, 0) : seen_of[tok];
+                maxlo = see.x, minhi = see.y;
+            }
+            maxlo = __reduce_max_sync(0xffffffffu, maxlo);
+            minhi = __reduce_min_sync(0xffffffffu, minhi);
+            int pos = pos0 + tok;
+            if constexpr (TREE) pos = ctx + (valid ? tree.depth[tok0 + tok] : 0);
+            // what the row sees of the w-th 32 columns of the tile at t0
+            const auto seen_bits = [&](int t0, int w) {
+                if constexpr (TREE) {   // (from shared memory: kept in registers over the loop, some of them spill)
+                    if (!valid) return 0u;
+                    const int4 e = seen_of[tok];
+                    return columns(e.x - t0, e.y - t0, w) | columns(e.z - t0, e.w - t0, w) | kvq_tree_bits(tree, tok0 + tok, t0 + 32 * w, ctx);
+                }
+                return columns(see.x - t0, see.y - t0, w) | columns(see.z - t0, see.w - t0, w);
+            };
+            const float slope2 = BIAS && valid ? a.mod.slopes[h * GQ + r % GQ] * KVQ_LOG2E : 0.0f;
+            float m = valid ? -INFINITY : INFINITY, l = 0.0f;   // (no row: weights 0, never a new anchor)
+            if (i < nq) {
+                for (int j = 0; j < nt; ++j) {
+                    const int t0 = (EXP ? it0 + j : tile_of(it0 + j)) * CA_KEYS;
+                    // rows at and behind T may hold anything: 0 * NaN must not reach O
+                    const bool tail = T < t0 + CA_KEYS && (EXP || (T & (PG - 1)) != 0) && T > t0;
+                    const auto v_wait = [&] {
+                        if (EXP) {
+                            for (int p = p0 + 5 * j + 3; p < p0 + 5 * j + 5; ++p)
+                                bar_wait(&S.abort, a.hdr, &S.kv_full[p % EX_NS], (p / EX_NS) & 1);
+                        } else {
+                            bar_wait(&S.abort, a.hdr, &S.kv_full[(2 * j + 1) % CA_NS], ((2 * j + 1) / CA_NS) & 1);
+                        }
+                    };
+                    bar_wait(&S.abort, a.hdr, &S.s_full[i], (turns + j) & 1);
+                    // tile 0's weights stand for V's arrival too (its products are issued after these waits, and tile
+                    // 1's after tile 0's): the issuing warp is the busier one.  1.38 -> 1.36 ms for the prompt
+                    if (!EXP && i == 0) v_wait();
+                    if (tail) {
+                        v_wait();
+                        const uint32_t base = skv + (2 * j + 1) % CA_NS * CA_TILE;
+                        const int r0 = T - t0, r1 = EXP ? CA_KEYS : (r0 + PG - 1) / PG * PG;
+                        for (int x = tid & 127; x < (r1 - r0) * 16; x += 128) {
+                            const int row = r0 + (x >> 4);
+                            const uint32_t at = EXP ? skv + (p0 + 5 * j + 3 + (row >> 6)) % EX_NS * CA_HALF + (x & 1) * (CA_HALF / 2) +
+                                                          (row & 63) * 128 + ((x >> 1) & 7) * 16
+                                                    : base + (row >> 3) * 2048 + (x & 1) * 1024 + (row & 7) * 128 + ((x >> 1) & 7) * 16;
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        if (CAP) {
+                            // The form of the cap below is the warp's choice, by the size of its scores: neither these rows
+                            // nor queries that are not the sequence's have a part in it, or what they hold would change
+                            // the others' last bits.
+                            tc_after();
 #pragma unroll 1
-                        for (int c = r0; c < r1; ++c) tm_st1(ts + c, 0);
-                        tm_wait_st();
-                    }
-                }
-                tc_after();
-                float s[128];
-                tm_ld128(ts, reinterpret_cast<uint32_t*>(s));
-                float scale = a.mod.pre;
-                if (CAP) {
-                    float big[2] = {0.0f, 0.0f};
-#pragma unroll
-                    for (int c = 0; c < 128; c += 4) {
-                        big[0] = max3(big[0], fabsf(s[c]), fabsf(s[c + 1]));
-                        big[1] = max3(big[1], fabsf(s[c + 2]), fabsf(s[c + 3]));
-                    }
-                    if (__all_sync(0xffffffffu, !valid || fmaxf(big[0], big[1]) * a.mod.pre <= 0.75f)) {
-                        // the usual case: tanh x = x P(x^2) on |x| <= 3/4, P the polynomial through the Chebyshev
-                        // points, 6e-7 relative; 3.5 instructions per score (below they are 2 special-function
-                        // results on top of the weight's one: packed documents 87 us instead of 73)
-                        const float z = a.mod.post;
-                        const uint64_t pre2 = pair(a.mod.pre, a.mod.pre);
-                        const uint64_t c0 = pair(0.999999463558197f * z, 0.999999463558197f * z),
-                                       c1 = pair(-0.3332834839820862f * z, -0.3332834839820862f * z),
-                                       c2 = pair(0.13259831070899963f * z, 0.13259831070899963f * z),
-                                       c3 = pair(-0.05008019134402275f * z, -0.05008019134402275f * z),
-                                       c4 = pair(0.012950727716088295f * z, 0.012950727716088295f * z);
-#pragma unroll
-                        for (int c = 0; c < 128; c += 2) {
-                            const uint64_t x = mul2(pair(s[c], s[c + 1]), pre2), u = mul2(x, x);
-                            unpair(mul2(x, fma2(fma2(fma2(fma2(c4, u, c3), u, c2), u, c1), u, c0)), &s[c], &s[c + 1]);
+                            for (int c = r0; c < r1; ++c) tm_st1(ts + c, 0);
+                            tm_wait_st();
                         }
-                    } else {
-                        // tanh x = 1 - 2 / (1 + e^2x), 5e-7 absolute: ex2's and rcp's 2^-22, and three fp32 roundings
-                        const float k2 = a.mod.pre * (2.0f * KVQ_LOG2E), p2 = -2.0f * a.mod.post;
-#pragma unroll
-                        for (int c = 0; c < 128; ++c) s[c] = fmaf(p2, rcp(1.0f + ex2(s[c] * k2)), a.mod.post);
                     }
-                    scale = 1.0f;
-                }
-                if (BIAS) {
-                    const float from = (float)(pos - t0);   // (whole numbers: exact below 2^24)
-                    const float mul = CAP ? 1.0f : a.mod.pre;
-                    bool nodes = false;
-                    if constexpr (TREE) {
-                        nodes = t0 + CA_KEYS > ctx;
+                    tc_after();
+                    float s[128];
+                    tm_ld128(ts, reinterpret_cast<uint32_t*>(s));
+                    float scale = a.mod.pre;
+                    if (CAP) {
+                        float big[2] = {0.0f, 0.0f};
+#pragma unroll
+                        for (int c = 0; c < 128; c += 4) {
+                            big[0] = max3(big[0], fabsf(s[c]), fabsf(s[c + 1]));
+                            big[1] = max3(big[1], fabsf(s[c + 2]), fabsf(s[c + 3]));
+                        }
+                        if (__all_sync(0xffffffffu, !valid || fmaxf(big[0], big[1]) * a.mod.pre <= 0.75f)) {
+                            // the usual case: tanh x = x P(x^2) on |x| <= 3/4, P the polynomial through the Chebyshev
+                            // points, 6e-7 relative; 3.5 instructions per score (below they are 2 special-function
+                            // results on top of the weight's one: packed documents 87 us instead of 73)
+                            const float z = a.mod.post;
+                            const uint64_t pre2 = pair(a.mod.pre, a.mod.pre);
+                            const uint64_t c0 = pair(0.999999463558197f * z, 0.999999463558197f * z),
+                                           c1 = pair(-0.3332834839820862f * z, -0.3332834839820862f * z),
+                                           c2 = pair(0.13259831070899963f * z, 0.13259831070899963f * z),
+                                           c3 = pair(-0.05008019134402275f * z, -0.05008019134402275f * z),
+                                           c4 = pair(0.012950727716088295f * z, 0.012950727716088295f * z);
+#pragma unroll
+                            for (int c = 0; c < 128; c += 2) {
+                                const uint64_t x = mul2(pair(s[c], s[c + 1]), pre2), u = mul2(x, x);
+                                unpair(mul2(x, fma2(fma2(fma2(fma2(c4, u, c3), u, c2), u, c1), u, c0)), &s[c], &s[c + 1]);
+                            }
+                        } else {
+                            // tanh x = 1 - 2 / (1 + e^2x), 5e-7 absolute: ex2's and rcp's 2^-22, and three fp32 roundings
+                            const float k2 = a.mod.pre * (2.0f * KVQ_LOG2E), p2 = -2.0f * a.mod.post;
+#pragma unroll
+                            for (int c = 0; c < 128; ++c) s[c] = fmaf(p2, rcp(1.0f + ex2(s[c] * k2)), a.mod.post);
+                        }
+                        scale = 1.0f;
+                    }
+                    if (BIAS) {
+                        const float from = (float)(pos - t0);   // (whole numbers: exact below 2^24)
+                        const float mul = CAP ? 1.0f : a.mod.pre;
+                        bool nodes = false;
+                        if constexpr (TREE) {
+                            nodes = t0 + CA_KEYS > ctx;
+                            if (nodes) {
+#pragma unroll
+                                for (int c = 0; c < 128; ++c) {
+                                    const int k = t0 + c - ctx;
+                                    const int at = k < 0 ? t0 + c : k < n ? ctx + tree.depth[k] : pos;
+                                    s[c] = fmaf(s[c], mul, -slope2 * fabsf((float)(pos - at)));
+                                }
+                            }
+                        }
                         if (nodes) {
+                        } else if (TREE || a.mod.prefix_len == nullptr) {
+                            // what is seen is not ahead: -slope (from - c), linear in the column
+                            const float at0 = -slope2 * from;
+                            const uint64_t mul_2 = pair(mul, mul);
 #pragma unroll
-                            for (int c = 0; c < 128; ++c) {
-                                const int k = t0 + c - ctx;
-                                const int at = k < 0 ? t0 + c : k < n ? ctx + tree.depth[k] : pos;
-                                s[c] = fmaf(s[c], mul, -slope2 * fabsf((float)(pos - at)));
+                            for (int c = 0; c < 128; c += 2) {
+                                const uint64_t b = pair(fmaf(slope2, (float)c, at0), fmaf(slope2, (float)(c + 1), at0));
+                                unpair(CAP ? add2(pair(s[c], s[c + 1]), b) : fma2(pair(s[c], s[c + 1]), mul_2, b), &s[c], &s[c + 1]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 128; ++c) s[c] = fmaf(s[c], mul, -slope2 * fabsf(from - (float)c));
+                        }
+                        scale = 1.0f;
+                    }
+                    if (t0 < maxlo || t0 + CA_KEYS > minhi) {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            // an edge crosses few of a warp's words of 32 columns
+                            const uint32_t bits = seen_bits(t0, w);
+                            if (__all_sync(0xffffffffu, bits == ~0u)) continue;
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (!(bits >> c & 1)) s[32 * w + c] = -INFINITY;
+                        }
+                    }
+                    // The first half's weights are taken with the anchor so far, while the tile's maximum is still being
+                    // found; only when that is too far above a row's anchor are they taken again.
+                    uint32_t p[32];
+                    uint64_t sum2[2];
+                    float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    // The steps of a pair are spread over eight turns of the loop, so that no instruction waits
+                    // for the one before; the maximum's comparisons fill the gaps of the first half.
+                    const auto weights = [&](int c, bool with_max) {
+                        const float ms = m == -INFINITY ? 0.0f : m;
+                        const uint64_t scale2 = pair(scale, scale), ms2 = pair(-ms, -ms);
+                        uint64_t t[32];
+                        float e[64];
+#pragma unroll
+                        for (int x = 0; x < 32 + 8; ++x) {
+                            if (x < 32) {
+                                t[x] = fma2(pair(s[c + 2 * x], s[c + 2 * x + 1]), scale2, ms2);
+                                if (with_max) {
+                                    mx4[x & 1] = max3(mx4[x & 1], s[2 * x], s[2 * x + 1]);
+                                    mx4[2 + (x & 1)] = max3(mx4[2 + (x & 1)], s[64 + 2 * x], s[64 + 2 * x + 1]);
+                                }
+                            }
+                            if (x >= 4 && x < 36) {
+                                unpair(t[x - 4], &e[2 * (x - 4)], &e[2 * (x - 4) + 1]);
+                                e[2 * (x - 4)] = ex2(e[2 * (x - 4)]);
+                                e[2 * (x - 4) + 1] = ex2(e[2 * (x - 4) + 1]);
+                            }
+                            if (x >= 8) {
+                                const int y = x - 8;
+                                sum2[y & 1] = add2(sum2[y & 1], pair(e[2 * y], e[2 * y + 1]));
+                                p[y] = half2_bits(e[2 * y], e[2 * y + 1]);
                             }
                         }
-                    }
-                    if (nodes) {
-                    } else if (TREE || a.mod.prefix_len == nullptr) {
-                        // what is seen is not ahead: -slope (from - c), linear in the column
-                        const float at0 = -slope2 * from;
-                        const uint64_t mul_2 = pair(mul, mul);
+                    };
+                    const auto rescale = [&](float f) {
 #pragma unroll
-                        for (int c = 0; c < 128; c += 2) {
-                            const uint64_t b = pair(fmaf(slope2, (float)c, at0), fmaf(slope2, (float)(c + 1), at0));
-                            unpair(CAP ? add2(pair(s[c], s[c + 1]), b) : fma2(pair(s[c], s[c + 1]), mul_2, b), &s[c], &s[c + 1]);
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tm_ld32(to + c, o);
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                            tm_st32(to + c, o);
                         }
-                    } else {
+                    };
+                    const auto hand_over = [&](int c) {   // the products start on the first half of the keys
+                        tm_st32(ts + c / 2, p);
+                        tm_wait_st();
+                        tc_before();
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(&S.p_full[i][c / 64]);
+                    };
+                    // A weight's exponent s * scale - m is rounded once, behind the difference.  That is exact enough until an
+                    // fp32 step of m is no longer far below 1: a row's largest weight would be 2^(m's rounding error), 0 or
+                    // infinite.  Then the products are rounded like m itself, from S as it still lies in TMEM (an own path,
+                    // since a change of s in the loop below costs every prompt 3%).
+                    const auto far_tile = [&] {
+                        const auto seen = [&](int c) {
+                            return seen_bits(t0, c >> 5) >> (c & 31) & 1;
+                        };
+                        uint32_t v[32];
+                        float top = -INFINITY;
+                        for (int c = 0; c < 128; c += 32) {
+                            tm_ld32(ts + c, v);
 #pragma unroll
-                        for (int c = 0; c < 128; ++c) s[c] = fmaf(s[c], mul, -slope2 * fabsf(from - (float)c));
-                    }
-                    scale = 1.0f;
-                }
-                if (t0 < maxlo || t0 + CA_KEYS > minhi) {
+                            for (int x = 0; x < 32; ++x)
+                                if (seen(c + x)) top = fmaxf(top, __fmul_rn(__uint_as_float(v[x]), scale));
+                        }
+                        const float anchor = fmaxf(m, top - CA_HEAD);
+                        const float f = m == anchor ? 1.0f : ex2(m - anchor);
+                        m = anchor;
+                        l *= f;
+                        if (j > 0) rescale(f);
+                        const float ms = m == -INFINITY ? 0.0f : m;
+                        for (int c = 0; c < 128; c += 64) {
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        // an edge crosses few of a warp's words of 32 columns
-                        const uint32_t bits = seen_bits(t0, w);
-                        if (__all_sync(0xffffffffu, bits == ~0u)) continue;
+                            for (int k = 0; k < 64; k += 32) {
+                                tm_ld32(ts + c + k, v);
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (!(bits >> c & 1)) s[32 * w + c] = -INFINITY;
-                    }
-                }
-                // The first half's weights are taken with the anchor so far, while the tile's maximum is still being
-                // found; only when that is too far above a row's anchor are they taken again.
-                uint32_t p[32];
-                uint64_t sum2[2];
-                float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                // The steps of a pair are spread over eight turns of the loop, so that no instruction waits
-                // for the one before; the maximum's comparisons fill the gaps of the first half.
-                const auto weights = [&](int c, bool with_max) {
-                    const float ms = m == -INFINITY ? 0.0f : m;
-                    const uint64_t scale2 = pair(scale, scale), ms2 = pair(-ms, -ms);
-                    uint64_t t[32];
-                    float e[64];
-#pragma unroll
-                    for (int x = 0; x < 32 + 8; ++x) {
-                        if (x < 32) {
-                            t[x] = fma2(pair(s[c + 2 * x], s[c + 2 * x + 1]), scale2, ms2);
-                            if (with_max) {
-                                mx4[x & 1] = max3(mx4[x & 1], s[2 * x], s[2 * x + 1]);
-                                mx4[2 + (x & 1)] = max3(mx4[2 + (x & 1)], s[64 + 2 * x], s[64 + 2 * x + 1]);
+                                for (int x = 0; x < 32; x += 2) {
+                                    const float e0 = seen(c + k + x) ? ex2(__fmul_rn(__uint_as_float(v[x]), scale) - ms) : 0.0f;
+                                    const float e1 = seen(c + k + x + 1) ? ex2(__fmul_rn(__uint_as_float(v[x + 1]), scale) - ms) : 0.0f;
+                                    l += e0 + e1;
+                                    p[(k + x) / 2] = half2_bits(e0, e1);
+                                }
                             }
+                            hand_over(c);
                         }
-                        if (x >= 4 && x < 36) {
-                            unpair(t[x - 4], &e[2 * (x - 4)], &e[2 * (x - 4) + 1]);
-                            e[2 * (x - 4)] = ex2(e[2 * (x - 4)]);
-                            e[2 * (x - 4) + 1] = ex2(e[2 * (x - 4) + 1]);
+                    };
+                    // At most two turns (with far_tile in place of a third): behind a move of m the largest exponent is
+                    // CA_HEAD and the roundings of m, under 1/8 up to CA_FAR.
+                    bool done = false;
+                    for (;;) {
+                        sum2[0] = sum2[1] = 0;
+                        weights(0, true);
+                        const float top = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]);
+                        // the exponent of the row's largest weight, rounded as the weights' are
+                        const float most = fmaf(top, scale, -m);
+                        if (!__any_sync(0xffffffffu, most > CA_TOP || (m == -INFINITY && top > m))) break;
+                        // one row's turn is every row's: an anchor that would have to follow later is set now
+                        const bool grew = most > CA_HEAD;
+                        const float mx = top * scale;
+                        if (!CAP && !BIAS && __any_sync(0xffffffffu, grew && fabsf(mx) > CA_FAR)) {
+                            far_tile();
+                            done = true;
+                            break;
                         }
-                        if (x >= 8) {
-                            const int y = x - 8;
-                            sum2[y & 1] = add2(sum2[y & 1], pair(e[2 * y], e[2 * y + 1]));
-                            p[y] = half2_bits(e[2 * y], e[2 * y + 1]);
-                        }
+                        const float anchor = mx - CA_HEAD;
+                        const float f = grew ? ex2(m - anchor) : 1.0f;
+                        if (grew) m = anchor;
+                        l *= f;
+                        if (j > 0) rescale(f);
                     }
-                };
-                const auto rescale = [&](float f) {
+                    if (done) continue;
+                    hand_over(0);
+                    weights(64, false);
+                    hand_over(64);
+                    float l0, l1;
+                    unpair(add2(sum2[0], sum2[1]), &l0, &l1);
+                    l += l0 + l1;
+                }
+                // ---- this row's output
+                if (nt > 0) bar_wait(&S.abort, a.hdr, &S.o_full[i], outs & 1);
+                if (!aborted(&S.abort)) {
+                    tc_after();
+                    const int64_t out_row = (int64_t)(row0 + tok) * a.H * GQ + h * GQ + r % GQ;
+                    const int64_t part_row = (((int64_t)item * a.H + h) * a.n_splits + split) * CA_ROWS + r;
+                    const float inv = a.n_splits > 1 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
                     for (int c = 0; c < D; c += 32) {
                         uint32_t o[32];
-                        tm_ld32(to + c, o);
+                        if (nt > 0) {
+                            tm_ld32(to + c, o);
+                        } else {
 #pragma unroll
-                        for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                        tm_st32(to + c, o);
-                    }
-                };
-                const auto hand_over = [&](int c) {   // the products start on the first half of the keys
-                    tm_st32(ts + c / 2, p);
-                    tm_wait_st();
-                    tc_before();
-                    __syncwarp();
-                    if (lane == 0) bar_arrive(&S.p_full[i][c / 64]);
-                };
-                // A weight's exponent s * scale - m is rounded once, behind the difference.  That is exact enough until an
-                // fp32 step of m is no longer far below 1: a row's largest weight would be 2^(m's rounding error), 0 or
-                // infinite.  Then the products are rounded like m itself, from S as it still lies in TMEM (an own path,
-                // since a change of s in the loop below costs every prompt 3%).
-                const auto far_tile = [&] {
-                    const auto seen = [&](int c) {
-                        return seen_bits(t0, c >> 5) >> (c & 31) & 1;
-                    };
-                    uint32_t v[32];
-                    float top = -INFINITY;
-                    for (int c = 0; c < 128; c += 32) {
-                        tm_ld32(ts + c, v);
-#pragma unroll
-                        for (int x = 0; x < 32; ++x)
-                            if (seen(c + x)) top = fmaxf(top, __fmul_rn(__uint_as_float(v[x]), scale));
-                    }
-                    const float anchor = fmaxf(m, top - CA_HEAD);
-                    const float f = m == anchor ? 1.0f : ex2(m - anchor);
-                    m = anchor;
-                    l *= f;
-                    if (j > 0) rescale(f);
-                    const float ms = m == -INFINITY ? 0.0f : m;
-                    for (int c = 0; c < 128; c += 64) {
-#pragma unroll
-                        for (int k = 0; k < 64; k += 32) {
-                            tm_ld32(ts + c + k, v);
-#pragma unroll
-                            for (int x = 0; x < 32; x += 2) {
-                                const float e0 = seen(c + k + x) ? ex2(__fmul_rn(__uint_as_float(v[x]), scale) - ms) : 0.0f;
-                                const float e1 = seen(c + k + x + 1) ? ex2(__fmul_rn(__uint_as_float(v[x + 1]), scale) - ms) : 0.0f;
-                                l += e0 + e1;
-                                p[(k + x) / 2] = half2_bits(e0, e1);
-                            }
+                            for (int x = 0; x < 32; ++x) o[x] = 0;
                         }
-                        hand_over(c);
+                        if (!valid) continue;
+                        if (a.n_splits > 1) {
+                            if (nt == 0) continue;
+                            uint4* dst = reinterpret_cast<uint4*>(a.part + part_row * D + c);
+#pragma unroll
+                            for (int x = 0; x < 32; x += 4) dst[x / 4] = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+                        } else {
+                            uint4* dst = reinterpret_cast<uint4*>(a.out + out_row * D + c);
+                            uint32_t w[16];
+#pragma unroll
+                            for (int x = 0; x < 16; ++x)
+                                w[x] = half2_bits(__uint_as_float(o[2 * x]) * inv, __uint_as_float(o[2 * x + 1]) * inv);
+#pragma unroll
+                            for (int x = 0; x < 16; x += 4) dst[x / 4] = make_uint4(w[x], w[x + 1], w[x + 2], w[x + 3]);
+                        }
                     }
-                };
-                // At most two turns (with far_tile in place of a third): behind a move of m the largest exponent is
-                // CA_HEAD and the roundings of m, under 1/8 up to CA_FAR.
-                bool done = false;
-                for (;;) {
-                    sum2[0] = sum2[1] = 0;
-                    weights(0, true);
-                    const float top = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]);
-                    // the exponent of the row's largest weight, rounded as the weights' are
-                    const float most = fmaf(top, scale, -m);
-                    if (!__any_sync(0xffffffffu, most > CA_TOP || (m == -INFINITY && top > m))) break;
-                    // one row's turn is every row's: an anchor that would have to follow later is set now
-                    const bool grew = most > CA_HEAD;
-                    const float mx = top * scale;
-                    if (!CAP && !BIAS && __any_sync(0xffffffffu, grew && fabsf(mx) > CA_FAR)) {
-                        far_tile();
-                        done = true;
-                        break;
-                    }
-                    const float anchor = mx - CA_HEAD;
-                    const float f = grew ? ex2(m - anchor) : 1.0f;
-                    if (grew) m = anchor;
-                    l *= f;
-                    if (j > 0) rescale(f);
+                    if (valid && a.n_splits > 1) a.ml[part_row] = make_float2(m, l);
+                    if (valid && a.n_splits == 1 && a.lse != nullptr)
+                        a.lse[out_row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * KVQ_LN2;
                 }
-                if (done) continue;
-                hand_over(0);
-                weights(64, false);
-                hand_over(64);
-                float l0, l1;
-                unpair(add2(sum2[0], sum2[1]), &l0, &l1);
-                l += l0 + l1;
+                turns += nt, outs += nt > 0;
             }
-            // ---- this row's output
-            if (nt > 0) bar_wait(&S.abort, a.hdr, &S.o_full[i], 0);
-            if (!aborted(&S.abort)) {
-                tc_after();
-                const int64_t out_row = (int64_t)(first + tok0 + tok) * a.H * GQ + h * GQ + r % GQ;
-                const int64_t part_row = (((int64_t)item * a.H + h) * a.n_splits + split) * CA_ROWS + r;
-                const float inv = a.n_splits > 1 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t o[32];
-                    if (nt > 0) {
-                        tm_ld32(to + c, o);
-                    } else {
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) o[x] = 0;
-                    }
-                    if (!valid) continue;
-                    if (a.n_splits > 1) {
-                        if (nt == 0) continue;
-                        uint4* dst = reinterpret_cast<uint4*>(a.part + part_row * D + c);
-#pragma unroll
-                        for (int x = 0; x < 32; x += 4) dst[x / 4] = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
-                    } else {
-                        uint4* dst = reinterpret_cast<uint4*>(a.out + out_row * D + c);
-                        uint32_t w[16];
-#pragma unroll
-                        for (int x = 0; x < 16; ++x)
-                            w[x] = half2_bits(__uint_as_float(o[2 * x]) * inv, __uint_as_float(o[2 * x + 1]) * inv);
-#pragma unroll
-                        for (int x = 0; x < 16; x += 4) dst[x / 4] = make_uint4(w[x], w[x + 1], w[x + 2], w[x + 3]);
-                    }
-                }
-                if (valid && a.n_splits > 1) a.ml[part_row] = make_float2(m, l);
-                if (valid && a.n_splits == 1 && a.lse != nullptr)
-                    a.lse[out_row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * KVQ_LN2;
-            }
+            if (!EXP) break;
+            p0 += 5 * nt;
         }
     }
     __syncwarp();

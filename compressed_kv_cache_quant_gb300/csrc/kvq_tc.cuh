@@ -182,16 +182,17 @@ __device__ __forceinline__ bool bar_done(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-// Waits for a phase of bar.  After KVQ_SPIN polls it flags the timeout, and every wait of the CTA that is
+// Waits for a phase of bar.  After `limit` polls it flags the timeout, and every wait of the CTA that is
 // not over by then returns at once: the roles run through to their ends without waiting, on data that is
 // not valid, so no step needs a branch for the failure; only the loads stop (a barrier must not be armed
 // twice).  Most waits of the issuing warps find their phase done: one poll and nothing else.
-__device__ __forceinline__ void bar_wait(int32_t* abort, KvqWsHeader* hdr, uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ void bar_wait(int32_t* abort, KvqWsHeader* hdr, uint64_t* bar, uint32_t parity,
+                                         uint32_t limit = KVQ_SPIN) {
     const uint32_t at = saddr(bar);
     for (uint32_t it = 0; !bar_done(at, parity); ++it) {
         if ((it & 63) != 63) continue;
         if (*(volatile int32_t*)abort) return;
-        if (it > KVQ_SPIN) {
+        if (it > limit) {
             *(volatile int32_t*)abort = 1;
             kvq_dev_flag(hdr, KVQ_DEV_TIMEOUT, (int32_t)blockIdx.x);
             return;

@@ -149,6 +149,35 @@ def test_expanded_long():
     expanded([3000, 1025], [1500, 1025], 2, seed=2, sample={0, 1, 255, 256, 1499, 1500, 2000, 2524})
 
 
+def test_expanded_many_groups():
+    """More groups of queries than SMs, of one and two tiles in turn and with sequences that have none: a CTA works through
+    several of them."""
+    lens = [(37 * b) % 401 + 1 for b in range(41)] + [900, 0, 128]
+    news = [t if b % 3 else min(t, b % 5) for b, t in enumerate(lens)]
+    rows = sum(news)
+    expanded(lens, news, 16, seed=4, gap=5, sample={0, rows // 3, rows // 2, rows - 129, rows - 1})
+    expanded([2300, 1], [2300, 1], 70, seed=5, sample={0, 1023, 2299, 2300})
+
+
+def test_expanded_runs_alike():
+    """Which CTA takes which group differs from run to run, the results do not."""
+    require_gpu()
+    lens, heads = [700, 129, 2000, 31, 256], 24
+    starts = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    m = sum(lens)
+    kv, lat, q = rnd((m, heads, 2 * D), 1).cuda(), rnd((m, ROW), 2).cuda(), rnd((m, heads, D + ROT), 3).cuda()
+    w = ws(kvq.kv_latent_expanded_attn_ws(len(lens), heads, m, max(lens), max(lens)))
+    first = None
+    for _ in range(20):
+        out = torch.empty((m, heads, D), dtype=torch.float16, device="cuda")
+        lse = torch.empty((m, heads), device="cuda")
+        kvq.kv_latent_expanded_attn(q, kv[..., :D], lat[:, LAT:], kv[..., D:], starts, starts, max(lens), max(lens), out, w, lse=lse)
+        if first is None:
+            first = out, lse
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    kvq.kvq_check(w)
+
+
 def test_expanded_scales():
     for scale in (1e-6, 0.6, 3.0):
         expanded([200], [130], 1, seed=3, scale=scale)
