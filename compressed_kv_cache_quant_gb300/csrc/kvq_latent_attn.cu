@@ -57,12 +57,14 @@ constexpr int LA_STAGE = LA_KEYS / 8 * LA_GROUP;
 constexpr int LA_SMEM = 232448 - 1024;    // dynamic shared memory of a CTA, at most (static: under 1 KB)
 constexpr float LA_HEAD = 7.0f;           // log2 of a row's largest weight when its anchor is set
 constexpr float LA_TOP = 15.99f;          // log2 of the largest weight before the anchor is set anew
+constexpr int LA_WHOLE = 6;                        // steps of a row group that is not cut, at most
 constexpr uint32_t TM_O = 0, TM_S = 256, TM_COLS = 512;   // TMEM columns: O (O^T in four blocks of 64), two S
 
 struct LatArgs {
     const int32_t *bt, *seq_lens, *q_starts, *parents;
     int64_t n_rows, num_blocks;
     int32_t batch, max_blocks, max_len, max_new, H, items;   // items: row groups, at most
+    int32_t whole;                                        // a CTA (or pair) takes one row group, none is cut
     int32_t nr, ns;                                       // rows per CTA as the products see them, a multiple of 16; stages
     float scale2;                                         // of a score, in log2 units
     uint16_t* out;
@@ -129,20 +131,18 @@ struct Segment {
     }
 };
 
-// One warp: the first segment (b = -1: none) of the index-th of `count` CTAs, or pairs of them, and the steps of each.
-// Steps of all sequences are below 2^31.
+// One warp: the first segment (b = -1: none) of the index-th of `count` CTAs, or pairs of them, and the steps of each
+// (where groups are not cut, the index-th group).  Steps of all sequences are below 2^31.
 template <int KEYS>
 __device__ __forceinline__ Segment<KEYS> first_segment(const LatArgs& a, int index, int count, int* per_out) {
     const int lane = threadIdx.x & 31;
     const Seq none = {0, 0, 0, 0, 0};
     const Seq mine = lane < a.batch ? seq_at<KEYS>(a, lane) : none;   // (of the first 32 sequences, kept)
-    int sum = mine.groups * mine.steps;
-    for (int b = lane + 32; b < a.batch; b += 32) {
-        const Seq s = seq_at<KEYS>(a, b);
-        sum += s.groups * s.steps;
-    }
+    const auto share = [&](const Seq& s) { return a.whole ? s.groups : s.groups * s.steps; };
+    int sum = share(mine);
+    for (int b = lane + 32; b < a.batch; b += 32) sum += share(seq_at<KEYS>(a, b));
     const int total = (int)__reduce_add_sync(0xffffffffu, (unsigned)sum);
-    const int per = max(1, (int)((uint32_t)(total + count - 1) / (uint32_t)count));
+    const int per = a.whole ? 1 : max(1, (int)((uint32_t)(total + count - 1) / (uint32_t)count));
     *per_out = per;
     Segment<KEYS> g = {0, 0, 0, -1, 0, 0, 0, 0, 0, none};
     const int64_t x64 = (int64_t)per * index;
@@ -151,7 +151,7 @@ __device__ __forceinline__ Segment<KEYS> first_segment(const LatArgs& a, int ind
     int base = 0, items = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 32) {
         const Seq s = b0 == 0 ? mine : b0 + lane < a.batch ? seq_at<KEYS>(a, b0 + lane) : none;
-        const int steps = s.groups * s.steps;
+        const int steps = share(s);
         int incl = steps, incl_items = s.groups;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -164,10 +164,15 @@ __device__ __forceinline__ Segment<KEYS> first_segment(const LatArgs& a, int ind
             const auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, src); };
             g.s = Seq{of(s.first), of(s.n), of(s.T), of(s.groups), of(s.steps)};
             const uint32_t in = (uint32_t)(x - of(base + incl - steps));
-            g.at = x, g.end_at = min(x + per, total);
             g.b = b0 + src;
-            g.group = (int)(in / (uint32_t)g.s.steps);
-            g.step = (int)in - g.group * g.s.steps;
+            if (a.whole) {
+                g.end_at = g.s.steps;
+                g.group = (int)in;
+            } else {
+                g.at = x, g.end_at = min(x + per, total);
+                g.group = (int)(in / (uint32_t)g.s.steps);
+                g.step = (int)in - g.group * g.s.steps;
+            }
             g.item = of(items + incl_items - s.groups) + g.group;
             g.clip(a);
             return g;
@@ -1106,7 +1111,7 @@ __global__ void __cluster_dims__(LQ, 1, 1) __launch_bounds__(LQ_W * LQ_GR) laten
 }
 
 struct LatPlan {
-    bool pairs;
+    bool pairs, whole;
     int nr, ns, keys, ctas;   // ctas: CTAs, or pairs of them
     int64_t items, steps;   // row groups and steps of the list, at most
     size_t smem, off_ml, off_cuts, off_part, bytes;
@@ -1147,15 +1152,20 @@ LatPlan latent_plan(const kvq_seqs* S, int32_t n_heads, int64_t n_rows, int32_t 
     const int64_t by_max = S->batch * ((most + p.nr - 1) / p.nr);
     p.items = std::max<int64_t>(1, std::min(by_max, n_rows * n_heads / p.nr + S->batch));
     p.keys = p.pairs ? LB_KEYS : LA_KEYS;
-    p.steps = p.items * ((S->max_len + p.keys - 1) / p.keys);
-    p.ctas = (int)std::max<int64_t>(1, std::min<int64_t>({p.steps, p.pairs ? latent_pairs() : kvq_num_sms(), KVQ_LATENT_MAX_CTAS}));
+    const int64_t each = (S->max_len + p.keys - 1) / p.keys;
+    const int at_once = std::min(p.pairs ? latent_pairs() : kvq_num_sms(), KVQ_LATENT_MAX_CTAS);
+    p.steps = p.items * each;
+    // Few steps per row group: one CTA takes them all, since parts and their join cost more (12 sequences of 53-69 tokens, 60
+    // rows each 14.1 -> 10.1 us, four of 200-300, 128 rows 16.3 -> 12.5; seven steps of 16 rows 10.7 in parts, 13.7 in one).
+    p.whole = p.items <= at_once && each <= LA_WHOLE;
+    p.ctas = (int)std::max<int64_t>(1, p.whole ? p.items : std::min<int64_t>(p.steps, at_once));
     const size_t fixed = 1024 + (size_t)p.nr * (ROW * 2 + 2 * 128);
     p.ns = p.pairs ? LB_NS : (int)std::min<size_t>((LA_SMEM - fixed) / LA_STAGE, LA_MAX_NS);
     p.smem = p.pairs ? LB_SMEM : fixed + p.ns * LA_STAGE;
-    const size_t rows = (size_t)2 * p.ctas * p.nr;
+    const size_t rows = p.whole ? 0 : (size_t)2 * p.ctas * p.nr;
     p.off_ml = sizeof(KvqWsHeader);
     p.off_cuts = kvq_round_up(p.off_ml + rows * sizeof(float2), 256);
-    p.off_part = kvq_round_up(p.off_cuts + (size_t)p.items * p.nr * sizeof(int4), 256);
+    p.off_part = kvq_round_up(p.off_cuts + (p.whole ? 0 : (size_t)p.items * p.nr * sizeof(int4)), 256);
     p.bytes = kvq_round_up(p.off_part + rows * LAT * sizeof(float), 256);
     return p;
 }
@@ -1200,7 +1210,7 @@ extern "C" int kv_latent_attn(const kvq_latent* C, const kvq_seqs* S, int32_t n_
     if (st) return st;
     a.bt = S->block_table, a.seq_lens = S->seq_lens, a.q_starts = q_starts, a.parents = parents;
     a.n_rows = n_rows, a.num_blocks = C->num_blocks;
-    a.batch = S->batch, a.max_blocks = S->max_blocks, a.max_len = S->max_len, a.max_new = max_new, a.H = n_heads, a.nr = p.nr, a.ns = p.ns, a.items = (int)p.items;
+    a.batch = S->batch, a.max_blocks = S->max_blocks, a.max_len = S->max_len, a.max_new = max_new, a.H = n_heads, a.whole = p.whole, a.nr = p.nr, a.ns = p.ns, a.items = (int)p.items;
     a.out = out, a.lse = lse, a.hdr = static_cast<KvqWsHeader*>(ws);
     a.ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + p.off_ml);
     a.cuts = reinterpret_cast<int4*>(static_cast<char*>(ws) + p.off_cuts);
@@ -1213,9 +1223,12 @@ extern "C" int kv_latent_attn(const kvq_latent* C, const kvq_seqs* S, int32_t n_
                             : kvq_launch_pdl(latent_attn_kernel, dim3(p.ctas), dim3(LA_NT), p.smem, kvq_stream(stream), map_q,
                                              map_rows, a);
     if (e != cudaSuccess) return kvq_fail(KVQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
-    if (p.ctas == 1) return KVQ_OK;
+    if (p.whole || p.ctas == 1) return KVQ_OK;
     const int64_t group_rows = p.items * p.nr;
-    e = group_rows <= 128 && p.ctas > 6
+    // A cluster per row where rows are few and parts many: 10 sequences of 2000 tokens, 160 rows in 15 parts, 17.9 us, with a
+    // warp per row 20.2; 14 of them, 224 rows in 11 parts, 25.3 and 23.4.
+    const bool wide = p.ctas > 6 && (group_rows <= 128 || (group_rows <= 256 && p.ctas >= 12 * p.items));
+    e = wide
             ? kvq_launch_pdl(latent_join_wide_kernel, dim3((unsigned)group_rows * LQ), dim3(LQ_W * LQ_GR), 0, kvq_stream(stream), a)
             : kvq_launch_pdl(latent_join_kernel, dim3((unsigned)((group_rows + LJ_NW - 1) / LJ_NW)), dim3(32 * LJ_NW), 0,
                              kvq_stream(stream), a, (int)group_rows);

@@ -89,6 +89,30 @@ def test_absorbed_long_and_ragged():
     absorbed([4097, 800], [2, 1], 128, seed=5, sample={1, 2})
 
 
+@pytest.mark.parametrize("lens,news,heads", [
+    ([288, 1, 287], [1, 1, 1], 16),        # six steps of 48 tokens: not cut; one token more: cut
+    ([289, 1, 287], [1, 1, 1], 16),
+    ([384, 5, 129], [2, 2, 1], 64),        # six steps of 64 for more than 32 rows
+    ([385, 5, 129], [2, 2, 1], 64),
+    ([96] * 200, [1] * 200, 1),            # more row groups than SMs
+    ([200, 0, 150], [1, 0, 2], 16),
+])
+def test_absorbed_short(lens, news, heads):
+    absorbed(lens, news, heads, seed=7)
+
+
+def test_absorbed_short_tree():
+    absorbed([130, 288, 60], [25, 7, 1], 2, "random", seed=8)
+
+
+def test_absorbed_joins():
+    """Parts joined by a cluster per row and by a warp per row, up to 256 rows of row groups and beyond."""
+    absorbed([1119, 900, 182, 600, 700, 333, 800, 1000, 450], [1] * 9, 12, seed=9, sample={0, 2, 8})
+    absorbed([700] * 14, [1] * 14, 16, seed=10, sample={0, 13})
+    absorbed([3000, 2000], [1, 1], 128, seed=11, sample={0, 1})
+    absorbed([1500] * 17, [1] * 17, 16, seed=12, sample={0, 16})
+
+
 def test_absorbed_scores_of_every_size():
     """Flat, sharp and far scores."""
     for s, scale in ((0.01, 0.0), (8.0, 0.0), (30.0, 0.5), (1.0, 1e-6)):
