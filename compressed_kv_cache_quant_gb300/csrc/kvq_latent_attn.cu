@@ -1158,14 +1158,15 @@ LatPlan latent_plan(const kvq_seqs* S, int32_t n_heads, int64_t n_rows, int32_t 
     // Few steps per row group: one CTA takes them all, since parts and their join cost more (12 sequences of 53-69 tokens, 60
     // rows each 14.1 -> 10.1 us, four of 200-300, 128 rows 16.3 -> 12.5; seven steps of 16 rows 10.7 in parts, 13.7 in one).
     p.whole = p.items <= at_once && each <= LA_WHOLE;
-    p.ctas = (int)std::max<int64_t>(1, p.whole ? p.items : std::min<int64_t>(p.steps, at_once));
+    const int64_t cut = std::max<int64_t>(1, std::min<int64_t>(p.steps, at_once));
+    p.ctas = (int)(p.whole ? p.items : cut);
     const size_t fixed = 1024 + (size_t)p.nr * (ROW * 2 + 2 * 128);
     p.ns = p.pairs ? LB_NS : (int)std::min<size_t>((LA_SMEM - fixed) / LA_STAGE, LA_MAX_NS);
     p.smem = p.pairs ? LB_SMEM : fixed + p.ns * LA_STAGE;
-    const size_t rows = p.whole ? 0 : (size_t)2 * p.ctas * p.nr;
+    const size_t rows = (size_t)2 * cut * p.nr;   // (of either kind, so that a workspace serves every shorter max_len)
     p.off_ml = sizeof(KvqWsHeader);
     p.off_cuts = kvq_round_up(p.off_ml + rows * sizeof(float2), 256);
-    p.off_part = kvq_round_up(p.off_cuts + (p.whole ? 0 : (size_t)p.items * p.nr * sizeof(int4)), 256);
+    p.off_part = kvq_round_up(p.off_cuts + (size_t)p.items * p.nr * sizeof(int4), 256);
     p.bytes = kvq_round_up(p.off_part + rows * LAT * sizeof(float), 256);
     return p;
 }
