@@ -216,6 +216,8 @@ __global__ void __launch_bounds__(CA_NT, 1)
     __shared__ Shared S;
     __shared__ int4 seen_of[EXP ? 1 : CA_ROWS];   // lo, hi, doc, sink of every token
     __shared__ std::conditional_t<TREE, KvqTree, int> tree;
+    // places of the columns from the first node's tile on, less ctx
+    __shared__ __align__(16) float place_of[TREE && BIAS ? KVQ_TREE_MAX + CA_KEYS : 4];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int GQ = a.GQ, tpc = CA_ROWS / GQ;
     const auto place = [&](int x, int* h, int* item) {
@@ -253,6 +255,10 @@ __global__ void __launch_bounds__(CA_NT, 1)
         __syncthreads();
         if (tid < n) kvq_tree_walk(tree, tid, ctx & 31);
         __syncthreads();   // (of the nodes' paths a row reads its own, of their depths all)
+        if (BIAS && tid < KVQ_TREE_MAX + CA_KEYS) {
+            const int k = tid - ctx % CA_KEYS;
+            place_of[tid] = (float)(k < 0 ? k : k < n ? (int)tree.depth[k] : 0);
+        }
     }
     if (!EXP && tid < ntok) {
         const int i = tok0 + tid;
@@ -711,11 +717,15 @@ __global__ void __launch_bounds__(CA_NT, 1)
                         if constexpr (TREE) {
                             nodes = t0 + CA_KEYS > ctx;
                             if (nodes) {
+                                const float depth = (float)(pos - ctx);
+                                const float4* at = reinterpret_cast<const float4*>(place_of + (t0 - ctx / CA_KEYS * CA_KEYS));
 #pragma unroll
-                                for (int c = 0; c < 128; ++c) {
-                                    const int k = t0 + c - ctx;
-                                    const int at = k < 0 ? t0 + c : k < n ? ctx + tree.depth[k] : pos;
-                                    s[c] = fmaf(s[c], mul, -slope2 * fabsf((float)(pos - at)));
+                                for (int c = 0; c < 128; c += 4) {
+                                    const float4 p = at[c / 4];
+                                    s[c] = fmaf(s[c], mul, -slope2 * fabsf(depth - p.x));
+                                    s[c + 1] = fmaf(s[c + 1], mul, -slope2 * fabsf(depth - p.y));
+                                    s[c + 2] = fmaf(s[c + 2], mul, -slope2 * fabsf(depth - p.z));
+                                    s[c + 3] = fmaf(s[c + 3], mul, -slope2 * fabsf(depth - p.w));
                                 }
                             }
                         }
@@ -896,7 +906,7 @@ __global__ void __launch_bounds__(CA_NT, 1)
                             for (int x = 0; x < 16; x += 8) store8(a.out + out_row * D + c + 2 * x, w + x, wide);
                         }
                     }
-                    if (valid && a.n_splits > 1) a.ml[part_row] = make_float2(m, l);
+                    if (valid && a.n_splits > 1 && nt > 0) a.ml[part_row] = make_float2(m, l);
                     if (valid && a.n_splits == 1 && a.lse != nullptr)
                         a.lse[out_row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * KVQ_LN2;
                 }
@@ -918,8 +928,12 @@ __global__ void __launch_bounds__(CA_NT, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TM_COLS) : "memory");
 }
 
-// Joins the splits of an item's rows, a warp per row, in their order, and leaves the workspace zeroed.
-constexpr int CJ_NW = 8;
+// Joins the splits of an item's rows, a warp per row, in their order, and leaves the workspace zeroed.  A split without a
+// tile wrote nothing, one without a visible token a sum of 0.  MANY: the splits that wrote are found first and their rows
+// fetched sixteen at a time (a tree of 25 nodes in 16 splits 20.0 -> 18.8 us, a window of six tokens in 38 splits 61 -> 20);
+// with few splits that takes longer than reading all of them (64 nodes in two splits 219 -> 235 us).
+constexpr int CJ_NW = 8, CJ_MANY = 8, CJ_G = 16;
+template <bool MANY>
 __global__ void __launch_bounds__(32 * CJ_NW) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
     __shared__ int item[4];   // its sequence, first new token, the sequence's first row, rows of the item
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -940,29 +954,63 @@ __global__ void __launch_bounds__(32 * CJ_NW) chunk_join_kernel(const __grid_con
     if (item[0] < 0 || r >= item[3]) return;
     const int tok = item[1], first = item[2];
     const int64_t p0 = ((int64_t)blockIdx.x * a.H + h) * a.n_splits * CA_ROWS + r;
-    float mx = -INFINITY;
-    for (int s = lane; s < a.n_splits; s += 32) mx = fmaxf(mx, a.ml[p0 + (int64_t)s * CA_ROWS].x);
+    const auto ml_at = [&](int s) { return a.ml + p0 + (int64_t)s * CA_ROWS; };
+    float2 mine = lane < a.n_splits ? *ml_at(lane) : make_float2(0.0f, 0.0f);
+    float mx = mine.y != 0.0f ? mine.x : -INFINITY;
+    for (int s = lane + 32; s < a.n_splits; s += 32) {
+        const float2 v = *ml_at(s);
+        if (v.y != 0.0f) mx = fmaxf(mx, v.x);
+    }
     mx = kvq_warp_max(mx);
     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float y = 0.0f;
+    if constexpr (MANY) {
+        for (int s0 = 0; s0 < a.n_splits; s0 += 32) {
+            if (s0 > 0) mine = s0 + lane < a.n_splits ? *ml_at(s0 + lane) : make_float2(0.0f, 0.0f);
+            const unsigned some = __ballot_sync(0xffffffffu, mine.y != 0.0f);
+            const unsigned written = __ballot_sync(0xffffffffu, mine.x != 0.0f || mine.y != 0.0f);
+            if (mine.x != 0.0f || mine.y != 0.0f) *ml_at(s0 + lane) = make_float2(0.0f, 0.0f);
+            const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int g = 0; g < 32 && written >> g; g += CJ_G) {
+                float4* const part = reinterpret_cast<float4*>(a.part + (p0 + (int64_t)(s0 + g) * CA_ROWS) * D) + lane;
+                float4 w[CJ_G];
+#pragma unroll
+                for (int k = 0; k < CJ_G; ++k) w[k] = some >> (g + k) & 1 ? part[k * CA_ROWS * (D / 4)] : zero;
+#pragma unroll
+                for (int k = 0; k < CJ_G; ++k)
+                    if (written >> (g + k) & 1) part[k * CA_ROWS * (D / 4)] = zero;
+#pragma unroll
+                for (int k = 0; k < CJ_G; ++k) {
+                    const float2 v = make_float2(__shfl_sync(0xffffffffu, mine.x, g + k), __shfl_sync(0xffffffffu, mine.y, g + k));
+                    const bool one = some >> (g + k) & 1;
+                    const float f = one ? exp2f(v.x - mx) : 0.0f;
+                    x.x += one ? f * w[k].x : 0.0f;
+                    x.y += one ? f * w[k].y : 0.0f;
+                    x.z += one ? f * w[k].z : 0.0f;
+                    x.w += one ? f * w[k].w : 0.0f;
+                    y += f * v.y;
+                }
+            }
+        }
+    } else {
 #pragma unroll 8
-    for (int s = 0; s < a.n_splits; ++s) {
-        const int64_t row = p0 + (int64_t)s * CA_ROWS;
-        const float2 v = a.ml[row];
-        const float4 w = reinterpret_cast<const float4*>(a.part + row * D)[lane];
-        const bool some = v.y != 0.0f;   // (a split without a visible token wrote no row)
-        const float f = some ? exp2f(v.x - mx) : 0.0f;
-        x.x += some ? f * w.x : 0.0f;
-        x.y += some ? f * w.y : 0.0f;
-        x.z += some ? f * w.z : 0.0f;
-        x.w += some ? f * w.w : 0.0f;
-        y += f * v.y;
+        for (int s = 0; s < a.n_splits; ++s) {
+            const float2 v = *ml_at(s);
+            const float4 w = reinterpret_cast<const float4*>(a.part + (p0 + (int64_t)s * CA_ROWS) * D)[lane];
+            const bool some = v.y != 0.0f;
+            const float f = some ? exp2f(v.x - mx) : 0.0f;
+            x.x += some ? f * w.x : 0.0f;
+            x.y += some ? f * w.y : 0.0f;
+            x.z += some ? f * w.z : 0.0f;
+            x.w += some ? f * w.w : 0.0f;
+            y += f * v.y;
+        }
+        // (behind the loads: a store between them would hold up the next one)
+        for (int s = 0; s < a.n_splits; ++s)
+            reinterpret_cast<float4*>(a.part + (p0 + (int64_t)s * CA_ROWS) * D)[lane] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        __syncwarp();
+        for (int s = lane; s < a.n_splits; s += 32) *ml_at(s) = make_float2(0.0f, 0.0f);
     }
-    // (behind the loads: a store between them would hold up the next one)
-    for (int s = 0; s < a.n_splits; ++s)
-        reinterpret_cast<float4*>(a.part + (p0 + (int64_t)s * CA_ROWS) * D)[lane] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    __syncwarp();
-    for (int s = lane; s < a.n_splits; s += 32) a.ml[p0 + (int64_t)s * CA_ROWS] = make_float2(0.0f, 0.0f);
     const float inv = y == 0.0f ? 0.0f : 1.0f / y;
     const int64_t out_row = (int64_t)(first + tok + r / GQ) * a.H * GQ + h * GQ + r % GQ;
     reinterpret_cast<uint2*>(a.out + out_row * D)[lane] =
@@ -1046,7 +1094,8 @@ int launch_chunk(Kernel kernel, int smem, const ChunkPlan& p, ChunkArgs& a, cons
     cudaError_t e = kvq_launch_pdl(kernel, dim3((unsigned)(p.items * a.H), p.n_splits), dim3(CA_NT), smem, stream, map_q, map_k,
                                    map_v, map_r, a);
     if (e == cudaSuccess && p.n_splits > 1)
-        e = kvq_launch_pdl(chunk_join_kernel, dim3((unsigned)p.items, a.H, CA_ROWS / CJ_NW), dim3(32 * CJ_NW), 0, stream, a);
+        e = kvq_launch_pdl(p.n_splits > CJ_MANY ? chunk_join_kernel<true> : chunk_join_kernel<false>,
+                           dim3((unsigned)p.items, a.H, CA_ROWS / CJ_NW), dim3(32 * CJ_NW), 0, stream, a);
     if (e != cudaSuccess) return kvq_fail(KVQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
     return KVQ_OK;
 }

@@ -119,6 +119,13 @@ def test_long_split_contexts(mod):
     check([9001, 4096], [64, 7], 8, 2, "random", mod, seed=3, sample={0, 31, 63, 64, 70})
 
 
+@pytest.mark.parametrize("mod", ["plain", "bias", "window", "window_one_sink", "docs_window_sink_bias"])
+def test_many_parts(mod):
+    """One or two row groups and long contexts: dozens of parts, of which a window or a document leaves few."""
+    check([9001], [30], 8, 1, "random", mod, seed=4, sample={0, 13, 29})
+    check([20000, 77], [8, 2], 8, 1, "binary", mod, seed=5, sample={7, 9})
+
+
 def test_chain_is_kv_chunk_attn():
     """A chain is the causal run: the same bits, where both take the cache whole."""
     require_gpu()
