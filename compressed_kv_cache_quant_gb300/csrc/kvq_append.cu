@@ -127,12 +127,14 @@ __global__ void __launch_bounds__(AP_NT) rope_append_kernel(const __grid_constan
 }
 
 // The same into an fp16 layer with a channel-major copy of its keys and their channels' maxima.  A CTA takes the new
-// tokens of eight places of a sequence (0 .. 7 modulo 8), so that a channel's values are one 16-byte piece of the copy:
-// queries and values as above, then the keys, SC_HEADS heads at a time, which are written to their pages and, through
-// shared memory, to the copy.  (As a second launch over the rows just written: 32 us for 4097 tokens of 32 + 8 + 8 heads.)
-constexpr int SC_TOK = 8, SC_HEADS = 16;
+// tokens of eight places of a sequence (0 .. 7 modulo 8), so that a channel's values are one 16-byte piece of the copy, and
+// up to SC_HEADS key heads with their part of the queries and values: first those as above, then the keys, which are
+// written to their pages and, through shared memory, to the copy.  A row is on its way while the one before is turned.  (As a
+// second launch over the rows just written: 32 us for 4097 tokens of 32 + 8 + 8 heads, here 23; with all heads in one CTA
+// 3.5K tokens of 40 + 40 + 40 heads took 94 instead of 63 us.)
+constexpr int SC_TOK = 8, SC_HEADS = 8;
 template <typename T, bool INTER>
-__global__ void __launch_bounds__(AP_NT) rope_append_scored_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(AP_NT, 4) rope_append_scored_kernel(const __grid_constant__ AppendArgs a, int heads) {
     __shared__ __align__(16) float2 cs[SC_TOK][D / 2];
     __shared__ __align__(16) float wt[2][D];
     __shared__ __align__(16) uint16_t keys[SC_HEADS][SC_TOK][D];
@@ -183,15 +185,34 @@ __global__ void __launch_bounds__(AP_NT) rope_append_scored_kernel(const __grid_
     __syncthreads();
     // (the rows here share a page)
     const auto row_at = [&](int g, int k) { return (((int64_t)page * a.H + g) * PG + place % PG + k) * D; };
-    // queries and values
-    for (int i = grp; i < nt * (a.Hq + a.H); i += AP_NT / 8) {
-        const int k = i / (a.Hq + a.H), h = i - k * (a.Hq + a.H);
+    const int g0 = blockIdx.y * heads, ng = min(heads, a.H - g0);   // this CTA's key heads
+    uint4 kx4, ky4;
+    const auto fetch_key = [&](int i) {
+        const int k = i / ng, g = i - k * ng;
+        const T* src = static_cast<const T*>(a.k) + (r0 + k) * a.k_stride + (int64_t)(g0 + g) * D;
+        kx4 = *reinterpret_cast<const uint4*>(src + 8 * ca);
+        ky4 = *reinterpret_cast<const uint4*>(src + 8 * cb);
+    };
+    if (grp < nt * ng) fetch_key(grp);
+    // its queries and values, the next row on its way
+    const int share = (a.Hq + a.H + gridDim.y - 1) / gridDim.y, h0 = blockIdx.y * share, nh = min(share, a.Hq + a.H - h0);
+    uint4 x4, y4;
+    const auto fetch = [&](int i) {
+        const int k = i / nh, h = h0 + i - k * nh;
+        const T* src = h < a.Hq ? static_cast<const T*>(a.q) + (r0 + k) * a.q_stride + (int64_t)h * D
+                                : static_cast<const T*>(a.v) + (r0 + k) * a.v_stride + (int64_t)(h - a.Hq) * D;
+        x4 = *reinterpret_cast<const uint4*>(src + 8 * ca);
+        y4 = *reinterpret_cast<const uint4*>(src + 8 * cb);
+    };
+    const int n_rows = nt * max(nh, 0);
+    if (grp < n_rows) fetch(grp);
+    for (int i = grp; i < n_rows; i += AP_NT / 8) {
+        const int k = i / nh, h = h0 + i - k * nh;
         const bool is_q = h < a.Hq;
-        const T* src = is_q ? static_cast<const T*>(a.q) + (r0 + k) * a.q_stride + (int64_t)h * D
-                            : static_cast<const T*>(a.v) + (r0 + k) * a.v_stride + (int64_t)(h - a.Hq) * D;
         float x[8], y[8];
-        unpack(*reinterpret_cast<const uint4*>(src + 8 * ca), x, (T*)nullptr);
-        unpack(*reinterpret_cast<const uint4*>(src + 8 * cb), y, (T*)nullptr);
+        unpack(x4, x, (T*)nullptr);
+        unpack(y4, y, (T*)nullptr);
+        if (i + AP_NT / 8 < n_rows) fetch(i + AP_NT / 8);
         uint16_t* dst;
         if (is_q) {
             if (a.qw != nullptr) norm_row(x, y, wt[0], ca, cb, a.eps);
@@ -206,48 +227,44 @@ __global__ void __launch_bounds__(AP_NT) rope_append_scored_kernel(const __grid_
     }
     if (page < 0) return;
     // keys
-    for (int g0 = 0; g0 < a.H; g0 += SC_HEADS) {
-        const int ng = min(SC_HEADS, a.H - g0);
-        for (int i = grp; i < nt * ng; i += AP_NT / 8) {
-            const int k = i / ng, g = i - k * ng;
-            const T* src = static_cast<const T*>(a.k) + (r0 + k) * a.k_stride + (int64_t)(g0 + g) * D;
-            float x[8], y[8];
-            unpack(*reinterpret_cast<const uint4*>(src + 8 * ca), x, (T*)nullptr);
-            unpack(*reinterpret_cast<const uint4*>(src + 8 * cb), y, (T*)nullptr);
-            if (a.kw != nullptr) norm_row(x, y, wt[1], ca, cb, a.eps);
-            turn_row<INTER>(x, y, cs[k], l, ca, cb, a.rot);
-            const uint4 u = pack_half(x), v = pack_half(y);
-            uint16_t* dst = static_cast<uint16_t*>(a.k_pages) + row_at(g0 + g, k);
-            *reinterpret_cast<uint4*>(dst + 8 * ca) = u;
-            *reinterpret_cast<uint4*>(dst + 8 * cb) = v;
-            *reinterpret_cast<uint4*>(&keys[g][k][8 * ca]) = u;
-            *reinterpret_cast<uint4*>(&keys[g][k][8 * cb]) = v;
-        }
-        __syncthreads();
-        for (int i = tid; i < ng * D; i += AP_NT) {
-            const int g = i / D, c = i % D;
-            const int64_t ch = ((int64_t)b * a.H + g0 + g) * D + c;
-            const float so_far = a.k_absmax[ch];
-            __align__(16) uint16_t w[SC_TOK];
-            float top = 0.0f;
+    for (int i = grp; i < nt * ng; i += AP_NT / 8) {
+        const int k = i / ng, g = i - k * ng;
+        float x[8], y[8];
+        unpack(kx4, x, (T*)nullptr);
+        unpack(ky4, y, (T*)nullptr);
+        if (i + AP_NT / 8 < nt * ng) fetch_key(i + AP_NT / 8);
+        if (a.kw != nullptr) norm_row(x, y, wt[1], ca, cb, a.eps);
+        turn_row<INTER>(x, y, cs[k], l, ca, cb, a.rot);
+        const uint4 u = pack_half(x), v = pack_half(y);
+        uint16_t* dst = static_cast<uint16_t*>(a.k_pages) + row_at(g0 + g, k);
+        *reinterpret_cast<uint4*>(dst + 8 * ca) = u;
+        *reinterpret_cast<uint4*>(dst + 8 * cb) = v;
+        *reinterpret_cast<uint4*>(&keys[g][k][8 * ca]) = u;
+        *reinterpret_cast<uint4*>(&keys[g][k][8 * cb]) = v;
+    }
+    __syncthreads();
+    for (int i = tid; i < ng * D; i += AP_NT) {
+        const int g = i / D, c = i % D;
+        const int64_t ch = ((int64_t)b * a.H + g0 + g) * D + c;
+        const float so_far = a.k_absmax[ch];
+        __align__(16) uint16_t w[SC_TOK];
+        float top = 0.0f;
 #pragma unroll
-            for (int k = 0; k < SC_TOK; ++k) {
-                w[k] = k < nt ? keys[g][k][c] : (uint16_t)0;
-                top = fmaxf(top, fabsf(kvq_h2f(w[k])));
-            }
-            uint16_t* dst = a.kT + ch * a.t_cap + place;
-            if (nt == SC_TOK) {
-                *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(w);
-            } else {
-#pragma unroll
-                for (int k = 0; k < SC_TOK; ++k)
-                    if (k < nt) dst[k] = w[k];
-            }
-            // (maxima are not negative, so their bits are ordered as integers; the order of arrival does not matter, and a
-            // maximum only grows: most CTAs find theirs passed already)
-            if (top > so_far) atomicMax(reinterpret_cast<int*>(a.k_absmax + ch), __float_as_int(top));
+        for (int k = 0; k < SC_TOK; ++k) {
+            w[k] = k < nt ? keys[g][k][c] : (uint16_t)0;
+            top = fmaxf(top, fabsf(kvq_h2f(w[k])));
         }
-        __syncthreads();
+        uint16_t* dst = a.kT + ch * a.t_cap + place;
+        if (nt == SC_TOK) {
+            *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(w);
+        } else {
+#pragma unroll
+            for (int k = 0; k < SC_TOK; ++k)
+                if (k < nt) dst[k] = w[k];
+        }
+        // (maxima are not negative, so their bits are ordered as integers; the order of arrival does not matter, and a
+        // maximum only grows: most CTAs find theirs passed already)
+        if (top > so_far) atomicMax(reinterpret_cast<int*>(a.k_absmax + ch), __float_as_int(top));
     }
 }
 
@@ -431,8 +448,12 @@ extern "C" int kv_rope_append(const kvq_layout* L, const kvq_pool* P, const kvq_
         // n new tokens of a sequence touch at most n / 8 + 2 groups of eight places
         const int64_t tiles = n_rows / SC_TOK + 2 * (int64_t)S->batch;
         KVQ_REQUIRE(tiles <= INT32_MAX, KVQ_ERR_UNSUPPORTED, "%s: batch", fn);
+        // Fewer key heads per CTA while CTAs are few: 1820 tokens of 8 heads, 230 groups, 13 us by four and 17 by eight;
+        // 8192 tokens of 32 heads, 1026 groups, 120 and 108 (98 with four CTAs per SM).
+        const int heads = tiles * ((a.H + SC_HEADS - 1) / SC_HEADS) >= 3 * (int64_t)kvq_num_sms() ? SC_HEADS : SC_HEADS / 2;
         const auto go = [&](auto kernel) {
-            return launched(kvq_launch_pdl(kernel, dim3((unsigned)tiles), dim3(AP_NT), 0, kvq_stream(stream), a));
+            return launched(kvq_launch_pdl(kernel, dim3((unsigned)tiles, (a.H + heads - 1) / heads), dim3(AP_NT), 0,
+                                           kvq_stream(stream), a, heads));
         };
         if (dtype == KVQ_F16)
             return rope->interleaved ? go(rope_append_scored_kernel<__half, true>) : go(rope_append_scored_kernel<__half, false>);

@@ -104,6 +104,18 @@ def test_rope_append(lens, news, hq, hkv, dt, cache, norm, rot, inter):
             assert torch.equal(top[b], want)
 
 
+@pytest.mark.parametrize("lens,news,hq,hkv,dt,norm,rot,inter", [
+    ([50], [9], 24, 12, torch.bfloat16, True, 128, True),
+    ([100, 7], [100, 1], 10, 5, torch.float16, False, 64, False),
+    ([800, 33], [790, 20], 40, 40, torch.bfloat16, True, 96, False),
+    ([33] * 40, [1] * 40, 32, 8, torch.float16, True, 128, False),
+    ([4], [4], 1, 1, torch.float16, False, 0, True),
+])
+def test_scored_layers_by_heads(lens, news, hq, hkv, dt, norm, rot, inter):
+    """A scored layer's key heads spread over several CTAs, by four and by eight, the last ones fewer."""
+    test_rope_append(lens, news, hq, hkv, dt, "scored", norm, rot, inter)
+
+
 def test_append_agrees_with_the_calls_it_replaces():
     """The same bits as kv_qk_norm_rope followed by kv_quant_pack (fp16), one token at a time included."""
     require_gpu()
