@@ -8,7 +8,7 @@
 // rounded once, from fp32 to the cache's type.
 //
 // Measured (in a graph): two prompts of 16001 and 16384 tokens, bf16, normed, 32 + 8 + 8 heads into E4M3 pages 121 us,
-// 6.0 TB/s (89% of the copy rate); 16385 latent rows with the rotated part of 16 heads 24 us, 4.3 TB/s, where 3.4 waves of
+// 6.0 TB/s (89% of the copy rate); 16385 latent rows with the rotated part of 16 heads 23 us, 4.5 TB/s, where 3.4 waves of
 // CTAs each begin with the chain of lookups; one token of 16 sequences 3 us.  More loads per lane cost CTAs per SM and
 // more time (24 -> 34 us with four head rows on their way).
 #include <algorithm>

@@ -25,7 +25,8 @@
 // More query rows: pairs of CTAs, further below.
 //
 // The steps of all sequences and row groups are one list, cut into equal ranges, one per SM (or pair): a CTA works
-// through its range segment by segment, and a second launch joins the row groups that a cut runs through.  Weights are
+// through its range segment by segment, and a second launch joins the row groups that a cut runs through (groups of a few
+// steps are left whole).  Weights are
 // taken against an anchor per row as in kv_chunk_attn: 2^7 below the row's maximum when it is set, set anew (O rescaled)
 // when a weight would pass 2^15.99; their exponents are differences of rounded products, so that far scores stay exact
 // enough.
@@ -57,8 +58,9 @@ constexpr int LA_STAGE = LA_KEYS / 8 * LA_GROUP;
 constexpr int LA_SMEM = 232448 - 1024;    // dynamic shared memory of a CTA, at most (static: under 1 KB)
 constexpr float LA_HEAD = 7.0f;           // log2 of a row's largest weight when its anchor is set
 constexpr float LA_TOP = 15.99f;          // log2 of the largest weight before the anchor is set anew
-constexpr int LA_WHOLE = 6;                        // steps of a row group that is not cut, at most
-constexpr uint32_t TM_O = 0, TM_S = 256, TM_COLS = 512;   // TMEM columns: O (O^T in four blocks of 64), two S
+constexpr int LA_WHOLE = 6;               // steps of a row group that is not cut, at most
+// TMEM columns: O (O^T in four blocks of 64), two S.  All of them are the CTA's, so they start at column 0.
+constexpr uint32_t TM_O = 0, TM_S = 256, TM_COLS = 512;
 
 struct LatArgs {
     const int32_t *bt, *seq_lens, *q_starts, *parents;
@@ -353,64 +355,64 @@ __global__ void __launch_bounds__(LA_NT, 1)
     } else if (warp == 4) {
         // ---- tensor cores: one lane walks the loop (elected anew for every batch, it starts some 100 cycles later)
         if (elect()) {
-        const uint32_t hi_q = (uint32_t)(smem_desc(0, 16, 1024) >> 32), hi_kv = (uint32_t)(smem_desc(0, 16, LA_GROUP) >> 32);
-        const uint32_t lq = (uint32_t)smem_desc(sq, 16, 0), lk = (uint32_t)smem_desc(skv, 16, 0),
-                       lv = (uint32_t)smem_desc(skv, 1024, 0), lp = (uint32_t)smem_desc(sp, 16, 0);
-        const uint32_t idesc_s = idesc_f16(64, LA_KEYS), idesc_o = idesc_f16(128, a.nr) | KVQ_A_MN;
-        const auto desc = [](uint32_t hi, uint32_t lo) { return (uint64_t)hi << 32 | lo; };
-        const uint32_t q_chunk = (uint32_t)a.nr * 128 >> 4;
-        Place in, s, out, p;   // stage and S of the next first product, stage and P of the next second one
-        const auto qk = [&] {
-            bar_wait(&S.abort, a.hdr, &S.kv_full[in.i], in.round);
-            tc_after();
-            {
-                uint32_t x = lq, y = lk + (in.i * LA_STAGE >> 4);
-                asm volatile("" : "+r"(x), "+r"(y));
-#pragma unroll
-                for (int c = 0; c < LA_CHUNKS; ++c) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_ss(TM_S + s.i * LA_KEYS, desc(hi_q, x + 2 * k), desc(hi_kv, y + (c * 1024 >> 4) + 2 * k), idesc_s, c + k > 0);
-                    x += q_chunk;
-                }
-                // (all products so far: where S is there, so is O^T of two steps before, and P's place is free)
-                tc_commit(&S.s_full[s.i]);
-            }
-            in.next(a.ns);
-            s.next(2);
-        };
-        for (int seg = 0;;) {
-            const int nt = g.nt;
-            if (nt > 0) {
-                bar_wait(&S.abort, a.hdr, &S.q_full, seg & 1);
-                ++seg;
-                qk();
-                if (nt == 1) tc_commit(&S.q_free);
-            }
-            for (int j = 0; j < nt; ++j) {
-                if (j + 1 < nt) {
-                    qk();
-                    if (j + 2 == nt) tc_commit(&S.q_free);
-                }
-                bar_wait(&S.abort, a.hdr, &S.p_full[p.i], p.round);
+            const uint32_t hi_q = (uint32_t)(smem_desc(0, 16, 1024) >> 32), hi_kv = (uint32_t)(smem_desc(0, 16, LA_GROUP) >> 32);
+            const uint32_t lq = (uint32_t)smem_desc(sq, 16, 0), lk = (uint32_t)smem_desc(skv, 16, 0),
+                           lv = (uint32_t)smem_desc(skv, 1024, 0), lp = (uint32_t)smem_desc(sp, 16, 0);
+            const uint32_t idesc_s = idesc_f16(64, LA_KEYS), idesc_o = idesc_f16(128, a.nr) | KVQ_A_MN;
+            const auto desc = [](uint32_t hi, uint32_t lo) { return (uint64_t)hi << 32 | lo; };
+            const uint32_t q_chunk = (uint32_t)a.nr * 128 >> 4;
+            Place in, s, out, p;   // stage and S of the next first product, stage and P of the next second one
+            const auto qk = [&] {
+                bar_wait(&S.abort, a.hdr, &S.kv_full[in.i], in.round);
                 tc_after();
                 {
-                    uint32_t y = lv + (out.i * LA_STAGE >> 4), z = lp + (p.i * p_bytes >> 4);
-                    asm volatile("" : "+r"(y), "+r"(z));
+                    uint32_t x = lq, y = lk + (in.i * LA_STAGE >> 4);
+                    asm volatile("" : "+r"(x), "+r"(y));
 #pragma unroll
-                    for (int d = 0; d < LAT / 128; ++d)
+                    for (int c = 0; c < LA_CHUNKS; ++c) {
 #pragma unroll
-                        for (int k = 0; k < LA_KEYS / 16; ++k)
-                            mma_ss(TM_O + 64 * d, desc(hi_kv, y + ((k * 2 * LA_GROUP + d * 2048) >> 4)), desc(hi_q, z + 2 * k), idesc_o,
-                                   j > 0 || k > 0);
-                    tc_commit(&S.kv_empty[out.i]);
-                    tc_commit(&S.pv_done[p.i]);
+                        for (int k = 0; k < 4; ++k)
+                            mma_ss(TM_S + s.i * LA_KEYS, desc(hi_q, x + 2 * k), desc(hi_kv, y + (c * 1024 >> 4) + 2 * k), idesc_s, c + k > 0);
+                        x += q_chunk;
+                    }
+                    // (all products so far: where S is there, so is O^T of two steps before, and P's place is free)
+                    tc_commit(&S.s_full[s.i]);
                 }
-                out.next(a.ns);
-                p.next(2);
+                in.next(a.ns);
+                s.next(2);
+            };
+            for (int seg = 0;;) {
+                const int nt = g.nt;
+                if (nt > 0) {
+                    bar_wait(&S.abort, a.hdr, &S.q_full, seg & 1);
+                    ++seg;
+                    qk();
+                    if (nt == 1) tc_commit(&S.q_free);
+                }
+                for (int j = 0; j < nt; ++j) {
+                    if (j + 1 < nt) {
+                        qk();
+                        if (j + 2 == nt) tc_commit(&S.q_free);
+                    }
+                    bar_wait(&S.abort, a.hdr, &S.p_full[p.i], p.round);
+                    tc_after();
+                    {
+                        uint32_t y = lv + (out.i * LA_STAGE >> 4), z = lp + (p.i * p_bytes >> 4);
+                        asm volatile("" : "+r"(y), "+r"(z));
+#pragma unroll
+                        for (int d = 0; d < LAT / 128; ++d)
+#pragma unroll
+                            for (int k = 0; k < LA_KEYS / 16; ++k)
+                                mma_ss(TM_O + 64 * d, desc(hi_kv, y + ((k * 2 * LA_GROUP + d * 2048) >> 4)), desc(hi_q, z + 2 * k), idesc_o,
+                                       j > 0 || k > 0);
+                        tc_commit(&S.kv_empty[out.i]);
+                        tc_commit(&S.pv_done[p.i]);
+                    }
+                    out.next(a.ns);
+                    p.next(2);
+                }
+                if (!g.next(a)) break;
             }
-            if (!g.next(a)) break;
-        }
         }
     } else {
         // ---- softmax: a thread has columns 8k + 2 (lane % 4) and the one behind of rows ra and ra + 8
@@ -600,7 +602,7 @@ __global__ void __launch_bounds__(LA_NT, 1)
 // Bound: the shared-memory reads of the products, 128 bytes per cycle: 24 cycles for each of the 36 products of S, 64 for
 // each of the eight of O, 1376 per step; measured 1420.  Two stages of keys and of values fit beside 64 rows of queries,
 // too few for the latency of HBM, which L2 takes up (three steps ahead; 186 -> 141 us together with loads of keys and
-// values by warps of their own).  Five drafted tokens of eight sequences of 12001 to 16384 tokens, 128 heads: 142 us,
+// values by warps of their own).  Five drafted tokens of eight sequences of 12001 to 16384 tokens, 128 heads: 139 us,
 // 1.11 PFLOP/s, of which the steps 100 us, the join 12 us, the rest starts and outputs of the segments.
 constexpr int LB_KEYS = 64;
 constexpr int LB_K = LB_KEYS / 2 * ROW * 2;      // bytes of a CTA's keys of a step
