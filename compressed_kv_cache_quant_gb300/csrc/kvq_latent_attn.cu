@@ -1146,17 +1146,23 @@ int latent_pairs() {
     return found[dev];
 }
 
-LatPlan latent_plan(const kvq_seqs* S, int32_t n_heads, int64_t n_rows, int32_t max_new) {
-    LatPlan p;
+// Fills in p, or refuses what the kernels' 32-bit numbers do not hold.  The arguments are those that check_latent_rows and
+// kvq_check_max_len let through, so every product here is below 2^63.
+int latent_plan(const kvq_seqs* S, int32_t n_heads, int64_t n_rows, int32_t max_new, const char* fn, LatPlan* plan) {
+    LatPlan& p = *plan;
+    KVQ_REQUIRE(n_rows * n_heads <= INT32_MAX - 128, KVQ_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 query rows", fn);
     const int64_t most = (int64_t)max_new * n_heads;   // query rows of a sequence
     p.pairs = most > LA_ROWS;
     p.nr = p.pairs ? 128 : std::max(16, (int)((most + 15) / 16 * 16));
-    const int64_t by_max = S->batch * ((most + p.nr - 1) / p.nr);
-    p.items = std::max<int64_t>(1, std::min(by_max, n_rows * n_heads / p.nr + S->batch));
+    const int64_t groups = (most + p.nr - 1) / p.nr, by_rows = n_rows * n_heads / p.nr + S->batch;
+    // (the batch's groups by max_new, where they are the fewer)
+    p.items = std::max<int64_t>(1, S->batch > 0 && groups > by_rows / S->batch ? by_rows : S->batch * groups);
     p.keys = p.pairs ? LB_KEYS : LA_KEYS;
     const int64_t each = (S->max_len + p.keys - 1) / p.keys;
     const int at_once = std::min(p.pairs ? latent_pairs() : kvq_num_sms(), KVQ_LATENT_MAX_CTAS);
     p.steps = p.items * each;
+    KVQ_REQUIRE(p.items * p.nr <= INT32_MAX / 8 && p.steps <= INT32_MAX - KVQ_LATENT_MAX_CTAS, KVQ_ERR_UNSUPPORTED,
+                "%s: more than 2^31 steps (queries times max_len)", fn);
     // Few steps per row group: one CTA takes them all, since parts and their join cost more (12 sequences of 53-69 tokens, 60
     // rows each 14.1 -> 10.1 us, four of 200-300, 128 rows 16.3 -> 12.5; seven steps of 16 rows 10.7 in parts, 13.7 in one).
     p.whole = p.items <= at_once && each <= LA_WHOLE;
@@ -1170,15 +1176,18 @@ LatPlan latent_plan(const kvq_seqs* S, int32_t n_heads, int64_t n_rows, int32_t 
     p.off_cuts = kvq_round_up(p.off_ml + rows * sizeof(float2), 256);
     p.off_part = kvq_round_up(p.off_cuts + (size_t)p.items * p.nr * sizeof(int4), 256);
     p.bytes = kvq_round_up(p.off_part + rows * LAT * sizeof(float), 256);
-    return p;
+    return KVQ_OK;
 }
 
 }  // namespace
 
 extern "C" size_t kv_latent_attn_ws(const kvq_seqs* S, int32_t n_heads, int64_t n_rows, int32_t max_new) {
     static const char* fn = "kv_latent_attn_ws";
-    if (kvq_check_seqs_sizes(S, fn) || kvq_check_max_len(S, fn) || check_latent_rows(n_heads, n_rows, max_new, false, fn)) return 0;
-    return latent_plan(S, n_heads, n_rows, max_new).bytes;
+    LatPlan p;
+    if (kvq_check_seqs_sizes(S, fn) || kvq_check_max_len(S, fn) || check_latent_rows(n_heads, n_rows, max_new, false, fn) ||
+        latent_plan(S, n_heads, n_rows, max_new, fn, &p))
+        return 0;
+    return p.bytes;
 }
 
 extern "C" int kv_latent_attn(const kvq_latent* C, const kvq_seqs* S, int32_t n_heads, const uint16_t* q,
@@ -1193,12 +1202,11 @@ extern "C" int kv_latent_attn(const kvq_latent* C, const kvq_seqs* S, int32_t n_
     LatArgs a;
     if (!st) st = latent_scale(scale, fn, &a.scale2);
     if (st) return st;
-    const LatPlan p = latent_plan(S, n_heads, n_rows, max_new);
-    st = kvq_check_ws(ws, ws_bytes, p.bytes, fn);
+    LatPlan p;
+    st = latent_plan(S, n_heads, n_rows, max_new, fn, &p);
+    if (!st) st = kvq_check_ws(ws, ws_bytes, p.bytes, fn);
     if (st) return st;
-    KVQ_REQUIRE(C->num_blocks * PG <= INT32_MAX && n_rows * n_heads <= INT32_MAX - 128, KVQ_ERR_UNSUPPORTED,
-                "%s: more than 2^31 - 1 rows in the pool or queries", fn);
-    KVQ_REQUIRE(p.items * p.nr <= INT32_MAX / 8 && p.steps <= INT32_MAX - KVQ_LATENT_MAX_CTAS, KVQ_ERR_UNSUPPORTED, "%s: more than 2^31 steps (queries times max_len)", fn);
+    KVQ_REQUIRE(C->num_blocks * PG <= INT32_MAX, KVQ_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 rows in the pool", fn);
     if (S->batch == 0 || n_rows == 0) return KVQ_OK;
     KVQ_REQUIRE(q && out && q_starts && (S->block_table || S->max_len == 0), KVQ_ERR_INVALID_ARG, "%s: NULL buffer", fn);
     KVQ_REQUIRE((((uintptr_t)q | (uintptr_t)out) & 15u) == 0, KVQ_ERR_INVALID_ARG, "%s: q and out must be 16-byte aligned", fn);

@@ -128,6 +128,23 @@ def test_latent_attn_refusals(lib):
         assert attn(lib, heads=heads, n=n, max_new=m, S=seqs(batch=3), nbytes=need - 1) == BAD
 
 
+def test_latent_attn_sizes_that_pass_32_bits(lib):
+    """Products of batch, rows, heads and lengths that no 64-bit number holds are refused, and whatever the call refuses has no
+    workspace size."""
+    ws = lambda S, heads, n, max_new: lib.kv_latent_attn_ws(by(S), heads, n, max_new)  # noqa: E731
+    most = (1 << 31) - 1
+    far = dict(max_blocks=1 << 26, max_len=1 << 30)
+    for S, heads, n, max_new in ((seqs(batch=1 << 30), 1 << 16, 4, most),       # 2^70 row groups
+                                 (seqs(batch=1 << 27), 1 << 16, 4, 1 << 30),    # 2^66
+                                 (seqs(batch=most, **far), 1 << 16, most, most),
+                                 (seqs(batch=1 << 20, **far), 128, 1 << 20, 1), # 2^44 steps
+                                 (seqs(), 2, 1 << 30, 1)):                      # 2^31 query rows
+        assert attn(lib, S=S, heads=heads, n=n, max_new=max_new, out=None) == UNSUP, (S.batch, heads, n, max_new)
+        assert ws(S, heads, n, max_new) == 0, (S.batch, heads, n, max_new)
+    # a bound on the new tokens far above their number costs nothing but the choice of the kernel
+    assert 256 < ws(seqs(), 128, 4, most) == ws(seqs(), 128, 4, 1 << 20)
+
+
 def expanded(lib, batch=2, heads=4, q=256, kn=256, kns=1024, knh=256, kr=256, krs=576, v=512, vs=1024, vh=256, m=64, qs=256, ks=256, n=4, max_new=4,
              max_len=32, scale=0.0, out=256, ws=256, nbytes=1 << 40):
     return lib.kv_latent_expanded_attn(batch, heads, q, kn, kns, knh, kr, krs, v, vs, vh, m, qs, ks, n, max_new, max_len, scale, out, None, ws, nbytes,
