@@ -400,6 +400,9 @@ extern "C" int kv_rope_append(const kvq_layout* L, const kvq_pool* P, const kvq_
     const bool fp8 = L->bits == KVQ_BITS_E4M3;
     KVQ_REQUIRE(fp8 || L->bits == 16, KVQ_ERR_UNSUPPORTED, "%s: bits %d (an fp16 or an E4M3 layer)", fn, L->bits);
     KVQ_REQUIRE(dtype == KVQ_F16 || dtype == KVQ_BF16, KVQ_ERR_UNSUPPORTED, "%s: dtype %d", fn, dtype);
+    // (a token's head rows are counted in 32 bits)
+    KVQ_REQUIRE(L->n_q_heads <= 1 << 16 && L->n_kv_heads <= 1 << 16, KVQ_ERR_UNSUPPORTED, "%s: %d + %d heads (at most 65536 each)",
+                fn, L->n_q_heads, L->n_kv_heads);
     KVQ_REQUIRE(n_rows >= 0 && n_rows <= INT32_MAX, KVQ_ERR_INVALID_ARG, "%s: n_rows", fn);
     KVQ_REQUIRE(P != nullptr && S->batch <= P->max_seqs, KVQ_ERR_INVALID_ARG, "%s: NULL pool, or batch above max_seqs", fn);
     if (S->batch == 0 || n_rows == 0) return KVQ_OK;

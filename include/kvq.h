@@ -790,10 +790,10 @@ size_t kv_chunk_attn_ws(const kvq_layout* layout, const kvq_seqs* seqs, int64_t 
  * tokens must be allocated and not shared.  Rows behind row_starts[batch] and rows
  * of a sequence whose lengths do not fit (flagged) are left as they were, q_out
  * included; where a page id is none (flagged) the row's K and V are skipped.
- * No two sequences may write the same page's rows.  Quantized layers
- * are written by kv_quant_pack and kv_page_append.
+ * No two sequences may write the same page's rows.  At most 65536 query and
+ * 65536 kv heads.  Quantized layers are written by kv_quant_pack and kv_page_append.
  * ws: kv_rope_append_ws() bytes (status word only).
- * Errors: INVALID_ARG, UNSUPPORTED (bits, dtype, rot_dim), CUDA.
+ * Errors: INVALID_ARG, UNSUPPORTED (bits, dtype, rot_dim, heads), CUDA.
  * ---------------------------------------------------------------------- */
 int kv_rope_append(const kvq_layout* layout, const kvq_pool* pool, const kvq_seqs* seqs, const kvq_rope* rope,
                    const uint64_t* steps, float mscale, int32_t dtype, int64_t n_rows,

@@ -62,6 +62,15 @@ def test_rope_append_refusals(lib):
     assert lib.kv_rope_append_ws() == 256
 
 
+def test_rope_append_refuses_head_counts_that_pass_32_bits(lib):
+    """2 + 2 (2^31 - 1) is 0 in 32 bits: no such count may reach the division of a CTA's rows."""
+    most = (1 << 31) - 1
+    for heads in (dict(hq=2, hkv=most), dict(hq=most, hkv=most), dict(hq=2, hkv=1 << 30), dict(hq=(1 << 16) + 1), dict(hkv=(1 << 16) + 1)):
+        for bits in (16, _abi.BITS_E4M3):
+            assert append(lib, bits=bits, qs=1 << 39, ks=1 << 39, vs=1 << 39, **heads) == UNSUP, heads
+    assert "65536" in _abi.last_error()
+
+
 def latent(dim=512, rot=64, blocks=8, rows=256):
     return _abi.Latent(dim, rot, blocks, rows)
 
