@@ -1076,6 +1076,15 @@ ChunkPlan chunk_plan(const kvq_layout* L, const kvq_seqs* S, int64_t n_rows, int
     return chunk_plan(L->n_kv_heads, L->n_q_heads / L->n_kv_heads, S->batch, S->max_len, n_rows, max_new, tree ? 2 : 4);
 }
 
+// A call with something to do: its groups over all heads are a grid's x.
+int check_plan(const ChunkPlan& p, int H, int32_t batch, int64_t n_rows, const char* fn) {
+    KVQ_REQUIRE(batch == 0 || n_rows == 0 || p.items <= INT32_MAX / H, KVQ_ERR_UNSUPPORTED, "%s: n_rows", fn);
+    return KVQ_OK;
+}
+size_t plan_bytes(const ChunkPlan& p, int H, int32_t batch, int64_t n_rows, const char* fn) {
+    return check_plan(p, H, batch, n_rows, fn) ? 0 : p.bytes;
+}
+
 // Fills in what follows from the plan and launches the kernel and, over parts of the cache, their join.
 template <typename Kernel>
 int launch_chunk(Kernel kernel, int smem, const ChunkPlan& p, ChunkArgs& a, const CUtensorMap& map_q, const CUtensorMap& map_k,
@@ -1106,7 +1115,7 @@ extern "C" size_t kv_chunk_attn_ws(const kvq_layout* L, const kvq_seqs* S, int64
     if (kvq_check_layout(L, "kv_chunk_attn_ws", true) || kvq_check_seqs_sizes(S, "kv_chunk_attn_ws") ||
         kvq_check_max_len(S, "kv_chunk_attn_ws") || check_rows(n_rows, max_new, "kv_chunk_attn_ws"))
         return 0;
-    return chunk_plan(L, S, n_rows, max_new, false).bytes;
+    return plan_bytes(chunk_plan(L, S, n_rows, max_new, false), L->n_kv_heads, S->batch, n_rows, "kv_chunk_attn_ws");
 }
 
 // kv_chunk_attn, or with `tree` kv_tree_attn.
@@ -1137,7 +1146,8 @@ static int chunk_attn(const char* fn, bool tree, const kvq_layout* L, const kvq_
     KVQ_REQUIRE(q && out && q_starts && (!tree || parents) && (S->block_table || S->max_len == 0), KVQ_ERR_INVALID_ARG, "%s: NULL buffer", fn);
     KVQ_REQUIRE((((uintptr_t)q | (uintptr_t)out | (uintptr_t)P->k16 | (uintptr_t)P->v16) & 15u) == 0,
                 KVQ_ERR_INVALID_ARG, "%s: q, out, k16 and v16 must be 16-byte aligned", fn);
-    KVQ_REQUIRE(p.items * L->n_kv_heads <= INT32_MAX, KVQ_ERR_UNSUPPORTED, "%s: n_rows", fn);
+    st = check_plan(p, L->n_kv_heads, S->batch, n_rows, fn);
+    if (st) return st;
     const int H = L->n_kv_heads, GQ = L->n_q_heads / H;
     CUtensorMap map_q, map_k, map_v;
     const uint64_t qd[3] = {D, (uint64_t)L->n_q_heads, (uint64_t)n_rows};
@@ -1179,7 +1189,7 @@ extern "C" size_t kv_tree_attn_ws(const kvq_layout* L, const kvq_seqs* S, int64_
     if (kvq_check_layout(L, "kv_tree_attn_ws", true) || kvq_check_seqs_sizes(S, "kv_tree_attn_ws") ||
         kvq_check_max_len(S, "kv_tree_attn_ws") || check_tree_rows(n_rows, max_new, "kv_tree_attn_ws"))
         return 0;
-    return chunk_plan(L, S, n_rows, max_new, true).bytes;
+    return plan_bytes(chunk_plan(L, S, n_rows, max_new, true), L->n_kv_heads, S->batch, n_rows, "kv_tree_attn_ws");
 }
 
 extern "C" int kv_tree_attn(const kvq_layout* L, const kvq_pool* P, const kvq_seqs* S, const uint16_t* q,
@@ -1198,7 +1208,7 @@ static int check_expanded(int32_t batch, int32_t n_heads, int64_t n_rows, int32_
 extern "C" size_t kv_latent_expanded_attn_ws(int32_t batch, int32_t n_heads, int64_t n_rows, int32_t max_new, int32_t max_len) {
     kvq_clear_error();
     if (check_expanded(batch, n_heads, n_rows, max_new, max_len, "kv_latent_expanded_attn_ws")) return 0;
-    return chunk_plan(n_heads, 1, batch, max_len, n_rows, max_new).bytes;
+    return plan_bytes(chunk_plan(n_heads, 1, batch, max_len, n_rows, max_new), n_heads, batch, n_rows, "kv_latent_expanded_attn_ws");
 }
 
 extern "C" int kv_latent_expanded_attn(int32_t batch, int32_t n_heads, const uint16_t* q, const uint16_t* k_nope,
@@ -1230,7 +1240,8 @@ extern "C" int kv_latent_expanded_attn(int32_t batch, int32_t n_heads, const uin
     KVQ_REQUIRE(kn_stride >= D && kn_head_stride >= D && v_stride >= D && v_head_stride >= D && kr_stride >= KVQ_LATENT_ROPE &&
                     std::max({kn_stride, kn_head_stride, kr_stride, v_stride, v_head_stride}) < (int64_t)1 << 39,
                 KVQ_ERR_INVALID_ARG, "%s: a stride below the row's width, or above 2^39", fn);
-    KVQ_REQUIRE(p.items * n_heads <= INT32_MAX, KVQ_ERR_UNSUPPORTED, "%s: n_rows", fn);
+    st = check_plan(p, n_heads, batch, n_rows, fn);
+    if (st) return st;
     const uint64_t H = n_heads;
     CUtensorMap map_q, map_k, map_v, map_r;
     const uint64_t qd[3] = {D + KVQ_LATENT_ROPE, H, (uint64_t)n_rows}, qs[2] = {(D + KVQ_LATENT_ROPE) * 2, H * (D + KVQ_LATENT_ROPE) * 2};

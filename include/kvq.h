@@ -39,7 +39,8 @@
  *     as void*; NULL is the legacy default stream).
  *   - fp16 data is IEEE binary16 passed as uint16_t.  head_dim d is 128.
  *   - Workspaces ("ws") are device buffers of at least the size the matching
- *     *_ws() function returns, 256-byte aligned, ZERO-FILLED BEFORE FIRST USE.
+ *     *_ws() function returns (0: the call would be refused), 256-byte aligned,
+ *     ZERO-FILLED BEFORE FIRST USE.
  *     The library leaves them zeroed after every call that completes, so they
  *     can be reused; after a call that failed on the device, zero them again.
  *     The one exception is a handful of diagnostic path counters in the first

@@ -172,6 +172,20 @@ def test_expanded_refusals(lib):
     assert lib.kv_latent_expanded_attn_ws(2, 0, 4, 4, 32) == 0 and lib.kv_latent_expanded_attn_ws(-2, 4, 4, 4, 32) == 0
 
 
+def test_what_is_refused_has_no_workspace_size(lib):
+    """Trees and expanded runs of more than 2^31 - 1 groups of query rows over all heads."""
+    most = (1 << 31) - 1
+    S = seqs(batch=1 << 20)
+    L = kvq.make_layout(1 << 15, 1 << 14, 16)
+    rows = 1 << 30
+    assert lib.kv_tree_attn(by(L), by(pool()), by(S), 256, 256, 256, rows, 256, None, 256, None, 256, 1 << 40, None) == UNSUP
+    assert lib.kv_tree_attn_ws(by(L), by(S), rows, 256) == 0
+    assert expanded(lib, batch=1 << 20, heads=1 << 16, n=most, max_new=most, max_len=1 << 30) == UNSUP
+    assert lib.kv_latent_expanded_attn_ws(1 << 20, 1 << 16, most, most, 1 << 30) == 0
+    # with nothing to do, nothing is refused
+    assert lib.kv_tree_attn_ws(by(L), by(S), 0, 0) == 256 and lib.kv_latent_expanded_attn_ws(0, 1 << 16, most, most, 1 << 30) == 256
+
+
 def test_refusals_say_why(lib):
     assert tree(lib, max_new=300) == UNSUP and "256" in _abi.last_error()
     assert attn(lib, C=latent(dim=448)) == UNSUP and "448" in _abi.last_error()
