@@ -106,7 +106,8 @@ class Batch:
         self.max_len = int(max_len)
         B, mb = self.block_table.shape
         self.c = Seqs(_p(self.block_table), _p(self.seq_lens), B, mb, self.max_len, 0)
-        self.gpu = self.seq_lens.get_device()
+        gpu = self.seq_lens.get_device()
+        self.gpu = gpu if self.block_table.get_device() == gpu else -2   # (-1: the host, -2: not all in one place)
 
     @property
     def batch(self):
@@ -603,7 +604,7 @@ def _dtype_of(x, fn):
 
 def _elsewhere(gpu, fn, *parts):
     """The refusal of a call whose caches, tables or workspaces are not all on GPU `gpu`."""
-    where = ", ".join(f"{type(x).__name__} on {x.gpu}" for x in parts)
+    where = ", ".join(f"{type(x).__name__} on {'several' if x.gpu == -2 else x.gpu}" for x in parts)
     raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, f"{where}: not all on GPU {gpu}")
 
 

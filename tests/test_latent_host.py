@@ -4,6 +4,7 @@ import ctypes
 import math
 
 import pytest
+import torch
 
 from compressed_kv_cache_quant_gb300 import _abi, kvq
 from compressed_kv_cache_quant_gb300.build import build
@@ -190,3 +191,27 @@ def test_refusals_say_why(lib):
     assert tree(lib, max_new=300) == UNSUP and "256" in _abi.last_error()
     assert attn(lib, C=latent(dim=448)) == UNSUP and "448" in _abi.last_error()
     assert append(lib, bits=4) == UNSUP and "bits 4" in _abi.last_error()
+
+
+class On:
+    """Stands for an int32 tensor on a GPU."""
+    dtype, shape = torch.int32, (1, 4)
+
+    def __init__(self, gpu):
+        self.gpu = gpu
+
+    def contiguous(self):
+        return self
+
+    def data_ptr(self):
+        return 256
+
+    def get_device(self):
+        return self.gpu
+
+
+def test_a_batch_is_on_a_gpu_only_when_both_of_its_tables_are():
+    """The calls compare Batch.gpu with the current GPU: a block table elsewhere would be read through a foreign address."""
+    assert kvq.Batch(On(0), On(0), 64).gpu == 0 and kvq.Batch(On(3), On(3), 64).gpu == 3
+    for table, lens in ((0, 1), (1, 0), (-1, 0), (0, -1), (-1, -1)):
+        assert kvq.Batch(On(table), On(lens), 64).gpu < 0, (table, lens)
