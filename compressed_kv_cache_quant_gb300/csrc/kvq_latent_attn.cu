@@ -599,11 +599,17 @@ __global__ void __launch_bounds__(LA_NT, 1)
 // of M = 128 in 128 lanes: lanes 64 and up have the second half of the columns).  Half a token's values is thus staged
 // twice, since one descriptor serves both CTAs, and at different places they cannot read it.
 //
+// Rank 1's weights (and its values, zeroed rows and reads of TMEM) are handed to rank 0 in three steps, each ordered: its
+// softmax warps arrive at a barrier of their own CTA, one lane there (warp 4's) waits for them and arrives at rank 0's
+// with a release to the cluster, and rank 0's issuing lane waits with an acquire.  The release takes some 2000 cycles, so S
+// is two steps ahead of O; in the softmax warps themselves, it would hold them up (five drafted tokens as below 233 us; by
+// the lane with S one step ahead 178 us).
+//
 // Bound: the shared-memory reads of the products, 128 bytes per cycle: 24 cycles for each of the 36 products of S, 64 for
-// each of the eight of O, 1376 per step; measured 1420.  Two stages of keys and of values fit beside 64 rows of queries,
-// too few for the latency of HBM, which L2 takes up (three steps ahead; 186 -> 141 us together with loads of keys and
-// values by warps of their own).  Five drafted tokens of eight sequences of 12001 to 16384 tokens, 128 heads: 139 us,
-// 1.11 PFLOP/s, of which the steps 100 us, the join 12 us, the rest starts and outputs of the segments.
+// each of the eight of O, 1376 per step; and the way of the weights: a place of theirs is written, handed over, read and
+// free again in two steps.  Two stages of keys and of values fit beside 64 rows of queries,
+// too few for the latency of HBM, which L2 takes up (three steps ahead).  Five drafted tokens of eight sequences of
+// 12001 to 16384 tokens, 128 heads: 152 us, 1.02 PFLOP/s, of which the join 12 us.
 constexpr int LB_KEYS = 64;
 constexpr int LB_K = LB_KEYS / 2 * ROW * 2;      // bytes of a CTA's keys of a step
 constexpr int LB_V = LB_KEYS * LAT;              // and of its values (two bytes each, half of them)
@@ -615,7 +621,7 @@ constexpr int LB_Q = 64 * ROW * 2, LB_P = 64 * 128;
 constexpr int LB_SMEM = 1024 + LB_Q + LB_NS * (LB_K + LB_V) + 2 * LB_P;
 
 struct SharedPair {
-    uint64_t q_full, q_free, k_full[LB_NS], k_empty[LB_NS], v_full[LB_NS], v_empty[LB_NS], s_full[2], p_full[2], pv_done[2];
+    uint64_t q_full, q_free, k_full[LB_NS], k_empty[LB_NS], v_full[LB_NS], v_empty[LB_NS], s_full[3], p_full[2], p_here[2], pv_done[2];
     uint32_t tmem;
     int32_t abort, per;
     Segment<LB_KEYS> seg;
@@ -641,10 +647,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LB_NT, 1)
             bar_init(&S.k_empty[i], 1);
             bar_init(&S.v_full[i], 1);
             bar_init(&S.v_empty[i], 1);
-            bar_init(&S.s_full[i], 1);
-            bar_init(&S.p_full[i], 8);
+            bar_init(&S.p_full[i], 4 + 1);   // rank 0: its softmax warps, and the other CTA's by one lane
+            bar_init(&S.p_here[i], 4);       // rank 1: its softmax warps
             bar_init(&S.pv_done[i], 1);
         }
+        for (int i = 0; i < 3; ++i) bar_init(&S.s_full[i], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 4) {
@@ -762,7 +769,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LB_NT, 1)
                            lv = (uint32_t)smem_desc(sv, 1024, 0), lp = (uint32_t)smem_desc(sp, 16, 0);
             constexpr uint32_t idesc_s = idesc_f16(128, LB_KEYS), idesc_o = idesc_f16(128, 256) | KVQ_B_MN;
             const auto desc = [](uint32_t hi, uint32_t lo) { return (uint64_t)hi << 32 | lo; };
-            Place in, out;   // of the next S and the next O (stages and buffers alike: two of each)
+            Place in, s, out;   // stage and buffer (of three) of the next S; stage and buffer of the next O
             const auto qk = [&] {
                 bar_wait(&S.abort, a.hdr, &S.k_full[in.i], in.round);
                 tc_after();
@@ -772,26 +779,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LB_NT, 1)
                 for (int c = 0; c < LA_CHUNKS; ++c)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_ss_pair(TM_S + in.i * (LB_KEYS / 2), desc(hi_q, x + (c * 8192 >> 4) + 2 * k),
+                        mma_ss_pair(TM_S + s.i * (LB_KEYS / 2), desc(hi_q, x + (c * 8192 >> 4) + 2 * k),
                                     desc(hi_k, y + (c * 1024 >> 4) + 2 * k), idesc_s, c + k > 0);
-                // (all products so far: where S is there, so is O of two steps before, and P's place is free)
-                tc_commit_pair(&S.s_full[in.i]);
+                // (all products so far: where S is there, so is O of three steps before)
+                tc_commit_pair(&S.s_full[s.i]);
                 tc_commit_pair(&S.k_empty[in.i]);
                 in.next(2);
+                s.next(3);
             };
             for (int seg = 0;;) {
                 if (g.nt > 0) {
                     bar_wait(&S.abort, a.hdr, &S.q_full, seg & 1);
                     ++seg;
                     qk();
-                    if (g.nt == 1) tc_commit_pair(&S.q_free);
+                    if (g.nt > 1) qk();
+                    if (g.nt <= 2) tc_commit_pair(&S.q_free);
                 }
                 for (int j = 0; j < g.nt; ++j) {
-                    if (j + 1 < g.nt) {
+                    if (j + 2 < g.nt) {
                         qk();
-                        if (j + 2 == g.nt) tc_commit_pair(&S.q_free);
+                        if (j + 3 == g.nt) tc_commit_pair(&S.q_free);
                     }
-                    bar_wait(&S.abort, a.hdr, &S.p_full[out.i], out.round);
+                    bar_wait<true>(&S.abort, a.hdr, &S.p_full[out.i], out.round);
                     tc_after();
                     uint32_t y = lv + (out.i * LB_V >> 4), z = lp + (out.i * LB_P >> 4);
                     asm volatile("" : "+r"(y), "+r"(z));
@@ -807,6 +816,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LB_NT, 1)
                 }
                 if (!g.next(a)) break;
             }
+        } else if (rank == 1 && elect()) {
+            // ---- hands this CTA's weights to rank 0
+            const uint32_t p_full[2] = {saddr_in(&S.p_full[0], 0), saddr_in(&S.p_full[1], 0)};
+            Place at;
+            do {
+                for (int j = 0; j < g.nt; ++j, at.next(2)) {
+                    bar_wait(&S.abort, a.hdr, &S.p_here[at.i], at.round);
+                    tc_after();
+                    tc_before();
+                    bar_arrive_in(p_full[at.i]);
+                }
+            } while (g.next(a));
         }
         __syncwarp();
     } else {
@@ -814,8 +835,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LB_NT, 1)
         const uint32_t lane_base = tmem + ((uint32_t)warp << 21);   // TMEM lanes 32 warp ..
         const int r = tid & 63, half = tid >> 6;
         const bool tree = a.parents != nullptr;
-        const uint32_t p_full[2] = {saddr_in(&S.p_full[0], 0), saddr_in(&S.p_full[1], 0)};
-        Place at, done;   // `done`: the step before
+        uint64_t* const handed = rank == 0 ? S.p_full : S.p_here;
+        Place s_at, at, done;   // buffer of S; of the weights, and stage; `done`: the step before
         do {
             const int nt = g.nt, end = g.end, ctx = g.s.T - g.s.n;
             const int row0 = g.group * a.nr + 64 * (int)rank;   // of the sequence
@@ -827,12 +848,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LB_NT, 1)
             if (tree && valid) walk_path(a, g.s.first, tok, path);
             const int full = __reduce_min_sync(0xffffffffu, cut);
             float m = -INFINITY, l = 0.0f;
-            for (int j = 0; j < nt; ++j, done = at, at.next(2)) {
+            for (int j = 0; j < nt; ++j, done = at, at.next(2), s_at.next(3)) {
                 const int t0 = (g.step + j) * LB_KEYS, c0 = t0 + 32 * half;
-                bar_wait(&S.abort, a.hdr, &S.s_full[at.i], at.round);
+                bar_wait(&S.abort, a.hdr, &S.s_full[s_at.i], s_at.round);
                 tc_after();
                 float s[32];
-                tm_ld32(lane_base + TM_S + at.i * (LB_KEYS / 2), reinterpret_cast<uint32_t*>(s));
+                tm_ld32(lane_base + TM_S + s_at.i * (LB_KEYS / 2), reinterpret_cast<uint32_t*>(s));
 #pragma unroll
                 for (int c = 0; c < 32; ++c) s[c] = __fmul_rn(s[c], a.scale2);
                 if (c0 + 32 > full) {   // (full: what every row of the warp sees all of)
@@ -849,7 +870,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LB_NT, 1)
                     for (int x = 0; x < 4; ++x) t4[x] = max3(t4[x], s[c + 2 * x], s[c + 2 * x + 1]);
                 float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
                 // a first anchor, or a weight that would leave fp16's range (either thread of a row tells)
-                if (sm_any(m == -INFINITY ? top > m : top - m > LA_TOP)) {
+                const bool turn = sm_any(m == -INFINITY ? top > m : top - m > LA_TOP);
+                if (j >= 2) bar_wait(&S.abort, a.hdr, &S.pv_done[at.i], at.round ^ 1);   // the weights' place is free
+                if (turn) {
                     // one row's turn is every row's: an anchor that would have to follow later is set now
                     S.half[tid] = top;
                     sm_any(false);
@@ -907,7 +930,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LB_NT, 1)
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 tc_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive_in(p_full[at.i]);
+                if (lane == 0) bar_arrive(&handed[at.i]);
             }
             // ---- the segment's rows: to the output, or as a part of them
             const bool whole = g.step == 0 && g.cnt == g.s.steps, last = g.step + g.cnt == g.s.steps;

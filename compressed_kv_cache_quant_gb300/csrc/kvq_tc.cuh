@@ -173,23 +173,33 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
     return r;
 }
 
+// CLUSTER: arrivals of other CTAs of the cluster are among those waited for (bar_arrive_in)
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_done(uint32_t bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
+    if constexpr (CLUSTER)
+        asm volatile(
+            "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
     return ok != 0;
 }
 // Waits for a phase of bar.  After `limit` polls it flags the timeout, and every wait of the CTA that is
 // not over by then returns at once: the roles run through to their ends without waiting, on data that is
 // not valid, so no step needs a branch for the failure; only the loads stop (a barrier must not be armed
 // twice).  Most waits of the issuing warps find their phase done: one poll and nothing else.
+template <bool CLUSTER = false>
 __device__ __forceinline__ void bar_wait(int32_t* abort, KvqWsHeader* hdr, uint64_t* bar, uint32_t parity,
                                          uint32_t limit = KVQ_SPIN) {
     const uint32_t at = saddr(bar);
-    for (uint32_t it = 0; !bar_done(at, parity); ++it) {
+    for (uint32_t it = 0; !bar_done<CLUSTER>(at, parity); ++it) {
         if ((it & 63) != 63) continue;
         if (*(volatile int32_t*)abort) return;
         if (it > limit) {
@@ -231,10 +241,10 @@ __device__ __forceinline__ uint32_t saddr_in(const void* p, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr(p)), "r"(rank));
     return r;
 }
-// (what an arrival stands for lies in the arriving CTA's own shared memory, where products of the pair read it: the
-// order within that CTA is enough, and a release to the cluster costs 1000 to 2500 cycles)
+// Arrives at a barrier of another CTA (an address of saddr_in), and releases to the cluster what the arriving thread has
+// written or seen: the waiting thread acquires it with bar_wait<true>.  It takes some 2000 cycles under load.
 __device__ __forceinline__ void bar_arrive_in(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // a copy into this CTA that signals a barrier of the pair (an address of saddr_in)
 __device__ __forceinline__ void tma_page_pair(uint32_t dst, const CUtensorMap* map, int group, uint32_t bar) {
