@@ -51,11 +51,13 @@ constexpr int LA_NT = 192;
 constexpr int LA_ROWS = 32;               // query rows per CTA, at most
 constexpr int LA_KEYS = 48;               // tokens per step
 constexpr int LA_FAR = 2;                 // steps that pages are brought into L2 ahead of their load
-constexpr int LA_MAX_NS = 8;              // most stages
+constexpr int LA_NS = 3;                  // stages: as many as fit
 constexpr int LA_CHUNKS = ROW / 64;
 constexpr int LA_GROUP = LA_CHUNKS * 1024;              // bytes of eight staged rows
 constexpr int LA_STAGE = LA_KEYS / 8 * LA_GROUP;
 constexpr int LA_SMEM = 232448 - 1024;    // dynamic shared memory of a CTA, at most (static: under 1 KB)
+constexpr int la_smem(int nr) { return 1024 + nr * (ROW * 2 + 2 * 128) + LA_NS * LA_STAGE; }
+static_assert(la_smem(LA_ROWS) <= LA_SMEM && la_smem(16) + LA_STAGE > LA_SMEM, "stages");
 constexpr float LA_HEAD = 7.0f;           // log2 of a row's largest weight when its anchor is set
 constexpr float LA_TOP = 15.99f;          // log2 of the largest weight before the anchor is set anew
 constexpr int LA_WHOLE = 6;               // steps of a row group that is not cut, at most
@@ -67,7 +69,7 @@ struct LatArgs {
     int64_t n_rows, num_blocks;
     int32_t batch, max_blocks, max_len, max_new, H, items;   // items: row groups, at most
     int32_t whole;                                        // a CTA (or pair) takes one row group, none is cut
-    int32_t nr, ns;                                       // rows per CTA as the products see them, a multiple of 16; stages
+    int32_t nr;                                           // rows per CTA (or pair) as the products see them: 16, 32 or 128
     float scale2;                                         // of a score, in log2 units
     uint16_t* out;
     float* lse;
@@ -81,7 +83,7 @@ struct LatArgs {
 
 struct Seq {
     int32_t first, n, T;   // first row of the call, new tokens, tokens
-    int32_t groups, steps; // of 64 query rows; of tokens, per group
+    int32_t groups, steps; // of nr query rows; of KEYS tokens, per group
 };
 
 template <int KEYS>
@@ -195,7 +197,7 @@ struct Place {
 };
 
 struct Shared {
-    uint64_t q_full, q_free, kv_full[LA_MAX_NS], kv_empty[LA_MAX_NS], s_full[2], p_full[2], pv_done[2], drain;
+    uint64_t q_full, q_free, kv_full[LA_NS], kv_empty[LA_NS], s_full[2], p_full[2], pv_done[2], drain;
     uint32_t tmem;
     int32_t abort;
     Segment<LA_KEYS> seg;
@@ -263,13 +265,13 @@ __global__ void __launch_bounds__(LA_NT, 1)
     // queries, stages, weights: with nr below 64 the first product reads behind the queries, into the stages, for
     // rows of S that nothing looks at
     if (tid == 64) map_prefetch(&map_q), map_prefetch(&map_rows);
-    const uint32_t sq = (saddr(raw) + 1023) & ~1023u, skv = sq + a.nr * ROW * 2, sp = skv + a.ns * LA_STAGE,
+    const uint32_t sq = (saddr(raw) + 1023) & ~1023u, skv = sq + a.nr * ROW * 2, sp = skv + LA_NS * LA_STAGE,
                    p_bytes = a.nr * 128;   // (a row of weights takes 128 bytes, as the swizzle wants it)
     // (what does not read global memory goes before the wait for the launch before)
     if (tid == 32) {
         bar_init(&S.q_full, 1);
         bar_init(&S.q_free, 1);
-        for (int i = 0; i < a.ns; ++i) {
+        for (int i = 0; i < LA_NS; ++i) {
             bar_init(&S.kv_full[i], 1);
             bar_init(&S.kv_empty[i], 1);
         }
@@ -334,7 +336,7 @@ __global__ void __launch_bounds__(LA_NT, 1)
                 int to[LA_KEYS / PG];
 #pragma unroll
                 for (int k = 0; k < LA_KEYS / PG; ++k) to[k] = __shfl_sync(0xffffffffu, y, k);
-                if (loaded >= a.ns) bar_wait(&S.abort, a.hdr, &S.kv_empty[st.i], st.round ^ 1);
+                if (loaded >= LA_NS) bar_wait(&S.abort, a.hdr, &S.kv_empty[st.i], st.round ^ 1);
                 ok = !aborted(&S.abort);
                 if (ok && elect()) {
                     bar_expect(&S.kv_full[st.i], pages * PG * ROW * 2);
@@ -348,7 +350,7 @@ __global__ void __launch_bounds__(LA_NT, 1)
 #pragma unroll
                 for (int k = 0; k + 1 < LA_FAR; ++k) ahead[k] = ahead[k + 1];
                 ahead[LA_FAR - 1] = group_of(j + 1 + LA_FAR);
-                st.next(a.ns);
+                st.next(LA_NS);
             }
             if (!g.next(a)) break;
         }
@@ -378,7 +380,7 @@ __global__ void __launch_bounds__(LA_NT, 1)
                     // (all products so far: where S is there, so is O^T of two steps before, and P's place is free)
                     tc_commit(&S.s_full[s.i]);
                 }
-                in.next(a.ns);
+                in.next(LA_NS);
                 s.next(2);
             };
             for (int seg = 0;;) {
@@ -408,7 +410,7 @@ __global__ void __launch_bounds__(LA_NT, 1)
                         tc_commit(&S.kv_empty[out.i]);
                         tc_commit(&S.pv_done[p.i]);
                     }
-                    out.next(a.ns);
+                    out.next(LA_NS);
                     p.next(2);
                 }
                 if (!g.next(a)) break;
@@ -439,7 +441,7 @@ __global__ void __launch_bounds__(LA_NT, 1)
                 if (tree && valid[i]) walk_path(a, g.s.first, tok, path[i]);
             }
             const int full = __reduce_min_sync(0xffffffffu, min(cut[0], cut[1]));
-            for (int j = 0; j < nt; ++j, done = s_at, st.next(a.ns), s_at.next(2)) {
+            for (int j = 0; j < nt; ++j, done = s_at, st.next(LA_NS), s_at.next(2)) {
                 const int t0 = (g.step + j) * LA_KEYS;
                 bar_wait(&S.abort, a.hdr, &S.s_full[s_at.i], s_at.round);
                 tc_after();
@@ -1137,7 +1139,7 @@ __global__ void __cluster_dims__(LQ, 1, 1) __launch_bounds__(LQ_W * LQ_GR) laten
 
 struct LatPlan {
     bool pairs, whole;
-    int nr, ns, keys, ctas;   // ctas: CTAs, or pairs of them
+    int nr, keys, ctas;   // ctas: CTAs, or pairs of them
     int64_t items, steps;   // row groups and steps of the list, at most
     size_t smem, off_ml, off_cuts, off_part, bytes;
 };
@@ -1191,9 +1193,7 @@ int latent_plan(const kvq_seqs* S, int32_t n_heads, int64_t n_rows, int32_t max_
     p.whole = p.items <= at_once && each <= LA_WHOLE;
     const int64_t cut = std::max<int64_t>(1, std::min<int64_t>(p.steps, at_once));
     p.ctas = (int)(p.whole ? p.items : cut);
-    const size_t fixed = 1024 + (size_t)p.nr * (ROW * 2 + 2 * 128);
-    p.ns = p.pairs ? LB_NS : (int)std::min<size_t>((LA_SMEM - fixed) / LA_STAGE, LA_MAX_NS);
-    p.smem = p.pairs ? LB_SMEM : fixed + p.ns * LA_STAGE;
+    p.smem = p.pairs ? LB_SMEM : la_smem(p.nr);
     const size_t rows = (size_t)2 * cut * p.nr;   // (of either kind, so that a workspace serves every shorter max_len)
     p.off_ml = sizeof(KvqWsHeader);
     p.off_cuts = kvq_round_up(p.off_ml + rows * sizeof(float2), 256);
@@ -1244,7 +1244,7 @@ extern "C" int kv_latent_attn(const kvq_latent* C, const kvq_seqs* S, int32_t n_
     if (st) return st;
     a.bt = S->block_table, a.seq_lens = S->seq_lens, a.q_starts = q_starts, a.parents = parents;
     a.n_rows = n_rows, a.num_blocks = C->num_blocks;
-    a.batch = S->batch, a.max_blocks = S->max_blocks, a.max_len = S->max_len, a.max_new = max_new, a.H = n_heads, a.whole = p.whole, a.nr = p.nr, a.ns = p.ns, a.items = (int)p.items;
+    a.batch = S->batch, a.max_blocks = S->max_blocks, a.max_len = S->max_len, a.max_new = max_new, a.H = n_heads, a.whole = p.whole, a.nr = p.nr, a.items = (int)p.items;
     a.out = out, a.lse = lse, a.hdr = static_cast<KvqWsHeader*>(ws);
     a.ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + p.off_ml);
     a.cuts = reinterpret_cast<int4*>(static_cast<char*>(ws) + p.off_cuts);
