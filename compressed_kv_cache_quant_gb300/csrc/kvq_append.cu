@@ -1,16 +1,16 @@
 // kv_rope_append and kv_latent_append: a run of new tokens per sequence into the pages, normed and rotated on
 // the way, so that no rotated copy is written and read again.
 //
-// Bound: bytes (about 3 flops per byte).  One CTA takes a few rows of the call.  Its first warp finds each row's
+// Bound: bytes (about 3 flops per byte).  One CTA takes a few rows of the call.  Its last warp finds each row's
 // sequence, page and position (three loads in sequence) while the others' first head rows are on their way; 256
 // threads then compute the rows' cosines and sines once into shared memory, and every group of lanes takes whole
 // head rows in two 16-byte loads per lane, as kv_qk_norm_rope does.  Angles are 64-bit turns.  Every value is
 // rounded once, from fp32 to the cache's type.
 //
 // Measured (in a graph): two prompts of 16001 and 16384 tokens, bf16, normed, 32 + 8 + 8 heads into E4M3 pages 121 us,
-// 6.0 TB/s (89% of the copy rate); 16385 latent rows with the rotated part of 16 heads 23 us, 4.5 TB/s, where 3.4 waves of
-// CTAs each begin with the chain of lookups; one token of 16 sequences 3 us.  More loads per lane cost CTAs per SM and
-// more time (24 -> 34 us with four head rows on their way).
+// 6.0 TB/s (89% of the copy rate); 16385 latent rows with the rotated part of 16 heads 23 us, 4.5 TB/s, where 2.7 waves of
+// CTAs (2049, five per SM) each begin with the chain of lookups; one token of 16 sequences 3 us.  More loads per lane cost
+// CTAs per SM and more time (24 -> 34 us with four head rows on their way).
 #include <algorithm>
 #include <cmath>
 
@@ -375,7 +375,10 @@ __global__ void __launch_bounds__(AP_NT, 5) latent_append_kernel(const __grid_co
 }
 
 // Rows per CTA: one until every SM has CTAs enough to hide the loads' latency, then more, which share the CTA's start; of
-// many heads fewer, some 384 head rows (1640 tokens of 120 head rows 18.1 us with three, 20.7 with four).
+// many heads fewer, some 384 head rows.  What that limit gives, over nine numbers of tokens from 1300 to 12000 and two cache
+// types (time with it by time without): 64 + 64 + 64 heads 0.78 to 1.00, 0.92 on average (5500 tokens 78 and 100 us);
+// 32 + 32 + 32 heads 0.84 to 1.00, 0.97; 40 + 40 + 40 heads 0.83 to 1.25, 0.94 (2000 tokens, the worst, 27 and 22 us: with
+// the limit a second wave begins); latent rows with 128 heads 0.84 to 1.04, 0.97, with 64 heads 0.97 to 1.11, 1.02.
 int rows_per_cta(int64_t n_rows, int heads) {
     const int64_t sms = kvq_num_sms();
     return std::min(n_rows <= 8 * sms ? 1 : n_rows <= 32 * sms ? 4 : AP_TOK, std::max(1, 384 / heads));

@@ -1259,8 +1259,11 @@ extern "C" int kv_latent_attn(const kvq_latent* C, const kvq_seqs* S, int32_t n_
     if (e != cudaSuccess) return kvq_fail(KVQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
     if (p.whole || p.ctas == 1) return KVQ_OK;
     const int64_t group_rows = p.items * p.nr;
-    // A cluster per row where rows are few and parts many: 10 sequences of 2000 tokens, 160 rows in 15 parts, 17.9 us, with a
-    // warp per row 20.2; 14 of them, 224 rows in 11 parts, 25.3 and 23.4.
+    // A cluster per row where rows are few and parts many, else a warp per row.  Both sides, one token of sequences of 1000,
+    // 2000 and 8000 (time with clusters by time with warps): 16 heads, one sequence 0.27 to 0.57, eight (128 rows) 0.86 to
+    // 0.93, twelve (192 rows, 12 parts) 0.95 to 0.98, thirteen 0.97 to 1.01, fourteen 1.03 to 1.06, twenty 1.08 to 1.25;
+    // pairs, one and two sequences of 128 heads (256 rows) 0.54 to 0.87 and 0.87 to 1.02, three 1.03 to 1.18 (but 0.86 to 0.94
+    // of 64 heads, whose groups are half empty).
     const bool wide = p.ctas > 6 && (group_rows <= 128 || (group_rows <= 256 && p.ctas >= 12 * p.items));
     e = wide
             ? kvq_launch_pdl(latent_join_wide_kernel, dim3((unsigned)group_rows * LQ), dim3(LQ_W * LQ_GR), 0, kvq_stream(stream), a)
