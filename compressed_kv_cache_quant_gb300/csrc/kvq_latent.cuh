@@ -1,11 +1,11 @@
-// What the two attention forms of latent layers share: host checks and the cut of the absorbed form's steps.
+// What the two attention forms of latent layers share: host checks and the default scale.
 #pragma once
 
 #include <cmath>
 
 #include "kvq_internal.cuh"
 
-constexpr int KVQ_LATENT_MAX_CTAS = 256;
+constexpr int KVQ_LATENT_MAX_CTAS = 256;   // CTAs or pairs of the absorbed form, at most
 
 static inline int check_latent_rows(int32_t n_heads, int64_t n_rows, int32_t max_new, bool tree, const char* fn) {
     KVQ_REQUIRE(n_heads > 0 && n_heads <= 1 << 16, KVQ_ERR_INVALID_ARG, "%s: n_heads", fn);

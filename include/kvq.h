@@ -48,10 +48,14 @@
  *     read.  Two calls that share a workspace must not run concurrently.
  *   - Data-dependent device errors (a page id outside the pool, a selected id
  *     outside the sequence) skip the faulty access and set a status word in
- *     the workspace; kvq_check() reads and clears it.  Nothing traps, and no
- *     kernel waits on another CTA's flag: the only waits are bounded waits for
- *     a kernel's own asynchronous copies, which on expiry set the status word
- *     (KVQ_ERR_DEVICE_CHECK from kvq_check, "a bounded wait ... gave up").
+ *     the workspace; kvq_check() reads and clears it.  Nothing traps.  A kernel
+ *     waits for its own asynchronous copies and products, and where its CTAs
+ *     form clusters, which the hardware runs at the same time, for the other
+ *     CTAs of the cluster; never for a CTA that may not be running.  Waits that
+ *     poll are bounded and on expiry set the status word
+ *     (KVQ_ERR_DEVICE_CHECK from kvq_check, "a bounded wait ... gave up"); the
+ *     hardware's barriers of a CTA and of a cluster are not, and every thread
+ *     reaches them, whatever expired before.
  */
 #ifndef KVQ_H
 #define KVQ_H
