@@ -666,6 +666,14 @@ def _strided(x, shape, dtype, gpu, fn, name):
     return x.data_ptr(), st[0] if shape[0] > 1 else 1 << 30, st[1] if shape[1] > 1 else 1 << 30
 
 
+def _heads_of(x, width, fn, name):
+    """(rows, heads) of x [n][heads][width]; the rest of its form is checked with its address."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        have = f"{tuple(x.shape)}" if isinstance(x, torch.Tensor) else type(x).__name__
+        raise KvqError(_abi.KVQ_ERR_INVALID_ARG, fn, f"{name}: {have} instead of [rows][heads][{width}]")
+    return x.shape[:2]
+
+
 def kv_latent_append(cache, seqs, rope, row_starts, c, k_rope, ws, c_weight=None, eps=1e-6, positions=None, q=None,
                      q_out=None, stream=None):
     """The latent rows of new tokens into a LatentCache: c [n][512] (normed with a weight) and k_rope [n][64] (rotated),
@@ -682,7 +690,7 @@ def kv_latent_append(cache, seqs, rope, row_starts, c, k_rope, ws, c_weight=None
     ka, ks = _strided(_need(k_rope, fn, "k_rope"), (n, LATENT_ROPE), dt, gpu, fn, "k_rope")
     heads, qa, qs, qh, oa, os, oh = 0, None, 0, 0, None, 0, 0
     if q is not None and n:
-        heads = q.shape[1]
+        heads = _heads_of(q, LATENT_ROPE, fn, "q")[1]
         qa, qs, qh = _strided(q, (n, heads, LATENT_ROPE), dt, gpu, fn, "q")
         oa, os, oh = _strided(q_out, (n, heads, LATENT_ROPE), torch.float16, gpu, fn, "q_out")
     return check(lib().kv_latent_append(
@@ -702,7 +710,7 @@ def kv_latent_attn(cache, seqs, q, q_starts, max_new, out, ws, scale=0.0, parent
     LatentCache; q [n_rows][heads][576] and out [n_rows][heads][512] fp16, lse [n_rows][heads] fp32 (optional).
     scale 0: 1/sqrt(192).  parents: the new tokens are trees, as kv_tree_attn."""
     fn, gpu = "kv_latent_attn", _gpu()
-    n, H = _need(q, fn, "q").shape[:2]
+    n, H = _heads_of(_need(q, fn, "q"), LATENT_DIM + LATENT_ROPE, fn, "q")
     if not cache.gpu == seqs.gpu == ws.gpu == gpu:
         _elsewhere(gpu, fn, cache, seqs, ws)
     return check(lib().kv_latent_attn(
@@ -725,7 +733,7 @@ def kv_latent_expanded_attn(q, k_nope, k_rope, v, q_starts, k_starts, max_new, m
     k_rope may be slices of wider rows.  Sequence b has the queries q_starts[b] .. q_starts[b+1] - 1, the last of its
     tokens k_starts[b] .. k_starts[b+1] - 1.  scale 0: 1/sqrt(192)."""
     fn, gpu = "kv_latent_expanded_attn", _gpu()
-    n, H = _need(q, fn, "q").shape[:2]
+    n, H = _heads_of(_need(q, fn, "q"), HEAD_DIM + LATENT_ROPE, fn, "q")
     m, B = _need(k_nope, fn, "k_nope").shape[0], _need(q_starts, fn, "q_starts").shape[0] - 1
     if ws.gpu != gpu:
         _elsewhere(gpu, fn, ws)

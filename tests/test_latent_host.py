@@ -215,3 +215,24 @@ def test_a_batch_is_on_a_gpu_only_when_both_of_its_tables_are():
     assert kvq.Batch(On(0), On(0), 64).gpu == 0 and kvq.Batch(On(3), On(3), 64).gpu == 3
     for table, lens in ((0, 1), (1, 0), (-1, 0), (0, -1), (-1, -1)):
         assert kvq.Batch(On(table), On(lens), 64).gpu < 0, (table, lens)
+
+
+@pytest.mark.parametrize("q", [torch.zeros(4), torch.zeros((4, 576)), torch.zeros(()), torch.zeros((2, 3, 4, 5))])
+def test_queries_without_heads_are_refused_as_such(monkeypatch, q):
+    """Not an unpacking or an index error from inside the binding."""
+    monkeypatch.setattr(kvq, "_gpu", lambda: 0)
+    x = torch.zeros((4, 8), dtype=torch.float16)
+    with pytest.raises(kvq.KvqError) as e:
+        kvq.kv_latent_attn(None, None, q, None, 1, None, None)
+    assert e.value.code == BAD and "q:" in str(e.value)
+    with pytest.raises(kvq.KvqError) as e:
+        kvq.kv_latent_expanded_attn(q, x, x, x, x, x, 1, 1, None, None)
+    assert e.value.code == BAD and "q:" in str(e.value)
+
+    class Part:
+        gpu = 0
+
+    monkeypatch.setattr(kvq, "_strided", lambda x, shape, dtype, gpu, fn, name: (256, 64, 64)[:len(shape)])
+    with pytest.raises(kvq.KvqError) as e:
+        kvq.kv_latent_append(Part, Part, Part, None, x, x, Part, q=q, q_out=q)
+    assert e.value.code == BAD and "q:" in str(e.value)
