@@ -46,3 +46,29 @@ def test_pairs_repeat_themselves(heads, lens, news):
     pick = sorted({0, 1, heads // 2, heads - 1})
     rows = set(np.cumsum(news).tolist()) - {n} | {0, n - 1}
     agrees(first[0][:, pick], first[1][:, pick], expect(q[:, pick], L.rows, lens, news, rows=rows))
+
+
+def test_one_workspace_for_calls_of_every_kind():
+    """Calls of other sizes, heads and kinds in turn, with parts and without, all in one workspace: what each gives alone."""
+    require_gpu()
+    cases = [(16, [5000, 77], [1, 1]), (128, [3000], [1]), (64, [60, 90], [2, 1]), (1, [20001], [1]), (40, [700, 1, 1500], [3, 1, 2]), (8, [100] * 40, [1] * 40)]
+    calls = []
+    for heads, lens, news in cases:
+        L, n = LatentLayer(lens, seed=heads), sum(news)
+        q, starts = rnd((n, heads, ROW), heads, 7).cuda(), starts_of(news)
+        need = kvq.kv_latent_attn_ws(L.batch, heads, n, max(news))
+
+        def call(w, L=L, q=q, starts=starts, n=n, heads=heads, news=news):
+            out, lse = torch.empty((n, heads, LAT), dtype=torch.float16, device="cuda"), torch.empty((n, heads), device="cuda")
+            kvq.kv_latent_attn(L.cache, L.batch, q, starts, max(news), out, w, lse=lse)
+            return out, lse
+
+        calls.append((need, call))
+    alone = [call(ws(need)) for need, call in calls]
+    w = ws(max(need for need, _ in calls))
+    for order in (range(len(calls)), reversed(range(len(calls))), [0, 3, 1, 3, 4, 0, 5, 1, 2, 4]):
+        got = [(i, calls[i][1](w)) for i in order]   # (no wait between them)
+        for i, (out, lse) in got:
+            assert torch.equal(out, alone[i][0]) and torch.equal(lse, alone[i][1]), i
+    kvq.kvq_check(w)
+    assert not bool(w.t.any())

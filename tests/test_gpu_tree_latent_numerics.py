@@ -134,3 +134,49 @@ def test_absorbed_far_scores(heads, lens, news, sign):
                 told += largest_takes_all(R.as64(q[row, h]), K, K[:, :LAT], np.arange(t) <= t - m + i, 1 / math.sqrt(192), out[row, h], lse[row, h])
             row += 1
     assert told > n * heads // 4
+
+
+@pytest.mark.parametrize("op,heads,lens,news", [
+    ("absorbed", 16, [40, 700], [1, 2]), ("absorbed", 8, [20001], [1]), ("absorbed", 64, [130, 700], [3, 2]), ("absorbed", 128, [9001], [1]),
+    ("expanded", 3, [40, 700], [40, 300]), ("expanded", 2, [9001], [3]), ("tree", 8, [150, 700], [130, 9]), ("tree", 8, [9001], [30]),
+])
+def test_nan_in_a_query(op, heads, lens, news):
+    """NaN in one head of one query gives NaN in that row, and changes no bit of any other."""
+    require_gpu()
+    B, n, m = len(lens), sum(news), sum(lens)
+    pool = sum(-(-t // 16) for t in lens) + 2
+    batch, _ = paged_batch(lens, kvq.Allocator(pool, seed=9))
+    starts = torch.tensor(np.concatenate([[0], np.cumsum(news)]), dtype=torch.int32, device="cuda")
+    if op == "absorbed":
+        dq, dv, cache = ROW, LAT, kvq.LatentCache(pool)
+        cache.rows.copy_(rnd(cache.rows.shape, 1))
+        w = ws(kvq.kv_latent_attn_ws(batch, heads, n, max(news)))
+        call = lambda q, out, lse: kvq.kv_latent_attn(cache, batch, q, starts, max(news), out, w, lse=lse)  # noqa: E731
+    elif op == "tree":
+        dq, dv, cache = D, D, kvq.LayerCache(heads, 2, 16, pool, B)
+        cache.k16.copy_(rnd(cache.k16.shape, 1))
+        cache.v16.copy_(rnd(cache.v16.shape, 2))
+        par = torch.tensor([(i - 1) // 2 if i else -1 for k in news for i in range(k)], dtype=torch.int32, device="cuda")
+        w = ws(kvq.kv_tree_attn_ws(cache, batch, n, max(news)))
+        call = lambda q, out, lse: kvq.kv_tree_attn(cache, batch, q, par, starts, max(news), out, w, lse=lse)  # noqa: E731
+    else:
+        dq, dv = D + ROT, D
+        kv, kr = rnd((m, heads, 2 * D), 1).half().cuda(), rnd((m, ROT), 2).half().cuda()
+        at = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+        w = ws(kvq.kv_latent_expanded_attn_ws(B, heads, n, max(news), max(lens)))
+        call = lambda q, out, lse: kvq.kv_latent_expanded_attn(q, kv[..., :D], kr, kv[..., D:], starts, at, max(news), max(lens), out, w, lse=lse)  # noqa: E731
+    q = rnd((n, heads, dq), 5).half().cuda()
+    got = []
+    for bad in (False, True):
+        if bad:
+            q[n - 1, 1, 5] = math.nan
+        out, lse = torch.empty((n, heads, dv), dtype=torch.float16, device="cuda"), torch.empty((n, heads), device="cuda")
+        call(q, out, lse)
+        got.append((out, lse))
+    kvq.kvq_check(w)
+    hit = torch.zeros((n, heads), dtype=torch.bool, device="cuda")
+    hit[n - 1, 1] = True
+    (clean, clean_lse), (out, lse) = got
+    assert bool(out[hit].isnan().all()) and bool(lse[hit].isnan().all())
+    assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse[~hit], clean_lse[~hit]) and not bool(clean.isnan().any())
+    assert not bool(w.t.any())   # left zeroed, NaN included
